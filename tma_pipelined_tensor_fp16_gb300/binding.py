@@ -1,4 +1,5 @@
-"""ctypes binding of libtmagemm.so (the C ABI in include/tmagemm.h).
+"""ctypes binding of libtmagemm.so (the C ABI in include/tmagemm.h and
+include/tmaexperts.h; the object wrappers of the latter are in experts.py).
 
 Argument marshalling only: every step of the GEMM runs in the library's CUDA
 kernels.  If the library has not been built, or the device is not a GB300,
@@ -80,6 +81,25 @@ _SIGS = {
     "gemm_set_trace": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int]),
     "gemm_run_noalloc": (ctypes.c_int, [ctypes.c_int64] * 3 + [ctypes.c_int] + [ctypes.c_void_p] * 4
                          + [ctypes.POINTER(ctypes.c_int)]),
+    # include/tmaexperts.h
+    "gemm_expert_sort": (ctypes.c_int, [ctypes.c_int64] + [ctypes.c_int] * 2
+                         + [ctypes.c_void_p] * 5),
+    "gemm_expert_gather": (ctypes.c_int, [ctypes.c_int64] + [ctypes.c_int] * 2 + [ctypes.c_int64]
+                           + [ctypes.c_void_p] * 5),
+    "gemm_expert_combine": (ctypes.c_int, [ctypes.c_int64] + [ctypes.c_int] * 2 + [ctypes.c_int64]
+                            + [ctypes.c_void_p] * 4 + [ctypes.c_int] + [ctypes.c_void_p] * 2),
+    "gemm_expert_combine_grad": (ctypes.c_int, [ctypes.c_int64] + [ctypes.c_int] * 2
+                                 + [ctypes.c_int64] + [ctypes.c_void_p] * 8),
+    "gemm_grouped_create_plan": (ctypes.c_void_p, [ctypes.c_int64] * 3 + [ctypes.c_int] * 3),
+    "gemm_grouped_run": (ctypes.c_int, [ctypes.c_void_p] * 6),
+    "gemm_grouped_get_device_status": (ctypes.c_int, [ctypes.c_void_p]),
+    "gemm_grouped_destroy": (None, [ctypes.c_void_p]),
+    "gemm_grouped_describe": (ctypes.c_char_p, [ctypes.c_void_p]),
+    "gemm_w4_create_plan": (ctypes.c_void_p, [ctypes.c_int64] * 3 + [ctypes.c_int] * 4),
+    "gemm_w4_run": (ctypes.c_int, [ctypes.c_void_p] * 8),
+    "gemm_w4_get_device_status": (ctypes.c_int, [ctypes.c_void_p]),
+    "gemm_w4_destroy": (None, [ctypes.c_void_p]),
+    "gemm_w4_describe": (ctypes.c_char_p, [ctypes.c_void_p]),
 }
 
 _lib = None

@@ -16,6 +16,7 @@
 #include "../../include/tmagemm.h"
 #include "gemm_common.h"
 #include "launch.h"
+#include "runtime.h"
 
 using namespace tg;
 
@@ -47,10 +48,12 @@ void smem_limit_record(const void* kernel, unsigned bytes)
 
 }  // namespace tg
 
-namespace {
+namespace tg {
 
+namespace {
 thread_local std::string g_err;
 thread_local int g_status = GEMM_OK;
+}  // namespace
 
 int fail(int status, const std::string& msg)
 {
@@ -71,6 +74,25 @@ int cuda_fail(const char* what, cudaError_t e)
     return fail(GEMM_ERR_CUDA, std::string(what) + ": " + cudaGetErrorName(e) + " (" +
                                    cudaGetErrorString(e) + ")");
 }
+
+PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+}  // namespace tg
+
+namespace {
 
 const char* variant_name(int v)
 {
@@ -462,21 +484,6 @@ int select_config_impl(int64_t M, int64_t N, int64_t K, int dtype, const gemm_op
         }
     }
     return ok();
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
 }
 
 // 2-D tensor map over a row-major matrix with `rows` rows of `cols` elements
@@ -960,9 +967,9 @@ void gemm_destroy(gemm_plan* plan)
     delete plan;
 }
 
-const char* gemm_last_error(void) { return g_err.c_str(); }
+const char* gemm_last_error(void) { return tg::g_err.c_str(); }
 
-int gemm_last_status(void) { return g_status; }
+int gemm_last_status(void) { return tg::g_status; }
 
 const char* gemm_plan_describe(const gemm_plan* plan)
 {

@@ -1,0 +1,535 @@
+// expert_route.cu -- tokens sorted by expert and back: the stable counting
+// sort of the routing slots, the copy of the tokens into sorted order, the
+// weighted sum of the experts' rows per token, and the gradients of both.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "../../include/tmaexperts.h"
+#include "launch.h"
+#include "ptx.cuh"
+#include "runtime.h"
+
+namespace tg {
+
+namespace {
+
+// ------------------------------------------------------------------- sort
+//
+// Stable counting sort of S slots by key(s) = id, or E for a dropped slot:
+//
+//   position[s] = start[key] + |{s' < s : key(s') = key}|,
+//   start[e] = |{s : key(s) < e}|.
+//
+// One cluster does it in one launch.  Every warp owns a contiguous run of
+// slots and a histogram of its own in shared memory, so the count of equal
+// keys before a slot is (keys in earlier CTAs) + (earlier warps) + (earlier in
+// this warp), all taken in slot order: no result depends on timing.  The CTAs'
+// totals are exchanged through distributed shared memory.
+constexpr int SORT_MAX_EXPERTS = 1024;
+constexpr int SORT_BATCH = 8;  // ids a lane loads at once
+
+__device__ __forceinline__ uint32_t ld_shared_rank(uint32_t local, uint32_t rank)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_shared_rank(local, rank)));
+    return v;
+}
+
+__global__ void __launch_bounds__(1024, 1)
+    k_expert_sort(int slots, int experts, int run, const int32_t* ids, int32_t* offsets,
+                  int32_t* order, int32_t* position)
+{
+    extern __shared__ uint32_t sort_smem[];
+    const int keys = experts + 1;
+    const int warps = static_cast<int>(blockDim.x) / 32;
+    uint32_t* hist = sort_smem;             // [warps][keys]
+    uint32_t* total = hist + warps * keys;  // [keys] of this CTA, read by its peers
+    uint32_t* base = total + keys;          // [keys] first row of this CTA's slots of a key
+    uint32_t* warp_sum = base + keys;       // [33]
+    const int tid = static_cast<int>(threadIdx.x);
+    const int warp = tid >> 5;
+    const uint32_t lane = lane_id();
+    const uint32_t rank = cluster_ctarank();
+    const uint32_t ctas = gridDim.x;
+
+    for (int i = tid; i < warps * keys; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
+
+    uint32_t* mine = hist + warp * keys;
+    const int64_t first = (static_cast<int64_t>(rank) * warps + warp) * run;
+    const int begin = static_cast<int>(first < slots ? first : slots);
+    const int end = static_cast<int>(first + run < slots ? first + run : slots);
+    auto load_keys = [&](int s0, int (&key)[SORT_BATCH]) {
+#pragma unroll
+        for (int b = 0; b < SORT_BATCH; ++b) {
+            const int s = s0 + b * 32 + static_cast<int>(lane);
+            int id = -1;
+            if (s < end) id = ids[s];
+            key[b] = static_cast<unsigned>(id) < static_cast<unsigned>(experts) ? id : experts;
+        }
+    };
+    int key[SORT_BATCH];
+    for (int s0 = begin; s0 < end; s0 += 32 * SORT_BATCH) {
+        load_keys(s0, key);
+#pragma unroll
+        for (int b = 0; b < SORT_BATCH; ++b)
+            if (s0 + b * 32 + static_cast<int>(lane) < end) atomicAdd(&mine[key[b]], 1u);
+    }
+    __syncthreads();
+
+    // per key: exclusive sums over this CTA's warps, and the CTA's total
+    for (int k = tid; k < keys; k += blockDim.x) {
+        uint32_t acc = 0;
+        for (int w = 0; w < warps; ++w) {
+            const uint32_t v = hist[w * keys + k];
+            hist[w * keys + k] = acc;
+            acc += v;
+        }
+        total[k] = acc;
+    }
+    cluster_sync_all();
+
+    // per key: rows of earlier CTAs, and of all; then the exclusive sum over
+    // keys, a contiguous share of keys per thread
+    const int share = (keys + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
+    uint32_t sum = 0;
+    for (int i = 0; i < share; ++i) {
+        const int k = tid * share + i;
+        if (k >= keys) break;
+        uint32_t all = 0;
+        for (uint32_t c = 0; c < ctas; ++c) all += ld_shared_rank(smem_u32(total + k), c);
+        sum += all;
+    }
+    uint32_t scan = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, scan, d);
+        if (lane >= static_cast<uint32_t>(d)) scan += v;
+    }
+    if (lane == 31) warp_sum[warp] = scan;
+    __syncthreads();
+    if (warp == 0) {
+        uint32_t v = static_cast<int>(lane) < warps ? warp_sum[lane] : 0u;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, v, d);
+            if (lane >= static_cast<uint32_t>(d)) v += u;
+        }
+        warp_sum[lane] = v;
+    }
+    __syncthreads();
+    uint32_t row = scan - sum + (warp > 0 ? warp_sum[warp - 1] : 0u);
+    for (int i = 0; i < share; ++i) {
+        const int k = tid * share + i;
+        if (k >= keys) break;
+        uint32_t before = 0, all = 0;
+        for (uint32_t c = 0; c < ctas; ++c) {
+            const uint32_t v = ld_shared_rank(smem_u32(total + k), c);
+            if (c < rank) before += v;
+            all += v;
+        }
+        base[k] = row + before;
+        if (rank == 0) offsets[k] = static_cast<int32_t>(row);
+        row += all;
+    }
+    // peers have read this CTA's totals; base is complete
+    cluster_sync_all();
+
+    for (int s0 = begin; s0 < end; s0 += 32 * SORT_BATCH) {
+        load_keys(s0, key);
+#pragma unroll
+        for (int b = 0; b < SORT_BATCH; ++b) {
+            const int s = s0 + b * 32 + static_cast<int>(lane);
+            const bool live = s < end;
+            // lanes past the end share a key no slot has
+            const int k = live ? key[b] : keys;
+            const unsigned same = __match_any_sync(0xffffffffu, k);
+            const unsigned before = same & ((1u << lane) - 1u);
+            uint32_t r = 0;
+            if (live) r = mine[k] + __popc(before);
+            __syncwarp();
+            if (live && before == 0) mine[k] += __popc(same);
+            __syncwarp();
+            if (live) {
+                r += base[k];
+                position[s] = static_cast<int32_t>(r);
+                // always true for ids that nobody changes meanwhile
+                if (r < static_cast<uint32_t>(slots)) order[r] = s;
+            }
+        }
+    }
+}
+
+// ----------------------------------------------------------- rows by chunk
+//
+// The three kernels below move rows of `width` halves as 16-byte chunks.  A
+// thread owns one chunk column of one token, so a token's row is read once and
+// used for all of its slots.
+
+struct RowMap {
+    const int32_t* offsets;   // nullptr: slot order, none dropped
+    const int32_t* position;
+    int experts;
+    int64_t slots;
+};
+
+// Rows that belong to an expert: [0, kept).
+__device__ __forceinline__ uint32_t kept_rows(const RowMap& m)
+{
+    if (m.position == nullptr) return static_cast<uint32_t>(m.slots);
+    const int32_t n = m.offsets[m.experts];
+    return n < 0 ? 0u : (n > m.slots ? static_cast<uint32_t>(m.slots) : static_cast<uint32_t>(n));
+}
+
+__device__ __forceinline__ uint32_t row_of(const RowMap& m, int64_t slot)
+{
+    return m.position == nullptr ? static_cast<uint32_t>(slot)
+                                 : static_cast<uint32_t>(m.position[slot]);
+}
+
+__global__ void __launch_bounds__(256)
+    k_expert_gather(int64_t tokens, int topk, int chunks, RowMap map, const uint4* X, uint4* Xs)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int c = static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x);
+    if (t >= tokens || c >= chunks) return;
+    const uint32_t kept = kept_rows(map);
+    const uint4 v = X[t * chunks + c];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < topk; ++j) {
+        const uint32_t r = row_of(map, t * topk + j);
+        if (r < map.slots) Xs[static_cast<int64_t>(r) * chunks + c] = r < kept ? v : zero;
+    }
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8])
+{
+    const __half2* h = reinterpret_cast<const __half2*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 p = __half22float2(h[i]);
+        f[2 * i] = p.x;
+        f[2 * i + 1] = p.y;
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8])
+{
+    uint4 v;
+    __half2* h = reinterpret_cast<__half2*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    return v;
+}
+
+constexpr int SLOT_BATCH = 8;  // slots whose rows a thread has in flight
+
+template <bool F16OUT>
+__global__ void __launch_bounds__(256)
+    k_expert_combine(int64_t tokens, int topk, int chunks, RowMap map, const uint4* Ys,
+                     const float* weights, void* Y)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int c = static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x);
+    if (t >= tokens || c >= chunks) return;
+    const uint32_t kept = kept_rows(map);
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+    for (int j0 = 0; j0 < topk; j0 += SLOT_BATCH) {
+        uint32_t row[SLOT_BATCH];
+        float w[SLOT_BATCH];
+        uint4 v[SLOT_BATCH];
+#pragma unroll
+        for (int b = 0; b < SLOT_BATCH; ++b) {
+            row[b] = 0xffffffffu;
+            w[b] = 1.0f;
+            if (j0 + b < topk) {
+                row[b] = row_of(map, t * topk + j0 + b);
+                if (weights) w[b] = weights[t * topk + j0 + b];
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < SLOT_BATCH; ++b)
+            if (row[b] < kept) v[b] = Ys[static_cast<int64_t>(row[b]) * chunks + c];
+#pragma unroll
+        for (int b = 0; b < SLOT_BATCH; ++b) {
+            if (row[b] >= kept) continue;  // a dropped slot: its weight and row are not used
+            float f[8];
+            unpack8(v[b], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[b], f[i], acc[i]);
+        }
+    }
+    if constexpr (F16OUT) {
+        static_cast<uint4*>(Y)[t * chunks + c] = pack8(acc);
+    } else {
+        float4* y = static_cast<float4*>(Y) + (t * chunks + c) * 2;
+        y[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        y[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    }
+}
+
+// WPT warps share a token: each walks every WPT-th group of 32 chunks, and the
+// dot products of the token's slots are summed over lanes by shuffles and over
+// warps through shared memory, in a fixed order.  A thread reads a chunk of Ys
+// before it writes the same chunk of dYs and no other thread touches it, so the
+// two may be the same buffer.
+template <int WPT>
+__global__ void __launch_bounds__(256)
+    k_expert_combine_grad(int64_t tokens, int topk, int chunks, RowMap map, const uint4* dY,
+                          const uint4* Ys, const float* weights, uint4* dYs, float* dweights)
+{
+    __shared__ float part[8][SLOT_BATCH];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int warp = static_cast<int>(threadIdx.x) >> 5;
+    const uint32_t lane = lane_id();
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * (8 / WPT) + warp / WPT;
+    const bool live = t < tokens;
+    const uint32_t kept = kept_rows(map);
+    for (int j0 = 0; j0 < topk; j0 += SLOT_BATCH) {
+        uint32_t row[SLOT_BATCH];
+        float w[SLOT_BATCH], dot[SLOT_BATCH];
+#pragma unroll
+        for (int b = 0; b < SLOT_BATCH; ++b) {
+            row[b] = 0xffffffffu;
+            w[b] = 0.0f;
+            dot[b] = 0.0f;
+            if (live && j0 + b < topk) {
+                row[b] = row_of(map, t * topk + j0 + b);
+                if (row[b] < kept) w[b] = weights[t * topk + j0 + b];
+            }
+        }
+        if (live) {
+            for (int c = (warp % WPT) * 32 + static_cast<int>(lane); c < chunks; c += WPT * 32) {
+                float g[8];
+                unpack8(dY[t * chunks + c], g);
+                uint4 v[SLOT_BATCH];
+#pragma unroll
+                for (int b = 0; b < SLOT_BATCH; ++b)
+                    if (row[b] < kept) v[b] = Ys[static_cast<int64_t>(row[b]) * chunks + c];
+#pragma unroll
+                for (int b = 0; b < SLOT_BATCH; ++b) {
+                    if (row[b] >= map.slots) continue;  // past the last slot
+                    uint4 out = make_uint4(0, 0, 0, 0);
+                    if (row[b] < kept) {
+                        float f[8], o[8];
+                        unpack8(v[b], f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            dot[b] = fmaf(g[i], f[i], dot[b]);
+                            o[i] = w[b] * g[i];
+                        }
+                        out = pack8(o);
+                    }
+                    dYs[static_cast<int64_t>(row[b]) * chunks + c] = out;
+                }
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < SLOT_BATCH; ++b) {
+#pragma unroll
+            for (int d = 16; d > 0; d /= 2) dot[b] += __shfl_xor_sync(0xffffffffu, dot[b], d);
+        }
+        if (WPT == 1) {
+            if (lane == 0 && live) {
+#pragma unroll
+                for (int b = 0; b < SLOT_BATCH; ++b)
+                    if (j0 + b < topk) dweights[t * topk + j0 + b] = dot[b];
+            }
+        } else {
+            if (lane == 0) {
+#pragma unroll
+                for (int b = 0; b < SLOT_BATCH; ++b) part[warp][b] = dot[b];
+            }
+            __syncthreads();
+            if (warp % WPT == 0 && lane < SLOT_BATCH && live && j0 + static_cast<int>(lane) < topk) {
+                float s = 0.0f;
+#pragma unroll
+                for (int u = 0; u < WPT; ++u) s += part[warp + u][lane];
+                dweights[t * topk + j0 + lane] = s;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+int check_slots(int64_t tokens, int topk, int experts)
+{
+    if (tokens < 0 || topk < 1 || topk > 256)
+        return fail(GEMM_ERR_INVALID_ARG, "tokens must be >= 0 and topk in 1..256");
+    if (experts < 1 || experts > SORT_MAX_EXPERTS)
+        return fail(GEMM_ERR_INVALID_ARG, "experts must be in 1..1024");
+    if (tokens > (int64_t(1) << 30) / topk)
+        return fail(GEMM_ERR_UNSUPPORTED, "tokens * topk must be at most 2^30");
+    return GEMM_OK;
+}
+
+int check_width(int64_t width)
+{
+    if (width < 1 || width >= (int64_t(1) << 31))
+        return fail(GEMM_ERR_INVALID_ARG, "width must be in 1..2^31-1");
+    if (width % 8 != 0)
+        return fail(GEMM_ERR_UNSUPPORTED, "width must be a multiple of 8 (16-byte chunks of fp16)");
+    return GEMM_OK;
+}
+
+// Threads over the chunks of a row and, for narrow rows, over several tokens:
+// 256 threads a block, 64 where that leaves fewer blocks than SMs.
+struct RowGrid {
+    dim3 grid, block;
+};
+
+RowGrid row_grid(int64_t tokens, int chunks, int sms)
+{
+    int threads = 256;
+    while (threads > 64 && tokens * chunks / threads < sms) threads /= 2;
+    int cx = 8;
+    while (cx < threads && cx < chunks) cx *= 2;
+    const int ty = threads / cx;
+    RowGrid g;
+    g.block = dim3(cx, ty);
+    g.grid = dim3(static_cast<unsigned>((tokens + ty - 1) / ty),
+                  static_cast<unsigned>((chunks + cx - 1) / cx));
+    return g;
+}
+
+}  // namespace
+
+}  // namespace tg
+
+using namespace tg;
+
+extern "C" {
+
+int gemm_expert_sort(int64_t tokens, int topk, int experts, const int32_t* expert_ids,
+                     int32_t* offsets, int32_t* order, int32_t* position, void* cuda_stream)
+{
+    return guarded([&] {
+        int r = check_slots(tokens, topk, experts);
+        if (r != GEMM_OK) return r;
+        const int64_t slots = tokens * topk;
+        if (!offsets || (slots > 0 && (!expert_ids || !order || !position)))
+            return fail(GEMM_ERR_INVALID_ARG, "NULL pointer");
+        int dev, sms, smem_optin;
+        r = require_device(&dev, &sms, &smem_optin);
+        if (r != GEMM_OK) return r;
+        // One CTA up to 4096 slots, then as many as 8 (the portable cluster size).
+        int ctas = 1;
+        while (ctas < 8 && slots > static_cast<int64_t>(4096) * ctas) ctas *= 2;
+        int warps = 32;
+        while (warps > 8 && slots <= static_cast<int64_t>(warps) * 32 * ctas) warps /= 2;
+        const int64_t per_warp = (slots + ctas * warps - 1) / (ctas * warps);
+        const int run = static_cast<int>((per_warp + 31) / 32 * 32);
+        const unsigned smem = static_cast<unsigned>(((warps + 2) * (experts + 1) + 33) * 4);
+        cudaError_t e = ensure_smem_limit(k_expert_sort, smem);
+        if (e == cudaSuccess)
+            e = launch_dependent(k_expert_sort, dim3(ctas), dim3(warps * 32), smem, ctas,
+                                 static_cast<cudaStream_t>(cuda_stream), static_cast<int>(slots),
+                                 experts, run, expert_ids, offsets, order, position);
+        return e == cudaSuccess ? ok() : cuda_fail("expert sort launch", e);
+    });
+}
+
+int gemm_expert_gather(int64_t tokens, int topk, int experts, int64_t width, const void* X,
+                       const int32_t* offsets, const int32_t* position, void* Xs,
+                       void* cuda_stream)
+{
+    return guarded([&] {
+        int r = check_slots(tokens, topk, experts);
+        if (r == GEMM_OK) r = check_width(width);
+        if (r != GEMM_OK) return r;
+        if (tokens == 0) return ok();
+        if (!X || !offsets || !position || !Xs) return fail(GEMM_ERR_INVALID_ARG, "NULL pointer");
+        if (!aligned16(X) || !aligned16(Xs))
+            return fail(GEMM_ERR_UNSUPPORTED, "X and Xs must be 16-byte aligned");
+        int dev, sms;
+        r = require_device(&dev, &sms, nullptr);
+        if (r != GEMM_OK) return r;
+        const int chunks = static_cast<int>(width / 8);
+        const RowGrid g = row_grid(tokens, chunks, sms);
+        if (g.grid.y > 65535u) return fail(GEMM_ERR_UNSUPPORTED, "width is too large");
+        const RowMap map = {offsets, position, experts, tokens * topk};
+        cudaError_t e = launch_dependent(k_expert_gather, g.grid, g.block, 0, 1,
+                                         static_cast<cudaStream_t>(cuda_stream), tokens, topk,
+                                         chunks, map, static_cast<const uint4*>(X),
+                                         static_cast<uint4*>(Xs));
+        return e == cudaSuccess ? ok() : cuda_fail("expert gather launch", e);
+    });
+}
+
+int gemm_expert_combine(int64_t tokens, int topk, int experts, int64_t width, const void* Ys,
+                        const int32_t* offsets, const int32_t* position, const float* weights,
+                        int dtype_out, void* Y, void* cuda_stream)
+{
+    return guarded([&] {
+        int r = check_slots(tokens, topk, experts);
+        if (r == GEMM_OK) r = check_width(width);
+        if (r != GEMM_OK) return r;
+        if (dtype_out != GEMM_OUT_F32 && dtype_out != GEMM_OUT_F16)
+            return fail(GEMM_ERR_INVALID_ARG,
+                        "dtype_out must be GEMM_OUT_F32 (0) or GEMM_OUT_F16 (1)");
+        if (tokens == 0) return ok();
+        if (!Ys || !Y || (position && !offsets)) return fail(GEMM_ERR_INVALID_ARG, "NULL pointer");
+        if (!aligned16(Ys) || !aligned16(Y))
+            return fail(GEMM_ERR_UNSUPPORTED, "Ys and Y must be 16-byte aligned");
+        int dev, sms;
+        r = require_device(&dev, &sms, nullptr);
+        if (r != GEMM_OK) return r;
+        const int chunks = static_cast<int>(width / 8);
+        const RowGrid g = row_grid(tokens, chunks, sms);
+        if (g.grid.y > 65535u) return fail(GEMM_ERR_UNSUPPORTED, "width is too large");
+        const RowMap map = {offsets, position, experts, tokens * topk};
+        cudaError_t e = launch_dependent(
+            dtype_out == GEMM_OUT_F16 ? k_expert_combine<true> : k_expert_combine<false>, g.grid,
+            g.block, 0, 1, static_cast<cudaStream_t>(cuda_stream), tokens, topk, chunks, map,
+            static_cast<const uint4*>(Ys), weights, Y);
+        return e == cudaSuccess ? ok() : cuda_fail("expert combine launch", e);
+    });
+}
+
+int gemm_expert_combine_grad(int64_t tokens, int topk, int experts, int64_t width, const void* dY,
+                             const void* Ys, const int32_t* offsets, const int32_t* position,
+                             const float* weights, void* dYs, float* dweights, void* cuda_stream)
+{
+    return guarded([&] {
+        int r = check_slots(tokens, topk, experts);
+        if (r == GEMM_OK) r = check_width(width);
+        if (r != GEMM_OK) return r;
+        if (tokens == 0) return ok();
+        if (!dY || !Ys || !offsets || !position || !weights || !dYs || !dweights)
+            return fail(GEMM_ERR_INVALID_ARG, "NULL pointer");
+        if (!aligned16(dY) || !aligned16(Ys) || !aligned16(dYs))
+            return fail(GEMM_ERR_UNSUPPORTED, "dY, Ys and dYs must be 16-byte aligned");
+        int dev, sms;
+        r = require_device(&dev, &sms, nullptr);
+        if (r != GEMM_OK) return r;
+        const int chunks = static_cast<int>(width / 8);
+        const RowMap map = {offsets, position, experts, tokens * topk};
+        int wpt = 1;
+        while (wpt < 8 && chunks > 32 * wpt) wpt *= 2;
+        const int64_t blocks = (tokens + 8 / wpt - 1) / (8 / wpt);
+        auto kernel = wpt == 1   ? k_expert_combine_grad<1>
+                      : wpt == 2 ? k_expert_combine_grad<2>
+                      : wpt == 4 ? k_expert_combine_grad<4>
+                                 : k_expert_combine_grad<8>;
+        cudaError_t e = launch_dependent(
+            kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1,
+            static_cast<cudaStream_t>(cuda_stream), tokens, topk, chunks, map,
+            static_cast<const uint4*>(dY), static_cast<const uint4*>(Ys), weights,
+            static_cast<uint4*>(dYs), dweights);
+        return e == cudaSuccess ? ok() : cuda_fail("expert combine gradient launch", e);
+    });
+}
+
+}  // extern "C"

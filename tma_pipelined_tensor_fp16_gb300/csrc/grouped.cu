@@ -1,0 +1,291 @@
+// grouped.cu -- host side of the grouped products: argument checks, the choice
+// of the tile width, the tensor maps and the launch.
+#include "grouped.h"
+
+#include <algorithm>
+#include <cstdio>
+#include <cstring>
+#include <new>
+
+#include "../../include/tmaexperts.h"
+#include "runtime.h"
+
+using namespace tg;
+
+struct gemm_grouped_plan {
+    int64_t rows, N, K;
+    int experts, op, dtype;
+    int device;
+    int block_n, grid, pipe_depth;
+    unsigned smem_bytes;
+    int tiles_m, tiles_n;
+    DevStatus* d_status;
+    int epoch;
+    char desc[256];
+};
+
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int GROUP_M = 8;  // raster group height in tiles of 128 rows
+
+// Tensor map over `planes` row-major matrices of `rows` x `cols` (planes = 0: a
+// single matrix, a 2-D map), 128-byte swizzle, zero fill out of bounds.
+int encode(CUtensorMap* map, CUtensorMapDataType dt, int elt, const void* base, int64_t cols,
+           int64_t rows, int64_t planes, int box_cols, int box_rows, const char* what)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode_fn();
+    if (!enc) return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(planes)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols * elt),
+                                   static_cast<cuuint64_t>(cols * elt * rows)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols),
+                               static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const bool rows_on_256 =
+        (cols * elt) % 256 == 0 && reinterpret_cast<uintptr_t>(base) % 256 == 0;
+    CUresult r = enc(map, dt, planes ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     rows_on_256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                 : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        char buf[160];
+        std::snprintf(buf, sizeof(buf), "cuTensorMapEncodeTiled(%s) failed with CUresult %d", what,
+                      static_cast<int>(r));
+        return fail(GEMM_ERR_CUDA, buf);
+    }
+    return GEMM_OK;
+}
+
+const char* op_name(int op)
+{
+    return op == GROUPED_FORWARD      ? "forward"
+           : op == GROUPED_GRAD_INPUT ? "grad_input"
+                                      : "grad_weight";
+}
+
+// Output columns, and rows of one tile column of the whole output.
+int64_t out_cols_of(const gemm_grouped_plan& p)
+{
+    return p.op == GROUPED_FORWARD ? p.N : p.K;
+}
+
+int check_grouped(int64_t rows, int64_t N, int64_t K, int experts, int op, int dtype)
+{
+    const int64_t LIM = (int64_t(1) << 31) - 1;
+    if (rows < 0 || N < 1 || K < 1 || rows > LIM || N > LIM || K > LIM)
+        return fail(GEMM_ERR_INVALID_ARG, "rows must be in [0, 2^31-1], N and K in [1, 2^31-1]");
+    if (experts < 1 || experts > GROUPED_MAX_EXPERTS)
+        return fail(GEMM_ERR_INVALID_ARG, "experts must be in 1..1024");
+    if (op < GROUPED_FORWARD || op > GROUPED_GRAD_WEIGHT)
+        return fail(GEMM_ERR_INVALID_ARG, "unknown gemm_grouped_op");
+    if (dtype != GEMM_OUT_F32 && dtype != GEMM_OUT_F16)
+        return fail(GEMM_ERR_INVALID_ARG, "dtype_out must be GEMM_OUT_F32 (0) or GEMM_OUT_F16 (1)");
+    if (N % 8 != 0 || K % 8 != 0)
+        return fail(GEMM_ERR_UNSUPPORTED,
+                    "N and K must be multiples of 8: the TMA row strides must be multiples of 16 bytes");
+    if (N > LIM / experts || N * K >= (int64_t(1) << 38))
+        return fail(GEMM_ERR_UNSUPPORTED, "experts * N or N * K is too large");
+    return GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_grouped_plan* gemm_grouped_create_plan(int64_t rows, int64_t N, int64_t K, int experts, int op,
+                                            int dtype_out)
+{
+    gemm_grouped_plan* plan = nullptr;
+    guarded([&] {
+        int r = check_grouped(rows, N, K, experts, op, dtype_out);
+        if (r != GEMM_OK) return r;
+        int dev, sms, smem_optin;
+        r = require_device(&dev, &sms, &smem_optin);
+        if (r != GEMM_OK) return r;
+        gemm_grouped_plan p = {};
+        p.rows = rows;
+        p.N = N;
+        p.K = K;
+        p.experts = experts;
+        p.op = op;
+        p.dtype = dtype_out;
+        p.device = dev;
+        const int64_t cols = out_cols_of(p);
+        // Row tiles: exact for GRAD_WEIGHT; else every expert's last tile is
+        // half full on average, and at most one more tile than its rows fill
+        // (and one group for the rows that belong to none).
+        int64_t expect, most;
+        if (op == GROUPED_GRAD_WEIGHT) {
+            expect = most = ceil_div(N, BLK_M) * experts;
+        } else {
+            expect = ceil_div(rows, BLK_M) + std::min<int64_t>(experts, rows) / 2;
+            most = rows / BLK_M + std::min<int64_t>(experts + 1, rows);
+        }
+        p.block_n = cols > 128 && expect * ceil_div(cols, 256) >= sms ? 256 : 128;
+        const int64_t tn = ceil_div(cols, p.block_n);
+        if (most * tn >= (int64_t(1) << 31) - 65536)
+            return fail(GEMM_ERR_UNSUPPORTED, "too many output tiles");
+        p.tiles_n = static_cast<int>(tn);
+        p.tiles_m = static_cast<int>(ceil_div(N, BLK_M));
+        p.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, most * tn)));
+        const uint32_t table = grouped_table_bytes(op, experts);
+        for (int d = MAX_STAGES; d >= 1; --d) {
+            const uint32_t need = smem_layout(d, p.block_n, NUM_STAGING).total + table;
+            if (need <= static_cast<uint32_t>(smem_optin)) {
+                p.pipe_depth = d;
+                p.smem_bytes = need;
+                break;
+            }
+        }
+        if (p.pipe_depth < 2) return fail(GEMM_ERR_UNSUPPORTED, "no stage count fits shared memory");
+        std::snprintf(p.desc, sizeof(p.desc),
+                      "grouped op=%s rows=%lld N=%lld K=%lld experts=%d tile=128x%dx%d "
+                      "pipe_depth=%d smem=%u grid=%d out=%s",
+                      op_name(op), static_cast<long long>(rows), static_cast<long long>(N),
+                      static_cast<long long>(K), experts, p.block_n, BLK_K, p.pipe_depth,
+                      p.smem_bytes, p.grid, dtype_out == GEMM_OUT_F16 ? "f16" : "f32");
+        cudaError_t e = cudaMalloc(&p.d_status, sizeof(DevStatus));
+        if (e == cudaSuccess) e = cudaMemset(p.d_status, 0, sizeof(DevStatus));
+        if (e != cudaSuccess) {
+            if (p.d_status) cudaFree(p.d_status);
+            return cuda_fail("allocating the device status record", e);
+        }
+        plan = new (std::nothrow) gemm_grouped_plan(p);
+        if (!plan) {
+            cudaFree(p.d_status);
+            return fail(GEMM_ERR_CUDA, "out of host memory");
+        }
+        return ok();
+    });
+    return plan;
+}
+
+int gemm_grouped_run(gemm_grouped_plan* plan, const void* P, const void* Q,
+                     const int32_t* offsets, void* out, void* cuda_stream)
+{
+    return guarded([&] {
+        if (!plan) return fail(GEMM_ERR_INVALID_ARG, "plan is NULL");
+        const bool weight = plan->op == GROUPED_GRAD_WEIGHT;
+        if (plan->rows == 0 && !weight) return ok();
+        if (!offsets || !out || (plan->rows > 0 && (!P || !Q)))
+            return fail(GEMM_ERR_INVALID_ARG, "P, Q, offsets and out must be non-NULL");
+        if (!aligned16(P) || !aligned16(Q) || !aligned16(out))
+            return fail(GEMM_ERR_UNSUPPORTED, "P, Q and out must be 16-byte aligned (TMA)");
+        if (reinterpret_cast<uintptr_t>(offsets) & 3u)
+            return fail(GEMM_ERR_UNSUPPORTED, "offsets must be 4-byte aligned");
+        int dev = -1;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return cuda_fail("cudaGetDevice", e);
+        if (dev != plan->device)
+            return fail(GEMM_ERR_INVALID_ARG, "plan was created on another device");
+        cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+        const int64_t R = plan->rows, N = plan->N, K = plan->K, E = plan->experts;
+        const int elt = plan->dtype == GEMM_OUT_F16 ? 2 : 4;
+        const int64_t cols = out_cols_of(*plan);
+        if (R == 0) {  // no rows at all: every expert's weight gradient is zero
+            e = cudaMemsetAsync(out, 0, static_cast<size_t>(E) * N * K * elt, stream);
+            return e == cudaSuccess ? ok() : cuda_fail("cudaMemsetAsync", e);
+        }
+        const CUtensorMapDataType F16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        const CUtensorMapDataType OUT =
+            elt == 2 ? F16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+        CUtensorMap tmA, tmB, tmC;
+        int r;
+        if (plan->op == GROUPED_FORWARD) {
+            r = encode(&tmA, F16, 2, P, K, R, 0, BLK_K, BLK_M, "A");
+            if (r == GEMM_OK) r = encode(&tmB, F16, 2, Q, K, N, E, BLK_K, plan->block_n, "B");
+        } else if (plan->op == GROUPED_GRAD_INPUT) {
+            r = encode(&tmA, F16, 2, P, N, R, 0, BLK_K, BLK_M, "dC");
+            if (r == GEMM_OK) r = encode(&tmB, F16, 2, Q, K, N, E, 64, BLK_K, "B");
+        } else {
+            r = encode(&tmA, F16, 2, P, N, R, 0, 64, BLK_K, "dC");
+            if (r == GEMM_OK) r = encode(&tmB, F16, 2, Q, K, R, 0, 64, BLK_K, "A");
+        }
+        if (r == GEMM_OK)
+            r = weight ? encode(&tmC, OUT, elt, out, K, N, E, 128 / elt, 32, "dB")
+                       : encode(&tmC, OUT, elt, out, cols, R, 0, 128 / elt, 32, "out");
+        if (r != GEMM_OK) return r;
+
+        GroupedSpec s = {};
+        s.op = plan->op;
+        s.block_n = plan->block_n;
+        s.f16out = elt == 2;
+        s.grid = plan->grid;
+        s.smem_bytes = plan->smem_bytes;
+        s.tmA = &tmA;
+        s.tmB = &tmB;
+        s.tmC = &tmC;
+        GroupedParams& p = s.p;
+        p.rows = static_cast<int>(R);
+        p.out_rows = static_cast<int>(weight ? N : R);
+        p.out_cols = static_cast<int>(cols);
+        p.depth = static_cast<int>(plan->op == GROUPED_GRAD_INPUT ? N : K);
+        p.experts = plan->experts;
+        p.tiles_n = plan->tiles_n;
+        p.tiles_m = plan->tiles_m;
+        p.group_m = GROUP_M;
+        p.pipe_depth = plan->pipe_depth;
+        p.offsets = offsets;
+        p.out = out;
+        p.status = plan->d_status;
+        if (++plan->epoch <= 0) plan->epoch = 1;
+        p.epoch = plan->epoch;
+        p.budget_ns = 2000ull * 1000000ull;
+        e = launch_grouped(s, stream);
+        return e == cudaSuccess ? ok() : cuda_fail("grouped product launch", e);
+    });
+}
+
+int gemm_grouped_get_device_status(gemm_grouped_plan* plan)
+{
+    return guarded([&] {
+        if (!plan) return fail(GEMM_ERR_INVALID_ARG, "plan is NULL");
+        DevStatus st;
+        cudaError_t e = cudaMemcpy(&st, plan->d_status, sizeof(st), cudaMemcpyDeviceToHost);
+        if (e != cudaSuccess) return cuda_fail("reading the device status record", e);
+        if (st.code == DEV_OK) return ok();
+        DevStatus zero = {};
+        zero.abort_epoch = st.abort_epoch;  // a stale epoch never matches a new run
+        cudaMemcpy(plan->d_status, &zero, sizeof(zero), cudaMemcpyHostToDevice);
+        char buf[200];
+        std::snprintf(buf, sizeof(buf),
+                      "kernel wait timed out (where=%d block=%d column=%d k_block=%d); the run was abandoned",
+                      st.where, st.block, st.tile, st.kblock);
+        return fail(st.code == DEV_TIMEOUT ? GEMM_ERR_TIMEOUT : GEMM_ERR_CUDA, buf);
+    });
+}
+
+void gemm_grouped_destroy(gemm_grouped_plan* plan)
+{
+    if (!plan) return;
+    if (plan->d_status) cudaFree(plan->d_status);
+    delete plan;
+}
+
+const char* gemm_grouped_describe(const gemm_grouped_plan* plan)
+{
+    return plan ? plan->desc : "(null plan)";
+}
+
+}  // extern "C"
+
+namespace tg {
+
+template <int OP>
+cudaError_t launch_grouped_op(const GroupedSpec& s, cudaStream_t stream);
+
+cudaError_t launch_grouped(const GroupedSpec& s, cudaStream_t stream)
+{
+    switch (s.op) {
+    case GROUPED_FORWARD: return launch_grouped_op<GROUPED_FORWARD>(s, stream);
+    case GROUPED_GRAD_INPUT: return launch_grouped_op<GROUPED_GRAD_INPUT>(s, stream);
+    case GROUPED_GRAD_WEIGHT: return launch_grouped_op<GROUPED_GRAD_WEIGHT>(s, stream);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace tg

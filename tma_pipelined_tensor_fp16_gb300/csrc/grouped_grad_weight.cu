@@ -1,0 +1,8 @@
+// grouped_grad_weight.cu -- the GROUPED_GRAD_WEIGHT form of the grouped product.
+#include "kernel_grouped.cuh"
+
+namespace tg {
+
+template cudaError_t launch_grouped_op<GROUPED_GRAD_WEIGHT>(const GroupedSpec&, cudaStream_t);
+
+}  // namespace tg

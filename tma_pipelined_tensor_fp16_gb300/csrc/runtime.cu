@@ -1,0 +1,52 @@
+// runtime.cu -- the device check shared by the C entry points.
+#include <cstdio>
+#include <mutex>
+
+#include "runtime.h"
+
+namespace tg {
+
+namespace {
+constexpr int MAX_DEVICES = 64;
+struct DeviceInfo {
+    bool known;
+    int major, minor, sms, smem_optin;
+};
+std::mutex g_device_mutex;
+DeviceInfo g_devices[MAX_DEVICES] = {};
+}  // namespace
+
+int require_device(int* dev, int* sms, int* smem_optin)
+{
+    cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess)
+        return fail(GEMM_ERR_NO_DEVICE, std::string("no CUDA device: ") + cudaGetErrorString(e));
+    DeviceInfo info = {};
+    std::lock_guard<std::mutex> lock(g_device_mutex);
+    if (*dev < MAX_DEVICES) info = g_devices[*dev];
+    if (!info.known) {
+        e = cudaDeviceGetAttribute(&info.major, cudaDevAttrComputeCapabilityMajor, *dev);
+        if (e == cudaSuccess)
+            e = cudaDeviceGetAttribute(&info.minor, cudaDevAttrComputeCapabilityMinor, *dev);
+        if (e == cudaSuccess)
+            e = cudaDeviceGetAttribute(&info.sms, cudaDevAttrMultiProcessorCount, *dev);
+        if (e == cudaSuccess)
+            e = cudaDeviceGetAttribute(&info.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin,
+                                       *dev);
+        if (e != cudaSuccess) return cuda_fail("cudaDeviceGetAttribute", e);
+        info.known = true;
+        if (*dev < MAX_DEVICES) g_devices[*dev] = info;
+    }
+    if (info.major != 10 || info.minor != 3) {
+        char buf[160];
+        std::snprintf(buf, sizeof(buf),
+                      "device %d is sm_%d%d; this library is built for sm_103a (GB300) only", *dev,
+                      info.major, info.minor);
+        return fail(GEMM_ERR_NO_DEVICE, buf);
+    }
+    if (sms) *sms = info.sms;
+    if (smem_optin) *smem_optin = info.smem_optin;
+    return GEMM_OK;
+}
+
+}  // namespace tg

@@ -1,0 +1,327 @@
+"""The expert-layer operators of include/tmaexperts.h for torch CUDA tensors.
+
+A mixture-of-experts feed-forward sends each of ``tokens`` tokens to ``topk``
+of ``experts`` experts.  With ``ids`` (tokens x topk, int32; negative or too
+large = the slot is dropped) and routing ``weights`` (tokens x topk, float32):
+
+    route = ExpertRoute(tokens, topk, experts).sort(ids)
+    Xs = route.gather(X)                               # rows sorted by expert
+    up(Xs, W1, route.offsets, H)                       # GroupedPlan "forward"
+    ...                                                # activation
+    down(H, W2, route.offsets, Ys)
+    Y = route.combine(Ys, weights=weights)             # back to the tokens
+
+and backwards with ``combine_grad``, the ``grad_input`` and ``grad_weight``
+plans and ``gather_grad``.  ``W4Plan`` is the product for single tokens with
+weights in 4 bits, dense or by expert.  ``python -m
+tma_pipelined_tensor_fp16_gb300.expert_layer`` runs them together.
+
+Argument checks and marshalling only; every operator runs in the library's CUDA
+kernels, asynchronously on the current stream of the tensors' device (or on
+``stream``), and writes into the tensor it is given or a new one.
+"""
+from .binding import GEMM_OUT_F16, GEMM_OUT_F32, GemmError, _check, last_error, lib
+
+GROUPED_OPS = {"forward": 0, "grad_input": 1, "grad_weight": 2}
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _tensor(name, t, shape, dtype, device=None):
+    """Raise unless `t` is a contiguous CUDA tensor of this shape and type."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, device))
+    return t
+
+
+def _output(name, t, shape, dtype, device):
+    if t is None:
+        return _torch().empty(shape, dtype=dtype, device=device)
+    return _tensor(name, t, shape, dtype, device)
+
+
+def _out_dtype(out):
+    torch = _torch()
+    if out not in ("f16", "f32"):
+        raise ValueError("out must be 'f16' or 'f32'")
+    return (torch.float16, GEMM_OUT_F16) if out == "f16" else (torch.float32, GEMM_OUT_F32)
+
+
+def _on(device):
+    """Context in which `device` is current (the C calls use the current one)."""
+    return _torch().cuda.device(device)
+
+
+def _stream(device, stream):
+    s = stream if stream is not None else _torch().cuda.current_stream(device)
+    return s.cuda_stream
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None and t.numel() > 0 else None
+
+
+class ExpertRoute:
+    """The slots of one batch sorted by expert.
+
+    ``offsets`` (experts + 1), ``order`` (tokens * topk: sorted row -> slot) and
+    ``position`` (tokens x topk: slot -> sorted row) are int32 tensors, filled by
+    ``sort`` or taken over by ``load``.  Dropped slots take the rows from
+    ``offsets[experts]`` on.
+    """
+
+    def __init__(self, tokens, topk, experts):
+        if tokens < 0 or topk < 1 or experts < 1:
+            raise ValueError("tokens must be >= 0, topk and experts >= 1")
+        self.tokens, self.topk, self.experts = tokens, topk, experts
+        self.offsets = self.order = self.position = None
+
+    @property
+    def slots(self):
+        return self.tokens * self.topk
+
+    def sort(self, ids, stream=None):
+        """Sort by `ids` (tokens x topk int32); returns self."""
+        torch = _torch()
+        _tensor("ids", ids, (self.tokens, self.topk), torch.int32)
+        dev = ids.device
+        if self.offsets is None or self.offsets.device != dev:
+            self.offsets = torch.empty(self.experts + 1, dtype=torch.int32, device=dev)
+            self.order = torch.empty(self.slots, dtype=torch.int32, device=dev)
+            self.position = torch.empty((self.tokens, self.topk), dtype=torch.int32, device=dev)
+        with _on(dev):
+            _check(lib().gemm_expert_sort(self.tokens, self.topk, self.experts, _ptr(ids),
+                                          _ptr(self.offsets), _ptr(self.order),
+                                          _ptr(self.position), _stream(dev, stream)))
+        return self
+
+    def load(self, offsets, order, position):
+        """Take over a sorted routing made elsewhere; returns self."""
+        torch = _torch()
+        _tensor("offsets", offsets, (self.experts + 1,), torch.int32)
+        _tensor("order", order, (self.slots,), torch.int32, offsets.device)
+        _tensor("position", position, (self.tokens, self.topk), torch.int32, offsets.device)
+        self.offsets, self.order, self.position = offsets, order, position
+        return self
+
+    def _sorted_on(self):
+        if self.offsets is None:
+            raise RuntimeError("the route has not been sorted: call sort() or load() first")
+        return self.offsets.device
+
+    def gather(self, X, out=None, stream=None):
+        """Xs[position[t, j]] = X[t] (tokens x width fp16 -> tokens * topk x width);
+        zero rows for dropped slots."""
+        torch = _torch()
+        dev = self._sorted_on()
+        width = X.shape[-1]
+        _tensor("X", X, (self.tokens, width), torch.float16, dev)
+        Xs = _output("out", out, (self.slots, width), torch.float16, dev)
+        with _on(dev):
+            _check(lib().gemm_expert_gather(self.tokens, self.topk, self.experts, width, _ptr(X),
+                                            _ptr(self.offsets), _ptr(self.position), _ptr(Xs),
+                                            _stream(dev, stream)))
+        return Xs
+
+    def combine(self, Ys, out=None, weights=None, stream=None):
+        """Y[t] = sum_j weights[t, j] * Ys[position[t, j]] over the slots that are
+        not dropped (a plain sum without `weights`).  `out` is fp16 or fp32
+        (fp16 when not given)."""
+        torch = _torch()
+        dev = self._sorted_on()
+        return self._combine(dev, Ys, out, weights, self.offsets, self.position, stream)
+
+    def combine_slots(self, Ys, out=None, weights=None, stream=None):
+        """As ``combine`` for rows in slot order (row t * topk + j), as W4Plan
+        leaves them; needs no sort.  No slot counts as dropped."""
+        dev = Ys.device
+        return self._combine(dev, Ys, out, weights, None, None, stream)
+
+    def _combine(self, dev, Ys, out, weights, offsets, position, stream):
+        torch = _torch()
+        width = Ys.shape[-1]
+        _tensor("Ys", Ys, (self.slots, width), torch.float16, dev)
+        if weights is not None:
+            _tensor("weights", weights, (self.tokens, self.topk), torch.float32, dev)
+        dtype = torch.float32 if out is not None and out.dtype == torch.float32 else torch.float16
+        Y = _output("out", out, (self.tokens, width), dtype, dev)
+        with _on(dev):
+            _check(lib().gemm_expert_combine(
+                self.tokens, self.topk, self.experts, width, _ptr(Ys), _ptr(offsets),
+                _ptr(position), _ptr(weights),
+                GEMM_OUT_F32 if dtype == torch.float32 else GEMM_OUT_F16, _ptr(Y),
+                _stream(dev, stream)))
+        return Y
+
+    def gather_grad(self, dXs, out=None, stream=None):
+        """Gradient of ``gather`` with respect to X: the sum of a token's rows."""
+        return self.combine(dXs, out=out, stream=stream)
+
+    def combine_grad(self, dY, Ys, weights, out=None, dweights=None, stream=None):
+        """Gradients (dYs, dweights) of the weighted ``combine`` for dY (tokens x
+        width fp16).  `out` (dYs) may be Ys itself."""
+        torch = _torch()
+        dev = self._sorted_on()
+        width = dY.shape[-1]
+        _tensor("dY", dY, (self.tokens, width), torch.float16, dev)
+        _tensor("Ys", Ys, (self.slots, width), torch.float16, dev)
+        _tensor("weights", weights, (self.tokens, self.topk), torch.float32, dev)
+        dYs = _output("out", out, (self.slots, width), torch.float16, dev)
+        dw = _output("dweights", dweights, (self.tokens, self.topk), torch.float32, dev)
+        with _on(dev):
+            _check(lib().gemm_expert_combine_grad(
+                self.tokens, self.topk, self.experts, width, _ptr(dY), _ptr(Ys),
+                _ptr(self.offsets), _ptr(self.position), _ptr(weights), _ptr(dYs), _ptr(dw),
+                _stream(dev, stream)))
+        return dYs, dw
+
+
+class _Handle:
+    """Owner of a plan of the C library."""
+    _destroy = _describe = _status = None
+
+    def _own(self, handle):
+        self._h = handle
+        if not handle:
+            raise GemmError(lib().gemm_last_status(), last_error())
+
+    @property
+    def handle(self):
+        return self._h
+
+    def describe(self):
+        return (getattr(lib(), self._describe)(self._h) or b"").decode()
+
+    def device_status(self):
+        """GEMM_OK, or GEMM_ERR_TIMEOUT if a wait inside a kernel ran out; call
+        after synchronising."""
+        return getattr(lib(), self._status)(self._h)
+
+    def close(self):
+        if getattr(self, "_h", None):
+            getattr(lib(), self._destroy)(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class GroupedPlan(_Handle):
+    """The experts' products over rows sorted by expert (expert e owns rows
+    offsets[e] .. offsets[e + 1] - 1; B is experts x N x K):
+
+    * ``forward``:      C[r]  = A[r] . B[e]^T      plan(A, B, offsets, C)
+    * ``grad_input``:   dA[r] = dC[r] . B[e]       plan(dC, B, offsets, dA)
+    * ``grad_weight``:  dB[e] = dC_e^T . A_e       plan(dC, A, offsets, dB)
+    """
+    _destroy, _describe = "gemm_grouped_destroy", "gemm_grouped_describe"
+    _status = "gemm_grouped_get_device_status"
+
+    def __init__(self, rows, N, K, experts, op="forward", out="f16"):
+        if op not in GROUPED_OPS:
+            raise ValueError("op must be one of %s" % sorted(GROUPED_OPS))
+        self.rows, self.N, self.K, self.experts, self.op = rows, N, K, experts, op
+        self.dtype, code = _out_dtype(out)
+        self._own(lib().gemm_grouped_create_plan(rows, N, K, experts, GROUPED_OPS[op], code))
+
+    def shapes(self):
+        """Shapes of (P, Q, out)."""
+        R, N, K, E = self.rows, self.N, self.K, self.experts
+        return {"forward": ((R, K), (E, N, K), (R, N)),
+                "grad_input": ((R, N), (E, N, K), (R, K)),
+                "grad_weight": ((R, N), (R, K), (E, N, K))}[self.op]
+
+    def __call__(self, P, Q, offsets, out=None, stream=None):
+        torch = _torch()
+        sp, sq, so = self.shapes()
+        _tensor("P", P, sp, torch.float16)
+        dev = P.device
+        _tensor("Q", Q, sq, torch.float16, dev)
+        _tensor("offsets", offsets, (self.experts + 1,), torch.int32, dev)
+        out = _output("out", out, so, self.dtype, dev)
+        with _on(dev):
+            _check(lib().gemm_grouped_run(self._h, _ptr(P), _ptr(Q), _ptr(offsets), _ptr(out),
+                                          _stream(dev, stream)))
+        return out
+
+
+class W4Plan(_Handle):
+    """Y = X . W^T with W[n, k] = scales[n, k // group] * (q[n, k] - zero) in 4 bits.
+
+    ``packed`` is N x K/2 uint8 (the low half of byte b is q[2b], the high half
+    q[2b + 1]), ``scales`` N x K/group fp16, ``zeros`` N x K/group uint8 or None
+    for 8 (``w4_pack`` makes them).  With ``experts`` they are stacked, and row m
+    of Y is the product of X[m // share] with the weights of expert ids[m].
+    """
+    _destroy, _describe, _status = "gemm_w4_destroy", "gemm_w4_describe", "gemm_w4_get_device_status"
+
+    def __init__(self, M, N, K, group=128, out="f16", experts=0, share=1):
+        self.M, self.N, self.K, self.group = M, N, K, group
+        self.experts, self.share = experts, share
+        self.dtype, code = _out_dtype(out)
+        self._own(lib().gemm_w4_create_plan(M, N, K, group, experts, share, code))
+
+    def __call__(self, X, packed, scales, out=None, zeros=None, ids=None, stream=None):
+        torch = _torch()
+        _tensor("X", X, (-(-self.M // self.share), self.K), torch.float16)
+        dev = X.device
+        lead = (self.experts,) if self.experts else ()
+        groups = lead + (self.N, self.K // self.group)
+        _tensor("packed", packed, lead + (self.N, self.K // 2), torch.uint8, dev)
+        _tensor("scales", scales, groups, torch.float16, dev)
+        if zeros is not None:
+            _tensor("zeros", zeros, groups, torch.uint8, dev)
+        if (ids is not None) != (self.experts > 0):
+            raise ValueError("ids must be given exactly when the plan has experts")
+        if ids is not None:
+            if ids.numel() != self.M:
+                raise ValueError("ids must hold one expert per row (%d)" % self.M)
+            _tensor("ids", ids, ids.shape, torch.int32, dev)
+        Y = _output("out", out, (self.M, self.N), self.dtype, dev)
+        with _on(dev):
+            _check(lib().gemm_w4_run(self._h, _ptr(X), _ptr(packed), _ptr(scales), _ptr(zeros),
+                                     _ptr(ids), _ptr(Y), _stream(dev, stream)))
+        return Y
+
+
+def w4_pack(W, group=128, zeros=False):
+    """Round W (... x N x K float) to 4-bit codes: (packed, scales, zeros or None)
+    as W4Plan takes them.  Without `zeros` the codes are symmetric around 8 and
+    the scale is the group's largest magnitude / 7; with them the group's range
+    (which always holds 0) is spread over the 16 codes.  A set-up step."""
+    torch = _torch()
+    if W.shape[-1] % group != 0 or group not in (32, 64, 128):
+        raise ValueError("K must be a multiple of group, and group 32, 64 or 128")
+    w = W.float().reshape(W.shape[:-1] + (-1, group))
+    if zeros:
+        lo = w.amin(-1).clamp(max=0.0)
+        hi = w.amax(-1).clamp(min=0.0)
+        scale = ((hi - lo) / 15.0)
+    else:
+        scale = w.abs().amax(-1) / 7.0
+    tiny = torch.finfo(torch.float16).tiny
+    scales = scale.clamp(min=tiny).to(torch.float16)
+    s = scales.float()[..., None]
+    if zeros:
+        z = (-lo / scales.float()).round().clamp(0, 15)
+        q = (w / s + z[..., None]).round().clamp(0, 15)
+        z = z.to(torch.uint8)
+    else:
+        z = None
+        q = (w / s).round().clamp(-7, 7) + 8.0
+    q = q.to(torch.uint8).reshape(W.shape)
+    packed = q[..., 0::2] | (q[..., 1::2] << 4)
+    return packed.contiguous(), scales.contiguous(), z
