@@ -1,5 +1,6 @@
 """Argument checks of the expert-layer entry points that need no device, and the
-pages of arithmetic the kernels rely on, checked on the CPU."""
+arithmetic the kernels rely on, checked on the CPU.  Every call here is refused
+before a launch: none passes the checks with an address that is not real."""
 import numpy as np
 import pytest
 
@@ -35,14 +36,12 @@ def test_row_arguments(b):
         b.GEMM_ERR_INVALID_ARG
     # nothing to do, nothing checked on the device
     assert L.gemm_expert_gather(0, 2, 4, 64, None, None, None, None, None) == b.GEMM_OK
-    # a complete call without a device
-    assert L.gemm_expert_gather(4, 2, 4, 64, 16, 16, 16, 16, None) == b.GEMM_ERR_NO_DEVICE
 
 
 @pytest.mark.parametrize("args,status", [
     ((16, 64, 64, 2, 0, 2), 1), ((16, 64, 64, 2, 3, 0), 1), ((-1, 64, 64, 2, 0, 0), 1),
     ((16, 60, 64, 2, 0, 0), 2), ((16, 64, 60, 2, 0, 0), 2), ((16, 64, 64, 0, 0, 0), 1),
-    ((16, 1 << 30, 64, 2, 0, 0), 2), ((16, 64, 64, 2, 0, 0), 5),
+    ((16, 1 << 30, 64, 2, 0, 0), 2),
 ])
 def test_grouped_arguments(b, args, status):
     assert not b.lib().gemm_grouped_create_plan(*args)
@@ -53,7 +52,7 @@ def test_grouped_arguments(b, args, status):
 @pytest.mark.parametrize("args,status", [
     ((1, 64, 256, 48, 0, 1, 1), 1), ((1, 64, 192, 128, 0, 1, 1), 2), ((1, 60, 128, 128, 0, 1, 1), 2),
     ((0, 64, 128, 128, 0, 1, 1), 1), ((1, 64, 128, 128, 0, 2, 1), 1),
-    ((1025, 64, 128, 128, 4, 1, 1), 2), ((1, 64, 128, 128, 0, 1, 1), 5),
+    ((1025, 64, 128, 128, 4, 1, 1), 2),
 ])
 def test_w4_arguments(b, args, status):
     assert not b.lib().gemm_w4_create_plan(*args)

@@ -32,12 +32,11 @@ def _torch():
 
 def _tensor(name, t, shape, dtype, device=None):
     """Raise unless `t` is a contiguous CUDA tensor of this shape and type."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+    if not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA tensor" % name)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
     if device is not None and t.device != device:
         raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, device))
@@ -57,18 +56,26 @@ def _out_dtype(out):
     return (torch.float16, GEMM_OUT_F16) if out == "f16" else (torch.float32, GEMM_OUT_F32)
 
 
-def _on(device):
-    """Context in which `device` is current (the C calls use the current one)."""
-    return _torch().cuda.device(device)
+def _call(fn, device, stream, *args):
+    """fn(*args, stream) with `device` current, on `stream` or the device's
+    current stream; tensors become their addresses.  Raises on an error status."""
+    torch = _torch()
+    args = [a if a is None or type(a) is int else (a.data_ptr() or None) for a in args]
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _launch(fn, device, stream, args)
+    return _launch(fn, device, stream, args)
 
 
-def _stream(device, stream):
-    s = stream if stream is not None else _torch().cuda.current_stream(device)
-    return s.cuda_stream
-
-
-def _ptr(t):
-    return t.data_ptr() if t is not None and t.numel() > 0 else None
+def _launch(fn, device, stream, args):
+    if stream is None:
+        # the handle alone: a Stream object would cost as much as the launch
+        handle = _torch()._C._cuda_getCurrentRawStream(device.index)
+    else:
+        handle = stream.cuda_stream
+    status = fn(*args, handle)
+    if status != 0:
+        _check(status)
 
 
 class ExpertRoute:
@@ -99,10 +106,8 @@ class ExpertRoute:
             self.offsets = torch.empty(self.experts + 1, dtype=torch.int32, device=dev)
             self.order = torch.empty(self.slots, dtype=torch.int32, device=dev)
             self.position = torch.empty((self.tokens, self.topk), dtype=torch.int32, device=dev)
-        with _on(dev):
-            _check(lib().gemm_expert_sort(self.tokens, self.topk, self.experts, _ptr(ids),
-                                          _ptr(self.offsets), _ptr(self.order),
-                                          _ptr(self.position), _stream(dev, stream)))
+        _call(lib().gemm_expert_sort, dev, stream, self.tokens, self.topk, self.experts, ids,
+              self.offsets, self.order, self.position)
         return self
 
     def load(self, offsets, order, position):
@@ -127,17 +132,14 @@ class ExpertRoute:
         width = X.shape[-1]
         _tensor("X", X, (self.tokens, width), torch.float16, dev)
         Xs = _output("out", out, (self.slots, width), torch.float16, dev)
-        with _on(dev):
-            _check(lib().gemm_expert_gather(self.tokens, self.topk, self.experts, width, _ptr(X),
-                                            _ptr(self.offsets), _ptr(self.position), _ptr(Xs),
-                                            _stream(dev, stream)))
+        _call(lib().gemm_expert_gather, dev, stream, self.tokens, self.topk, self.experts, width,
+              X, self.offsets, self.position, Xs)
         return Xs
 
     def combine(self, Ys, out=None, weights=None, stream=None):
         """Y[t] = sum_j weights[t, j] * Ys[position[t, j]] over the slots that are
         not dropped (a plain sum without `weights`).  `out` is fp16 or fp32
         (fp16 when not given)."""
-        torch = _torch()
         dev = self._sorted_on()
         return self._combine(dev, Ys, out, weights, self.offsets, self.position, stream)
 
@@ -155,12 +157,9 @@ class ExpertRoute:
             _tensor("weights", weights, (self.tokens, self.topk), torch.float32, dev)
         dtype = torch.float32 if out is not None and out.dtype == torch.float32 else torch.float16
         Y = _output("out", out, (self.tokens, width), dtype, dev)
-        with _on(dev):
-            _check(lib().gemm_expert_combine(
-                self.tokens, self.topk, self.experts, width, _ptr(Ys), _ptr(offsets),
-                _ptr(position), _ptr(weights),
-                GEMM_OUT_F32 if dtype == torch.float32 else GEMM_OUT_F16, _ptr(Y),
-                _stream(dev, stream)))
+        _call(lib().gemm_expert_combine, dev, stream, self.tokens, self.topk, self.experts, width,
+              Ys, offsets, position, weights,
+              GEMM_OUT_F32 if dtype == torch.float32 else GEMM_OUT_F16, Y)
         return Y
 
     def gather_grad(self, dXs, out=None, stream=None):
@@ -178,11 +177,8 @@ class ExpertRoute:
         _tensor("weights", weights, (self.tokens, self.topk), torch.float32, dev)
         dYs = _output("out", out, (self.slots, width), torch.float16, dev)
         dw = _output("dweights", dweights, (self.tokens, self.topk), torch.float32, dev)
-        with _on(dev):
-            _check(lib().gemm_expert_combine_grad(
-                self.tokens, self.topk, self.experts, width, _ptr(dY), _ptr(Ys),
-                _ptr(self.offsets), _ptr(self.position), _ptr(weights), _ptr(dYs), _ptr(dw),
-                _stream(dev, stream)))
+        _call(lib().gemm_expert_combine_grad, dev, stream, self.tokens, self.topk, self.experts,
+              width, dY, Ys, self.offsets, self.position, weights, dYs, dw)
         return dYs, dw
 
 
@@ -252,9 +248,7 @@ class GroupedPlan(_Handle):
         _tensor("Q", Q, sq, torch.float16, dev)
         _tensor("offsets", offsets, (self.experts + 1,), torch.int32, dev)
         out = _output("out", out, so, self.dtype, dev)
-        with _on(dev):
-            _check(lib().gemm_grouped_run(self._h, _ptr(P), _ptr(Q), _ptr(offsets), _ptr(out),
-                                          _stream(dev, stream)))
+        _call(lib().gemm_grouped_run, dev, stream, self._h, P, Q, offsets, out)
         return out
 
 
@@ -291,9 +285,7 @@ class W4Plan(_Handle):
                 raise ValueError("ids must hold one expert per row (%d)" % self.M)
             _tensor("ids", ids, ids.shape, torch.int32, dev)
         Y = _output("out", out, (self.M, self.N), self.dtype, dev)
-        with _on(dev):
-            _check(lib().gemm_w4_run(self._h, _ptr(X), _ptr(packed), _ptr(scales), _ptr(zeros),
-                                     _ptr(ids), _ptr(Y), _stream(dev, stream)))
+        _call(lib().gemm_w4_run, dev, stream, self._h, X, packed, scales, zeros, ids, Y)
         return Y
 
 
