@@ -52,7 +52,7 @@ def _run(op, rows, N, K, counts, out, make, poison=None):
             Q2[offsets[-1]:] = poison
     plan(device(P2), device(Q2), device(offsets), got[:-1])
     torch.cuda.synchronize()
-    assert plan.device_status() == 0, plan.describe()
+    assert plan.device_status() == 0, tg.gemm_last_error() + "; " + plan.describe()
     assert torch.isnan(got[-1]).all(), "wrote past the end"
     want = _product(op, P, Q, offsets, so)
     mag = _product(op, np.abs(P), np.abs(Q), offsets, so)

@@ -42,7 +42,7 @@ def _run(M, N, K, group, zeros, out, exact, rng):
     plan(device(X), device(packed), device(scales), Y[:-1],
          zeros=device(z) if zeros else None)
     torch.cuda.synchronize()
-    assert plan.device_status() == 0, plan.describe()
+    assert plan.device_status() == 0, tg.gemm_last_error() + "; " + plan.describe()
     assert torch.isnan(Y[-1]).all(), "wrote past the end"
     X = X.astype(np.float64)
     return Y[:-1].cpu().numpy(), X @ w.T, np.abs(X) @ np.abs(w).T, plan.describe()

@@ -1,4 +1,5 @@
-// runtime.cu -- the device check shared by the C entry points.
+// runtime.cu -- the device check and the status record's reader, shared by the C
+// entry points.
 #include <cstdio>
 #include <mutex>
 
@@ -47,6 +48,22 @@ int require_device(int* dev, int* sms, int* smem_optin)
     if (sms) *sms = info.sms;
     if (smem_optin) *smem_optin = info.smem_optin;
     return GEMM_OK;
+}
+
+int read_device_status(DevStatus* record)
+{
+    DevStatus st;
+    cudaError_t e = cudaMemcpy(&st, record, sizeof(st), cudaMemcpyDeviceToHost);
+    if (e != cudaSuccess) return cuda_fail("reading the device status record", e);
+    if (st.code == DEV_OK) return ok();
+    DevStatus zero = {};
+    zero.abort_epoch = st.abort_epoch;  // a stale epoch never matches a new run
+    cudaMemcpy(record, &zero, sizeof(zero), cudaMemcpyHostToDevice);
+    char buf[200];
+    std::snprintf(buf, sizeof(buf),
+                  "kernel wait timed out (where=%d block=%d tile=%d k_block=%d); the run was abandoned",
+                  st.where, st.block, st.tile, st.kblock);
+    return fail(st.code == DEV_TIMEOUT ? GEMM_ERR_TIMEOUT : GEMM_ERR_CUDA, buf);
 }
 
 }  // namespace tg

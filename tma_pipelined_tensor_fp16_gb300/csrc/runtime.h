@@ -11,6 +11,7 @@
 #include <string>
 
 #include "../../include/tmagemm.h"
+#include "gemm_common.h"
 
 namespace tg {
 
@@ -28,6 +29,10 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn();
 // GEMM_ERR_NO_DEVICE when there is none or it is not sm_103.  The attributes
 // are read once per device.
 int require_device(int* dev, int* sms, int* smem_optin);
+
+// Read a plan's device status record after its stream has been synchronised, and
+// clear it: GEMM_OK, GEMM_ERR_TIMEOUT or GEMM_ERR_CUDA.
+int read_device_status(DevStatus* record);
 
 // Launch `kernel` as a programmatic dependent of the work before it on `stream`
 // (clusters of `cluster` CTAs along x when that is above 1).  The kernel

@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "../../include/tmaexperts.h"
+#include "device_common.cuh"
 #include "launch.h"
 #include "ptx.cuh"
 #include "runtime.h"
@@ -31,234 +32,232 @@ struct W4Params {
     const int32_t* ids;
     void* Y;
     int f16out;
+    int tile_rows;         // rows of the weights per CTA (a multiple of 8, up to 128)
+    int wide_scales;       // a stage's scales and zeros of a row are aligned vectors
+    DevStatus* status;
+    int epoch;
+    unsigned long long budget_ns;
 };
 
 // ---------------------------------------------------------------- few rows
 //
-// Both kernels below run the product on mma.sync m16n8k16 with the weights as
-// the 16-row operand and rows of X as the 8-column one: a row of X needs one
-// multiply-add per weight whatever the unit, and on the tensor cores that leaves
-// the conversion of the codes as the only arithmetic.  (tcgen05.mma would need
-// the converted weights written back to shared memory.)
+// Up to 64 rows of X, bound by reading the codes once.  The product runs on
+// tcgen05.mma with 128 rows of the weights as the M side and the rows of X as
+// the N side (16, 32 or 64).
 //
 // A 32-bit word holds the codes k..k+7.  Masking the word and its shift by 8
 // with 0x000f000f and 0x00f000f0 and setting the exponent of 1024 gives half
 // pairs (k, k+4), (k+1, k+5), (k+2, k+6), (k+3, k+7) of 1024 + q or 1024 + 16 q;
 // one half2 add or fused multiply-add makes them q - zero, exact in fp16.  The
-// pairs of X are permuted alike.  Each group is summed in fp32 by the tensor
-// core and enters the row's sum times its scale, so no weight is rounded.
+// operand keeps that order, and X is stored with the same order inside each 8.
 //
-// Weights arrive as blocks of 256 codes a row (128 bytes), 16 rows x 128 bytes
-// per warp and block, swizzled by 16-byte chunk, through asynchronous copies
-// with W4_STAGES - 1 blocks in flight.  Scales are read a block ahead into
-// registers and their lines brought into L2 with the weights' (a DRAM access
-// one block ahead would be waited for in every block: 57 us instead of 32 for
-// one row of 16384 x 16384, groups of 128).
-constexpr int W4_WARPS = 8;
-constexpr int W4_THREADS = W4_WARPS * 32;
-constexpr int W4_ROWS = 16;
-constexpr int W4_BLOCK = 256;  // weights of a row per block: 128 bytes
-constexpr int W4_STAGES = 4;
-constexpr int W4_FEW_STAGES = 3;
-constexpr int W4_STAGE_BYTES = W4_ROWS * W4_BLOCK / 2;
+// No weight is rounded: the tensor core sums whole q - zero of one group into
+// an accumulator of its own, and the group's sum enters the row's sum times its
+// scale in fp32.
+//
+// The converted weights are the MMA's A operand in TMEM: a lane holds a row, so
+// a worker thread converts 128 codes of its row in registers and stores them
+// with tcgen05.st, and shared memory is left to the codes in flight.
+//
+// Roles of a CTA (W4_THREADS = 512), joined by mbarriers only:
+//   warps 0..7    workers, two teams of four warps; warp w owns rows
+//                 32 (w % 4) .. + 31 of the tile.  Team h takes the h-th block of
+//                 128 codes of every stage: converts it into one of A_BUFS
+//                 operands and copies the block's part of X beside it.
+//   warps 8..11   sums: read a block's group sums from TMEM, scale and add them.
+//                 (With the workers doing this after each block, every block
+//                 paid the round trip to the tensor core, about 1500 cycles:
+//                 54 us for one row of 16384 x 16384.)
+//   warps 12, 13  take alternate stages of 256 codes: start the TMA copy of the
+//                 codes, 128 bytes a row, and bring the stage's scales and zero
+//                 points from global memory into a table in shared memory.
+//   warps 14, 15  MMA issuers, one per team (a block's eight MMAs and the waits
+//                 around them take one warp about as long as a team takes to
+//                 convert it); warp 15 allocates TMEM.
+//
+// A tile has up to 128 rows, as few as spread the rows evenly over the SMs;
+// where that is not enough, the CTAs of a cluster share the rows' length, and
+// rank r sums and stores columns r, r + size, ... through distributed shared
+// memory, in rank order.
+//
+// By expert, grid.y is the row of Y.  A row whose expert has a multiple of 16
+// rows before it does that row and the expert's next 15; the others have
+// nothing to do, and nothing has to be sorted.
+constexpr int W4_WORKERS = 8;
+constexpr int W4_SUMMERS = 4;
+constexpr int W4_THREADS = 512;
+constexpr int W4_TEAMS = 2;
+constexpr int W4_TEAM_WARPS = W4_WORKERS / W4_TEAMS;
+constexpr int W4_TILE = 128;
+constexpr int W4_STAGE_K = 256;                       // codes of a row per stage
+constexpr int W4_STAGE_BYTES = W4_TILE * W4_STAGE_K / 2;
+constexpr int W4_BLOCK_K = 128;                       // codes of a row per team and stage
+constexpr int W4_A_COLS = W4_BLOCK_K / 2;             // TMEM columns of an operand
+constexpr int W4_MAX_STAGES = 8;
+constexpr int W4_MAX_BUFS = 4;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
+// Barriers of a team's blocks, in turn.  A wait by parity must not meet a later
+// phase of its barrier: a team is never three blocks ahead of its issuer or of
+// the other team (the operand buffers are a ring of both teams' blocks), so four
+// turns are enough.
+constexpr int W4_TURNS = 4;
 
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool valid)
-{
-    const int bytes = valid ? 16 : 0;  // 0: fill with zeros, nothing is read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                 : "memory");
-}
+// Barrier slots.
+enum : int {
+    W4_WFULL = 0,                             // codes and scales of a stage are there
+    W4_WEMPTY = W4_WFULL + W4_MAX_STAGES,     // every reader is done with them
+    W4_AFULL = W4_WEMPTY + W4_MAX_STAGES,     // [team][turn] a block's operands are written
+    W4_DONE = W4_AFULL + W4_TEAMS * W4_TURNS, // [team][turn] the MMAs have read them
+    W4_GFULL = W4_DONE + W4_TEAMS * W4_TURNS, // a block's group sums are complete
+    W4_GEMPTY = W4_GFULL + W4_MAX_BUFS,       // they have been read
+    W4_DRAIN = W4_GEMPTY + W4_MAX_BUFS,       // [team]
+    W4_BARRIERS = W4_DRAIN + W4_TEAMS
+};
 
-__device__ __forceinline__ void cp_async_commit()
-{
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
+// CTAs per SM.  From 32 columns on the sums need more registers than two CTAs
+// leave.
+__host__ __device__ constexpr int w4_ctas(int cols) { return cols == 16 ? 2 : 1; }
 
-template <int N>
-__device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void mma_m16n8k16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// The same onto zero: the first product of a group.
-__device__ __forceinline__ void mma_m16n8k16_first(float (&d)[4], uint32_t a0, uint32_t a1,
-                                                   uint32_t a2, uint32_t a3, uint32_t b0,
-                                                   uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-}
+template <int NC, int GROUP>
+struct W4Layout {
+    static constexpr int CTAS = w4_ctas(NC);
+    static constexpr int STAGES = CTAS == 2 ? 4 : 8;
+    static constexpr int GPS = W4_STAGE_K / GROUP;          // groups per stage and row
+    static constexpr int GPB = W4_BLOCK_K / GROUP;          // groups per block
+    static constexpr int SUM_COLS = GPB * NC;               // TMEM columns of a block's sums
+    static constexpr int TMEM_COLS = CTAS == 2 ? 256 : 512;
+    static constexpr int A_BUFS = TMEM_COLS - 3 * W4_A_COLS >= 2 * SUM_COLS ? 3 : 2;
+    static constexpr int FIT = (TMEM_COLS - A_BUFS * W4_A_COLS) / SUM_COLS;
+    // accumulator sets in turn, an even number of them so that a set always
+    // belongs to the same team; with a single one the first issuer does all
+    static constexpr int SETS = FIT >= 4 ? 4 : FIT >= 2 ? 2 : 1;
+    static constexpr int ISSUERS = SETS >= 2 ? 2 : 1;
+    static constexpr int X_BYTES = NC * W4_BLOCK_K * 2;     // a block's part of X
+    static constexpr int W = 0;
+    static constexpr int X = W + STAGES * W4_STAGE_BYTES;
+    // [stage][group][row]: the scale's bits, and -(1024 + zero) in fp16 above
+    static constexpr int TABLE = X + A_BUFS * X_BYTES;
+    static constexpr int TABLE_WORDS = GPS * W4_TILE;
+    static constexpr int BARS = TABLE + STAGES * TABLE_WORDS * 4;
+    static constexpr int LIST = BARS + (W4_BARRIERS + 1) * 8;  // rows of Y by expert
+    static constexpr int TOTAL = LIST + 64 + 1024;
+    static_assert(FIT >= 1, "TMEM columns");
+    static_assert(NC * W4_TILE * 4 <= X, "the sums fit the code ring");
+    // 228 KB an SM, 1 KB of it taken by the system per CTA
+    static_assert(TOTAL <= (CTAS == 2 ? 113 : 227) * 1024, "shared memory");
+};
 
 __device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
 __device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
 
-// q - zero of the eight codes of `w` as four half pairs (k, k + 4), (k + 1,
-// k + 5), (k + 2, k + 6), (k + 3, k + 7).  `z` is -(1024 + zero), twice.
-__device__ __forceinline__ void decode8(uint32_t w, __half2 z, uint32_t (&e)[4])
+// q - zero of the eight codes of `w` as half pairs (k, k + 4), (k + 1, k + 5),
+// (k + 2, k + 6), (k + 3, k + 7).  `z` is -(1024 + zero), twice, and z64 -(64 + zero).
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t mask)
 {
-    const __half2 sixteenth = as_half2(0x2c002c00u);               // 1/16
-    const __half2 z64 = __hadd2(z, as_half2(0x63806380u));         // + 960: -(64 + zero)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        e[2 * h] = as_u32(__hadd2(as_half2((w & 0x000f000fu) | 0x64006400u), z));
-        e[2 * h + 1] =
-            as_u32(__hfma2(as_half2((w & 0x00f000f0u) | 0x64006400u), sixteenth, z64));
-        w >>= 8;
-    }
+    // (w & mask) | the exponent of 1024, twice: one instruction, which the
+    // compiler does not make of the expression
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(0x64006400u));
+    return r;
 }
 
-// One warp's ROWS = 16 * RT rows of the weights: the copies into its stage
-// slots and the scales of a block, staged in shared memory as
-// {scale, -(1024 + zero) twice}.
-template <int GROUP, int RT>
-struct W4Rows {
-    static constexpr int ROWS = W4_ROWS * RT;
-    static constexpr int GPS = W4_BLOCK / GROUP;  // groups per block and row
-    static constexpr int SCALES = ROWS * GPS;
-    static constexpr int EPL = SCALES / 32;       // scales a lane handles per block
-    static constexpr int SLOT_BYTES = RT * W4_STAGE_BYTES;
-    const uint8_t* packed;  // this lane's first chunk: row lane / 8, chunk lane % 8
-    const __half* scales;   // this lane's first scale: row lane / GPS, group lane % GPS
-    const uint8_t* zeros;   // alike, or nullptr
-    int rows;               // rows that exist (0..ROWS)
-    int half_k;             // bytes of a row
-    int groups;             // groups of a row
-    int whole;              // blocks below this need no check
-    uint32_t lane;
-    uint32_t dst[2];        // slot offset of the lane's even and odd chunks
-    uint32_t ahead[EPL];    // scale bits | zero << 16
-
-    __device__ __forceinline__ void init(const W4Params& p, int expert, int n0, uint32_t lane_)
-    {
-        lane = lane_;
-        groups = p.K / GROUP;
-        half_k = p.K / 2;
-        rows = p.N - n0 < ROWS ? p.N - n0 : ROWS;
-        if (rows < 0) rows = 0;
-        whole = rows == ROWS ? p.K / W4_BLOCK : 0;
-        const int64_t row = static_cast<int64_t>(expert) * p.N + (rows > 0 ? n0 : 0);
-        const int r = static_cast<int>(lane >> 3), c = static_cast<int>(lane & 7u);
-        packed = p.packed + (row + r) * half_k + c * 16;
-        const int64_t at = (row + lane / GPS) * groups + lane % GPS;
-        scales = p.scales + at;
-        zeros = p.zeros ? p.zeros + at : nullptr;
-        dst[0] = r * 128 + ((c ^ r) << 4);
-        dst[1] = (r + 4) * 128 + ((c ^ (r + 4)) << 4);
-    }
-
-    __device__ __forceinline__ void copy_block(uint32_t slot, int kb) const
-    {
-        const uint8_t* src = packed + kb * (W4_BLOCK / 2);
-        const int64_t next = static_cast<int64_t>(half_k) * 4;
-        if (kb < whole) {
-#pragma unroll
-            for (int i = 0; i < SLOT_BYTES / 512; ++i) {
-                cp_async16(slot + dst[i & 1] + (i / 2) * 1024, src);
-                src += next;
-            }
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < SLOT_BYTES / 512; ++i) {
-            const int row = static_cast<int>(lane >> 3) + 4 * i;
-            const int byte = kb * (W4_BLOCK / 2) + static_cast<int>(lane & 7u) * 16;
-            const bool ok = row < rows && byte < half_k;
-            cp_async16_or_zero(slot + dst[i & 1] + (i / 2) * 1024, src + i * next, ok);
-        }
-    }
-
-    // Whether the lane's i-th scale of block kb exists.
-    __device__ __forceinline__ bool exists(int kb, int i) const
-    {
-        const int id = static_cast<int>(lane) + 32 * i;
-        return kb < whole || (id / GPS < rows && kb * GPS + id % GPS < groups);
-    }
-
-    __device__ __forceinline__ int64_t index(int kb, int i) const
-    {
-        return static_cast<int64_t>(i) * (32 / GPS) * groups + kb * GPS;
-    }
-
-    // Into L2; one 32-byte sector holds 16 scales of a row.
-    __device__ __forceinline__ void touch_scales(int kb) const
-    {
-        if (kb % (16 / GPS) != 0) return;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            if (!exists(kb, i)) continue;
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(scales + index(kb, i)));
-            if (zeros) asm volatile("prefetch.global.L2 [%0];" ::"l"(zeros + index(kb, i)));
-        }
-    }
-
-    __device__ __forceinline__ void load_scales(int kb)
-    {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            ahead[i] = 8u << 16;
-            if (exists(kb, i)) {
-                const int64_t at = index(kb, i);
-                ahead[i] = __half_as_ushort(scales[at]);
-                ahead[i] |= (zeros ? zeros[at] : 8u) << 16;
-            }
-        }
-    }
-
-    __device__ __forceinline__ void stage_scales(uint2* buf) const
-    {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const float s =
-                __half2float(__ushort_as_half(static_cast<unsigned short>(ahead[i] & 0xffffu)));
-            const __half2 z = __float2half2_rn(-1024.0f - static_cast<float>(ahead[i] >> 16));
-            buf[lane + 32 * i] = make_uint2(__float_as_uint(s), as_u32(z));
-        }
-    }
-};
-
-// The products of 16 rows with 32 codes each: e and f are decode8 of the words of
-// rows g and g + 8, v the same positions of X in decode8's order.
-__device__ __forceinline__ void mma_word(float (&d)[4], bool first, const uint32_t (&e)[4],
-                                         const uint32_t (&f)[4], const uint4& v)
+__device__ __forceinline__ void decode8(uint32_t w, __half2 z, __half2 z64, uint32_t* e)
 {
-    if (first)
-        mma_m16n8k16_first(d, e[0], f[0], e[2], f[2], v.x, v.y);
-    else
-        mma_m16n8k16(d, e[0], f[0], e[2], f[2], v.x, v.y);
-    mma_m16n8k16(d, e[1], f[1], e[3], f[3], v.z, v.w);
+    const __half2 sixteenth = as_half2(0x2c002c00u);
+    const uint32_t v = w >> 8;
+    e[0] = as_u32(__hadd2(as_half2(code_pair(w, 0x000f000fu)), z));
+    e[1] = as_u32(__hfma2(as_half2(code_pair(w, 0x00f000f0u)), sixteenth, z64));
+    e[2] = as_u32(__hadd2(as_half2(code_pair(v, 0x000f000fu)), z));
+    e[3] = as_u32(__hfma2(as_half2(code_pair(v, 0x00f000f0u)), sixteenth, z64));
 }
 
-// X[k..k+7] as decode8 orders the codes: pairs (k, k+4), (k+2, k+6), (k+1, k+5),
-// (k+3, k+7).
+// X[k..k+7] in the same order.
 __device__ __forceinline__ uint4 order_x(const uint4& v)
 {
-    return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.y, v.w, 0x5410),
-                      __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x7632));
+    return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                      __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
 }
 
-__device__ __forceinline__ void add_scaled(float (&acc)[4], const float (&part)[4], uint32_t s0,
-                                           uint32_t s1)
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
 {
-    acc[0] = fmaf(__uint_as_float(s0), part[0], acc[0]);
-    acc[1] = fmaf(__uint_as_float(s0), part[1], acc[1]);
-    acc[2] = fmaf(__uint_as_float(s1), part[2], acc[2]);
-    acc[3] = fmaf(__uint_as_float(s1), part[3], acc[3]);
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
+}
+
+// TMEM -> registers, 32 lanes x 16 columns, complete on return.
+__device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// Registers -> TMEM, 32 lanes x 8 columns.  (One store of 32 columns ties 32
+// registers together; its moves made the conversion a tenth slower.)
+__device__ __forceinline__ void tmem_store_8cols(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// One lane of a converged warp (the same one every time): 1 there, else 0.
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t"
+        ".reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "}\n"
+        : "=r"(r));
+    return r;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, fp16 x fp16 -> fp32, issued by the lane with
+// `elected` set.  The whole warp executes the statement: without a branch around
+// it the operands stay in uniform registers (behind `if (lane == 0)` the issue of
+// a block's eight MMAs took 950 cycles, more than their conversion).
+__device__ __forceinline__ void mma_f16_ts(uint32_t elected, uint32_t d_tmem, uint32_t a_tmem,
+                                           uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t"
+        ".reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "setp.ne.b32 q, %4, 0;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t"
+        "}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_elected(uint32_t elected, uint32_t bar)
+{
+    asm volatile(
+        "{\n\t"
+        ".reg .pred p;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t"
+        "}\n" ::"r"(bar),
+        "r"(elected)
+        : "memory");
 }
 
 __device__ __forceinline__ void store_y(const W4Params& p, int64_t row, int n, float v)
@@ -270,366 +269,426 @@ __device__ __forceinline__ void store_y(const W4Params& p, int64_t row, int n, f
         static_cast<float*>(p.Y)[at] = v;
 }
 
-__device__ __forceinline__ float ld_shared_rank(const float* local, uint32_t rank)
-{
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                 : "=f"(v)
-                 : "r"(map_shared_rank(smem_u32(local), rank))
-                 : "memory");
-    return v;
-}
+// A bounded wait that leaves the issue slots to the warps that work: the hint
+// lets the hardware suspend the thread for up to 100 us at a time.
+struct W4Wait : Watchdog {
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, int where, int tile, int kb)
+    {
+        if (aborted) return false;
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = globaltimer_ns();
+        while (true) {
+            uint32_t done;
+            asm volatile(
+                "{\n\t"
+                ".reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t"
+                "}\n"
+                : "=r"(done)
+                : "r"(bar), "r"(parity), "r"(100000u)
+                : "memory");
+            if (done) return true;
+            if (peer_aborted()) {
+                aborted = true;
+                return false;
+            }
+            if (globaltimer_ns() - t0 > budget_ns) {
+                record(where, tile, kb);
+                return false;
+            }
+        }
+    }
+};
 
-// Up to eight rows of X (and, by expert, eight at a time).  Bound by reading the
-// codes once.  A CTA owns 16 * RT rows of the weights and its eight warps take
-// every eighth block of them, so that neighbouring warps read neighbouring
-// 128-byte pieces of a row; no barrier joins the warps before the final sum.
-// Where the rows alone leave SMs idle, the CTAs of a cluster share the rows'
-// length and their sums meet through distributed shared memory, in rank order.
-//
-// By expert, grid.y is the row of Y: the first row of an expert does all of
-// them, so an expert's weights are read once per eight rows, and nothing has to
-// be sorted.
-constexpr int W4_FEW = 8;
-constexpr int W4_FEW_RT = 2;
-
-template <int GROUP, int RT>
-__host__ __device__ constexpr int w4_few_smem()
+template <int NC, int GROUP>
+__global__ void __launch_bounds__(W4_THREADS, W4Layout<NC, GROUP>::CTAS)
+    k_w4(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ W4Params p)
 {
-    return W4_WARPS * (W4_FEW_STAGES * RT * W4_STAGE_BYTES +
-                       2 * RT * W4_ROWS * (W4_BLOCK / GROUP) * 8);
-}
-
-template <int GROUP, int RT>
-__global__ void __launch_bounds__(W4_THREADS, 2)
-    k_w4_few(const __grid_constant__ W4Params p)
-{
-    using Rows = W4Rows<GROUP, RT>;
-    constexpr int STAGES = W4_FEW_STAGES;
-    constexpr int WARP_BYTES = STAGES * Rows::SLOT_BYTES;
-    extern __shared__ __align__(128) uint8_t w4_smem[];
-    __shared__ int list[W4_FEW];
-    __shared__ int list_count;
+    using L = W4Layout<NC, GROUP>;
+    constexpr int STAGES = L::STAGES, A_BUFS = L::A_BUFS, SETS = L::SETS;
+    constexpr int GPS = L::GPS, GPB = L::GPB;
+    constexpr int XPT = NC * (W4_BLOCK_K / 8) / 128;  // chunks of X per worker and block
+    extern __shared__ __align__(1024) uint8_t w4_smem[];
+    const uint32_t raw = smem_u32(w4_smem);
+    const uint32_t base = align1024(raw);
+    uint8_t* gen = w4_smem + (base - raw);
+    const uint32_t bars = base + L::BARS;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gen + L::BARS + W4_BARRIERS * 8);
+    int* list = reinterpret_cast<int*>(gen + L::LIST);
     const int tid = static_cast<int>(threadIdx.x);
     const int warp = tid >> 5;
     const uint32_t lane = lane_id();
-    const int g = static_cast<int>(lane >> 2), t = static_cast<int>(lane & 3u);
-    uint8_t* ring = w4_smem + warp * WARP_BYTES;
-    uint2* scale_buf =
-        reinterpret_cast<uint2*>(w4_smem + W4_WARPS * WARP_BYTES) + warp * 2 * Rows::SCALES;
-    float* partial = reinterpret_cast<float*>(w4_smem);      // [warps][8][ROWS] after the loop
-    float* sums = partial + W4_WARPS * W4_FEW * Rows::ROWS;  // [8][ROWS]
     const uint32_t csize = gridDim.z, crank = blockIdx.z;
-    const int n0 = static_cast<int>(blockIdx.x) * Rows::ROWS;
+    const int n0 = static_cast<int>(blockIdx.x) * p.tile_rows;
+    auto bar = [&](int slot) { return bars + static_cast<uint32_t>(slot) * 8u; };
+    W4Wait wd;
+    wd.st = p.status;
+    wd.epoch = p.epoch;
+    wd.budget_ns = p.budget_ns;
+    wd.aborted = false;
     griddep_wait();
     griddep_launch_dependents();
 
-    int expert = 0;
+    // the rows of Y of this CTA
+    int expert = 0, count = p.M;
     if (p.experts > 0) {
-        expert = p.ids[blockIdx.y];
+        const int first = static_cast<int>(blockIdx.y);
+        expert = p.ids[first];
         if (expert < 0 || expert >= p.experts) {  // a dropped row
-            if (crank == 0 && tid < Rows::ROWS && n0 + tid < p.N)
-                store_y(p, blockIdx.y, n0 + tid, 0.0f);
+            if (crank == 0 && tid < p.tile_rows && n0 + tid < p.N)
+                store_y(p, first, n0 + tid, 0.0f);
             return;
         }
-        bool earlier = false;
-        for (int r = tid; r < static_cast<int>(blockIdx.y); r += W4_THREADS)
-            earlier |= p.ids[r] == expert;
-        if (__syncthreads_or(earlier)) return;
-    }
-    Rows rows;
-    rows.init(p, expert, n0, lane);
-    const int blocks = (p.K + W4_BLOCK - 1) / W4_BLOCK;
-    const int step = W4_WARPS * static_cast<int>(csize);
-    const int kb0 = static_cast<int>(crank) * W4_WARPS + warp;
-
-    int next_row = p.experts > 0 ? static_cast<int>(blockIdx.y) : 0;
-    while (next_row < p.M) {
-        // the rows of Y of this pass
-        if (p.experts > 0) {
-            if (warp == 0) {
-                int found = 0;
-                for (int r = next_row; r < p.M && found < W4_FEW; r += 32) {
-                    const int i = r + static_cast<int>(lane);
-                    const unsigned hit = __ballot_sync(0xffffffffu, i < p.M && p.ids[i] == expert);
-                    const int slot = found + __popc(hit & ((1u << lane) - 1u));
-                    if (((hit >> lane) & 1u) && slot < W4_FEW) list[slot] = i;
-                    found += __popc(hit);
-                }
-                if (lane == 0) list_count = found < W4_FEW ? found : W4_FEW;
+        int before = 0;
+        for (int r = tid; r - tid < first; r += W4_THREADS)
+            before += __syncthreads_count(r < first && p.ids[r] == expert);
+        if (before % 16 != 0) return;
+        if (warp == 0) {
+            int found = 0;
+            for (int r = first; r < p.M && found < 16; r += 32) {
+                const int i = r + static_cast<int>(lane);
+                const unsigned hit = __ballot_sync(0xffffffffu, i < p.M && p.ids[i] == expert);
+                const int slot = found + __popc(hit & ((1u << lane) - 1u));
+                if (((hit >> lane) & 1u) && slot < 16) list[slot] = i;
+                found += __popc(hit);
             }
-            __syncthreads();
+            if (lane < 16 && static_cast<int>(lane) >= found) list[lane] = -1;
         }
-        const int left = p.M - next_row;
-        const int count = p.experts > 0 ? list_count : (left < W4_FEW ? left : W4_FEW);
-        if (count == 0) break;
-        // columns past the last row repeat the first one and are not stored
-        const int column = g < count ? g : 0;
-        const int xrow = p.experts > 0 ? list[column] : next_row + column;
-        const __half* x = p.X + static_cast<int64_t>(xrow / p.share) * p.K + 8 * t;
+    }
+    const int stages = (p.K + W4_STAGE_K - 1) / W4_STAGE_K;
+    const int s_begin = static_cast<int>(static_cast<int64_t>(stages) * crank / csize);
+    const int s_end = static_cast<int>(static_cast<int64_t>(stages) * (crank + 1) / csize);
 
-        float acc[RT][4];
+    if (warp == 14 && lane == 0) {
+        prefetch_tensormap(&tmW);
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(bar(W4_WFULL + i), 2);  // the copy's announcement, the table
+            mbar_init(bar(W4_WEMPTY + i), W4_WORKERS + W4_SUMMERS);
+        }
+        for (int i = 0; i < W4_TEAMS * W4_TURNS; ++i) {
+            mbar_init(bar(W4_AFULL + i), W4_TEAM_WARPS);
+            mbar_init(bar(W4_DONE + i), 1);
+        }
+        for (int i = 0; i < SETS; ++i) {
+            mbar_init(bar(W4_GFULL + i), 1);
+            mbar_init(bar(W4_GEMPTY + i), W4_SUMMERS);
+        }
+        for (int i = 0; i < W4_TEAMS; ++i) mbar_init(bar(W4_DRAIN + i), 1);
+        fence_mbar_init();
+    }
+    if (warp == 15) {
+        tmem_alloc(smem_u32(tmem_slot), L::TMEM_COLS);
+        tmem_relinquish_alloc_permit();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    if (p.experts > 0) {
+        count = 0;
+        while (count < 16 && list[count] >= 0) ++count;
+    }
+    float acc[NC];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[rt][i] = 0.0f;
+    for (int i = 0; i < NC; ++i) acc[i] = 0.0f;
+    const int q = warp & 3;  // workers and sums: TMEM lane quarter
+    const int row = 32 * q + static_cast<int>(lane);
+    const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+    const uint32_t sum_tmem = tmem_base + A_BUFS * W4_A_COLS;
 
-        // one block: FULL blocks lie inside K
-        auto block = [&](auto full, int kb, const uint8_t* slot, const uint2* sc) {
-            constexpr bool FULL = decltype(full)::value;
-            constexpr int PER = GROUP / 32;
-            const uint32_t* a = reinterpret_cast<const uint32_t*>(slot + g * 128) + t;
-            float part[RT][4];
-            uint2 s[RT][2];
+    if (warp < W4_WORKERS) {
+        // -------------------------------------------------------- workers
+        const int team = warp >> 2;
+        // X: row m0, chunk c0 of the block's 16, then rows m0 + 8, m0 + 16, ...;
+        // two operand tiles of 64 codes.  By expert there are two rows a thread
+        // at most, so a first row and a distance describe them too.
+        const int m0 = (tid & 127) >> 4, c0 = tid & 15;
+        const uint32_t xdst = base + L::X + static_cast<uint32_t>(
+            (c0 >> 3) * NC * 128 + m0 * 128 + (((c0 & 7) ^ m0) << 4));
+        static_assert(XPT * 8 == NC, "rows of a thread");
+        const __half* x = p.X;
+        int64_t xnext = static_cast<int64_t>(p.K) * 8;
+        if (m0 < count) {
+            const int y = p.experts > 0 ? list[m0] : m0;
+            x = p.X + static_cast<int64_t>(y / p.share) * p.K + c0 * 8;
+            if (p.experts > 0 && m0 + 8 < count)
+                xnext = static_cast<int64_t>(list[m0 + 8] / p.share - y / p.share) * p.K;
+        }
+        const bool has_x = 2 * q < count;  // a warp holds rows 2 q, 2 q + 1 and 8, 16, ... on
+        int left = p.K - (s_begin * W4_STAGE_K + team * W4_BLOCK_K);  // codes from this block on
+        x += s_begin * W4_STAGE_K + team * W4_BLOCK_K;
+        uint4 xv[XPT];
+        auto load_x = [&] {  // zeros past K
 #pragma unroll
-            for (int j = 0; j < W4_BLOCK / 32; ++j) {
-                const int k = kb * W4_BLOCK + j * 32;
-                if (!FULL && k >= p.K) break;
-                const uint4 v = order_x(*reinterpret_cast<const uint4*>(x + k));
-                const int chunk = (g * 4) ^ (j * 4);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    if (j % PER == 0) {
-                        s[rt][0] = sc[(rt * 16 + g) * Rows::GPS + j / PER];
-                        s[rt][1] = sc[(rt * 16 + g + 8) * Rows::GPS + j / PER];
-                    }
-                    uint32_t e[4], f[4];
-                    decode8(a[rt * 512 + chunk], as_half2(s[rt][0].y), e);
-                    decode8(a[rt * 512 + 256 + chunk], as_half2(s[rt][1].y), f);
-                    mma_word(part[rt], j % PER == 0, e, f, v);
-                    if (j % PER == PER - 1) add_scaled(acc[rt], part[rt], s[rt][0].x, s[rt][1].x);
-                }
+            for (int i = 0; i < XPT; ++i) {
+                xv[i] = make_uint4(0, 0, 0, 0);
+                if (m0 + 8 * i < count && c0 * 8 < left)
+                    xv[i] = *reinterpret_cast<const uint4*>(x + i * xnext);
             }
         };
-
+        if (has_x) load_x();
+        const uint32_t sw = static_cast<uint32_t>(row & 7) << 4;
+        const uint32_t a_tmem = tmem_base + lanes;
+        // ring positions and their phases
+        int ws = 0, buf = team % A_BUFS, n = 0;
+        uint32_t ws_phase = 0;
+        const uint32_t* words = reinterpret_cast<const uint32_t*>(gen + L::TABLE) +
+                                team * GPB * W4_TILE + row;
+        const uint32_t src0 = base + L::W + row * 128;
+        for (int s = s_begin; s < s_end; ++s) {
+            const bool work = left > 0;  // the last stage may end in the first team's block
+            wd.wait(bar(W4_WFULL + ws), ws_phase, WAIT_FULL, s, 0);
+            if (work) {
+                __half2 zero[GPB];
 #pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i) {
-            const int kb = kb0 + i * step;
-            if (kb < blocks) {
-                rows.copy_block(smem_u32(ring + i * Rows::SLOT_BYTES), kb);
-                rows.touch_scales(kb);
+                for (int i = 0; i < GPB; ++i)
+                    zero[i] = as_half2(
+                        __byte_perm(words[ws * L::TABLE_WORDS + i * W4_TILE], 0u, 0x3232));
+                const uint32_t src = src0 + ws * W4_STAGE_BYTES;
+                // the block that had this buffer before: A_BUFS blocks ago
+                const int other = A_BUFS % 2 == 1 ? team ^ 1 : team;
+                const int m = A_BUFS % 2 == 1 ? n - (A_BUFS + 1) / 2 + team : n - A_BUFS / 2;
+                if (m >= 0)
+                    wd.wait(bar(W4_DONE + other * W4_TURNS + m % W4_TURNS),
+                            static_cast<uint32_t>(m / W4_TURNS) & 1u, WAIT_EMPTY, s, m);
+                const uint32_t a_block = a_tmem + static_cast<uint32_t>(buf * W4_A_COLS);
+#pragma unroll
+                for (int c = 0; c < W4_BLOCK_K / 32; ++c) {  // 32 codes at a time
+                    const uint4 w =
+                        ld_shared_v4(src + ((static_cast<uint32_t>(team * 64 + c * 16)) ^ sw));
+                    const __half2 z = zero[c * 32 / GROUP];
+                    const __half2 z64 = __hadd2(z, as_half2(0x63806380u));
+                    uint32_t e[8];
+                    decode8(w.x, z, z64, e);
+                    decode8(w.y, z, z64, e + 4);
+                    tmem_store_8cols(a_block + c * 16, e);
+                    decode8(w.z, z, z64, e);
+                    decode8(w.w, z, z64, e + 4);
+                    tmem_store_8cols(a_block + c * 16 + 8, e);
+                }
+                if (has_x) {
+#pragma unroll
+                    for (int i = 0; i < XPT; ++i) {
+                        if (m0 + 8 * i >= count) continue;
+                        const uint4 v = order_x(xv[i]);
+                        st_shared_v4(xdst + buf * L::X_BYTES + i * 8 * 128, v.x, v.y, v.z, v.w);
+                    }
+                    fence_proxy_async_smem();
+                }
+                tmem_wait_st();
+                tc_fence_before_sync();
             }
-            cp_async_commit();
-        }
-        if (kb0 < blocks) rows.load_scales(kb0);
-        int stage = 0, parity = 0;
-        for (int kb = kb0; kb < blocks; kb += step) {
-            const int far = kb + (STAGES - 1) * step;
-            if (far < blocks) {
-                const int slot = stage == 0 ? STAGES - 1 : stage - 1;
-                rows.copy_block(smem_u32(ring + slot * Rows::SLOT_BYTES), far);
-                rows.touch_scales(far);
-            }
-            cp_async_commit();
-            uint2* sc = scale_buf + parity * Rows::SCALES;
-            rows.stage_scales(sc);
-            if (kb + step < blocks) rows.load_scales(kb + step);
-            cp_async_wait<STAGES - 1>();
             __syncwarp();
-            const uint8_t* slot = ring + stage * Rows::SLOT_BYTES;
-            if ((kb + 1) * W4_BLOCK <= p.K)
-                block(std::true_type(), kb, slot, sc);
-            else
-                block(std::false_type(), kb, slot, sc);
+            if (lane == 0) {
+                if (work) mbar_arrive(bar(W4_AFULL + team * W4_TURNS + n % W4_TURNS));
+                mbar_arrive(bar(W4_WEMPTY + ws));
+            }
+            left -= W4_STAGE_K;
+            if (has_x) {
+                x += W4_STAGE_K;
+                load_x();
+            }
+            if (++ws == STAGES) {
+                ws = 0;
+                ws_phase ^= 1u;
+            }
+            ++n;
+            buf += W4_TEAMS;
+            if (buf >= A_BUFS) buf -= A_BUFS;
+        }
+    } else if (warp < W4_WORKERS + W4_SUMMERS) {
+        // ----------------------------------------------------------- sums
+        int ws = 0, set = 0;
+        uint32_t ws_phase = 0, set_phase = 0;
+        const uint32_t* words = reinterpret_cast<const uint32_t*>(gen + L::TABLE) + row;
+        int left = p.K - s_begin * W4_STAGE_K;
+        for (int s = s_begin; s < s_end; ++s) {
+            wd.wait(bar(W4_WFULL + ws), ws_phase, WAIT_FULL, s, 4);
+            float scale[GPS];
+#pragma unroll
+            for (int i = 0; i < GPS; ++i)
+                scale[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(
+                    words[ws * L::TABLE_WORDS + i * W4_TILE] & 0xffffu)));
             __syncwarp();
-            if (++stage == STAGES) stage = 0;
-            parity ^= 1;
-        }
-        cp_async_wait<0>();
-        __syncthreads();
-
-        // sum over the warps, then over the CTAs that share the length, in order
+            if (lane == 0) mbar_arrive(bar(W4_WEMPTY + ws));
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+            for (int part = 0; part < 2; ++part) {
+                if (left <= part * W4_BLOCK_K) break;
+                wd.wait(bar(W4_GFULL + set), set_phase, WAIT_TMEM_FULL, s, part);
+                tc_fence_after_sync();
+                const uint32_t from = sum_tmem + lanes + static_cast<uint32_t>(set * L::SUM_COLS);
+                if constexpr (L::SUM_COLS == 16) {
+                    uint32_t v[16];
+                    tmem_load_16cols(from, v);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                partial[(warp * W4_FEW + 2 * t + (i & 1)) * Rows::ROWS + rt * 16 + g +
-                        8 * (i >> 1)] = acc[rt][i];
-        __syncthreads();
-        float v = 0.0f;
-        static_assert(W4_FEW * Rows::ROWS <= W4_THREADS, "one sum per thread");
-        if (tid < W4_FEW * Rows::ROWS) {
+                    for (int j = 0; j < 16; ++j)
+                        acc[j] = fmaf(scale[part], __uint_as_float(v[j]), acc[j]);
+                } else {
 #pragma unroll
-            for (int w = 0; w < W4_WARPS; ++w) v += partial[w * W4_FEW * Rows::ROWS + tid];
-            if (csize > 1) sums[tid] = v;
-        }
-        if (csize > 1) cluster_sync_all();
-        const int c = tid / Rows::ROWS, n = n0 + tid % Rows::ROWS;
-        if (crank == 0 && c < count && n < p.N) {
-            for (uint32_t r = 1; r < csize; ++r) v += ld_shared_rank(sums + tid, r);
-            store_y(p, p.experts > 0 ? list[c] : next_row + c, n, v);
-        }
-        const int last = p.experts > 0 ? list[count - 1] : next_row + count - 1;
-        if (csize > 1)
-            cluster_sync_all();  // rank 0 has read its peers' sums
-        else
-            __syncthreads();
-        if (count < W4_FEW) break;
-        next_row = last + 1;
-    }
-}
-
-// 9 to 64 rows of X, COLS = 16, 32 or 64.  Every code now feeds COLS / 8 MMAs
-// and X is read as often as the weights: a CTA owns 128 rows of the weights (16
-// per warp) and keeps the block's part of X in shared memory for all of them, in
-// decode8's order, read a block ahead through registers.  The CTAs of a cluster
-// share the rows' length where the rows alone leave SMs idle; rank r then sums
-// and stores columns r, r + size, ....
-constexpr int W4_TILE = W4_WARPS * W4_ROWS;
-// Bytes between rows of X in shared memory: 256 halves and 64 bytes more, so
-// that the two rows a quarter of a warp reads at once lie in different banks.
-constexpr int W4_X_PITCH = W4_BLOCK * 2 + 64;
-
-template <int COLS, int GROUP>
-__host__ __device__ constexpr int w4_tile_smem()
-{
-    return W4_WARPS * (W4_STAGES * W4_STAGE_BYTES + 2 * W4_ROWS * (W4_BLOCK / GROUP) * 8) +
-           2 * COLS * W4_X_PITCH;
-}
-
-template <int COLS, int GROUP>
-__global__ void __launch_bounds__(W4_THREADS, 1)
-    k_w4_tile(const __grid_constant__ W4Params p)
-{
-    using Rows = W4Rows<GROUP, 1>;
-    constexpr int NT = COLS / 8;
-    constexpr int STAGES = W4_STAGES;
-    constexpr int XPT = COLS * (W4_BLOCK / 8) / W4_THREADS;  // chunks of X per thread and block
-    constexpr int SUM_PITCH = W4_TILE + 4;  // floats between columns of the sums
-    constexpr int WARP_BYTES = STAGES * Rows::SLOT_BYTES;
-    static_assert(COLS * SUM_PITCH * 4 <= W4_WARPS * WARP_BYTES, "sums fit the ring");
-    extern __shared__ __align__(128) uint8_t w4_smem[];
-    const int tid = static_cast<int>(threadIdx.x);
-    const int warp = tid >> 5;
-    const uint32_t lane = lane_id();
-    const int g = static_cast<int>(lane >> 2), t = static_cast<int>(lane & 3u);
-    uint8_t* ring = w4_smem + warp * WARP_BYTES;
-    uint8_t* xbuf = w4_smem + W4_WARPS * WARP_BYTES;
-    uint2* scale_buf =
-        reinterpret_cast<uint2*>(xbuf + 2 * COLS * W4_X_PITCH) + warp * 2 * Rows::SCALES;
-    float* sums = reinterpret_cast<float*>(w4_smem);  // [COLS][SUM_PITCH] after the loop
-    const uint32_t csize = gridDim.z, crank = blockIdx.z;
-    griddep_wait();
-    griddep_launch_dependents();
-
-    Rows rows;
-    rows.init(p, 0, static_cast<int>(blockIdx.x) * W4_TILE + warp * W4_ROWS, lane);
-    const int blocks = (p.K + W4_BLOCK - 1) / W4_BLOCK;
-    const int step = static_cast<int>(csize);
-    const int kb0 = static_cast<int>(crank);
-    // rows past the last one repeat it and are not stored
-    uint4 xa[XPT];
-    auto load_x = [&](int kb) {
+                    for (int c = 0; c < L::SUM_COLS; c += 32) {
+                        uint32_t v[32];
+                        tmem_load_32cols(from + c, v);
 #pragma unroll
-        for (int i = 0; i < XPT; ++i) {
-            const int id = tid + W4_THREADS * i;
-            int m = id / (W4_BLOCK / 8);
-            if (m >= p.M) m = p.M - 1;
-            const int k = kb * W4_BLOCK + id % (W4_BLOCK / 8) * 8;
-            xa[i] = make_uint4(0, 0, 0, 0);
-            if (k < p.K)
-                xa[i] = *reinterpret_cast<const uint4*>(p.X + static_cast<int64_t>(m) * p.K + k);
-        }
-    };
-    float acc[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-        const int kb = kb0 + s * step;
-        if (kb < blocks) {
-            rows.copy_block(smem_u32(ring + s * Rows::SLOT_BYTES), kb);
-            rows.touch_scales(kb);
-        }
-        cp_async_commit();
-    }
-    if (kb0 < blocks) {
-        rows.load_scales(kb0);
-        load_x(kb0);
-    }
-    int stage = 0, parity = 0;
-    for (int kb = kb0; kb < blocks; kb += step) {
-        const int far = kb + (STAGES - 1) * step;
-        if (far < blocks) {
-            const int slot = stage == 0 ? STAGES - 1 : stage - 1;
-            rows.copy_block(smem_u32(ring + slot * Rows::SLOT_BYTES), far);
-            rows.touch_scales(far);
-        }
-        cp_async_commit();
-        uint2* sc = scale_buf + parity * Rows::SCALES;
-        rows.stage_scales(sc);
-        uint8_t* xs = xbuf + parity * COLS * W4_X_PITCH;
-#pragma unroll
-        for (int i = 0; i < XPT; ++i) {
-            const int id = tid + W4_THREADS * i;
-            *reinterpret_cast<uint4*>(xs + id / (W4_BLOCK / 8) * W4_X_PITCH +
-                                      id % (W4_BLOCK / 8) * 16) = order_x(xa[i]);
-        }
-        if (kb + step < blocks) {
-            rows.load_scales(kb + step);
-            load_x(kb + step);
-        }
-        cp_async_wait<STAGES - 1>();
-        // X and the scales of this block are staged; those of the block before
-        // the last are used up, so their buffers may be written next time
-        __syncthreads();
-        const uint32_t* a = reinterpret_cast<const uint32_t*>(ring + stage * Rows::SLOT_BYTES +
-                                                              g * 128) + t;
-        const uint8_t* xg = xs + g * W4_X_PITCH + t * 16;
-        constexpr int PER = GROUP / 32;
-        float part[NT][4];
-        uint2 s0, s1;
-#pragma unroll
-        for (int j = 0; j < W4_BLOCK / 32; ++j) {
-            if (kb * W4_BLOCK + j * 32 >= p.K) break;
-            if (j % PER == 0) {
-                s0 = sc[g * Rows::GPS + j / PER];
-                s1 = sc[(g + 8) * Rows::GPS + j / PER];
+                        for (int j = 0; j < 32; ++j)
+                            acc[(c + j) % NC] = fmaf(scale[part * GPB + (c + j) / NC],
+                                                     __uint_as_float(v[j]), acc[(c + j) % NC]);
+                    }
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(W4_GEMPTY + set));
+                if (++set == SETS) {
+                    set = 0;
+                    set_phase ^= 1u;
+                }
             }
-            uint32_t e[4], f[4];
-            const int chunk = (g * 4) ^ (j * 4);
-            decode8(a[chunk], as_half2(s0.y), e);
-            decode8(a[256 + chunk], as_half2(s1.y), f);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                mma_word(part[nt], j % PER == 0, e, f,
-                         *reinterpret_cast<const uint4*>(xg + nt * 8 * W4_X_PITCH + j * 64));
-            if (j % PER == PER - 1) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) add_scaled(acc[nt], part[nt], s0.x, s1.x);
+            left -= W4_STAGE_K;
+            if (++ws == STAGES) {
+                ws = 0;
+                ws_phase ^= 1u;
             }
+        }
+    } else if (warp < 14) {
+        // ------------------------------------------------ codes and scales
+        const int groups = p.K / GROUP;
+        const uint32_t tx = static_cast<uint32_t>(p.tile_rows) * 128u;
+        int last_n = -1;
+        for (int s = s_begin + warp - 12; s < s_end; s += 2) {
+            const int n = s - s_begin;
+            const int ws = n % STAGES;
+            const bool ok = wd.wait(bar(W4_WEMPTY + ws),
+                                    (static_cast<uint32_t>(n / STAGES) & 1u) ^ 1u, WAIT_EMPTY, s, 3);
+            if (lane == 0 && ok) {
+                mbar_arrive_expect_tx(bar(W4_WFULL + ws), tx);
+                tma_load_2d(base + L::W + ws * W4_STAGE_BYTES, &tmW, bar(W4_WFULL + ws),
+                            s * (W4_STAGE_K / 2), expert * p.N + n0);
+                last_n = n;
+            }
+            __syncwarp();
+            struct alignas(2 * GPS) Scales { unsigned short v[GPS]; };
+            struct alignas(GPS) Zeros { uint8_t v[GPS]; };
+            Scales sc[W4_TILE / 32];
+            Zeros ze[W4_TILE / 32];
+#pragma unroll
+            for (int i = 0; i < W4_TILE / 32; ++i) {
+                const int r = 32 * i + static_cast<int>(lane);
+                const bool exists = r < p.tile_rows && n0 + r < p.N;
+                const int64_t at =
+                    (static_cast<int64_t>(expert) * p.N + n0 + r) * groups + s * GPS;
+#pragma unroll
+                for (int g = 0; g < GPS; ++g) {
+                    sc[i].v[g] = 0;
+                    ze[i].v[g] = 8;
+                }
+                if (!exists) continue;
+                if (p.wide_scales) {
+                    sc[i] = *reinterpret_cast<const Scales*>(p.scales + at);
+                    if (p.zeros) ze[i] = *reinterpret_cast<const Zeros*>(p.zeros + at);
+                } else {
+#pragma unroll
+                    for (int g = 0; g < GPS; ++g) {
+                        if (s * GPS + g >= groups) continue;
+                        sc[i].v[g] = __half_as_ushort(p.scales[at + g]);
+                        if (p.zeros) ze[i].v[g] = p.zeros[at + g];
+                    }
+                }
+            }
+            uint32_t* to = reinterpret_cast<uint32_t*>(gen + L::TABLE) + ws * L::TABLE_WORDS;
+#pragma unroll
+            for (int i = 0; i < W4_TILE / 32; ++i)
+#pragma unroll
+                for (int g = 0; g < GPS; ++g) {
+                    const uint32_t z = __half_as_ushort(
+                        __float2half_rn(-1024.0f - static_cast<float>(ze[i].v[g])));
+                    to[g * W4_TILE + 32 * i + lane] = sc[i].v[g] | (z << 16);
+                }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(W4_WFULL + ws));
+        }
+        // an abandoned run: this warp's copies in flight land before the CTA exits
+        if (lane == 0 && wd.aborted) {
+            for (int n = last_n; n >= 0 && n > last_n - STAGES; n -= 2)
+                wd.drain(bar(W4_WFULL + n % STAGES), static_cast<uint32_t>(n / STAGES) & 1u);
         }
         __syncwarp();
-        if (++stage == STAGES) stage = 0;
-        parity ^= 1;
+    } else {
+        // ------------------------------------------------------ MMA issuer
+        constexpr uint32_t idesc = idesc_f16_f32(W4_TILE, NC);
+        const uint32_t elected = elect_one();
+        const int issuer = warp - 14;
+        const int end = s_end * W4_STAGE_K < p.K ? s_end * W4_STAGE_K : p.K;
+        int k0 = s_begin * W4_STAGE_K;
+        for (int b = 0; k0 < end; ++b, k0 += W4_BLOCK_K) {
+            const int team = b & 1, n = b >> 1;
+            if (L::ISSUERS == 2 ? team != issuer : issuer != 0) continue;
+            const int buf = b % A_BUFS, set = b % SETS;
+            wd.wait(bar(W4_GEMPTY + set), (static_cast<uint32_t>(b / SETS) & 1u) ^ 1u,
+                    WAIT_TMEM_EMPTY, k0, 0);
+            const bool ok = wd.wait(bar(W4_AFULL + team * W4_TURNS + n % W4_TURNS),
+                                    static_cast<uint32_t>(n / W4_TURNS) & 1u, WAIT_FULL, k0, 1);
+            if (!__all_sync(0xffffffffu, ok)) break;  // an abandoned run
+            const uint32_t a_tmem = tmem_base + static_cast<uint32_t>(buf * W4_A_COLS);
+            const uint32_t d_tmem = sum_tmem + static_cast<uint32_t>(set * L::SUM_COLS);
+            const uint64_t bdesc = sw128_kmajor_desc(base + L::X + buf * L::X_BYTES);
+            tc_fence_after_sync();
+#pragma unroll
+            for (int k = 0; k < W4_BLOCK_K; k += MMA_K)
+                mma_f16_ts(elected, d_tmem + static_cast<uint32_t>(k / GROUP * NC),
+                           a_tmem + static_cast<uint32_t>(k / 2),
+                           bdesc + static_cast<uint64_t>(((k / 64) * NC * 128 + (k % 64) * 2) >> 4),
+                           idesc, k % GROUP == 0 ? 0u : 1u);
+            mma_commit_elected(elected, bar(W4_DONE + team * W4_TURNS + n % W4_TURNS));
+            mma_commit_elected(elected, bar(W4_GFULL + set));
+        }
+        mma_commit_elected(elected, bar(W4_DRAIN + issuer));  // by the lane that issued
+        wd.drain(bar(W4_DRAIN + issuer), 0);
+        __syncwarp();
     }
-    cp_async_wait<0>();
+
+    // every MMA has been waited for and every block used up
+    tc_fence_before_sync();
     __syncthreads();
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            sums[(nt * 8 + 2 * t + (i & 1)) * SUM_PITCH + warp * W4_ROWS + g + 8 * (i >> 1)] =
-                acc[nt][i];
-    if (csize > 1)
-        cluster_sync_all();
-    else
-        __syncthreads();
-    for (int i = tid; i < COLS * W4_TILE; i += W4_THREADS) {
-        const int m = i / W4_TILE, r = i % W4_TILE;
-        const int n = static_cast<int>(blockIdx.x) * W4_TILE + r;
-        if (m >= p.M || n >= p.N || static_cast<uint32_t>(m) % csize != crank) continue;
-        const float* at = sums + m * SUM_PITCH + r;
-        float v = 0.0f;
-        if (csize == 1)
-            v = *at;
-        else
-            for (uint32_t c = 0; c < csize; ++c) v += ld_shared_rank(at, c);
-        store_y(p, m, n, v);
+    if (warp == 15) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem_base, L::TMEM_COLS);
     }
-    if (csize > 1) cluster_sync_all();  // nobody reads this CTA's sums any more
+    const bool summer = warp >= W4_WORKERS && warp < W4_WORKERS + W4_SUMMERS;
+    const bool stores = row < p.tile_rows && n0 + row < p.N && !wd.aborted;
+    if (csize == 1) {
+        if (summer && stores) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                if (c < count) store_y(p, p.experts > 0 ? list[c] : c, n0 + row, acc[c]);
+        }
+        return;
+    }
+    // this CTA's part of the length, [NC][128], over the code ring
+    float* sums = reinterpret_cast<float*>(gen + L::W);
+    if (summer) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            if (c < count) sums[c * W4_TILE + row] = acc[c];
+    }
+    cluster_sync_all();
+    if (stores) {
+        // four warps a column
+        const int step = W4_THREADS / W4_TILE * static_cast<int>(csize);
+        for (int m = static_cast<int>(crank) + (warp >> 2) * static_cast<int>(csize); m < count;
+             m += step) {
+            float v = 0.0f;
+            for (uint32_t r = 0; r < csize; ++r) {
+                float part;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                             : "=f"(part)
+                             : "r"(map_shared_rank(smem_u32(sums + m * W4_TILE + row), r))
+                             : "memory");
+                v += part;
+            }
+            store_y(p, p.experts > 0 ? list[m] : m, n0 + row, v);
+        }
+    }
+    cluster_sync_all();  // nobody reads this CTA's sums any more
 }
 
 // ------------------------------------------------------------ many rows
@@ -665,10 +724,11 @@ __global__ void __launch_bounds__(256)
 }
 
 // Clusters along z: the CTAs that share the rows' length.
-cudaError_t launch_w4(void (*kernel)(W4Params), const W4Params& p, unsigned smem, dim3 grid,
-                      cudaStream_t stream)
+template <int NC, int GROUP>
+cudaError_t launch_w4(const CUtensorMap& map, const W4Params& p, dim3 grid, cudaStream_t stream)
 {
-    cudaError_t e = ensure_smem_limit(kernel, smem);
+    constexpr unsigned smem = W4Layout<NC, GROUP>::TOTAL;
+    cudaError_t e = ensure_smem_limit(k_w4<NC, GROUP>, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -684,19 +744,17 @@ cudaError_t launch_w4(void (*kernel)(W4Params), const W4Params& p, unsigned smem
     attr[1].val.clusterDim.z = grid.z;
     cfg.attrs = attr;
     cfg.numAttrs = grid.z > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaLaunchKernelEx(&cfg, k_w4<NC, GROUP>, map, p);
 }
 
 template <int GROUP>
-cudaError_t launch_group(const W4Params& p, int cols, dim3 grid, cudaStream_t stream)
+cudaError_t launch_group(const CUtensorMap& map, const W4Params& p, int cols, dim3 grid,
+                         cudaStream_t stream)
 {
     switch (cols) {
-    case 8:
-        return launch_w4(k_w4_few<GROUP, W4_FEW_RT>, p, w4_few_smem<GROUP, W4_FEW_RT>(), grid,
-                         stream);
-    case 16: return launch_w4(k_w4_tile<16, GROUP>, p, w4_tile_smem<16, GROUP>(), grid, stream);
-    case 32: return launch_w4(k_w4_tile<32, GROUP>, p, w4_tile_smem<32, GROUP>(), grid, stream);
-    case 64: return launch_w4(k_w4_tile<64, GROUP>, p, w4_tile_smem<64, GROUP>(), grid, stream);
+    case 16: return launch_w4<16, GROUP>(map, p, grid, stream);
+    case 32: return launch_w4<32, GROUP>(map, p, grid, stream);
+    case 64: return launch_w4<64, GROUP>(map, p, grid, stream);
     default: return cudaErrorInvalidValue;
     }
 }
@@ -711,16 +769,42 @@ struct gemm_w4_plan {
     int64_t M, N, K;
     int group, experts, share, dtype;
     int device, sms;
-    int cols;        // rows of X per pass of the few-row kernel; 0: expand + GEMM
-    int length_ctas; // CTAs that share a row's length
+    int cols;         // N side of the few-row kernel's MMA; 0: expand + GEMM
+    int length_ctas;  // CTAs that share a row's length
+    int tile_rows;    // rows of the weights per CTA
+    DevStatus* d_status;
+    int epoch;
     void* d_weights; // N x K fp16
     gemm_plan* gemm;
     char desc[256];
 };
 
 namespace {
+
 constexpr int W4_MAX_ROWS = 64;
+
+// Tensor map over the codes, `rows` rows of `bytes`: boxes of 128 bytes x
+// `box_rows`, 128-byte swizzle, zeros past the end of a row.
+int encode_codes(CUtensorMap* map, const void* packed, int64_t bytes, int64_t rows, int box_rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode_fn();
+    if (!enc) return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(bytes), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(bytes)};
+    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(packed), dims,
+                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return GEMM_OK;
+    char buf[100];
+    std::snprintf(buf, sizeof(buf), "cuTensorMapEncodeTiled(packed) failed with CUresult %d",
+                  static_cast<int>(r));
+    return fail(GEMM_ERR_CUDA, buf);
 }
+
+}  // namespace
 
 extern "C" {
 
@@ -746,6 +830,8 @@ gemm_w4_plan* gemm_w4_create_plan(int64_t M, int64_t N, int64_t K, int group, in
         if ((N * elt) % 16 != 0)
             return fail(GEMM_ERR_UNSUPPORTED,
                         "N * sizeof(output) must be a multiple of 16 bytes");
+        if (N > LIM / std::max(experts, 1))
+            return fail(GEMM_ERR_UNSUPPORTED, "experts * N is too large");
         if (experts > 0 && M > 1024)
             return fail(GEMM_ERR_UNSUPPORTED, "a plan with experts takes at most 1024 rows");
         gemm_w4_plan p = {};
@@ -759,28 +845,35 @@ gemm_w4_plan* gemm_w4_create_plan(int64_t M, int64_t N, int64_t K, int group, in
         p.share = share;
         p.dtype = dtype_out;
         if (experts > 0 || M <= W4_MAX_ROWS) {
-            p.cols = 8;
+            p.cols = 16;
             while (experts == 0 && p.cols < M) p.cols *= 2;
-            // CTAs of a cluster share a row's length where the rows alone leave
-            // SMs idle: up to two CTAs per SM of the few-row kernel, each with
-            // two blocks of 256 per warp at least; up to one of the tile kernel,
-            // each with two blocks.
-            const bool few = p.cols == W4_FEW;
-            const int tile = few ? W4_ROWS * W4_FEW_RT : W4_TILE;
-            const int64_t tiles =
-                (N + tile - 1) / tile * (experts > 0 ? std::min<int64_t>(M, experts) : 1);
-            const int64_t most = few ? 2 * p.sms : p.sms;
-            const int64_t block = few ? W4_BLOCK * W4_WARPS : W4_BLOCK;
+            // Few tiles of 128 rows: the CTAs of a cluster share the rows' length
+            // (at least two stages of 256 codes each), then tiles of fewer rows
+            // fill the last SMs.
+            const int64_t slots = w4_ctas(p.cols) * p.sms;
+            const int64_t matrices = experts > 0 ? std::min<int64_t>(M, experts) : 1;
+            const int64_t full = (N + W4_TILE - 1) / W4_TILE * matrices;
             p.length_ctas = 1;
-            while (p.length_ctas < 8 && tiles * p.length_ctas * 2 <= most &&
-                   K >= block * p.length_ctas * 4)
+            while (p.length_ctas < 8 && full * p.length_ctas * 2 <= slots &&
+                   K >= static_cast<int64_t>(W4_STAGE_K) * p.length_ctas * 4)
                 p.length_ctas *= 2;
+            p.tile_rows = W4_TILE;
+            const int64_t per_matrix = slots / (p.length_ctas * matrices);
+            if (per_matrix > 0 && N <= per_matrix * W4_TILE)
+                p.tile_rows =
+                    static_cast<int>(((N + per_matrix - 1) / per_matrix + 7) / 8 * 8);
             std::snprintf(p.desc, sizeof(p.desc),
-                          "w4 rows M=%lld N=%lld K=%lld group=%d experts=%d cols=%d "
+                          "w4 rows M=%lld N=%lld K=%lld group=%d experts=%d tile=%dx%d "
                           "length_ctas=%d out=%s",
                           static_cast<long long>(M), static_cast<long long>(N),
-                          static_cast<long long>(K), group, experts, p.cols, p.length_ctas,
+                          static_cast<long long>(K), group, experts, p.tile_rows, p.cols, p.length_ctas,
                           elt == 2 ? "f16" : "f32");
+            cudaError_t e = cudaMalloc(&p.d_status, sizeof(DevStatus));
+            if (e == cudaSuccess) e = cudaMemset(p.d_status, 0, sizeof(DevStatus));
+            if (e != cudaSuccess) {
+                if (p.d_status) cudaFree(p.d_status);
+                return cuda_fail("allocating the device status record", e);
+            }
         } else {
             p.gemm = gemm_create_plan(M, N, K, dtype_out);
             if (!p.gemm) return gemm_last_status();
@@ -796,6 +889,7 @@ gemm_w4_plan* gemm_w4_create_plan(int64_t M, int64_t N, int64_t K, int group, in
         if (!plan) {
             if (p.gemm) gemm_destroy(p.gemm);
             if (p.d_weights) cudaFree(p.d_weights);
+            if (p.d_status) cudaFree(p.d_status);
             return fail(GEMM_ERR_CUDA, "out of host memory");
         }
         return ok();
@@ -847,21 +941,33 @@ int gemm_w4_run(gemm_w4_plan* plan, const void* X, const void* packed, const voi
         p.ids = expert_ids;
         p.Y = Y;
         p.f16out = plan->dtype == GEMM_OUT_F16;
-        const int tile = plan->cols == W4_FEW ? W4_ROWS * W4_FEW_RT : W4_TILE;
-        const dim3 grid(static_cast<unsigned>((plan->N + tile - 1) / tile),
+        p.tile_rows = plan->tile_rows;
+        p.wide_scales = plan->K % W4_STAGE_K == 0 && (reinterpret_cast<uintptr_t>(zeros) & 7u) == 0;
+        p.status = plan->d_status;
+        if (++plan->epoch <= 0) plan->epoch = 1;
+        p.epoch = plan->epoch;
+        p.budget_ns = 2000ull * 1000000ull;
+        CUtensorMap map;
+        const int r = encode_codes(&map, packed, plan->K / 2,
+                                   plan->N * std::max(plan->experts, 1), plan->tile_rows);
+        if (r != GEMM_OK) return r;
+        const dim3 grid(static_cast<unsigned>((plan->N + plan->tile_rows - 1) / plan->tile_rows),
                         plan->experts > 0 ? static_cast<unsigned>(plan->M) : 1u,
                         static_cast<unsigned>(plan->length_ctas));
-        e = plan->group == 32   ? launch_group<32>(p, plan->cols, grid, stream)
-            : plan->group == 64 ? launch_group<64>(p, plan->cols, grid, stream)
-                                : launch_group<128>(p, plan->cols, grid, stream);
+        e = plan->group == 32   ? launch_group<32>(map, p, plan->cols, grid, stream)
+            : plan->group == 64 ? launch_group<64>(map, p, plan->cols, grid, stream)
+                                : launch_group<128>(map, p, plan->cols, grid, stream);
         return e == cudaSuccess ? ok() : cuda_fail("w4 product launch", e);
     });
 }
 
 int gemm_w4_get_device_status(gemm_w4_plan* plan)
 {
-    if (!plan) return fail(GEMM_ERR_INVALID_ARG, "plan is NULL");
-    return plan->gemm ? gemm_get_device_status(plan->gemm) : ok();
+    return guarded([&] {
+        if (!plan) return fail(GEMM_ERR_INVALID_ARG, "plan is NULL");
+        return plan->gemm ? gemm_get_device_status(plan->gemm)
+                          : read_device_status(plan->d_status);
+    });
 }
 
 void gemm_w4_destroy(gemm_w4_plan* plan)
@@ -869,6 +975,7 @@ void gemm_w4_destroy(gemm_w4_plan* plan)
     if (!plan) return;
     if (plan->gemm) gemm_destroy(plan->gemm);
     if (plan->d_weights) cudaFree(plan->d_weights);
+    if (plan->d_status) cudaFree(plan->d_status);
     delete plan;
 }
 
