@@ -59,21 +59,22 @@ struct W4Params {
 // a worker thread converts 128 codes of its row in registers and stores them
 // with tcgen05.st, and shared memory is left to the codes in flight.
 //
-// Roles of a CTA (W4_THREADS = 512), joined by mbarriers only:
+// Roles of a CTA, joined by mbarriers only:
 //   warps 0..7    workers, two teams of four warps; warp w owns rows
 //                 32 (w % 4) .. + 31 of the tile.  Team h takes the h-th block of
 //                 128 codes of every stage: converts it into one of A_BUFS
 //                 operands and copies the block's part of X beside it.
-//   warps 8..11   sums: read a block's group sums from TMEM, scale and add them.
+//   warps 12..15  sums (12..19 for 64 rows of X, each half of the columns): read
+//                 the groups' sums from TMEM, scale and add them.
 //                 (With the workers doing this after each block, every block
 //                 paid the round trip to the tensor core, about 1500 cycles:
 //                 54 us for one row of 16384 x 16384.)
-//   warps 12, 13  take alternate stages of 256 codes: start the TMA copy of the
+//   warps 8, 9    take alternate stages of 256 codes: start the TMA copy of the
 //                 codes, 128 bytes a row, and bring the stage's scales and zero
 //                 points from global memory into a table in shared memory.
-//   warps 14, 15  MMA issuers, one per team (a block's eight MMAs and the waits
+//   warps 10, 11  MMA issuers, one per team (a block's eight MMAs and the waits
 //                 around them take one warp about as long as a team takes to
-//                 convert it); warp 15 allocates TMEM.
+//                 convert it); warp 11 allocates TMEM.
 //
 // A tile has up to 128 rows, as few as spread the rows evenly over the SMs;
 // where that is not enough, the CTAs of a cluster share the rows' length, and
@@ -84,8 +85,6 @@ struct W4Params {
 // rows before it does that row and the expert's next 15; the others have
 // nothing to do, and nothing has to be sorted.
 constexpr int W4_WORKERS = 8;
-constexpr int W4_SUMMERS = 4;
-constexpr int W4_THREADS = 512;
 constexpr int W4_TEAMS = 2;
 constexpr int W4_TEAM_WARPS = W4_WORKERS / W4_TEAMS;
 constexpr int W4_TILE = 128;
@@ -124,14 +123,19 @@ struct W4Layout {
     static constexpr int STAGES = CTAS == 2 ? 4 : 8;
     static constexpr int GPS = W4_STAGE_K / GROUP;          // groups per stage and row
     static constexpr int GPB = W4_BLOCK_K / GROUP;          // groups per block
-    static constexpr int SUM_COLS = GPB * NC;               // TMEM columns of a block's sums
+    static constexpr int SUMMERS = NC == 64 ? 8 : 4;        // warps that add up
+    static constexpr int COLS = NC * 4 / SUMMERS;           // columns each of them has
+    static constexpr int THREADS = (12 + SUMMERS) * 32;
+    // a set of accumulators: the groups that one commit completes
+    static constexpr int SET_GROUPS = GPB * NC > 128 ? 128 / NC : GPB;
+    static constexpr int SETS_PER_BLOCK = GPB / SET_GROUPS;
+    static constexpr int SUM_COLS = SET_GROUPS * NC;        // TMEM columns of a set
     static constexpr int TMEM_COLS = CTAS == 2 ? 256 : 512;
     static constexpr int A_BUFS = TMEM_COLS - 3 * W4_A_COLS >= 2 * SUM_COLS ? 3 : 2;
-    static constexpr int FIT = (TMEM_COLS - A_BUFS * W4_A_COLS) / SUM_COLS;
-    // accumulator sets in turn, an even number of them so that a set always
-    // belongs to the same team; with a single one the first issuer does all
-    static constexpr int SETS = FIT >= 4 ? 4 : FIT >= 2 ? 2 : 1;
-    static constexpr int ISSUERS = SETS >= 2 ? 2 : 1;
+    static constexpr int SETS = TMEM_COLS - A_BUFS * W4_A_COLS >= 4 * SUM_COLS ? 4 : 2;
+    // Two issuers where every set always belongs to the same team; else the
+    // first one does all.
+    static constexpr int ISSUERS = SETS % (W4_TEAMS * SETS_PER_BLOCK) == 0 ? 2 : 1;
     static constexpr int X_BYTES = NC * W4_BLOCK_K * 2;     // a block's part of X
     static constexpr int W = 0;
     static constexpr int X = W + STAGES * W4_STAGE_BYTES;
@@ -141,7 +145,7 @@ struct W4Layout {
     static constexpr int BARS = TABLE + STAGES * TABLE_WORDS * 4;
     static constexpr int LIST = BARS + (W4_BARRIERS + 1) * 8;  // rows of Y by expert
     static constexpr int TOTAL = LIST + 64 + 1024;
-    static_assert(FIT >= 1, "TMEM columns");
+    static_assert(A_BUFS * W4_A_COLS + SETS * SUM_COLS <= TMEM_COLS, "TMEM columns");
     static_assert(NC * W4_TILE * 4 <= X, "the sums fit the code ring");
     // 228 KB an SM, 1 KB of it taken by the system per CTA
     static_assert(TOTAL <= (CTAS == 2 ? 113 : 227) * 1024, "shared memory");
@@ -302,12 +306,13 @@ struct W4Wait : Watchdog {
 };
 
 template <int NC, int GROUP>
-__global__ void __launch_bounds__(W4_THREADS, W4Layout<NC, GROUP>::CTAS)
+__global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GROUP>::CTAS)
     k_w4(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ W4Params p)
 {
     using L = W4Layout<NC, GROUP>;
     constexpr int STAGES = L::STAGES, A_BUFS = L::A_BUFS, SETS = L::SETS;
-    constexpr int GPS = L::GPS, GPB = L::GPB;
+    constexpr int GPS = L::GPS, GPB = L::GPB, COLS = L::COLS;
+    constexpr int FIRST_SUMMER = 12;
     constexpr int XPT = NC * (W4_BLOCK_K / 8) / 128;  // chunks of X per worker and block
     extern __shared__ __align__(1024) uint8_t w4_smem[];
     const uint32_t raw = smem_u32(w4_smem);
@@ -341,7 +346,7 @@ __global__ void __launch_bounds__(W4_THREADS, W4Layout<NC, GROUP>::CTAS)
             return;
         }
         int before = 0;
-        for (int r = tid; r - tid < first; r += W4_THREADS)
+        for (int r = tid; r - tid < first; r += L::THREADS)
             before += __syncthreads_count(r < first && p.ids[r] == expert);
         if (before % 16 != 0) return;
         if (warp == 0) {
@@ -360,11 +365,11 @@ __global__ void __launch_bounds__(W4_THREADS, W4Layout<NC, GROUP>::CTAS)
     const int s_begin = static_cast<int>(static_cast<int64_t>(stages) * crank / csize);
     const int s_end = static_cast<int>(static_cast<int64_t>(stages) * (crank + 1) / csize);
 
-    if (warp == 14 && lane == 0) {
+    if (warp == 8 && lane == 0) {
         prefetch_tensormap(&tmW);
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(bar(W4_WFULL + i), 2);  // the copy's announcement, the table
-            mbar_init(bar(W4_WEMPTY + i), W4_WORKERS + W4_SUMMERS);
+            mbar_init(bar(W4_WEMPTY + i), W4_WORKERS + L::SUMMERS);
         }
         for (int i = 0; i < W4_TEAMS * W4_TURNS; ++i) {
             mbar_init(bar(W4_AFULL + i), W4_TEAM_WARPS);
@@ -372,12 +377,12 @@ __global__ void __launch_bounds__(W4_THREADS, W4Layout<NC, GROUP>::CTAS)
         }
         for (int i = 0; i < SETS; ++i) {
             mbar_init(bar(W4_GFULL + i), 1);
-            mbar_init(bar(W4_GEMPTY + i), W4_SUMMERS);
+            mbar_init(bar(W4_GEMPTY + i), L::SUMMERS);
         }
         for (int i = 0; i < W4_TEAMS; ++i) mbar_init(bar(W4_DRAIN + i), 1);
         fence_mbar_init();
     }
-    if (warp == 15) {
+    if (warp == 11) {
         tmem_alloc(smem_u32(tmem_slot), L::TMEM_COLS);
         tmem_relinquish_alloc_permit();
     }
@@ -389,9 +394,10 @@ __global__ void __launch_bounds__(W4_THREADS, W4Layout<NC, GROUP>::CTAS)
         count = 0;
         while (count < 16 && list[count] >= 0) ++count;
     }
-    float acc[NC];
+    float acc[COLS];  // sums: columns col0 .. col0 + COLS - 1 of the thread's row
 #pragma unroll
-    for (int i = 0; i < NC; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
+    const int col0 = (warp - FIRST_SUMMER) / 4 * COLS;
     const int q = warp & 3;  // workers and sums: TMEM lane quarter
     const int row = 32 * q + static_cast<int>(lane);
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
@@ -497,7 +503,7 @@ __global__ void __launch_bounds__(W4_THREADS, W4Layout<NC, GROUP>::CTAS)
             buf += W4_TEAMS;
             if (buf >= A_BUFS) buf -= A_BUFS;
         }
-    } else if (warp < W4_WORKERS + W4_SUMMERS) {
+    } else if (warp >= FIRST_SUMMER) {
         // ----------------------------------------------------------- sums
         int ws = 0, set = 0;
         uint32_t ws_phase = 0, set_phase = 0;
@@ -513,27 +519,22 @@ __global__ void __launch_bounds__(W4_THREADS, W4Layout<NC, GROUP>::CTAS)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(W4_WEMPTY + ws));
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                if (left <= part * W4_BLOCK_K) break;
-                wd.wait(bar(W4_GFULL + set), set_phase, WAIT_TMEM_FULL, s, part);
+            for (int g0 = 0; g0 < GPS; g0 += L::SET_GROUPS) {
+                if (g0 * GROUP / W4_BLOCK_K * W4_BLOCK_K >= left) break;  // no such block
+                wd.wait(bar(W4_GFULL + set), set_phase, WAIT_TMEM_FULL, s, g0);
                 tc_fence_after_sync();
-                const uint32_t from = sum_tmem + lanes + static_cast<uint32_t>(set * L::SUM_COLS);
-                if constexpr (L::SUM_COLS == 16) {
-                    uint32_t v[16];
-                    tmem_load_16cols(from, v);
+                const uint32_t from =
+                    sum_tmem + lanes + static_cast<uint32_t>(set * L::SUM_COLS + col0);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        acc[j] = fmaf(scale[part], __uint_as_float(v[j]), acc[j]);
-                } else {
+                for (int g = 0; g < L::SET_GROUPS; ++g) {
+                    uint32_t v[COLS];
+                    if constexpr (COLS == 16)
+                        tmem_load_16cols(from + g * NC, v);
+                    else
+                        tmem_load_32cols(from + g * NC, v);
 #pragma unroll
-                    for (int c = 0; c < L::SUM_COLS; c += 32) {
-                        uint32_t v[32];
-                        tmem_load_32cols(from + c, v);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            acc[(c + j) % NC] = fmaf(scale[part * GPB + (c + j) / NC],
-                                                     __uint_as_float(v[j]), acc[(c + j) % NC]);
-                    }
+                    for (int j = 0; j < COLS; ++j)
+                        acc[j] = fmaf(scale[g0 + g], __uint_as_float(v[j]), acc[j]);
                 }
                 tc_fence_before_sync();
                 __syncwarp();
@@ -549,12 +550,24 @@ __global__ void __launch_bounds__(W4_THREADS, W4Layout<NC, GROUP>::CTAS)
                 ws_phase ^= 1u;
             }
         }
-    } else if (warp < 14) {
+    } else if (warp < 10) {
         // ------------------------------------------------ codes and scales
         const int groups = p.K / GROUP;
         const uint32_t tx = static_cast<uint32_t>(p.tile_rows) * 128u;
         int last_n = -1;
-        for (int s = s_begin + warp - 12; s < s_end; s += 2) {
+        struct alignas(2 * GPS) Scales { unsigned short v[GPS]; };
+        struct alignas(GPS) Zeros { uint8_t v[GPS]; };
+        const __half* scales[W4_TILE / 32];  // of the lane's rows; rows that are not
+        const uint8_t* zeros[W4_TILE / 32];  // there repeat the tile's first
+#pragma unroll
+        for (int i = 0; i < W4_TILE / 32; ++i) {
+            const int r = 32 * i + static_cast<int>(lane);
+            const int exists = r < p.tile_rows && n0 + r < p.N ? r : 0;
+            const int64_t at = (static_cast<int64_t>(expert) * p.N + n0 + exists) * groups;
+            scales[i] = p.scales + at;
+            zeros[i] = p.zeros ? p.zeros + at : nullptr;
+        }
+        for (int s = s_begin + warp - 8; s < s_end; s += 2) {
             const int n = s - s_begin;
             const int ws = n % STAGES;
             const bool ok = wd.wait(bar(W4_WEMPTY + ws),
@@ -566,31 +579,19 @@ __global__ void __launch_bounds__(W4_THREADS, W4Layout<NC, GROUP>::CTAS)
                 last_n = n;
             }
             __syncwarp();
-            struct alignas(2 * GPS) Scales { unsigned short v[GPS]; };
-            struct alignas(GPS) Zeros { uint8_t v[GPS]; };
             Scales sc[W4_TILE / 32];
             Zeros ze[W4_TILE / 32];
 #pragma unroll
             for (int i = 0; i < W4_TILE / 32; ++i) {
-                const int r = 32 * i + static_cast<int>(lane);
-                const bool exists = r < p.tile_rows && n0 + r < p.N;
-                const int64_t at =
-                    (static_cast<int64_t>(expert) * p.N + n0 + r) * groups + s * GPS;
-#pragma unroll
-                for (int g = 0; g < GPS; ++g) {
-                    sc[i].v[g] = 0;
-                    ze[i].v[g] = 8;
-                }
-                if (!exists) continue;
                 if (p.wide_scales) {
-                    sc[i] = *reinterpret_cast<const Scales*>(p.scales + at);
-                    if (p.zeros) ze[i] = *reinterpret_cast<const Zeros*>(p.zeros + at);
+                    sc[i] = *reinterpret_cast<const Scales*>(scales[i] + s * GPS);
+                    if (zeros[i]) ze[i] = *reinterpret_cast<const Zeros*>(zeros[i] + s * GPS);
                 } else {
 #pragma unroll
                     for (int g = 0; g < GPS; ++g) {
-                        if (s * GPS + g >= groups) continue;
-                        sc[i].v[g] = __half_as_ushort(p.scales[at + g]);
-                        if (p.zeros) ze[i].v[g] = p.zeros[at + g];
+                        const bool inside = s * GPS + g < groups;
+                        sc[i].v[g] = inside ? __half_as_ushort(scales[i][s * GPS + g]) : 0;
+                        ze[i].v[g] = inside && zeros[i] ? zeros[i][s * GPS + g] : 8;
                     }
                 }
             }
@@ -599,8 +600,8 @@ __global__ void __launch_bounds__(W4_THREADS, W4Layout<NC, GROUP>::CTAS)
             for (int i = 0; i < W4_TILE / 32; ++i)
 #pragma unroll
                 for (int g = 0; g < GPS; ++g) {
-                    const uint32_t z = __half_as_ushort(
-                        __float2half_rn(-1024.0f - static_cast<float>(ze[i].v[g])));
+                    // -(1024 + zero) in fp16 is -1024's bits plus the zero point
+                    const uint32_t z = 0xe400u + (zeros[i] ? ze[i].v[g] : 8u);
                     to[g * W4_TILE + 32 * i + lane] = sc[i].v[g] | (z << 16);
                 }
             __syncwarp();
@@ -616,30 +617,39 @@ __global__ void __launch_bounds__(W4_THREADS, W4Layout<NC, GROUP>::CTAS)
         // ------------------------------------------------------ MMA issuer
         constexpr uint32_t idesc = idesc_f16_f32(W4_TILE, NC);
         const uint32_t elected = elect_one();
-        const int issuer = warp - 14;
+        const int issuer = warp - 10;
         const int end = s_end * W4_STAGE_K < p.K ? s_end * W4_STAGE_K : p.K;
         int k0 = s_begin * W4_STAGE_K;
         for (int b = 0; k0 < end; ++b, k0 += W4_BLOCK_K) {
             const int team = b & 1, n = b >> 1;
             if (L::ISSUERS == 2 ? team != issuer : issuer != 0) continue;
-            const int buf = b % A_BUFS, set = b % SETS;
-            wd.wait(bar(W4_GEMPTY + set), (static_cast<uint32_t>(b / SETS) & 1u) ^ 1u,
-                    WAIT_TMEM_EMPTY, k0, 0);
-            const bool ok = wd.wait(bar(W4_AFULL + team * W4_TURNS + n % W4_TURNS),
-                                    static_cast<uint32_t>(n / W4_TURNS) & 1u, WAIT_FULL, k0, 1);
-            if (!__all_sync(0xffffffffu, ok)) break;  // an abandoned run
+            const int buf = b % A_BUFS;
+            bool ok = wd.wait(bar(W4_AFULL + team * W4_TURNS + n % W4_TURNS),
+                              static_cast<uint32_t>(n / W4_TURNS) & 1u, WAIT_FULL, k0, 1);
             const uint32_t a_tmem = tmem_base + static_cast<uint32_t>(buf * W4_A_COLS);
-            const uint32_t d_tmem = sum_tmem + static_cast<uint32_t>(set * L::SUM_COLS);
             const uint64_t bdesc = sw128_kmajor_desc(base + L::X + buf * L::X_BYTES);
-            tc_fence_after_sync();
 #pragma unroll
-            for (int k = 0; k < W4_BLOCK_K; k += MMA_K)
-                mma_f16_ts(elected, d_tmem + static_cast<uint32_t>(k / GROUP * NC),
-                           a_tmem + static_cast<uint32_t>(k / 2),
-                           bdesc + static_cast<uint64_t>(((k / 64) * NC * 128 + (k % 64) * 2) >> 4),
-                           idesc, k % GROUP == 0 ? 0u : 1u);
+            for (int h = 0; h < L::SETS_PER_BLOCK; ++h) {
+                constexpr int SET_K = L::SET_GROUPS * GROUP;  // codes of a set
+                const int u = b * L::SETS_PER_BLOCK + h, set = u % SETS;
+                ok = wd.wait(bar(W4_GEMPTY + set), (static_cast<uint32_t>(u / SETS) & 1u) ^ 1u,
+                             WAIT_TMEM_EMPTY, k0, h);
+                if (!__all_sync(0xffffffffu, ok)) break;  // an abandoned run
+                const uint32_t d_tmem = sum_tmem + static_cast<uint32_t>(set * L::SUM_COLS);
+                tc_fence_after_sync();
+#pragma unroll
+                for (int i = 0; i < SET_K; i += MMA_K) {
+                    const int k = h * SET_K + i;
+                    mma_f16_ts(elected, d_tmem + static_cast<uint32_t>(i / GROUP * NC),
+                               a_tmem + static_cast<uint32_t>(k / 2),
+                               bdesc + static_cast<uint64_t>(
+                                           ((k / 64) * NC * 128 + (k % 64) * 2) >> 4),
+                               idesc, k % GROUP == 0 ? 0u : 1u);
+                }
+                mma_commit_elected(elected, bar(W4_GFULL + set));
+            }
+            if (!__all_sync(0xffffffffu, ok)) break;
             mma_commit_elected(elected, bar(W4_DONE + team * W4_TURNS + n % W4_TURNS));
-            mma_commit_elected(elected, bar(W4_GFULL + set));
         }
         mma_commit_elected(elected, bar(W4_DRAIN + issuer));  // by the lane that issued
         wd.drain(bar(W4_DRAIN + issuer), 0);
@@ -649,17 +659,19 @@ __global__ void __launch_bounds__(W4_THREADS, W4Layout<NC, GROUP>::CTAS)
     // every MMA has been waited for and every block used up
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 15) {
+    if (warp == 11) {
         tc_fence_after_sync();
         tmem_dealloc(tmem_base, L::TMEM_COLS);
     }
-    const bool summer = warp >= W4_WORKERS && warp < W4_WORKERS + W4_SUMMERS;
+    const bool summer = warp >= FIRST_SUMMER;
     const bool stores = row < p.tile_rows && n0 + row < p.N && !wd.aborted;
     if (csize == 1) {
         if (summer && stores) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-                if (c < count) store_y(p, p.experts > 0 ? list[c] : c, n0 + row, acc[c]);
+            for (int c = 0; c < COLS; ++c) {
+                const int m = col0 + c;
+                if (m < count) store_y(p, p.experts > 0 ? list[m] : m, n0 + row, acc[c]);
+            }
         }
         return;
     }
@@ -667,13 +679,13 @@ __global__ void __launch_bounds__(W4_THREADS, W4Layout<NC, GROUP>::CTAS)
     float* sums = reinterpret_cast<float*>(gen + L::W);
     if (summer) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (c < count) sums[c * W4_TILE + row] = acc[c];
+        for (int c = 0; c < COLS; ++c)
+            if (col0 + c < count) sums[(col0 + c) * W4_TILE + row] = acc[c];
     }
     cluster_sync_all();
     if (stores) {
         // four warps a column
-        const int step = W4_THREADS / W4_TILE * static_cast<int>(csize);
+        const int step = L::THREADS / W4_TILE * static_cast<int>(csize);
         for (int m = static_cast<int>(crank) + (warp >> 2) * static_cast<int>(csize); m < count;
              m += step) {
             float v = 0.0f;
@@ -732,7 +744,7 @@ cudaError_t launch_w4(const CUtensorMap& map, const W4Params& p, dim3 grid, cuda
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(W4_THREADS);
+    cfg.blockDim = dim3(W4Layout<NC, GROUP>::THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
