@@ -96,7 +96,9 @@ typedef enum {
 /* Plan for `rows` rows (an upper bound is fixed by the tensors, the split over
  * experts is read from `offsets` on the device at every run).  rows >= 0,
  * 1 <= experts <= 1024, N and K multiples of 8, all below 2^31 (and experts * N
- * too).  Returns NULL on error.  The plan owns a 32-byte device status record. */
+ * too).  Returns NULL on error.  The plan owns a device record of 40 bytes (its
+ * status and the counter from which a run hands out its tiles), so runs of one
+ * plan must not overlap on the GPU. */
 TMAGEMM_API gemm_grouped_plan* gemm_grouped_create_plan(int64_t rows, int64_t N, int64_t K,
                                                         int experts, int op, int dtype_out);
 

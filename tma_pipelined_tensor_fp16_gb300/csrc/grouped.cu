@@ -148,8 +148,10 @@ gemm_grouped_plan* gemm_grouped_create_plan(int64_t rows, int64_t N, int64_t K, 
                       op_name(op), static_cast<long long>(rows), static_cast<long long>(N),
                       static_cast<long long>(K), experts, p.block_n, BLK_K, p.pipe_depth,
                       p.smem_bytes, p.grid, dtype_out == GEMM_OUT_F16 ? "f16" : "f32");
-        cudaError_t e = cudaMalloc(&p.d_status, sizeof(DevStatus));
-        if (e == cudaSuccess) e = cudaMemset(p.d_status, 0, sizeof(DevStatus));
+        // the status record and, behind it, the two counters
+        cudaError_t e = cudaMalloc(&p.d_status, sizeof(DevStatus) + 2 * sizeof(unsigned));
+        if (e == cudaSuccess)
+            e = cudaMemset(p.d_status, 0, sizeof(DevStatus) + 2 * sizeof(unsigned));
         if (e != cudaSuccess) {
             if (p.d_status) cudaFree(p.d_status);
             return cuda_fail("allocating the device status record", e);
@@ -232,6 +234,7 @@ int gemm_grouped_run(gemm_grouped_plan* plan, const void* P, const void* Q,
         p.offsets = offsets;
         p.out = out;
         p.status = plan->d_status;
+        p.counters = reinterpret_cast<unsigned*>(plan->d_status + 1);
         if (++plan->epoch <= 0) plan->epoch = 1;
         p.epoch = plan->epoch;
         p.budget_ns = 2000ull * 1000000ull;

@@ -25,6 +25,7 @@ struct GroupedParams {
     const int* offsets;
     void* out;
     DevStatus* status;
+    unsigned* counters;  // tiles taken beyond the first ones, CTAs finished
     int epoch;
     unsigned long long budget_ns;
 };

@@ -16,8 +16,11 @@
 //
 // The split of the rows over the experts is data: it is read from `offsets` on
 // the device.  Every CTA builds the prefix sum of the experts' row tiles in
-// shared memory and walks the tiles u = blockIdx.x, + gridDim.x, ... expert by
-// expert, so no host copy of the counts and no padding of the rows is needed.
+// shared memory, so no host copy of the counts and no padding of the rows is
+// needed.  A tile's cost depends on its expert (GRAD_WEIGHT contracts over the
+// expert's rows), so tiles are handed out while the kernel runs: a CTA starts on
+// tile blockIdx.x and takes the next ones from a counter, which the last CTA to
+// finish sets back to zero.  Which CTA computes a tile varies, its sum does not.
 //   * A row tile that reaches past its expert's last row multiplies the next
 //     expert's rows too and does not store them.
 //   * Rows from offsets[experts] on form a last group without products: its
@@ -92,18 +95,47 @@ struct GroupedUnit {
 
 __device__ __forceinline__ int clamp_row(int r, int rows) { return r < 0 ? 0 : (r > rows ? rows : r); }
 
-// The CTA's tiles, in order.
+// Tiles handed from the producer warp to the others through a ring in shared
+// memory: GROUPED_SLOTS words, each with a full and an empty barrier.
+constexpr int GROUPED_SLOTS = 4;
+constexpr int GROUPED_READERS = 5;  // the MMA warp and the four epilogue warps
+
+__device__ __forceinline__ int ld_shared_int(uint32_t addr)
+{
+    int v;
+    asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_shared_int(uint32_t addr, int v)
+{
+    asm volatile("st.shared.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// A reader warp's next tile, or -1 when there is none (or the run is abandoned).
+__device__ __forceinline__ int grouped_read(uint32_t bars, int use, Watchdog& wd, uint32_t lane)
+{
+    const int slot = use % GROUPED_SLOTS;
+    if (!wd.wait(bars + (BAR_CLC_FULL + slot) * 8u, static_cast<uint32_t>(use / GROUPED_SLOTS) & 1u,
+                 WAIT_CLC_FULL, -1, use))
+        return -1;
+    const int u = ld_shared_int(bars + CLC_RESP_OFFSET + slot * 4u);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + (BAR_CLC_EMPTY + slot) * 8u);
+    return u;
+}
+
+// Decoding of a tile number.
 template <int OP, int BN>
 struct GroupedTiles {
     const GroupedParams* p;
     const int* row0;   // [experts + 2] first row of a group; the end
     const int* tile0;  // [experts + 2] first row tile of a group; the end
-    int u;             // next unit
-    int total;
+    int total;         // tiles
 
-    __device__ __forceinline__ bool next(GroupedUnit& w)
+    __device__ __forceinline__ bool at(int u, GroupedUnit& w) const
     {
-        if (u >= total) return false;
+        if (u < 0 || u >= total) return false;
         int l, tm;
         if constexpr (OP == GROUPED_GRAD_WEIGHT) {
             const int per = p->tiles_m * p->tiles_n;
@@ -140,7 +172,6 @@ struct GroupedTiles {
             w.k0 = 0;
             w.klen = w.expert < p->experts ? p->depth : 0;
         }
-        u += static_cast<int>(gridDim.x);
         return true;
     }
 };
@@ -254,6 +285,10 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
             mbar_init(bar(BAR_TMEM_FULL + a), 1);
             mbar_init(bar(BAR_TMEM_EMPTY + a), 128);
         }
+        for (int j = 0; j < GROUPED_SLOTS; ++j) {
+            mbar_init(bar(BAR_CLC_FULL + j), 1);
+            mbar_init(bar(BAR_CLC_EMPTY + j), GROUPED_READERS);
+        }
         mbar_init(bar(BAR_DRAIN), 1);
         fence_mbar_init();
     }
@@ -272,7 +307,6 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     tiles0.p = &p;
     tiles0.row0 = row0;
     tiles0.tile0 = tile0;
-    tiles0.u = static_cast<int>(blockIdx.x);
     if constexpr (OP == GROUPED_GRAD_WEIGHT) {
         tiles0.total = p.experts * p.tiles_m * p.tiles_n;
     } else {
@@ -322,9 +356,22 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
         int issued = 0;
         int end_stage = 0;
         uint32_t end_phase = 0;
-        GroupedTiles<OP, BN> tiles = tiles0;
         GroupedUnit w;
-        while (tiles.next(w)) {
+        int u = static_cast<int>(blockIdx.x);
+        for (int use = 0;; ++use) {
+            // hand the tile out (also the one past the end), then fetch the next
+            const int slot = use % GROUPED_SLOTS;
+            const bool free = wd.wait(bar(BAR_CLC_EMPTY + slot),
+                                      (static_cast<uint32_t>(use / GROUPED_SLOTS) & 1u) ^ 1u,
+                                      WAIT_CLC_EMPTY, -1, use);
+            if (lane == 0 && free) {
+                st_shared_int(bars + CLC_RESP_OFFSET + slot * 4u, u);
+                mbar_arrive(bar(BAR_CLC_FULL + slot));
+            }
+            __syncwarp();
+            if (wd.aborted || !tiles0.at(u, w)) break;
+            int next = 0;
+            if (lane == 0) next = static_cast<int>(gridDim.x + atomicAdd(p.counters, 1u));
             const int kb_count = (w.klen + BLK_K - 1) / BLK_K;
             for (int kb = 0; kb < kb_count; ++kb) {
                 const bool ok = wd.wait(bar(BAR_EMPTY + stage), phase ^ 1u, WAIT_EMPTY, w.n0, kb);
@@ -365,6 +412,13 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
                     end_phase = phase;
                 }
             }
+            u = __shfl_sync(0xffffffffu, next, 0);
+        }
+        // the last CTA to get here sets the counters back for the next run
+        if (lane == 0 && atomicAdd(p.counters + 1, 1u) == gridDim.x - 1) {
+            p.counters[0] = 0;
+            p.counters[1] = 0;
+            __threadfence();
         }
         // an abandoned run: the loads in flight land before the CTA exits
         if (lane == 0 && wd.aborted) {
@@ -389,9 +443,8 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
         uint32_t phase = 0;
         int acc = 0;
         uint32_t acc_phase = 0;
-        GroupedTiles<OP, BN> tiles = tiles0;
         GroupedUnit w;
-        while (tiles.next(w)) {
+        for (int use = 0; tiles0.at(grouped_read(bars, use, wd, lane), w); ++use) {
             const int kb_count = (w.klen + BLK_K - 1) / BLK_K;
             if (kb_count == 0) continue;  // a tile of zeros has no accumulator
             wd.wait(bar(BAR_TMEM_EMPTY + acc), acc_phase ^ 1u, WAIT_TMEM_EMPTY, w.n0, -1);
@@ -458,9 +511,8 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
         int acc = 0;
         uint32_t acc_phase = 0;
         uint32_t sub_count = 0;
-        GroupedTiles<OP, BN> tiles = tiles0;
         GroupedUnit w;
-        while (tiles.next(w)) {
+        for (int use = 0; tiles0.at(grouped_read(bars, use, wd, lane), w); ++use) {
             const bool zero = w.klen == 0;
             if (!zero) {
                 wd.wait(bar(BAR_TMEM_FULL + acc), acc_phase, WAIT_TMEM_FULL, w.n0, -1);
