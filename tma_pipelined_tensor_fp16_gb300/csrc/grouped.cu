@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <new>
 
@@ -16,7 +17,8 @@ struct gemm_grouped_plan {
     int64_t rows, N, K;
     int experts, op, dtype;
     int device;
-    int block_n, grid, pipe_depth;
+    bool pair;
+    int block_m, block_n, grid, pipe_depth;
     unsigned smem_bytes;
     int tiles_m, tiles_n;
     DevStatus* d_status;
@@ -58,6 +60,17 @@ int encode(CUtensorMap* map, CUtensorMapDataType dt, int elt, const void* base, 
         return fail(GEMM_ERR_CUDA, buf);
     }
     return GEMM_OK;
+}
+
+constexpr int PAIR_DEPTH = 3;  // stages of two K blocks in the pair kernel
+
+// CTA pairs (tiles of 256 x 256) or single CTAs (128 x 256 or 128 x 128).
+bool use_pairs(int64_t rows, int64_t N, int64_t K, int experts, int op, int sms)
+{
+    const char* force = std::getenv("GROUPED_PAIR");
+    if (force) return force[0] == '1';
+    (void)rows; (void)N; (void)K; (void)experts; (void)op; (void)sms;
+    return false;
 }
 
 const char* op_name(int op)
@@ -115,38 +128,50 @@ gemm_grouped_plan* gemm_grouped_create_plan(int64_t rows, int64_t N, int64_t K, 
         p.dtype = dtype_out;
         p.device = dev;
         const int64_t cols = out_cols_of(p);
+        const uint32_t table = grouped_table_bytes(op, experts);
+        p.pair = use_pairs(rows, N, K, experts, op, sms) &&
+                 smem_layout(2 * PAIR_DEPTH, 128, NUM_STAGING).total + table <=
+                     static_cast<uint32_t>(smem_optin);
+        p.block_m = p.pair ? 2 * BLK_M : BLK_M;
         // Row tiles: exact for GRAD_WEIGHT; else every expert's last tile is
         // half full on average, and at most one more tile than its rows fill
         // (and one group for the rows that belong to none).
         int64_t expect, most;
         if (op == GROUPED_GRAD_WEIGHT) {
-            expect = most = ceil_div(N, BLK_M) * experts;
+            expect = most = ceil_div(N, p.block_m) * experts;
         } else {
-            expect = ceil_div(rows, BLK_M) + std::min<int64_t>(experts, rows) / 2;
-            most = rows / BLK_M + std::min<int64_t>(experts + 1, rows);
+            expect = ceil_div(rows, p.block_m) + std::min<int64_t>(experts, rows) / 2;
+            most = rows / p.block_m + std::min<int64_t>(experts + 1, rows);
         }
-        p.block_n = cols > 128 && expect * ceil_div(cols, 256) >= sms ? 256 : 128;
+        p.block_n = p.pair || (cols > 128 && expect * ceil_div(cols, 256) >= sms) ? 256 : 128;
         const int64_t tn = ceil_div(cols, p.block_n);
         if (most * tn >= (int64_t(1) << 31) - 65536)
             return fail(GEMM_ERR_UNSUPPORTED, "too many output tiles");
         p.tiles_n = static_cast<int>(tn);
-        p.tiles_m = static_cast<int>(ceil_div(N, BLK_M));
-        p.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, most * tn)));
-        const uint32_t table = grouped_table_bytes(op, experts);
-        for (int d = MAX_STAGES; d >= 1; --d) {
-            const uint32_t need = smem_layout(d, p.block_n, NUM_STAGING).total + table;
-            if (need <= static_cast<uint32_t>(smem_optin)) {
-                p.pipe_depth = d;
-                p.smem_bytes = need;
-                break;
+        p.tiles_m = static_cast<int>(ceil_div(N, p.block_m));
+        if (p.pair) {
+            p.grid = static_cast<int>(2 * std::max<int64_t>(1, std::min<int64_t>(sms / 2, most * tn)));
+            p.pipe_depth = PAIR_DEPTH;
+            p.smem_bytes = smem_layout(2 * PAIR_DEPTH, 128, NUM_STAGING).total + table;
+        } else {
+            p.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, most * tn)));
+            for (int d = MAX_STAGES; d >= 1; --d) {
+                const uint32_t need = smem_layout(d, p.block_n, NUM_STAGING).total + table;
+                if (need <= static_cast<uint32_t>(smem_optin)) {
+                    p.pipe_depth = d;
+                    p.smem_bytes = need;
+                    break;
+                }
             }
+            if (p.pipe_depth < 2)
+                return fail(GEMM_ERR_UNSUPPORTED, "no stage count fits shared memory");
         }
-        if (p.pipe_depth < 2) return fail(GEMM_ERR_UNSUPPORTED, "no stage count fits shared memory");
         std::snprintf(p.desc, sizeof(p.desc),
-                      "grouped op=%s rows=%lld N=%lld K=%lld experts=%d tile=128x%dx%d "
+                      "grouped op=%s rows=%lld N=%lld K=%lld experts=%d tile=%dx%dx%d "
                       "pipe_depth=%d smem=%u grid=%d out=%s",
                       op_name(op), static_cast<long long>(rows), static_cast<long long>(N),
-                      static_cast<long long>(K), experts, p.block_n, BLK_K, p.pipe_depth,
+                      static_cast<long long>(K), experts, p.block_m, p.block_n,
+                      p.pair ? 2 * BLK_K : BLK_K, p.pipe_depth,
                       p.smem_bytes, p.grid, dtype_out == GEMM_OUT_F16 ? "f16" : "f32");
         // the status record and, behind it, the two counters
         cudaError_t e = cudaMalloc(&p.d_status, sizeof(DevStatus) + 2 * sizeof(unsigned));
@@ -199,7 +224,9 @@ int gemm_grouped_run(gemm_grouped_plan* plan, const void* P, const void* Q,
         int r;
         if (plan->op == GROUPED_FORWARD) {
             r = encode(&tmA, F16, 2, P, K, R, 0, BLK_K, BLK_M, "A");
-            if (r == GEMM_OK) r = encode(&tmB, F16, 2, Q, K, N, E, BLK_K, plan->block_n, "B");
+            if (r == GEMM_OK) 
+                r = encode(&tmB, F16, 2, Q, K, N, E, BLK_K,
+                           plan->pair ? plan->block_n / 2 : plan->block_n, "B");
         } else if (plan->op == GROUPED_GRAD_INPUT) {
             r = encode(&tmA, F16, 2, P, N, R, 0, BLK_K, BLK_M, "dC");
             if (r == GEMM_OK) r = encode(&tmB, F16, 2, Q, K, N, E, 64, BLK_K, "B");
@@ -215,6 +242,7 @@ int gemm_grouped_run(gemm_grouped_plan* plan, const void* P, const void* Q,
         GroupedSpec s = {};
         s.op = plan->op;
         s.block_n = plan->block_n;
+        s.pair = plan->pair;
         s.f16out = elt == 2;
         s.grid = plan->grid;
         s.smem_bytes = plan->smem_bytes;

@@ -33,6 +33,7 @@ struct GroupedParams {
 struct GroupedSpec {
     int op;
     int block_n;
+    bool pair;  // CTA pairs: tiles of 256 x 256
     bool f16out;
     int grid;
     unsigned smem_bytes;

@@ -1,5 +1,6 @@
 // grouped_forward.cu -- the GROUPED_FORWARD form of the grouped product.
 #include "kernel_grouped.cuh"
+#include "kernel_grouped_pair.cuh"
 
 namespace tg {
 

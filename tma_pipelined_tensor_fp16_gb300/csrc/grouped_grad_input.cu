@@ -1,5 +1,6 @@
 // grouped_grad_input.cu -- the GROUPED_GRAD_INPUT form of the grouped product.
 #include "kernel_grouped.cuh"
+#include "kernel_grouped_pair.cuh"
 
 namespace tg {
 

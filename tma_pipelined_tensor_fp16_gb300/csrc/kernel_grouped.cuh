@@ -116,9 +116,9 @@ __device__ __forceinline__ void st_shared_int(uint32_t addr, int v)
 __device__ __forceinline__ int grouped_read(uint32_t bars, int use, Watchdog& wd, uint32_t lane)
 {
     const int slot = use % GROUPED_SLOTS;
-    if (!wd.wait(bars + (BAR_CLC_FULL + slot) * 8u, static_cast<uint32_t>(use / GROUPED_SLOTS) & 1u,
-                 WAIT_CLC_FULL, -1, use))
-        return -1;
+    const bool ok = wd.wait(bars + (BAR_CLC_FULL + slot) * 8u,
+                            static_cast<uint32_t>(use / GROUPED_SLOTS) & 1u, WAIT_CLC_FULL, -1, use);
+    if (!__all_sync(0xffffffffu, ok)) return -1;  // the warp stays together
     const int u = ld_shared_int(bars + CLC_RESP_OFFSET + slot * 4u);
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + (BAR_CLC_EMPTY + slot) * 8u);
@@ -126,7 +126,7 @@ __device__ __forceinline__ int grouped_read(uint32_t bars, int use, Watchdog& wd
 }
 
 // Decoding of a tile number.
-template <int OP, int BN>
+template <int OP, int BM, int BN>
 struct GroupedTiles {
     const GroupedParams* p;
     const int* row0;   // [experts + 2] first row of a group; the end
@@ -161,13 +161,13 @@ struct GroupedTiles {
         raster_tile(l, tm, p->tiles_n, p->group_m, mt, nt);
         w.n0 = nt * BN;
         if constexpr (OP == GROUPED_GRAD_WEIGHT) {
-            w.m0 = mt * BLK_M;
+            w.m0 = mt * BM;
             w.row_end = p->out_rows;
             w.k0 = clamp_row(p->offsets[w.expert], p->rows);
             w.klen = clamp_row(p->offsets[w.expert + 1], p->rows) - w.k0;
             if (w.klen < 0) w.klen = 0;
         } else {
-            w.m0 = row0[w.expert] + mt * BLK_M;
+            w.m0 = row0[w.expert] + mt * BM;
             w.row_end = row0[w.expert + 1];
             w.k0 = 0;
             w.klen = w.expert < p->experts ? p->depth : 0;
@@ -175,6 +175,46 @@ struct GroupedTiles {
         return true;
     }
 };
+
+// First row and first tile of BM rows of the experts and of the rest, by all
+// threads of the CTA: each sums a contiguous share of the groups, the shares are
+// scanned.  `warp_tiles` is scratch for one word per warp.
+template <int BM>
+__device__ __forceinline__ void grouped_table(const GroupedParams& p, int* row0, int* tile0,
+                                              int* warp_tiles, int tid, uint32_t lane)
+{
+    const int warp = tid >> 5;
+    const int groups = p.experts + 1;
+    const int share = (groups + GROUPED_THREADS - 1) / GROUPED_THREADS;
+    const int g0 = tid * share;
+    auto start = [&](int g) { return g <= p.experts ? clamp_row(p.offsets[g], p.rows) : p.rows; };
+    int sum = 0;
+    for (int i = 0; i < share && g0 + i < groups; ++i) {
+        const int a = start(g0 + i), b = start(g0 + i + 1);
+        sum += b > a ? (b - a + BM - 1) / BM : 0;
+    }
+    int scan = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, scan, d);
+        if (lane >= static_cast<uint32_t>(d)) scan += v;
+    }
+    if (lane == 31) warp_tiles[warp] = scan;
+    __syncthreads();
+    int at = scan - sum;
+    for (int w = 0; w < warp; ++w) at += warp_tiles[w];
+    for (int i = 0; i < share && g0 + i < groups; ++i) {
+        const int a = start(g0 + i), b = start(g0 + i + 1);
+        row0[g0 + i] = a;
+        tile0[g0 + i] = at;
+        at += b > a ? (b - a + BM - 1) / BM : 0;
+        if (g0 + i == groups - 1) {
+            row0[groups] = p.rows;
+            tile0[groups] = at;
+        }
+    }
+    __syncthreads();
+}
 
 // One 128-byte-wide sub-tile of the output: each warp stages its 32 rows
 // (swizzled) and stores them with one bulk tensor store, or, where only the
@@ -237,6 +277,33 @@ __device__ __forceinline__ void store_sub_tile(const uint32_t* v, int q, uint32_
     }
     if (lane == 0) bulk_commit_group();
     ++sub_count;
+}
+
+// A 128 x BN accumulator (or zeros) to the output, sub-tile by sub-tile.
+template <int OP, int BN, bool F16OUT>
+__device__ __forceinline__ void store_tile(uint32_t tmem_acc, bool zero, int q, uint32_t lane,
+                                           uint32_t staging, const CUtensorMap* tmC,
+                                           const GroupedParams& p, const GroupedUnit& w,
+                                           uint32_t& sub_count, bool do_store)
+{
+    constexpr int SUB_COLS = F16OUT ? 64 : 32;
+    const uint32_t taddr = tmem_acc + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+    for (int j = 0; j < BN / SUB_COLS; ++j) {
+        const int col0 = w.n0 + j * SUB_COLS;
+        if (col0 >= p.out_cols) break;
+        uint32_t v[SUB_COLS];
+        if (zero) {
+#pragma unroll
+            for (int i = 0; i < SUB_COLS; ++i) v[i] = 0u;
+        } else if constexpr (F16OUT) {
+            tmem_load_32cols(taddr + j * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+            tmem_load_32cols(taddr + j * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+        } else {
+            tmem_load_32cols(taddr + j * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+        }
+        store_sub_tile<OP, F16OUT>(v, q, lane, staging, tmC, p, w, col0, sub_count, do_store);
+    }
 }
 
 }  // namespace
@@ -303,49 +370,17 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     griddep_launch_dependents();
     const uint32_t tmem_base = *tmem_slot;
 
-    GroupedTiles<OP, BN> tiles0;
+    GroupedTiles<OP, BLK_M, BN> tiles0;
     tiles0.p = &p;
     tiles0.row0 = row0;
     tiles0.tile0 = tile0;
     if constexpr (OP == GROUPED_GRAD_WEIGHT) {
         tiles0.total = p.experts * p.tiles_m * p.tiles_n;
     } else {
-        // first row and first row tile of the experts and of the rest: each
-        // thread sums a contiguous share of the groups, the shares are scanned
-        int* warp_tiles = reinterpret_cast<int*>(gen + L.bars + CLC_RESP_OFFSET);
-        const int groups = p.experts + 1;
-        const int share = (groups + GROUPED_THREADS - 1) / GROUPED_THREADS;
-        const int g0 = tid * share;
-        auto start = [&](int g) {
-            return g <= p.experts ? clamp_row(p.offsets[g], p.rows) : p.rows;
-        };
-        int sum = 0;
-        for (int i = 0; i < share && g0 + i < groups; ++i) {
-            const int a = start(g0 + i), b = start(g0 + i + 1);
-            sum += b > a ? (b - a + BLK_M - 1) / BLK_M : 0;
-        }
-        int scan = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int v = __shfl_up_sync(0xffffffffu, scan, d);
-            if (lane >= static_cast<uint32_t>(d)) scan += v;
-        }
-        if (lane == 31) warp_tiles[warp] = scan;
-        __syncthreads();
-        int at = scan - sum;
-        for (int w = 0; w < warp; ++w) at += warp_tiles[w];
-        for (int i = 0; i < share && g0 + i < groups; ++i) {
-            const int a = start(g0 + i), b = start(g0 + i + 1);
-            row0[g0 + i] = a;
-            tile0[g0 + i] = at;
-            at += b > a ? (b - a + BLK_M - 1) / BLK_M : 0;
-            if (g0 + i == groups - 1) {
-                row0[groups] = p.rows;
-                tile0[groups] = at;
-            }
-        }
-        __syncthreads();
-        tiles0.total = tile0[groups] * p.tiles_n;
+        grouped_table<BLK_M>(p, row0, tile0,
+                             reinterpret_cast<int*>(gen + L.bars + CLC_RESP_OFFSET + 32), tid,
+                             lane);
+        tiles0.total = tile0[p.experts + 1] * p.tiles_n;
     }
 
     if (warp == 0) {
@@ -369,7 +404,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
                 mbar_arrive(bar(BAR_CLC_FULL + slot));
             }
             __syncwarp();
-            if (wd.aborted || !tiles0.at(u, w)) break;
+            if (__any_sync(0xffffffffu, wd.aborted) || !tiles0.at(u, w)) break;
             int next = 0;
             if (lane == 0) next = static_cast<int>(gridDim.x + atomicAdd(p.counters, 1u));
             const int kb_count = (w.klen + BLK_K - 1) / BLK_K;
@@ -506,7 +541,6 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
         __syncwarp();
     } else {
         // -------------------------------------------------------- epilogue
-        constexpr int SUB_COLS = F16OUT ? 64 : 32;
         const int q = warp & 3;
         int acc = 0;
         uint32_t acc_phase = 0;
@@ -518,26 +552,8 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
                 wd.wait(bar(BAR_TMEM_FULL + acc), acc_phase, WAIT_TMEM_FULL, w.n0, -1);
                 tc_fence_after_sync();
             }
-            const uint32_t taddr = tmem_base + static_cast<uint32_t>(acc * BN) +
-                                   (static_cast<uint32_t>(q * 32) << 16);
-#pragma unroll 1
-            for (int j = 0; j < BN / SUB_COLS; ++j) {
-                const int col0 = w.n0 + j * SUB_COLS;
-                if (col0 >= p.out_cols) break;
-                uint32_t v[SUB_COLS];
-                if (zero) {
-#pragma unroll
-                    for (int i = 0; i < SUB_COLS; ++i) v[i] = 0u;
-                } else if constexpr (F16OUT) {
-                    tmem_load_32cols(taddr + j * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-                    tmem_load_32cols(taddr + j * 64 + 32,
-                                     *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
-                } else {
-                    tmem_load_32cols(taddr + j * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-                }
-                store_sub_tile<OP, F16OUT>(v, q, lane, staging, &tmC, p, w, col0, sub_count,
-                                           !wd.aborted);
-            }
+            store_tile<OP, BN, F16OUT>(tmem_base + static_cast<uint32_t>(acc * BN), zero, q, lane,
+                                       staging, &tmC, p, w, sub_count, !wd.aborted);
             if (!zero) {
                 tc_fence_before_sync();
                 mbar_arrive(bar(BAR_TMEM_EMPTY + acc));
@@ -556,11 +572,15 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     }
 }
 
+template <int OP>
+cudaError_t launch_grouped_pair(const GroupedSpec& s, cudaStream_t stream);
+
 // Launch one of the built tile widths of form OP; each form is instantiated by
 // a translation unit of its own, so that they compile in parallel.
 template <int OP>
 cudaError_t launch_grouped_op(const GroupedSpec& s, cudaStream_t stream)
 {
+    if (s.pair) return launch_grouped_pair<OP>(s, stream);
     auto kernel = s.block_n == 256
                       ? (s.f16out ? k_grouped<OP, 256, true> : k_grouped<OP, 256, false>)
                       : (s.f16out ? k_grouped<OP, 128, true> : k_grouped<OP, 128, false>);
