@@ -392,9 +392,12 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
         int end_stage = 0;
         uint32_t end_phase = 0;
         GroupedUnit w;
-        int u = static_cast<int>(blockIdx.x);
-        for (int use = 0;; ++use) {
-            // hand the tile out (also the one past the end), then fetch the next
+        // The tile after the one whose loads are being issued is handed out
+        // before them, and the one after that is on its way from the counter.
+        auto take = [&] {
+            return lane == 0 ? static_cast<int>(gridDim.x + atomicAdd(p.counters, 1u)) : 0;
+        };
+        auto hand_out = [&](int use, int u) {
             const int slot = use % GROUPED_SLOTS;
             const bool free = wd.wait(bar(BAR_CLC_EMPTY + slot),
                                       (static_cast<uint32_t>(use / GROUPED_SLOTS) & 1u) ^ 1u,
@@ -404,9 +407,15 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
                 mbar_arrive(bar(BAR_CLC_FULL + slot));
             }
             __syncwarp();
-            if (__any_sync(0xffffffffu, wd.aborted) || !tiles0.at(u, w)) break;
-            int next = 0;
-            if (lane == 0) next = static_cast<int>(gridDim.x + atomicAdd(p.counters, 1u));
+        };
+        int u = static_cast<int>(blockIdx.x);
+        int after = take();
+        hand_out(0, u);
+        for (int use = 1; tiles0.at(u, w); ++use) {
+            const int next = __shfl_sync(0xffffffffu, after, 0);
+            hand_out(use, next);  // also the first one past the end
+            if (__any_sync(0xffffffffu, wd.aborted)) break;
+            after = take();
             const int kb_count = (w.klen + BLK_K - 1) / BLK_K;
             for (int kb = 0; kb < kb_count; ++kb) {
                 const bool ok = wd.wait(bar(BAR_EMPTY + stage), phase ^ 1u, WAIT_EMPTY, w.n0, kb);
@@ -447,7 +456,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
                     end_phase = phase;
                 }
             }
-            u = __shfl_sync(0xffffffffu, next, 0);
+            u = next;
         }
         // the last CTA to get here sets the counters back for the next run
         if (lane == 0 && atomicAdd(p.counters + 1, 1u) == gridDim.x - 1) {

@@ -202,26 +202,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GROUPED_THREADS, 1)
         int end_stage = 0;
         uint32_t end_phase = 0;
         GroupedUnit w;
-        int u = static_cast<int>(blockIdx.x) / 2;
-        for (int use = 0;; ++use) {
-            if (leader) {
-                const int slot = use % GROUPED_SLOTS;
-                const bool free = wd.wait(bar(BAR_CLC_EMPTY + slot),
-                                          (static_cast<uint32_t>(use / GROUPED_SLOTS) & 1u) ^ 1u,
-                                          WAIT_CLC_EMPTY, -1, use);
-                if (lane < 2 && free) {  // lane r tells the CTA of rank r
-                    const uint32_t to = map_shared_rank(bars + CLC_RESP_OFFSET + slot * 4u, lane);
-                    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(to), "r"(u) : "memory");
-                    mbar_arrive_cluster(map_shared_rank(bar(BAR_CLC_FULL + slot), lane));
-                }
-                __syncwarp();
-            } else {
-                u = pair_read(bars, use, wd, lane);
+        // The leader hands the tile after the one whose loads are being issued to
+        // both CTAs before them, and has the one after that on its way from the
+        // counter.
+        auto take = [&] {
+            return leader && lane == 0
+                       ? static_cast<int>(gridDim.x / 2 + atomicAdd(p.counters, 1u))
+                       : 0;
+        };
+        auto hand_out = [&](int use, int tile) {
+            const int slot = use % GROUPED_SLOTS;
+            const bool free = wd.wait(bar(BAR_CLC_EMPTY + slot),
+                                      (static_cast<uint32_t>(use / GROUPED_SLOTS) & 1u) ^ 1u,
+                                      WAIT_CLC_EMPTY, -1, use);
+            if (lane < 2 && free) {  // lane r tells the CTA of rank r
+                const uint32_t to = map_shared_rank(bars + CLC_RESP_OFFSET + slot * 4u, lane);
+                asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(to), "r"(tile) : "memory");
+                mbar_arrive_cluster(map_shared_rank(bar(BAR_CLC_FULL + slot), lane));
             }
-            if (__any_sync(0xffffffffu, wd.aborted) || !tiles0.at(u, w)) break;
-            int next = 0;
-            if (leader && lane == 0)
-                next = static_cast<int>(gridDim.x / 2 + atomicAdd(p.counters, 1u));
+            __syncwarp();
+        };
+        int u = static_cast<int>(blockIdx.x) / 2;
+        int after = take();
+        if (leader)
+            hand_out(0, u);
+        else
+            u = pair_read(bars, 0, wd, lane);
+        for (int use = 1; tiles0.at(u, w); ++use) {
+            const int next = __shfl_sync(0xffffffffu, after, 0);
+            if (leader) {
+                hand_out(use, next);  // also the first one past the end
+                after = take();
+            }
+            if (__any_sync(0xffffffffu, wd.aborted)) break;
             const int stages = (w.klen + PAIR_STAGE_K - 1) / PAIR_STAGE_K;
             for (int ki = 0; ki < stages; ++ki) {
                 const bool tail = ki == stages - 1 && dirty_of(w);
@@ -279,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GROUPED_THREADS, 1)
                     end_phase = phase;
                 }
             }
-            u = __shfl_sync(0xffffffffu, next, 0);
+            u = leader ? next : pair_read(bars, use, wd, lane);
         }
         // the last leader to get here sets the counters back for the next run
         if (leader && lane == 0 && atomicAdd(p.counters + 1, 1u) == gridDim.x / 2 - 1) {
