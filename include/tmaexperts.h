@@ -102,6 +102,20 @@ typedef enum {
 TMAGEMM_API gemm_grouped_plan* gemm_grouped_create_plan(int64_t rows, int64_t N, int64_t K,
                                                         int experts, int op, int dtype_out);
 
+/* Same with an explicit output tile: 128 x 128 or 128 x 256 on single CTAs, 256 x
+ * 256 on CTA pairs (up to about 200 experts).  GEMM_GROUPED_TILE_AUTO chooses by
+ * the number of tiles and the rows per expert. */
+typedef enum {
+    GEMM_GROUPED_TILE_AUTO = 0,
+    GEMM_GROUPED_TILE_128X128 = 1,
+    GEMM_GROUPED_TILE_128X256 = 2,
+    GEMM_GROUPED_TILE_256X256 = 3
+} gemm_grouped_tile;
+
+TMAGEMM_API gemm_grouped_plan* gemm_grouped_create_plan_ex(int64_t rows, int64_t N, int64_t K,
+                                                           int experts, int op, int dtype_out,
+                                                           int tile);
+
 /* Enqueue the product.  `offsets` (experts + 1 int32, device memory) is as
  * gemm_expert_sort writes it: ascending from 0 to at most rows.  Values outside
  * [0, rows] are taken as the nearest bound, so a bad table gives wrong rows but

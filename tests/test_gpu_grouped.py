@@ -35,13 +35,13 @@ def _product(op, P, Q, offsets, shape):
     return out
 
 
-def _run(op, rows, N, K, counts, out, make, poison=None):
+def _run(op, rows, N, K, counts, out, make, poison=None, tile="auto"):
     import torch
 
     import tma_pipelined_tensor_fp16_gb300 as tg
     E = len(counts)
     offsets = offsets_of(counts)
-    plan = tg.GroupedPlan(rows, N, K, E, op=op, out=out)
+    plan = tg.GroupedPlan(rows, N, K, E, op=op, out=out, tile=tile)
     sp, sq, so = plan.shapes()
     P, Q = make(sp), make(sq)
     got = torch.full((so[0] + 1,) + so[1:], float("nan"), dtype=plan.dtype, device="cuda")
@@ -73,28 +73,34 @@ CASES = [  # rows, N, K, counts per expert
 ]
 
 
+TILES = ["128x128", "128x256", "256x256"]
+
+
+@pytest.mark.parametrize("tile", TILES)
 @pytest.mark.parametrize("out", ["f16", "f32"])
 @pytest.mark.parametrize("op", OPS)
 @pytest.mark.parametrize("rows,N,K,counts", CASES)
-def test_integers_exact(op, rows, N, K, counts, out):
+def test_integers_exact(op, rows, N, K, counts, out, tile):
     rng = np.random.default_rng(N + K)
     got, want, _, what = _run(op, rows, N, K, counts, out, lambda s: integers(rng, s),
-                              poison=np.nan)
+                              poison=np.nan, tile=tile)
     assert_same(got, want, out, what)
 
 
+@pytest.mark.parametrize("tile", TILES)
 @pytest.mark.parametrize("op", OPS)
 @pytest.mark.parametrize("rows,N,K,counts", [CASES[4], CASES[5], CASES[8]])
-def test_random(op, rows, N, K, counts):
+def test_random(op, rows, N, K, counts, tile):
     rng = np.random.default_rng(rows)
     for out in ("f16", "f32"):
         got, want, tol, what = _run(op, rows, N, K, counts, out, lambda s: normals(rng, s, 0.5),
-                                    poison=np.inf)
+                                    poison=np.inf, tile=tile)
         assert_within(got, want, tol, what)
 
 
+@pytest.mark.parametrize("tile", TILES)
 @pytest.mark.parametrize("op", OPS)
-def test_another_expert_s_infinity_stays_out(op):
+def test_another_expert_s_infinity_stays_out(op, tile):
     """A NaN or infinity in one expert's rows or weights reaches no other."""
     import torch
 
@@ -102,7 +108,7 @@ def test_another_expert_s_infinity_stays_out(op):
     rng = np.random.default_rng(9)
     counts, N, K = [70, 30, 90], 200, 136
     offsets = offsets_of(counts)
-    plan = tg.GroupedPlan(190, N, K, 3, op=op, out="f32")
+    plan = tg.GroupedPlan(190, N, K, 3, op=op, out="f32", tile=tile)
     sp, sq, so = plan.shapes()
     P, Q = integers(rng, sp), integers(rng, sq)
     want = _product(op, P, Q, offsets, so)
@@ -120,15 +126,36 @@ def test_another_expert_s_infinity_stays_out(op):
         assert_same(got[keep], want[keep], "f32")
 
 
+@pytest.mark.parametrize("tile", TILES)
 @pytest.mark.parametrize("op", OPS)
-def test_wide_tiles_and_many_units_per_cta(op):
-    """Enough tiles for 256 columns and for several tiles per CTA."""
+def test_many_tiles_per_cta(op, tile):
+    """Enough tiles that every CTA takes several from the counter."""
     rng = np.random.default_rng(4)
     N, K = (2304, 776) if op != "grad_input" else (776, 2304)
     counts = [300, 0, 1, 511, 640, 128, 700, 257, 129, 90]
     got, want, _, what = _run(op, sum(counts) + 44, N, K, counts, "f16",
-                              lambda s: integers(rng, s, -1, 1), poison=np.nan)
+                              lambda s: integers(rng, s, -1, 1), poison=np.nan, tile=tile)
     assert_same(got, want, "f16", what)
+
+
+@pytest.mark.parametrize("tile", TILES)
+def test_repeated_runs_of_one_plan(tile):
+    """The counter starts over with every run, whatever the split was before."""
+    import torch
+
+    import tma_pipelined_tensor_fp16_gb300 as tg
+    rng = np.random.default_rng(15)
+    A, B = integers(rng, (1100, 64)), integers(rng, (7, 1288, 64))
+    plan = tg.GroupedPlan(1100, 1288, 64, 7, tile=tile)
+    dA, dB = device(A), device(B)
+    for _ in range(6):
+        counts = rng.multinomial(rng.integers(0, 1101), np.ones(7) / 7)
+        C = torch.full((1100, 1288), float("nan"), dtype=torch.float16, device="cuda")
+        plan(dA, dB, device(offsets_of(counts)), C)
+        torch.cuda.synchronize()
+        assert plan.device_status() == 0
+        assert_same(C.cpu().numpy(),
+                    _product("forward", A, B, offsets_of(counts), (1100, 1288)), "f16")
 
 
 def test_many_experts():
@@ -232,6 +259,10 @@ def test_refusals():
         tg.GroupedPlan(16, 64, 64, 2, op="backward")
     with pytest.raises(ValueError):
         tg.GroupedPlan(16, 64, 64, 2, out="bf16")
+    with pytest.raises(ValueError):
+        tg.GroupedPlan(16, 64, 64, 2, tile="64x64")
+    with pytest.raises(tg.GemmError, match="so many experts"):
+        tg.GroupedPlan(16, 64, 64, 1024, tile="256x256")
     plan = tg.GroupedPlan(16, 64, 64, 2)
     z = lambda *s: torch.zeros(s, dtype=torch.float16, device="cuda")
     offs = torch.zeros(3, dtype=torch.int32, device="cuda")

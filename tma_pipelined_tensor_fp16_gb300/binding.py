@@ -91,6 +91,7 @@ _SIGS = {
     "gemm_expert_combine_grad": (ctypes.c_int, [ctypes.c_int64] + [ctypes.c_int] * 2
                                  + [ctypes.c_int64] + [ctypes.c_void_p] * 8),
     "gemm_grouped_create_plan": (ctypes.c_void_p, [ctypes.c_int64] * 3 + [ctypes.c_int] * 3),
+    "gemm_grouped_create_plan_ex": (ctypes.c_void_p, [ctypes.c_int64] * 3 + [ctypes.c_int] * 4),
     "gemm_grouped_run": (ctypes.c_int, [ctypes.c_void_p] * 6),
     "gemm_grouped_get_device_status": (ctypes.c_int, [ctypes.c_void_p]),
     "gemm_grouped_destroy": (None, [ctypes.c_void_p]),

@@ -4,7 +4,6 @@
 
 #include <algorithm>
 #include <cstdio>
-#include <cstdlib>
 #include <cstring>
 #include <new>
 
@@ -64,13 +63,51 @@ int encode(CUtensorMap* map, CUtensorMapDataType dt, int elt, const void* base, 
 
 constexpr int PAIR_DEPTH = 3;  // stages of two K blocks in the pair kernel
 
-// CTA pairs (tiles of 256 x 256) or single CTAs (128 x 256 or 128 x 128).
-bool use_pairs(int64_t rows, int64_t N, int64_t K, int experts, int op, int sms)
+// Row tiles of height bm that a plan can expect: exact for GRAD_WEIGHT; else an
+// expert's last tile is half full on average, and every expert has one.
+int64_t expected_row_tiles(int64_t rows, int64_t N, int experts, int op, int bm)
 {
-    const char* force = std::getenv("GROUPED_PAIR");
-    if (force) return force[0] == '1';
-    (void)rows; (void)N; (void)K; (void)experts; (void)op; (void)sms;
-    return false;
+    if (op == GROUPED_GRAD_WEIGHT) return ceil_div(N, bm) * experts;
+    const int64_t used = std::min<int64_t>(experts, rows);
+    return std::max(ceil_div(rows, bm) + used / 2, used);
+}
+
+// The automatic tile: the one whose waves of tiles (a launch that hands out its
+// tiles ends half a wave after the last full one) take the least time, at each
+// tile's throughput per SM relative to pairs: 0.82 for 128 x 256 on single CTAs,
+// 0.73 for 128 x 128.  Measured, pairs against 128 x 256: 16 even experts of 4096 x
+// 4096 with 1024 rows each 316 and 356 us; uneven experts of 2816 x 2048, input
+// gradient, 32 with 256 rows on average 94 and 101, 64 with 128 rows 138 and 126; a
+// single expert with 1024 rows 28 and 37 (53 with 128 x 128).  40 experts of 1416 x
+// 2056 with 777 rows in all: 128 x 128 47, 128 x 256 50, pairs 53 us.  GRAD_WEIGHT's
+// tiles of few rows are bounded by their stores, in which pairs are slower (24
+// experts of 2048 x 4096, fp32: 273 against 285 us at 682 rows per expert, 333
+// against 314 at 512).
+int choose_tile(int64_t rows, int64_t N, int64_t cols, int experts, int op, int sms, bool pair_fits)
+{
+    struct Tile {
+        int kind, bm, bn, slots;
+        double rate;
+    };
+    const Tile tiles[3] = {{GEMM_GROUPED_TILE_256X256, 256, 256, std::max(1, sms / 2), 2.0},
+                           {GEMM_GROUPED_TILE_128X256, 128, 256, sms, 0.82},
+                           {GEMM_GROUPED_TILE_128X128, 128, 128, sms, 0.73}};
+    int best = GEMM_GROUPED_TILE_128X256;
+    double best_time = -1.0;
+    for (const Tile& t : tiles) {
+        if (t.kind == GEMM_GROUPED_TILE_256X256 &&
+            (!pair_fits || (op == GROUPED_GRAD_WEIGHT && rows < 600ll * experts)))
+            continue;
+        const int64_t count = expected_row_tiles(rows, N, experts, op, t.bm) * ceil_div(cols, t.bn);
+        const double waves =
+            count <= t.slots ? 1.0 : static_cast<double>(count) / t.slots + 0.5;
+        const double time = waves * t.bm * t.bn / t.rate;
+        if (best_time < 0.0 || time < best_time) {
+            best_time = time;
+            best = t.kind;
+        }
+    }
+    return best;
 }
 
 const char* op_name(int op)
@@ -112,10 +149,18 @@ extern "C" {
 gemm_grouped_plan* gemm_grouped_create_plan(int64_t rows, int64_t N, int64_t K, int experts, int op,
                                             int dtype_out)
 {
+    return gemm_grouped_create_plan_ex(rows, N, K, experts, op, dtype_out, GEMM_GROUPED_TILE_AUTO);
+}
+
+gemm_grouped_plan* gemm_grouped_create_plan_ex(int64_t rows, int64_t N, int64_t K, int experts,
+                                               int op, int dtype_out, int tile)
+{
     gemm_grouped_plan* plan = nullptr;
     guarded([&] {
         int r = check_grouped(rows, N, K, experts, op, dtype_out);
         if (r != GEMM_OK) return r;
+        if (tile < GEMM_GROUPED_TILE_AUTO || tile > GEMM_GROUPED_TILE_256X256)
+            return fail(GEMM_ERR_INVALID_ARG, "unknown gemm_grouped_tile");
         int dev, sms, smem_optin;
         r = require_device(&dev, &sms, &smem_optin);
         if (r != GEMM_OK) return r;
@@ -129,21 +174,21 @@ gemm_grouped_plan* gemm_grouped_create_plan(int64_t rows, int64_t N, int64_t K, 
         p.device = dev;
         const int64_t cols = out_cols_of(p);
         const uint32_t table = grouped_table_bytes(op, experts);
-        p.pair = use_pairs(rows, N, K, experts, op, sms) &&
-                 smem_layout(2 * PAIR_DEPTH, 128, NUM_STAGING).total + table <=
-                     static_cast<uint32_t>(smem_optin);
+        const bool pair_fits = smem_layout(2 * PAIR_DEPTH, 128, NUM_STAGING).total + table <=
+                               static_cast<uint32_t>(smem_optin);
+        if (tile == GEMM_GROUPED_TILE_256X256 && !pair_fits)
+            return fail(GEMM_ERR_UNSUPPORTED,
+                        "tiles of 256 x 256 leave no shared memory for so many experts");
+        if (tile == GEMM_GROUPED_TILE_AUTO)
+            tile = choose_tile(rows, N, cols, experts, op, sms, pair_fits);
+        p.pair = tile == GEMM_GROUPED_TILE_256X256;
         p.block_m = p.pair ? 2 * BLK_M : BLK_M;
-        // Row tiles: exact for GRAD_WEIGHT; else every expert's last tile is
-        // half full on average, and at most one more tile than its rows fill
-        // (and one group for the rows that belong to none).
-        int64_t expect, most;
-        if (op == GROUPED_GRAD_WEIGHT) {
-            expect = most = ceil_div(N, p.block_m) * experts;
-        } else {
-            expect = ceil_div(rows, p.block_m) + std::min<int64_t>(experts, rows) / 2;
-            most = rows / p.block_m + std::min<int64_t>(experts + 1, rows);
-        }
-        p.block_n = p.pair || (cols > 128 && expect * ceil_div(cols, 256) >= sms) ? 256 : 128;
+        p.block_n = tile == GEMM_GROUPED_TILE_128X128 ? 128 : 256;
+        // at most one more tile per expert than its rows fill (and one group for
+        // the rows that belong to none)
+        const int64_t most = op == GROUPED_GRAD_WEIGHT
+                                 ? ceil_div(N, p.block_m) * experts
+                                 : rows / p.block_m + std::min<int64_t>(experts + 1, rows);
         const int64_t tn = ceil_div(cols, p.block_n);
         if (most * tn >= (int64_t(1) << 31) - 65536)
             return fail(GEMM_ERR_UNSUPPORTED, "too many output tiles");

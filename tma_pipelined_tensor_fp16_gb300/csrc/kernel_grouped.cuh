@@ -131,6 +131,7 @@ struct GroupedTiles {
     const GroupedParams* p;
     const int* row0;   // [experts + 2] first row of a group; the end
     const int* tile0;  // [experts + 2] first row tile of a group; the end
+                       // (GRAD_WEIGHT: the experts in the order of their turns)
     int total;         // tiles
 
     __device__ __forceinline__ bool at(int u, GroupedUnit& w) const
@@ -139,8 +140,9 @@ struct GroupedTiles {
         int l, tm;
         if constexpr (OP == GROUPED_GRAD_WEIGHT) {
             const int per = p->tiles_m * p->tiles_n;
-            w.expert = u / per;
-            l = u - w.expert * per;
+            const int turn = u / per;
+            w.expert = p->experts <= GROUPED_SORT_EXPERTS ? tile0[turn] : turn;
+            l = u - turn * per;
             tm = p->tiles_m;
         } else {
             // last group whose first unit is at or before u (empty groups in
@@ -163,8 +165,9 @@ struct GroupedTiles {
         if constexpr (OP == GROUPED_GRAD_WEIGHT) {
             w.m0 = mt * BM;
             w.row_end = p->out_rows;
-            w.k0 = clamp_row(p->offsets[w.expert], p->rows);
-            w.klen = clamp_row(p->offsets[w.expert + 1], p->rows) - w.k0;
+            const int* from = p->experts <= GROUPED_SORT_EXPERTS ? row0 : p->offsets;
+            w.k0 = clamp_row(from[w.expert], p->rows);
+            w.klen = clamp_row(from[w.expert + 1], p->rows) - w.k0;
             if (w.klen < 0) w.klen = 0;
         } else {
             w.m0 = row0[w.expert] + mt * BM;
@@ -175,6 +178,25 @@ struct GroupedTiles {
         return true;
     }
 };
+
+// GRAD_WEIGHT: the experts with the most rows, whose tiles take longest, come
+// first, so that the last tiles of a launch are short ones.
+__device__ __forceinline__ void grouped_order(const GroupedParams& p, int* row0, int* order, int tid)
+{
+    if (p.experts > GROUPED_SORT_EXPERTS) return;
+    for (int e = tid; e <= p.experts; e += GROUPED_THREADS) row0[e] = clamp_row(p.offsets[e], p.rows);
+    __syncthreads();
+    for (int e = tid; e < p.experts; e += GROUPED_THREADS) {
+        const int n = row0[e + 1] - row0[e];
+        int rank = 0;
+        for (int o = 0; o < p.experts; ++o) {
+            const int m = row0[o + 1] - row0[o];
+            rank += m > n || (m == n && o < e) ? 1 : 0;
+        }
+        order[rank] = e;
+    }
+    __syncthreads();
+}
 
 // First row and first tile of BM rows of the experts and of the rest, by all
 // threads of the CTA: each sums a contiguous share of the groups, the shares are
@@ -375,6 +397,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     tiles0.row0 = row0;
     tiles0.tile0 = tile0;
     if constexpr (OP == GROUPED_GRAD_WEIGHT) {
+        grouped_order(p, row0, tile0, tid);
         tiles0.total = p.experts * p.tiles_m * p.tiles_n;
     } else {
         grouped_table<BLK_M>(p, row0, tile0,

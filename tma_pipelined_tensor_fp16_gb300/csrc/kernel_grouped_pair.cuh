@@ -179,6 +179,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GROUPED_THREADS, 1)
     tiles0.row0 = row0;
     tiles0.tile0 = tile0;
     if constexpr (OP == GROUPED_GRAD_WEIGHT) {
+        grouped_order(p, row0, tile0, tid);
         tiles0.total = p.experts * p.tiles_m * p.tiles_n;
     } else {
         grouped_table<PAIR_TILE_M>(p, row0, tile0,

@@ -23,6 +23,7 @@ kernels, asynchronously on the current stream of the tensors' device (or on
 from .binding import GEMM_OUT_F16, GEMM_OUT_F32, GemmError, _check, last_error, lib
 
 GROUPED_OPS = {"forward": 0, "grad_input": 1, "grad_weight": 2}
+GROUPED_TILES = {"auto": 0, "128x128": 1, "128x256": 2, "256x256": 3}
 
 
 def _torch():
@@ -226,12 +227,15 @@ class GroupedPlan(_Handle):
     _destroy, _describe = "gemm_grouped_destroy", "gemm_grouped_describe"
     _status = "gemm_grouped_get_device_status"
 
-    def __init__(self, rows, N, K, experts, op="forward", out="f16"):
+    def __init__(self, rows, N, K, experts, op="forward", out="f16", tile="auto"):
         if op not in GROUPED_OPS:
             raise ValueError("op must be one of %s" % sorted(GROUPED_OPS))
+        if tile not in GROUPED_TILES:
+            raise ValueError("tile must be one of %s" % sorted(GROUPED_TILES))
         self.rows, self.N, self.K, self.experts, self.op = rows, N, K, experts, op
         self.dtype, code = _out_dtype(out)
-        self._own(lib().gemm_grouped_create_plan(rows, N, K, experts, GROUPED_OPS[op], code))
+        self._own(lib().gemm_grouped_create_plan_ex(rows, N, K, experts, GROUPED_OPS[op], code,
+                                                    GROUPED_TILES[tile]))
 
     def shapes(self):
         """Shapes of (P, Q, out)."""
