@@ -26,22 +26,31 @@ GROUPED_OPS = {"forward": 0, "grad_input": 1, "grad_weight": 2}
 GROUPED_TILES = {"auto": 0, "128x128": 1, "128x256": 2, "256x256": 3}
 
 
+_modules = {}
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported at the first use."""
+    try:
+        return _modules["torch"]
+    except KeyError:
+        import torch
+        _modules["torch"] = torch
+        return torch
 
 
 def _tensor(name, t, shape, dtype, device=None):
     """Raise unless `t` is a contiguous CUDA tensor of this shape and type."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda and \
+            (device is None or t.device == device):
+        return t
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA tensor" % name)
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
-    if device is not None and t.device != device:
-        raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, device))
-    return t
+    raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, device))
 
 
 def _output(name, t, shape, dtype, device):
@@ -57,21 +66,22 @@ def _out_dtype(out):
     return (torch.float16, GEMM_OUT_F16) if out == "f16" else (torch.float32, GEMM_OUT_F32)
 
 
+def _ptr(t):
+    """A tensor's address; None for no tensor and for an empty one."""
+    return t.data_ptr() or None if t is not None else None
+
+
 def _call(fn, device, stream, *args):
     """fn(*args, stream) with `device` current, on `stream` or the device's
-    current stream; tensors become their addresses.  Raises on an error status."""
+    current stream.  Raises on an error status."""
     torch = _torch()
-    args = [a if a is None or type(a) is int else (a.data_ptr() or None) for a in args]
-    if torch.cuda.current_device() != device.index:
+    index = device.index
+    if torch.cuda.current_device() != index:
         with torch.cuda.device(device):
-            return _launch(fn, device, stream, args)
-    return _launch(fn, device, stream, args)
-
-
-def _launch(fn, device, stream, args):
+            return _call(fn, device, stream, *args)
     if stream is None:
         # the handle alone: a Stream object would cost as much as the launch
-        handle = _torch()._C._cuda_getCurrentRawStream(device.index)
+        handle = torch._C._cuda_getCurrentRawStream(index)
     else:
         handle = stream.cuda_stream
     status = fn(*args, handle)
@@ -107,8 +117,8 @@ class ExpertRoute:
             self.offsets = torch.empty(self.experts + 1, dtype=torch.int32, device=dev)
             self.order = torch.empty(self.slots, dtype=torch.int32, device=dev)
             self.position = torch.empty((self.tokens, self.topk), dtype=torch.int32, device=dev)
-        _call(lib().gemm_expert_sort, dev, stream, self.tokens, self.topk, self.experts, ids,
-              self.offsets, self.order, self.position)
+        _call(lib().gemm_expert_sort, dev, stream, self.tokens, self.topk, self.experts, _ptr(ids),
+              _ptr(self.offsets), _ptr(self.order), _ptr(self.position))
         return self
 
     def load(self, offsets, order, position):
@@ -134,7 +144,7 @@ class ExpertRoute:
         _tensor("X", X, (self.tokens, width), torch.float16, dev)
         Xs = _output("out", out, (self.slots, width), torch.float16, dev)
         _call(lib().gemm_expert_gather, dev, stream, self.tokens, self.topk, self.experts, width,
-              X, self.offsets, self.position, Xs)
+              _ptr(X), _ptr(self.offsets), _ptr(self.position), _ptr(Xs))
         return Xs
 
     def combine(self, Ys, out=None, weights=None, stream=None):
@@ -159,8 +169,8 @@ class ExpertRoute:
         dtype = torch.float32 if out is not None and out.dtype == torch.float32 else torch.float16
         Y = _output("out", out, (self.tokens, width), dtype, dev)
         _call(lib().gemm_expert_combine, dev, stream, self.tokens, self.topk, self.experts, width,
-              Ys, offsets, position, weights,
-              GEMM_OUT_F32 if dtype == torch.float32 else GEMM_OUT_F16, Y)
+              _ptr(Ys), _ptr(offsets), _ptr(position), _ptr(weights),
+              GEMM_OUT_F32 if dtype == torch.float32 else GEMM_OUT_F16, _ptr(Y))
         return Y
 
     def gather_grad(self, dXs, out=None, stream=None):
@@ -179,7 +189,8 @@ class ExpertRoute:
         dYs = _output("out", out, (self.slots, width), torch.float16, dev)
         dw = _output("dweights", dweights, (self.tokens, self.topk), torch.float32, dev)
         _call(lib().gemm_expert_combine_grad, dev, stream, self.tokens, self.topk, self.experts,
-              width, dY, Ys, self.offsets, self.position, weights, dYs, dw)
+              width, _ptr(dY), _ptr(Ys), _ptr(self.offsets), _ptr(self.position),
+              _ptr(weights), _ptr(dYs), _ptr(dw))
         return dYs, dw
 
 
@@ -252,7 +263,8 @@ class GroupedPlan(_Handle):
         _tensor("Q", Q, sq, torch.float16, dev)
         _tensor("offsets", offsets, (self.experts + 1,), torch.int32, dev)
         out = _output("out", out, so, self.dtype, dev)
-        _call(lib().gemm_grouped_run, dev, stream, self._h, P, Q, offsets, out)
+        _call(lib().gemm_grouped_run, dev, stream, self._h, _ptr(P), _ptr(Q), _ptr(offsets),
+              _ptr(out))
         return out
 
 
@@ -289,7 +301,8 @@ class W4Plan(_Handle):
                 raise ValueError("ids must hold one expert per row (%d)" % self.M)
             _tensor("ids", ids, ids.shape, torch.int32, dev)
         Y = _output("out", out, (self.M, self.N), self.dtype, dev)
-        _call(lib().gemm_w4_run, dev, stream, self._h, X, packed, scales, zeros, ids, Y)
+        _call(lib().gemm_w4_run, dev, stream, self._h, _ptr(X), _ptr(packed), _ptr(scales),
+              _ptr(zeros), _ptr(ids), _ptr(Y))
         return Y
 
 
