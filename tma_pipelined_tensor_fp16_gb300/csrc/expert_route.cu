@@ -27,6 +27,12 @@ namespace {
 // this warp), all taken in slot order: no result depends on timing.  The CTAs'
 // totals are exchanged through distributed shared memory.
 constexpr int SORT_MAX_EXPERTS = 1024;
+constexpr int SORT_CTAS = 16;         // more than the portable 8
+constexpr int SORT_CTA_SLOTS = 1024;  // slots for which another CTA pays
+// Slots per warp from which equal keys are found bit by bit.  The match
+// instruction answers sooner (128 slots per warp in one CTA: 4.0 against 4.9 us)
+// but few at a time (131072 slots of 128 experts: 13.4 against 10.7 us).
+constexpr int SORT_BALLOT_RUN = 192;
 constexpr int SORT_BATCH = 8;  // ids a lane loads at once
 
 __device__ __forceinline__ uint32_t ld_shared_rank(uint32_t local, uint32_t rank)
@@ -146,7 +152,16 @@ __global__ void __launch_bounds__(1024, 1)
             const bool live = s < end;
             // lanes past the end share a key no slot has
             const int k = live ? key[b] : keys;
-            const unsigned same = __match_any_sync(0xffffffffu, k);
+            unsigned same;
+            if (run < SORT_BALLOT_RUN) {
+                same = __match_any_sync(0xffffffffu, k);
+            } else {
+                same = 0xffffffffu;
+                for (int bit = 0; (keys >> bit) != 0; ++bit) {
+                    const unsigned ones = __ballot_sync(0xffffffffu, (k >> bit) & 1);
+                    same &= ((k >> bit) & 1) ? ones : ~ones;
+                }
+            }
             const unsigned before = same & ((1u << lane) - 1u);
             uint32_t r = 0;
             if (live) r = mine[k] + __popc(before);
@@ -227,10 +242,15 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
     return v;
 }
 
-constexpr int SLOT_BATCH = 8;  // slots whose rows a thread has in flight
-
-template <bool F16OUT>
-__global__ void __launch_bounds__(256)
+// The sum of a token's rows.  Bound by reading Ys once.  BATCH is the number of
+// slots whose rows a thread has in flight at once: registers for slots that a
+// token does not have cost
+// resident warps (32768 tokens x 2 slots of 1024: 84 us with 8, 42 with 4), and
+// with many tokens four in flight and more warps beat eight (8192 tokens x 8 slots
+// of 4096: 110 and 90 us, 6.7 TB/s); with few tokens the second batch is one more
+// wait (3 tokens x 6 slots: 2.4 and 2.5 us).
+template <bool F16OUT, int BATCH>
+__global__ void __launch_bounds__(256, BATCH == 8 ? 3 : 6)
     k_expert_combine(int64_t tokens, int topk, int chunks, RowMap map, const uint4* Ys,
                      const float* weights, void* Y)
 {
@@ -243,12 +263,12 @@ __global__ void __launch_bounds__(256)
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-    for (int j0 = 0; j0 < topk; j0 += SLOT_BATCH) {
-        uint32_t row[SLOT_BATCH];
-        float w[SLOT_BATCH];
-        uint4 v[SLOT_BATCH];
+    for (int j0 = 0; j0 < topk; j0 += BATCH) {
+        uint32_t row[BATCH];
+        float w[BATCH];
+        uint4 v[BATCH];
 #pragma unroll
-        for (int b = 0; b < SLOT_BATCH; ++b) {
+        for (int b = 0; b < BATCH; ++b) {
             row[b] = 0xffffffffu;
             w[b] = 1.0f;
             if (j0 + b < topk) {
@@ -257,10 +277,10 @@ __global__ void __launch_bounds__(256)
             }
         }
 #pragma unroll
-        for (int b = 0; b < SLOT_BATCH; ++b)
+        for (int b = 0; b < BATCH; ++b)
             if (row[b] < kept) v[b] = Ys[static_cast<int64_t>(row[b]) * chunks + c];
 #pragma unroll
-        for (int b = 0; b < SLOT_BATCH; ++b) {
+        for (int b = 0; b < BATCH; ++b) {
             if (row[b] >= kept) continue;  // a dropped slot: its weight and row are not used
             float f[8];
             unpack8(v[b], f);
@@ -281,13 +301,15 @@ __global__ void __launch_bounds__(256)
 // dot products of the token's slots are summed over lanes by shuffles and over
 // warps through shared memory, in a fixed order.  A thread reads a chunk of Ys
 // before it writes the same chunk of dYs and no other thread touches it, so the
-// two may be the same buffer.
-template <int WPT>
-__global__ void __launch_bounds__(256)
+// two may be the same buffer.  BATCH as above (16384 tokens x 4 slots of 4096: 200
+// us with 8, 178 with 4, 6.8 TB/s; 6 slots of 1000: 99 and 81 us; 3 tokens x 6
+// slots: 4.0 and 5.2 us).
+template <int WPT, int BATCH>
+__global__ void __launch_bounds__(256, BATCH == 8 ? 2 : 4)
     k_expert_combine_grad(int64_t tokens, int topk, int chunks, RowMap map, const uint4* dY,
                           const uint4* Ys, const float* weights, uint4* dYs, float* dweights)
 {
-    __shared__ float part[8][SLOT_BATCH];
+    __shared__ float part[8][BATCH];
     griddep_wait();
     griddep_launch_dependents();
     const int warp = static_cast<int>(threadIdx.x) >> 5;
@@ -295,11 +317,11 @@ __global__ void __launch_bounds__(256)
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (8 / WPT) + warp / WPT;
     const bool live = t < tokens;
     const uint32_t kept = kept_rows(map);
-    for (int j0 = 0; j0 < topk; j0 += SLOT_BATCH) {
-        uint32_t row[SLOT_BATCH];
-        float w[SLOT_BATCH], dot[SLOT_BATCH];
+    for (int j0 = 0; j0 < topk; j0 += BATCH) {
+        uint32_t row[BATCH];
+        float w[BATCH], dot[BATCH];
 #pragma unroll
-        for (int b = 0; b < SLOT_BATCH; ++b) {
+        for (int b = 0; b < BATCH; ++b) {
             row[b] = 0xffffffffu;
             w[b] = 0.0f;
             dot[b] = 0.0f;
@@ -312,12 +334,12 @@ __global__ void __launch_bounds__(256)
             for (int c = (warp % WPT) * 32 + static_cast<int>(lane); c < chunks; c += WPT * 32) {
                 float g[8];
                 unpack8(dY[t * chunks + c], g);
-                uint4 v[SLOT_BATCH];
+                uint4 v[BATCH];
 #pragma unroll
-                for (int b = 0; b < SLOT_BATCH; ++b)
+                for (int b = 0; b < BATCH; ++b)
                     if (row[b] < kept) v[b] = Ys[static_cast<int64_t>(row[b]) * chunks + c];
 #pragma unroll
-                for (int b = 0; b < SLOT_BATCH; ++b) {
+                for (int b = 0; b < BATCH; ++b) {
                     if (row[b] >= map.slots) continue;  // past the last slot
                     uint4 out = make_uint4(0, 0, 0, 0);
                     if (row[b] < kept) {
@@ -335,23 +357,23 @@ __global__ void __launch_bounds__(256)
             }
         }
 #pragma unroll
-        for (int b = 0; b < SLOT_BATCH; ++b) {
+        for (int b = 0; b < BATCH; ++b) {
 #pragma unroll
             for (int d = 16; d > 0; d /= 2) dot[b] += __shfl_xor_sync(0xffffffffu, dot[b], d);
         }
         if (WPT == 1) {
             if (lane == 0 && live) {
 #pragma unroll
-                for (int b = 0; b < SLOT_BATCH; ++b)
+                for (int b = 0; b < BATCH; ++b)
                     if (j0 + b < topk) dweights[t * topk + j0 + b] = dot[b];
             }
         } else {
             if (lane == 0) {
 #pragma unroll
-                for (int b = 0; b < SLOT_BATCH; ++b) part[warp][b] = dot[b];
+                for (int b = 0; b < BATCH; ++b) part[warp][b] = dot[b];
             }
             __syncthreads();
-            if (warp % WPT == 0 && lane < SLOT_BATCH && live && j0 + static_cast<int>(lane) < topk) {
+            if (warp % WPT == 0 && lane < BATCH && live && j0 + static_cast<int>(lane) < topk) {
                 float s = 0.0f;
 #pragma unroll
                 for (int u = 0; u < WPT; ++u) s += part[warp + u][lane];
@@ -384,11 +406,27 @@ int check_width(int64_t width)
     return GEMM_OK;
 }
 
+template <int BATCH>
+auto grad_kernel(int wpt)
+{
+    return wpt == 1   ? k_expert_combine_grad<1, BATCH>
+           : wpt == 2 ? k_expert_combine_grad<2, BATCH>
+           : wpt == 4 ? k_expert_combine_grad<4, BATCH>
+                      : k_expert_combine_grad<8, BATCH>;
+}
+
 // Threads over the chunks of a row and, for narrow rows, over several tokens:
 // 256 threads a block, 64 where that leaves fewer blocks than SMs.
 struct RowGrid {
     dim3 grid, block;
 };
+
+// Slots in flight per thread (see k_expert_combine).
+int slot_batch(int topk, bool few)
+{
+    if (topk <= 2) return 2;
+    return topk <= 4 || !few ? 4 : 8;
+}
 
 RowGrid row_grid(int64_t tokens, int chunks, int sms)
 {
@@ -424,15 +462,17 @@ int gemm_expert_sort(int64_t tokens, int topk, int experts, const int32_t* exper
         int dev, sms, smem_optin;
         r = require_device(&dev, &sms, &smem_optin);
         if (r != GEMM_OK) return r;
-        // One CTA up to 4096 slots, then as many as 8 (the portable cluster size).
         int ctas = 1;
-        while (ctas < 8 && slots > static_cast<int64_t>(4096) * ctas) ctas *= 2;
+        while (ctas < SORT_CTAS && slots > static_cast<int64_t>(SORT_CTA_SLOTS) * ctas) ctas *= 2;
         int warps = 32;
         while (warps > 8 && slots <= static_cast<int64_t>(warps) * 32 * ctas) warps /= 2;
         const int64_t per_warp = (slots + ctas * warps - 1) / (ctas * warps);
         const int run = static_cast<int>((per_warp + 31) / 32 * 32);
         const unsigned smem = static_cast<unsigned>(((warps + 2) * (experts + 1) + 33) * 4);
-        cudaError_t e = ensure_smem_limit(k_expert_sort, smem);
+        cudaError_t e = cudaSuccess;
+        if (ctas > 8)
+            e = cudaFuncSetAttribute(k_expert_sort, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess) e = ensure_smem_limit(k_expert_sort, smem);
         if (e == cudaSuccess)
             e = launch_dependent(k_expert_sort, dim3(ctas), dim3(warps * 32), smem, ctas,
                                  static_cast<cudaStream_t>(cuda_stream), static_cast<int>(slots),
@@ -490,10 +530,15 @@ int gemm_expert_combine(int64_t tokens, int topk, int experts, int64_t width, co
         const RowGrid g = row_grid(tokens, chunks, sms);
         if (g.grid.y > 65535u) return fail(GEMM_ERR_UNSUPPORTED, "width is too large");
         const RowMap map = {offsets, position, experts, tokens * topk};
-        cudaError_t e = launch_dependent(
-            dtype_out == GEMM_OUT_F16 ? k_expert_combine<true> : k_expert_combine<false>, g.grid,
-            g.block, 0, 1, static_cast<cudaStream_t>(cuda_stream), tokens, topk, chunks, map,
-            static_cast<const uint4*>(Ys), weights, Y);
+        const bool f16 = dtype_out == GEMM_OUT_F16;
+        const int64_t blocks = static_cast<int64_t>(g.grid.x) * g.grid.y;
+        const int batch = slot_batch(topk, blocks <= 2 * sms);
+        auto kernel = batch == 2   ? (f16 ? k_expert_combine<true, 2> : k_expert_combine<false, 2>)
+                      : batch == 4 ? (f16 ? k_expert_combine<true, 4> : k_expert_combine<false, 4>)
+                                   : (f16 ? k_expert_combine<true, 8> : k_expert_combine<false, 8>);
+        cudaError_t e = launch_dependent(kernel, g.grid, g.block, 0, 1,
+                                         static_cast<cudaStream_t>(cuda_stream), tokens, topk,
+                                         chunks, map, static_cast<const uint4*>(Ys), weights, Y);
         return e == cudaSuccess ? ok() : cuda_fail("expert combine launch", e);
     });
 }
@@ -519,12 +564,10 @@ int gemm_expert_combine_grad(int64_t tokens, int topk, int experts, int64_t widt
         int wpt = 1;
         while (wpt < 8 && chunks > 32 * wpt) wpt *= 2;
         const int64_t blocks = (tokens + 8 / wpt - 1) / (8 / wpt);
-        auto kernel = wpt == 1   ? k_expert_combine_grad<1>
-                      : wpt == 2 ? k_expert_combine_grad<2>
-                      : wpt == 4 ? k_expert_combine_grad<4>
-                                 : k_expert_combine_grad<8>;
+        const int batch = slot_batch(topk, blocks <= 2 * sms);
         cudaError_t e = launch_dependent(
-            kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1,
+            batch == 2 ? grad_kernel<2>(wpt) : batch == 4 ? grad_kernel<4>(wpt) : grad_kernel<8>(wpt),
+            dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1,
             static_cast<cudaStream_t>(cuda_stream), tokens, topk, chunks, map,
             static_cast<const uint4*>(dY), static_cast<const uint4*>(Ys), weights,
             static_cast<uint4*>(dYs), dweights);
