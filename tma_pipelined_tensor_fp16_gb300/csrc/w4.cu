@@ -61,9 +61,10 @@ struct W4Params {
 //
 // Roles of a CTA, joined by mbarriers only:
 //   warps 0..7    workers, two teams of four warps; warp w owns rows
-//                 32 (w % 4) .. + 31 of the tile.  Team h takes the h-th block of
-//                 128 codes of every stage: converts it into one of A_BUFS
-//                 operands and copies the block's part of X beside it.
+//                 32 (w % 4) .. + 31 of the tile.  The teams take alternate
+//                 stages of 256 codes; a team converts a stage's two blocks of
+//                 128 codes one after the other into the next of A_BUFS operands
+//                 each and copies the block's part of X beside it.
 //   warps 12..15  sums (12..19 for 64 rows of X, each half of the columns): read
 //                 the groups' sums from TMEM, scale and add them.
 //                 (With the workers doing this after each block, every block
@@ -95,10 +96,12 @@ constexpr int W4_A_COLS = W4_BLOCK_K / 2;             // TMEM columns of an oper
 constexpr int W4_MAX_STAGES = 8;
 constexpr int W4_MAX_BUFS = 4;
 
-// Barriers of a team's blocks, in turn.  A wait by parity must not meet a later
-// phase of its barrier: a team is never three blocks ahead of its issuer or of
-// the other team (the operand buffers are a ring of both teams' blocks), so four
-// turns are enough.
+// Barriers of a team's blocks, in turn: block `part` of stage n is the team's block
+// m = 2 (n / 2) + part.  A wait by parity must not meet a later phase of its
+// barrier.  Four turns are enough: a team can only start on a stage four later
+// after its issuer has consumed this one (the operand buffers are a ring of all
+// blocks), and that stage's MMAs wait for sums that come, in order, after the
+// other team's stage in between.
 constexpr int W4_TURNS = 4;
 
 // Barrier slots.
@@ -133,9 +136,9 @@ struct W4Layout {
     static constexpr int TMEM_COLS = CTAS == 2 ? 256 : 512;
     static constexpr int A_BUFS = TMEM_COLS - 3 * W4_A_COLS >= 2 * SUM_COLS ? 3 : 2;
     static constexpr int SETS = TMEM_COLS - A_BUFS * W4_A_COLS >= 4 * SUM_COLS ? 4 : 2;
-    // Two issuers where every set always belongs to the same team; else the
-    // first one does all.
-    static constexpr int ISSUERS = SETS % (W4_TEAMS * SETS_PER_BLOCK) == 0 ? 2 : 1;
+    // Two issuers where every set always belongs to the same team's stages; else
+    // the first one does all.
+    static constexpr int ISSUERS = SETS % (W4_TEAMS * 2 * SETS_PER_BLOCK) == 0 ? 2 : 1;
     static constexpr int X_BYTES = NC * W4_BLOCK_K * 2;     // a block's part of X
     static constexpr int W = 0;
     static constexpr int X = W + STAGES * W4_STAGE_BYTES;
@@ -369,7 +372,7 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
         prefetch_tensormap(&tmW);
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(bar(W4_WFULL + i), 2);  // the copy's announcement, the table
-            mbar_init(bar(W4_WEMPTY + i), W4_WORKERS + L::SUMMERS);
+            mbar_init(bar(W4_WEMPTY + i), W4_TEAM_WARPS + L::SUMMERS);
         }
         for (int i = 0; i < W4_TEAMS * W4_TURNS; ++i) {
             mbar_init(bar(W4_AFULL + i), W4_TEAM_WARPS);
@@ -422,47 +425,51 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
                 xnext = static_cast<int64_t>(list[m0 + 8] / p.share - y / p.share) * p.K;
         }
         const bool has_x = 2 * q < count;  // a warp holds rows 2 q, 2 q + 1 and 8, 16, ... on
-        int left = p.K - (s_begin * W4_STAGE_K + team * W4_BLOCK_K);  // codes from this block on
-        x += s_begin * W4_STAGE_K + team * W4_BLOCK_K;
+        int k = (s_begin + team) * W4_STAGE_K;  // first code of the block whose X comes next
         uint4 xv[XPT];
         auto load_x = [&] {  // zeros past K
+            const int left = p.K - k - c0 * 8;
 #pragma unroll
             for (int i = 0; i < XPT; ++i) {
                 xv[i] = make_uint4(0, 0, 0, 0);
-                if (m0 + 8 * i < count && c0 * 8 < left)
-                    xv[i] = *reinterpret_cast<const uint4*>(x + i * xnext);
+                if (m0 + 8 * i >= count) continue;
+                const __half* from = x + i * xnext + k;
+                if (left > 0) xv[i] = *reinterpret_cast<const uint4*>(from);
+                // the team's next stage comes from the L1 cache then
+                if (left > 2 * W4_STAGE_K)
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(from + 2 * W4_STAGE_K));
             }
         };
         if (has_x) load_x();
         const uint32_t sw = static_cast<uint32_t>(row & 7) << 4;
         const uint32_t a_tmem = tmem_base + lanes;
-        // ring positions and their phases
-        int ws = 0, buf = team % A_BUFS, n = 0;
-        uint32_t ws_phase = 0;
-        const uint32_t* words = reinterpret_cast<const uint32_t*>(gen + L::TABLE) +
-                                team * GPB * W4_TILE + row;
+        const uint32_t* words = reinterpret_cast<const uint32_t*>(gen + L::TABLE) + row;
         const uint32_t src0 = base + L::W + row * 128;
-        for (int s = s_begin; s < s_end; ++s) {
-            const bool work = left > 0;  // the last stage may end in the first team's block
-            wd.wait(bar(W4_WFULL + ws), ws_phase, WAIT_FULL, s, 0);
-            if (work) {
+        static_assert(STAGES % W4_TEAMS == 0, "a slot always belongs to the same team");
+        for (int s = s_begin + team; s < s_end; s += W4_TEAMS) {
+            const int n = s - s_begin;
+            const int ws = n % STAGES;
+            wd.wait(bar(W4_WFULL + ws), static_cast<uint32_t>(n / STAGES) & 1u, WAIT_FULL, s, 0);
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                if (s * W4_STAGE_K + part * W4_BLOCK_K >= p.K) break;  // no such block
+                const int b = 2 * n + part, buf = b % A_BUFS;
                 __half2 zero[GPB];
 #pragma unroll
                 for (int i = 0; i < GPB; ++i)
-                    zero[i] = as_half2(
-                        __byte_perm(words[ws * L::TABLE_WORDS + i * W4_TILE], 0u, 0x3232));
+                    zero[i] = as_half2(__byte_perm(
+                        words[ws * L::TABLE_WORDS + (part * GPB + i) * W4_TILE], 0u, 0x3232));
+                if (b >= A_BUFS) {  // the block that had this buffer before
+                    const int n1 = (b - A_BUFS) >> 1, m = 2 * (n1 >> 1) + ((b - A_BUFS) & 1);
+                    wd.wait(bar(W4_DONE + (n1 & 1) * W4_TURNS + m % W4_TURNS),
+                            static_cast<uint32_t>(m / W4_TURNS) & 1u, WAIT_EMPTY, s, b);
+                }
                 const uint32_t src = src0 + ws * W4_STAGE_BYTES;
-                // the block that had this buffer before: A_BUFS blocks ago
-                const int other = A_BUFS % 2 == 1 ? team ^ 1 : team;
-                const int m = A_BUFS % 2 == 1 ? n - (A_BUFS + 1) / 2 + team : n - A_BUFS / 2;
-                if (m >= 0)
-                    wd.wait(bar(W4_DONE + other * W4_TURNS + m % W4_TURNS),
-                            static_cast<uint32_t>(m / W4_TURNS) & 1u, WAIT_EMPTY, s, m);
                 const uint32_t a_block = a_tmem + static_cast<uint32_t>(buf * W4_A_COLS);
 #pragma unroll
                 for (int c = 0; c < W4_BLOCK_K / 32; ++c) {  // 32 codes at a time
                     const uint4 w =
-                        ld_shared_v4(src + ((static_cast<uint32_t>(team * 64 + c * 16)) ^ sw));
+                        ld_shared_v4(src + ((static_cast<uint32_t>(part * 64 + c * 16)) ^ sw));
                     const __half2 z = zero[c * 32 / GROUP];
                     const __half2 z64 = __hadd2(z, as_half2(0x63806380u));
                     uint32_t e[8];
@@ -484,24 +491,18 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
                 }
                 tmem_wait_st();
                 tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    const int m = 2 * (n >> 1) + part;
+                    mbar_arrive(bar(W4_AFULL + team * W4_TURNS + m % W4_TURNS));
+                }
+                if (has_x) {  // the stage's second block, then the team's next stage
+                    k += part == 0 ? W4_BLOCK_K : W4_TEAMS * W4_STAGE_K - W4_BLOCK_K;
+                    load_x();
+                }
             }
             __syncwarp();
-            if (lane == 0) {
-                if (work) mbar_arrive(bar(W4_AFULL + team * W4_TURNS + n % W4_TURNS));
-                mbar_arrive(bar(W4_WEMPTY + ws));
-            }
-            left -= W4_STAGE_K;
-            if (has_x) {
-                x += W4_STAGE_K;
-                load_x();
-            }
-            if (++ws == STAGES) {
-                ws = 0;
-                ws_phase ^= 1u;
-            }
-            ++n;
-            buf += W4_TEAMS;
-            if (buf >= A_BUFS) buf -= A_BUFS;
+            if (lane == 0) mbar_arrive(bar(W4_WEMPTY + ws));
         }
     } else if (warp >= FIRST_SUMMER) {
         // ----------------------------------------------------------- sums
@@ -621,11 +622,11 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
         const int end = s_end * W4_STAGE_K < p.K ? s_end * W4_STAGE_K : p.K;
         int k0 = s_begin * W4_STAGE_K;
         for (int b = 0; k0 < end; ++b, k0 += W4_BLOCK_K) {
-            const int team = b & 1, n = b >> 1;
+            const int n = b >> 1, team = n & 1, m = 2 * (n >> 1) + (b & 1);
             if (L::ISSUERS == 2 ? team != issuer : issuer != 0) continue;
             const int buf = b % A_BUFS;
-            bool ok = wd.wait(bar(W4_AFULL + team * W4_TURNS + n % W4_TURNS),
-                              static_cast<uint32_t>(n / W4_TURNS) & 1u, WAIT_FULL, k0, 1);
+            bool ok = wd.wait(bar(W4_AFULL + team * W4_TURNS + m % W4_TURNS),
+                              static_cast<uint32_t>(m / W4_TURNS) & 1u, WAIT_FULL, k0, 1);
             const uint32_t a_tmem = tmem_base + static_cast<uint32_t>(buf * W4_A_COLS);
             const uint64_t bdesc = sw128_kmajor_desc(base + L::X + buf * L::X_BYTES);
 #pragma unroll
@@ -649,7 +650,7 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
                 mma_commit_elected(elected, bar(W4_GFULL + set));
             }
             if (!__all_sync(0xffffffffu, ok)) break;
-            mma_commit_elected(elected, bar(W4_DONE + team * W4_TURNS + n % W4_TURNS));
+            mma_commit_elected(elected, bar(W4_DONE + team * W4_TURNS + m % W4_TURNS));
         }
         mma_commit_elected(elected, bar(W4_DRAIN + issuer));  // by the lane that issued
         wd.drain(bar(W4_DRAIN + issuer), 0);
