@@ -736,40 +736,103 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Clusters along z: the CTAs that share the rows' length.
-template <int NC, int GROUP>
-cudaError_t launch_w4(const CUtensorMap& map, const W4Params& p, dim3 grid, cudaStream_t stream)
-{
-    constexpr unsigned smem = W4Layout<NC, GROUP>::TOTAL;
-    cudaError_t e = ensure_smem_limit(k_w4<NC, GROUP>, smem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(W4Layout<NC, GROUP>::THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 1;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = grid.z;
-    cfg.attrs = attr;
-    cfg.numAttrs = grid.z > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k_w4<NC, GROUP>, map, p);
-}
+// One instantiation of the few-row kernel.
+struct W4Kernel {
+    void (*fn)(CUtensorMap, W4Params);
+    unsigned smem;
+    int threads;
+};
 
 template <int GROUP>
-cudaError_t launch_group(const CUtensorMap& map, const W4Params& p, int cols, dim3 grid,
-                         cudaStream_t stream)
+W4Kernel kernel_of_group(int cols)
 {
     switch (cols) {
-    case 16: return launch_w4<16, GROUP>(map, p, grid, stream);
-    case 32: return launch_w4<32, GROUP>(map, p, grid, stream);
-    case 64: return launch_w4<64, GROUP>(map, p, grid, stream);
-    default: return cudaErrorInvalidValue;
+    case 16: return {k_w4<16, GROUP>, W4Layout<16, GROUP>::TOTAL, W4Layout<16, GROUP>::THREADS};
+    case 32: return {k_w4<32, GROUP>, W4Layout<32, GROUP>::TOTAL, W4Layout<32, GROUP>::THREADS};
+    default: return {k_w4<64, GROUP>, W4Layout<64, GROUP>::TOTAL, W4Layout<64, GROUP>::THREADS};
     }
+}
+
+W4Kernel kernel_of(int cols, int group)
+{
+    return group == 32   ? kernel_of_group<32>(cols)
+           : group == 64 ? kernel_of_group<64>(cols)
+                         : kernel_of_group<128>(cols);
+}
+
+// Clusters along z: the CTAs that share the rows' length.
+struct W4Launch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+
+    W4Launch(const W4Kernel& k, dim3 grid, cudaStream_t stream)
+    {
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(static_cast<unsigned>(k.threads));
+        cfg.dynamicSmemBytes = k.smem;
+        cfg.stream = stream;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 1;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = grid.z;
+        cfg.attrs = attr;
+        cfg.numAttrs = grid.z > 1 ? 2 : 1;
+    }
+};
+
+// Rows per tile and CTAs per cluster of the few-row kernel.  A stage of 256 codes
+// takes a CTA the same time whatever its rows (the kernel is bound by the
+// instructions and waits of its warps), a launch about 5 us more: so the length is
+// shared by as many CTAs as are resident at once, and the tiles are as low as
+// spread the rows evenly over those.  Measured per stage, one CTA per SM: 0.6, 0.9
+// and 1.2 us with groups of 128, 64 and 32 and up to 16 rows of X, 1.0 with 32 rows,
+// 1.4 with 64; two CTAs per SM (up to 16 rows) take 1.7 times as long, each.  How
+// many clusters are resident with one CTA per SM is asked of the runtime: clusters
+// of four and eight leave SMs of a GPC idle.  One row, 4096 x 14336: 13.7 us on 4 x
+// 35 CTAs, 18.9 on 8 x 37, of which not all are resident; 16384 x 16384: 39 us on 2
+// x 147, two per SM, 71 on 1 x 293.
+cudaError_t choose_w4_tile(int64_t N, int64_t K, int64_t matrices, int cols, int group, int sms,
+                           int* tile_rows, int* length_ctas)
+{
+    const W4Kernel k = kernel_of(cols, group);
+    cudaError_t e = ensure_smem_limit(k.fn, k.smem);
+    if (e != cudaSuccess) return e;
+    const int64_t stages = (K + W4_STAGE_K - 1) / W4_STAGE_K;
+    const double one = cols == 64     ? 1.4
+                       : cols == 32   ? 1.0
+                       : group == 32  ? 1.2
+                       : group == 64  ? 0.9
+                                      : 0.6;
+    double best = -1.0;
+    for (int ctas = 1; ctas <= 8 && (ctas == 1 || ctas * 2 <= stages); ctas *= 2) {
+        int resident = sms;
+        if (ctas > 1) {
+            W4Launch launch(k, dim3(1, 1, static_cast<unsigned>(ctas)), nullptr);
+            e = cudaOccupancyMaxActiveClusters(&resident, k.fn, &launch.cfg);
+            if (e != cudaSuccess) return e;
+            resident = std::min(resident, sms / ctas);
+            if (resident < 1) continue;
+        }
+        for (int per_sm = 1; per_sm <= w4_ctas(cols); ++per_sm) {
+            const int64_t clusters = static_cast<int64_t>(resident) * per_sm;
+            const int64_t per_matrix = std::max<int64_t>(1, clusters / matrices);
+            const int64_t rows =
+                std::min<int64_t>(W4_TILE, ((N + per_matrix - 1) / per_matrix + 7) / 8 * 8);
+            const int64_t tiles = (N + rows - 1) / rows * matrices;
+            const int64_t waves = (tiles + clusters - 1) / clusters;
+            const double time =
+                3.6 + waves * (1.4 + one * (per_sm == 2 ? 1.7 : 1.0) *
+                                         static_cast<double>((stages + ctas - 1) / ctas));
+            if (best < 0.0 || time < best) {
+                best = time;
+                *tile_rows = static_cast<int>(rows);
+                *length_ctas = ctas;
+            }
+        }
+    }
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -860,28 +923,17 @@ gemm_w4_plan* gemm_w4_create_plan(int64_t M, int64_t N, int64_t K, int group, in
         if (experts > 0 || M <= W4_MAX_ROWS) {
             p.cols = 16;
             while (experts == 0 && p.cols < M) p.cols *= 2;
-            // Few tiles of 128 rows: the CTAs of a cluster share the rows' length
-            // (at least two stages of 256 codes each), then tiles of fewer rows
-            // fill the last SMs.
-            const int64_t slots = w4_ctas(p.cols) * p.sms;
-            const int64_t matrices = experts > 0 ? std::min<int64_t>(M, experts) : 1;
-            const int64_t full = (N + W4_TILE - 1) / W4_TILE * matrices;
-            p.length_ctas = 1;
-            while (p.length_ctas < 8 && full * p.length_ctas * 2 <= slots &&
-                   K >= static_cast<int64_t>(W4_STAGE_K) * p.length_ctas * 4)
-                p.length_ctas *= 2;
-            p.tile_rows = W4_TILE;
-            const int64_t per_matrix = slots / (p.length_ctas * matrices);
-            if (per_matrix > 0 && N <= per_matrix * W4_TILE)
-                p.tile_rows =
-                    static_cast<int>(((N + per_matrix - 1) / per_matrix + 7) / 8 * 8);
+            cudaError_t e =
+                choose_w4_tile(N, K, experts > 0 ? std::min<int64_t>(M, experts) : 1, p.cols, group,
+                               p.sms, &p.tile_rows, &p.length_ctas);
+            if (e != cudaSuccess) return cuda_fail("choosing the tile", e);
             std::snprintf(p.desc, sizeof(p.desc),
                           "w4 rows M=%lld N=%lld K=%lld group=%d experts=%d tile=%dx%d "
                           "length_ctas=%d out=%s",
                           static_cast<long long>(M), static_cast<long long>(N),
                           static_cast<long long>(K), group, experts, p.tile_rows, p.cols, p.length_ctas,
                           elt == 2 ? "f16" : "f32");
-            cudaError_t e = cudaMalloc(&p.d_status, sizeof(DevStatus));
+            e = cudaMalloc(&p.d_status, sizeof(DevStatus));
             if (e == cudaSuccess) e = cudaMemset(p.d_status, 0, sizeof(DevStatus));
             if (e != cudaSuccess) {
                 if (p.d_status) cudaFree(p.d_status);
@@ -967,9 +1019,9 @@ int gemm_w4_run(gemm_w4_plan* plan, const void* X, const void* packed, const voi
         const dim3 grid(static_cast<unsigned>((plan->N + plan->tile_rows - 1) / plan->tile_rows),
                         plan->experts > 0 ? static_cast<unsigned>(plan->M) : 1u,
                         static_cast<unsigned>(plan->length_ctas));
-        e = plan->group == 32   ? launch_group<32>(map, p, plan->cols, grid, stream)
-            : plan->group == 64 ? launch_group<64>(map, p, plan->cols, grid, stream)
-                                : launch_group<128>(map, p, plan->cols, grid, stream);
+        const W4Kernel k = kernel_of(plan->cols, plan->group);
+        W4Launch launch(k, grid, stream);
+        e = cudaLaunchKernelEx(&launch.cfg, k.fn, map, p);
         return e == cudaSuccess ? ok() : cuda_fail("w4 product launch", e);
     });
 }
