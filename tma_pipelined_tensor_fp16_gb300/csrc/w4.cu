@@ -98,11 +98,13 @@ constexpr int W4_MAX_BUFS = 4;
 
 // Barriers of a team's blocks, in turn: block `part` of stage n is the team's block
 // m = 2 (n / 2) + part.  A wait by parity must not meet a later phase of its
-// barrier.  Four turns are enough: a team can only start on a stage four later
-// after its issuer has consumed this one (the operand buffers are a ring of all
-// blocks), and that stage's MMAs wait for sums that come, in order, after the
-// other team's stage in between.
+// barrier.  Four turns are enough.  The turn of block b comes back with block
+// b + 8.  A team writes that one after its issuer has consumed b (the operand
+// buffers are a ring of all blocks).  Its MMAs wait for the sums of a block at most
+// W4_SET_BLOCKS before it, which come, in order, after those of b + 3, the last one
+// whose worker waits for b to be done.
 constexpr int W4_TURNS = 4;
+constexpr int W4_SET_BLOCKS = 4;  // blocks that all sets of accumulators hold
 
 // Barrier slots.
 enum : int {
@@ -129,16 +131,21 @@ struct W4Layout {
     static constexpr int SUMMERS = NC == 64 ? 8 : 4;        // warps that add up
     static constexpr int COLS = NC * 4 / SUMMERS;           // columns each of them has
     static constexpr int THREADS = (12 + SUMMERS) * 32;
-    // a set of accumulators: the groups that one commit completes
-    static constexpr int SET_GROUPS = GPB * NC > 128 ? 128 / NC : GPB;
-    static constexpr int SETS_PER_BLOCK = GPB / SET_GROUPS;
+    // A set of accumulators, the groups that one commit completes: both groups of a
+    // stage with groups of 128 (half as many waits for the sums), else a block's,
+    // or half a block's where those would fill TMEM.
+    static constexpr bool STAGE_SETS = GPB == 1;
+    static constexpr int SET_GROUPS = STAGE_SETS ? GPS : GPB * NC > 128 ? 128 / NC : GPB;
+    static constexpr int SETS_PER_BLOCK = STAGE_SETS ? 1 : GPB / SET_GROUPS;
     static constexpr int SUM_COLS = SET_GROUPS * NC;        // TMEM columns of a set
     static constexpr int TMEM_COLS = CTAS == 2 ? 256 : 512;
     static constexpr int A_BUFS = TMEM_COLS - 3 * W4_A_COLS >= 2 * SUM_COLS ? 3 : 2;
-    static constexpr int SETS = TMEM_COLS - A_BUFS * W4_A_COLS >= 4 * SUM_COLS ? 4 : 2;
+    static constexpr int SETS =
+        !STAGE_SETS && TMEM_COLS - A_BUFS * W4_A_COLS >= 4 * SUM_COLS ? 4 : 2;
     // Two issuers where every set always belongs to the same team's stages; else
     // the first one does all.
-    static constexpr int ISSUERS = SETS % (W4_TEAMS * 2 * SETS_PER_BLOCK) == 0 ? 2 : 1;
+    static constexpr int ISSUERS =
+        SETS % (W4_TEAMS * (STAGE_SETS ? 1 : 2 * SETS_PER_BLOCK)) == 0 ? 2 : 1;
     static constexpr int X_BYTES = NC * W4_BLOCK_K * 2;     // a block's part of X
     static constexpr int W = 0;
     static constexpr int X = W + STAGES * W4_STAGE_BYTES;
@@ -149,6 +156,8 @@ struct W4Layout {
     static constexpr int LIST = BARS + (W4_BARRIERS + 1) * 8;  // rows of Y by expert
     static constexpr int TOTAL = LIST + 64 + 1024;
     static_assert(A_BUFS * W4_A_COLS + SETS * SUM_COLS <= TMEM_COLS, "TMEM columns");
+    static_assert(SETS * (STAGE_SETS ? 2 : 1) <= W4_SET_BLOCKS * SETS_PER_BLOCK && A_BUFS <= 3,
+                  "a wait by parity could meet a later phase");
     static_assert(NC * W4_TILE * 4 <= X, "the sums fit the code ring");
     // 228 KB an SM, 1 KB of it taken by the system per CTA
     static_assert(TOTAL <= (CTAS == 2 ? 113 : 227) * 1024, "shared memory");
@@ -528,6 +537,8 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
                     sum_tmem + lanes + static_cast<uint32_t>(set * L::SUM_COLS + col0);
 #pragma unroll
                 for (int g = 0; g < L::SET_GROUPS; ++g) {
+                    // the last stage may end before the set's second group
+                    if (L::STAGE_SETS && g > 0 && left <= W4_BLOCK_K) break;
                     uint32_t v[COLS];
                     if constexpr (COLS == 16)
                         tmem_load_16cols(from + g * NC, v);
@@ -631,12 +642,16 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
             const uint64_t bdesc = sw128_kmajor_desc(base + L::X + buf * L::X_BYTES);
 #pragma unroll
             for (int h = 0; h < L::SETS_PER_BLOCK; ++h) {
-                constexpr int SET_K = L::SET_GROUPS * GROUP;  // codes of a set
-                const int u = b * L::SETS_PER_BLOCK + h, set = u % SETS;
-                ok = wd.wait(bar(W4_GEMPTY + set), (static_cast<uint32_t>(u / SETS) & 1u) ^ 1u,
-                             WAIT_TMEM_EMPTY, k0, h);
+                // codes of the block that go to this set, and the set's first column
+                constexpr int SET_K = L::STAGE_SETS ? W4_BLOCK_K : L::SET_GROUPS * GROUP;
+                const int u = L::STAGE_SETS ? n : b * L::SETS_PER_BLOCK + h, set = u % SETS;
+                if (!L::STAGE_SETS || (b & 1) == 0)
+                    ok = wd.wait(bar(W4_GEMPTY + set), (static_cast<uint32_t>(u / SETS) & 1u) ^ 1u,
+                                 WAIT_TMEM_EMPTY, k0, h);
                 if (!__all_sync(0xffffffffu, ok)) break;  // an abandoned run
-                const uint32_t d_tmem = sum_tmem + static_cast<uint32_t>(set * L::SUM_COLS);
+                const uint32_t d_tmem =
+                    sum_tmem + static_cast<uint32_t>(set * L::SUM_COLS +
+                                                     (L::STAGE_SETS ? (b & 1) * NC : 0));
                 tc_fence_after_sync();
 #pragma unroll
                 for (int i = 0; i < SET_K; i += MMA_K) {
@@ -647,7 +662,8 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
                                            ((k / 64) * NC * 128 + (k % 64) * 2) >> 4),
                                idesc, k % GROUP == 0 ? 0u : 1u);
                 }
-                mma_commit_elected(elected, bar(W4_GFULL + set));
+                if (!L::STAGE_SETS || (b & 1) == 1 || k0 + W4_BLOCK_K >= end)
+                    mma_commit_elected(elected, bar(W4_GFULL + set));
             }
             if (!__all_sync(0xffffffffu, ok)) break;
             mma_commit_elected(elected, bar(W4_DONE + team * W4_TURNS + m % W4_TURNS));
