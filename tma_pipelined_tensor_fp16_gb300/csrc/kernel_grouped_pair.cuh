@@ -5,10 +5,15 @@
 // hold two K blocks of 64 (three stages of 64 KB a CTA), as the dense pair kernel's.
 //
 // Why pairs: a tile of 256 columns leaves a single CTA room for four stages of 64,
-// and every operand byte from L2 feeds half as many MMAs (measured at 16 experts
-// of 4096 x 4096 with 1024 rows each: 1497 against the pairs' rate beside the rule
-// in grouped.cu).  A tile of 256 rows wastes more of an expert's last tile, so few
-// rows per expert stay with single CTAs.
+// and every operand byte from L2 feeds half as many MMAs (16 experts of 4096 x 4096
+// with 1024 rows each: 1545 TFLOP/s on single CTAs, 1742 on pairs; one expert of
+// 8192 x 8192 with 8192 rows: 1582 and 1842).  A tile of 256 rows wastes more of an
+// expert's last tile, so few rows per expert stay with single CTAs (the rule and its
+// figures are in grouped.cu).
+//
+// Measured: 16384 uneven rows, 16 experts of 4096 x 4096, 360 us, 1527 TFLOP/s, the
+// tensor pipe busy 81 % of the time; the rest is the last tiles of experts, part of
+// whose rows are the next expert's, and the last wave.
 //
 // The leader's producer takes tiles from the counter and hands them to both CTAs.
 // Contraction rows past an expert's last one (GRAD_WEIGHT) have to be zeroed in

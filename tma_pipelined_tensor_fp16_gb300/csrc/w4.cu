@@ -59,20 +59,32 @@ struct W4Params {
 // a worker thread converts 128 codes of its row in registers and stores them
 // with tcgen05.st, and shared memory is left to the codes in flight.
 //
+// Bound on paper by reading the codes, in fact by the instructions of the warps that
+// convert and add up (about 3200 a stage and CTA, half of them the conversion and its
+// stores to TMEM; issue slots 65 % used, DRAM 41 %).  One row of 16384 x 16384, groups
+// of 128: 38.8 us, 3.6 TB/s; 32 slots of 64 experts of 2048 x 4096: 32.7 us; 64 rows
+// of 8192 x 4096, groups of 32: 18.1 us.  Without the conversion one row takes 26
+// us, without the sums 34.
+//
 // Roles of a CTA, joined by mbarriers only:
 //   warps 0..7    workers, two teams of four warps; warp w owns rows
 //                 32 (w % 4) .. + 31 of the tile.  The teams take alternate
 //                 stages of 256 codes; a team converts a stage's two blocks of
 //                 128 codes one after the other into the next of A_BUFS operands
-//                 each and copies the block's part of X beside it.
+//                 each and, up to 16 rows, copies the block's part of X to shared
+//                 memory.
 //   warps 12..15  sums (12..19 for 64 rows of X, each half of the columns): read
 //                 the groups' sums from TMEM, scale and add them.
 //                 (With the workers doing this after each block, every block
 //                 paid the round trip to the tensor core, about 1500 cycles:
 //                 54 us for one row of 16384 x 16384.)
 //   warps 8, 9    take alternate stages of 256 codes: start the TMA copy of the
-//                 codes, 128 bytes a row, and bring the stage's scales and zero
-//                 points from global memory into a table in shared memory.
+//                 codes, 128 bytes a row, and for more than 16 rows of X's
+//                 part, and bring the stage's scales and zero points from global
+//                 memory into a table in shared memory.  (64 rows of 8192 x 8192,
+//                 groups of 128: 19.4 us, and 26.1 with X by the workers; 32 rows
+//                 17.0 and 18.9.  Up to 16 rows X is little work, and the cheaper
+//                 conversion that its reordering allows counts for more.)
 //   warps 10, 11  MMA issuers, one per team (a block's eight MMAs and the waits
 //                 around them take one warp about as long as a team takes to
 //                 convert it); warp 11 allocates TMEM.
@@ -125,20 +137,23 @@ __host__ __device__ constexpr int w4_ctas(int cols) { return cols == 16 ? 2 : 1;
 template <int NC, int GROUP>
 struct W4Layout {
     static constexpr int CTAS = w4_ctas(NC);
-    static constexpr int STAGES = CTAS == 2 ? 4 : 8;
+    // X comes by TMA with the codes, in its own order; up to 16 rows the workers
+    // bring it, in the codes' order (see decode8)
+    static constexpr bool X_TMA = NC > 16;
+    static constexpr int STAGES = NC == 32 ? 6 : 4;
     static constexpr int GPS = W4_STAGE_K / GROUP;          // groups per stage and row
     static constexpr int GPB = W4_BLOCK_K / GROUP;          // groups per block
     static constexpr int SUMMERS = NC == 64 ? 8 : 4;        // warps that add up
     static constexpr int COLS = NC * 4 / SUMMERS;           // columns each of them has
     static constexpr int THREADS = (12 + SUMMERS) * 32;
-    // A set of accumulators, the groups that one commit completes: both groups of a
-    // stage with groups of 128 (half as many waits for the sums), else a block's,
-    // or half a block's where those would fill TMEM.
-    static constexpr bool STAGE_SETS = GPB == 1;
+    // A set of accumulators, the groups that one commit completes: all of a stage
+    // where two such sets fit TMEM (fewer waits: half of them with groups of 128),
+    // else a block's, or half a block's.
+    static constexpr int TMEM_COLS = CTAS == 2 ? 256 : 512;
+    static constexpr bool STAGE_SETS = 2 * GPS * NC + 2 * W4_A_COLS <= TMEM_COLS;
     static constexpr int SET_GROUPS = STAGE_SETS ? GPS : GPB * NC > 128 ? 128 / NC : GPB;
     static constexpr int SETS_PER_BLOCK = STAGE_SETS ? 1 : GPB / SET_GROUPS;
     static constexpr int SUM_COLS = SET_GROUPS * NC;        // TMEM columns of a set
-    static constexpr int TMEM_COLS = CTAS == 2 ? 256 : 512;
     static constexpr int A_BUFS = TMEM_COLS - 3 * W4_A_COLS >= 2 * SUM_COLS ? 3 : 2;
     static constexpr int SETS =
         !STAGE_SETS && TMEM_COLS - A_BUFS * W4_A_COLS >= 4 * SUM_COLS ? 4 : 2;
@@ -147,10 +162,11 @@ struct W4Layout {
     static constexpr int ISSUERS =
         SETS % (W4_TEAMS * (STAGE_SETS ? 1 : 2 * SETS_PER_BLOCK)) == 0 ? 2 : 1;
     static constexpr int X_BYTES = NC * W4_BLOCK_K * 2;     // a block's part of X
+    static constexpr int STAGE = W4_STAGE_BYTES + (X_TMA ? 2 * X_BYTES : 0);
     static constexpr int W = 0;
-    static constexpr int X = W + STAGES * W4_STAGE_BYTES;
+    static constexpr int X = X_TMA ? W + W4_STAGE_BYTES : W + STAGES * STAGE;
     // [stage][group][row]: the scale's bits, and -(1024 + zero) in fp16 above
-    static constexpr int TABLE = X + A_BUFS * X_BYTES;
+    static constexpr int TABLE = W + STAGES * STAGE + (X_TMA ? 0 : A_BUFS * X_BYTES);
     static constexpr int TABLE_WORDS = GPS * W4_TILE;
     static constexpr int BARS = TABLE + STAGES * TABLE_WORDS * 4;
     static constexpr int LIST = BARS + (W4_BARRIERS + 1) * 8;  // rows of Y by expert
@@ -158,7 +174,7 @@ struct W4Layout {
     static_assert(A_BUFS * W4_A_COLS + SETS * SUM_COLS <= TMEM_COLS, "TMEM columns");
     static_assert(SETS * (STAGE_SETS ? 2 : 1) <= W4_SET_BLOCKS * SETS_PER_BLOCK && A_BUFS <= 3,
                   "a wait by parity could meet a later phase");
-    static_assert(NC * W4_TILE * 4 <= X, "the sums fit the code ring");
+    static_assert(NC * W4_TILE * 4 <= STAGES * STAGE, "the sums fit the code ring");
     // 228 KB an SM, 1 KB of it taken by the system per CTA
     static_assert(TOTAL <= (CTAS == 2 ? 113 : 227) * 1024, "shared memory");
 };
@@ -187,7 +203,20 @@ __device__ __forceinline__ void decode8(uint32_t w, __half2 z, __half2 z64, uint
     e[3] = as_u32(__hfma2(as_half2(code_pair(v, 0x00f000f0u)), sixteenth, z64));
 }
 
-// X[k..k+7] in the same order.
+// The same in the codes' own order: (k, k + 1) and so on, from one byte each, with
+// 1024 + q in the lower and 1024 + 16 q in the upper half.  `z` is -(1024 + zero)
+// below and -(64 + zero) above.  Three instructions a pair against two and a quarter.
+__device__ __forceinline__ void decode8_in_order(uint32_t w, __half2 z, uint32_t* e)
+{
+    const __half2 unit = as_half2(0x2c003c00u);  // 1, 1/16
+    const uint32_t sel[4] = {0x4040u, 0x4141u, 0x4242u, 0x4343u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        e[i] = as_u32(
+            __hfma2(as_half2(__byte_perm(w, 0x64646464u, sel[i]) & 0x64f0640fu), unit, z));
+}
+
+// X[k..k+7] in the order of decode8.
 __device__ __forceinline__ uint4 order_x(const uint4& v)
 {
     return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
@@ -319,7 +348,8 @@ struct W4Wait : Watchdog {
 
 template <int NC, int GROUP>
 __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GROUP>::CTAS)
-    k_w4(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ W4Params p)
+    k_w4(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+         const __grid_constant__ W4Params p)
 {
     using L = W4Layout<NC, GROUP>;
     constexpr int STAGES = L::STAGES, A_BUFS = L::A_BUFS, SETS = L::SETS;
@@ -379,9 +409,11 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
 
     if (warp == 8 && lane == 0) {
         prefetch_tensormap(&tmW);
+        if (L::X_TMA) prefetch_tensormap(&tmX);
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(bar(W4_WFULL + i), 2);  // the copy's announcement, the table
-            mbar_init(bar(W4_WEMPTY + i), W4_TEAM_WARPS + L::SUMMERS);
+            mbar_init(bar(W4_WFULL + i), 2);  // the copies' announcement, the table
+            // workers, sums and, where they read X there, the MMAs
+            mbar_init(bar(W4_WEMPTY + i), W4_TEAM_WARPS + L::SUMMERS + (L::X_TMA ? 1 : 0));
         }
         for (int i = 0; i < W4_TEAMS * W4_TURNS; ++i) {
             mbar_init(bar(W4_AFULL + i), W4_TEAM_WARPS);
@@ -427,13 +459,14 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
         static_assert(XPT * 8 == NC, "rows of a thread");
         const __half* x = p.X;
         int64_t xnext = static_cast<int64_t>(p.K) * 8;
-        if (m0 < count) {
+        if (!L::X_TMA && m0 < count) {
             const int y = p.experts > 0 ? list[m0] : m0;
             x = p.X + static_cast<int64_t>(y / p.share) * p.K + c0 * 8;
             if (p.experts > 0 && m0 + 8 < count)
                 xnext = static_cast<int64_t>(list[m0 + 8] / p.share - y / p.share) * p.K;
         }
-        const bool has_x = 2 * q < count;  // a warp holds rows 2 q, 2 q + 1 and 8, 16, ... on
+        // a warp holds rows 2 q, 2 q + 1 and 8, 16, ... on
+        const bool has_x = !L::X_TMA && 2 * q < count;
         int k = (s_begin + team) * W4_STAGE_K;  // first code of the block whose X comes next
         uint4 xv[XPT];
         auto load_x = [&] {  // zeros past K
@@ -473,20 +506,29 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
                     wd.wait(bar(W4_DONE + (n1 & 1) * W4_TURNS + m % W4_TURNS),
                             static_cast<uint32_t>(m / W4_TURNS) & 1u, WAIT_EMPTY, s, b);
                 }
-                const uint32_t src = src0 + ws * W4_STAGE_BYTES;
+                const uint32_t src = src0 + ws * L::STAGE;
                 const uint32_t a_block = a_tmem + static_cast<uint32_t>(buf * W4_A_COLS);
 #pragma unroll
                 for (int c = 0; c < W4_BLOCK_K / 32; ++c) {  // 32 codes at a time
                     const uint4 w =
                         ld_shared_v4(src + ((static_cast<uint32_t>(part * 64 + c * 16)) ^ sw));
                     const __half2 z = zero[c * 32 / GROUP];
-                    const __half2 z64 = __hadd2(z, as_half2(0x63806380u));
                     uint32_t e[8];
-                    decode8(w.x, z, z64, e);
-                    decode8(w.y, z, z64, e + 4);
-                    tmem_store_8cols(a_block + c * 16, e);
-                    decode8(w.z, z, z64, e);
-                    decode8(w.w, z, z64, e + 4);
+                    if constexpr (L::X_TMA) {
+                        const __half2 zz = __hadd2(z, as_half2(0x63800000u));  // 0, 960
+                        decode8_in_order(w.x, zz, e);
+                        decode8_in_order(w.y, zz, e + 4);
+                        tmem_store_8cols(a_block + c * 16, e);
+                        decode8_in_order(w.z, zz, e);
+                        decode8_in_order(w.w, zz, e + 4);
+                    } else {
+                        const __half2 z64 = __hadd2(z, as_half2(0x63806380u));
+                        decode8(w.x, z, z64, e);
+                        decode8(w.y, z, z64, e + 4);
+                        tmem_store_8cols(a_block + c * 16, e);
+                        decode8(w.z, z, z64, e);
+                        decode8(w.w, z, z64, e + 4);
+                    }
                     tmem_store_8cols(a_block + c * 16 + 8, e);
                 }
                 if (has_x) {
@@ -521,14 +563,12 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
         int left = p.K - s_begin * W4_STAGE_K;
         for (int s = s_begin; s < s_end; ++s) {
             wd.wait(bar(W4_WFULL + ws), ws_phase, WAIT_FULL, s, 4);
-            float scale[GPS];
-#pragma unroll
-            for (int i = 0; i < GPS; ++i)
-                scale[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(
+            // read when needed: a stage's eight scales beside the sums spill
+            auto scale_of = [&](int i) {
+                return __half2float(__ushort_as_half(static_cast<unsigned short>(
                     words[ws * L::TABLE_WORDS + i * W4_TILE] & 0xffffu)));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(W4_WEMPTY + ws));
-#pragma unroll
+            };
+#pragma unroll 1
             for (int g0 = 0; g0 < GPS; g0 += L::SET_GROUPS) {
                 if (g0 * GROUP / W4_BLOCK_K * W4_BLOCK_K >= left) break;  // no such block
                 wd.wait(bar(W4_GFULL + set), set_phase, WAIT_TMEM_FULL, s, g0);
@@ -537,8 +577,9 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
                     sum_tmem + lanes + static_cast<uint32_t>(set * L::SUM_COLS + col0);
 #pragma unroll
                 for (int g = 0; g < L::SET_GROUPS; ++g) {
-                    // the last stage may end before the set's second group
-                    if (L::STAGE_SETS && g > 0 && left <= W4_BLOCK_K) break;
+                    // the last stage may have one block only
+                    if (L::STAGE_SETS && g >= GPB && left <= W4_BLOCK_K) break;
+                    const float sg = scale_of(g0 + g);
                     uint32_t v[COLS];
                     if constexpr (COLS == 16)
                         tmem_load_16cols(from + g * NC, v);
@@ -546,7 +587,7 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
                         tmem_load_32cols(from + g * NC, v);
 #pragma unroll
                     for (int j = 0; j < COLS; ++j)
-                        acc[j] = fmaf(scale[g0 + g], __uint_as_float(v[j]), acc[j]);
+                        acc[j] = fmaf(sg, __uint_as_float(v[j]), acc[j]);
                 }
                 tc_fence_before_sync();
                 __syncwarp();
@@ -556,6 +597,8 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
                     set_phase ^= 1u;
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(W4_WEMPTY + ws));
             left -= W4_STAGE_K;
             if (++ws == STAGES) {
                 ws = 0;
@@ -565,7 +608,8 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
     } else if (warp < 10) {
         // ------------------------------------------------ codes and scales
         const int groups = p.K / GROUP;
-        const uint32_t tx = static_cast<uint32_t>(p.tile_rows) * 128u;
+        const uint32_t tx =
+            static_cast<uint32_t>(p.tile_rows) * 128u + (L::X_TMA ? 2 * L::X_BYTES : 0);
         int last_n = -1;
         struct alignas(2 * GPS) Scales { unsigned short v[GPS]; };
         struct alignas(GPS) Zeros { uint8_t v[GPS]; };
@@ -586,36 +630,52 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
                                     (static_cast<uint32_t>(n / STAGES) & 1u) ^ 1u, WAIT_EMPTY, s, 3);
             if (lane == 0 && ok) {
                 mbar_arrive_expect_tx(bar(W4_WFULL + ws), tx);
-                tma_load_2d(base + L::W + ws * W4_STAGE_BYTES, &tmW, bar(W4_WFULL + ws),
+                tma_load_2d(base + L::W + ws * L::STAGE, &tmW, bar(W4_WFULL + ws),
                             s * (W4_STAGE_K / 2), expert * p.N + n0);
+                if constexpr (L::X_TMA) {
+#pragma unroll
+                    for (int i = 0; i < W4_STAGE_K / 64; ++i)  // zeros past M and K
+                        tma_load_2d(base + L::X + ws * L::STAGE + i * NC * 128, &tmX,
+                                    bar(W4_WFULL + ws), s * W4_STAGE_K + i * 64, 0);
+                }
                 last_n = n;
             }
             __syncwarp();
-            Scales sc[W4_TILE / 32];
-            Zeros ze[W4_TILE / 32];
+            uint32_t* to =
+                reinterpret_cast<uint32_t*>(gen + L::TABLE) + ws * L::TABLE_WORDS + lane;
+            // -(1024 + zero) in fp16 is -1024's bits plus the zero point
+            if (p.wide_scales) {
+                constexpr int ROWS = GPS == 8 ? 2 : W4_TILE / 32;  // as registers allow
 #pragma unroll
-            for (int i = 0; i < W4_TILE / 32; ++i) {
-                if (p.wide_scales) {
-                    sc[i] = *reinterpret_cast<const Scales*>(scales[i] + s * GPS);
-                    if (zeros[i]) ze[i] = *reinterpret_cast<const Zeros*>(zeros[i] + s * GPS);
-                } else {
+                for (int i0 = 0; i0 < W4_TILE / 32; i0 += ROWS) {
+                    Scales sc[ROWS];
+                    Zeros ze[ROWS];
 #pragma unroll
-                    for (int g = 0; g < GPS; ++g) {
-                        const bool inside = s * GPS + g < groups;
-                        sc[i].v[g] = inside ? __half_as_ushort(scales[i][s * GPS + g]) : 0;
-                        ze[i].v[g] = inside && zeros[i] ? zeros[i][s * GPS + g] : 8;
+                    for (int i = 0; i < ROWS; ++i) {
+                        sc[i] = *reinterpret_cast<const Scales*>(scales[i0 + i] + s * GPS);
+                        if (zeros[i0 + i])
+                            ze[i] = *reinterpret_cast<const Zeros*>(zeros[i0 + i] + s * GPS);
+                    }
+#pragma unroll
+                    for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+                        for (int g = 0; g < GPS; ++g)
+                            to[g * W4_TILE + 32 * (i0 + i)] =
+                                sc[i].v[g] | ((0xe400u + (zeros[i0 + i] ? ze[i].v[g] : 8u)) << 16);
+                    __syncwarp();
+                }
+            } else {
+#pragma unroll 1
+                for (int g = 0; g < GPS; ++g) {
+                    const bool inside = s * GPS + g < groups;
+#pragma unroll
+                    for (int i = 0; i < W4_TILE / 32; ++i) {
+                        const uint32_t sc = inside ? __half_as_ushort(scales[i][s * GPS + g]) : 0u;
+                        const uint32_t ze = inside && zeros[i] ? zeros[i][s * GPS + g] : 8u;
+                        to[g * W4_TILE + 32 * i] = sc | ((0xe400u + ze) << 16);
                     }
                 }
             }
-            uint32_t* to = reinterpret_cast<uint32_t*>(gen + L::TABLE) + ws * L::TABLE_WORDS;
-#pragma unroll
-            for (int i = 0; i < W4_TILE / 32; ++i)
-#pragma unroll
-                for (int g = 0; g < GPS; ++g) {
-                    // -(1024 + zero) in fp16 is -1024's bits plus the zero point
-                    const uint32_t z = 0xe400u + (zeros[i] ? ze[i].v[g] : 8u);
-                    to[g * W4_TILE + 32 * i + lane] = sc[i].v[g] | (z << 16);
-                }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(W4_WFULL + ws));
         }
@@ -639,7 +699,12 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
             bool ok = wd.wait(bar(W4_AFULL + team * W4_TURNS + m % W4_TURNS),
                               static_cast<uint32_t>(m / W4_TURNS) & 1u, WAIT_FULL, k0, 1);
             const uint32_t a_tmem = tmem_base + static_cast<uint32_t>(buf * W4_A_COLS);
-            const uint64_t bdesc = sw128_kmajor_desc(base + L::X + buf * L::X_BYTES);
+            const int ws = n % STAGES;
+            if (L::X_TMA)
+                ok = ok && wd.wait(bar(W4_WFULL + ws), static_cast<uint32_t>(n / STAGES) & 1u,
+                                   WAIT_FULL, k0, 2);
+            const uint64_t bdesc = sw128_kmajor_desc(
+                base + L::X + (L::X_TMA ? ws * L::STAGE + (b & 1) * L::X_BYTES : buf * L::X_BYTES));
 #pragma unroll
             for (int h = 0; h < L::SETS_PER_BLOCK; ++h) {
                 // codes of the block that go to this set, and the set's first column
@@ -651,7 +716,7 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
                 if (!__all_sync(0xffffffffu, ok)) break;  // an abandoned run
                 const uint32_t d_tmem =
                     sum_tmem + static_cast<uint32_t>(set * L::SUM_COLS +
-                                                     (L::STAGE_SETS ? (b & 1) * NC : 0));
+                                                     (L::STAGE_SETS ? (b & 1) * GPB * NC : 0));
                 tc_fence_after_sync();
 #pragma unroll
                 for (int i = 0; i < SET_K; i += MMA_K) {
@@ -667,6 +732,8 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
             }
             if (!__all_sync(0xffffffffu, ok)) break;
             mma_commit_elected(elected, bar(W4_DONE + team * W4_TURNS + m % W4_TURNS));
+            if (L::X_TMA && ((b & 1) == 1 || k0 + W4_BLOCK_K >= end))
+                mma_commit_elected(elected, bar(W4_WEMPTY + ws));
         }
         mma_commit_elected(elected, bar(W4_DRAIN + issuer));  // by the lane that issued
         wd.drain(bar(W4_DRAIN + issuer), 0);
@@ -726,35 +793,32 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
 // the weights are written out once, scale * (q - zero) rounded to fp16 (nearest
 // even), and the GEMM multiplies them.  The rounding is at most half a unit in
 // the last place of each weight, the same as the output's.  A thread expands
-// eight codes (4 bytes) to 16 bytes.
+// eight codes (4 bytes) to 16 bytes: bound by writing the weights, which the GEMM
+// then reads from L2 where they fit (2000 rows of 4096 x 4096: 47.5 us in all, 52 with
+// the arithmetic in fp32 and a division per word to find its scale).
 __global__ void __launch_bounds__(256)
-    k_w4_expand(int64_t words, int words_per_row, int group_words, int groups,
-                const uint32_t* packed, const __half* scales, const uint8_t* zeros, uint4* out)
+    k_w4_expand(int64_t words, int group_shift, const uint32_t* packed, const __half* scales,
+                const uint8_t* zeros, uint4* out)
 {
     griddep_wait();
     griddep_launch_dependents();
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < words;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t row = i / words_per_row;
-        const int64_t at = row * groups + static_cast<int>(i - row * words_per_row) / group_words;
-        const uint32_t w = packed[i];
-        const float s = __half2float(scales[at]);
-        const float z = zeros ? static_cast<float>(zeros[at]) : 8.0f;
-        uint4 v;
-        uint32_t* h = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const __half2 q = __floats2half2_rn(s * (static_cast<float>((w >> (8 * j)) & 15u) - z),
-                                                s * (static_cast<float>((w >> (8 * j + 4)) & 15u) - z));
-            h[j] = *reinterpret_cast<const uint32_t*>(&q);
-        }
-        out[i] = v;
+         i += step) {
+        const int64_t at = i >> group_shift;  // a row has whole groups
+        const __half2 s = __half2half2(scales[at]);
+        const __half2 z = as_half2((0xe400u + (zeros ? zeros[at] : 8u)) * 0x10001u);
+        uint32_t e[4];
+        decode8_in_order(packed[i], __hadd2(z, as_half2(0x63800000u)), e);
+        // a product of two fp16 numbers, rounded once
+        out[i] = make_uint4(as_u32(__hmul2(as_half2(e[0]), s)), as_u32(__hmul2(as_half2(e[1]), s)),
+                            as_u32(__hmul2(as_half2(e[2]), s)), as_u32(__hmul2(as_half2(e[3]), s)));
     }
 }
 
 // One instantiation of the few-row kernel.
 struct W4Kernel {
-    void (*fn)(CUtensorMap, W4Params);
+    void (*fn)(CUtensorMap, CUtensorMap, W4Params);
     unsigned smem;
     int threads;
 };
@@ -802,13 +866,12 @@ struct W4Launch {
 // takes a CTA the same time whatever its rows (the kernel is bound by the
 // instructions and waits of its warps), a launch about 5 us more: so the length is
 // shared by as many CTAs as are resident at once, and the tiles are as low as
-// spread the rows evenly over those.  Measured per stage, one CTA per SM: 0.6, 0.9
-// and 1.2 us with groups of 128, 64 and 32 and up to 16 rows of X, 1.0 with 32 rows,
-// 1.4 with 64; two CTAs per SM (up to 16 rows) take 1.7 times as long, each.  How
-// many clusters are resident with one CTA per SM is asked of the runtime: clusters
-// of four and eight leave SMs of a GPC idle.  One row, 4096 x 14336: 13.7 us on 4 x
-// 35 CTAs, 18.9 on 8 x 37, of which not all are resident; 16384 x 16384: 39 us on 2
-// x 147, two per SM, 71 on 1 x 293.
+// spread the rows evenly over those.  The table below is measured with one CTA per
+// SM; two (up to 16 rows) take 1.7 times as long, each.  How many clusters are
+// resident with one CTA per SM is asked of the runtime: clusters of four and eight
+// leave SMs of a GPC idle.  One row, 4096 x 14336: 13.5 us on 4 x 35 CTAs, 18.9 on 8 x
+// 37, of which not all are resident; 16384 x 16384: 39 us on 2 x 147, two per SM, 71
+// on 1 x 293.
 cudaError_t choose_w4_tile(int64_t N, int64_t K, int64_t matrices, int cols, int group, int sms,
                            int* tile_rows, int* length_ctas)
 {
@@ -816,11 +879,9 @@ cudaError_t choose_w4_tile(int64_t N, int64_t K, int64_t matrices, int cols, int
     cudaError_t e = ensure_smem_limit(k.fn, k.smem);
     if (e != cudaSuccess) return e;
     const int64_t stages = (K + W4_STAGE_K - 1) / W4_STAGE_K;
-    const double one = cols == 64     ? 1.4
-                       : cols == 32   ? 1.0
-                       : group == 32  ? 1.2
-                       : group == 64  ? 0.9
-                                      : 0.6;
+    // us per stage by columns (16, 32, 64) and group (32, 64, 128)
+    static const double stage_us[3][3] = {{0.9, 0.75, 0.6}, {1.15, 0.8, 0.75}, {1.6, 1.25, 0.9}};
+    const double one = stage_us[cols / 32][group / 64];
     double best = -1.0;
     for (int ctas = 1; ctas <= 8 && (ctas == 1 || ctas * 2 <= stages); ctas *= 2) {
         int resident = sms;
@@ -875,23 +936,23 @@ namespace {
 
 constexpr int W4_MAX_ROWS = 64;
 
-// Tensor map over the codes, `rows` rows of `bytes`: boxes of 128 bytes x
-// `box_rows`, 128-byte swizzle, zeros past the end of a row.
-int encode_codes(CUtensorMap* map, const void* packed, int64_t bytes, int64_t rows, int box_rows)
+// Tensor map over a row-major matrix: boxes of 128 bytes x `box_rows`, 128-byte
+// swizzle, zeros outside.
+int encode_rows(CUtensorMap* map, const char* what, CUtensorMapDataType type, int elt,
+                const void* from, int64_t cols, int64_t rows, int box_rows)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode_fn();
     if (!enc) return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(bytes), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(bytes)};
-    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * elt)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t estr[2] = {1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(packed), dims,
-                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    CUresult r = enc(map, type, 2, const_cast<void*>(from), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r == CUDA_SUCCESS) return GEMM_OK;
     char buf[100];
-    std::snprintf(buf, sizeof(buf), "cuTensorMapEncodeTiled(packed) failed with CUresult %d",
+    std::snprintf(buf, sizeof(buf), "cuTensorMapEncodeTiled(%s) failed with CUresult %d", what,
                   static_cast<int>(r));
     return fail(GEMM_ERR_CUDA, buf);
 }
@@ -1000,8 +1061,8 @@ int gemm_w4_run(gemm_w4_plan* plan, const void* X, const void* packed, const voi
             const int64_t words = plan->N * (plan->K / 8);
             const int64_t blocks = std::min<int64_t>((words + 255) / 256, plan->sms * 32);
             e = launch_dependent(k_w4_expand, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1,
-                                 stream, words, static_cast<int>(plan->K / 8), plan->group / 8,
-                                 static_cast<int>(plan->K / plan->group),
+                                 stream, words,
+                                 plan->group == 32 ? 2 : plan->group == 64 ? 3 : 4,
                                  static_cast<const uint32_t*>(packed),
                                  static_cast<const __half*>(scales),
                                  static_cast<const uint8_t*>(zeros),
@@ -1028,16 +1089,21 @@ int gemm_w4_run(gemm_w4_plan* plan, const void* X, const void* packed, const voi
         if (++plan->epoch <= 0) plan->epoch = 1;
         p.epoch = plan->epoch;
         p.budget_ns = 2000ull * 1000000ull;
-        CUtensorMap map;
-        const int r = encode_codes(&map, packed, plan->K / 2,
-                                   plan->N * std::max(plan->experts, 1), plan->tile_rows);
+        CUtensorMap codes, x;
+        int r = encode_rows(&codes, "packed", CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, packed, plan->K / 2,
+                            plan->N * std::max(plan->experts, 1), plan->tile_rows);
+        if (r == GEMM_OK && plan->cols > 16)
+            r = encode_rows(&x, "X", CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, X, plan->K, plan->M,
+                            plan->cols);
+        else
+            x = codes;  // not used
         if (r != GEMM_OK) return r;
         const dim3 grid(static_cast<unsigned>((plan->N + plan->tile_rows - 1) / plan->tile_rows),
                         plan->experts > 0 ? static_cast<unsigned>(plan->M) : 1u,
                         static_cast<unsigned>(plan->length_ctas));
         const W4Kernel k = kernel_of(plan->cols, plan->group);
         W4Launch launch(k, grid, stream);
-        e = cudaLaunchKernelEx(&launch.cfg, k.fn, map, p);
+        e = cudaLaunchKernelEx(&launch.cfg, k.fn, codes, x, p);
         return e == cudaSuccess ? ok() : cuda_fail("w4 product launch", e);
     });
 }
