@@ -11,8 +11,7 @@
 // expert's last tile, so few rows per expert stay with single CTAs (the rule and its
 // figures are in grouped.cu).
 //
-// Measured: 16384 uneven rows, 16 experts of 4096 x 4096, 360 us, 1527 TFLOP/s, the
-// tensor pipe busy 81 % of the time; the rest is the last tiles of experts, part of
+// Measured: 16384 uneven rows, 16 experts of 4096 x 4096, 353 us, 1557 TFLOP/s; the rest is the last tiles of experts, part of
 // whose rows are the next expert's, and the last wave.
 //
 // The leader's producer takes tiles from the counter and hands them to both CTAs.
@@ -105,6 +104,39 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
+        : "memory");
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T over the pair, issued by the lane with `elected`
+// set.  The whole warp executes the statement: without a branch around it the
+// operands stay in uniform registers (8192 x 8192 x 8192 as one expert: 586 us, 619
+// behind `if (lane == 0)`).
+__device__ __forceinline__ void mma_pair_elected(uint32_t elected, uint32_t d_tmem, uint64_t a_desc,
+                                                 uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t"
+        ".reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "setp.ne.b32 q, %4, 0;\n\t"
+        "@p tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, q;\n\t"
+        "}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+}
+
+// An arrival in both CTAs once the lane's MMAs so far are complete.
+__device__ __forceinline__ void commit_pair_elected(uint32_t elected, uint32_t bar)
+{
+    asm volatile(
+        "{\n\t"
+        ".reg .pred p;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "@p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+        ".b64 [%0], %2;\n\t"
+        "}\n" ::"r"(bar),
+        "r"(elected), "h"(static_cast<uint16_t>(3))
         : "memory");
 }
 
@@ -336,6 +368,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GROUPED_THREADS, 1)
                                    (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
         int stage = 0;
         uint32_t phase = 0;
+        constexpr uint64_t A_STEP = A_MN ? KSTEP_MNMAJOR : KSTEP_KMAJOR;
+        constexpr uint64_t B_STEP = B_MN ? KSTEP_MNMAJOR : KSTEP_KMAJOR;
+        const uint32_t elected = lane == 0 ? 1u : 0u;
         int acc = 0;
         uint32_t acc_phase = 0;
         uint32_t tail_bits = 0;
@@ -383,26 +418,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GROUPED_THREADS, 1)
                         mbar_arrive_cluster(map_shared_rank(bar(BAR_TAIL_READY + stage), 0));
                     tail_bits ^= 1u << stage;
                 }
-                if (leader && lane == 0 && ok) {
+                if (leader && __all_sync(0xffffffffu, ok)) {
                     tc_fence_after_sync();
+                    const uint32_t a = sA + stage * PAIR_KS * A_TILE_BYTES;
+                    const uint32_t b = sB + stage * PAIR_KS * B_BYTES;
+                    auto issue = [&](int i) {  // slice i of the stage
+                        const int s = i / (BLK_K / MMA_K), kk = i % (BLK_K / MMA_K);
+                        const uint32_t as = a + s * A_TILE_BYTES, bs = b + s * B_BYTES;
+                        mma_pair_elected(
+                            elected, d_tmem,
+                            (A_MN ? sw128_mnmajor_desc(as) : sw128_kmajor_desc(as)) + kk * A_STEP,
+                            (B_MN ? sw128_mnmajor_desc(bs) : sw128_kmajor_desc(bs)) + kk * B_STEP,
+                            idesc, i == 0 && ki == 0 ? 0u : 1u);
+                    };
+                    if (left >= PAIR_STAGE_K) {
 #pragma unroll
-                    for (int s = 0; s < PAIR_KS; ++s) {
-                        const int rest = left - s * BLK_K;
-                        if (rest <= 0) break;
-                        const int slices = rest >= BLK_K ? BLK_K / MMA_K : (rest + MMA_K - 1) / MMA_K;
-                        const uint32_t a = sA + (stage * PAIR_KS + s) * A_TILE_BYTES;
-                        const uint32_t b = sB + (stage * PAIR_KS + s) * B_BYTES;
-                        const uint64_t adesc = A_MN ? sw128_mnmajor_desc(a) : sw128_kmajor_desc(a);
-                        const uint64_t bdesc = B_MN ? sw128_mnmajor_desc(b) : sw128_kmajor_desc(b);
-                        for (int kk = 0; kk < slices; ++kk)
-                            mma_f16_ss_pair(d_tmem,
-                                            adesc + static_cast<uint64_t>(kk) *
-                                                        (A_MN ? KSTEP_MNMAJOR : KSTEP_KMAJOR),
-                                            bdesc + static_cast<uint64_t>(kk) *
-                                                        (B_MN ? KSTEP_MNMAJOR : KSTEP_KMAJOR),
-                                            idesc, (ki == 0 && s == 0 && kk == 0) ? 0u : 1u);
+                        for (int i = 0; i < PAIR_STAGE_K / MMA_K; ++i) issue(i);
+                    } else {
+                        for (int i = 0; i * MMA_K < left; ++i) issue(i);
                     }
-                    mma_commit_pair_multicast(bar(BAR_EMPTY + stage), 0x3);
+                    commit_pair_elected(elected, bar(BAR_EMPTY + stage));
                 }
                 __syncwarp();
                 if (++stage == D) {
@@ -410,9 +445,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GROUPED_THREADS, 1)
                     phase ^= 1u;
                 }
             }
-            if (leader && lane == 0 && !wd.aborted)
-                mma_commit_pair_multicast(bar(BAR_TMEM_FULL + acc), 0x3);
-            __syncwarp();
+            if (leader && __all_sync(0xffffffffu, !wd.aborted))
+                commit_pair_elected(elected, bar(BAR_TMEM_FULL + acc));
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }
