@@ -75,14 +75,14 @@ int64_t expected_row_tiles(int64_t rows, int64_t N, int experts, int op, int bm)
 // The automatic tile: the one whose waves of tiles (a launch that hands out its
 // tiles ends half a wave after the last full one) take the least time, at each
 // tile's throughput per SM relative to pairs: 0.82 for 128 x 256 on single CTAs,
-// 0.73 for 128 x 128.  Measured, pairs against 128 x 256: 16 even experts of 4096 x
-// 4096 with 1024 rows each 316 and 356 us; uneven experts of 2816 x 2048, input
-// gradient, 32 with 256 rows on average 94 and 101, 64 with 128 rows 138 and 126; a
-// single expert with 1024 rows 28 and 37 (53 with 128 x 128).  40 experts of 1416 x
-// 2056 with 777 rows in all: 128 x 128 47, 128 x 256 50, pairs 53 us.  GRAD_WEIGHT's
-// tiles of few rows are bounded by their stores, in which pairs are slower (24
-// experts of 2048 x 4096, fp32: 273 against 285 us at 682 rows per expert, 333
-// against 314 at 512).
+// 0.70 for 128 x 128.  Measured, pairs, 128 x 256, 128 x 128: 16 even experts of 4096 x
+// 4096 with 1024 rows each 334, 351, 457 us; 29 uneven experts of 1400 x 1744 with 18013
+// rows, input gradient, 84, 92, 119; uneven experts of 2816 x 2048, input gradient, 32
+// with 256 rows on average 97, 102, 126, and 64 with 128 rows 148, 126, 146; 4 experts
+// of 488 x 2136 with 1810 rows 22, 25, 18; 41 experts of 3440 x 1920 with 78 rows in all
+// 87, 77, 79.  GRAD_WEIGHT's tiles of few rows are bounded by their stores, in which
+// pairs are slower (fp32, experts of 2048 x 4096: pairs 247 and 128 x 256 233 us at 512
+// rows per expert, 287 and 280 at 682, 226 and 232 at 1024, 186 and 194 at 2048).
 int choose_tile(int64_t rows, int64_t N, int64_t cols, int experts, int op, int sms, bool pair_fits)
 {
     struct Tile {
@@ -91,12 +91,12 @@ int choose_tile(int64_t rows, int64_t N, int64_t cols, int experts, int op, int 
     };
     const Tile tiles[3] = {{GEMM_GROUPED_TILE_256X256, 256, 256, std::max(1, sms / 2), 2.0},
                            {GEMM_GROUPED_TILE_128X256, 128, 256, sms, 0.82},
-                           {GEMM_GROUPED_TILE_128X128, 128, 128, sms, 0.73}};
+                           {GEMM_GROUPED_TILE_128X128, 128, 128, sms, 0.70}};
     int best = GEMM_GROUPED_TILE_128X256;
     double best_time = -1.0;
     for (const Tile& t : tiles) {
         if (t.kind == GEMM_GROUPED_TILE_256X256 &&
-            (!pair_fits || (op == GROUPED_GRAD_WEIGHT && rows < 600ll * experts)))
+            (!pair_fits || (op == GROUPED_GRAD_WEIGHT && rows < 800ll * experts)))
             continue;
         const int64_t count = expected_row_tiles(rows, N, experts, op, t.bm) * ceil_div(cols, t.bn);
         const double waves =

@@ -6,8 +6,8 @@
 //
 // Why pairs: a tile of 256 columns leaves a single CTA room for four stages of 64,
 // and every operand byte from L2 feeds half as many MMAs (16 experts of 4096 x 4096
-// with 1024 rows each: 1545 TFLOP/s on single CTAs, 1742 on pairs; one expert of
-// 8192 x 8192 with 8192 rows: 1582 and 1842).  A tile of 256 rows wastes more of an
+// with 1024 rows each: 1564 TFLOP/s on single CTAs, 1646 on pairs; one expert of 8192
+// x 8192 with 8192 rows: 1582 and 1878).  A tile of 256 rows wastes more of an
 // expert's last tile, so few rows per expert stay with single CTAs (the rule and its
 // figures are in grouped.cu).
 //
@@ -108,9 +108,8 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
 }
 
 // D[tmem] (+)= A[smem] * B[smem]^T over the pair, issued by the lane with `elected`
-// set.  The whole warp executes the statement: without a branch around it the
-// operands stay in uniform registers (8192 x 8192 x 8192 as one expert: 586 us, 619
-// behind `if (lane == 0)`).
+// set, as mma_elected (8192 x 8192 x 8192 as one expert: 586 us, 619 behind `if (lane
+// == 0)`).
 __device__ __forceinline__ void mma_pair_elected(uint32_t elected, uint32_t d_tmem, uint64_t a_desc,
                                                  uint64_t b_desc, uint32_t idesc,
                                                  uint32_t accumulate)
