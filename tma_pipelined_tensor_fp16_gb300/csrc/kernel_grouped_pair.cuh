@@ -11,8 +11,9 @@
 // expert's last tile, so few rows per expert stay with single CTAs (the rule and its
 // figures are in grouped.cu).
 //
-// Measured: 16384 uneven rows, 16 experts of 4096 x 4096, 353 us, 1557 TFLOP/s; the rest is the last tiles of experts, part of
-// whose rows are the next expert's, and the last wave.
+// Measured: 16384 uneven rows, 16 experts of 4096 x 4096, 355 us, 1548 TFLOP/s; what
+// is lost are the last tiles of experts, part of whose rows are the next expert's, and
+// the last wave.
 //
 // The leader's producer takes tiles from the counter and hands them to both CTAs.
 // Contraction rows past an expert's last one (GRAD_WEIGHT) have to be zeroed in

@@ -60,11 +60,11 @@ struct W4Params {
 // with tcgen05.st, and shared memory is left to the codes in flight.
 //
 // Bound on paper by reading the codes, in fact by the instructions of the warps that
-// convert and add up (about 3200 a stage and CTA, half of them the conversion and its
-// stores to TMEM; issue slots 65 % used, DRAM 41 %).  One row of 16384 x 16384, groups
-// of 128: 38.8 us, 3.6 TB/s; 32 slots of 64 experts of 2048 x 4096: 32.7 us; 64 rows
-// of 8192 x 4096, groups of 32: 18.1 us.  Without the conversion one row takes 26
-// us, without the sums 34.
+// convert and add up (about 3100 a stage and CTA, half of them the conversion and its
+// stores to TMEM; 2.6 instructions a cycle over the whole launch, DRAM 41 % used).  One row of 16384 x 16384, groups
+// of 128: 38.2 us, 3.6 TB/s; 32 slots of 64 experts of 2048 x 4096: 32.1 us; 64 rows
+// of 8192 x 4096, groups of 32: 18.1 us.  Without the conversion one row takes 31
+// us.
 //
 // Roles of a CTA, joined by mbarriers only:
 //   warps 0..7    workers, two teams of four warps; warp w owns rows
@@ -242,6 +242,17 @@ __device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, uint32_t (&r)[1
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
           "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// The same for 4 columns.
+__device__ __forceinline__ void tmem_load_4cols(uint32_t taddr, uint32_t (&r)[4])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
         : "r"(taddr)
         : "memory");
 }
@@ -580,6 +591,17 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
                     // the last stage may have one block only
                     if (L::STAGE_SETS && g >= GPB && left <= W4_BLOCK_K) break;
                     const float sg = scale_of(g0 + g);
+                    // Few rows, the usual case, pay for few columns only (one row of 16384
+                    // x 16384: 38.2 us and 38.8, with groups of 32 50.9 and 53.0; 16 rows
+                    // lose a hundredth by the branch).
+                    if (COLS == 16 && count <= 4) {
+                        uint32_t v[4];
+                        tmem_load_4cols(from + g * NC, v);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            acc[j] = fmaf(sg, __uint_as_float(v[j]), acc[j]);
+                        continue;
+                    }
                     uint32_t v[COLS];
                     if constexpr (COLS == 16)
                         tmem_load_16cols(from + g * NC, v);
