@@ -61,10 +61,10 @@ struct W4Params {
 //
 // Bound on paper by reading the codes, in fact by the instructions of the warps that
 // convert and add up (about 3100 a stage and CTA, half of them the conversion and its
-// stores to TMEM; 2.6 instructions a cycle over the whole launch, DRAM 41 % used).  One row of 16384 x 16384, groups
-// of 128: 38.2 us, 3.6 TB/s; 32 slots of 64 experts of 2048 x 4096: 32.1 us; 64 rows
-// of 8192 x 4096, groups of 32: 18.1 us.  Without the conversion one row takes 31
-// us.
+// stores to TMEM; 2.6 instructions a cycle over a whole launch, DRAM 41 % used).  One
+// row of 16384 x 16384, groups of 128: 38.2 us, 3.6 TB/s, 31 without the conversion; 32
+// slots of 64 experts of 2048 x 4096: 32.1 us; 64 rows of 8192 x 4096, groups of 32:
+// 18.1 us.
 //
 // Roles of a CTA, joined by mbarriers only:
 //   warps 0..7    workers, two teams of four warps; warp w owns rows
