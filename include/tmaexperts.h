@@ -162,8 +162,7 @@ TMAGEMM_API int gemm_w4_run(gemm_w4_plan* plan, const void* X, const void* packe
                             const void* scales, const void* zeros, const int32_t* expert_ids,
                             void* Y, void* cuda_stream);
 
-/* As gemm_get_device_status (only the product of more than 64 rows has waits
- * that can run out), gemm_destroy and gemm_plan_describe. */
+/* As gemm_get_device_status, gemm_destroy and gemm_plan_describe. */
 TMAGEMM_API int gemm_w4_get_device_status(gemm_w4_plan* plan);
 TMAGEMM_API void gemm_w4_destroy(gemm_w4_plan* plan);
 TMAGEMM_API const char* gemm_w4_describe(const gemm_w4_plan* plan);
