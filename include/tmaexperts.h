@@ -141,18 +141,20 @@ typedef struct gemm_w4_plan gemm_w4_plan; /* opaque; owned by the library */
  *   X      : M x K fp16      Y : M x N of dtype_out
  *
  * group is 32, 64 or 128, K a multiple of group, N of 8 (fp16) or 4 (fp32).
- * Up to 64 rows q - zero enters the tensor cores as the integer it is, each
- * group is summed in fp32 and scaled there; for more rows the weights are
- * expanded once per run to fp16 (rounded to nearest even) in a workspace of
- * N * K * 2 bytes that the plan owns, and the GEMM of tmagemm.h multiplies them.
+ * Up to 64 rows, and up to some hundreds where that is expected to be faster, q -
+ * zero enters the tensor cores as the integer it is, each group is summed in fp32
+ * and scaled there; for more rows the weights are expanded once per run to fp16
+ * (rounded to nearest even) in a workspace of N * K * 2 bytes that the plan owns,
+ * and the GEMM of tmagemm.h multiplies them.  gemm_w4_describe says which ("rows",
+ * "expand").
  *
  * experts > 0: packed, scales and zeros are stacked (experts x N x ...), and row
  * m of Y is the product of X[m / share] with the weights of expert
  * expert_ids[m]; X has ceil(M / share) rows.  M <= 1024 then.  A row whose id is
  * negative or >= experts is set to zero.  experts = 0: one matrix, share = 1.
  *
- * Returns NULL on error.  Runs of one plan must not overlap on the GPU when
- * M > 64 (they share the workspace). */
+ * Returns NULL on error.  Runs of one plan must not overlap on the GPU when it
+ * expands the weights (they share the workspace). */
 TMAGEMM_API gemm_w4_plan* gemm_w4_create_plan(int64_t M, int64_t N, int64_t K, int group,
                                               int experts, int share, int dtype_out);
 

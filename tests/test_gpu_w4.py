@@ -87,6 +87,38 @@ def test_many_rows(M, N, K, group, zeros):
         assert_within(got, want, tolerance(want, mag, K, out) + 2.0 ** -11 * mag, what)
 
 
+# Blocks of 64 rows: the last one of one row, half and whole, a length that ends in half
+# a stage and in a part of a block, with the length on one CTA and on several.
+BLOCKS = [(65, 264, 2176, 32), (128, 1032, 2112, 64), (193, 136, 4224, 128),
+          (256, 520, 2208, 32), (400, 72, 4096, 64), (130, 4096, 1024, 128)]
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("M,N,K,group", BLOCKS)
+def test_blocks_of_rows(M, N, K, group, zeros):
+    """More rows than a block without rounding the weights."""
+    rng = np.random.default_rng(M + N)
+    for out in ("f16", "f32"):
+        got, want, _, what = _run(M, N, K, group, zeros, out, True, rng)
+        assert what.startswith("w4 rows"), what
+        assert_same(got, want, out, what)
+        got, want, mag, what = _run(M, N, K, group, zeros, out, False, rng)
+        assert_within(got, want, tolerance(want, mag, K, out), what)
+
+
+@pytest.mark.parametrize("M,N,K,group", [(2000, 136, 256, 32), (3000, 512, 512, 64),
+                                         (1500, 1032, 1152, 128)])
+def test_expanded(M, N, K, group):
+    """Many rows take the expansion to fp16."""
+    rng = np.random.default_rng(M + K)
+    for zeros in (False, True):
+        got, want, _, what = _run(M, N, K, group, zeros, "f32", True, rng)
+        assert what.startswith("w4 expand"), what
+        assert_same(got, want, "f32", what)
+        got, want, mag, what = _run(M, N, K, group, zeros, "f16", False, rng)
+        assert_within(got, want, tolerance(want, mag, K, "f16") + 2.0 ** -11 * mag, what)
+
+
 def test_zero_points_beyond_four_bits():
     """Zero points are whole numbers 0..255 and stay exact."""
     import tma_pipelined_tensor_fp16_gb300 as tg

@@ -41,9 +41,9 @@ struct W4Params {
 
 // ---------------------------------------------------------------- few rows
 //
-// Up to 64 rows of X, bound by reading the codes once.  The product runs on
+// Blocks of up to 64 rows of X, bound by reading the codes once.  The product runs on
 // tcgen05.mma with 128 rows of the weights as the M side and the rows of X as
-// the N side (16, 32 or 64).
+// the N side (16, 32 or 64).  Without experts grid.y is the block.
 //
 // A 32-bit word holds the codes k..k+7.  Masking the word and its shift by 8
 // with 0x000f000f and 0x00f000f0 and setting the exponent of 1024 gives half
@@ -388,9 +388,12 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
     griddep_wait();
     griddep_launch_dependents();
 
-    // the rows of Y of this CTA
-    int expert = 0, count = p.M;
-    if (p.experts > 0) {
+    // the rows of Y of this CTA: y0 and the following, or those on the list
+    int expert = 0, y0 = 0, count = p.M;
+    if (p.experts == 0) {
+        y0 = static_cast<int>(blockIdx.y) * NC;
+        count = p.M - y0 < NC ? p.M - y0 : NC;
+    } else {
         const int first = static_cast<int>(blockIdx.y);
         expert = p.ids[first];
         if (expert < 0 || expert >= p.experts) {  // a dropped row
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
         const __half* x = p.X;
         int64_t xnext = static_cast<int64_t>(p.K) * 8;
         if (!L::X_TMA && m0 < count) {
-            const int y = p.experts > 0 ? list[m0] : m0;
+            const int y = p.experts > 0 ? list[m0] : y0 + m0;
             x = p.X + static_cast<int64_t>(y / p.share) * p.K + c0 * 8;
             if (p.experts > 0 && m0 + 8 < count)
                 xnext = static_cast<int64_t>(list[m0 + 8] / p.share - y / p.share) * p.K;
@@ -658,7 +661,7 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
 #pragma unroll
                     for (int i = 0; i < W4_STAGE_K / 64; ++i)  // zeros past M and K
                         tma_load_2d(base + L::X + ws * L::STAGE + i * NC * 128, &tmX,
-                                    bar(W4_WFULL + ws), s * W4_STAGE_K + i * 64, 0);
+                                    bar(W4_WFULL + ws), s * W4_STAGE_K + i * 64, y0);
                 }
                 last_n = n;
             }
@@ -776,7 +779,7 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
 #pragma unroll
             for (int c = 0; c < COLS; ++c) {
                 const int m = col0 + c;
-                if (m < count) store_y(p, p.experts > 0 ? list[m] : m, n0 + row, acc[c]);
+                if (m < count) store_y(p, p.experts > 0 ? list[m] : y0 + m, n0 + row, acc[c]);
             }
         }
         return;
@@ -803,7 +806,7 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
                              : "memory");
                 v += part;
             }
-            store_y(p, p.experts > 0 ? list[m] : m, n0 + row, v);
+            store_y(p, p.experts > 0 ? list[m] : y0 + m, n0 + row, v);
         }
     }
     cluster_sync_all();  // nobody reads this CTA's sums any more
@@ -884,25 +887,25 @@ struct W4Launch {
     }
 };
 
-// Rows per tile and CTAs per cluster of the few-row kernel.  A stage of 256 codes
-// takes a CTA the same time whatever its rows (the kernel is bound by the
-// instructions and waits of its warps), a launch about 5 us more: so the length is
-// shared by as many CTAs as are resident at once, and the tiles are as low as
-// spread the rows evenly over those.  The table below is measured with one CTA per
-// SM; two (up to 16 rows) take 1.7 times as long, each.  How many clusters are
-// resident with one CTA per SM is asked of the runtime: clusters of four and eight
-// leave SMs of a GPC idle.  One row, 4096 x 14336: 13.5 us on 4 x 35 CTAs, 18.9 on 8 x
-// 37, of which not all are resident; 16384 x 16384: 39 us on 2 x 147, two per SM, 71
-// on 1 x 293.
+// Rows per tile and CTAs per cluster of the few-row kernel, and the time they are
+// expected to take.  A stage of 256 codes takes a CTA the same time whatever its rows
+// (the kernel is bound by the instructions and waits of its warps), a launch about 5 us
+// more: so the length is shared by as many CTAs as are resident at once, and the tiles
+// are as low as spread the rows evenly over those.  The table below is measured with
+// one CTA per SM; two (up to 16 rows) take 1.7 times as long, each.  A second wave of
+// CTAs sets up anew: 3.6 us, 7 for clusters.  How many clusters are resident with one
+// CTA per SM is asked of the runtime: clusters of four and eight leave SMs of a GPC
+// idle.  One row, 4096 x 14336: 13.5 us on 4 x 35 CTAs, 18.9 on 8 x 37, of which not
+// all are resident; 16384 x 16384: 39 us on 2 x 147, two per SM, 71 on 1 x 293.
 cudaError_t choose_w4_tile(int64_t N, int64_t K, int64_t matrices, int cols, int group, int sms,
-                           int* tile_rows, int* length_ctas)
+                           int* tile_rows, int* length_ctas, double* us)
 {
     const W4Kernel k = kernel_of(cols, group);
     cudaError_t e = ensure_smem_limit(k.fn, k.smem);
     if (e != cudaSuccess) return e;
     const int64_t stages = (K + W4_STAGE_K - 1) / W4_STAGE_K;
     // us per stage by columns (16, 32, 64) and group (32, 64, 128)
-    static const double stage_us[3][3] = {{0.9, 0.75, 0.6}, {1.15, 0.8, 0.75}, {1.6, 1.25, 0.9}};
+    static const double stage_us[3][3] = {{0.9, 0.75, 0.6}, {1.15, 0.8, 0.75}, {1.36, 1.14, 0.76}};
     const double one = stage_us[cols / 32][group / 64];
     double best = -1.0;
     for (int ctas = 1; ctas <= 8 && (ctas == 1 || ctas * 2 <= stages); ctas *= 2) {
@@ -922,16 +925,31 @@ cudaError_t choose_w4_tile(int64_t N, int64_t K, int64_t matrices, int cols, int
             const int64_t tiles = (N + rows - 1) / rows * matrices;
             const int64_t waves = (tiles + clusters - 1) / clusters;
             const double time =
-                3.6 + waves * (1.4 + one * (per_sm == 2 ? 1.7 : 1.0) *
-                                         static_cast<double>((stages + ctas - 1) / ctas));
+                5.0 + static_cast<double>(waves - 1) * (ctas > 1 ? 7.0 : 3.6) +
+                static_cast<double>(waves * ((stages + ctas - 1) / ctas)) * one *
+                    (per_sm == 2 ? 1.7 : 1.0);
             if (best < 0.0 || time < best) {
                 best = time;
                 *tile_rows = static_cast<int>(rows);
                 *length_ctas = ctas;
+                *us = time;
             }
         }
     }
     return cudaSuccess;
+}
+
+// Expected time of the expansion and the GEMM: the weights are written, and read by a
+// GEMM that takes 5.8 us per 1024 of the length at least (few tiles), and for more rows
+// 1500 TFLOP/s.  Few-row kernel, expansion and GEMM, groups of 128: 128 rows of 8192 x
+// 8192 29 and 75 us, 256 rows 57 and 75, 384 rows 85 and 74; 512 rows of 1024 x 4096 13
+// and 28; groups of 32: 128 rows of 16384 x 4096 52 and 58, 192 rows 77 and 60.
+double expanded_us(int64_t M, int64_t N, int64_t K)
+{
+    const double weights = static_cast<double>(N) * static_cast<double>(K);
+    return 3.5 + weights * 2.6 / 6.5e6 +
+           std::max({5.8 * static_cast<double>(K) / 1024.0, weights * 2.0 / 4.7e6,
+                     2.0 * static_cast<double>(M) * weights / 1.5e9});
 }
 
 }  // namespace
@@ -955,8 +973,6 @@ struct gemm_w4_plan {
 };
 
 namespace {
-
-constexpr int W4_MAX_ROWS = 64;
 
 // Tensor map over a row-major matrix: boxes of 128 bytes x `box_rows`, 128-byte
 // swizzle, zeros outside.
@@ -1019,13 +1035,15 @@ gemm_w4_plan* gemm_w4_create_plan(int64_t M, int64_t N, int64_t K, int group, in
         p.experts = experts;
         p.share = share;
         p.dtype = dtype_out;
-        if (experts > 0 || M <= W4_MAX_ROWS) {
-            p.cols = 16;
-            while (experts == 0 && p.cols < M) p.cols *= 2;
-            cudaError_t e =
-                choose_w4_tile(N, K, experts > 0 ? std::min<int64_t>(M, experts) : 1, p.cols, group,
-                               p.sms, &p.tile_rows, &p.length_ctas);
-            if (e != cudaSuccess) return cuda_fail("choosing the tile", e);
+        p.cols = 16;
+        while (experts == 0 && p.cols < std::min<int64_t>(M, 64)) p.cols *= 2;
+        const int64_t blocks = (M + p.cols - 1) / p.cols;  // of rows, without experts
+        double us = 0.0;
+        cudaError_t e = choose_w4_tile(N, K, experts > 0 ? std::min<int64_t>(M, experts) : blocks,
+                                       p.cols, group, p.sms, &p.tile_rows, &p.length_ctas, &us);
+        if (e != cudaSuccess) return cuda_fail("choosing the tile", e);
+        if (experts == 0 && blocks > 1 && (blocks > 65535 || us > expanded_us(M, N, K))) p.cols = 0;
+        if (p.cols > 0) {
             std::snprintf(p.desc, sizeof(p.desc),
                           "w4 rows M=%lld N=%lld K=%lld group=%d experts=%d tile=%dx%d "
                           "length_ctas=%d out=%s",
@@ -1041,7 +1059,7 @@ gemm_w4_plan* gemm_w4_create_plan(int64_t M, int64_t N, int64_t K, int group, in
         } else {
             p.gemm = gemm_create_plan(M, N, K, dtype_out);
             if (!p.gemm) return gemm_last_status();
-            cudaError_t e = cudaMalloc(&p.d_weights, static_cast<size_t>(N) * K * 2);
+            e = cudaMalloc(&p.d_weights, static_cast<size_t>(N) * K * 2);
             if (e != cudaSuccess) {
                 gemm_destroy(p.gemm);
                 return cuda_fail("allocating the expanded weights", e);
@@ -1121,7 +1139,9 @@ int gemm_w4_run(gemm_w4_plan* plan, const void* X, const void* packed, const voi
             x = codes;  // not used
         if (r != GEMM_OK) return r;
         const dim3 grid(static_cast<unsigned>((plan->N + plan->tile_rows - 1) / plan->tile_rows),
-                        plan->experts > 0 ? static_cast<unsigned>(plan->M) : 1u,
+                        static_cast<unsigned>(plan->experts > 0
+                                                  ? plan->M
+                                                  : (plan->M + plan->cols - 1) / plan->cols),
                         static_cast<unsigned>(plan->length_ctas));
         const W4Kernel k = kernel_of(plan->cols, plan->group);
         W4Launch launch(k, grid, stream);
