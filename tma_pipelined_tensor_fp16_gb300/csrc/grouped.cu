@@ -265,11 +265,11 @@ int gemm_grouped_run(gemm_grouped_plan* plan, const void* P, const void* Q,
         const CUtensorMapDataType F16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
         const CUtensorMapDataType OUT =
             elt == 2 ? F16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-        CUtensorMap tmA, tmB, tmC;
+        CUtensorMap tmA, tmS, tmB, tmC;
         int r;
         if (plan->op == GROUPED_FORWARD) {
             r = encode(&tmA, F16, 2, P, K, R, 0, BLK_K, BLK_M, "A");
-            if (r == GEMM_OK) 
+            if (r == GEMM_OK)
                 r = encode(&tmB, F16, 2, Q, K, N, E, BLK_K,
                            plan->pair ? plan->block_n / 2 : plan->block_n, "B");
         } else if (plan->op == GROUPED_GRAD_INPUT) {
@@ -279,6 +279,11 @@ int gemm_grouped_run(gemm_grouped_plan* plan, const void* P, const void* Q,
             r = encode(&tmA, F16, 2, P, N, R, 0, 64, BLK_K, "dC");
             if (r == GEMM_OK) r = encode(&tmB, F16, 2, Q, K, R, 0, 64, BLK_K, "A");
         }
+        if (r == GEMM_OK && !weight && !plan->pair)
+            r = encode(&tmS, F16, 2, P, plan->op == GROUPED_FORWARD ? K : N, R, 0, BLK_K,
+                       GROUPED_SMALL_ROWS, "rows");
+        else
+            tmS = tmA;  // not used
         if (r == GEMM_OK)
             r = weight ? encode(&tmC, OUT, elt, out, K, N, E, 128 / elt, 32, "dB")
                        : encode(&tmC, OUT, elt, out, cols, R, 0, 128 / elt, 32, "out");
@@ -292,6 +297,7 @@ int gemm_grouped_run(gemm_grouped_plan* plan, const void* P, const void* Q,
         s.grid = plan->grid;
         s.smem_bytes = plan->smem_bytes;
         s.tmA = &tmA;
+        s.tmS = &tmS;
         s.tmB = &tmB;
         s.tmC = &tmC;
         GroupedParams& p = s.p;

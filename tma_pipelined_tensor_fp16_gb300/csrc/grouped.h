@@ -38,6 +38,7 @@ struct GroupedSpec {
     int grid;
     unsigned smem_bytes;
     const CUtensorMap* tmA;  // the operand whose rows are output rows
+    const CUtensorMap* tmS;  // the same with boxes of GROUPED_SMALL_ROWS rows (not GRAD_WEIGHT)
     const CUtensorMap* tmB;  // the operand whose rows (or columns) are output columns
     const CUtensorMap* tmC;
     GroupedParams p;
@@ -46,6 +47,7 @@ struct GroupedSpec {
 cudaError_t launch_grouped(const GroupedSpec& s, cudaStream_t stream);
 
 constexpr int GROUPED_THREADS = 192;
+constexpr int GROUPED_SMALL_ROWS = 32;
 constexpr int GROUPED_MAX_EXPERTS = 1024;
 
 // GRAD_WEIGHT sorts the experts by their rows up to this many of them (the sort
