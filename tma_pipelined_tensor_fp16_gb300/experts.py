@@ -67,8 +67,8 @@ def _out_dtype(out):
 
 
 def _ptr(t):
-    """A tensor's address; None for no tensor and for an empty one."""
-    return t.data_ptr() or None if t is not None else None
+    """A tensor's address; None for no tensor (an empty one has the address 0)."""
+    return None if t is None else t.data_ptr()
 
 
 def _call(fn, device, stream, *args):
@@ -76,7 +76,7 @@ def _call(fn, device, stream, *args):
     current stream.  Raises on an error status."""
     torch = _torch()
     index = device.index
-    if torch.cuda.current_device() != index:
+    if torch._C._cuda_getDevice() != index:  # the tensors have set CUDA up
         with torch.cuda.device(device):
             return _call(fn, device, stream, *args)
     if stream is None:
