@@ -141,12 +141,14 @@ typedef struct gemm_w4_plan gemm_w4_plan; /* opaque; owned by the library */
  *   X      : M x K fp16      Y : M x N of dtype_out
  *
  * group is 32, 64 or 128, K a multiple of group, N of 8 (fp16) or 4 (fp32).
- * Up to 64 rows, and up to some hundreds where that is expected to be faster, q -
- * zero enters the tensor cores as the integer it is, each group is summed in fp32
- * and scaled there; for more rows the weights are expanded once per run to fp16
- * (rounded to nearest even) in a workspace of N * K * 2 bytes that the plan owns,
- * and the GEMM of tmagemm.h multiplies them.  gemm_w4_describe says which ("rows",
- * "expand").
+ * No weight is rounded, whatever the number of rows.  Up to 64 rows, and above where
+ * that is expected to be faster, q - zero enters the tensor cores as the integer
+ * it is, each group is summed in fp32 and scaled there ("rows" in gemm_w4_describe).
+ * For more rows each weight is written out once per run as the sum of two fp16 numbers
+ * and the GEMM of tmagemm.h multiplies them over twice the length ("expand"); where a
+ * weight is beyond 65504 or an entry of X is not finite, which that form does not
+ * cover, the kernel of "rows" computes Y.  The plan then owns workspaces of N * K * 4
+ * and M * K * 4 bytes.
  *
  * experts > 0: packed, scales and zeros are stacked (experts x N x ...), and row
  * m of Y is the product of X[m / share] with the weights of expert
@@ -157,6 +159,16 @@ typedef struct gemm_w4_plan gemm_w4_plan; /* opaque; owned by the library */
  * expands the weights (they share the workspace). */
 TMAGEMM_API gemm_w4_plan* gemm_w4_create_plan(int64_t M, int64_t N, int64_t K, int group,
                                               int experts, int share, int dtype_out);
+
+/* Same with the caller's choice for many rows: GEMM_W4_WEIGHTS_ROUNDED lets a plan that
+ * expands round each weight to fp16 (nearest even; beyond 65504 to an infinity), which
+ * halves the GEMM and needs a workspace of N * K * 2 bytes only.  Y is then off by up
+ * to half a unit in the last place of each weight. */
+typedef enum { GEMM_W4_WEIGHTS_EXACT = 0, GEMM_W4_WEIGHTS_ROUNDED = 1 } gemm_w4_weights;
+
+TMAGEMM_API gemm_w4_plan* gemm_w4_create_plan_ex(int64_t M, int64_t N, int64_t K, int group,
+                                                 int experts, int share, int dtype_out,
+                                                 int weights);
 
 /* Enqueue the product.  expert_ids (M int32) must be given exactly when the
  * plan has experts. */

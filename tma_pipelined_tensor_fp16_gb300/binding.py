@@ -97,6 +97,7 @@ _SIGS = {
     "gemm_grouped_destroy": (None, [ctypes.c_void_p]),
     "gemm_grouped_describe": (ctypes.c_char_p, [ctypes.c_void_p]),
     "gemm_w4_create_plan": (ctypes.c_void_p, [ctypes.c_int64] * 3 + [ctypes.c_int] * 4),
+    "gemm_w4_create_plan_ex": (ctypes.c_void_p, [ctypes.c_int64] * 3 + [ctypes.c_int] * 5),
     "gemm_w4_run": (ctypes.c_int, [ctypes.c_void_p] * 8),
     "gemm_w4_get_device_status": (ctypes.c_int, [ctypes.c_void_p]),
     "gemm_w4_destroy": (None, [ctypes.c_void_p]),

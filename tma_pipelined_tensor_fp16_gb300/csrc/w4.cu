@@ -34,6 +34,8 @@ struct W4Params {
     int f16out;
     int tile_rows;         // rows of the weights per CTA (a multiple of 8, up to 128)
     int wide_scales;       // a stage's scales and zeros of a row are aligned vectors
+    const int* verdicts;   // 64 columns; not nullptr: run only if one of them is not zero
+    int verdict_count;
     DevStatus* status;
     int epoch;
     unsigned long long budget_ns;
@@ -387,6 +389,13 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
     wd.aborted = false;
     griddep_wait();
     griddep_launch_dependents();
+    if constexpr (NC == 64) {  // more rows than that are expanded
+        if (p.verdicts) {
+            int any = 0;
+            for (int i = tid; i < p.verdict_count; i += L::THREADS) any |= p.verdicts[i];
+            if (!__syncthreads_or(any)) return;  // the GEMM's result stands (k_w4_expand)
+        }
+    }
 
     // the rows of Y of this CTA: y0 and the following, or those on the list
     int expert = 0, y0 = 0, count = p.M;
@@ -814,30 +823,77 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
 
 // ------------------------------------------------------------ many rows
 //
-// For many rows of X the product is bound by the tensor cores, which read fp16:
-// the weights are written out once, scale * (q - zero) rounded to fp16 (nearest
-// even), and the GEMM multiplies them.  The rounding is at most half a unit in
-// the last place of each weight, the same as the output's.  A thread expands
-// eight codes (4 bytes) to 16 bytes: bound by writing the weights, which the GEMM
-// then reads from L2 where they fit (2000 rows of 4096 x 4096: 47.5 us in all, 52 with
-// the arithmetic in fp32 and a division per word to find its scale).
+// For many rows of X the GEMM multiplies expanded weights.  w = scale * (q - zero) is a
+// multiple of 2^-24 with at most 11 + 8 significant bits, so
+//
+//     hi = w rounded to fp16 (nearest even),   lo = w - hi
+//
+// are both fp16 numbers and hi + lo = w: lo is a multiple of 2^-24 too, at most half a
+// unit of hi.  Each chunk of eight codes becomes a chunk of hi and a chunk of lo, each
+// chunk of X the same chunk twice, and the GEMM sums over twice the length: no weight
+// is rounded.  (The tensor cores then do twice the work; the caller may ask for hi
+// alone.)
+//
+// That form does not hold where hi or an entry of X is not finite: w beyond 65504, and
+// infinity * lo where lo = 0.  So every CTA leaves a verdict on what it has seen, and
+// the few-row kernel runs behind the GEMM: it returns at once where all verdicts are
+// zero and else computes Y anew.  Every word is written in every run, so none is kept
+// from one to the next.
+//
+// A thread expands eight codes (4 bytes) to 32 bytes, or copies a chunk of X: bound by
+// the writes, which the GEMM then reads from L2 where they fit (2048 rows of 4096 x 4096,
+// groups of 64: 115 us in all, 48 with rounded weights, 169 by the few-row kernel).
+constexpr int W4_EXPAND_CTAS = 8;  // per SM
+
+// Whether one of the two halves is an infinity or NaN.
+__device__ __forceinline__ uint32_t not_finite(uint32_t v)
+{
+    return ((v & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+}
+
+template <bool ROUNDED>
 __global__ void __launch_bounds__(256)
     k_w4_expand(int64_t words, int group_shift, const uint32_t* packed, const __half* scales,
-                const uint8_t* zeros, uint4* out)
+                const uint8_t* zeros, uint4* out, int64_t chunks, const uint4* X, uint4* X2,
+                int* verdicts)
 {
     griddep_wait();
     griddep_launch_dependents();
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < words;
-         i += step) {
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    uint32_t bad = 0;
+    for (int64_t i = first; i < words; i += step) {
         const int64_t at = i >> group_shift;  // a row has whole groups
         const __half2 s = __half2half2(scales[at]);
         const __half2 z = as_half2((0xe400u + (zeros ? zeros[at] : 8u)) * 0x10001u);
-        uint32_t e[4];
+        uint32_t e[4], hi[4], lo[4];
         decode8_in_order(packed[i], __hadd2(z, as_half2(0x63800000u)), e);
-        // a product of two fp16 numbers, rounded once
-        out[i] = make_uint4(as_u32(__hmul2(as_half2(e[0]), s)), as_u32(__hmul2(as_half2(e[1]), s)),
-                            as_u32(__hmul2(as_half2(e[2]), s)), as_u32(__hmul2(as_half2(e[3]), s)));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __half2 d = as_half2(e[j]);
+            const __half2 h = __hmul2(d, s);  // a product of two fp16 numbers, rounded once
+            hi[j] = as_u32(h);
+            if constexpr (!ROUNDED) {
+                lo[j] = as_u32(__hfma2(d, s, __hneg2(h)));
+                bad |= not_finite(hi[j]);
+            }
+        }
+        if constexpr (ROUNDED) {
+            out[i] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        } else {
+            out[2 * i] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            out[2 * i + 1] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
+    if constexpr (!ROUNDED) {
+        for (int64_t i = first; i < chunks; i += step) {
+            const uint4 v = X[i];
+            X2[2 * i] = v;
+            X2[2 * i + 1] = v;
+            bad |= not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w);
+        }
+        const int any = __syncthreads_or(static_cast<int>(bad != 0));
+        if (threadIdx.x == 0) verdicts[blockIdx.x] = any;
     }
 }
 
@@ -939,17 +995,29 @@ cudaError_t choose_w4_tile(int64_t N, int64_t K, int64_t matrices, int cols, int
     return cudaSuccess;
 }
 
-// Expected time of the expansion and the GEMM: the weights are written, and read by a
-// GEMM that takes 5.8 us per 1024 of the length at least (few tiles), and for more rows
-// 1500 TFLOP/s.  Few-row kernel, expansion and GEMM, groups of 128: 128 rows of 8192 x
-// 8192 29 and 75 us, 256 rows 57 and 75, 384 rows 85 and 74; 512 rows of 1024 x 4096 13
-// and 28; groups of 32: 128 rows of 16384 x 4096 52 and 58, 192 rows 77 and 60.
-double expanded_us(int64_t M, int64_t N, int64_t K)
+// Expected time of the expansion and the GEMM: the weights (and X, twice) are written,
+// and read by a GEMM that takes 5.8 us per 1024 of its length at least (few tiles), and
+// for more rows 1500 TFLOP/s.  Few-row kernel, expansion and GEMM, rounded weights, us:
+// 8192 x 8192, groups of 128: 256 rows 62, 174, 84; 512 rows 121, 170, 77; 1024 rows 211,
+// 244, 111; 2048 rows 419, 396, 187.  4096 x 4096, groups of 64: 512 rows 49, 75, 35;
+// 1024 rows 97, 72, 30; 2048 rows 169, 115, 48.  16384 x 4096, groups of 32: 256 rows 110,
+// 144, 61; 512 rows 193, 175, 78.  1024 x 4096, groups of 128: 2048 rows 37, 68, 30.
+double expanded_us(int64_t M, int64_t N, int64_t K, bool rounded)
 {
     const double weights = static_cast<double>(N) * static_cast<double>(K);
-    return 3.5 + weights * 2.6 / 6.5e6 +
-           std::max({5.8 * static_cast<double>(K) / 1024.0, weights * 2.0 / 4.7e6,
-                     2.0 * static_cast<double>(M) * weights / 1.5e9});
+    const double x = static_cast<double>(M) * static_cast<double>(K);
+    const double gemm = std::max({5.8 * static_cast<double>(K) / 1024.0, weights * 2.0 / 4.7e6,
+                                  2.0 * static_cast<double>(M) * weights / 1.5e9});
+    if (rounded) return 3.5 + weights * 2.6 / 6.5e6 + gemm;
+    return 8.0 + (weights * 5.2 + x * 6.0) / 6.5e6 + 2.0 * gemm;
+}
+
+// Whether a plan of more than one block of rows expands.  Many rows of a short length
+// always do: the two are then close (few-row kernel and expansion, us: 1500 rows of 1032 x
+// 1152 20.0 and 24.9, 3000 of 512 x 512 16.5 and 15.6, 2000 of 136 x 256 8.6 and 10.8).
+bool prefers_expansion(int64_t M, int64_t N, int64_t K, bool rounded, double rows_us)
+{
+    return (M > 1024 && K < 2048) || rows_us > expanded_us(M, N, K, rounded);
 }
 
 }  // namespace
@@ -962,12 +1030,16 @@ struct gemm_w4_plan {
     int64_t M, N, K;
     int group, experts, share, dtype;
     int device, sms;
-    int cols;         // N side of the few-row kernel's MMA; 0: expand + GEMM
+    bool expand;      // expand + GEMM, the few-row kernel where that does not hold
+    bool rounded;     // the weights rounded to fp16, no more
+    int cols;         // N side of the few-row kernel's MMA
     int length_ctas;  // CTAs that share a row's length
     int tile_rows;    // rows of the weights per CTA
     DevStatus* d_status;
     int epoch;
-    void* d_weights; // N x K fp16
+    void* d_weights;  // N x 2 K fp16 (rounded: N x K)
+    void* d_x;        // M x 2 K fp16
+    int* d_verdicts;  // one per CTA of the expansion
     gemm_plan* gemm;
     char desc[256];
 };
@@ -995,12 +1067,82 @@ int encode_rows(CUtensorMap* map, const char* what, CUtensorMapDataType type, in
     return fail(GEMM_ERR_CUDA, buf);
 }
 
+void release(const gemm_w4_plan& p)
+{
+    if (p.gemm) gemm_destroy(p.gemm);
+    if (p.d_weights) cudaFree(p.d_weights);
+    if (p.d_x) cudaFree(p.d_x);
+    if (p.d_verdicts) cudaFree(p.d_verdicts);
+    if (p.d_status) cudaFree(p.d_status);
+}
+
+constexpr int64_t MAX_ROW_BLOCKS = 65535;  // grid.y
+
+// The few-row kernel over all of a plan's rows; with `verdicts`, behind an expansion
+// of so many CTAs.
+int run_rows(gemm_w4_plan* plan, const void* X, const void* packed, const void* scales,
+             const void* zeros, const int32_t* expert_ids, void* Y, cudaStream_t stream,
+             int verdicts)
+{
+    W4Params p = {};
+    p.N = static_cast<int>(plan->N);
+    p.K = static_cast<int>(plan->K);
+    p.experts = plan->experts;
+    p.share = plan->share;
+    p.packed = static_cast<const uint8_t*>(packed);
+    p.scales = static_cast<const __half*>(scales);
+    p.zeros = static_cast<const uint8_t*>(zeros);
+    p.ids = expert_ids;
+    p.f16out = plan->dtype == GEMM_OUT_F16;
+    p.tile_rows = plan->tile_rows;
+    p.wide_scales = plan->K % W4_STAGE_K == 0 && (reinterpret_cast<uintptr_t>(zeros) & 7u) == 0;
+    p.verdicts = verdicts > 0 ? plan->d_verdicts : nullptr;
+    p.verdict_count = verdicts;
+    p.status = plan->d_status;
+    if (++plan->epoch <= 0) plan->epoch = 1;
+    p.epoch = plan->epoch;
+    p.budget_ns = 2000ull * 1000000ull;
+    CUtensorMap codes, x;
+    int r = encode_rows(&codes, "packed", CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, packed, plan->K / 2,
+                        plan->N * std::max(plan->experts, 1), plan->tile_rows);
+    if (r != GEMM_OK) return r;
+    const W4Kernel k = kernel_of(plan->cols, plan->group);
+    const int64_t most = plan->experts > 0 ? plan->M : MAX_ROW_BLOCKS * plan->cols;
+    for (int64_t m0 = 0; m0 < plan->M; m0 += most) {
+        const int64_t rows = std::min(most, plan->M - m0);
+        p.M = static_cast<int>(rows);
+        p.X = static_cast<const __half*>(X) + m0 * plan->K;
+        p.Y = static_cast<char*>(Y) + m0 * plan->N * (p.f16out ? 2 : 4);
+        x = codes;  // not used
+        if (plan->cols > 16)
+            r = encode_rows(&x, "X", CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p.X, plan->K, rows,
+                            plan->cols);
+        if (r != GEMM_OK) return r;
+        const dim3 grid(static_cast<unsigned>((plan->N + plan->tile_rows - 1) / plan->tile_rows),
+                        static_cast<unsigned>(plan->experts > 0
+                                                  ? rows
+                                                  : (rows + plan->cols - 1) / plan->cols),
+                        static_cast<unsigned>(plan->length_ctas));
+        W4Launch launch(k, grid, stream);
+        const cudaError_t e = cudaLaunchKernelEx(&launch.cfg, k.fn, codes, x, p);
+        if (e != cudaSuccess) return cuda_fail("w4 product launch", e);
+    }
+    return ok();
+}
+
 }  // namespace
 
 extern "C" {
 
 gemm_w4_plan* gemm_w4_create_plan(int64_t M, int64_t N, int64_t K, int group, int experts,
                                   int share, int dtype_out)
+{
+    return gemm_w4_create_plan_ex(M, N, K, group, experts, share, dtype_out,
+                                  GEMM_W4_WEIGHTS_EXACT);
+}
+
+gemm_w4_plan* gemm_w4_create_plan_ex(int64_t M, int64_t N, int64_t K, int group, int experts,
+                                     int share, int dtype_out, int weights)
 {
     gemm_w4_plan* plan = nullptr;
     guarded([&] {
@@ -1012,6 +1154,8 @@ gemm_w4_plan* gemm_w4_create_plan(int64_t M, int64_t N, int64_t K, int group, in
         if (dtype_out != GEMM_OUT_F32 && dtype_out != GEMM_OUT_F16)
             return fail(GEMM_ERR_INVALID_ARG,
                         "dtype_out must be GEMM_OUT_F32 (0) or GEMM_OUT_F16 (1)");
+        if (weights != GEMM_W4_WEIGHTS_EXACT && weights != GEMM_W4_WEIGHTS_ROUNDED)
+            return fail(GEMM_ERR_INVALID_ARG, "unknown gemm_w4_weights");
         if (experts < 0 || share < 1 || (experts == 0 && share != 1))
             return fail(GEMM_ERR_INVALID_ARG,
                         "experts must be >= 0 and share >= 1 (1 without experts)");
@@ -1035,6 +1179,7 @@ gemm_w4_plan* gemm_w4_create_plan(int64_t M, int64_t N, int64_t K, int group, in
         p.experts = experts;
         p.share = share;
         p.dtype = dtype_out;
+        p.rounded = weights == GEMM_W4_WEIGHTS_ROUNDED;
         p.cols = 16;
         while (experts == 0 && p.cols < std::min<int64_t>(M, 64)) p.cols *= 2;
         const int64_t blocks = (M + p.cols - 1) / p.cols;  // of rows, without experts
@@ -1042,37 +1187,44 @@ gemm_w4_plan* gemm_w4_create_plan(int64_t M, int64_t N, int64_t K, int group, in
         cudaError_t e = choose_w4_tile(N, K, experts > 0 ? std::min<int64_t>(M, experts) : blocks,
                                        p.cols, group, p.sms, &p.tile_rows, &p.length_ctas, &us);
         if (e != cudaSuccess) return cuda_fail("choosing the tile", e);
-        if (experts == 0 && blocks > 1 && (blocks > 65535 || us > expanded_us(M, N, K))) p.cols = 0;
-        if (p.cols > 0) {
-            std::snprintf(p.desc, sizeof(p.desc),
-                          "w4 rows M=%lld N=%lld K=%lld group=%d experts=%d tile=%dx%d "
-                          "length_ctas=%d out=%s",
-                          static_cast<long long>(M), static_cast<long long>(N),
-                          static_cast<long long>(K), group, experts, p.tile_rows, p.cols, p.length_ctas,
-                          elt == 2 ? "f16" : "f32");
+        const int64_t depth = p.rounded ? K : 2 * K;
+        p.expand = experts == 0 && blocks > 1 && depth <= LIM &&
+                   std::max(M, N) <= (int64_t(1) << 45) / depth &&
+                   prefers_expansion(M, N, K, p.rounded, us);
+        int length = 0;
+        if (p.expand) {
+            p.gemm = gemm_create_plan(M, N, depth, dtype_out);
+            if (!p.gemm) return gemm_last_status();
+            length = std::snprintf(p.desc, sizeof(p.desc), "w4 expand group=%d weights=%s; %.180s",
+                                   group, p.rounded ? "rounded" : "exact",
+                                   gemm_plan_describe(p.gemm));
+        } else {
+            length = std::snprintf(p.desc, sizeof(p.desc),
+                                   "w4 rows M=%lld N=%lld K=%lld group=%d experts=%d tile=%dx%d "
+                                   "length_ctas=%d out=%s",
+                                   static_cast<long long>(M), static_cast<long long>(N),
+                                   static_cast<long long>(K), group, experts, p.tile_rows, p.cols,
+                                   p.length_ctas, elt == 2 ? "f16" : "f32");
+        }
+        if (length < 0) p.desc[0] = '\0';
+        const char* what = "allocating the device status record";
+        if (!p.expand || !p.rounded) {
             e = cudaMalloc(&p.d_status, sizeof(DevStatus));
             if (e == cudaSuccess) e = cudaMemset(p.d_status, 0, sizeof(DevStatus));
-            if (e != cudaSuccess) {
-                if (p.d_status) cudaFree(p.d_status);
-                return cuda_fail("allocating the device status record", e);
-            }
-        } else {
-            p.gemm = gemm_create_plan(M, N, K, dtype_out);
-            if (!p.gemm) return gemm_last_status();
-            e = cudaMalloc(&p.d_weights, static_cast<size_t>(N) * K * 2);
-            if (e != cudaSuccess) {
-                gemm_destroy(p.gemm);
-                return cuda_fail("allocating the expanded weights", e);
-            }
-            std::snprintf(p.desc, sizeof(p.desc), "w4 expand group=%d; %.180s", group,
-                          gemm_plan_describe(p.gemm));
         }
-        plan = new (std::nothrow) gemm_w4_plan(p);
+        if (e == cudaSuccess && p.expand) {
+            what = "allocating the expanded weights";
+            e = cudaMalloc(&p.d_weights, static_cast<size_t>(N) * depth * 2);
+            if (e == cudaSuccess && !p.rounded)
+                e = cudaMalloc(&p.d_x, static_cast<size_t>(M) * depth * 2);
+            if (e == cudaSuccess && !p.rounded)
+                e = cudaMalloc(&p.d_verdicts,
+                               static_cast<size_t>(p.sms) * W4_EXPAND_CTAS * sizeof(int));
+        }
+        if (e == cudaSuccess) plan = new (std::nothrow) gemm_w4_plan(p);
         if (!plan) {
-            if (p.gemm) gemm_destroy(p.gemm);
-            if (p.d_weights) cudaFree(p.d_weights);
-            if (p.d_status) cudaFree(p.d_status);
-            return fail(GEMM_ERR_CUDA, "out of host memory");
+            release(p);
+            return e != cudaSuccess ? cuda_fail(what, e) : fail(GEMM_ERR_CUDA, "out of host memory");
         }
         return ok();
     });
@@ -1097,56 +1249,27 @@ int gemm_w4_run(gemm_w4_plan* plan, const void* X, const void* packed, const voi
         if (dev != plan->device)
             return fail(GEMM_ERR_INVALID_ARG, "plan was created on another device");
         cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-        if (plan->cols == 0) {
-            const int64_t words = plan->N * (plan->K / 8);
-            const int64_t blocks = std::min<int64_t>((words + 255) / 256, plan->sms * 32);
-            e = launch_dependent(k_w4_expand, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1,
-                                 stream, words,
-                                 plan->group == 32 ? 2 : plan->group == 64 ? 3 : 4,
-                                 static_cast<const uint32_t*>(packed),
-                                 static_cast<const __half*>(scales),
-                                 static_cast<const uint8_t*>(zeros),
-                                 static_cast<uint4*>(plan->d_weights));
-            if (e != cudaSuccess) return cuda_fail("weight expansion launch", e);
-            return gemm_run(plan->gemm, X, plan->d_weights, Y, cuda_stream);
-        }
-        W4Params p = {};
-        p.M = static_cast<int>(plan->M);
-        p.N = static_cast<int>(plan->N);
-        p.K = static_cast<int>(plan->K);
-        p.experts = plan->experts;
-        p.share = plan->share;
-        p.packed = static_cast<const uint8_t*>(packed);
-        p.scales = static_cast<const __half*>(scales);
-        p.zeros = static_cast<const uint8_t*>(zeros);
-        p.X = static_cast<const __half*>(X);
-        p.ids = expert_ids;
-        p.Y = Y;
-        p.f16out = plan->dtype == GEMM_OUT_F16;
-        p.tile_rows = plan->tile_rows;
-        p.wide_scales = plan->K % W4_STAGE_K == 0 && (reinterpret_cast<uintptr_t>(zeros) & 7u) == 0;
-        p.status = plan->d_status;
-        if (++plan->epoch <= 0) plan->epoch = 1;
-        p.epoch = plan->epoch;
-        p.budget_ns = 2000ull * 1000000ull;
-        CUtensorMap codes, x;
-        int r = encode_rows(&codes, "packed", CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, packed, plan->K / 2,
-                            plan->N * std::max(plan->experts, 1), plan->tile_rows);
-        if (r == GEMM_OK && plan->cols > 16)
-            r = encode_rows(&x, "X", CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, X, plan->K, plan->M,
-                            plan->cols);
-        else
-            x = codes;  // not used
-        if (r != GEMM_OK) return r;
-        const dim3 grid(static_cast<unsigned>((plan->N + plan->tile_rows - 1) / plan->tile_rows),
-                        static_cast<unsigned>(plan->experts > 0
-                                                  ? plan->M
-                                                  : (plan->M + plan->cols - 1) / plan->cols),
-                        static_cast<unsigned>(plan->length_ctas));
-        const W4Kernel k = kernel_of(plan->cols, plan->group);
-        W4Launch launch(k, grid, stream);
-        e = cudaLaunchKernelEx(&launch.cfg, k.fn, codes, x, p);
-        return e == cudaSuccess ? ok() : cuda_fail("w4 product launch", e);
+        if (!plan->expand)
+            return run_rows(plan, X, packed, scales, zeros, expert_ids, Y, stream, 0);
+        const int64_t words = plan->N * (plan->K / 8);
+        const int64_t chunks = plan->rounded ? 0 : plan->M * (plan->K / 8);
+        const int64_t blocks = std::min<int64_t>((std::max(words, chunks) + 255) / 256,
+                                                 static_cast<int64_t>(plan->sms) * W4_EXPAND_CTAS);
+        e = launch_dependent(plan->rounded ? k_w4_expand<true> : k_w4_expand<false>,
+                             dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1, stream, words,
+                             plan->group == 32 ? 2 : plan->group == 64 ? 3 : 4,
+                             static_cast<const uint32_t*>(packed),
+                             static_cast<const __half*>(scales),
+                             static_cast<const uint8_t*>(zeros),
+                             static_cast<uint4*>(plan->d_weights), chunks,
+                             static_cast<const uint4*>(X), static_cast<uint4*>(plan->d_x),
+                             plan->d_verdicts);
+        if (e != cudaSuccess) return cuda_fail("weight expansion launch", e);
+        const int r = gemm_run(plan->gemm, plan->rounded ? X : plan->d_x, plan->d_weights, Y,
+                               cuda_stream);
+        if (r != GEMM_OK || plan->rounded) return r;
+        return run_rows(plan, X, packed, scales, zeros, nullptr, Y, stream,
+                        static_cast<int>(blocks));
     });
 }
 
@@ -1154,17 +1277,15 @@ int gemm_w4_get_device_status(gemm_w4_plan* plan)
 {
     return guarded([&] {
         if (!plan) return fail(GEMM_ERR_INVALID_ARG, "plan is NULL");
-        return plan->gemm ? gemm_get_device_status(plan->gemm)
-                          : read_device_status(plan->d_status);
+        const int r = plan->gemm ? gemm_get_device_status(plan->gemm) : GEMM_OK;
+        return r == GEMM_OK && plan->d_status ? read_device_status(plan->d_status) : r;
     });
 }
 
 void gemm_w4_destroy(gemm_w4_plan* plan)
 {
     if (!plan) return;
-    if (plan->gemm) gemm_destroy(plan->gemm);
-    if (plan->d_weights) cudaFree(plan->d_weights);
-    if (plan->d_status) cudaFree(plan->d_status);
+    release(*plan);
     delete plan;
 }
 

@@ -23,6 +23,7 @@ kernels, asynchronously on the current stream of the tensors' device (or on
 from .binding import GEMM_OUT_F16, GEMM_OUT_F32, GemmError, _check, last_error, lib
 
 GROUPED_OPS = {"forward": 0, "grad_input": 1, "grad_weight": 2}
+W4_WEIGHTS = {"exact": 0, "rounded": 1}
 GROUPED_TILES = {"auto": 0, "128x128": 1, "128x256": 2, "256x256": 3}
 
 
@@ -275,14 +276,22 @@ class W4Plan(_Handle):
     q[2b + 1]), ``scales`` N x K/group fp16, ``zeros`` N x K/group uint8 or None
     for 8 (``w4_pack`` makes them).  With ``experts`` they are stacked, and row m
     of Y is the product of X[m // share] with the weights of expert ids[m].
+
+    Many rows are multiplied as fp16 matrices: with ``weights="exact"`` each weight
+    as the sum of two fp16 numbers, with ``"rounded"`` rounded to one (half the
+    work; the result is off by up to half a unit in the last place of each weight).
     """
     _destroy, _describe, _status = "gemm_w4_destroy", "gemm_w4_describe", "gemm_w4_get_device_status"
 
-    def __init__(self, M, N, K, group=128, out="f16", experts=0, share=1):
+    def __init__(self, M, N, K, group=128, out="f16", experts=0, share=1,
+                 weights="exact"):
+        if weights not in W4_WEIGHTS:
+            raise ValueError("weights must be one of %s" % sorted(W4_WEIGHTS))
         self.M, self.N, self.K, self.group = M, N, K, group
         self.experts, self.share = experts, share
         self.dtype, code = _out_dtype(out)
-        self._own(lib().gemm_w4_create_plan(M, N, K, group, experts, share, code))
+        self._own(lib().gemm_w4_create_plan_ex(M, N, K, group, experts, share, code,
+                                               W4_WEIGHTS[weights]))
 
     def __call__(self, X, packed, scales, out=None, zeros=None, ids=None, stream=None):
         torch = _torch()
