@@ -297,6 +297,10 @@ __device__ __forceinline__ uint32_t map_shared_rank(uint32_t local, uint32_t ran
 // are visible.  launch_dependents: let the next launch on the stream, if it
 // was launched as a programmatic dependent, be scheduled before this grid
 // completes (its CTAs still wait for resources and for its own `wait`).
+// A kernel that uses tensor memory allocates it before launch_dependents: the
+// next kernel may start on the same SM, take the rest of the columns and hold
+// them in its `wait` until this kernel ends, so an allocation here that comes
+// later and does not fit would never return, and no wait limit covers it.
 __device__ __forceinline__ void griddep_wait()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -388,7 +388,6 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
     wd.budget_ns = p.budget_ns;
     wd.aborted = false;
     griddep_wait();
-    griddep_launch_dependents();
     if constexpr (NC == 64) {  // more rows than that are expanded
         if (p.verdicts) {
             int any = 0;
@@ -456,6 +455,7 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    griddep_launch_dependents();  // CTAs that have returned count as having done so
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     if (p.experts > 0) {
         count = 0;
