@@ -37,3 +37,65 @@ def test_tensor_memory_is_allocated_before_dependents_start():
             seen += 1
             assert max(alloc) < min(trigger), "%s: %s triggers before it allocates" % (file, name)
     assert seen >= 4
+
+
+def _orders(ops):
+    """The orders in which one thread's operations may take effect: program order for
+    operations on one address and across a fence, any order otherwise."""
+    for p in itertools.permutations(range(len(ops))):
+        place = {i: k for k, i in enumerate(p)}
+        if all(place[i] < place[j] for i in range(len(ops)) for j in range(i + 1, len(ops))
+               if ops[i][1] == ops[j][1] or "fence" in (ops[i][0], ops[j][0])):
+            yield [ops[i] for i in p]
+
+
+def _merges(a, b):
+    if not a or not b:
+        yield list(a) + list(b)
+        return
+    for rest in _merges(a[1:], b):
+        yield [a[0]] + rest
+    for rest in _merges(a, b[1:]):
+        yield [b[0]] + rest
+
+
+def _left_over(take, done, fence):
+    """Whether some order leaves tiles counted as taken after two CTAs have each taken
+    two tiles and arrived, the last one setting the counters back."""
+    cta = [("take", take), ("take", take)] + ([("fence", None)] if fence else []) + \
+        [("done", done)]
+    for x, y in itertools.product(list(_orders(cta)), repeat=2):
+        for order in _merges([(0,) + o for o in x], [(1,) + o for o in y]):
+            taken = arrived = 0
+            for _, op, _addr in order:
+                if op == "take":
+                    taken += 1
+                elif op == "done":
+                    arrived += 1
+                    if arrived == 2:
+                        taken = 0
+            if taken:
+                return True
+    return False
+
+
+@pytest.mark.parametrize("file", ["kernel_grouped.cuh", "kernel_grouped_pair.cuh"])
+def test_tile_counter_starts_every_run_at_zero(file):
+    """Tiles are handed out from a counter that the last CTA to finish sets back.  A
+    tile taken must not be counted after that."""
+    text = _source(file)
+    if "grouped_take(p.counter)" in text:  # through the functions of kernel_grouped.cuh
+        assert len(re.findall(r"grouped_(?:take|finish)\(p\.counter", text)) == 2
+        text = _source("kernel_grouped.cuh")
+    calls = re.findall(r"atomicAdd\(\s*([^,]+?)\s*,", text)
+    assert len(calls) == 2, calls
+    take, done = calls
+    at = text.index("atomicAdd(" + take)
+    fence = "__threadfence" in text[at:text.index("atomicAdd(" + done, at + 1)]
+    assert not _left_over(take, done, fence)
+
+
+def test_the_model_finds_a_late_count():
+    assert _left_over("a", "b", False)
+    assert not _left_over("a", "b", True)
+    assert not _left_over("a", "a", False)

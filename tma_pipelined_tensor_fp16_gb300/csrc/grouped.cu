@@ -222,10 +222,10 @@ gemm_grouped_plan* gemm_grouped_create_plan_ex(int64_t rows, int64_t N, int64_t 
                       static_cast<long long>(K), experts, p.block_m, p.block_n,
                       p.pair ? 2 * BLK_K : BLK_K, p.pipe_depth,
                       p.smem_bytes, p.grid, dtype_out == GEMM_OUT_F16 ? "f16" : "f32");
-        // the status record and, behind it, the two counters
-        cudaError_t e = cudaMalloc(&p.d_status, sizeof(DevStatus) + 2 * sizeof(unsigned));
+        // the status record and, behind it, the counter
+        cudaError_t e = cudaMalloc(&p.d_status, sizeof(DevStatus) + sizeof(unsigned long long));
         if (e == cudaSuccess)
-            e = cudaMemset(p.d_status, 0, sizeof(DevStatus) + 2 * sizeof(unsigned));
+            e = cudaMemset(p.d_status, 0, sizeof(DevStatus) + sizeof(unsigned long long));
         if (e != cudaSuccess) {
             if (p.d_status) cudaFree(p.d_status);
             return cuda_fail("allocating the device status record", e);
@@ -317,7 +317,7 @@ int gemm_grouped_run(gemm_grouped_plan* plan, const void* P, const void* Q,
         p.offsets = offsets;
         p.out = out;
         p.status = plan->d_status;
-        p.counters = reinterpret_cast<unsigned*>(plan->d_status + 1);
+        p.counter = reinterpret_cast<unsigned long long*>(plan->d_status + 1);
         if (++plan->epoch <= 0) plan->epoch = 1;
         p.epoch = plan->epoch;
         p.budget_ns = 2000ull * 1000000ull;

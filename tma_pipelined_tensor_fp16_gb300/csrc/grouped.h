@@ -25,7 +25,7 @@ struct GroupedParams {
     const int* offsets;
     void* out;
     DevStatus* status;
-    unsigned* counters;  // tiles taken beyond the first ones, CTAs finished
+    unsigned long long* counter;  // see grouped_take
     int epoch;
     unsigned long long budget_ns;
 };

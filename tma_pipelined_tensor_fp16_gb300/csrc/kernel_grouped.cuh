@@ -179,6 +179,22 @@ struct GroupedTiles {
     }
 };
 
+// The run's counter: tiles taken beyond each worker's first one in the lower half,
+// workers that have finished in the upper half.  Both halves are one word on
+// purpose: a worker's operations on one address take effect in program order, on
+// two they need not, and a tile counted after the last worker has set the counter
+// back would be missing from the next run.
+__device__ __forceinline__ int grouped_take(unsigned long long* counter)
+{
+    return static_cast<int>(static_cast<unsigned>(atomicAdd(counter, 1ull)));
+}
+
+// A worker takes no more; the last one sets the counter back.
+__device__ __forceinline__ void grouped_finish(unsigned long long* counter, unsigned workers)
+{
+    if (atomicAdd(counter, 1ull << 32) >> 32 == workers - 1) atomicExch(counter, 0ull);
+}
+
 // GRAD_WEIGHT: the experts with the most rows, whose tiles take longest, come
 // first, so that the last tiles of a launch are short ones.
 __device__ __forceinline__ void grouped_order(const GroupedParams& p, int* row0, int* order, int tid)
@@ -450,7 +466,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
         // The tile after the one whose loads are being issued is handed out
         // before them, and the one after that is on its way from the counter.
         auto take = [&] {
-            return lane == 0 ? static_cast<int>(gridDim.x + atomicAdd(p.counters, 1u)) : 0;
+            return lane == 0 ? static_cast<int>(gridDim.x) + grouped_take(p.counter) : 0;
         };
         auto hand_out = [&](int use, int u) {
             const int slot = use % GROUPED_SLOTS;
@@ -527,12 +543,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
             }
             u = next;
         }
-        // the last CTA to get here sets the counters back for the next run
-        if (lane == 0 && atomicAdd(p.counters + 1, 1u) == gridDim.x - 1) {
-            p.counters[0] = 0;
-            p.counters[1] = 0;
-            __threadfence();
-        }
+        if (lane == 0) grouped_finish(p.counter, gridDim.x);
         // an abandoned run: the loads in flight land before the CTA exits
         if (lane == 0 && wd.aborted) {
             int st = end_stage;

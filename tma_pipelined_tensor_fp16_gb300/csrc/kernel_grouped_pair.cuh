@@ -245,7 +245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GROUPED_THREADS, 1)
         // counter.
         auto take = [&] {
             return leader && lane == 0
-                       ? static_cast<int>(gridDim.x / 2 + atomicAdd(p.counters, 1u))
+                       ? static_cast<int>(gridDim.x / 2) + grouped_take(p.counter)
                        : 0;
         };
         auto hand_out = [&](int use, int tile) {
@@ -332,12 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GROUPED_THREADS, 1)
             }
             u = leader ? next : pair_read(bars, use, wd, lane);
         }
-        // the last leader to get here sets the counters back for the next run
-        if (leader && lane == 0 && atomicAdd(p.counters + 1, 1u) == gridDim.x / 2 - 1) {
-            p.counters[0] = 0;
-            p.counters[1] = 0;
-            __threadfence();
-        }
+        if (leader && lane == 0) grouped_finish(p.counter, gridDim.x / 2);
         // An abandoned run: let the copies in flight land.  The leader waits for
         // the phases it armed, both for their last tail; the peer's other copies
         // signal the leader, so it gives them a while.
