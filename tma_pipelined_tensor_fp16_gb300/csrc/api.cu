@@ -785,19 +785,7 @@ int gemm_run(gemm_plan* plan, const void* A, const void* B, void* C, void* cuda_
 int gemm_get_device_status(gemm_plan* plan)
 {
     if (!plan) return fail(GEMM_ERR_INVALID_ARG, "plan is NULL");
-    DevStatus st;
-    cudaError_t e = cudaMemcpy(&st, plan->d_status, sizeof(st), cudaMemcpyDeviceToHost);
-    if (e != cudaSuccess) return cuda_fail("reading the device status record", e);
-    if (st.code == DEV_OK) return ok();
-    DevStatus zero;
-    std::memset(&zero, 0, sizeof(zero));
-    zero.abort_epoch = st.abort_epoch;  // keep: a stale epoch never matches a new run
-    cudaMemcpy(plan->d_status, &zero, sizeof(zero), cudaMemcpyHostToDevice);
-    char buf[200];
-    std::snprintf(buf, sizeof(buf),
-                  "kernel wait timed out (where=%d block=%d tile=%d k_block=%d); the run was abandoned",
-                  st.where, st.block, st.tile, st.kblock);
-    return fail(st.code == DEV_TIMEOUT ? GEMM_ERR_TIMEOUT : GEMM_ERR_CUDA, buf);
+    return read_device_status(plan->d_status);
 }
 
 namespace {

@@ -71,6 +71,17 @@ struct DevStatus {
     int pad[2];
 };
 
+// The host's reading of a record (its stream synchronised): the code, and the record
+// cleared.  abort_epoch goes too: a CUDA graph gives every replay the run number it was
+// captured with, so a record that kept it would make the waits of each later replay give
+// up without a code.  A run marked abandoned is a timeout even where no code is left.
+TG_HD int take_status(DevStatus* st)
+{
+    const int code = st->code != DEV_OK ? st->code : st->abort_epoch != 0 ? DEV_TIMEOUT : DEV_OK;
+    *st = DevStatus{};
+    return code;
+}
+
 struct Params {
     int M, N, K;
     int tiles_m, tiles_n, num_tiles, k_blocks;

@@ -55,15 +55,16 @@ int read_device_status(DevStatus* record)
     DevStatus st;
     cudaError_t e = cudaMemcpy(&st, record, sizeof(st), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_fail("reading the device status record", e);
-    if (st.code == DEV_OK) return ok();
-    DevStatus zero = {};
-    zero.abort_epoch = st.abort_epoch;  // a stale epoch never matches a new run
-    cudaMemcpy(record, &zero, sizeof(zero), cudaMemcpyHostToDevice);
+    DevStatus left = st;
+    const int code = take_status(&left);
+    if (code == DEV_OK) return ok();
+    e = cudaMemcpy(record, &left, sizeof(left), cudaMemcpyHostToDevice);
+    if (e != cudaSuccess) return cuda_fail("clearing the device status record", e);
     char buf[200];
     std::snprintf(buf, sizeof(buf),
                   "kernel wait timed out (where=%d block=%d tile=%d k_block=%d); the run was abandoned",
                   st.where, st.block, st.tile, st.kblock);
-    return fail(st.code == DEV_TIMEOUT ? GEMM_ERR_TIMEOUT : GEMM_ERR_CUDA, buf);
+    return fail(code == DEV_TIMEOUT ? GEMM_ERR_TIMEOUT : GEMM_ERR_CUDA, buf);
 }
 
 }  // namespace tg
