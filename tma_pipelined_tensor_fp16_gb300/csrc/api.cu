@@ -22,28 +22,10 @@ using namespace tg;
 
 namespace tg {
 
-namespace {
-std::mutex g_smem_mutex;
-std::vector<std::pair<const void*, unsigned>> g_smem_limits;
-}  // namespace
-
-bool smem_limit_known(const void* kernel, unsigned bytes)
+SmemLimits& smem_limits()
 {
-    std::lock_guard<std::mutex> lock(g_smem_mutex);
-    for (const auto& kv : g_smem_limits)
-        if (kv.first == kernel) return bytes <= kv.second;
-    return false;
-}
-
-void smem_limit_record(const void* kernel, unsigned bytes)
-{
-    std::lock_guard<std::mutex> lock(g_smem_mutex);
-    for (auto& kv : g_smem_limits)
-        if (kv.first == kernel) {
-            if (bytes > kv.second) kv.second = bytes;
-            return;
-        }
-    g_smem_limits.emplace_back(kernel, bytes);
+    static SmemLimits limits;
+    return limits;
 }
 
 }  // namespace tg

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "gemm_common.h"
+#include "smem_limits.h"
 
 namespace tg {
 
@@ -48,20 +49,22 @@ cudaError_t launch_ws(const LaunchSpec& s, cudaStream_t stream);
 // blocks of 64.
 cudaError_t launch_pair(const LaunchSpec& s, cudaStream_t stream);
 
-// Raise `kernel`'s dynamic shared-memory limit to at least `bytes`, calling
-// the runtime only when a larger limit than any set before for that kernel is
-// needed (the limit belongs to the kernel, for the whole process).
-bool smem_limit_known(const void* kernel, unsigned bytes);
-void smem_limit_record(const void* kernel, unsigned bytes);
+// Raise `kernel`'s dynamic shared-memory limit on the current device to at least
+// `bytes`, calling the runtime only when a larger limit than any set before for that
+// kernel on that device is needed.
+SmemLimits& smem_limits();  // of the process
 
 template <typename KernelT>
 cudaError_t ensure_smem_limit(KernelT kernel, unsigned bytes)
 {
     const void* key = reinterpret_cast<const void*>(kernel);
-    if (smem_limit_known(key, bytes)) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(bytes));
-    if (e == cudaSuccess) smem_limit_record(key, bytes);
+    int device = -1;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    if (smem_limits().known(device, key, bytes)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(bytes));
+    if (e == cudaSuccess) smem_limits().record(device, key, bytes);
     return e;
 }
 
