@@ -18,7 +18,11 @@ tma_pipelined_tensor_fp16_gb300.expert_layer`` runs them together.
 
 Argument checks and marshalling only; every operator runs in the library's CUDA
 kernels, asynchronously on the current stream of the tensors' device (or on
-``stream``), and writes into the tensor it is given or a new one.
+``stream``), and writes into the tensor it is given or a new one.  A new tensor is
+allocated on the stream that writes it, and with ``stream`` every tensor of the call
+is marked as used there, so that its memory is not handed out again too early; as
+everywhere in torch, the caller orders that stream behind the one that made the
+inputs.
 """
 from .binding import GEMM_OUT_F16, GEMM_OUT_F32, GemmError, _check, last_error, lib
 
@@ -54,10 +58,26 @@ def _tensor(name, t, shape, dtype, device=None):
     raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, device))
 
 
-def _output(name, t, shape, dtype, device):
+def _empty(shape, dtype, device, stream):
+    """A new tensor, of the memory of the stream that will write it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _output(name, t, shape, dtype, device, stream):
     if t is None:
-        return _torch().empty(shape, dtype=dtype, device=device)
+        return _empty(shape, dtype, device, stream)
     return _tensor(name, t, shape, dtype, device)
+
+
+def _used_on(stream, *tensors):
+    """Keep the memory of these tensors until the work now on `stream` is done."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _out_dtype(out):
@@ -74,7 +94,7 @@ def _ptr(t):
 
 def _call(fn, device, stream, *args):
     """fn(*args, stream) with `device` current, on `stream` or the device's
-    current stream.  Raises on an error status."""
+    current stream, whose handle is returned.  Raises on an error status."""
     torch = _torch()
     index = device.index
     if torch._C._cuda_getDevice() != index:  # the tensors have set CUDA up
@@ -88,6 +108,7 @@ def _call(fn, device, stream, *args):
     status = fn(*args, handle)
     if status != 0:
         _check(status)
+    return handle
 
 
 class ExpertRoute:
@@ -104,6 +125,7 @@ class ExpertRoute:
             raise ValueError("tokens must be >= 0, topk and experts >= 1")
         self.tokens, self.topk, self.experts = tokens, topk, experts
         self.offsets = self.order = self.position = None
+        self._home = None  # handle of the stream that the tables' memory belongs to
 
     @property
     def slots(self):
@@ -115,12 +137,25 @@ class ExpertRoute:
         _tensor("ids", ids, (self.tokens, self.topk), torch.int32)
         dev = ids.device
         if self.offsets is None or self.offsets.device != dev:
-            self.offsets = torch.empty(self.experts + 1, dtype=torch.int32, device=dev)
-            self.order = torch.empty(self.slots, dtype=torch.int32, device=dev)
-            self.position = torch.empty((self.tokens, self.topk), dtype=torch.int32, device=dev)
-        _call(lib().gemm_expert_sort, dev, stream, self.tokens, self.topk, self.experts, _ptr(ids),
-              _ptr(self.offsets), _ptr(self.order), _ptr(self.position))
+            self.offsets = _empty((self.experts + 1,), torch.int32, dev, stream)
+            self.order = _empty((self.slots,), torch.int32, dev, stream)
+            self.position = _empty((self.tokens, self.topk), torch.int32, dev, stream)
+            self._home = None
+        handle = _call(lib().gemm_expert_sort, dev, stream, self.tokens, self.topk, self.experts,
+                       _ptr(ids), _ptr(self.offsets), _ptr(self.order), _ptr(self.position))
+        if self._home is None:
+            self._home = handle
+        self._tables_used(handle, dev, stream, ids)
         return self
+
+    def _tables_used(self, handle, dev, stream, *tensors):
+        """After a launch on the stream of `handle`: the tables are the route's own, so
+        it keeps them for a stream that is not theirs; the call's tensors as always."""
+        if handle != self._home:
+            _used_on(stream or _torch().cuda.current_stream(dev), self.offsets, self.order,
+                     self.position)
+        if stream is not None:
+            _used_on(stream, *tensors)
 
     def load(self, offsets, order, position):
         """Take over a sorted routing made elsewhere; returns self."""
@@ -129,6 +164,7 @@ class ExpertRoute:
         _tensor("order", order, (self.slots,), torch.int32, offsets.device)
         _tensor("position", position, (self.tokens, self.topk), torch.int32, offsets.device)
         self.offsets, self.order, self.position = offsets, order, position
+        self._home = torch.cuda.current_stream(offsets.device).cuda_stream
         return self
 
     def _sorted_on(self):
@@ -143,9 +179,11 @@ class ExpertRoute:
         dev = self._sorted_on()
         width = X.shape[-1]
         _tensor("X", X, (self.tokens, width), torch.float16, dev)
-        Xs = _output("out", out, (self.slots, width), torch.float16, dev)
-        _call(lib().gemm_expert_gather, dev, stream, self.tokens, self.topk, self.experts, width,
-              _ptr(X), _ptr(self.offsets), _ptr(self.position), _ptr(Xs))
+        Xs = _output("out", out, (self.slots, width), torch.float16, dev, stream)
+        handle = _call(lib().gemm_expert_gather, dev, stream, self.tokens, self.topk,
+                       self.experts, width, _ptr(X), _ptr(self.offsets), _ptr(self.position),
+                       _ptr(Xs))
+        self._tables_used(handle, dev, stream, X, Xs)
         return Xs
 
     def combine(self, Ys, out=None, weights=None, stream=None):
@@ -168,10 +206,15 @@ class ExpertRoute:
         if weights is not None:
             _tensor("weights", weights, (self.tokens, self.topk), torch.float32, dev)
         dtype = torch.float32 if out is not None and out.dtype == torch.float32 else torch.float16
-        Y = _output("out", out, (self.tokens, width), dtype, dev)
-        _call(lib().gemm_expert_combine, dev, stream, self.tokens, self.topk, self.experts, width,
-              _ptr(Ys), _ptr(offsets), _ptr(position), _ptr(weights),
-              GEMM_OUT_F32 if dtype == torch.float32 else GEMM_OUT_F16, _ptr(Y))
+        Y = _output("out", out, (self.tokens, width), dtype, dev, stream)
+        handle = _call(lib().gemm_expert_combine, dev, stream, self.tokens, self.topk,
+                       self.experts, width, _ptr(Ys), _ptr(offsets), _ptr(position),
+                       _ptr(weights), GEMM_OUT_F32 if dtype == torch.float32 else GEMM_OUT_F16,
+                       _ptr(Y))
+        if position is not None:
+            self._tables_used(handle, dev, stream, Ys, weights, Y)
+        elif stream is not None:
+            _used_on(stream, Ys, weights, Y)
         return Y
 
     def gather_grad(self, dXs, out=None, stream=None):
@@ -187,11 +230,12 @@ class ExpertRoute:
         _tensor("dY", dY, (self.tokens, width), torch.float16, dev)
         _tensor("Ys", Ys, (self.slots, width), torch.float16, dev)
         _tensor("weights", weights, (self.tokens, self.topk), torch.float32, dev)
-        dYs = _output("out", out, (self.slots, width), torch.float16, dev)
-        dw = _output("dweights", dweights, (self.tokens, self.topk), torch.float32, dev)
-        _call(lib().gemm_expert_combine_grad, dev, stream, self.tokens, self.topk, self.experts,
-              width, _ptr(dY), _ptr(Ys), _ptr(self.offsets), _ptr(self.position),
-              _ptr(weights), _ptr(dYs), _ptr(dw))
+        dYs = _output("out", out, (self.slots, width), torch.float16, dev, stream)
+        dw = _output("dweights", dweights, (self.tokens, self.topk), torch.float32, dev, stream)
+        handle = _call(lib().gemm_expert_combine_grad, dev, stream, self.tokens, self.topk,
+                       self.experts, width, _ptr(dY), _ptr(Ys), _ptr(self.offsets),
+                       _ptr(self.position), _ptr(weights), _ptr(dYs), _ptr(dw))
+        self._tables_used(handle, dev, stream, dY, Ys, weights, dYs, dw)
         return dYs, dw
 
 
@@ -263,9 +307,11 @@ class GroupedPlan(_Handle):
         dev = P.device
         _tensor("Q", Q, sq, torch.float16, dev)
         _tensor("offsets", offsets, (self.experts + 1,), torch.int32, dev)
-        out = _output("out", out, so, self.dtype, dev)
+        out = _output("out", out, so, self.dtype, dev, stream)
         _call(lib().gemm_grouped_run, dev, stream, self._h, _ptr(P), _ptr(Q), _ptr(offsets),
               _ptr(out))
+        if stream is not None:
+            _used_on(stream, P, Q, offsets, out)
         return out
 
 
@@ -309,9 +355,11 @@ class W4Plan(_Handle):
             if ids.numel() != self.M:
                 raise ValueError("ids must hold one expert per row (%d)" % self.M)
             _tensor("ids", ids, ids.shape, torch.int32, dev)
-        Y = _output("out", out, (self.M, self.N), self.dtype, dev)
+        Y = _output("out", out, (self.M, self.N), self.dtype, dev, stream)
         _call(lib().gemm_w4_run, dev, stream, self._h, _ptr(X), _ptr(packed), _ptr(scales),
               _ptr(zeros), _ptr(ids), _ptr(Y))
+        if stream is not None:
+            _used_on(stream, X, packed, scales, zeros, ids, Y)
         return Y
 
 
