@@ -117,7 +117,9 @@ class ExpertRoute:
     ``offsets`` (experts + 1), ``order`` (tokens * topk: sorted row -> slot) and
     ``position`` (tokens x topk: slot -> sorted row) are int32 tensors, filled by
     ``sort`` or taken over by ``load``.  Dropped slots take the rows from
-    ``offsets[experts]`` on.
+    ``offsets[experts]`` on.  A further ``sort`` writes the tables of the one before
+    anew (so that a CUDA graph finds them in place), but never those of ``load``, which
+    are the caller's.
     """
 
     def __init__(self, tokens, topk, experts):
@@ -126,6 +128,7 @@ class ExpertRoute:
         self.tokens, self.topk, self.experts = tokens, topk, experts
         self.offsets = self.order = self.position = None
         self._home = None  # handle of the stream that the tables' memory belongs to
+        self._loaded = False
 
     @property
     def slots(self):
@@ -136,7 +139,8 @@ class ExpertRoute:
         torch = _torch()
         _tensor("ids", ids, (self.tokens, self.topk), torch.int32)
         dev = ids.device
-        if self.offsets is None or self.offsets.device != dev:
+        if self.offsets is None or self._loaded or self.offsets.device != dev:
+            self._loaded = False
             self.offsets = _empty((self.experts + 1,), torch.int32, dev, stream)
             self.order = _empty((self.slots,), torch.int32, dev, stream)
             self.position = _empty((self.tokens, self.topk), torch.int32, dev, stream)
@@ -165,6 +169,7 @@ class ExpertRoute:
         _tensor("position", position, (self.tokens, self.topk), torch.int32, offsets.device)
         self.offsets, self.order, self.position = offsets, order, position
         self._home = torch.cuda.current_stream(offsets.device).cuda_stream
+        self._loaded = True
         return self
 
     def _sorted_on(self):
