@@ -1,0 +1,25 @@
+"""The expert layer called again and at its edges."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def test_backward_twice():
+    import torch
+
+    from tma_pipelined_tensor_fp16_gb300 import expert_layer
+    layer = expert_layer.random_layer(4, 64, 128, 2)
+    X, ids, w = expert_layer.random_batch(50, 2, 4, 64)
+    Y, saved = layer.forward(X, ids, w)
+    first = layer.backward(Y, saved)
+    for a, b in zip(first, layer.backward(Y, saved)):
+        assert torch.equal(a, b)

@@ -45,10 +45,11 @@ class ExpertLayer:
         return Y, (route, Xs, H, A, Ys, weights)
 
     def backward(self, dY, saved):
-        """Gradients (dX, dweights, dW1, dW2); the weights' in fp32."""
+        """Gradients (dX, dweights, dW1, dW2); the weights' in fp32.  `saved` stays as
+        it is, so the same forward can be differentiated again."""
         route, Xs, H, A, Ys, weights = saved
         rows, I, W = Xs.shape[0], self.inner, self.width
-        dYs, dweights = route.combine_grad(dY, Ys, weights, out=Ys)  # in place of Ys
+        dYs, dweights = route.combine_grad(dY, Ys, weights)
         dW2 = self._plan(rows, W, I, "grad_weight", "f32")(dYs, A, route.offsets)
         dA = self._plan(rows, W, I, "grad_input")(dYs, self.W2, route.offsets)
         dH = dA.mul_(H > 0)
