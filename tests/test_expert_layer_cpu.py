@@ -20,3 +20,27 @@ def test_backward_leaves_what_forward_saved():
         assert torch.equal(t, b)
     for a, b in zip(first, layer.backward(Y, saved)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_masked_gradient_is_zero_whatever_it_was(value):
+    """One token's gradient is not finite: the units that its relu masks out get none
+    of it."""
+    layer, X, ids, w = layer_doubles.layer()
+    Y, saved = layer.forward(X, ids, w)
+    clean = layer.backward(Y, saved)
+    dY = Y.clone()
+    dY[2, 0] = value
+    _, _, dW1, _ = layer.backward(dY, saved)
+    route, _, H = saved[:3]
+    off = {(e, i): False for e in range(layer.experts) for i in range(layer.inner)}
+    for j in range(layer.topk):
+        e, row = int(ids[2, j]), int(route.position[2, j])
+        for i in range(layer.inner):
+            off[e, i] |= bool(H[row, i] > 0)
+    for (e, i), touched in off.items():
+        if not touched:
+            assert torch.isfinite(dW1[e, i]).all()
+        else:
+            assert not torch.isfinite(dW1[e, i]).all()
+    assert all(torch.isfinite(t).all() for t in clean)

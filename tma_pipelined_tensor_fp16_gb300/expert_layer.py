@@ -52,7 +52,7 @@ class ExpertLayer:
         dYs, dweights = route.combine_grad(dY, Ys, weights)
         dW2 = self._plan(rows, W, I, "grad_weight", "f32")(dYs, A, route.offsets)
         dA = self._plan(rows, W, I, "grad_input")(dYs, self.W2, route.offsets)
-        dH = dA.mul_(H > 0)
+        dH = dA.masked_fill_(H <= 0, 0.0)  # not a product: dA need not be finite there
         dW1 = self._plan(rows, I, W, "grad_weight", "f32")(dH, Xs, route.offsets)
         dXs = self._plan(rows, I, W, "grad_input")(dH, self.W1, route.offsets)
         return route.gather_grad(dXs), dweights, dW1, dW2
