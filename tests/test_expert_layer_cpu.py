@@ -44,3 +44,12 @@ def test_masked_gradient_is_zero_whatever_it_was(value):
         else:
             assert not torch.isfinite(dW1[e, i]).all()
     assert all(torch.isfinite(t).all() for t in clean)
+
+
+def test_pack_again_with_another_group():
+    layer, X, ids, w = layer_doubles.layer(width=128, inner=128)
+    want, _ = layer.forward(X, ids, w)
+    for group in (128, 32, 64, 128):
+        layer.pack(group=group)
+        got = layer.decode(X, ids, w)
+        assert (got - want).norm() < 0.4 * want.norm()

@@ -23,3 +23,14 @@ def test_backward_twice():
     first = layer.backward(Y, saved)
     for a, b in zip(first, layer.backward(Y, saved)):
         assert torch.equal(a, b)
+
+
+def test_pack_again_with_another_group():
+    from tma_pipelined_tensor_fp16_gb300 import expert_layer
+    layer = expert_layer.random_layer(4, 128, 256, 2)
+    X, ids, w = expert_layer.random_batch(3, 2, 4, 128)
+    want, _ = layer.forward(X, ids, w)
+    for group in (128, 32, 64, 128):
+        layer.pack(group=group)
+        got = layer.decode(X, ids, w)
+        assert (got.float() - want.float()).norm() < 0.4 * want.float().norm()

@@ -67,7 +67,7 @@ class ExpertLayer:
         tokens = X.shape[0]
         rows = tokens * self.topk
         group, (p1, s1, z1), (p2, s2, z2) = self._packed
-        key = ("w4", rows)
+        key = ("w4", rows, group)
         if key not in self._plans:
             self._plans[key] = (
                 W4Plan(rows, self.inner, self.width, group=group, experts=self.experts,
