@@ -53,3 +53,14 @@ def test_pack_again_with_another_group():
         layer.pack(group=group)
         got = layer.decode(X, ids, w)
         assert (got - want).norm() < 0.4 * want.norm()
+
+
+def test_no_tokens():
+    layer, X, ids, w = layer_doubles.layer()
+    layer.pack(group=32)
+    X, ids, w = X[:0], ids[:0], w[:0]
+    Y, saved = layer.forward(X, ids, w)
+    assert Y.shape == (0, 32)
+    dX, dw, dW1, dW2 = layer.backward(Y, saved)
+    assert dX.shape == (0, 32) and (dW1 == 0).all() and (dW2 == 0).all()
+    assert layer.decode(X, ids, w).shape == (0, 32)

@@ -34,3 +34,18 @@ def test_pack_again_with_another_group():
         layer.pack(group=group)
         got = layer.decode(X, ids, w)
         assert (got.float() - want.float()).norm() < 0.4 * want.float().norm()
+
+
+def test_no_tokens():
+    import torch
+
+    from tma_pipelined_tensor_fp16_gb300 import expert_layer
+    layer = expert_layer.random_layer(4, 64, 128, 2)
+    layer.pack(group=64)
+    X, ids, w = expert_layer.random_batch(3, 2, 4, 64)
+    X, ids, w = X[:0], ids[:0], w[:0]
+    Y, saved = layer.forward(X, ids, w)
+    dX, dw, dW1, dW2 = layer.backward(Y, saved)
+    torch.cuda.synchronize()
+    assert Y.shape == dX.shape == layer.decode(X, ids, w).shape == (0, 64)
+    assert (dW1 == 0).all() and (dW2 == 0).all()

@@ -66,6 +66,8 @@ class ExpertLayer:
         straight from its expert's codes."""
         tokens = X.shape[0]
         rows = tokens * self.topk
+        if tokens == 0:  # a plan has a row at least
+            return X.new_empty(X.shape)
         group, (p1, s1, z1), (p2, s2, z2) = self._packed
         key = ("w4", rows, group)
         if key not in self._plans:
