@@ -27,7 +27,7 @@ class Route:
         return rows
 
     def _sum(self, rows, weights, kept):
-        rows = rows.reshape(self.tokens, self.topk, -1)
+        rows = rows.reshape(self.tokens, self.topk, rows.shape[-1])
         if weights is not None:
             rows = rows * weights[:, :, None].to(rows.dtype)
         return torch.where(kept[:, :, None], rows, torch.zeros_like(rows)).sum(1)
