@@ -65,6 +65,14 @@ TMAGEMM_API int gemm_expert_combine(int64_t tokens, int topk, int experts, int64
                                     const int32_t* position, const float* weights, int dtype_out,
                                     void* Y, void* cuda_stream);
 
+/* As gemm_expert_combine for rows in slot order (row t * topk + j), as gemm_w4_run
+ * leaves them; needs no sort.  A slot whose entry in `expert_ids` is negative or >=
+ * experts is dropped, with the same meaning as there; expert_ids = NULL: none is. */
+TMAGEMM_API int gemm_expert_combine_slots(int64_t tokens, int topk, int experts, int64_t width,
+                                          const void* Ys, const int32_t* expert_ids,
+                                          const float* weights, int dtype_out, void* Y,
+                                          void* cuda_stream);
+
 /* Gradients of the weighted gemm_expert_combine, given dY (tokens x width fp16):
  *   dYs[position[s]] = weights[s] * dY[t]               (fp16, every row written)
  *   dweights[s]      = sum_c dY[t][c] * Ys[position[s]][c]   (fp32)

@@ -64,3 +64,17 @@ def test_no_tokens():
     dX, dw, dW1, dW2 = layer.backward(Y, saved)
     assert dX.shape == (0, 32) and (dW1 == 0).all() and (dW2 == 0).all()
     assert layer.decode(X, ids, w).shape == (0, 32)
+
+
+def test_decode_ignores_what_a_dropped_slot_holds():
+    """As forward does: a routing weight that is not a number counts for nothing there."""
+    layer, X, ids, w = layer_doubles.layer()
+    layer.pack(group=32)
+    ids[0, 1], ids[3] = -1, layer.experts
+    clean = layer.decode(X, ids, w)
+    w = w.clone()
+    w[0, 1] = w[3, 0] = float("nan")
+    w[3, 1] = float("inf")
+    assert torch.equal(layer.decode(X, ids, w), clean)
+    assert (clean[3] == 0).all()
+    assert torch.isfinite(layer.forward(X, ids, w)[0]).all()

@@ -49,3 +49,18 @@ def test_no_tokens():
     torch.cuda.synchronize()
     assert Y.shape == dX.shape == layer.decode(X, ids, w).shape == (0, 64)
     assert (dW1 == 0).all() and (dW2 == 0).all()
+
+
+def test_decode_ignores_what_a_dropped_slot_holds():
+    import torch
+
+    from tma_pipelined_tensor_fp16_gb300 import expert_layer
+    layer = expert_layer.random_layer(4, 128, 256, 3)
+    layer.pack(group=64)
+    X, ids, w = expert_layer.random_batch(5, 3, 4, 128)
+    ids[0, 1], ids[3] = -1, 4
+    clean = layer.decode(X, ids, w)
+    w[0, 1] = w[3, 0] = float("nan")
+    w[3, 1] = float("inf")
+    assert torch.equal(layer.decode(X, ids, w), clean)
+    assert torch.isfinite(clean).all() and (clean[3] == 0).all()

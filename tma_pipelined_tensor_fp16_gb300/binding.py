@@ -88,6 +88,9 @@ _SIGS = {
                            + [ctypes.c_void_p] * 5),
     "gemm_expert_combine": (ctypes.c_int, [ctypes.c_int64] + [ctypes.c_int] * 2 + [ctypes.c_int64]
                             + [ctypes.c_void_p] * 4 + [ctypes.c_int] + [ctypes.c_void_p] * 2),
+    "gemm_expert_combine_slots": (ctypes.c_int, [ctypes.c_int64] + [ctypes.c_int] * 2
+                                  + [ctypes.c_int64] + [ctypes.c_void_p] * 3 + [ctypes.c_int]
+                                  + [ctypes.c_void_p] * 2),
     "gemm_expert_combine_grad": (ctypes.c_int, [ctypes.c_int64] + [ctypes.c_int] * 2
                                  + [ctypes.c_int64] + [ctypes.c_void_p] * 8),
     "gemm_grouped_create_plan": (ctypes.c_void_p, [ctypes.c_int64] * 3 + [ctypes.c_int] * 3),

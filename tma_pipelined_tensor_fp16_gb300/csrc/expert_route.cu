@@ -193,10 +193,11 @@ __global__ void __launch_bounds__(1024, 1)
 // TB/s).
 
 struct RowMap {
-    const int32_t* offsets;   // nullptr: slot order, none dropped
-    const int32_t* position;
+    const int32_t* offsets;
+    const int32_t* position;  // nullptr: slot order
     int experts;
     int64_t slots;
+    const int32_t* ids;       // slot order: the slots' experts, or nullptr: none is dropped
 };
 
 // Rows that belong to an expert: [0, kept).
@@ -209,8 +210,10 @@ __device__ __forceinline__ uint32_t kept_rows(const RowMap& m)
 
 __device__ __forceinline__ uint32_t row_of(const RowMap& m, int64_t slot)
 {
-    return m.position == nullptr ? static_cast<uint32_t>(slot)
-                                 : static_cast<uint32_t>(m.position[slot]);
+    if (m.position != nullptr) return static_cast<uint32_t>(m.position[slot]);
+    if (m.ids != nullptr && static_cast<unsigned>(m.ids[slot]) >= static_cast<unsigned>(m.experts))
+        return 0xffffffffu;  // dropped
+    return static_cast<uint32_t>(slot);
 }
 
 __global__ void __launch_bounds__(256)
@@ -449,6 +452,43 @@ RowGrid row_grid(int64_t tokens, int chunks, int sms)
     return g;
 }
 
+// Both forms of the combination: by `position`, or in slot order (position = nullptr)
+// with the slots' expert ids or without.
+int combine_rows(int64_t tokens, int topk, int experts, int64_t width, const void* Ys,
+                 const int32_t* offsets, const int32_t* position, const int32_t* ids,
+                 const float* weights, int dtype_out, void* Y, void* cuda_stream)
+{
+    return guarded([&] {
+        int r = check_slots(tokens, topk, experts);
+        if (r == GEMM_OK) r = check_width(width);
+        if (r != GEMM_OK) return r;
+        if (dtype_out != GEMM_OUT_F32 && dtype_out != GEMM_OUT_F16)
+            return fail(GEMM_ERR_INVALID_ARG,
+                        "dtype_out must be GEMM_OUT_F32 (0) or GEMM_OUT_F16 (1)");
+        if (tokens == 0) return ok();
+        if (!Ys || !Y || (position && !offsets)) return fail(GEMM_ERR_INVALID_ARG, "NULL pointer");
+        if (!aligned16(Ys) || !aligned16(Y))
+            return fail(GEMM_ERR_UNSUPPORTED, "Ys and Y must be 16-byte aligned");
+        int dev, sms;
+        r = require_device(&dev, &sms, nullptr);
+        if (r != GEMM_OK) return r;
+        const int chunks = static_cast<int>(width / 8);
+        const RowGrid g = row_grid(tokens, chunks, sms);
+        if (g.grid.y > 65535u) return fail(GEMM_ERR_UNSUPPORTED, "width is too large");
+        const RowMap map = {offsets, position, experts, tokens * topk, ids};
+        const bool f16 = dtype_out == GEMM_OUT_F16;
+        const int64_t blocks = static_cast<int64_t>(g.grid.x) * g.grid.y;
+        const int batch = slot_batch(topk, blocks <= 2 * sms);
+        auto kernel = batch == 2   ? (f16 ? k_expert_combine<true, 2> : k_expert_combine<false, 2>)
+                      : batch == 4 ? (f16 ? k_expert_combine<true, 4> : k_expert_combine<false, 4>)
+                                   : (f16 ? k_expert_combine<true, 8> : k_expert_combine<false, 8>);
+        cudaError_t e = launch_dependent(kernel, g.grid, g.block, 0, 1,
+                                         static_cast<cudaStream_t>(cuda_stream), tokens, topk,
+                                         chunks, map, static_cast<const uint4*>(Ys), weights, Y);
+        return e == cudaSuccess ? ok() : cuda_fail("expert combine launch", e);
+    });
+}
+
 }  // namespace
 
 }  // namespace tg
@@ -506,7 +546,7 @@ int gemm_expert_gather(int64_t tokens, int topk, int experts, int64_t width, con
         const int chunks = static_cast<int>(width / 8);
         const RowGrid g = row_grid(tokens, chunks, sms);
         if (g.grid.y > 65535u) return fail(GEMM_ERR_UNSUPPORTED, "width is too large");
-        const RowMap map = {offsets, position, experts, tokens * topk};
+        const RowMap map = {offsets, position, experts, tokens * topk, nullptr};
         cudaError_t e = launch_dependent(k_expert_gather, g.grid, g.block, 0, 1,
                                          static_cast<cudaStream_t>(cuda_stream), tokens, topk,
                                          chunks, map, static_cast<const uint4*>(X),
@@ -519,35 +559,16 @@ int gemm_expert_combine(int64_t tokens, int topk, int experts, int64_t width, co
                         const int32_t* offsets, const int32_t* position, const float* weights,
                         int dtype_out, void* Y, void* cuda_stream)
 {
-    return guarded([&] {
-        int r = check_slots(tokens, topk, experts);
-        if (r == GEMM_OK) r = check_width(width);
-        if (r != GEMM_OK) return r;
-        if (dtype_out != GEMM_OUT_F32 && dtype_out != GEMM_OUT_F16)
-            return fail(GEMM_ERR_INVALID_ARG,
-                        "dtype_out must be GEMM_OUT_F32 (0) or GEMM_OUT_F16 (1)");
-        if (tokens == 0) return ok();
-        if (!Ys || !Y || (position && !offsets)) return fail(GEMM_ERR_INVALID_ARG, "NULL pointer");
-        if (!aligned16(Ys) || !aligned16(Y))
-            return fail(GEMM_ERR_UNSUPPORTED, "Ys and Y must be 16-byte aligned");
-        int dev, sms;
-        r = require_device(&dev, &sms, nullptr);
-        if (r != GEMM_OK) return r;
-        const int chunks = static_cast<int>(width / 8);
-        const RowGrid g = row_grid(tokens, chunks, sms);
-        if (g.grid.y > 65535u) return fail(GEMM_ERR_UNSUPPORTED, "width is too large");
-        const RowMap map = {offsets, position, experts, tokens * topk};
-        const bool f16 = dtype_out == GEMM_OUT_F16;
-        const int64_t blocks = static_cast<int64_t>(g.grid.x) * g.grid.y;
-        const int batch = slot_batch(topk, blocks <= 2 * sms);
-        auto kernel = batch == 2   ? (f16 ? k_expert_combine<true, 2> : k_expert_combine<false, 2>)
-                      : batch == 4 ? (f16 ? k_expert_combine<true, 4> : k_expert_combine<false, 4>)
-                                   : (f16 ? k_expert_combine<true, 8> : k_expert_combine<false, 8>);
-        cudaError_t e = launch_dependent(kernel, g.grid, g.block, 0, 1,
-                                         static_cast<cudaStream_t>(cuda_stream), tokens, topk,
-                                         chunks, map, static_cast<const uint4*>(Ys), weights, Y);
-        return e == cudaSuccess ? ok() : cuda_fail("expert combine launch", e);
-    });
+    return combine_rows(tokens, topk, experts, width, Ys, offsets, position, nullptr, weights,
+                        dtype_out, Y, cuda_stream);
+}
+
+int gemm_expert_combine_slots(int64_t tokens, int topk, int experts, int64_t width, const void* Ys,
+                              const int32_t* expert_ids, const float* weights, int dtype_out,
+                              void* Y, void* cuda_stream)
+{
+    return combine_rows(tokens, topk, experts, width, Ys, nullptr, nullptr, expert_ids, weights,
+                        dtype_out, Y, cuda_stream);
 }
 
 int gemm_expert_combine_grad(int64_t tokens, int topk, int experts, int64_t width, const void* dY,
@@ -567,7 +588,7 @@ int gemm_expert_combine_grad(int64_t tokens, int topk, int experts, int64_t widt
         r = require_device(&dev, &sms, nullptr);
         if (r != GEMM_OK) return r;
         const int chunks = static_cast<int>(width / 8);
-        const RowMap map = {offsets, position, experts, tokens * topk};
+        const RowMap map = {offsets, position, experts, tokens * topk, nullptr};
         int wpt = 1;
         while (wpt < 8 && chunks > 32 * wpt) wpt *= 2;
         const int64_t blocks = (tokens + 8 / wpt - 1) / (8 / wpt);

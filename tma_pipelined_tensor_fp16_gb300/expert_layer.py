@@ -78,7 +78,8 @@ class ExpertLayer:
         up, down = self._plans[key]
         A = up(X, p1, s1, zeros=z1, ids=ids).relu_()
         Ys = down(A, p2, s2, zeros=z2, ids=ids)
-        return ExpertRoute(tokens, self.topk, self.experts).combine_slots(Ys, weights=weights)
+        return ExpertRoute(tokens, self.topk, self.experts).combine_slots(
+            Ys, weights=weights, ids=ids)
 
 
 def random_layer(experts, width, inner, topk, seed=0):

@@ -196,15 +196,29 @@ class ExpertRoute:
         not dropped (a plain sum without `weights`).  `out` is fp16 or fp32
         (fp16 when not given)."""
         dev = self._sorted_on()
-        return self._combine(dev, Ys, out, weights, self.offsets, self.position, stream)
+        Y, code = self._combine_output(dev, Ys, out, weights, stream)
+        handle = _call(lib().gemm_expert_combine, dev, stream, self.tokens, self.topk,
+                       self.experts, Ys.shape[-1], _ptr(Ys), _ptr(self.offsets),
+                       _ptr(self.position), _ptr(weights), code, _ptr(Y))
+        self._tables_used(handle, dev, stream, Ys, weights, Y)
+        return Y
 
-    def combine_slots(self, Ys, out=None, weights=None, stream=None):
+    def combine_slots(self, Ys, out=None, weights=None, ids=None, stream=None):
         """As ``combine`` for rows in slot order (row t * topk + j), as W4Plan
-        leaves them; needs no sort.  No slot counts as dropped."""
+        leaves them; needs no sort.  Slots that `ids` (tokens x topk) drops take no
+        part, neither their rows nor their weights; without `ids` none is dropped."""
         dev = Ys.device
-        return self._combine(dev, Ys, out, weights, None, None, stream)
+        if ids is not None:
+            _tensor("ids", ids, (self.tokens, self.topk), _torch().int32, dev)
+        Y, code = self._combine_output(dev, Ys, out, weights, stream)
+        _call(lib().gemm_expert_combine_slots, dev, stream, self.tokens, self.topk, self.experts,
+              Ys.shape[-1], _ptr(Ys), _ptr(ids), _ptr(weights), code, _ptr(Y))
+        if stream is not None:
+            _used_on(stream, Ys, ids, weights, Y)
+        return Y
 
-    def _combine(self, dev, Ys, out, weights, offsets, position, stream):
+    def _combine_output(self, dev, Ys, out, weights, stream):
+        """The output and its type's code; checks the operands."""
         torch = _torch()
         width = Ys.shape[-1]
         _tensor("Ys", Ys, (self.slots, width), torch.float16, dev)
@@ -212,15 +226,7 @@ class ExpertRoute:
             _tensor("weights", weights, (self.tokens, self.topk), torch.float32, dev)
         dtype = torch.float32 if out is not None and out.dtype == torch.float32 else torch.float16
         Y = _output("out", out, (self.tokens, width), dtype, dev, stream)
-        handle = _call(lib().gemm_expert_combine, dev, stream, self.tokens, self.topk,
-                       self.experts, width, _ptr(Ys), _ptr(offsets), _ptr(position),
-                       _ptr(weights), GEMM_OUT_F32 if dtype == torch.float32 else GEMM_OUT_F16,
-                       _ptr(Y))
-        if position is not None:
-            self._tables_used(handle, dev, stream, Ys, weights, Y)
-        elif stream is not None:
-            _used_on(stream, Ys, weights, Y)
-        return Y
+        return Y, GEMM_OUT_F32 if dtype == torch.float32 else GEMM_OUT_F16
 
     def gather_grad(self, dXs, out=None, stream=None):
         """Gradient of ``gather`` with respect to X: the sum of a token's rows."""
