@@ -104,9 +104,10 @@ typedef enum {
 /* Plan for `rows` rows (an upper bound is fixed by the tensors, the split over
  * experts is read from `offsets` on the device at every run).  rows >= 0,
  * 1 <= experts <= 1024, N and K multiples of 8, all below 2^31 (and experts * N
- * too).  Returns NULL on error.  The plan owns a device record of 40 bytes (its
- * status and the counter from which a run hands out its tiles), so runs of one
- * plan must not overlap on the GPU. */
+ * too).  Returns NULL on error.  The plan owns a device record of 32 KB: its status and
+ * the counters from which runs hand out their tiles, one for every stream and every
+ * captured launch.  So runs of one plan may overlap on the GPU, on several streams,
+ * from several threads, and with replays of graphs that hold runs of it. */
 TMAGEMM_API gemm_grouped_plan* gemm_grouped_create_plan(int64_t rows, int64_t N, int64_t K,
                                                         int experts, int op, int dtype_out);
 

@@ -5,9 +5,11 @@
 #include <algorithm>
 #include <cstdio>
 #include <cstring>
+#include <memory>
 #include <new>
 
 #include "../../include/tmaexperts.h"
+#include "counter_slots.h"
 #include "runtime.h"
 
 using namespace tg;
@@ -20,8 +22,8 @@ struct gemm_grouped_plan {
     int block_m, block_n, grid, pipe_depth;
     unsigned smem_bytes;
     int tiles_m, tiles_n;
-    DevStatus* d_status;
-    int epoch;
+    DevStatus* d_status;  // and the counters behind it
+    std::shared_ptr<CounterSlots> slots;  // graphs that captured a run hold it too
     char desc[256];
 };
 
@@ -146,6 +148,59 @@ int check_grouped(int64_t rows, int64_t N, int64_t K, int experts, int op, int d
     return GEMM_OK;
 }
 
+// A captured launch's hold on its counter, which ends with the graph.
+struct CapturedSlot {
+    std::shared_ptr<CounterSlots> slots;
+    int slot;
+};
+
+void CUDART_CB release_captured(void* p)
+{
+    CapturedSlot* held = static_cast<CapturedSlot*>(p);
+    held->slots->release(held->slot);
+    delete held;
+}
+
+// The tile counter of a run on `stream` (see counter_slots.h).
+int counter_of(const gemm_grouped_plan& plan, cudaStream_t stream, int* slot)
+{
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(stream, &status);
+    if (e != cudaSuccess) return cuda_fail("cudaStreamIsCapturing", e);
+    if (status != cudaStreamCaptureStatusActive) {
+        unsigned long long id = 0;
+        e = cudaStreamGetId(stream, &id);
+        if (e != cudaSuccess) return cuda_fail("cudaStreamGetId", e);
+        bool taken_over = false;
+        *slot = plan.slots->of_stream(id, &taken_over);
+        if (taken_over) e = cudaDeviceSynchronize();
+        if (e == cudaSuccess) return GEMM_OK;
+        plan.slots->give_up(*slot);
+        return cuda_fail("cudaDeviceSynchronize", e);
+    }
+    std::unique_ptr<CapturedSlot> held(new CapturedSlot{plan.slots, plan.slots->of_capture()});
+    *slot = held->slot;
+    if (held->slot < 0)
+        return fail(GEMM_ERR_UNSUPPORTED, "too many live CUDA graphs hold runs of this plan");
+    cudaGraph_t graph = nullptr;
+    cudaUserObject_t object = nullptr;
+    e = cudaStreamGetCaptureInfo(stream, &status, nullptr, &graph, nullptr, nullptr, nullptr);
+    if (e == cudaSuccess)
+        e = cudaUserObjectCreate(&object, held.get(), release_captured, 1,
+                                 cudaUserObjectNoDestructorSync);
+    if (e != cudaSuccess) {
+        plan.slots->release(*slot);
+        return cuda_fail("tying a tile counter to the graph", e);
+    }
+    held.release();  // the object's now
+    e = cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove);
+    if (e != cudaSuccess) {
+        cudaUserObjectRelease(object, 1);
+        return cuda_fail("tying a tile counter to the graph", e);
+    }
+    return GEMM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -222,10 +277,12 @@ gemm_grouped_plan* gemm_grouped_create_plan_ex(int64_t rows, int64_t N, int64_t 
                       static_cast<long long>(K), experts, p.block_m, p.block_n,
                       p.pair ? 2 * BLK_K : BLK_K, p.pipe_depth,
                       p.smem_bytes, p.grid, dtype_out == GEMM_OUT_F16 ? "f16" : "f32");
-        // the status record and, behind it, the counter
-        cudaError_t e = cudaMalloc(&p.d_status, sizeof(DevStatus) + sizeof(unsigned long long));
-        if (e == cudaSuccess)
-            e = cudaMemset(p.d_status, 0, sizeof(DevStatus) + sizeof(unsigned long long));
+        p.slots = std::make_shared<CounterSlots>();
+        // the status record and, behind it, the counters
+        constexpr size_t RECORD =
+            sizeof(DevStatus) + CounterSlots::COUNT * sizeof(unsigned long long);
+        cudaError_t e = cudaMalloc(&p.d_status, RECORD);
+        if (e == cudaSuccess) e = cudaMemset(p.d_status, 0, RECORD);
         if (e != cudaSuccess) {
             if (p.d_status) cudaFree(p.d_status);
             return cuda_fail("allocating the device status record", e);
@@ -317,9 +374,11 @@ int gemm_grouped_run(gemm_grouped_plan* plan, const void* P, const void* Q,
         p.offsets = offsets;
         p.out = out;
         p.status = plan->d_status;
-        p.counter = reinterpret_cast<unsigned long long*>(plan->d_status + 1);
-        if (++plan->epoch <= 0) plan->epoch = 1;
-        p.epoch = plan->epoch;
+        int slot = -1;
+        r = counter_of(*plan, stream, &slot);
+        if (r != GEMM_OK) return r;
+        p.counter = reinterpret_cast<unsigned long long*>(plan->d_status + 1) + slot;
+        p.epoch = plan->slots->next_epoch();
         p.budget_ns = 2000ull * 1000000ull;
         e = launch_grouped(s, stream);
         return e == cudaSuccess ? ok() : cuda_fail("grouped product launch", e);

@@ -1036,7 +1036,7 @@ struct gemm_w4_plan {
     int length_ctas;  // CTAs that share a row's length
     int tile_rows;    // rows of the weights per CTA
     DevStatus* d_status;
-    int epoch;
+    unsigned epoch;
     void* d_weights;  // N x 2 K fp16 (rounded: N x K)
     void* d_x;        // M x 2 K fp16
     int* d_verdicts;  // one per CTA of the expansion
@@ -1099,8 +1099,8 @@ int run_rows(gemm_w4_plan* plan, const void* X, const void* packed, const void* 
     p.verdicts = verdicts > 0 ? plan->d_verdicts : nullptr;
     p.verdict_count = verdicts;
     p.status = plan->d_status;
-    if (++plan->epoch <= 0) plan->epoch = 1;
-    p.epoch = plan->epoch;
+    // threads may run one plan at a time of their own; any number above 0 will do
+    p.epoch = static_cast<int>(__atomic_add_fetch(&plan->epoch, 1u, __ATOMIC_RELAXED) % 0x7fffffffu) + 1;
     p.budget_ns = 2000ull * 1000000ull;
     CUtensorMap codes, x;
     int r = encode_rows(&codes, "packed", CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, packed, plan->K / 2,

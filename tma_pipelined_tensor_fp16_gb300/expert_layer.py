@@ -18,7 +18,11 @@ from .experts import ExpertRoute, GroupedPlan, W4Plan, w4_pack
 
 
 class ExpertLayer:
-    """W1 is experts x inner x width, W2 experts x width x inner (fp16)."""
+    """W1 is experts x inner x width, W2 experts x width x inner (fp16).
+
+    Calls may come on several streams and from several threads, and graphs that
+    captured them may be replayed beside them: none of the plans that the layer keeps
+    minds runs that overlap."""
 
     def __init__(self, W1, W2, topk):
         self.W1, self.W2, self.topk = W1, W2, topk

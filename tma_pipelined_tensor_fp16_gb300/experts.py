@@ -337,6 +337,8 @@ class W4Plan(_Handle):
     Many rows are multiplied as fp16 matrices: with ``weights="exact"`` each weight
     as the sum of two fp16 numbers, with ``"rounded"`` rounded to one (half the
     work; the result is off by up to half a unit in the last place of each weight).
+    The matrices are the plan's, so runs of a plan whose description says ``expand``
+    must not overlap on the GPU (streams, threads, graph replays): one plan for each.
     """
     _destroy, _describe, _status = "gemm_w4_destroy", "gemm_w4_describe", "gemm_w4_get_device_status"
 
