@@ -53,6 +53,7 @@ int ok()
 
 int cuda_fail(const char* what, cudaError_t e)
 {
+    cudaGetLastError();  // reported here; whoever looks at the last error next did not cause it
     return fail(GEMM_ERR_CUDA, std::string(what) + ": " + cudaGetErrorName(e) + " (" +
                                    cudaGetErrorString(e) + ")");
 }
