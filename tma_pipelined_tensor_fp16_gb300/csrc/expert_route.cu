@@ -4,11 +4,14 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <mutex>
+#include <vector>
 
 #include "../../include/tmaexperts.h"
 #include "launch.h"
 #include "ptx.cuh"
 #include "runtime.h"
+#include "sort_shape.h"
 
 namespace tg {
 
@@ -33,8 +36,6 @@ namespace {
 // each (131072 slots of 128 experts: 11.0 us on 16 CTAs, 21.2 on 8; 128 slots: 2.6 us
 // on one).
 constexpr int SORT_MAX_EXPERTS = 1024;
-constexpr int SORT_CTAS = 16;         // more than the portable 8
-constexpr int SORT_CTA_SLOTS = 1024;  // slots for which another CTA pays
 // Slots per warp from which equal keys are found bit by bit.  The match
 // instruction answers sooner (128 slots per warp in one CTA: 4.0 against 4.9 us)
 // but few at a time (131072 slots of 128 experts: 13.4 against 10.7 us).
@@ -452,6 +453,46 @@ RowGrid row_grid(int64_t tokens, int chunks, int sms)
     return g;
 }
 
+// Whether a cluster of SORT_CTAS fits the device (a GPC may have fewer SMs to spare than
+// that, and with many experts each takes a CTA's worth of shared memory), asked of the
+// runtime once for every size that earlier answers do not cover.
+cudaError_t large_sort_cluster_fits(int dev, unsigned smem, bool* fits)
+{
+    struct Answer {
+        unsigned fits, fails;  // the largest size that does, the smallest that does not
+    };
+    static std::mutex mutex;
+    static std::vector<Answer> answers;
+    std::lock_guard<std::mutex> lock(mutex);
+    if (answers.size() <= static_cast<size_t>(dev)) answers.resize(dev + 1, Answer{0u, ~0u});
+    Answer& a = answers[dev];
+    if (smem > a.fits && smem < a.fails) {
+        cudaError_t e =
+            cudaFuncSetAttribute(k_expert_sort, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(SORT_CTAS);
+        cfg.blockDim = dim3(1024);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = SORT_CTAS;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        e = cudaOccupancyMaxActiveClusters(&clusters, k_expert_sort, &cfg);
+        if (e != cudaSuccess) return e;
+        if (clusters > 0)
+            a.fits = smem;
+        else
+            a.fails = smem;
+    }
+    *fits = smem <= a.fits;
+    return cudaSuccess;
+}
+
 // Both forms of the combination: by `position`, or in slot order (position = nullptr)
 // with the slots' expert ids or without.
 int combine_rows(int64_t tokens, int topk, int experts, int64_t width, const void* Ys,
@@ -509,21 +550,21 @@ int gemm_expert_sort(int64_t tokens, int topk, int experts, const int32_t* exper
         int dev, sms, smem_optin;
         r = require_device(&dev, &sms, &smem_optin);
         if (r != GEMM_OK) return r;
-        int ctas = 1;
-        while (ctas < SORT_CTAS && slots > static_cast<int64_t>(SORT_CTA_SLOTS) * ctas) ctas *= 2;
-        int warps = 32;
-        while (warps > 8 && slots <= static_cast<int64_t>(warps) * 32 * ctas) warps /= 2;
-        const int64_t per_warp = (slots + ctas * warps - 1) / (ctas * warps);
-        const int run = static_cast<int>((per_warp + 31) / 32 * 32);
-        const unsigned smem = static_cast<unsigned>(((warps + 2) * (experts + 1) + 33) * 4);
-        cudaError_t e = cudaSuccess;
-        if (ctas > 8)
-            e = cudaFuncSetAttribute(k_expert_sort, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e == cudaSuccess) e = ensure_smem_limit(k_expert_sort, smem);
+        SortShape s = sort_shape(slots, SORT_CTAS);
+        cudaError_t e = ensure_smem_limit(k_expert_sort, s.smem_bytes(experts));
+        if (e == cudaSuccess && s.ctas > SORT_PORTABLE_CTAS) {
+            bool fits = false;
+            e = large_sort_cluster_fits(dev, s.smem_bytes(experts), &fits);
+            if (e == cudaSuccess && !fits) {
+                s = sort_shape(slots, SORT_PORTABLE_CTAS);
+                e = ensure_smem_limit(k_expert_sort, s.smem_bytes(experts));
+            }
+        }
         if (e == cudaSuccess)
-            e = launch_dependent(k_expert_sort, dim3(ctas), dim3(warps * 32), smem, ctas,
+            e = launch_dependent(k_expert_sort, dim3(s.ctas), dim3(s.warps * 32),
+                                 s.smem_bytes(experts), s.ctas,
                                  static_cast<cudaStream_t>(cuda_stream), static_cast<int>(slots),
-                                 experts, run, expert_ids, offsets, order, position);
+                                 experts, s.run, expert_ids, offsets, order, position);
         return e == cudaSuccess ? ok() : cuda_fail("expert sort launch", e);
     });
 }
