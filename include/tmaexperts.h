@@ -103,8 +103,8 @@ typedef enum {
 
 /* Plan for `rows` rows (an upper bound is fixed by the tensors, the split over
  * experts is read from `offsets` on the device at every run).  rows >= 0,
- * 1 <= experts <= 1024, N and K multiples of 8, all below 2^31 (and experts * N
- * too).  Returns NULL on error.  The plan owns a device record of 32 KB: its status and
+ * 1 <= experts <= 1024, N and K multiples of 8, all at most 2^31 - 65536 (and
+ * experts * N too).  Returns NULL on error.  The plan owns a device record of 32 KB: its status and
  * the counters from which runs hand out their tiles, one for every stream and every
  * captured launch.  So runs of one plan may overlap on the GPU, on several streams,
  * from several threads, and with replays of graphs that hold runs of it. */
@@ -149,7 +149,8 @@ typedef struct gemm_w4_plan gemm_w4_plan; /* opaque; owned by the library */
  *   zeros  : N x K/group uint8 zero points, or NULL for 8 everywhere
  *   X      : M x K fp16      Y : M x N of dtype_out
  *
- * group is 32, 64 or 128, K a multiple of group, N of 8 (fp16) or 4 (fp32).
+ * group is 32, 64 or 128, K a multiple of group, N of 8 (fp16) or 4 (fp32); all are at
+ * most 2^31 - 65536, and experts * N too.
  * No weight is rounded, whatever the number of rows.  Up to 64 rows, and above where
  * that is expected to be faster, q - zero enters the tensor cores as the integer
  * it is, each group is summed in fp32 and scaled there ("rows" in gemm_w4_describe).

@@ -131,9 +131,10 @@ int64_t out_cols_of(const gemm_grouped_plan& p)
 
 int check_grouped(int64_t rows, int64_t N, int64_t K, int experts, int op, int dtype)
 {
-    const int64_t LIM = (int64_t(1) << 31) - 1;
+    const int64_t LIM = MAX_COORDINATE;
     if (rows < 0 || N < 1 || K < 1 || rows > LIM || N > LIM || K > LIM)
-        return fail(GEMM_ERR_INVALID_ARG, "rows must be in [0, 2^31-1], N and K in [1, 2^31-1]");
+        return fail(GEMM_ERR_INVALID_ARG,
+                    "rows must be in [0, 2^31-65536], N and K in [1, 2^31-65536]");
     if (experts < 1 || experts > GROUPED_MAX_EXPERTS)
         return fail(GEMM_ERR_INVALID_ARG, "experts must be in 1..1024");
     if (op < GROUPED_FORWARD || op > GROUPED_GRAD_WEIGHT)

@@ -58,6 +58,10 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, u
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
+// The largest size of a dimension in the expert-layer operators: a coordinate plus the
+// width of a tile or the stages in flight stays within 32 bits.
+constexpr int64_t MAX_COORDINATE = (int64_t(1) << 31) - 65536;
+
 inline bool aligned16(const void* p)
 {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;

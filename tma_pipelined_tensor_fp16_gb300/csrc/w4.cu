@@ -1146,9 +1146,9 @@ gemm_w4_plan* gemm_w4_create_plan_ex(int64_t M, int64_t N, int64_t K, int group,
 {
     gemm_w4_plan* plan = nullptr;
     guarded([&] {
-        const int64_t LIM = (int64_t(1) << 31) - 1;
-        if (M < 1 || N < 1 || K < 1 || M > LIM || N > LIM || K > LIM - 65536)
-            return fail(GEMM_ERR_INVALID_ARG, "M, N, K must be in [1, 2^31-1]");
+        const int64_t LIM = MAX_COORDINATE;
+        if (M < 1 || N < 1 || K < 1 || M > LIM || N > LIM || K > LIM)
+            return fail(GEMM_ERR_INVALID_ARG, "M, N, K must be in [1, 2^31-65536]");
         if (group != 32 && group != 64 && group != 128)
             return fail(GEMM_ERR_INVALID_ARG, "group must be 32, 64 or 128");
         if (dtype_out != GEMM_OUT_F32 && dtype_out != GEMM_OUT_F16)
