@@ -128,7 +128,8 @@ TMAGEMM_API gemm_grouped_plan* gemm_grouped_create_plan_ex(int64_t rows, int64_t
 /* Enqueue the product.  `offsets` (experts + 1 int32, device memory) is as
  * gemm_expert_sort writes it: ascending from 0 to at most rows.  Values outside
  * [0, rows] are taken as the nearest bound, so a bad table gives wrong rows but
- * no access out of range. */
+ * no access out of range; with one that descends no row belongs to an expert in
+ * FORWARD and GRAD_INPUT. */
 TMAGEMM_API int gemm_grouped_run(gemm_grouped_plan* plan, const void* P, const void* Q,
                                  const int32_t* offsets, void* out, void* cuda_stream);
 

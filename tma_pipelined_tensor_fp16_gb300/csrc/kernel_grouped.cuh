@@ -216,7 +216,9 @@ __device__ __forceinline__ void grouped_order(const GroupedParams& p, int* row0,
 
 // First row and first tile of BM rows of the experts and of the rest, by all
 // threads of the CTA: each sums a contiguous share of the groups, the shares are
-// scanned.  `warp_tiles` is scratch for one word per warp.
+// scanned.  `warp_tiles` is scratch for one word per warp.  The experts of a table that
+// descends could overlap, and their tiles together pass what the plan has counted on
+// (and 32 bits), so such a table gives every row to none.
 template <int BM>
 __device__ __forceinline__ void grouped_table(const GroupedParams& p, int* row0, int* tile0,
                                               int* warp_tiles, int tid, uint32_t lane)
@@ -227,10 +229,13 @@ __device__ __forceinline__ void grouped_table(const GroupedParams& p, int* row0,
     const int g0 = tid * share;
     auto start = [&](int g) { return g <= p.experts ? clamp_row(p.offsets[g], p.rows) : p.rows; };
     int sum = 0;
+    bool descends = false;
     for (int i = 0; i < share && g0 + i < groups; ++i) {
         const int a = start(g0 + i), b = start(g0 + i + 1);
         sum += b > a ? (b - a + BM - 1) / BM : 0;
+        descends |= b < a;
     }
+    descends = __syncthreads_or(descends);
     int scan = sum;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -243,12 +248,12 @@ __device__ __forceinline__ void grouped_table(const GroupedParams& p, int* row0,
     for (int w = 0; w < warp; ++w) at += warp_tiles[w];
     for (int i = 0; i < share && g0 + i < groups; ++i) {
         const int a = start(g0 + i), b = start(g0 + i + 1);
-        row0[g0 + i] = a;
-        tile0[g0 + i] = at;
+        row0[g0 + i] = descends ? 0 : a;
+        tile0[g0 + i] = descends ? 0 : at;
         at += b > a ? (b - a + BM - 1) / BM : 0;
         if (g0 + i == groups - 1) {
             row0[groups] = p.rows;
-            tile0[groups] = at;
+            tile0[groups] = descends ? (p.rows + BM - 1) / BM : at;
         }
     }
     __syncthreads();
