@@ -99,3 +99,23 @@ def test_the_model_finds_a_late_count():
     assert _left_over("a", "b", False)
     assert not _left_over("a", "b", True)
     assert not _left_over("a", "a", False)
+
+
+@pytest.mark.parametrize("file", ["kernel_ws.cu", "kernel_ws2.cuh", "kernel_grouped.cuh",
+                                  "kernel_grouped_pair.cuh", "w4.cu"])
+def test_copies_in_flight_are_waited_for_whoever_gave_up(file):
+    """A producer that issued all its copies may end before any wait of its own fails,
+    while the role that reads them has given up: its drain must not depend on its own
+    state."""
+    for _, name, body in _kernels():
+        if _ != file:
+            continue
+        for m in re.finditer(r"wd\.drain\(bar(?:_addr)?\([^;]*?(?:FULL|TAIL)", body):
+            depth, conditions = 0, []
+            for line in reversed(body[:m.start()].split("\n")):
+                depth += line.count("{") - line.count("}")
+                if depth > len(conditions):
+                    conditions.append(line.strip())
+                if "warp == 0" in line or "warp < 10" in line:
+                    break
+            assert not any("aborted" in c for c in conditions), (name, conditions)

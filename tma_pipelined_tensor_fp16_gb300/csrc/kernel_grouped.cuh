@@ -549,8 +549,9 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
             u = next;
         }
         if (lane == 0) grouped_finish(p.counter, gridDim.x);
-        // an abandoned run: the loads in flight land before the CTA exits
-        if (lane == 0 && wd.aborted) {
+        // the last min(D, issued) loads land before the CTA exits, whichever role may have
+        // given up without waiting for them
+        if (lane == 0) {
             int st = end_stage;
             uint32_t ph = end_phase;
             for (int i = 0; i < D && i < issued; ++i) {

@@ -236,7 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GROUPED_THREADS, 1)
         uint32_t phase = 0;
         int armed = 0;
         uint32_t tail_bits = 0;  // phase of each stage's tail barrier
-        int last_tail = -1;
+        uint32_t tails = 0;      // the stages that have had a tail
         int end_stage = 0;
         uint32_t end_phase = 0;
         GroupedUnit w;
@@ -286,7 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GROUPED_THREADS, 1)
                         to_bar = map_shared_rank(bar(BAR_TAIL + stage), rank);
                         if (leader) mbar_arrive(bar(BAR_FULL + stage));
                         tail_bits ^= 1u << stage;
-                        last_tail = stage;
+                        tails |= 1u << stage;
                     } else {
                         if (leader) mbar_arrive_expect_tx(bar(BAR_FULL + stage), 2 * cta_tx);
                         to_bar = map_shared_rank(bar(BAR_FULL + stage), 0);
@@ -333,10 +333,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GROUPED_THREADS, 1)
             u = leader ? next : pair_read(bars, use, wd, lane);
         }
         if (leader && lane == 0) grouped_finish(p.counter, gridDim.x / 2);
-        // An abandoned run: let the copies in flight land.  The leader waits for
-        // the phases it armed, both for their last tail; the peer's other copies
-        // signal the leader, so it gives them a while.
-        if (lane == 0 && wd.aborted) {
+        // The copies in flight land before the CTAs can exit, whichever role may have
+        // given up without waiting for them: the leader drains the phases it armed, which
+        // take in the peer's copies, each CTA those of its tails; a peer that gave up
+        // allows a grace period too, as its leader may not have armed a phase for them.
+        if (lane == 0) {
             if (leader) {
                 int st = end_stage;
                 uint32_t ph = end_phase;
@@ -350,10 +351,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GROUPED_THREADS, 1)
                     wd.drain(bar(BAR_FULL + st), ph);
                 }
             }
-            if (last_tail >= 0)
-                wd.drain(bar(BAR_TAIL + last_tail), ((tail_bits >> last_tail) & 1u) ^ 1u);
-            const uint64_t t0 = globaltimer_ns();
-            while (globaltimer_ns() - t0 < 200000ull) {
+            for (int st = 0; st < D; ++st)
+                if ((tails >> st) & 1u) wd.drain(bar(BAR_TAIL + st), ((tail_bits >> st) & 1u) ^ 1u);
+            if (!leader && wd.aborted) {
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 200000ull) {
+                }
             }
         }
         __syncwarp();

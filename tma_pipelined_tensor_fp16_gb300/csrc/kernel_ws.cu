@@ -197,8 +197,9 @@ __global__ void __launch_bounds__(WS_THREADS, 1) k_ws(const __grid_constant__ CU
             if (tr) trace_unit(p, ui, TRACE_U_EMPTY_WAIT, empty_wait_ns);
             ++ui;
         }
-        // drain: the last min(D, issued) loads have landed before exit
-        if (lane == 0 && wd.aborted) {
+        // drain: the last min(D, issued) loads have landed before exit, whichever role
+        // may have given up without waiting for them
+        if (lane == 0) {
             int st = end_stage;
             uint32_t ph = end_phase;
             for (int i = 0; i < D && i < issued; ++i) {

@@ -378,34 +378,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
             if (tr) trace_unit(p, ui, TRACE_U_EMPTY_WAIT, empty_wait_ns);
             ++ui;
         }
-        if (lane == 0 && wd.aborted) {
-            // Let copies already in flight land before the CTA can exit: the
-            // leader drains the phases it armed, the peer waits one
-            // budget-bounded grace period (its copies signal the leader).
-            if (leader) {
-                int st = end_stage;
-                uint32_t ph = end_phase;
-                for (int i = 0; i < D && i < armed; ++i) {
-                    if (st == 0) {
-                        st = D - 1;
-                        ph ^= 1u;
-                    } else {
-                        --st;
-                    }
-                    wd.drain(bar_addr(bars, BAR_FULL + st), ph);
+        // The copies in flight land before the CTAs can exit, whichever role may have
+        // given up without waiting for them: the leader drains the phases it armed, which
+        // take in the peer's copies; a peer that gave up allows a grace period too, as
+        // its leader may not have armed a phase for them.
+        if (lane == 0 && leader) {
+            int st = end_stage;
+            uint32_t ph = end_phase;
+            for (int i = 0; i < D && i < armed; ++i) {
+                if (st == 0) {
+                    st = D - 1;
+                    ph ^= 1u;
+                } else {
+                    --st;
                 }
-                if constexpr (DYN) {
-                    // the last cancellation request may still be in flight
-                    if (requests > 0) {
-                        const int r = requests - 1;
-                        wd.drain(bar_addr(bars, BAR_CLC_FULL + r % CLC_SLOTS),
-                                 static_cast<uint32_t>(r / CLC_SLOTS) & 1u);
-                    }
+                wd.drain(bar_addr(bars, BAR_FULL + st), ph);
+            }
+            if constexpr (DYN) {
+                // the last cancellation request may still be in flight
+                if (requests > 0) {
+                    const int r = requests - 1;
+                    wd.drain(bar_addr(bars, BAR_CLC_FULL + r % CLC_SLOTS),
+                             static_cast<uint32_t>(r / CLC_SLOTS) & 1u);
                 }
-            } else {
-                const uint64_t t0 = globaltimer_ns();
-                while (globaltimer_ns() - t0 < 200000ull) {
-                }
+            }
+        } else if (lane == 0 && wd.aborted) {
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 200000ull) {
             }
         }
         __syncwarp();

@@ -713,8 +713,9 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(W4_WFULL + ws));
         }
-        // an abandoned run: this warp's copies in flight land before the CTA exits
-        if (lane == 0 && wd.aborted) {
+        // this warp's copies in flight land before the CTA exits, whichever role may have
+        // given up without waiting for them
+        if (lane == 0) {
             for (int n = last_n; n >= 0 && n > last_n - STAGES; n -= 2)
                 wd.drain(bar(W4_WFULL + n % STAGES), static_cast<uint32_t>(n / STAGES) & 1u);
         }
