@@ -133,6 +133,13 @@ TMAGEMM_API gemm_grouped_plan* gemm_grouped_create_plan_ex(int64_t rows, int64_t
 TMAGEMM_API int gemm_grouped_run(gemm_grouped_plan* plan, const void* P, const void* Q,
                                  const int32_t* offsets, void* out, void* cuda_stream);
 
+/* Later runs: the bound on any single wait inside the kernel in milliseconds (0: the
+ * default, 2000), and for tests of it `debug_stall` (0: none): 1 makes the producer of
+ * the copies, 2 the reader of the sums first wait on a barrier that nothing completes.
+ * Such a run ends with GEMM_ERR_TIMEOUT in the status; its output is not whole. */
+TMAGEMM_API int gemm_grouped_set_wait(gemm_grouped_plan* plan, int wait_budget_ms,
+                                      int debug_stall);
+
 /* As gemm_get_device_status, gemm_destroy and gemm_plan_describe. */
 TMAGEMM_API int gemm_grouped_get_device_status(gemm_grouped_plan* plan);
 TMAGEMM_API void gemm_grouped_destroy(gemm_grouped_plan* plan);
@@ -186,6 +193,10 @@ TMAGEMM_API gemm_w4_plan* gemm_w4_create_plan_ex(int64_t M, int64_t N, int64_t K
 TMAGEMM_API int gemm_w4_run(gemm_w4_plan* plan, const void* X, const void* packed,
                             const void* scales, const void* zeros, const int32_t* expert_ids,
                             void* Y, void* cuda_stream);
+
+/* As gemm_grouped_set_wait, for the kernel of "rows" (the GEMM of "expand" keeps its
+ * default). */
+TMAGEMM_API int gemm_w4_set_wait(gemm_w4_plan* plan, int wait_budget_ms, int debug_stall);
 
 /* As gemm_get_device_status, gemm_destroy and gemm_plan_describe. */
 TMAGEMM_API int gemm_w4_get_device_status(gemm_w4_plan* plan);

@@ -96,12 +96,14 @@ _SIGS = {
     "gemm_grouped_create_plan": (ctypes.c_void_p, [ctypes.c_int64] * 3 + [ctypes.c_int] * 3),
     "gemm_grouped_create_plan_ex": (ctypes.c_void_p, [ctypes.c_int64] * 3 + [ctypes.c_int] * 4),
     "gemm_grouped_run": (ctypes.c_int, [ctypes.c_void_p] * 6),
+    "gemm_grouped_set_wait": (ctypes.c_int, [ctypes.c_void_p] + [ctypes.c_int] * 2),
     "gemm_grouped_get_device_status": (ctypes.c_int, [ctypes.c_void_p]),
     "gemm_grouped_destroy": (None, [ctypes.c_void_p]),
     "gemm_grouped_describe": (ctypes.c_char_p, [ctypes.c_void_p]),
     "gemm_w4_create_plan": (ctypes.c_void_p, [ctypes.c_int64] * 3 + [ctypes.c_int] * 4),
     "gemm_w4_create_plan_ex": (ctypes.c_void_p, [ctypes.c_int64] * 3 + [ctypes.c_int] * 5),
     "gemm_w4_run": (ctypes.c_int, [ctypes.c_void_p] * 8),
+    "gemm_w4_set_wait": (ctypes.c_int, [ctypes.c_void_p] + [ctypes.c_int] * 2),
     "gemm_w4_get_device_status": (ctypes.c_int, [ctypes.c_void_p]),
     "gemm_w4_destroy": (None, [ctypes.c_void_p]),
     "gemm_w4_describe": (ctypes.c_char_p, [ctypes.c_void_p]),

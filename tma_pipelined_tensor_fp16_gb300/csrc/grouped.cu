@@ -24,6 +24,8 @@ struct gemm_grouped_plan {
     int tiles_m, tiles_n;
     DevStatus* d_status;  // and the counters behind it
     std::shared_ptr<CounterSlots> slots;  // graphs that captured a run hold it too
+    unsigned long long budget_ns;
+    int debug_stall;
     char desc[256];
 };
 
@@ -232,6 +234,7 @@ gemm_grouped_plan* gemm_grouped_create_plan_ex(int64_t rows, int64_t N, int64_t 
         p.op = op;
         p.dtype = dtype_out;
         p.device = dev;
+        p.budget_ns = DEFAULT_WAIT_NS;
         const int64_t cols = out_cols_of(p);
         const uint32_t table = grouped_table_bytes(op, experts);
         const bool pair_fits = smem_layout(2 * PAIR_DEPTH, 128, NUM_STAGING).total + table <=
@@ -380,9 +383,22 @@ int gemm_grouped_run(gemm_grouped_plan* plan, const void* P, const void* Q,
         if (r != GEMM_OK) return r;
         p.counter = reinterpret_cast<unsigned long long*>(plan->d_status + 1) + slot;
         p.epoch = plan->slots->next_epoch();
-        p.budget_ns = 2000ull * 1000000ull;
+        p.budget_ns = plan->budget_ns;
+        p.debug_stall = plan->debug_stall;
         e = launch_grouped(s, stream);
         return e == cudaSuccess ? ok() : cuda_fail("grouped product launch", e);
+    });
+}
+
+int gemm_grouped_set_wait(gemm_grouped_plan* plan, int wait_budget_ms, int debug_stall)
+{
+    return guarded([&] {
+        if (!plan) return fail(GEMM_ERR_INVALID_ARG, "plan is NULL");
+        const int r = check_wait(wait_budget_ms, debug_stall);
+        if (r != GEMM_OK) return r;
+        plan->budget_ns = wait_ns(wait_budget_ms);
+        plan->debug_stall = debug_stall;
+        return ok();
     });
 }
 

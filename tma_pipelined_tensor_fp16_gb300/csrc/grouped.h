@@ -28,6 +28,7 @@ struct GroupedParams {
     unsigned long long* counter;  // see grouped_take
     int epoch;
     unsigned long long budget_ns;
+    int debug_stall;  // 1: the producer, 2: the epilogue first waits on a barrier nothing completes
 };
 
 struct GroupedSpec {

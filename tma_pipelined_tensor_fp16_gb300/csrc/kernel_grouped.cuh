@@ -432,6 +432,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
             mbar_init(bar(BAR_CLC_EMPTY + j), GROUPED_READERS);
         }
         mbar_init(bar(BAR_DRAIN), 1);
+        mbar_init(bar(BAR_STALL), 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -462,6 +463,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
         constexpr uint32_t SMALL_BYTES = GROUPED_SMALL_ROWS * 128;
+        if (p.debug_stall == 1) wd.wait(bar(BAR_STALL), 0, WAIT_STALL, -1, -1);
         int stage = 0;
         uint32_t phase = 0;
         int issued = 0;
@@ -644,6 +646,7 @@ __global__ void __launch_bounds__(GROUPED_THREADS, 1)
         __syncwarp();
     } else {
         // -------------------------------------------------------- epilogue
+        if (p.debug_stall == 2) wd.wait(bar(BAR_STALL), 0, WAIT_STALL, -1, -1);
         const int q = warp & 3;
         int acc = 0;
         uint32_t acc_phase = 0;

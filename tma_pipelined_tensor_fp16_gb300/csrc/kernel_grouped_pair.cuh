@@ -198,6 +198,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GROUPED_THREADS, 1)
             mbar_init(bar(BAR_CLC_EMPTY + j), PAIR_READERS);
         }
         mbar_init(bar(BAR_DRAIN), 1);
+        mbar_init(bar(BAR_STALL), 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -232,6 +233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GROUPED_THREADS, 1)
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
         constexpr uint32_t cta_tx = (A_TILE_BYTES + B_BYTES) * PAIR_KS;
+        if (p.debug_stall == 1) wd.wait(bar(BAR_STALL), 0, WAIT_STALL, -1, -1);
         int stage = 0;
         uint32_t phase = 0;
         int armed = 0;
@@ -455,6 +457,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GROUPED_THREADS, 1)
         __syncwarp();
     } else {
         // -------------------------------------------------------- epilogue
+        if (p.debug_stall == 2) wd.wait(bar(BAR_STALL), 0, WAIT_STALL, -1, -1);
         const int q = warp & 3;
         int acc = 0;
         uint32_t acc_phase = 0;

@@ -62,6 +62,23 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, u
 // width of a tile or the stages in flight stays within 32 bits.
 constexpr int64_t MAX_COORDINATE = (int64_t(1) << 31) - 65536;
 
+// The bound on a wait inside a kernel, and the checks of its setters.
+constexpr unsigned long long DEFAULT_WAIT_NS = 2000ull * 1000000ull;
+
+inline unsigned long long wait_ns(int budget_ms)
+{
+    return budget_ms > 0 ? static_cast<unsigned long long>(budget_ms) * 1000000ull
+                         : DEFAULT_WAIT_NS;
+}
+
+inline int check_wait(int budget_ms, int debug_stall)
+{
+    if (budget_ms < 0) return fail(GEMM_ERR_INVALID_ARG, "wait_budget_ms must be >= 0");
+    if (debug_stall < 0 || debug_stall > 2)
+        return fail(GEMM_ERR_INVALID_ARG, "debug_stall must be 0, 1 or 2");
+    return GEMM_OK;
+}
+
 inline bool aligned16(const void* p)
 {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;

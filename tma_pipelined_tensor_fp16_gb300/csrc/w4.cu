@@ -39,6 +39,7 @@ struct W4Params {
     DevStatus* status;
     int epoch;
     unsigned long long budget_ns;
+    int debug_stall;  // 1: the loaders, 2: the sums wait on a barrier nothing completes
 };
 
 // ---------------------------------------------------------------- few rows
@@ -129,7 +130,8 @@ enum : int {
     W4_GFULL = W4_DONE + W4_TEAMS * W4_TURNS, // a block's group sums are complete
     W4_GEMPTY = W4_GFULL + W4_MAX_BUFS,       // they have been read
     W4_DRAIN = W4_GEMPTY + W4_MAX_BUFS,       // [team]
-    W4_BARRIERS = W4_DRAIN + W4_TEAMS
+    W4_STALL = W4_DRAIN + W4_TEAMS,           // stall test: never completed
+    W4_BARRIERS
 };
 
 // CTAs per SM.  From 32 columns on the sums need more registers than two CTAs
@@ -446,6 +448,7 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
             mbar_init(bar(W4_GEMPTY + i), L::SUMMERS);
         }
         for (int i = 0; i < W4_TEAMS; ++i) mbar_init(bar(W4_DRAIN + i), 1);
+        mbar_init(bar(W4_STALL), 1);
         fence_mbar_init();
     }
     if (warp == 11) {
@@ -585,7 +588,9 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
         const uint32_t* words = reinterpret_cast<const uint32_t*>(gen + L::TABLE) + row;
         int left = p.K - s_begin * W4_STAGE_K;
         for (int s = s_begin; s < s_end; ++s) {
-            wd.wait(bar(W4_WFULL + ws), ws_phase, WAIT_FULL, s, 4);
+            // (a stalled role waits in this place: a wait of its own costs registers)
+            const bool stall = p.debug_stall == 2;
+            wd.wait(bar(stall ? W4_STALL : W4_WFULL + ws), stall ? 0u : ws_phase, WAIT_FULL, s, 4);
             // read when needed: a stage's eight scales beside the sums spill
             auto scale_of = [&](int i) {
                 return __half2float(__ushort_as_half(static_cast<unsigned short>(
@@ -660,8 +665,10 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
         for (int s = s_begin + warp - 8; s < s_end; s += 2) {
             const int n = s - s_begin;
             const int ws = n % STAGES;
-            const bool ok = wd.wait(bar(W4_WEMPTY + ws),
-                                    (static_cast<uint32_t>(n / STAGES) & 1u) ^ 1u, WAIT_EMPTY, s, 3);
+            const bool stall = p.debug_stall == 1;
+            const bool ok =
+                wd.wait(bar(stall ? W4_STALL : W4_WEMPTY + ws),
+                        stall ? 0u : (static_cast<uint32_t>(n / STAGES) & 1u) ^ 1u, WAIT_EMPTY, s, 3);
             if (lane == 0 && ok) {
                 mbar_arrive_expect_tx(bar(W4_WFULL + ws), tx);
                 tma_load_2d(base + L::W + ws * L::STAGE, &tmW, bar(W4_WFULL + ws),
@@ -674,7 +681,8 @@ __global__ void __launch_bounds__(W4Layout<NC, GROUP>::THREADS, W4Layout<NC, GRO
                 }
                 last_n = n;
             }
-            __syncwarp();
+            // an abandoned run: no arrival on a barrier whose bytes are on their way
+            if (!__all_sync(0xffffffffu, ok)) break;
             uint32_t* to =
                 reinterpret_cast<uint32_t*>(gen + L::TABLE) + ws * L::TABLE_WORDS + lane;
             // -(1024 + zero) in fp16 is -1024's bits plus the zero point
@@ -1038,6 +1046,8 @@ struct gemm_w4_plan {
     int tile_rows;    // rows of the weights per CTA
     DevStatus* d_status;
     unsigned epoch;
+    unsigned long long budget_ns;
+    int debug_stall;
     void* d_weights;  // N x 2 K fp16 (rounded: N x K)
     void* d_x;        // M x 2 K fp16
     int* d_verdicts;  // one per CTA of the expansion
@@ -1102,7 +1112,8 @@ int run_rows(gemm_w4_plan* plan, const void* X, const void* packed, const void* 
     p.status = plan->d_status;
     // threads may run one plan at a time of their own; any number above 0 will do
     p.epoch = static_cast<int>(__atomic_add_fetch(&plan->epoch, 1u, __ATOMIC_RELAXED) % 0x7fffffffu) + 1;
-    p.budget_ns = 2000ull * 1000000ull;
+    p.budget_ns = plan->budget_ns;
+    p.debug_stall = plan->debug_stall;
     CUtensorMap codes, x;
     int r = encode_rows(&codes, "packed", CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, packed, plan->K / 2,
                         plan->N * std::max(plan->experts, 1), plan->tile_rows);
@@ -1181,6 +1192,7 @@ gemm_w4_plan* gemm_w4_create_plan_ex(int64_t M, int64_t N, int64_t K, int group,
         p.share = share;
         p.dtype = dtype_out;
         p.rounded = weights == GEMM_W4_WEIGHTS_ROUNDED;
+        p.budget_ns = DEFAULT_WAIT_NS;
         p.cols = 16;
         while (experts == 0 && p.cols < std::min<int64_t>(M, 64)) p.cols *= 2;
         const int64_t blocks = (M + p.cols - 1) / p.cols;  // of rows, without experts
@@ -1271,6 +1283,18 @@ int gemm_w4_run(gemm_w4_plan* plan, const void* X, const void* packed, const voi
         if (r != GEMM_OK || plan->rounded) return r;
         return run_rows(plan, X, packed, scales, zeros, nullptr, Y, stream,
                         static_cast<int>(blocks));
+    });
+}
+
+int gemm_w4_set_wait(gemm_w4_plan* plan, int wait_budget_ms, int debug_stall)
+{
+    return guarded([&] {
+        if (!plan) return fail(GEMM_ERR_INVALID_ARG, "plan is NULL");
+        const int r = check_wait(wait_budget_ms, debug_stall);
+        if (r != GEMM_OK) return r;
+        plan->budget_ns = wait_ns(wait_budget_ms);
+        plan->debug_stall = debug_stall;
+        return ok();
     });
 }
 

@@ -252,7 +252,7 @@ class ExpertRoute:
 
 class _Handle:
     """Owner of a plan of the C library."""
-    _destroy = _describe = _status = None
+    _destroy = _describe = _status = _wait = None
 
     def _own(self, handle):
         self._h = handle
@@ -270,6 +270,13 @@ class _Handle:
         """GEMM_OK, or GEMM_ERR_TIMEOUT if a wait inside a kernel ran out; call
         after synchronising."""
         return getattr(lib(), self._status)(self._h)
+
+    def set_wait(self, budget_ms=0, debug_stall=0):
+        """For later runs: the bound on a wait inside the kernel (0: 2000 ms), and a
+        role that is to wait in vain, for tests (see include/tmaexperts.h)."""
+        status = getattr(lib(), self._wait)(self._h, budget_ms, debug_stall)
+        if status != 0:
+            _check(status)
 
     def close(self):
         if getattr(self, "_h", None):
@@ -292,7 +299,7 @@ class GroupedPlan(_Handle):
     * ``grad_weight``:  dB[e] = dC_e^T . A_e       plan(dC, A, offsets, dB)
     """
     _destroy, _describe = "gemm_grouped_destroy", "gemm_grouped_describe"
-    _status = "gemm_grouped_get_device_status"
+    _status, _wait = "gemm_grouped_get_device_status", "gemm_grouped_set_wait"
 
     def __init__(self, rows, N, K, experts, op="forward", out="f16", tile="auto"):
         if op not in GROUPED_OPS:
@@ -340,7 +347,8 @@ class W4Plan(_Handle):
     The matrices are the plan's, so runs of a plan whose description says ``expand``
     must not overlap on the GPU (streams, threads, graph replays): one plan for each.
     """
-    _destroy, _describe, _status = "gemm_w4_destroy", "gemm_w4_describe", "gemm_w4_get_device_status"
+    _destroy, _describe = "gemm_w4_destroy", "gemm_w4_describe"
+    _status, _wait = "gemm_w4_get_device_status", "gemm_w4_set_wait"
 
     def __init__(self, M, N, K, group=128, out="f16", experts=0, share=1,
                  weights="exact"):
