@@ -58,6 +58,9 @@ class Grouped:
     def __init__(self, rows, N, K, experts, op="forward", out="f16"):
         self.rows, self.N, self.K, self.experts, self.op = rows, N, K, experts, op
 
+    def device_status(self):
+        return 0
+
     def __call__(self, P, Q, offsets):
         E = self.experts
         shape = {"forward": (self.rows, self.N), "grad_input": (self.rows, self.K),
@@ -79,6 +82,9 @@ class W4:
         if M < 1:
             raise ValueError("M must be at least 1")
         self.M, self.N, self.K, self.group, self.experts, self.share = M, N, K, group, experts, share
+
+    def device_status(self):
+        return 0
 
     def __call__(self, X, packed, scales, zeros=None, ids=None):
         if tuple(scales.shape) != (self.experts, self.N, self.K // self.group):

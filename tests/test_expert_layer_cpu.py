@@ -78,3 +78,19 @@ def test_decode_ignores_what_a_dropped_slot_holds():
     assert torch.equal(layer.decode(X, ids, w), clean)
     assert (clean[3] == 0).all()
     assert torch.isfinite(layer.forward(X, ids, w)[0]).all()
+
+
+def test_device_status_is_that_of_every_plan(monkeypatch):
+    """A wait that ran out in any of the layer's kernels is reported."""
+    layer, X, ids, w = layer_doubles.layer()
+    assert layer.device_status() == 0
+    layer.pack(group=32)
+    Y, saved = layer.forward(X, ids, w)
+    layer.backward(Y, saved)
+    layer.decode(X, ids, w)
+    plans = layer.plans()
+    assert len(plans) >= 6
+    for i, plan in enumerate(plans):
+        monkeypatch.setattr(plan, "device_status", lambda: 4, raising=False)
+        assert layer.device_status() == 4
+        monkeypatch.setattr(plan, "device_status", lambda: 0, raising=False)

@@ -14,6 +14,7 @@ of a training step and of a decoding step, and how far the decoding step with
 """
 import argparse
 
+from .binding import GemmError
 from .experts import ExpertRoute, GroupedPlan, W4Plan, w4_pack
 
 
@@ -35,6 +36,16 @@ class ExpertLayer:
         if key not in self._plans:
             self._plans[key] = GroupedPlan(rows, N, K, self.experts, op=op, out=out)
         return self._plans[key]
+
+    def plans(self):
+        """The plans that the layer keeps."""
+        return [plan for kept in self._plans.values()
+                for plan in (kept if isinstance(kept, list) else [kept])]
+
+    def device_status(self):
+        """GEMM_OK, or the status of a plan with a wait that ran out inside a kernel, whose
+        results are not whole; call after synchronising."""
+        return next((s for s in [plan.device_status() for plan in self.plans()] if s != 0), 0)
 
     def forward(self, X, ids, weights):
         """Y (tokens x width) and what ``backward`` needs."""
@@ -75,10 +86,10 @@ class ExpertLayer:
         group, (p1, s1, z1), (p2, s2, z2) = self._packed
         key = ("w4", rows, group)
         if key not in self._plans:
-            self._plans[key] = (
+            self._plans[key] = [
                 W4Plan(rows, self.inner, self.width, group=group, experts=self.experts,
                        share=self.topk),
-                W4Plan(rows, self.width, self.inner, group=group, experts=self.experts))
+                W4Plan(rows, self.width, self.inner, group=group, experts=self.experts)]
         up, down = self._plans[key]
         A = up(X, p1, s1, zeros=z1, ids=ids).relu_()
         Ys = down(A, p2, s2, zeros=z2, ids=ids)
@@ -144,6 +155,9 @@ def main(argv=None):
     ms = _milliseconds(lambda: layer.decode(x, i, w), 10 * a.steps)
     exact, _ = layer.forward(x, i, w)
     coded = layer.decode(x, i, w)
+    status = layer.device_status()
+    if status != 0:
+        raise GemmError(status, "a wait inside a kernel ran out")
     off = float((coded.float() - exact.float()).norm() / exact.float().norm())
     print("decoding step: %d tokens with 4-bit weights: %.1f us, %.3f of the fp16 layer's norm off"
           % (a.decode, ms * 1e3, off))
