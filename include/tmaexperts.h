@@ -104,10 +104,11 @@ typedef enum {
 /* Plan for `rows` rows (an upper bound is fixed by the tensors, the split over
  * experts is read from `offsets` on the device at every run).  rows >= 0,
  * 1 <= experts <= 1024, N and K multiples of 8, all at most 2^31 - 65536 (and
- * experts * N too).  Returns NULL on error.  The plan owns a device record of 32 KB: its status and
- * the counters from which runs hand out their tiles, one for every stream and every
- * captured launch.  So runs of one plan may overlap on the GPU, on several streams,
- * from several threads, and with replays of graphs that hold runs of it. */
+ * experts * N too).  Returns NULL on error.  The plan owns a device record of 32
+ * bytes, its status.  The counters from which runs hand out their tiles are the
+ * device's (512 KB, allocated with its first plan and kept), one for every stream and
+ * every captured launch: so runs of one plan may overlap on the GPU, on several
+ * streams, from several threads, and with replays of graphs that hold runs of it. */
 TMAGEMM_API gemm_grouped_plan* gemm_grouped_create_plan(int64_t rows, int64_t N, int64_t K,
                                                         int experts, int op, int dtype_out);
 

@@ -79,7 +79,7 @@ def test_replay_beside_eager_calls():
 
 
 def test_a_graph_gives_its_counter_back():
-    """More captures, one after the other, than a plan has counters for."""
+    """More captured launches, one graph after the other, than there are counters."""
     import torch
 
     import tma_pipelined_tensor_fp16_gb300 as tg
@@ -90,7 +90,7 @@ def test_a_graph_gives_its_counter_back():
     plan(A, B, offsets, C)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    for _ in range(25):
+    for _ in range(340):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):
             for _ in range(200):

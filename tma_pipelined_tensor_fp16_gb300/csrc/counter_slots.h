@@ -1,8 +1,8 @@
-// counter_slots.h -- which of a plan's tile counters a run uses.  Runs that may be on
-// the GPU at the same time must not share one: runs on one stream never are, runs on
-// two streams may be, and a launch captured into a graph may be replayed beside any
-// other.  So every stream has a counter, and every captured launch one of its own for
-// as long as its graph lives.
+// counter_slots.h -- which of a device's tile counters a run uses.  Runs that may be on
+// the GPU at the same time must not share one: runs on one stream never are, whatever
+// their plans, runs on two streams may be, and a launch captured into a graph may be
+// replayed beside any other.  So every stream has a counter, and every captured launch
+// one of its own for as long as its graph lives.
 #pragma once
 
 #include <cstdint>
@@ -14,7 +14,7 @@ namespace tg {
 class CounterSlots {
 public:
     static constexpr int STREAMS = 256;    // counters of streams: the first ones
-    static constexpr int CAPTURES = 3840;  // counters of captured launches
+    static constexpr int CAPTURES = 65280; // counters of captured launches
     static constexpr int COUNT = STREAMS + CAPTURES;
 
     CounterSlots()
@@ -74,14 +74,6 @@ public:
         free_.push_back(slot);
     }
 
-    // The number of the next run, > 0.
-    int next_epoch()
-    {
-        std::lock_guard<std::mutex> lock(mutex_);
-        if (++epoch_ <= 0) epoch_ = 1;
-        return epoch_;
-    }
-
 private:
     static constexpr uint64_t NOBODY = ~uint64_t(0);
     struct Stream {
@@ -92,7 +84,6 @@ private:
     std::vector<int> free_;
     uint64_t clock_ = 0;
     int captured_ = 0;
-    int epoch_ = 0;
 };
 
 }  // namespace tg

@@ -6,7 +6,9 @@
 #include <cstdio>
 #include <cstring>
 #include <memory>
+#include <mutex>
 #include <new>
+#include <vector>
 
 #include "../../include/tmaexperts.h"
 #include "counter_slots.h"
@@ -22,8 +24,8 @@ struct gemm_grouped_plan {
     int block_m, block_n, grid, pipe_depth;
     unsigned smem_bytes;
     int tiles_m, tiles_n;
-    DevStatus* d_status;  // and the counters behind it
-    std::shared_ptr<CounterSlots> slots;  // graphs that captured a run hold it too
+    DevStatus* d_status;
+    unsigned epoch;
     unsigned long long budget_ns;
     int debug_stall;
     char desc[256];
@@ -151,9 +153,42 @@ int check_grouped(int64_t rows, int64_t N, int64_t K, int experts, int op, int d
     return GEMM_OK;
 }
 
+// A device's tile counters, all zero between runs.  Made with its first plan and kept:
+// graphs may outlive every plan.
+struct CounterPool {
+    CounterSlots slots;
+    unsigned long long* d_counters = nullptr;
+};
+
+std::mutex g_pool_mutex;
+std::vector<CounterPool*> g_pools;  // by device
+
+int make_counters(int dev)
+{
+    std::lock_guard<std::mutex> lock(g_pool_mutex);
+    if (g_pools.size() <= static_cast<size_t>(dev)) g_pools.resize(dev + 1, nullptr);
+    if (g_pools[dev]) return GEMM_OK;
+    std::unique_ptr<CounterPool> pool(new CounterPool);
+    constexpr size_t BYTES = CounterSlots::COUNT * sizeof(unsigned long long);
+    cudaError_t e = cudaMalloc(&pool->d_counters, BYTES);
+    if (e == cudaSuccess) e = cudaMemset(pool->d_counters, 0, BYTES);
+    if (e != cudaSuccess) {
+        if (pool->d_counters) cudaFree(pool->d_counters);
+        return cuda_fail("allocating the tile counters", e);
+    }
+    g_pools[dev] = pool.release();
+    return GEMM_OK;
+}
+
+CounterPool& pool_of(int dev)
+{
+    std::lock_guard<std::mutex> lock(g_pool_mutex);
+    return *g_pools[dev];
+}
+
 // A captured launch's hold on its counter, which ends with the graph.
 struct CapturedSlot {
-    std::shared_ptr<CounterSlots> slots;
+    CounterSlots* slots;
     int slot;
 };
 
@@ -165,7 +200,7 @@ void CUDART_CB release_captured(void* p)
 }
 
 // The tile counter of a run on `stream` (see counter_slots.h).
-int counter_of(const gemm_grouped_plan& plan, cudaStream_t stream, int* slot)
+int counter_of(CounterSlots& slots, cudaStream_t stream, int* slot)
 {
     cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
     cudaError_t e = cudaStreamIsCapturing(stream, &status);
@@ -175,16 +210,16 @@ int counter_of(const gemm_grouped_plan& plan, cudaStream_t stream, int* slot)
         e = cudaStreamGetId(stream, &id);
         if (e != cudaSuccess) return cuda_fail("cudaStreamGetId", e);
         bool taken_over = false;
-        *slot = plan.slots->of_stream(id, &taken_over);
+        *slot = slots.of_stream(id, &taken_over);
         if (taken_over) e = cudaDeviceSynchronize();
         if (e == cudaSuccess) return GEMM_OK;
-        plan.slots->give_up(*slot);
+        slots.give_up(*slot);
         return cuda_fail("cudaDeviceSynchronize", e);
     }
-    std::unique_ptr<CapturedSlot> held(new CapturedSlot{plan.slots, plan.slots->of_capture()});
+    std::unique_ptr<CapturedSlot> held(new CapturedSlot{&slots, slots.of_capture()});
     *slot = held->slot;
     if (held->slot < 0)
-        return fail(GEMM_ERR_UNSUPPORTED, "too many live CUDA graphs hold runs of this plan");
+        return fail(GEMM_ERR_UNSUPPORTED, "too many live CUDA graphs hold grouped products");
     cudaGraph_t graph = nullptr;
     cudaUserObject_t object = nullptr;
     e = cudaStreamGetCaptureInfo(stream, &status, nullptr, &graph, nullptr, nullptr, nullptr);
@@ -192,7 +227,7 @@ int counter_of(const gemm_grouped_plan& plan, cudaStream_t stream, int* slot)
         e = cudaUserObjectCreate(&object, held.get(), release_captured, 1,
                                  cudaUserObjectNoDestructorSync);
     if (e != cudaSuccess) {
-        plan.slots->release(*slot);
+        slots.release(*slot);
         return cuda_fail("tying a tile counter to the graph", e);
     }
     held.release();  // the object's now
@@ -281,12 +316,10 @@ gemm_grouped_plan* gemm_grouped_create_plan_ex(int64_t rows, int64_t N, int64_t 
                       static_cast<long long>(K), experts, p.block_m, p.block_n,
                       p.pair ? 2 * BLK_K : BLK_K, p.pipe_depth,
                       p.smem_bytes, p.grid, dtype_out == GEMM_OUT_F16 ? "f16" : "f32");
-        p.slots = std::make_shared<CounterSlots>();
-        // the status record and, behind it, the counters
-        constexpr size_t RECORD =
-            sizeof(DevStatus) + CounterSlots::COUNT * sizeof(unsigned long long);
-        cudaError_t e = cudaMalloc(&p.d_status, RECORD);
-        if (e == cudaSuccess) e = cudaMemset(p.d_status, 0, RECORD);
+        r = make_counters(dev);
+        if (r != GEMM_OK) return r;
+        cudaError_t e = cudaMalloc(&p.d_status, sizeof(DevStatus));
+        if (e == cudaSuccess) e = cudaMemset(p.d_status, 0, sizeof(DevStatus));
         if (e != cudaSuccess) {
             if (p.d_status) cudaFree(p.d_status);
             return cuda_fail("allocating the device status record", e);
@@ -379,10 +412,11 @@ int gemm_grouped_run(gemm_grouped_plan* plan, const void* P, const void* Q,
         p.out = out;
         p.status = plan->d_status;
         int slot = -1;
-        r = counter_of(*plan, stream, &slot);
+        CounterPool& pool = pool_of(dev);
+        r = counter_of(pool.slots, stream, &slot);
         if (r != GEMM_OK) return r;
-        p.counter = reinterpret_cast<unsigned long long*>(plan->d_status + 1) + slot;
-        p.epoch = plan->slots->next_epoch();
+        p.counter = pool.d_counters + slot;
+        p.epoch = next_epoch(&plan->epoch);
         p.budget_ns = plan->budget_ns;
         p.debug_stall = plan->debug_stall;
         e = launch_grouped(s, stream);

@@ -62,6 +62,12 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, u
 // width of a tile or the stages in flight stays within 32 bits.
 constexpr int64_t MAX_COORDINATE = (int64_t(1) << 31) - 65536;
 
+// The number of a plan's next run, > 0; threads may run one plan at the same time.
+inline int next_epoch(unsigned* epoch)
+{
+    return static_cast<int>(__atomic_add_fetch(epoch, 1u, __ATOMIC_RELAXED) % 0x7fffffffu) + 1;
+}
+
 // The bound on a wait inside a kernel, and the checks of its setters.
 constexpr unsigned long long DEFAULT_WAIT_NS = 2000ull * 1000000ull;
 

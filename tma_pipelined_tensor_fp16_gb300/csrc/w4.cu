@@ -1110,8 +1110,7 @@ int run_rows(gemm_w4_plan* plan, const void* X, const void* packed, const void* 
     p.verdicts = verdicts > 0 ? plan->d_verdicts : nullptr;
     p.verdict_count = verdicts;
     p.status = plan->d_status;
-    // threads may run one plan at a time of their own; any number above 0 will do
-    p.epoch = static_cast<int>(__atomic_add_fetch(&plan->epoch, 1u, __ATOMIC_RELAXED) % 0x7fffffffu) + 1;
+    p.epoch = next_epoch(&plan->epoch);
     p.budget_ns = plan->budget_ns;
     p.debug_stall = plan->debug_stall;
     CUtensorMap codes, x;
