@@ -149,12 +149,14 @@ class ExpertRoute:
                        _ptr(ids), _ptr(self.offsets), _ptr(self.order), _ptr(self.position))
         if self._home is None:
             self._home = handle
-        self._tables_used(handle, dev, stream, ids)
+        if handle != self._home or stream is not None:
+            self._tables_used(handle, dev, stream, ids)
         return self
 
     def _tables_used(self, handle, dev, stream, *tensors):
-        """After a launch on the stream of `handle`: the tables are the route's own, so
-        it keeps them for a stream that is not theirs; the call's tensors as always."""
+        """After a launch on the stream of `handle` that is not the tables', or on the
+        caller's: the tables are the route's own, so it keeps them for that stream; the
+        call's tensors as always.  (The checks are the callers', for decoding's sake.)"""
         if handle != self._home:
             _used_on(stream or _torch().cuda.current_stream(dev), self.offsets, self.order,
                      self.position)
@@ -188,7 +190,8 @@ class ExpertRoute:
         handle = _call(lib().gemm_expert_gather, dev, stream, self.tokens, self.topk,
                        self.experts, width, _ptr(X), _ptr(self.offsets), _ptr(self.position),
                        _ptr(Xs))
-        self._tables_used(handle, dev, stream, X, Xs)
+        if handle != self._home or stream is not None:
+            self._tables_used(handle, dev, stream, X, Xs)
         return Xs
 
     def combine(self, Ys, out=None, weights=None, stream=None):
@@ -200,7 +203,8 @@ class ExpertRoute:
         handle = _call(lib().gemm_expert_combine, dev, stream, self.tokens, self.topk,
                        self.experts, Ys.shape[-1], _ptr(Ys), _ptr(self.offsets),
                        _ptr(self.position), _ptr(weights), code, _ptr(Y))
-        self._tables_used(handle, dev, stream, Ys, weights, Y)
+        if handle != self._home or stream is not None:
+            self._tables_used(handle, dev, stream, Ys, weights, Y)
         return Y
 
     def combine_slots(self, Ys, out=None, weights=None, ids=None, stream=None):
@@ -246,7 +250,8 @@ class ExpertRoute:
         handle = _call(lib().gemm_expert_combine_grad, dev, stream, self.tokens, self.topk,
                        self.experts, width, _ptr(dY), _ptr(Ys), _ptr(self.offsets),
                        _ptr(self.position), _ptr(weights), _ptr(dYs), _ptr(dw))
-        self._tables_used(handle, dev, stream, dY, Ys, weights, dYs, dw)
+        if handle != self._home or stream is not None:
+            self._tables_used(handle, dev, stream, dY, Ys, weights, dYs, dw)
         return dYs, dw
 
 
