@@ -119,3 +119,16 @@ def test_copies_in_flight_are_waited_for_whoever_gave_up(file):
                 if "warp == 0" in line or "warp < 10" in line:
                     break
             assert not any("aborted" in c for c in conditions), (name, conditions)
+
+
+def test_a_relaxed_arrival_follows_the_use_of_what_was_read():
+    """A reader gives a tile's slot back with a relaxed arrival, which orders nothing by
+    itself: the value must have been used before (the instruction that uses it waits for
+    the load, and instructions issue in order), and no other lane may still be reading."""
+    text = _source("kernel_grouped_pair.cuh")
+    body = text[text.index("int pair_read("):]
+    body = body[:body.index("\n}\n")]
+    load, use, arrive = (body.index(s) for s in ("ld_shared_int(", "__shfl_sync(",
+                                                 "mbar_arrive_cluster_relaxed("))
+    assert load < use < arrive
+    assert "lane == 0" in body[:load].split(";")[-1]  # the others take it from lane 0
