@@ -94,3 +94,9 @@ def test_device_status_is_that_of_every_plan(monkeypatch):
         monkeypatch.setattr(plan, "device_status", lambda: 4, raising=False)
         assert layer.device_status() == 4
         monkeypatch.setattr(plan, "device_status", lambda: 0, raising=False)
+
+
+def test_decode_before_pack_says_so():
+    layer, X, ids, w = layer_doubles.layer()
+    with pytest.raises(RuntimeError, match="call pack"):
+        layer.decode(X, ids, w)

@@ -73,12 +73,14 @@ class ExpertLayer:
         return route.gather_grad(dXs), dweights, dW1, dW2
 
     def pack(self, group=128, zeros=True):
-        """Lay the weights out in 4 bits for ``decode``."""
+        """Lay the weights, as they are now, out in 4 bits for ``decode``."""
         self._packed = (group, w4_pack(self.W1, group, zeros), w4_pack(self.W2, group, zeros))
 
     def decode(self, X, ids, weights):
         """Y for a few tokens with the packed weights: no sort, every slot's row
         straight from its expert's codes."""
+        if self._packed is None:
+            raise RuntimeError("the weights have not been packed: call pack() first")
         tokens = X.shape[0]
         rows = tokens * self.topk
         if tokens == 0:  # a plan has a row at least
