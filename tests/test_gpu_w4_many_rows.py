@@ -163,3 +163,22 @@ def test_rounded_weights_on_request(M, N, K, group):
             assert_same(got, x @ w.T, "f32")
         else:
             assert_within(got, x @ w.T, tolerance(None, mag, K, "f32") + 2.0 ** -11 * mag)
+
+
+@pytest.mark.parametrize("M,N,K,group", [(1100, 136, 4096, 64), (2000, 264, 8192, 128),
+                                         (70, 4096, 8192, 32)])
+def test_long_sums_in_fp32(M, N, K, group):
+    """With fp32 outputs many rows are as exact as few ones: each group's sum is whole
+    q - zero times fp16, and the K / group of them are added in fp32 with rounding to
+    nearest, 2^-24 each, so the error stays below 8 * 2^-23 of the result's norm."""
+    import torch
+
+    import tma_pipelined_tensor_fp16_gb300 as tg
+    rng = np.random.default_rng(K)
+    scales = (rng.random((N, K // group)) + 0.5).astype(np.float16)
+    packed, z, w = _codes(rng, N, K, group, scales, True)
+    X = normals(rng, (M, K))
+    plan = tg.W4Plan(M, N, K, group=group, out="f32")
+    got = _product(plan, X, packed, scales, z).astype(np.float64)
+    want = (torch.from_numpy(X).cuda().double() @ torch.from_numpy(w).cuda().t()).cpu().numpy()
+    assert np.linalg.norm(got - want) < 8 * 2.0 ** -23 * np.linalg.norm(want), plan.describe()

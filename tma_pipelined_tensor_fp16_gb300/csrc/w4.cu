@@ -2,8 +2,8 @@
 //
 //     Y[m][n] = sum_g scale[n][g] * sum_{k in g} (q[n][k] - zero[n][g]) X[m][k],
 //
-// for a few rows of X (decoding), and the expansion of the weights to fp16 for
-// many rows.
+// for a few rows of X (decoding), and the expansion of the weights to pairs of fp16
+// numbers for many rows.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -49,7 +49,8 @@ struct W4Params {
 // the N side (16, 32 or 64).  Without experts grid.y is the block.
 //
 // A 32-bit word holds the codes k..k+7.  Masking the word and its shift by 8
-// with 0x000f000f and 0x00f000f0 and setting the exponent of 1024 gives half
+// with 0x000f000f and 0x00f000f0 and setting the exponent of 1024 (whose unit in
+// the last place is one: a common way to make floats of small integers) gives half
 // pairs (k, k+4), (k+1, k+5), (k+2, k+6), (k+3, k+7) of 1024 + q or 1024 + 16 q;
 // one half2 add or fused multiply-add makes them q - zero, exact in fp16.  The
 // operand keeps that order, and X is stored with the same order inside each 8.
@@ -1024,8 +1025,16 @@ double expanded_us(int64_t M, int64_t N, int64_t K, bool rounded)
 // Whether a plan of more than one block of rows expands.  Many rows of a short length
 // always do: the two are then close (few-row kernel and expansion, us: 1500 rows of 1032 x
 // 1152 20.0 and 24.9, 3000 of 512 x 512 16.5 and 15.6, 2000 of 136 x 256 8.6 and 10.8).
-bool prefers_expansion(int64_t M, int64_t N, int64_t K, bool rounded, double rows_us)
+//
+// The GEMM's sum loses 1.2e-9 of its norm per product of its doubled length (the tensor
+// cores' accumulator truncates: 9.6e-6 with K = 4096), where the few-row kernel's, which
+// adds groups of up to 128 exact products in fp32, loses 1.5e-7 in all.  That is far below
+// the rounding of an fp16 output, but not of an fp32 one, which is expanded up to a
+// length only whose error is that of the grouped products, 3e-6.
+bool prefers_expansion(int64_t M, int64_t N, int64_t K, int dtype, bool rounded, double rows_us)
 {
+    if (!rounded && dtype == GEMM_OUT_F32) return M > 1024 && K <= 1280;
+    if (!rounded && K > 32768) return false;
     return (M > 1024 && K < 2048) || rows_us > expanded_us(M, N, K, rounded);
 }
 
@@ -1202,7 +1211,7 @@ gemm_w4_plan* gemm_w4_create_plan_ex(int64_t M, int64_t N, int64_t K, int group,
         const int64_t depth = p.rounded ? K : 2 * K;
         p.expand = experts == 0 && blocks > 1 && depth <= LIM &&
                    std::max(M, N) <= (int64_t(1) << 45) / depth &&
-                   prefers_expansion(M, N, K, p.rounded, us);
+                   prefers_expansion(M, N, K, dtype_out, p.rounded, us);
         int length = 0;
         if (p.expand) {
             p.gemm = gemm_create_plan(M, N, depth, dtype_out);

@@ -346,7 +346,7 @@ class W4Plan(_Handle):
     for 8 (``w4_pack`` makes them).  With ``experts`` they are stacked, and row m
     of Y is the product of X[m // share] with the weights of expert ids[m].
 
-    Many rows are multiplied as fp16 matrices: with ``weights="exact"`` each weight
+    Many rows may be multiplied as fp16 matrices: with ``weights="exact"`` each weight
     as the sum of two fp16 numbers, with ``"rounded"`` rounded to one (half the
     work; the result is off by up to half a unit in the last place of each weight).
     The matrices are the plan's, so runs of a plan whose description says ``expand``
