@@ -15,13 +15,13 @@ def _built():
 
 
 def test_out_of_memory():
-    """A workspace of 1 TB: the allocation fails, nothing is launched."""
+    """A workspace of 4 TB: the allocation fails, nothing is launched."""
     import torch
 
     import tma_pipelined_tensor_fp16_gb300 as tg
     x = torch.zeros(1000, device="cuda")
     with pytest.raises(tg.GemmError, match="MemoryAllocation"):
-        tg.W4Plan(4096, 1 << 20, 1 << 18, group=32)
+        tg.W4Plan(4096, 1 << 25, 1 << 15, group=32)
     x += 1
     torch.cuda.synchronize()
     assert (x == 1).all()
