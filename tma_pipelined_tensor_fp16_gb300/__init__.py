@@ -9,6 +9,11 @@ seeded synthetic operands used by the tests and the benchmark.
 ``include/tmaexperts.h``): ``ExpertRoute`` (tokens sorted by expert and back),
 ``GroupedPlan`` (the experts' products) and ``W4Plan`` (products with 4-bit
 weights).
+
+``microscale`` adds block-scaled 8- and 4-bit floating point (declared in
+``include/tmamicro.h``): ``mx_quantize``, ``MXTensor`` and ``MXPlan`` (their products).
+``layer`` adds what surrounds the products (declared in ``include/tmalayer.h``):
+``rms_norm``, ``rms_norm_grad``, ``GradClip`` and ``clip_grad_norm``.
 """
 from .binding import (  # noqa: F401
     GEMM_OUT_F16, GEMM_OUT_F32, GemmError, Plan, VARIANTS, gemm_create_plan,
@@ -16,3 +21,5 @@ from .binding import (  # noqa: F401
     gemm_last_status, gemm_plan_config, gemm_plan_describe, gemm_run, gemm_run_host,
     gemm_schedule_tile, gemm_select_config, gemm_sw128_offset, make_options)
 from .experts import ExpertRoute, GroupedPlan, W4Plan, w4_pack  # noqa: F401
+from .layer import GradClip, clip_grad_norm, rms_norm, rms_norm_grad  # noqa: F401
+from .microscale import MXPlan, MXTensor, mx_quantize  # noqa: F401

@@ -107,6 +107,32 @@ _SIGS = {
     "gemm_w4_get_device_status": (ctypes.c_int, [ctypes.c_void_p]),
     "gemm_w4_destroy": (None, [ctypes.c_void_p]),
     "gemm_w4_describe": (ctypes.c_char_p, [ctypes.c_void_p]),
+    # include/tmamicro.h
+    "gemm_mx_sizes": (ctypes.c_int, [ctypes.c_int64] * 2 + [ctypes.c_int]
+                      + [ctypes.POINTER(ctypes.c_int64)] * 2),
+    "gemm_mx_quantize": (ctypes.c_int, [ctypes.c_int64] * 2 + [ctypes.c_int] * 2
+                         + [ctypes.c_void_p] * 6),
+    "gemm_mx_values": (ctypes.c_int, [ctypes.c_int64] * 2 + [ctypes.c_int]
+                       + [ctypes.c_void_p] * 3 + [ctypes.c_int] + [ctypes.c_void_p] * 2),
+    "gemm_mx_create_plan": (ctypes.c_void_p, [ctypes.c_int64] * 3 + [ctypes.c_int] * 2),
+    "gemm_mx_create_plan_ex": (ctypes.c_void_p, [ctypes.c_int64] * 3 + [ctypes.c_int] * 4),
+    "gemm_mx_run": (ctypes.c_int, [ctypes.c_void_p] * 9),
+    "gemm_mx_set_wait": (ctypes.c_int, [ctypes.c_void_p] + [ctypes.c_int] * 2),
+    "gemm_mx_get_device_status": (ctypes.c_int, [ctypes.c_void_p]),
+    "gemm_mx_destroy": (None, [ctypes.c_void_p]),
+    "gemm_mx_describe": (ctypes.c_char_p, [ctypes.c_void_p]),
+    # include/tmalayer.h
+    "gemm_rms_norm": (ctypes.c_int, [ctypes.c_int64] * 2 + [ctypes.c_void_p] * 3
+                      + [ctypes.c_float] + [ctypes.c_void_p] * 2 + [ctypes.c_int]
+                      + [ctypes.c_void_p] * 3),
+    "gemm_rms_norm_grad_workspace": (ctypes.c_int64, [ctypes.c_int64] * 2),
+    "gemm_rms_norm_grad": (ctypes.c_int, [ctypes.c_int64] * 2 + [ctypes.c_void_p] * 4
+                           + [ctypes.c_float] + [ctypes.c_void_p] * 4),
+    "gemm_clip_create_plan": (ctypes.c_void_p, [ctypes.c_int64] + [ctypes.c_void_p] * 4),
+    "gemm_clip_run": (ctypes.c_int, [ctypes.c_void_p] + [ctypes.c_float] * 2
+                      + [ctypes.c_void_p] * 3),
+    "gemm_clip_norm": (ctypes.c_int, [ctypes.c_void_p] * 4),
+    "gemm_clip_destroy": (None, [ctypes.c_void_p]),
 }
 
 _lib = None

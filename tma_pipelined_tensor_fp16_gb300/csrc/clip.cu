@@ -1,0 +1,351 @@
+// clip.cu -- the global norm of many gradient tensors, and clipping to it.  Two launches:
+// sums of squares, one per CTA, and then the scaled values, for which every CTA adds the
+// sums up for itself in the same order.  Bound by memory: the gradients are read twice
+// (the second time from the end, where the L2 still holds the last of them) and
+// written once.
+#include <algorithm>
+#include <cmath>
+#include <memory>
+#include <new>
+#include <vector>
+
+#include "../../include/tmalayer.h"
+#include "device_common.cuh"
+#include "launch.h"
+#include "runtime.h"
+
+using namespace tg;
+
+namespace {
+
+constexpr int64_t CHUNK = 16384;  // values of a tensor that a CTA takes at a time
+constexpr int CLIP_THREADS = 512;
+constexpr int MAX_PARTS = GEMM_CLIP_WORKSPACE_BYTES / 8;
+
+// A piece of a tensor.
+struct Chunk {
+    const void* src;
+    void* dst;
+    int count;
+    int f16;
+    int64_t pad;
+};
+static_assert(sizeof(Chunk) == 32, "two 16-byte loads");
+
+}  // namespace
+
+struct gemm_clip_plan {
+    Chunk* d_chunks;
+    int64_t chunks;
+    int device, grid;
+};
+
+namespace {
+
+__device__ __forceinline__ Chunk load_chunk(const Chunk* table, int64_t i)
+{
+    const int4* from = reinterpret_cast<const int4*>(table + i);
+    int4 v[2] = {__ldg(from), __ldg(from + 1)};
+    return *reinterpret_cast<Chunk*>(v);
+}
+
+// Sum of squares of four to eight values: in fp32 while no square leaves its range,
+// else (rare) in fp64.
+template <int N>
+__device__ __forceinline__ double square_sum(const float (&x)[N])
+{
+    float s = 0.0f, most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        s = fmaf(x[i], x[i], s);
+        most = fmaxf(most, fabsf(x[i]));
+    }
+    // 2^-50 <= most <= 2^60: the largest square and the sum are normal numbers, and
+    // what smaller squares lose is below 2^-49 of them
+    if (most > 0x1p60f || (most < 0x1p-50f && most > 0.0f)) {
+        double d = 0.0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) d = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), d);
+        return d;
+    }
+    return static_cast<double>(s);
+}
+
+__device__ __forceinline__ void widen(const uint4& v, float (&x)[8])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ double block_sum(double s, double* shared)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane_id() == 0) shared[threadIdx.x / 32] = s;
+    __syncthreads();
+    s = 0.0;
+    for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) s += shared[i];
+    return s;
+}
+
+__global__ void __launch_bounds__(CLIP_THREADS) k_grad_squares(const Chunk* table, int64_t chunks,
+                                                               double* parts)
+{
+    __shared__ double shared[CLIP_THREADS / 32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int tid = static_cast<int>(threadIdx.x);
+    double sum = 0.0;
+    for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const Chunk k = load_chunk(table, c);
+        const bool vectors = (reinterpret_cast<uintptr_t>(k.src) & 15u) == 0;
+        int done = 0;
+        if (k.f16) {
+            const __half* src = static_cast<const __half*>(k.src);
+            if (vectors) {
+                done = k.count & ~7;
+                const uint4* v = reinterpret_cast<const uint4*>(src);
+#pragma unroll 4
+                for (int i = tid; i < done / 8; i += CLIP_THREADS) {
+                    float x[8];
+                    widen(v[i], x);
+                    sum += square_sum(x);
+                }
+            }
+            for (int i = done + tid; i < k.count; i += CLIP_THREADS) {
+                const float x[1] = {__half2float(src[i])};
+                sum += square_sum(x);
+            }
+        } else {
+            const float* src = static_cast<const float*>(k.src);
+            if (vectors) {
+                done = k.count & ~3;
+                const float4* v = reinterpret_cast<const float4*>(src);
+#pragma unroll 8
+                for (int i = tid; i < done / 4; i += CLIP_THREADS) {
+                    const float4 f = v[i];
+                    const float x[4] = {f.x, f.y, f.z, f.w};
+                    sum += square_sum(x);
+                }
+            }
+            for (int i = done + tid; i < k.count; i += CLIP_THREADS) {
+                const float x[1] = {src[i]};
+                sum += square_sum(x);
+            }
+        }
+    }
+    sum = block_sum(sum, shared);
+    if (tid == 0) parts[blockIdx.x] = sum;
+}
+
+__global__ void __launch_bounds__(CLIP_THREADS)
+    k_grad_clip(const Chunk* table, int64_t chunks, const double* parts, int part_count,
+                float max_norm, float eps, float* norm, int scale)
+{
+    __shared__ double shared[CLIP_THREADS / 32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int tid = static_cast<int>(threadIdx.x);
+    double sum = 0.0;
+    for (int i = tid; i < part_count; i += CLIP_THREADS) sum += parts[i];
+    sum = block_sum(sum, shared);
+    const double length = sqrt(sum);
+    if (blockIdx.x == 0 && tid == 0) *norm = static_cast<float>(length);
+    if (!scale) return;
+    const double ratio = static_cast<double>(max_norm) / (length + static_cast<double>(eps));
+    // NaN stays NaN; no length, nothing to scale (and perhaps no quotient)
+    const double factor = ratio >= 1.0 || length == 0.0 ? 1.0 : ratio;
+    // in two steps, the first a power of two: fp32 does not hold the smallest factors whole
+    const float first = factor < 0x1p-100 ? 0x1p-64f : 1.0f;
+    const float f = static_cast<float>(factor / static_cast<double>(first));
+    for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const Chunk k = load_chunk(table, chunks - 1 - c);
+        const bool vectors =
+            ((reinterpret_cast<uintptr_t>(k.src) | reinterpret_cast<uintptr_t>(k.dst)) & 15u) == 0;
+        if (f == 1.0f && k.src == k.dst) continue;  // the values stay what they are
+        int done = 0;
+        if (k.f16) {
+            const __half* src = static_cast<const __half*>(k.src);
+            __half* dst = static_cast<__half*>(k.dst);
+            if (vectors) {
+                done = k.count & ~7;
+#pragma unroll 4
+                for (int i = tid; i < done / 8; i += CLIP_THREADS) {
+                    float x[8];
+                    widen(reinterpret_cast<const uint4*>(src)[i], x);
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const __half2 h = __floats2half2_rn(x[2 * j] * first * f, x[2 * j + 1] * first * f);
+                        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            for (int i = done + tid; i < k.count; i += CLIP_THREADS)
+                dst[i] = __float2half_rn(__half2float(src[i]) * first * f);
+        } else {
+            const float* src = static_cast<const float*>(k.src);
+            float* dst = static_cast<float*>(k.dst);
+            if (vectors) {
+                done = k.count & ~3;
+#pragma unroll 8
+                for (int i = tid; i < done / 4; i += CLIP_THREADS) {
+                    float4 v = reinterpret_cast<const float4*>(src)[i];
+                    v.x = v.x * first * f;
+                    v.y = v.y * first * f;
+                    v.z = v.z * first * f;
+                    v.w = v.w * first * f;
+                    reinterpret_cast<float4*>(dst)[i] = v;
+                }
+            }
+            for (int i = done + tid; i < k.count; i += CLIP_THREADS) dst[i] = src[i] * first * f;
+        }
+    }
+}
+
+// Whether no output shares memory with another output, or with a gradient other than the
+// one at the same place (a sweep over the tensors by their addresses).
+bool outputs_apart(int64_t count, const void* const* grads, void* const* outs,
+                   const int64_t* sizes, const int* dtypes)
+{
+    struct Span {
+        uintptr_t begin, end;
+        bool out;
+    };
+    std::vector<Span> spans;
+    for (int64_t i = 0; i < count; ++i) {
+        if (sizes[i] == 0) continue;
+        const uintptr_t bytes = static_cast<uintptr_t>(sizes[i]) * (dtypes[i] == GEMM_OUT_F16 ? 2 : 4);
+        const uintptr_t to = reinterpret_cast<uintptr_t>(outs[i]);
+        const uintptr_t from = reinterpret_cast<uintptr_t>(grads[i]);
+        spans.push_back({to, to + bytes, true});
+        if (from != to) spans.push_back({from, from + bytes, false});
+    }
+    std::sort(spans.begin(), spans.end(),
+              [](const Span& a, const Span& b) { return a.begin < b.begin; });
+    uintptr_t outs_end = 0, any_end = 0;
+    for (const Span& s : spans) {
+        if (s.begin < (s.out ? any_end : outs_end)) return false;
+        any_end = std::max(any_end, s.end);
+        if (s.out) outs_end = std::max(outs_end, s.end);
+    }
+    return true;
+}
+
+int run_clip(const gemm_clip_plan* plan, float max_norm, float eps, float* norm, void* workspace,
+             void* cuda_stream, bool scale)
+{
+    if (!plan) return fail(GEMM_ERR_INVALID_ARG, "plan is NULL");
+    if (!norm || !workspace)
+        return fail(GEMM_ERR_INVALID_ARG, "norm and workspace must be non-NULL");
+    if (reinterpret_cast<uintptr_t>(norm) & 3u || !aligned16(workspace))
+        return fail(GEMM_ERR_UNSUPPORTED, "norm must be 4-byte and workspace 16-byte aligned");
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail("cudaGetDevice", e);
+    if (dev != plan->device)
+        return fail(GEMM_ERR_INVALID_ARG, "plan was created on another device");
+    cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    const Chunk* table = plan->d_chunks;
+    double* parts = static_cast<double*>(workspace);
+    const dim3 grid(static_cast<unsigned>(plan->grid)), block(CLIP_THREADS);
+    e = launch_dependent(k_grad_squares, grid, block, 0, 1, stream, table, plan->chunks, parts);
+    if (e == cudaSuccess)
+        e = launch_dependent(k_grad_clip, scale ? grid : dim3(1), block, 0, 1, stream, table,
+                             plan->chunks, static_cast<const double*>(parts), plan->grid, max_norm,
+                             eps, norm, scale ? 1 : 0);
+    return e == cudaSuccess ? ok() : cuda_fail("clipping launch", e);
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_clip_plan* gemm_clip_create_plan(int64_t count, const void* const* grads, void* const* outs,
+                                      const int64_t* sizes, const int* dtypes)
+{
+    gemm_clip_plan* made = nullptr;
+    guarded([&] {
+        if (count < 0 || (count > 0 && (!grads || !outs || !sizes || !dtypes)))
+            return fail(GEMM_ERR_INVALID_ARG,
+                        "grads, outs, sizes and dtypes must hold `count` entries");
+        std::vector<Chunk> table;
+        for (int64_t i = 0; i < count; ++i) {
+            if (dtypes[i] != GEMM_OUT_F32 && dtypes[i] != GEMM_OUT_F16)
+                return fail(GEMM_ERR_INVALID_ARG,
+                            "dtypes must be GEMM_OUT_F32 (0) or GEMM_OUT_F16 (1)");
+            if (sizes[i] < 0) return fail(GEMM_ERR_INVALID_ARG, "sizes must be >= 0");
+            if (sizes[i] == 0) continue;
+            const int elt = dtypes[i] == GEMM_OUT_F16 ? 2 : 4;
+            const char* src = static_cast<const char*>(grads[i]);
+            char* dst = static_cast<char*>(outs[i]);
+            if (!src || !dst)
+                return fail(GEMM_ERR_INVALID_ARG, "a tensor's address is NULL");
+            if ((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) % elt != 0)
+                return fail(GEMM_ERR_UNSUPPORTED, "a tensor is not aligned to its values");
+            for (int64_t at = 0; at < sizes[i]; at += CHUNK) {
+                Chunk c = {};
+                c.src = src + at * elt;
+                c.dst = dst + at * elt;
+                c.count = static_cast<int>(std::min(CHUNK, sizes[i] - at));
+                c.f16 = elt == 2;
+                table.push_back(c);
+            }
+        }
+        if (!outputs_apart(count, grads, outs, sizes, dtypes))
+            return fail(GEMM_ERR_INVALID_ARG,
+                        "an output overlaps another one, or a gradient that is not its own");
+        int dev, sms;
+        const int r = require_device(&dev, &sms, nullptr);
+        if (r != GEMM_OK) return r;
+        std::unique_ptr<gemm_clip_plan> plan(new gemm_clip_plan{});
+        plan->chunks = static_cast<int64_t>(table.size());
+        plan->device = dev;
+        plan->grid = static_cast<int>(std::max<int64_t>(
+            1, std::min<int64_t>(plan->chunks, std::min(4 * sms, MAX_PARTS))));
+        if (!table.empty()) {
+            const size_t bytes = table.size() * sizeof(Chunk);
+            cudaError_t e = cudaMalloc(&plan->d_chunks, bytes);
+            if (e == cudaSuccess)
+                e = cudaMemcpy(plan->d_chunks, table.data(), bytes, cudaMemcpyHostToDevice);
+            if (e != cudaSuccess) {
+                if (plan->d_chunks) cudaFree(plan->d_chunks);
+                return cuda_fail("allocating the table of gradients", e);
+            }
+        }
+        made = plan.release();
+        return ok();
+    });
+    return made;
+}
+
+int gemm_clip_run(gemm_clip_plan* plan, float max_norm, float eps, float* norm, void* workspace,
+                  void* cuda_stream)
+{
+    return guarded([&] {
+        if (!(max_norm >= 0.0f) || !(eps >= 0.0f))
+            return fail(GEMM_ERR_INVALID_ARG, "max_norm and eps must be >= 0");
+        return run_clip(plan, max_norm, eps, norm, workspace, cuda_stream, true);
+    });
+}
+
+int gemm_clip_norm(gemm_clip_plan* plan, float* norm, void* workspace, void* cuda_stream)
+{
+    return guarded(
+        [&] { return run_clip(plan, 0.0f, 0.0f, norm, workspace, cuda_stream, false); });
+}
+
+void gemm_clip_destroy(gemm_clip_plan* plan)
+{
+    if (!plan) return;
+    if (plan->d_chunks) cudaFree(plan->d_chunks);
+    delete plan;
+}
+
+}  // extern "C"

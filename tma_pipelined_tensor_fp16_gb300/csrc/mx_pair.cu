@@ -1,0 +1,273 @@
+// mx_pair.cu -- block-scaled products on CTA pairs: tiles of 256 x 256 with
+// tcgen05.mma.cta_group::2, each CTA holding 128 rows of A, 128 of B, and the scales of
+// its rows of A and of all of B's; clusters take tiles t, t + clusters, ... of the grouped
+// raster.
+//
+// Tensor memory: two accumulators of 256 columns would leave no room for scales.  They
+// lie at columns 0 and 192 and share 64; scales take columns 448 on.  The epilogue reads
+// the shared columns first and gives them up, so the next tile's MMAs wait for a quarter
+// of a tile's reading and not for its stores.
+#include "mx_product.cuh"
+#include "runtime.h"
+
+namespace tg {
+
+namespace {
+
+constexpr int MX_THREADS = 192;
+constexpr int TILE = 256;
+constexpr uint32_t ACC_SHIFT = 192;   // second accumulator
+constexpr uint32_t SCALE_COL = 448;
+constexpr uint32_t TMEM_COLS = 512;
+
+}  // namespace
+
+template <int FORMAT, bool F16OUT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
+    k_mx_pair(const __grid_constant__ CUtensorMap tmAc, const __grid_constant__ CUtensorMap tmAs,
+              const __grid_constant__ CUtensorMap tmBc, const __grid_constant__ CUtensorMap tmBs,
+              const __grid_constant__ CUtensorMap tmC, const __grid_constant__ MxParams p)
+{
+    constexpr int GROUPS = mx_stage_groups(FORMAT);
+    constexpr int STEPS = MX_STAGE_CHUNKS / 2;
+    constexpr int SCALES = mx_step_scales<FORMAT>;
+    constexpr uint32_t CTA_TX = 2 * MX_STAGE_CHUNKS * MX_CHUNK_BYTES + 3 * GROUPS * MX_GROUP_BYTES;
+    static_assert(SCALE_COL + GROUPS * 12 <= TMEM_COLS, "scales fit");
+    extern __shared__ __align__(1024) uint8_t mx_smem[];
+    const uint32_t raw = smem_u32(mx_smem);
+    const uint32_t base = align1024(raw);
+    uint8_t* gen = mx_smem + (base - raw);
+    const int D = p.pipe_depth;
+    const MxPairLayout L = mx_pair_layout(FORMAT, D);
+    const uint32_t staging = base + L.staging;
+    const uint32_t bars = base + L.bars;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gen + L.bars + TMEM_SLOT_OFFSET);
+    const int warp = static_cast<int>(threadIdx.x) >> 5;
+    const uint32_t lane = lane_id();
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int clusters = static_cast<int>(gridDim.x) / 2;
+    const int first = static_cast<int>(blockIdx.x) / 2;
+    const int tiles = p.tiles_m * p.tiles_n;
+    Watchdog wd = mx_watchdog(p);
+    auto bar = [&](int slot) { return bars + static_cast<uint32_t>(slot) * 8u; };
+
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmAc);
+        prefetch_tensormap(&tmAs);
+        prefetch_tensormap(&tmBc);
+        prefetch_tensormap(&tmBs);
+        prefetch_tensormap(&tmC);
+        for (int s = 0; s < D; ++s) {
+            mbar_init(bar(BAR_FULL + s), 1);   // leader: its producer
+            mbar_init(bar(BAR_EMPTY + s), 1);  // the leader's multicast commit
+        }
+        mbar_init(bar(BAR_TMEM_FULL), 1);      // the leader's multicast commit
+        mbar_init(bar(BAR_TMEM_EMPTY), 8);     // leader: 4 epilogue warps x 2 CTAs
+        mbar_init(bar(BAR_DRAIN), 1);
+        mbar_init(bar(BAR_STALL), 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+        tmem_relinquish_alloc_permit_pair();
+    }
+    tc_fence_before_sync();
+    cluster_sync_all();
+    tc_fence_after_sync();
+    griddep_wait();
+    griddep_launch_dependents();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == 0) {
+        // ---------------------------------------------------- producer
+        if (p.debug_stall == 1) wd.wait(bar(BAR_STALL), 0, WAIT_STALL, -1, -1);
+        int stage = 0;
+        uint32_t phase = 0;
+        int armed = 0;
+        for (int t = first; t < tiles && !wd.aborted; t += clusters) {
+            int mt, nt;
+            raster_tile(t, p.tiles_m, p.tiles_n, p.group_m, mt, nt);
+            const int a_block = mt * 2 + static_cast<int>(rank);
+            const int b_block = nt * 2 + static_cast<int>(rank);
+            for (int s = 0; s < p.stages; ++s) {
+                const bool ok = wd.wait(bar(BAR_EMPTY + stage), phase ^ 1u, WAIT_EMPTY, t, s);
+                if (!ok) break;
+                if (lane == 0) {
+                    const uint32_t at = base + static_cast<uint32_t>(stage) * L.stage;
+                    if (leader) mbar_arrive_expect_tx(bar(BAR_FULL + stage), 2 * CTA_TX);
+                    const uint32_t full = map_shared_rank(bar(BAR_FULL + stage), 0);
+                    const int c = s * MX_STAGE_CHUNKS, g = s * GROUPS;
+                    tma_load_2d_pair(at, &tmAc, full, 0, a_block * p.chunks + c);
+                    tma_load_2d_pair(at + L.b_codes, &tmBc, full, 0, b_block * p.chunks + c);
+                    tma_load_2d_pair(at + L.a_scales, &tmAs, full, 0, a_block * p.groups + g);
+                    tma_load_2d_pair(at + L.b_scales, &tmBs, full, 0, nt * 2 * p.groups + g);
+                    tma_load_2d_pair(at + L.b_scales + GROUPS * MX_GROUP_BYTES, &tmBs, full, 0,
+                                     (nt * 2 + 1) * p.groups + g);
+                }
+                ++armed;
+                __syncwarp();
+                if (++stage == D) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        // The copies in flight land before the CTAs can exit: the leader drains the phases it
+        // armed, which take in the peer's copies; a peer that gave up allows a grace
+        // period too, as its leader may not have armed a phase for them.
+        if (lane == 0) {
+            if (leader) {
+                for (int i = 0; i < D && i < armed; ++i) {
+                    if (stage == 0) {
+                        stage = D - 1;
+                        phase ^= 1u;
+                    } else {
+                        --stage;
+                    }
+                    wd.drain(bar(BAR_FULL + stage), phase);
+                }
+            } else if (wd.aborted) {
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 200000ull) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ----------------------------------------- MMA issuer (leader)
+        if (leader) {
+            const uint32_t elected = lane == 0 ? 1u : 0u;
+            const uint32_t a_sc = tmem_base + SCALE_COL;
+            const uint32_t b_sc = a_sc + GROUPS * 4;
+            int stage = 0;
+            uint32_t phase = 0;
+            int j = 0;
+            for (int t = first; t < tiles && !wd.aborted; t += clusters, ++j) {
+                if (j > 0)
+                    wd.wait(bar(BAR_TMEM_EMPTY), static_cast<uint32_t>(j - 1) & 1u,
+                            WAIT_TMEM_EMPTY, t, -1);
+                tc_fence_after_sync();
+                const uint32_t d_tmem = tmem_base + (j & 1 ? ACC_SHIFT : 0u);
+                for (int s = 0; s < p.stages; ++s) {
+                    const bool ok = wd.wait(bar(BAR_FULL + stage), phase, WAIT_FULL, t, s);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    tc_fence_after_sync();
+                    const uint32_t at = base + static_cast<uint32_t>(stage) * L.stage;
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g) {
+                        const uint32_t off = g * MX_GROUP_BYTES;
+                        copy_scales<true>(elected, a_sc + g * 4, at + L.a_scales + off);
+                        copy_scales<true>(elected, b_sc + g * 8, at + L.b_scales + off);
+                        copy_scales<true>(elected, b_sc + g * 8 + 4,
+                                          at + L.b_scales + GROUPS * MX_GROUP_BYTES + off);
+                    }
+                    const uint64_t a_desc = core_desc(at, MX_CHUNK_BYTES);
+                    const uint64_t b_desc = core_desc(at + L.b_codes, MX_CHUNK_BYTES);
+                    const int left = p.steps - s * STEPS;
+#pragma unroll
+                    for (int i = 0; i < STEPS; ++i) {
+                        if (i >= left) break;  // uniform
+                        mx_mma<FORMAT, true>(elected, d_tmem,
+                                             a_desc + i * (2 * MX_CHUNK_BYTES >> 4),
+                                             b_desc + i * (2 * MX_CHUNK_BYTES >> 4),
+                                             mx_idesc<FORMAT>(TILE, TILE, i * SCALES % 4),
+                                             a_sc + i * SCALES / 4 * 4, b_sc + i * SCALES / 4 * 8,
+                                             s == 0 && i == 0 ? 0u : 1u);
+                    }
+                    mx_commit_pair(elected, bar(BAR_EMPTY + stage));
+                    __syncwarp();
+                    if (++stage == D) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (__all_sync(0xffffffffu, !wd.aborted)) mx_commit_pair(elected, bar(BAR_TMEM_FULL));
+            }
+            if (lane == 0) {
+                mma_commit_pair_multicast(bar(BAR_DRAIN), static_cast<uint16_t>(1u));
+                wd.drain(bar(BAR_DRAIN), 0);
+            }
+            __syncwarp();
+        }
+    } else {
+        // -------------------------------------------------------- epilogue
+        if (p.debug_stall == 2) wd.wait(bar(BAR_STALL), 0, WAIT_STALL, -1, -1);
+        constexpr int SUB = F16OUT ? 64 : 32;  // columns of 128 bytes
+        constexpr int SUBS = TILE / SUB;
+        constexpr int SHARED_SUBS = (TILE - static_cast<int>(ACC_SHIFT)) / SUB;
+        const uint32_t q = static_cast<uint32_t>(warp & 3);
+        const uint32_t row = q * 32u + lane;
+        const uint32_t to_leader = map_shared_rank(bar(BAR_TMEM_EMPTY), 0);
+        const float alpha = mx_alpha(p);
+        uint32_t sub_count = 0;
+        int j = 0;
+        for (int t = first; t < tiles; t += clusters, ++j) {
+            int mt, nt;
+            raster_tile(t, p.tiles_m, p.tiles_n, p.group_m, mt, nt);
+            const bool ok =
+                wd.wait(bar(BAR_TMEM_FULL), static_cast<uint32_t>(j) & 1u, WAIT_TMEM_FULL, t, -1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after_sync();
+            const uint32_t taddr = tmem_base + (j & 1 ? ACC_SHIFT : 0u) + (q * 32u << 16);
+            const int m0 = mt * TILE + static_cast<int>(rank) * MX_ROWS;
+            // the columns that the next tile's accumulator shares come first
+            const int start = j & 1 ? 0 : SUBS - SHARED_SUBS;
+#pragma unroll 1
+            for (int i = 0; i < SUBS; ++i) {
+                const int sub = (start + i) % SUBS;
+                const int col0 = nt * TILE + sub * SUB;
+                uint32_t v[SUB];
+                if (col0 < p.N) {
+#pragma unroll
+                    for (int h = 0; h < SUB; h += 32)
+                        tmem_load_32cols(taddr + sub * SUB + h,
+                                         *reinterpret_cast<uint32_t(*)[32]>(&v[h]));
+                }
+                if (i == SHARED_SUBS - 1) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(to_leader);
+                }
+                if (col0 < p.N) {
+#pragma unroll
+                    for (int c = 0; c < SUB; ++c)
+                        v[c] = __float_as_uint(__uint_as_float(v[c]) * alpha);
+                    stage_and_store<F16OUT>(v, row, staging, &tmC, col0, m0, p.M, sub_count, true);
+                }
+            }
+        }
+        if (lane == 0) bulk_wait_group<0>();
+        __syncwarp();
+    }
+
+    // nothing of either CTA is touched remotely after this point
+    tc_fence_before_sync();
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    }
+}
+
+template <int FORMAT>
+static cudaError_t launch_format(const MxSpec& s, cudaStream_t stream)
+{
+    auto kernel = s.f16out ? k_mx_pair<FORMAT, true> : k_mx_pair<FORMAT, false>;
+    cudaError_t e = ensure_smem_limit(kernel, s.smem_bytes);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(s.grid_x)), dim3(MX_THREADS),
+                            s.smem_bytes, 1, stream, *s.codes_u, *s.scales_u, *s.codes_v,
+                            *s.scales_v, *s.out, s.p);
+}
+
+cudaError_t launch_mx_pair(const MxSpec& s, cudaStream_t stream)
+{
+    switch (s.format) {
+    case MXFP8: return launch_format<MXFP8>(s, stream);
+    case MXFP4: return launch_format<MXFP4>(s, stream);
+    default: return launch_format<NVFP4>(s, stream);
+    }
+}
+
+}  // namespace tg

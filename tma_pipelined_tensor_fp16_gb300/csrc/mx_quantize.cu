@@ -1,0 +1,540 @@
+// mx_quantize.cu -- fp16 matrices to the block-scaled formats of include/tmamicro.h and
+// back.  All kernels are bound by memory: every value is read once (twice where the
+// tensor scale has to be found first) and its codes and scales are written once.
+#include <algorithm>
+
+#include "../../include/tmamicro.h"
+#include "device_common.cuh"
+#include "launch.h"
+#include "microscale.cuh"
+#include "runtime.h"
+
+namespace tg {
+
+namespace {
+
+constexpr int AMAX_PARTS = GEMM_MX_WORKSPACE_BYTES / 4;
+
+struct QuantizeParams {
+    int64_t rows, K;  // of the quantised matrix
+    int64_t chunks, groups;
+    const __half* X;
+    uint8_t* codes;
+    uint8_t* scales;
+    float* tensor_scale;
+    const uint32_t* parts;  // largest magnitudes of parts of X, or nullptr
+    int part_count;
+};
+
+// ------------------------------------------------------------ tensor scale
+
+// Largest finite magnitude of each CTA's share of `vecs` vectors of eight values.
+// Magnitudes of fp16 compare as their bits; infinities and NaN do not count.
+__global__ void __launch_bounds__(512) k_mx_most(const uint4* X, int64_t vecs, uint32_t* parts)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    uint32_t most = 0;
+    auto take = [&](uint32_t w) {
+        const uint32_t a = w & 0x7fffu, b = (w >> 16) & 0x7fffu;
+        if (a < 0x7c00u) most = max(most, a);
+        if (b < 0x7c00u) most = max(most, b);
+    };
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    for (; i + 3 * step < vecs; i += 4 * step) {
+        uint4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = X[i + j * step];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            take(v[j].x);
+            take(v[j].y);
+            take(v[j].z);
+            take(v[j].w);
+        }
+    }
+    for (; i < vecs; i += step) {
+        const uint4 v = X[i];
+        take(v.x);
+        take(v.y);
+        take(v.z);
+        take(v.w);
+    }
+    __shared__ uint32_t warps[16];
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane_id() == 0) warps[threadIdx.x / 32] = most;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        most = threadIdx.x < blockDim.x / 32 ? warps[threadIdx.x] : 0u;
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (threadIdx.x == 0) {
+            const float f = __half2float(__ushort_as_half(static_cast<unsigned short>(most)));
+            parts[blockIdx.x] = __float_as_uint(f);
+        }
+    }
+}
+
+// The tensor scale (nvfp4): from the parts, by every CTA for itself, or as given.
+template <int FORMAT>
+__device__ __forceinline__ float find_tensor_scale(const QuantizeParams& p, uint32_t* shared)
+{
+    if constexpr (FORMAT != NVFP4) return 1.0f;
+    if (p.parts == nullptr) {
+        const uint32_t e = (__float_as_uint(*p.tensor_scale) >> 23) & 0xffu;
+        return power_of_two(static_cast<int>(min(max(e, 1u), 254u)) - 127);
+    }
+    uint32_t most = 0;
+    for (int i = static_cast<int>(threadIdx.x); i < p.part_count; i += static_cast<int>(blockDim.x))
+        most = max(most, p.parts[i]);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane_id() == 0) shared[threadIdx.x / 32] = most;
+    __syncthreads();
+    most = 0;
+    for (int i = 0; i < static_cast<int>(blockDim.x / 32); ++i) most = max(most, shared[i]);
+    const float t = tensor_scale_of(most);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.tensor_scale = t;
+    return t;
+}
+
+// --------------------------------------------------------------- along rows
+//
+// A lane holds eight consecutive values; four lanes a block of 32, eight rows a warp.
+// So a warp's load touches 64 contiguous bytes of each of eight rows, and a store 128
+// contiguous bytes of a chunk's column.  A warp takes 8 rows x 128 values: a group of
+// four scales (two of nvfp4) is one 32-bit store.
+constexpr int ROW_WARPS = 8;
+constexpr int ROW_K = 128;  // values of a row per warp
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+template <int FORMAT>
+__global__ void __launch_bounds__(ROW_WARPS * 32)
+    k_mx_quantize(const __grid_constant__ QuantizeParams p, int64_t spans, int64_t tiles)
+{
+    __shared__ uint32_t shared[ROW_WARPS];
+    griddep_wait();
+    griddep_launch_dependents();
+    const float t = find_tensor_scale<FORMAT>(p, shared);
+    const float sixth = 1.0f / (6.0f * t);
+    const int lane = static_cast<int>(lane_id());
+    const int r = lane / 4, part = lane % 4;
+    const int64_t tile = static_cast<int64_t>(blockIdx.x) * ROW_WARPS + threadIdx.x / 32;
+    if (tile >= tiles) return;
+    const int64_t row = tile / spans * 8 + r;
+    const int64_t k0 = tile % spans * ROW_K;
+    const bool valid = row < p.rows;
+    const __half* x_row = p.X + (valid ? row : 0) * p.K;
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t k = k0 + j * 32 + part * 8;
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (valid && k < p.K) v[j] = *reinterpret_cast<const uint4*>(x_row + k);
+    }
+    uint8_t* codes = p.codes + mx_code_offset(row, k0 / mx_chunk(FORMAT), p.chunks);
+    uint32_t bytes[4];
+    constexpr int PER_CHUNK = mx_chunk(FORMAT) / 8;  // lanes of a chunk
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float x[8];
+        unpack8(v[j], x);
+        const BlockScale b = block_scale<FORMAT>(block_most<FORMAT>(most_of(x)), t, sixth);
+        const uint2 q = encode8<FORMAT>(x, b);
+        const int chunk = (j * 4 + part) / PER_CHUNK;
+        if (valid && k0 / mx_chunk(FORMAT) + chunk < p.chunks) {
+            uint8_t* to = codes + chunk * MX_CHUNK_BYTES;
+            if constexpr (FORMAT == MXFP8)
+                reinterpret_cast<uint2*>(to)[part % PER_CHUNK] = q;
+            else
+                reinterpret_cast<uint32_t*>(to)[part % PER_CHUNK] = q.x;
+        }
+        bytes[j] = b.byte;
+    }
+    uint8_t* scales = p.scales + mx_scale_offset(row, k0 / mx_group(FORMAT), p.groups);
+    if constexpr (FORMAT == NVFP4) {
+        // 128 values are eight blocks: the second of a pair is two lanes on
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bytes[j] |= __shfl_down_sync(0xffffffffu, bytes[j], 2) << 8;
+        if (valid && part == 0) {
+            const int64_t g = k0 / mx_group(FORMAT);
+            reinterpret_cast<uint32_t*>(scales)[0] = bytes[0] | bytes[1] << 16;
+            if (g + 1 < p.groups)
+                *reinterpret_cast<uint32_t*>(scales + MX_GROUP_BYTES) = bytes[2] | bytes[3] << 16;
+        }
+    } else {
+        if (valid && part == 0)
+            *reinterpret_cast<uint32_t*>(scales) =
+                bytes[0] | bytes[1] << 8 | bytes[2] << 16 | bytes[3] << 24;
+    }
+}
+
+// ------------------------------------------------------------ along columns
+//
+// X is K x rows; a CTA takes 128 of K x 64 columns through shared memory, and a thread
+// two columns x 32 of K: a block (two of nvfp4) of each, 16 or 32 bytes of codes a
+// column.  The columns are rows of the result, so a warp stores 1 KB without gaps.
+constexpr int COL_THREADS = 128;
+constexpr int COL_COLS = 64;
+constexpr int COL_K = 128;
+
+template <int FORMAT>
+__global__ void __launch_bounds__(COL_THREADS)
+    k_mx_quantize_columns(const __grid_constant__ QuantizeParams p, int64_t col_tiles)
+{
+    __shared__ uint32_t shared[COL_THREADS / 32];
+    __shared__ __align__(16) uint32_t tile[COL_K][COL_COLS / 2];
+    __shared__ uint8_t scale_bytes[COL_COLS][8];
+    griddep_wait();
+    griddep_launch_dependents();
+    const float t = find_tensor_scale<FORMAT>(p, shared);
+    const float sixth = 1.0f / (6.0f * t);
+    const int tid = static_cast<int>(threadIdx.x);
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) % col_tiles * COL_COLS;
+    const int64_t k0 = static_cast<int64_t>(blockIdx.x) / col_tiles * COL_K;
+#pragma unroll
+    for (int i = 0; i < COL_K * COL_COLS / 8 / COL_THREADS; ++i) {
+        const int line = i * (COL_THREADS / 8) + tid / 8;
+        const int64_t k = k0 + line, c = c0 + tid % 8 * 8;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (k < p.K && c < p.rows) v = *reinterpret_cast<const uint4*>(p.X + k * p.rows + c);
+        *reinterpret_cast<uint4*>(&tile[line][tid % 8 * 4]) = v;
+    }
+    __syncthreads();
+    const int pair = tid % 32, part = tid / 32;  // two columns, 32 of K
+    uint32_t w[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) w[i] = tile[part * 32 + i][pair];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t row = c0 + pair * 2 + h;  // of the result
+        constexpr int BLOCK = mx_block(FORMAT);
+        uint32_t out[8];
+#pragma unroll
+        for (int b0 = 0; b0 < 32; b0 += BLOCK) {
+            uint32_t most = 0;
+#pragma unroll
+            for (int i = 0; i < BLOCK; ++i) most = max(most, (w[b0 + i] >> (16 * h)) & 0x7fffu);
+            // magnitudes of fp16 order as their bits, NaN above the infinity
+            const BlockScale b = block_scale<FORMAT>(
+                __half2float(__ushort_as_half(static_cast<unsigned short>(most))), t, sixth);
+#pragma unroll
+            for (int i0 = 0; i0 < BLOCK; i0 += 8) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[i] = __half2float(__ushort_as_half(
+                        static_cast<unsigned short>(w[b0 + i0 + i] >> (16 * h))));
+                const uint2 q = encode8<FORMAT>(x, b);
+                if constexpr (FORMAT == MXFP8) {
+                    out[(b0 + i0) / 4] = q.x;
+                    out[(b0 + i0) / 4 + 1] = q.y;
+                } else {
+                    out[(b0 + i0) / 8] = q.x;
+                }
+            }
+            scale_bytes[pair * 2 + h][(part * 32 + b0) / BLOCK] = static_cast<uint8_t>(b.byte);
+        }
+        if (row < p.rows) {
+            constexpr int CHUNKS = 32 / mx_chunk(FORMAT);
+            const int64_t chunk = (k0 + part * 32) / mx_chunk(FORMAT);
+            uint8_t* to = p.codes + mx_code_offset(row, chunk, p.chunks);
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c)
+                if (chunk + c < p.chunks)
+                    *reinterpret_cast<uint4*>(to + c * MX_CHUNK_BYTES) =
+                        make_uint4(out[4 * c], out[4 * c + 1], out[4 * c + 2], out[4 * c + 3]);
+        }
+    }
+    __syncthreads();
+    constexpr int GROUPS = COL_K / mx_group(FORMAT);
+    for (int i = tid; i < COL_COLS * GROUPS; i += COL_THREADS) {
+        const int64_t row = c0 + i % COL_COLS;
+        const int64_t group = k0 / mx_group(FORMAT) + i / COL_COLS;
+        if (row < p.rows && group < p.groups)
+            *reinterpret_cast<uint32_t*>(p.scales + mx_scale_offset(row, group, p.groups)) =
+                *reinterpret_cast<const uint32_t*>(&scale_bytes[i % COL_COLS][i / COL_COLS * 4]);
+    }
+}
+
+// -------------------------------------------------------------------- values
+
+struct ValuesParams {
+    int64_t rows, K, chunks, groups;
+    const uint8_t* codes;
+    const uint8_t* scales;
+    const float* tensor_scale;
+    void* values;
+};
+
+// Eight codes to fp16 pairs (exact).
+template <int FORMAT>
+__device__ __forceinline__ void decode8(uint2 q, __half2 (&v)[4])
+{
+    uint32_t h[4];
+    if constexpr (FORMAT == MXFP8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = i < 2 ? q.x : q.y;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
+                : "=r"(h[i])
+                : "h"(static_cast<uint16_t>(w >> (16 * (i & 1)))));
+        }
+    } else {
+        asm("{\n\t"
+            ".reg .b8 a, b, c, d;\n\t"
+            "mov.b32 {a, b, c, d}, %4;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %3, d;\n\t"
+            "}\n"
+            : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+            : "r"(q.x));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<__half2*>(&h[i]);
+}
+
+// Lanes as in k_mx_quantize: a warp takes 8 rows x 128 values.
+template <int FORMAT, bool F16OUT>
+__global__ void __launch_bounds__(ROW_WARPS * 32)
+    k_mx_values(const __grid_constant__ ValuesParams p, int64_t spans, int64_t tiles)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t tile = static_cast<int64_t>(blockIdx.x) * ROW_WARPS + threadIdx.x / 32;
+    if (tile >= tiles) return;
+    const int lane = static_cast<int>(lane_id());
+    const int64_t row = tile / spans * 8 + lane / 4;
+    if (row >= p.rows) return;
+    const int part = lane % 4;
+    const int64_t k0 = tile % spans * ROW_K;
+    const float t = p.tensor_scale ? *p.tensor_scale : 1.0f;
+    constexpr int PER_CHUNK = mx_chunk(FORMAT) / 8;
+    const uint8_t* codes = p.codes + mx_code_offset(row, k0 / mx_chunk(FORMAT), p.chunks);
+    const uint8_t* scales = p.scales + mx_scale_offset(row, k0 / mx_group(FORMAT), p.groups);
+    constexpr int GROUPS = ROW_K / mx_group(FORMAT);
+    uint32_t words[GROUPS];
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g)
+        words[g] = k0 / mx_group(FORMAT) + g < p.groups
+                       ? *reinterpret_cast<const uint32_t*>(scales + g * MX_GROUP_BYTES)
+                       : 0u;
+    uint2 q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t k = k0 + j * 32 + part * 8;
+        const int chunk = (j * 4 + part) / PER_CHUNK;
+        q[j] = make_uint2(0, 0);
+        if (k < p.K) {
+            if constexpr (FORMAT == MXFP8)
+                q[j] = reinterpret_cast<const uint2*>(codes + chunk * MX_CHUNK_BYTES)[part % PER_CHUNK];
+            else
+                q[j].x =
+                    reinterpret_cast<const uint32_t*>(codes + chunk * MX_CHUNK_BYTES)[part % PER_CHUNK];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t k = k0 + j * 32 + part * 8;
+        if (k >= p.K) break;
+        float s;
+        if constexpr (FORMAT == NVFP4) {
+            const int b = j * 2 + part / 2;
+            s = float_of_e4m3((words[b / 4] >> (8 * (b % 4))) & 0xffu) * t;
+        } else {
+            s = float_of_e8m0((words[0] >> (8 * j)) & 0xffu);
+        }
+        __half2 v[4];
+        decode8<FORMAT>(q[j], v);
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(v[i]);
+            x[2 * i] = f.x * s;
+            x[2 * i + 1] = f.y * s;
+        }
+        if (p.K % 8 != 0) {  // rows of odd lengths start anywhere
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (k + i >= p.K) break;
+                if constexpr (F16OUT)
+                    static_cast<__half*>(p.values)[row * p.K + k + i] = __float2half_rn(x[i]);
+                else
+                    static_cast<float*>(p.values)[row * p.K + k + i] = x[i];
+            }
+        } else if constexpr (F16OUT) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            *reinterpret_cast<uint4*>(static_cast<__half*>(p.values) + row * p.K + k) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            float4* to = reinterpret_cast<float4*>(static_cast<float*>(p.values) + row * p.K + k);
+            to[0] = make_float4(x[0], x[1], x[2], x[3]);
+            to[1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
+    }
+}
+
+int check_mx(int64_t rows, int64_t K, int format)
+{
+    if (format < MXFP8 || format > NVFP4)
+        return fail(GEMM_ERR_INVALID_ARG, "unknown gemm_mx_format");
+    if (rows < 0 || rows > MAX_COORDINATE || K < 1 || K > MAX_COORDINATE)
+        return fail(GEMM_ERR_INVALID_ARG, "rows must be in [0, 2^31-65536], K in [1, 2^31-65536]");
+    if ((mx_row_blocks(rows) + 1) * mx_chunks(K, format) > MAX_COORDINATE)
+        return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
+    return GEMM_OK;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_format(int format, void (*k8)(P...), void (*k4)(P...), void (*kn)(P...),
+                          int64_t grid, int threads, cudaStream_t stream, A... args)
+{
+    auto kernel = format == MXFP8 ? k8 : format == MXFP4 ? k4 : kn;
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)),
+                            dim3(static_cast<unsigned>(threads)), 0, 1, stream, args...);
+}
+
+}  // namespace
+
+}  // namespace tg
+
+using namespace tg;
+
+extern "C" {
+
+int gemm_mx_sizes(int64_t rows, int64_t K, int format, int64_t* codes_bytes, int64_t* scales_bytes)
+{
+    return guarded([&] {
+        const int r = check_mx(rows, K, format);
+        if (r != GEMM_OK) return r;
+        if (!codes_bytes || !scales_bytes)
+            return fail(GEMM_ERR_INVALID_ARG, "codes_bytes and scales_bytes must be non-NULL");
+        *codes_bytes = mx_row_blocks(rows) * mx_chunks(K, format) * MX_CHUNK_BYTES;
+        *scales_bytes = mx_row_blocks(rows) * mx_groups(K, format) * MX_GROUP_BYTES;
+        return ok();
+    });
+}
+
+int gemm_mx_quantize(int64_t rows, int64_t K, int format, int transpose, const void* X, void* codes,
+                     void* scales, float* tensor_scale, void* workspace, void* cuda_stream)
+{
+    return guarded([&] {
+        int r = check_mx(rows, K, format);
+        if (r != GEMM_OK) return r;
+        if ((transpose ? rows : K) % 8 != 0)
+            return fail(GEMM_ERR_UNSUPPORTED, "the rows of X must hold a multiple of 8 values");
+        if ((format == NVFP4) != (tensor_scale != nullptr))
+            return fail(GEMM_ERR_INVALID_ARG, "tensor_scale must be given exactly for GEMM_NVFP4");
+        if (rows > 0 && (!X || !codes || !scales))
+            return fail(GEMM_ERR_INVALID_ARG, "X, codes and scales must be non-NULL");
+        if (!aligned16(X) || !aligned16(codes) || !aligned16(scales))
+            return fail(GEMM_ERR_UNSUPPORTED, "X, codes and scales must be 16-byte aligned");
+        if ((reinterpret_cast<uintptr_t>(tensor_scale) | reinterpret_cast<uintptr_t>(workspace)) & 3u)
+            return fail(GEMM_ERR_UNSUPPORTED, "tensor_scale and workspace must be 4-byte aligned");
+        int dev, sms;
+        r = require_device(&dev, &sms, nullptr);
+        if (r != GEMM_OK) return r;
+        cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+        cudaError_t e = cudaSuccess;
+        QuantizeParams p = {};
+        p.rows = rows;
+        p.K = K;
+        p.chunks = mx_chunks(K, format);
+        p.groups = mx_groups(K, format);
+        p.X = static_cast<const __half*>(X);
+        p.codes = static_cast<uint8_t*>(codes);
+        p.scales = static_cast<uint8_t*>(scales);
+        p.tensor_scale = tensor_scale;
+        if (format == NVFP4 && workspace) {
+            const int64_t vecs = rows * K / 8;
+            const int64_t want = std::max<int64_t>(1, (vecs + 4 * 512 - 1) / (4 * 512));
+            p.part_count = static_cast<int>(std::min<int64_t>(want, std::min(4 * sms, AMAX_PARTS)));
+            p.parts = static_cast<const uint32_t*>(workspace);
+            e = launch_dependent(k_mx_most, dim3(static_cast<unsigned>(p.part_count)), dim3(512), 0,
+                                 1, stream, static_cast<const uint4*>(X), vecs,
+                                 static_cast<uint32_t*>(workspace));
+            if (e != cudaSuccess) return cuda_fail("tensor scale launch", e);
+        }
+        if (rows == 0 && format != NVFP4) return ok();
+        if (transpose) {
+            const int64_t cols = std::max<int64_t>(1, (rows + COL_COLS - 1) / COL_COLS);
+            const int64_t grid = cols * ((K + COL_K - 1) / COL_K);
+            if (grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
+            e = launch_format(format, k_mx_quantize_columns<MXFP8>, k_mx_quantize_columns<MXFP4>,
+                              k_mx_quantize_columns<NVFP4>, grid, COL_THREADS, stream, p, cols);
+        } else {
+            const int64_t spans = (K + ROW_K - 1) / ROW_K;
+            const int64_t tiles = (rows + 7) / 8 * spans;
+            const int64_t grid = std::max<int64_t>(1, (tiles + ROW_WARPS - 1) / ROW_WARPS);
+            if (grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
+            e = launch_format(format, k_mx_quantize<MXFP8>, k_mx_quantize<MXFP4>,
+                              k_mx_quantize<NVFP4>, grid, ROW_WARPS * 32, stream, p, spans, tiles);
+        }
+        return e == cudaSuccess ? ok() : cuda_fail("quantisation launch", e);
+    });
+}
+
+int gemm_mx_values(int64_t rows, int64_t K, int format, const void* codes, const void* scales,
+                   const float* tensor_scale, int dtype_out, void* values, void* cuda_stream)
+{
+    return guarded([&] {
+        int r = check_mx(rows, K, format);
+        if (r != GEMM_OK) return r;
+        if (dtype_out != GEMM_OUT_F32 && dtype_out != GEMM_OUT_F16)
+            return fail(GEMM_ERR_INVALID_ARG,
+                        "dtype_out must be GEMM_OUT_F32 (0) or GEMM_OUT_F16 (1)");
+        if (rows > 0 && (!codes || !scales || !values))
+            return fail(GEMM_ERR_INVALID_ARG, "codes, scales and values must be non-NULL");
+        if (!aligned16(codes) || !aligned16(scales) || !aligned16(values))
+            return fail(GEMM_ERR_UNSUPPORTED, "codes, scales and values must be 16-byte aligned");
+        if (tensor_scale && format != NVFP4)
+            return fail(GEMM_ERR_INVALID_ARG, "only GEMM_NVFP4 has a tensor_scale");
+        if (reinterpret_cast<uintptr_t>(tensor_scale) & 3u)
+            return fail(GEMM_ERR_UNSUPPORTED, "tensor_scale must be 4-byte aligned");
+        int dev;
+        r = require_device(&dev, nullptr, nullptr);
+        if (r != GEMM_OK) return r;
+        if (rows == 0) return ok();
+        ValuesParams p = {};
+        p.rows = rows;
+        p.K = K;
+        p.chunks = mx_chunks(K, format);
+        p.groups = mx_groups(K, format);
+        p.codes = static_cast<const uint8_t*>(codes);
+        p.scales = static_cast<const uint8_t*>(scales);
+        p.tensor_scale = tensor_scale;
+        p.values = values;
+        const int64_t spans = (K + ROW_K - 1) / ROW_K;
+        const int64_t tiles = (rows + 7) / 8 * spans;
+        const int64_t grid = (tiles + ROW_WARPS - 1) / ROW_WARPS;
+        if (grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
+        cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+        const cudaError_t e =
+            dtype_out == GEMM_OUT_F16
+                ? launch_format(format, k_mx_values<MXFP8, true>, k_mx_values<MXFP4, true>,
+                                k_mx_values<NVFP4, true>, grid, ROW_WARPS * 32, stream, p, spans,
+                                tiles)
+                : launch_format(format, k_mx_values<MXFP8, false>, k_mx_values<MXFP4, false>,
+                                k_mx_values<NVFP4, false>, grid, ROW_WARPS * 32, stream, p, spans,
+                                tiles);
+        return e == cudaSuccess ? ok() : cuda_fail("decoding launch", e);
+    });
+}
+
+}  // extern "C"

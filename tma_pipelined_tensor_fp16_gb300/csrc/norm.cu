@@ -1,0 +1,459 @@
+// norm.cu -- root-mean-square norm with the residual's addition and quantised rows, and
+// its gradient.  Bound by memory: every value is read once and written once per output.
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/tmalayer.h"
+#include "device_common.cuh"
+#include "launch.h"
+#include "microscale.cuh"
+#include "runtime.h"
+
+namespace tg {
+
+namespace {
+
+struct NormParams {
+    int64_t tokens;
+    int width;
+    float eps, inv_width;
+    const __half* X;
+    const __half* residual;
+    const __half* weight;
+    __half* total;
+    __half* Z;
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t chunks, groups;
+};
+
+__device__ __forceinline__ void widen8(const uint4& v, float (&x)[8])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ uint4 narrow8(const float (&x)[8])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float warp_sum(float s)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+// Sum over the `WARPS` warps of a row; `shared` holds one slot per warp and is free again
+// after the next call's barrier (two alternate).
+template <int WARPS>
+__device__ __forceinline__ float row_sum(float s, float* shared)
+{
+    s = warp_sum(s);
+    if constexpr (WARPS > 1) {
+        if (lane_id() == 0) shared[threadIdx.x / 32] = s;
+        __syncthreads();
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) s += shared[i];
+    }
+    return s;
+}
+
+// A row by WARPS warps (1, or all of the CTA), VEC vectors of eight values per lane,
+// held in registers between the sum of squares and the outputs.
+template <int FORMAT, int WARPS, int VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_rms_norm(const __grid_constant__ NormParams p)
+{
+    constexpr int ROWS = THREADS / 32 / WARPS;  // per CTA
+    constexpr int LANES = WARPS * 32;
+    __shared__ float shared[THREADS / 32];
+    const int lane = static_cast<int>(threadIdx.x) % LANES;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / LANES;
+    const bool valid = row < p.tokens;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (WARPS == 1 && !valid) return;
+    float h[VEC][8];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        const int k = (i * LANES + lane) * 8;
+        uint4 x = make_uint4(0, 0, 0, 0), r = make_uint4(0, 0, 0, 0);
+        if (k < p.width) {
+            x = *reinterpret_cast<const uint4*>(p.X + row * p.width + k);
+            if (p.residual) r = *reinterpret_cast<const uint4*>(p.residual + row * p.width + k);
+        }
+        widen8(x, h[i]);
+        if (p.residual) {
+            float f[8];
+            widen8(r, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[i][j] += f[j];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fmaf(h[i][j], h[i][j], sum);
+    sum = row_sum<WARPS>(sum, shared);
+    const float rstd = 1.0f / sqrtf(fmaf(sum, p.inv_width, p.eps));
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        const int vec = i * LANES + lane;
+        const int k = vec * 8;
+        float z[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = 0.0f;
+        if (k < p.width) {
+            if (p.total) *reinterpret_cast<uint4*>(p.total + row * p.width + k) = narrow8(h[i]);
+            float w[8];
+            widen8(__ldg(reinterpret_cast<const uint4*>(p.weight + k)), w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[j] = h[i][j] * rstd * w[j];
+            if (p.Z) *reinterpret_cast<uint4*>(p.Z + row * p.width + k) = narrow8(z);
+        }
+        if constexpr (FORMAT >= 0)
+            quantize_store<FORMAT>(z, 1.0f, 1.0f / 6.0f, vec,
+                                   p.codes + mx_code_offset(row, 0, p.chunks),
+                                   p.scales + mx_scale_offset(row, 0, p.groups), p.chunks,
+                                   p.groups, valid);
+    }
+}
+
+template <int FORMAT>
+cudaError_t launch_norm(const NormParams& p, cudaStream_t stream)
+{
+    // the row's vectors, up to the end of its codes and scales
+    int64_t padded = p.width;
+    if constexpr (FORMAT >= 0)
+        padded = std::max<int64_t>(p.chunks * mx_chunk(FORMAT), p.groups * mx_group(FORMAT));
+    const int64_t vecs = (padded + 7) / 8;
+    auto go = [&](auto kernel, int rows_per_cta, int threads) {
+        const int64_t grid = (p.tokens + rows_per_cta - 1) / rows_per_cta;
+        return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)),
+                                dim3(static_cast<unsigned>(threads)), 0, 1, stream, p);
+    };
+    // up to 1024 values a warp holds a row
+    if (vecs <= 32) return go(k_rms_norm<FORMAT, 1, 1, 256>, 8, 256);
+    if (vecs <= 64) return go(k_rms_norm<FORMAT, 1, 2, 256>, 8, 256);
+    if (vecs <= 128) return go(k_rms_norm<FORMAT, 1, 4, 256>, 8, 256);
+    if (vecs <= 256) return go(k_rms_norm<FORMAT, 8, 1, 256>, 1, 256);
+    if (vecs <= 512) return go(k_rms_norm<FORMAT, 8, 2, 256>, 1, 256);
+    if (vecs <= 1024) return go(k_rms_norm<FORMAT, 8, 4, 256>, 1, 256);
+    if (vecs <= 2048) return go(k_rms_norm<FORMAT, 16, 4, 512>, 1, 512);
+    return go(k_rms_norm<FORMAT, 32, 4, 1024>, 1, 1024);
+}
+
+// ------------------------------------------------------------------ gradient
+
+struct NormGradParams {
+    int64_t tokens;
+    int width;
+    float eps, inv_width;
+    const __half* dZ;
+    const __half* H;
+    const __half* weight;
+    const __half* dH;
+    __half* dX;
+    float* parts;  // [part][width]
+};
+
+__device__ __forceinline__ float2 warp_sum2(float2 s)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) {
+        s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+        s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+    }
+    return s;
+}
+
+// Rows as in k_rms_norm, each group of WARPS warps taking every stride-th row; a lane's
+// columns stay the same, so their sums over its rows stay in registers and are written
+// once as the group's part of dweight.
+template <int WARPS, int VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_rms_norm_grad(const __grid_constant__ NormGradParams p)
+{
+    constexpr int ROWS = THREADS / 32 / WARPS;
+    constexpr int LANES = WARPS * 32;
+    __shared__ float2 shared[2][THREADS / 32];
+    const int lane = static_cast<int>(threadIdx.x) % LANES;
+    const int64_t group = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / LANES;
+    const int64_t groups = static_cast<int64_t>(gridDim.x) * ROWS;
+    griddep_wait();
+    griddep_launch_dependents();
+    float dw[VEC][8];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+    int turn = 0;
+    for (int64_t row = group; row < p.tokens; row += groups) {
+        uint4 hv[VEC], dv[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int k = (i * LANES + lane) * 8;
+            hv[i] = dv[i] = make_uint4(0, 0, 0, 0);
+            if (k < p.width) {
+                hv[i] = *reinterpret_cast<const uint4*>(p.H + row * p.width + k);
+                dv[i] = *reinterpret_cast<const uint4*>(p.dZ + row * p.width + k);
+            }
+        }
+        float2 s = make_float2(0.0f, 0.0f);  // sum of h^2, of u h
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int k = (i * LANES + lane) * 8;
+            if (k >= p.width) continue;
+            float h[8], d[8], w[8];
+            widen8(hv[i], h);
+            widen8(dv[i], d);
+            widen8(__ldg(reinterpret_cast<const uint4*>(p.weight + k)), w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                s.x = fmaf(h[j], h[j], s.x);
+                s.y = fmaf(d[j] * w[j], h[j], s.y);
+            }
+        }
+        s = warp_sum2(s);
+        if constexpr (WARPS > 1) {
+            float2* slots = shared[turn & 1];
+            ++turn;
+            if (lane_id() == 0) slots[threadIdx.x / 32] = s;
+            __syncthreads();
+            s = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < WARPS; ++i) {
+                s.x += slots[i].x;
+                s.y += slots[i].y;
+            }
+        }
+        const float rstd = 1.0f / sqrtf(fmaf(s.x, p.inv_width, p.eps));
+        const float along = s.y * p.inv_width * rstd * rstd;  // mean(u n) * rstd
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int k = (i * LANES + lane) * 8;
+            if (k >= p.width) continue;
+            float h[8], d[8], w[8], x[8];
+            widen8(hv[i], h);
+            widen8(dv[i], d);
+            widen8(__ldg(reinterpret_cast<const uint4*>(p.weight + k)), w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                dw[i][j] = fmaf(d[j], h[j] * rstd, dw[i][j]);
+                x[j] = rstd * fmaf(-h[j], along, d[j] * w[j]);
+            }
+            if (p.dH) {
+                float r[8];
+                widen8(*reinterpret_cast<const uint4*>(p.dH + row * p.width + k), r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] += r[j];
+            }
+            *reinterpret_cast<uint4*>(p.dX + row * p.width + k) = narrow8(x);
+        }
+    }
+    float* part = p.parts + group * p.width;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        const int k = (i * LANES + lane) * 8;
+        if (k >= p.width) continue;
+        reinterpret_cast<float4*>(part + k)[0] =
+            make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+        reinterpret_cast<float4*>(part + k)[1] =
+            make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+    }
+}
+
+// dweight = sum of the parts: a CTA takes 32 columns, its warps every eighth part.
+__global__ void __launch_bounds__(256) k_rms_norm_weight(const float* parts, int64_t count, int width,
+                                                         float* dweight)
+{
+    __shared__ float shared[8][33];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(threadIdx.x) / 32;
+    const int k = static_cast<int>(blockIdx.x) * 32 + lane;
+    float s = 0.0f;
+    if (k < width)
+        for (int64_t i = warp; i < count; i += 8) s += parts[i * width + k];
+    shared[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && k < width) {
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += shared[i][lane];
+        dweight[k] = s;
+    }
+}
+
+// How many parts dweight has: rows per CTA and CTAs, by the width.
+struct GradShape {
+    int config;
+    int rows;  // per CTA
+    int ctas;
+};
+
+// Independent of the device (GB300 has 152 SMs), so that the workspace is known without one.
+constexpr int GRAD_SMS = 152;
+
+GradShape grad_shape(int64_t tokens, int64_t width)
+{
+    const int64_t vecs = (width + 7) / 8;
+    GradShape s;
+    int resident;
+    if (vecs <= 32) s = {0, 8, 0}, resident = 4;
+    else if (vecs <= 64) s = {1, 8, 0}, resident = 3;
+    else if (vecs <= 256) s = {2, 1, 0}, resident = 5;
+    else if (vecs <= 512) s = {3, 1, 0}, resident = 3;
+    else if (vecs <= 1024) s = {4, 1, 0}, resident = 2;
+    else if (vecs <= 2048) s = {5, 1, 0}, resident = 1;
+    else s = {6, 1, 0}, resident = 1;
+    const int64_t want = (tokens + s.rows - 1) / s.rows;
+    s.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, resident * GRAD_SMS)));
+    return s;
+}
+
+cudaError_t launch_norm_grad(const NormGradParams& p, const GradShape& s, cudaStream_t stream)
+{
+    auto go = [&](auto kernel, int threads) {
+        return launch_dependent(kernel, dim3(static_cast<unsigned>(s.ctas)),
+                                dim3(static_cast<unsigned>(threads)), 0, 1, stream, p);
+    };
+    switch (s.config) {
+    case 0: return go(k_rms_norm_grad<1, 1, 256>, 256);
+    case 1: return go(k_rms_norm_grad<1, 2, 256>, 256);
+    case 2: return go(k_rms_norm_grad<8, 1, 256>, 256);
+    case 3: return go(k_rms_norm_grad<8, 2, 256>, 256);
+    case 4: return go(k_rms_norm_grad<16, 2, 512>, 512);
+    case 5: return go(k_rms_norm_grad<32, 2, 1024>, 1024);
+    default: return go(k_rms_norm_grad<32, 4, 1024>, 1024);
+    }
+}
+
+int check_norm(int64_t tokens, int64_t width, float eps)
+{
+    if (tokens < 0 || tokens > MAX_COORDINATE)
+        return fail(GEMM_ERR_INVALID_ARG, "tokens must be in [0, 2^31-65536]");
+    if (width < 8 || width > 32768 || width % 8 != 0)
+        return fail(GEMM_ERR_UNSUPPORTED, "width must be a multiple of 8 from 8 to 32768");
+    if (!(eps >= 0.0f)) return fail(GEMM_ERR_INVALID_ARG, "eps must be >= 0");
+    return GEMM_OK;
+}
+
+}  // namespace
+
+}  // namespace tg
+
+using namespace tg;
+
+extern "C" {
+
+int gemm_rms_norm(int64_t tokens, int64_t width, const void* X, const void* residual,
+                  const void* weight, float eps, void* total, void* Z, int format, void* codes,
+                  void* scales, void* cuda_stream)
+{
+    return guarded([&] {
+        int r = check_norm(tokens, width, eps);
+        if (r != GEMM_OK) return r;
+        if ((codes != nullptr) != (scales != nullptr))
+            return fail(GEMM_ERR_INVALID_ARG, "codes and scales must be given together");
+        if (codes && (format < MXFP8 || format > NVFP4))
+            return fail(GEMM_ERR_INVALID_ARG, "unknown gemm_mx_format");
+        if (!weight || (tokens > 0 && !X))
+            return fail(GEMM_ERR_INVALID_ARG, "X and weight must be non-NULL");
+        if (tokens > 0 && !total && !Z && !codes)
+            return fail(GEMM_ERR_INVALID_ARG, "no output is asked for");
+        if (total && total == Z) return fail(GEMM_ERR_INVALID_ARG, "total and Z must differ");
+        if (!aligned16(X) || !aligned16(residual) || !aligned16(weight) || !aligned16(total) ||
+            !aligned16(Z) || !aligned16(codes) || !aligned16(scales))
+            return fail(GEMM_ERR_UNSUPPORTED, "all tensors must be 16-byte aligned");
+        int dev;
+        r = require_device(&dev, nullptr, nullptr);
+        if (r != GEMM_OK) return r;
+        if (tokens == 0) return ok();
+        NormParams p = {};
+        p.tokens = tokens;
+        p.width = static_cast<int>(width);
+        p.eps = eps;
+        p.inv_width = static_cast<float>(1.0 / static_cast<double>(width));
+        p.X = static_cast<const __half*>(X);
+        p.residual = static_cast<const __half*>(residual);
+        p.weight = static_cast<const __half*>(weight);
+        p.total = static_cast<__half*>(total);
+        p.Z = static_cast<__half*>(Z);
+        p.codes = static_cast<uint8_t*>(codes);
+        p.scales = static_cast<uint8_t*>(scales);
+        cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+        cudaError_t e;
+        if (codes) {
+            p.chunks = mx_chunks(width, format);
+            p.groups = mx_groups(width, format);
+            e = format == MXFP8   ? launch_norm<MXFP8>(p, stream)
+                : format == MXFP4 ? launch_norm<MXFP4>(p, stream)
+                                  : launch_norm<NVFP4>(p, stream);
+        } else {
+            e = launch_norm<-1>(p, stream);
+        }
+        return e == cudaSuccess ? ok() : cuda_fail("norm launch", e);
+    });
+}
+
+int64_t gemm_rms_norm_grad_workspace(int64_t tokens, int64_t width)
+{
+    if (check_norm(tokens, width, 0.0f) != GEMM_OK) return -1;
+    ok();
+    const GradShape s = grad_shape(tokens, width);
+    return static_cast<int64_t>(s.ctas) * s.rows * width * 4;
+}
+
+int gemm_rms_norm_grad(int64_t tokens, int64_t width, const void* dZ, const void* H,
+                       const void* weight, const void* dH, float eps, void* dX, float* dweight,
+                       void* workspace, void* cuda_stream)
+{
+    return guarded([&] {
+        int r = check_norm(tokens, width, eps);
+        if (r != GEMM_OK) return r;
+        if (!weight || !dweight || !workspace || (tokens > 0 && (!dZ || !H || !dX)))
+            return fail(GEMM_ERR_INVALID_ARG,
+                        "dZ, H, weight, dX, dweight and workspace must be non-NULL");
+        if (!aligned16(dZ) || !aligned16(H) || !aligned16(weight) || !aligned16(dH) ||
+            !aligned16(dX) || !aligned16(dweight) || !aligned16(workspace))
+            return fail(GEMM_ERR_UNSUPPORTED, "all tensors must be 16-byte aligned");
+        int dev;
+        r = require_device(&dev, nullptr, nullptr);
+        if (r != GEMM_OK) return r;
+        NormGradParams p = {};
+        p.tokens = tokens;
+        p.width = static_cast<int>(width);
+        p.eps = eps;
+        p.inv_width = static_cast<float>(1.0 / static_cast<double>(width));
+        p.dZ = static_cast<const __half*>(dZ);
+        p.H = static_cast<const __half*>(H);
+        p.weight = static_cast<const __half*>(weight);
+        p.dH = static_cast<const __half*>(dH);
+        p.dX = static_cast<__half*>(dX);
+        p.parts = static_cast<float*>(workspace);
+        cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+        const GradShape s = grad_shape(tokens, width);
+        cudaError_t e = launch_norm_grad(p, s, stream);
+        if (e == cudaSuccess)
+            e = launch_dependent(k_rms_norm_weight, dim3(static_cast<unsigned>((width + 31) / 32)),
+                                 dim3(256), 0, 1, stream, static_cast<const float*>(p.parts),
+                                 static_cast<int64_t>(s.ctas) * s.rows, p.width, dweight);
+        return e == cudaSuccess ? ok() : cuda_fail("norm gradient launch", e);
+    });
+}
+
+}  // extern "C"

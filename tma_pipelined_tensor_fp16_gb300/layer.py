@@ -1,0 +1,164 @@
+"""The operators of include/tmalayer.h for torch CUDA tensors: what surrounds the products
+in a layer and in its training step.
+
+    Z, H, Q = rms_norm(X, weight, residual=R, format="mxfp8")   # H = X + R, Z = norm of H
+    dX, dweight = rms_norm_grad(dZ, H, weight, dH=dH)           # dX is R's gradient, too
+    clip = GradClip([dW1, dW2, dweight])
+    norm = clip(1.0)                                            # the norm before clipping
+
+Conventions are those of ``experts``.
+"""
+import ctypes
+import math
+
+from .binding import GemmError, last_error, lib
+from .experts import _call, _empty, _output, _ptr, _tensor, _torch, _used_on
+from .microscale import MXTensor, _format
+
+_CLIP_WORKSPACE = 16384  # GEMM_CLIP_WORKSPACE_BYTES
+
+
+def _matrix(name, t):
+    torch = _torch()
+    if t.dim() != 2:
+        raise ValueError("%s must be a matrix (tokens x width)" % name)
+    return _tensor(name, t, t.shape, torch.float16)
+
+
+def rms_norm(X, weight, residual=None, eps=1e-6, half=True, format=None, out=None, total=None,
+             stream=None):
+    """(Z, H, Q) with h = X + residual and z = h / sqrt(mean(h^2) + eps) * weight along the
+    rows of X (tokens x width fp16; weight: width fp16).
+
+    Z is z in fp16 (`out` or a new tensor; None with half=False), H is h in fp16 (`total`,
+    which may be X or residual itself, or a new tensor; X itself without a residual) and Q is
+    z as an MXTensor of `format` (None without; nvfp4 with the tensor scale 1)."""
+    torch = _torch()
+    _matrix("X", X)
+    dev = X.device
+    tokens, width = X.shape
+    _tensor("weight", weight, (width,), torch.float16, dev)
+    if residual is not None:
+        _tensor("residual", residual, X.shape, torch.float16, dev)
+    elif total is not None:
+        raise ValueError("total is for a residual: without one it would be X")
+    if out is not None and not half:
+        raise ValueError("out is not written with half=False")
+    if not half and format is None:
+        raise ValueError("half=False leaves no output without a format")
+    code = _format(format) if format is not None else 0
+    Z = _output("out", out, X.shape, torch.float16, dev, stream) if half else None
+    H = _output("total", total, X.shape, torch.float16, dev, stream) if residual is not None \
+        else None
+    Q = MXTensor._new(tokens, width, format, dev, stream) if format is not None else None
+    _call(lib().gemm_rms_norm, dev, stream, tokens, width, _ptr(X), _ptr(residual), _ptr(weight),
+          eps, _ptr(H), _ptr(Z), code, _ptr(Q.codes) if Q is not None else None,
+          _ptr(Q.scales) if Q is not None else None)
+    if stream is not None:
+        _used_on(stream, X, weight, residual, Z, H, *(Q._parts() if Q is not None else ()))
+    return Z, X if residual is None else H, Q
+
+
+def rms_norm_grad(dZ, H, weight, dH=None, eps=1e-6, out=None, dweight=None, stream=None):
+    """(dX, dweight) of ``rms_norm`` for dZ (tokens x width fp16), its H and, with a
+    residual, dH: the gradient that reaches H by its other uses.  dX (fp16; `out` may be
+    dZ or dH itself) is the gradient of X and of the residual, dweight is fp32."""
+    torch = _torch()
+    _matrix("dZ", dZ)
+    dev = dZ.device
+    tokens, width = dZ.shape
+    _tensor("H", H, dZ.shape, torch.float16, dev)
+    _tensor("weight", weight, (width,), torch.float16, dev)
+    if dH is not None:
+        _tensor("dH", dH, dZ.shape, torch.float16, dev)
+    dX = _output("out", out, dZ.shape, torch.float16, dev, stream)
+    dw = _output("dweight", dweight, (width,), torch.float32, dev, stream)
+    size = lib().gemm_rms_norm_grad_workspace(tokens, width)
+    if size < 0:
+        raise GemmError(lib().gemm_last_status(), last_error())
+    work = _empty((size,), torch.uint8, dev, stream)
+    _call(lib().gemm_rms_norm_grad, dev, stream, tokens, width, _ptr(dZ), _ptr(H), _ptr(weight),
+          _ptr(dH), eps, _ptr(dX), _ptr(dw), _ptr(work))
+    if stream is not None:
+        _used_on(stream, dZ, H, weight, dH, dX, dw, work)
+    return dX, dw
+
+
+class GradClip:
+    """The global norm of a list of gradients (fp32 and fp16 tensors, contiguous, any shapes,
+    on one device), and clipping to it.
+
+    ``clip(max_norm)`` writes every gradient times min(1, max_norm / (norm + eps)) into `out`
+    (tensors of the same shapes and types; in place when not given) and returns the norm
+    before clipping, one fp32; ``clip.norm()`` returns it alone.  The object keeps the tensors
+    and a table of their addresses; a tensor whose memory has moved since is refused."""
+
+    def __init__(self, grads, out=None):
+        torch = _torch()
+        self._h = None
+        grads = list(grads)
+        out = grads if out is None else list(out)
+        if not grads:
+            raise ValueError("there are no gradients")
+        if len(out) != len(grads):
+            raise ValueError("out must hold a tensor for each gradient")
+        dev = grads[0].device
+        codes = {torch.float32: 0, torch.float16: 1}
+        for i, (g, o) in enumerate(zip(grads, out)):
+            if g.dtype not in codes:
+                raise TypeError("gradient %d must be float32 or float16, not %s" % (i, g.dtype))
+            _tensor("gradient %d" % i, g, g.shape, g.dtype, dev)
+            if o is not g:
+                _tensor("out %d" % i, o, g.shape, g.dtype, dev)
+        self.grads, self.out, self.device = grads, out, dev
+        self._tensors = grads if out is grads else grads + out
+        self._addresses = [t.data_ptr() for t in self._tensors]
+        n = len(grads)
+        addresses = ctypes.c_void_p * n
+        with torch.cuda.device(dev):
+            self._h = lib().gemm_clip_create_plan(
+                n, addresses(*self._addresses[:n]), addresses(*self._addresses[-n:]),
+                (ctypes.c_int64 * n)(*[g.numel() for g in grads]),
+                (ctypes.c_int * n)(*[codes[g.dtype] for g in grads]))
+        if not self._h:
+            raise GemmError(lib().gemm_last_status(), last_error())
+
+    def _run(self, fn, stream, *args):
+        torch = _torch()
+        if [t.data_ptr() for t in self._tensors] != self._addresses:
+            raise ValueError("a tensor's memory has moved: make a new GradClip")
+        norm = _empty((1,), torch.float32, self.device, stream)
+        work = _empty((_CLIP_WORKSPACE,), torch.uint8, self.device, stream)
+        _call(fn, self.device, stream, self._h, *args, _ptr(norm), _ptr(work))
+        if stream is not None:
+            _used_on(stream, norm, work, *self._tensors)
+        return norm
+
+    def __call__(self, max_norm, eps=1e-6, stream=None):
+        if not max_norm >= 0.0 or not eps >= 0.0 or math.isinf(eps):
+            raise ValueError("max_norm and eps must be >= 0")
+        return self._run(lib().gemm_clip_run, stream, max_norm, eps)
+
+    def norm(self, stream=None):
+        return self._run(lib().gemm_clip_norm, stream)
+
+    def close(self):
+        if self._h:
+            lib().gemm_clip_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, stream=None):
+    """One pass of a GradClip; it is kept by no one, so this waits for the GPU.  A training
+    loop whose gradients stay where they are keeps a GradClip."""
+    clip = GradClip(grads, out)
+    norm = clip(max_norm, eps, stream)
+    _torch().cuda.synchronize(clip.device)
+    clip.close()
+    return norm

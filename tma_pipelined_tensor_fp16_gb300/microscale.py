@@ -1,0 +1,207 @@
+"""The block-scaled operators of include/tmamicro.h for torch CUDA tensors.
+
+    Wq = mx_quantize(W, "nvfp4")                  # N x K fp16, once
+    plan = MXPlan(M, N, K, format="nvfp4")
+    Y = plan(mx_quantize(X, "nvfp4"), Wq)         # X . W^T, M x N
+    Xt = mx_quantize(X, "nvfp4", transpose=True)  # X^T, blocked along X's columns
+    Xq.values()                                   # the rounded values, fp16
+
+Formats: ``mxfp8`` (e4m3, a power of two for every 32 values of a row), ``mxfp4``
+(e2m1, a power of two for every 32) and ``nvfp4`` (e2m1, an e4m3 scale for every 16 and
+a power of two for the whole tensor).
+
+Argument checks and marshalling only, with the conventions of ``experts``: every operator
+runs in the library's CUDA kernels, asynchronously on the current stream of the tensors'
+device (or on ``stream``).
+"""
+from .binding import _check, lib
+from .experts import (_call, _empty, _Handle, _out_dtype, _output, _ptr, _tensor, _torch,
+                      _used_on)
+
+MX_FORMATS = {"mxfp8": 0, "mxfp4": 1, "nvfp4": 2}
+MX_KERNELS = {"auto": 0, "pair": 1, "single": 2}
+_BLOCK = {"mxfp8": 32, "mxfp4": 32, "nvfp4": 16}
+_CHUNK = {"mxfp8": 16, "mxfp4": 32, "nvfp4": 32}
+_WORKSPACE = 4096  # GEMM_MX_WORKSPACE_BYTES
+
+
+def _format(name):
+    try:
+        return MX_FORMATS[name]
+    except (KeyError, TypeError):
+        raise ValueError("format must be one of %s" % sorted(MX_FORMATS)) from None
+
+
+def _shapes(rows, K, format):
+    """Shapes of the storage: codes (row blocks, chunks, 128, 16) and scales (row blocks,
+    groups, 32, 4, 4)."""
+    blocks = -(-rows // 128)
+    chunks = 2 * -(-K // (2 * _CHUNK[format]))
+    groups = -(-K // (4 * _BLOCK[format]))
+    return (blocks, chunks, 128, 16), (blocks, groups, 32, 4, 4)
+
+
+class MXTensor:
+    """A quantised matrix of ``rows`` x ``K``: ``codes`` and ``scales`` (uint8, in the
+    storage order that include/tmamicro.h describes) and for nvfp4 ``tensor_scale`` (one
+    fp32; None stands for 1)."""
+
+    def __init__(self, rows, K, format, codes, scales, tensor_scale=None):
+        torch = _torch()
+        _format(format)
+        if rows < 0 or K < 1:
+            raise ValueError("rows must be >= 0 and K >= 1")
+        shape_c, shape_s = _shapes(rows, K, format)
+        _tensor("codes", codes, shape_c, torch.uint8)
+        _tensor("scales", scales, shape_s, torch.uint8, codes.device)
+        if tensor_scale is not None:
+            if format != "nvfp4":
+                raise ValueError("only nvfp4 has a tensor_scale")
+            _tensor("tensor_scale", tensor_scale, (1,), torch.float32, codes.device)
+        self.rows, self.K, self.format = rows, K, format
+        self.codes, self.scales, self.tensor_scale = codes, scales, tensor_scale
+
+    @classmethod
+    def _new(cls, rows, K, format, device, stream, tensor_scale=None):
+        """Storage to be written by the library (no checks of its own tensors)."""
+        torch = _torch()
+        shape_c, shape_s = _shapes(rows, K, format)
+        t = cls.__new__(cls)
+        t.rows, t.K, t.format = rows, K, format
+        t.codes = _empty(shape_c, torch.uint8, device, stream)
+        t.scales = _empty(shape_s, torch.uint8, device, stream)
+        t.tensor_scale = tensor_scale
+        return t
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def _parts(self):
+        return self.codes, self.scales, self.tensor_scale
+
+    @classmethod
+    def from_codes(cls, codes, scales, K, format, tensor_scale=None):
+        """From row-major codes (rows x K uint8 for mxfp8, rows x ceil(K / 2) for the
+        others, the first of two in the low half) and row-major scales (rows x
+        ceil(K / block) bytes of e8m0, e4m3 for nvfp4), as other programs keep them.  A
+        set-up step."""
+        torch = _torch()
+        _format(format)
+        rows = codes.shape[0]
+        width = K if format == "mxfp8" else -(-K // 2)
+        per_row = -(-K // _BLOCK[format])
+        _tensor("codes", codes, (rows, width), torch.uint8)
+        _tensor("scales", scales, (rows, per_row), torch.uint8, codes.device)
+        (blocks, chunks, _, _), (_, groups, _, _, _) = _shapes(rows, K, format)
+        c = codes.new_zeros((blocks * 128, chunks * 16))
+        c[:rows, :width] = codes
+        if format != "mxfp8" and K % 2:
+            c[:, width - 1] &= 15
+        s = scales.new_zeros((blocks * 128, groups * 4))
+        s[:rows, :per_row] = scales
+        c = c.reshape(blocks, 128, chunks, 16).permute(0, 2, 1, 3).contiguous()
+        s = s.reshape(blocks, 4, 32, groups, 4).permute(0, 3, 2, 1, 4).contiguous()
+        return cls(rows, K, format, c, s, tensor_scale)
+
+    def to_codes(self):
+        """(codes, scales) in row-major order, as ``from_codes`` takes them."""
+        blocks, chunks, _, _ = self.codes.shape
+        groups = self.scales.shape[1]
+        width = self.K if self.format == "mxfp8" else -(-self.K // 2)
+        c = self.codes.permute(0, 2, 1, 3).reshape(blocks * 128, chunks * 16)
+        s = self.scales.permute(0, 3, 2, 1, 4).reshape(blocks * 128, groups * 4)
+        return (c[:self.rows, :width].contiguous(),
+                s[:self.rows, :-(-self.K // _BLOCK[self.format])].contiguous())
+
+    def values(self, out=None, stream=None):
+        """The values that the codes stand for (rows x K), rounded once to `out`'s type
+        (fp16 when not given; fp32 holds them exactly)."""
+        torch = _torch()
+        dev = self.codes.device
+        dtype = torch.float32 if out is not None and out.dtype == torch.float32 else torch.float16
+        V = _output("out", out, (self.rows, self.K), dtype, dev, stream)
+        _call(lib().gemm_mx_values, dev, stream, self.rows, self.K, MX_FORMATS[self.format],
+              _ptr(self.codes), _ptr(self.scales), _ptr(self.tensor_scale),
+              0 if dtype == torch.float32 else 1, _ptr(V))
+        if stream is not None:
+            _used_on(stream, *self._parts(), V)
+        return V
+
+
+def mx_quantize(X, format="mxfp8", transpose=False, tensor_scale=None, out=None, stream=None):
+    """Round X (fp16, contiguous; its rows hold a multiple of 8 values) to `format`:
+    an MXTensor of X's shape, or of X^T's with `transpose` (blocks run along X's columns).
+
+    nvfp4: without `tensor_scale` (one fp32, a power of two) it is found from X first.
+    `out`, an MXTensor of the result's shape and format, is written and returned; its
+    tensor_scale is written where none is given."""
+    torch = _torch()
+    code = _format(format)
+    if X.dim() != 2:
+        raise ValueError("X must be a matrix")
+    _tensor("X", X, X.shape, torch.float16)
+    dev = X.device
+    rows, K = (X.shape[1], X.shape[0]) if transpose else (X.shape[0], X.shape[1])
+    if K < 1:
+        raise ValueError("a row must hold a value at least")
+    if tensor_scale is not None:
+        if format != "nvfp4":
+            raise ValueError("only nvfp4 has a tensor_scale")
+        _tensor("tensor_scale", tensor_scale, (1,), torch.float32, dev)
+    if out is None:
+        Q = MXTensor._new(rows, K, format, dev, stream, tensor_scale)
+    else:
+        Q = out
+        if (Q.rows, Q.K, Q.format) != (rows, K, format) or Q.device != dev:
+            raise ValueError("out must be a %s MXTensor of %d x %d on %s"
+                             % (format, rows, K, dev))
+        if tensor_scale is not None:
+            Q.tensor_scale = tensor_scale
+    work = None
+    if format == "nvfp4" and tensor_scale is None:
+        work = _empty((_WORKSPACE,), torch.uint8, dev, stream)
+        if Q.tensor_scale is None:
+            Q.tensor_scale = _empty((1,), torch.float32, dev, stream)
+    _call(lib().gemm_mx_quantize, dev, stream, rows, K, code, 1 if transpose else 0, _ptr(X),
+          _ptr(Q.codes), _ptr(Q.scales), _ptr(Q.tensor_scale), _ptr(work))
+    if stream is not None:
+        _used_on(stream, X, *Q._parts(), work)
+    return Q
+
+
+class MXPlan(_Handle):
+    """C = A . B^T (M x N) of two MXTensors of one format, A of M x K and B of N x K.
+
+    `kernel` ("auto", "pair", "single") and `split` (CTAs that share a tile's length, for
+    "single") choose the kernel as in include/tmamicro.h.  Runs of a plan may overlap."""
+    _destroy, _describe = "gemm_mx_destroy", "gemm_mx_describe"
+    _status, _wait = "gemm_mx_get_device_status", "gemm_mx_set_wait"
+
+    def __init__(self, M, N, K, format="mxfp8", out="f16", kernel="auto", split=0):
+        if kernel not in MX_KERNELS:
+            raise ValueError("kernel must be one of %s" % sorted(MX_KERNELS))
+        code = _format(format)
+        self.M, self.N, self.K, self.format = M, N, K, format
+        self.dtype, out_code = _out_dtype(out)
+        self._own(lib().gemm_mx_create_plan_ex(M, N, K, code, out_code, MX_KERNELS[kernel], split))
+
+    def __call__(self, A, B, out=None, stream=None):
+        for name, t, rows in (("A", A, self.M), ("B", B, self.N)):
+            if not isinstance(t, MXTensor):
+                raise TypeError("%s must be an MXTensor" % name)
+            if t.rows != rows or t.K != self.K or t.format != self.format:
+                raise ValueError("%s must be a %s MXTensor of %d x %d, not %s of %d x %d"
+                                 % (name, self.format, rows, self.K, t.format, t.rows, t.K))
+        dev = A.codes.device
+        if B.codes.device != dev:
+            raise ValueError("B is on %s, the other tensors on %s" % (B.codes.device, dev))
+        C = _output("out", out, (self.M, self.N), self.dtype, dev, stream)
+        _call(lib().gemm_mx_run, dev, stream, self._h, _ptr(A.codes), _ptr(A.scales),
+              _ptr(A.tensor_scale), _ptr(B.codes), _ptr(B.scales), _ptr(B.tensor_scale), _ptr(C))
+        if stream is not None:
+            _used_on(stream, *A._parts(), *B._parts(), C)
+        return C
+
+
+__all__ = ["MXPlan", "MXTensor", "MX_FORMATS", "MX_KERNELS", "mx_quantize"]
