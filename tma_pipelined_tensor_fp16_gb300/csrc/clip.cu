@@ -49,26 +49,41 @@ __device__ __forceinline__ Chunk load_chunk(const Chunk* table, int64_t i)
     return *reinterpret_cast<Chunk*>(v);
 }
 
-// Sum of squares of four to eight values: in fp32 while no square leaves its range,
-// else (rare) in fp64.
+// Squares are added up in fp32 over the 32 values that a thread takes of a chunk (in
+// vectors of four or eight and those in a tree: each sum is off by at most 9 * 2^-24), and
+// in fp64 from there: one fp64 addition for 32 values, as GB300 does few of them (with one
+// for every four values 1.07 GB took 1.1 ms).  Sums that fp32 does not hold whole are
+// formed again in fp64: those that overflow, and those below 2^-100, where squares may
+// have vanished.
+__device__ __forceinline__ bool holds(float s) { return s >= 0x1p-100f && s <= 0x1p126f; }
+
+template <int N>
+__device__ __forceinline__ float squares(const float (&x)[N])
+{
+    float s = x[0] * x[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) s = fmaf(x[i], x[i], s);
+    return s;
+}
+
+template <int N>
+__device__ __noinline__ double squares_in_64(const float* x)
+{
+    float most = 0.0f;
+    for (int i = 0; i < N; ++i) most = fmaxf(most, fabsf(x[i]));
+    double d = 0.0;
+    for (int i = 0; i < N; ++i) {
+        if (most == 0.0f && x[i] == 0.0f) continue;  // zeros (NaN does not count as `most`)
+        d = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), d);
+    }
+    return d;
+}
+
 template <int N>
 __device__ __forceinline__ double square_sum(const float (&x)[N])
 {
-    float s = 0.0f, most = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        s = fmaf(x[i], x[i], s);
-        most = fmaxf(most, fabsf(x[i]));
-    }
-    // 2^-50 <= most <= 2^60: the largest square and the sum are normal numbers, and
-    // what smaller squares lose is below 2^-49 of them
-    if (most > 0x1p60f || (most < 0x1p-50f && most > 0.0f)) {
-        double d = 0.0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) d = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), d);
-        return d;
-    }
-    return static_cast<double>(s);
+    const float s = squares(x);
+    return holds(s) ? static_cast<double>(s) : squares_in_64<N>(x);
 }
 
 __device__ __forceinline__ void widen(const uint4& v, float (&x)[8])
@@ -82,16 +97,26 @@ __device__ __forceinline__ void widen(const uint4& v, float (&x)[8])
     }
 }
 
-__device__ __forceinline__ double block_sum(double s, double* shared)
+__device__ __forceinline__ double warp_sum(double s)
 {
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane_id() == 0) shared[threadIdx.x / 32] = s;
-    __syncthreads();
-    s = 0.0;
-    for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) s += shared[i];
     return s;
 }
+
+// The CTA's sum, in its first warp.
+__device__ __forceinline__ double block_sum(double s, double* shared)
+{
+    s = warp_sum(s);
+    if (lane_id() == 0) shared[threadIdx.x / 32] = s;
+    __syncthreads();
+    if (threadIdx.x >= 32) return 0.0;
+    return warp_sum(threadIdx.x < CLIP_THREADS / 32 ? shared[threadIdx.x] : 0.0);
+}
+
+// Vectors of a whole chunk per thread.
+constexpr int CHUNK_F32 = static_cast<int>(CHUNK / 4 / CLIP_THREADS);
+constexpr int CHUNK_F16 = static_cast<int>(CHUNK / 8 / CLIP_THREADS);
 
 __global__ void __launch_bounds__(CLIP_THREADS) k_grad_squares(const Chunk* table, int64_t chunks,
                                                                double* parts)
@@ -107,26 +132,63 @@ __global__ void __launch_bounds__(CLIP_THREADS) k_grad_squares(const Chunk* tabl
         int done = 0;
         if (k.f16) {
             const __half* src = static_cast<const __half*>(k.src);
+            const uint4* v = reinterpret_cast<const uint4*>(src);
+            if (vectors && k.count == CHUNK) {
+                uint4 w[CHUNK_F16];
+#pragma unroll
+                for (int i = 0; i < CHUNK_F16; ++i) w[i] = v[i * CLIP_THREADS + tid];
+                float s = 0.0f;  // squares of fp16 values and their sums: fp32 holds them
+#pragma unroll
+                for (int i = 0; i < CHUNK_F16; ++i) {
+                    float x[8];
+                    widen(w[i], x);
+                    s += squares(x);
+                }
+                sum += static_cast<double>(s);
+                continue;
+            }
             if (vectors) {
                 done = k.count & ~7;
-                const uint4* v = reinterpret_cast<const uint4*>(src);
-#pragma unroll 4
                 for (int i = tid; i < done / 8; i += CLIP_THREADS) {
                     float x[8];
                     widen(v[i], x);
-                    sum += square_sum(x);
+                    sum += static_cast<double>(squares(x));
                 }
             }
             for (int i = done + tid; i < k.count; i += CLIP_THREADS) {
-                const float x[1] = {__half2float(src[i])};
-                sum += square_sum(x);
+                const float x = __half2float(src[i]);
+                sum += static_cast<double>(x * x);
             }
         } else {
             const float* src = static_cast<const float*>(k.src);
+            const float4* v = reinterpret_cast<const float4*>(src);
+            if (vectors && k.count == CHUNK) {
+                float4 w[CHUNK_F32];
+#pragma unroll
+                for (int i = 0; i < CHUNK_F32; ++i) w[i] = v[i * CLIP_THREADS + tid];
+                float s[CHUNK_F32];
+#pragma unroll
+                for (int i = 0; i < CHUNK_F32; ++i) {
+                    const float x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                    s[i] = squares(x);
+                }
+#pragma unroll
+                for (int n = CHUNK_F32 / 2; n > 0; n /= 2)
+#pragma unroll
+                    for (int i = 0; i < n; ++i) s[i] += s[i + n];
+                if (holds(s[0])) {
+                    sum += static_cast<double>(s[0]);
+                } else {
+                    for (int i = 0; i < CHUNK_F32; ++i) {
+                        const float4 f = v[i * CLIP_THREADS + tid];
+                        const float x[4] = {f.x, f.y, f.z, f.w};
+                        sum += squares_in_64<4>(x);
+                    }
+                }
+                continue;
+            }
             if (vectors) {
                 done = k.count & ~3;
-                const float4* v = reinterpret_cast<const float4*>(src);
-#pragma unroll 8
                 for (int i = tid; i < done / 4; i += CLIP_THREADS) {
                     const float4 f = v[i];
                     const float x[4] = {f.x, f.y, f.z, f.w};
@@ -143,26 +205,51 @@ __global__ void __launch_bounds__(CLIP_THREADS) k_grad_squares(const Chunk* tabl
     if (tid == 0) parts[blockIdx.x] = sum;
 }
 
+__device__ __forceinline__ uint4 scaled8(const uint4& v, float first, float f)
+{
+    float x[8];
+    widen(v, x);
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __half2 h = __floats2half2_rn(x[2 * j] * first * f, x[2 * j + 1] * first * f);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float4 scaled4(const float4& v, float first, float f)
+{
+    return make_float4(v.x * first * f, v.y * first * f, v.z * first * f, v.w * first * f);
+}
+
 __global__ void __launch_bounds__(CLIP_THREADS)
     k_grad_clip(const Chunk* table, int64_t chunks, const double* parts, int part_count,
                 float max_norm, float eps, float* norm, int scale)
 {
-    __shared__ double shared[CLIP_THREADS / 32];
+    __shared__ float factors[2];
     griddep_wait();
     griddep_launch_dependents();
     const int tid = static_cast<int>(threadIdx.x);
-    double sum = 0.0;
-    for (int i = tid; i < part_count; i += CLIP_THREADS) sum += parts[i];
-    sum = block_sum(sum, shared);
-    const double length = sqrt(sum);
-    if (blockIdx.x == 0 && tid == 0) *norm = static_cast<float>(length);
+    if (tid < 32) {
+        // one warp adds the parts up, as fp64 instructions are slow
+        double sum = 0.0;
+        for (int i = tid; i < part_count; i += 32) sum += parts[i];
+        const double length = sqrt(warp_sum(sum));
+        if (tid == 0) {
+            if (blockIdx.x == 0) *norm = static_cast<float>(length);
+            const double ratio = static_cast<double>(max_norm) / (length + static_cast<double>(eps));
+            // NaN stays NaN; no length, nothing to scale (and perhaps no quotient)
+            const double factor = ratio >= 1.0 || length == 0.0 ? 1.0 : ratio;
+            // in two steps, the first a power of two: fp32 does not hold the smallest
+            // factors whole
+            factors[0] = factor < 0x1p-100 ? 0x1p-64f : 1.0f;
+            factors[1] = static_cast<float>(factor / static_cast<double>(factors[0]));
+        }
+    }
     if (!scale) return;
-    const double ratio = static_cast<double>(max_norm) / (length + static_cast<double>(eps));
-    // NaN stays NaN; no length, nothing to scale (and perhaps no quotient)
-    const double factor = ratio >= 1.0 || length == 0.0 ? 1.0 : ratio;
-    // in two steps, the first a power of two: fp32 does not hold the smallest factors whole
-    const float first = factor < 0x1p-100 ? 0x1p-64f : 1.0f;
-    const float f = static_cast<float>(factor / static_cast<double>(first));
+    __syncthreads();
+    const float first = factors[0], f = factors[1];
     for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
         const Chunk k = load_chunk(table, chunks - 1 - c);
         const bool vectors =
@@ -172,37 +259,43 @@ __global__ void __launch_bounds__(CLIP_THREADS)
         if (k.f16) {
             const __half* src = static_cast<const __half*>(k.src);
             __half* dst = static_cast<__half*>(k.dst);
+            if (vectors && k.count == CHUNK) {
+                uint4 w[CHUNK_F16];
+#pragma unroll
+                for (int i = 0; i < CHUNK_F16; ++i)
+                    w[i] = reinterpret_cast<const uint4*>(src)[i * CLIP_THREADS + tid];
+#pragma unroll
+                for (int i = 0; i < CHUNK_F16; ++i)
+                    reinterpret_cast<uint4*>(dst)[i * CLIP_THREADS + tid] = scaled8(w[i], first, f);
+                continue;
+            }
             if (vectors) {
                 done = k.count & ~7;
-#pragma unroll 4
-                for (int i = tid; i < done / 8; i += CLIP_THREADS) {
-                    float x[8];
-                    widen(reinterpret_cast<const uint4*>(src)[i], x);
-                    uint32_t w[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const __half2 h = __floats2half2_rn(x[2 * j] * first * f, x[2 * j + 1] * first * f);
-                        w[j] = *reinterpret_cast<const uint32_t*>(&h);
-                    }
-                    reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
+                for (int i = tid; i < done / 8; i += CLIP_THREADS)
+                    reinterpret_cast<uint4*>(dst)[i] =
+                        scaled8(reinterpret_cast<const uint4*>(src)[i], first, f);
             }
             for (int i = done + tid; i < k.count; i += CLIP_THREADS)
                 dst[i] = __float2half_rn(__half2float(src[i]) * first * f);
         } else {
             const float* src = static_cast<const float*>(k.src);
             float* dst = static_cast<float*>(k.dst);
+            if (vectors && k.count == CHUNK) {
+                float4 w[CHUNK_F32];
+#pragma unroll
+                for (int i = 0; i < CHUNK_F32; ++i)
+                    w[i] = reinterpret_cast<const float4*>(src)[i * CLIP_THREADS + tid];
+#pragma unroll
+                for (int i = 0; i < CHUNK_F32; ++i)
+                    reinterpret_cast<float4*>(dst)[i * CLIP_THREADS + tid] =
+                        scaled4(w[i], first, f);
+                continue;
+            }
             if (vectors) {
                 done = k.count & ~3;
-#pragma unroll 8
-                for (int i = tid; i < done / 4; i += CLIP_THREADS) {
-                    float4 v = reinterpret_cast<const float4*>(src)[i];
-                    v.x = v.x * first * f;
-                    v.y = v.y * first * f;
-                    v.z = v.z * first * f;
-                    v.w = v.w * first * f;
-                    reinterpret_cast<float4*>(dst)[i] = v;
-                }
+                for (int i = tid; i < done / 4; i += CLIP_THREADS)
+                    reinterpret_cast<float4*>(dst)[i] =
+                        scaled4(reinterpret_cast<const float4*>(src)[i], first, f);
             }
             for (int i = done + tid; i < k.count; i += CLIP_THREADS) dst[i] = src[i] * first * f;
         }

@@ -2,6 +2,7 @@
 // back.  All kernels are bound by memory: every value is read once (twice where the
 // tensor scale has to be found first) and its codes and scales are written once.
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/tmamicro.h"
 #include "device_common.cuh"
@@ -305,8 +306,10 @@ __device__ __forceinline__ void decode8(uint2 q, __half2 (&v)[4])
     for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<__half2*>(&h[i]);
 }
 
-// Lanes as in k_mx_quantize: a warp takes 8 rows x 128 values.
-template <int FORMAT, bool F16OUT>
+// Lanes as in k_mx_quantize: a warp takes 8 rows x 128 values.  With ODD a row's length is
+// no multiple of 8, so that rows start anywhere: the values go through shared memory and
+// leave as aligned words, 64 bytes and more at a time.
+template <int FORMAT, bool F16OUT, bool ODD>
 __global__ void __launch_bounds__(ROW_WARPS * 32)
     k_mx_values(const __grid_constant__ ValuesParams p, int64_t spans, int64_t tiles)
 {
@@ -315,8 +318,12 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
     const int64_t tile = static_cast<int64_t>(blockIdx.x) * ROW_WARPS + threadIdx.x / 32;
     if (tile >= tiles) return;
     const int lane = static_cast<int>(lane_id());
+    using T = typename std::conditional<F16OUT, __half, float>::type;
+    __shared__ T staged[ODD ? ROW_WARPS : 1][8][ROW_K + 2];
+    T(*rows)[ROW_K + 2] = staged[ODD ? threadIdx.x / 32 : 0];
     const int64_t row = tile / spans * 8 + lane / 4;
-    if (row >= p.rows) return;
+    if (!ODD && row >= p.rows) return;
+    const bool valid = row < p.rows;
     const int part = lane % 4;
     const int64_t k0 = tile % spans * ROW_K;
     const float t = p.tensor_scale ? *p.tensor_scale : 1.0f;
@@ -327,7 +334,7 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
     uint32_t words[GROUPS];
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g)
-        words[g] = k0 / mx_group(FORMAT) + g < p.groups
+        words[g] = valid && k0 / mx_group(FORMAT) + g < p.groups
                        ? *reinterpret_cast<const uint32_t*>(scales + g * MX_GROUP_BYTES)
                        : 0u;
     uint2 q[4];
@@ -336,7 +343,7 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
         const int64_t k = k0 + j * 32 + part * 8;
         const int chunk = (j * 4 + part) / PER_CHUNK;
         q[j] = make_uint2(0, 0);
-        if (k < p.K) {
+        if (valid && k < p.K) {
             if constexpr (FORMAT == MXFP8)
                 q[j] = reinterpret_cast<const uint2*>(codes + chunk * MX_CHUNK_BYTES)[part % PER_CHUNK];
             else
@@ -364,15 +371,10 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
             x[2 * i] = f.x * s;
             x[2 * i + 1] = f.y * s;
         }
-        if (p.K % 8 != 0) {  // rows of odd lengths start anywhere
+        if constexpr (ODD) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (k + i >= p.K) break;
-                if constexpr (F16OUT)
-                    static_cast<__half*>(p.values)[row * p.K + k + i] = __float2half_rn(x[i]);
-                else
-                    static_cast<float*>(p.values)[row * p.K + k + i] = x[i];
-            }
+            for (int i = 0; i < 8; ++i)
+                rows[lane / 4][j * 32 + part * 8 + i] = static_cast<T>(x[i]);
         } else if constexpr (F16OUT) {
             uint32_t w[4];
 #pragma unroll
@@ -386,6 +388,27 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
             float4* to = reinterpret_cast<float4*>(static_cast<float*>(p.values) + row * p.K + k);
             to[0] = make_float4(x[0], x[1], x[2], x[3]);
             to[1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
+    }
+    if constexpr (ODD) {
+        __syncwarp();
+        const int n = static_cast<int>(min(p.K - k0, static_cast<int64_t>(ROW_K)));
+        for (int r = 0; r < 8 && tile / spans * 8 + r < p.rows; ++r) {
+            const int64_t at = (tile / spans * 8 + r) * p.K + k0;
+            T* to = static_cast<T*>(p.values) + at;
+            if constexpr (F16OUT) {
+                const int shift = static_cast<int>(at & 1);
+                for (int e = 2 * lane - shift; e < n; e += 64) {
+                    if (e >= 0 && e + 1 < n) {
+                        *reinterpret_cast<__half2*>(to + e) = __halves2half2(rows[r][e], rows[r][e + 1]);
+                    } else {
+                        const int one = e < 0 ? 0 : e;  // n > 0
+                        to[one] = rows[r][one];
+                    }
+                }
+            } else {
+                for (int e = lane; e < n; e += 32) to[e] = rows[r][e];
+            }
         }
     }
 }
@@ -525,14 +548,18 @@ int gemm_mx_values(int64_t rows, int64_t K, int format, const void* codes, const
         const int64_t grid = (tiles + ROW_WARPS - 1) / ROW_WARPS;
         if (grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
         cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-        const cudaError_t e =
-            dtype_out == GEMM_OUT_F16
-                ? launch_format(format, k_mx_values<MXFP8, true>, k_mx_values<MXFP4, true>,
-                                k_mx_values<NVFP4, true>, grid, ROW_WARPS * 32, stream, p, spans,
-                                tiles)
-                : launch_format(format, k_mx_values<MXFP8, false>, k_mx_values<MXFP4, false>,
-                                k_mx_values<NVFP4, false>, grid, ROW_WARPS * 32, stream, p, spans,
-                                tiles);
+        auto launch = [&](auto f16, auto odd) {
+            constexpr bool F = decltype(f16)::value, O = decltype(odd)::value;
+            return launch_format(format, k_mx_values<MXFP8, F, O>, k_mx_values<MXFP4, F, O>,
+                                 k_mx_values<NVFP4, F, O>, grid, ROW_WARPS * 32, stream, p, spans,
+                                 tiles);
+        };
+        const std::true_type yes;
+        const std::false_type no;
+        const bool odd = K % 8 != 0;
+        const cudaError_t e = dtype_out == GEMM_OUT_F16 ? odd ? launch(yes, yes) : launch(yes, no)
+                              : odd                     ? launch(no, yes)
+                                                        : launch(no, no);
         return e == cudaSuccess ? ok() : cuda_fail("decoding launch", e);
     });
 }

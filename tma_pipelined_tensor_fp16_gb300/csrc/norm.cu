@@ -201,17 +201,24 @@ __global__ void __launch_bounds__(THREADS) k_rms_norm_grad(const __grid_constant
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
     int turn = 0;
-    for (int64_t row = group; row < p.tokens; row += groups) {
-        uint4 hv[VEC], dv[VEC];
+    uint4 hv[VEC], dv[VEC], rv[VEC];
+    auto load = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
             const int k = (i * LANES + lane) * 8;
-            hv[i] = dv[i] = make_uint4(0, 0, 0, 0);
-            if (k < p.width) {
+            hv[i] = dv[i] = rv[i] = make_uint4(0, 0, 0, 0);
+            if (k < p.width && row < p.tokens) {
                 hv[i] = *reinterpret_cast<const uint4*>(p.H + row * p.width + k);
                 dv[i] = *reinterpret_cast<const uint4*>(p.dZ + row * p.width + k);
+                if (p.dH) rv[i] = *reinterpret_cast<const uint4*>(p.dH + row * p.width + k);
             }
         }
+    };
+    // a row ahead, where the registers allow it
+    constexpr bool AHEAD = THREADS < 1024;
+    if (AHEAD) load(group);
+    for (int64_t row = group; row < p.tokens; row += groups) {
+        if (!AHEAD) load(row);
         float2 s = make_float2(0.0f, 0.0f);  // sum of h^2, of u h
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
@@ -240,6 +247,14 @@ __global__ void __launch_bounds__(THREADS) k_rms_norm_grad(const __grid_constant
                 s.y += slots[i].y;
             }
         }
+        uint4 h0[VEC], d0[VEC], r0[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            h0[i] = hv[i];
+            d0[i] = dv[i];
+            r0[i] = rv[i];
+        }
+        if (AHEAD) load(row + groups);  // on their way while this row is written
         const float rstd = 1.0f / sqrtf(fmaf(s.x, p.inv_width, p.eps));
         const float along = s.y * p.inv_width * rstd * rstd;  // mean(u n) * rstd
 #pragma unroll
@@ -247,8 +262,8 @@ __global__ void __launch_bounds__(THREADS) k_rms_norm_grad(const __grid_constant
             const int k = (i * LANES + lane) * 8;
             if (k >= p.width) continue;
             float h[8], d[8], w[8], x[8];
-            widen8(hv[i], h);
-            widen8(dv[i], d);
+            widen8(h0[i], h);
+            widen8(d0[i], d);
             widen8(__ldg(reinterpret_cast<const uint4*>(p.weight + k)), w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -257,7 +272,7 @@ __global__ void __launch_bounds__(THREADS) k_rms_norm_grad(const __grid_constant
             }
             if (p.dH) {
                 float r[8];
-                widen8(*reinterpret_cast<const uint4*>(p.dH + row * p.width + k), r);
+                widen8(r0[i], r);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] += r[j];
             }
@@ -276,26 +291,25 @@ __global__ void __launch_bounds__(THREADS) k_rms_norm_grad(const __grid_constant
     }
 }
 
-// dweight = sum of the parts: a CTA takes 32 columns, its warps every eighth part.
-__global__ void __launch_bounds__(256) k_rms_norm_weight(const float* parts, int64_t count, int width,
-                                                         float* dweight)
+// dweight = sum of the parts: a CTA takes 32 columns, its warps every 32nd part.
+__global__ void __launch_bounds__(1024) k_rms_norm_weight(const float* parts, int64_t count,
+                                                          int width, float* dweight)
 {
-    __shared__ float shared[8][33];
+    __shared__ float shared[32][33];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(threadIdx.x) / 32;
     const int k = static_cast<int>(blockIdx.x) * 32 + lane;
     float s = 0.0f;
-    if (k < width)
-        for (int64_t i = warp; i < count; i += 8) s += parts[i * width + k];
+    if (k < width) {
+#pragma unroll 8
+        for (int64_t i = warp; i < count; i += 32) s += parts[i * width + k];
+    }
     shared[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && k < width) {
-        s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s += shared[i][lane];
-        dweight[k] = s;
-    }
+    const int column = static_cast<int>(blockIdx.x) * 32 + warp;
+    s = warp_sum(shared[lane][warp]);
+    if (lane == 0 && column < width) dweight[column] = s;
 }
 
 // How many parts dweight has: rows per CTA and CTAs, by the width.
@@ -313,11 +327,11 @@ GradShape grad_shape(int64_t tokens, int64_t width)
     const int64_t vecs = (width + 7) / 8;
     GradShape s;
     int resident;
-    if (vecs <= 32) s = {0, 8, 0}, resident = 4;
-    else if (vecs <= 64) s = {1, 8, 0}, resident = 3;
-    else if (vecs <= 256) s = {2, 1, 0}, resident = 5;
+    if (vecs <= 32) s = {0, 8, 0}, resident = 4;  // by registers
+    else if (vecs <= 64) s = {1, 8, 0}, resident = 2;
+    else if (vecs <= 256) s = {2, 1, 0}, resident = 4;
     else if (vecs <= 512) s = {3, 1, 0}, resident = 3;
-    else if (vecs <= 1024) s = {4, 1, 0}, resident = 2;
+    else if (vecs <= 1024) s = {4, 1, 0}, resident = 1;
     else if (vecs <= 2048) s = {5, 1, 0}, resident = 1;
     else s = {6, 1, 0}, resident = 1;
     const int64_t want = (tokens + s.rows - 1) / s.rows;
@@ -450,7 +464,7 @@ int gemm_rms_norm_grad(int64_t tokens, int64_t width, const void* dZ, const void
         cudaError_t e = launch_norm_grad(p, s, stream);
         if (e == cudaSuccess)
             e = launch_dependent(k_rms_norm_weight, dim3(static_cast<unsigned>((width + 31) / 32)),
-                                 dim3(256), 0, 1, stream, static_cast<const float*>(p.parts),
+                                 dim3(1024), 0, 1, stream, static_cast<const float*>(p.parts),
                                  static_cast<int64_t>(s.ctas) * s.rows, p.width, dweight);
         return e == cudaSuccess ? ok() : cuda_fail("norm gradient launch", e);
     });

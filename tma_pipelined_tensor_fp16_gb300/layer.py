@@ -125,7 +125,7 @@ class GradClip:
 
     def _run(self, fn, stream, *args):
         torch = _torch()
-        if [t.data_ptr() for t in self._tensors] != self._addresses:
+        if list(map(torch._C.TensorBase.data_ptr, self._tensors)) != self._addresses:
             raise ValueError("a tensor's memory has moved: make a new GradClip")
         norm = _empty((1,), torch.float32, self.device, stream)
         work = _empty((_CLIP_WORKSPACE,), torch.uint8, self.device, stream)
