@@ -31,9 +31,10 @@
  * it, in blocks of 128 rows:
  *   codes   [row / 128][chunk][row % 128][16 bytes]; a chunk is 16 bytes of a row (16
  *           values of MXFP8, 32 of the others, the first of two in the low four bits);
- *           a row has 2 * ceil(K / 32) chunks of MXFP8, 2 * ceil(K / 64) of the others
+ *           a row has 2 * ceil(K / 32) chunks of MXFP8, 3 * ceil(K / 96) of MXFP4 and
+ *           2 * ceil(K / 64) of NVFP4
  *   scales  [row / 128][group][row % 32][row % 128 / 32][4 bytes]; a group is four
- *           consecutive blocks of a row; a row has ceil(blocks / 4) groups
+ *           consecutive blocks of a row, of MXFP4 three (its fourth byte is not used)
  * Behind a row's K values there are codes of zero with scales that are numbers.  The
  * rows that fill up the last block of 128 may hold anything.
  */

@@ -104,8 +104,10 @@ def storage(packed, scales, K, format):
     """Row-major bytes -> the storage order, entry by entry from its description."""
     rows = packed.shape[0]
     per_chunk = 16 if format == "mxfp8" else 32
-    chunks = 2 * -(-K // (2 * per_chunk))
-    groups = -(-K // (4 * BLOCK[format]))
+    step = 3 if format == "mxfp4" else 2      # chunks that a row is filled up to
+    per_group = 3 if format == "mxfp4" else 4  # blocks
+    chunks = step * -(-K // (step * per_chunk))
+    groups = -(-K // (per_group * BLOCK[format]))
     blocks = -(-rows // 128)
     c = np.zeros((blocks, chunks, 128, 16), np.uint8)
     s = np.zeros((blocks, groups, 32, 4, 4), np.uint8)
@@ -113,7 +115,7 @@ def storage(packed, scales, K, format):
         for b in range(packed.shape[1]):
             c[r // 128, b // 16, r % 128, b % 16] = packed[r, b]
         for b in range(scales.shape[1]):
-            s[r // 128, b // 4, r % 32, r % 128 // 32, b % 4] = scales[r, b]
+            s[r // 128, b // per_group, r % 32, r % 128 // 32, b % per_group] = scales[r, b]
     return c, s
 
 

@@ -161,7 +161,7 @@ __device__ __forceinline__ float most_of(const float (&x)[8])
 
 // Quantise eight consecutive values per lane (`vec` counts them from the row's start; lane
 // and lane + 1 hold neighbours, aligned so that a block's lanes are together) and store
-// the codes and, by the first lane of each group of four scales, the scales.  All lanes
+// the codes and, by the first lane of each group (or block) of scales, the scales.  All lanes
 // of the warp take part; those at or past the row's padded end store nothing.
 template <int FORMAT>
 __device__ __forceinline__ void quantize_store(const float (&x)[8], float t, float sixth,
@@ -181,14 +181,22 @@ __device__ __forceinline__ void quantize_store(const float (&x)[8], float t, flo
         else
             reinterpret_cast<uint32_t*>(to)[part] = q.x;
     }
-    // the bytes of four blocks: lanes LANES apart
     constexpr int LANES = mx_block(FORMAT) / 8;
-    uint32_t word = b.byte;
-    word |= __shfl_down_sync(0xffffffffu, word, LANES) << 8;
-    word |= __shfl_down_sync(0xffffffffu, word, 2 * LANES) << 16;
-    const int64_t group = vec / (4 * LANES);
-    if (row_valid && vec % (4 * LANES) == 0 && group < groups)
-        *reinterpret_cast<uint32_t*>(scales_row + group * MX_GROUP_BYTES) = word;
+    if constexpr (mx_group_blocks(FORMAT) == 4) {
+        // the bytes of four blocks: lanes LANES apart
+        uint32_t word = b.byte;
+        word |= __shfl_down_sync(0xffffffffu, word, LANES) << 8;
+        word |= __shfl_down_sync(0xffffffffu, word, 2 * LANES) << 16;
+        const int64_t group = vec / (4 * LANES);
+        if (row_valid && vec % (4 * LANES) == 0 && group < groups)
+            *reinterpret_cast<uint32_t*>(scales_row + group * MX_GROUP_BYTES) = word;
+    } else {
+        const int64_t block = vec / LANES;
+        const int64_t group = block / mx_group_blocks(FORMAT);
+        if (row_valid && vec % LANES == 0 && group < groups)
+            scales_row[group * MX_GROUP_BYTES + block % mx_group_blocks(FORMAT)] =
+                static_cast<uint8_t>(b.byte);
+    }
 }
 
 // Largest finite magnitude `bits` of a tensor -> the least power of two t with most <=

@@ -28,11 +28,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
               const __grid_constant__ CUtensorMap tmBc, const __grid_constant__ CUtensorMap tmBs,
               const __grid_constant__ CUtensorMap tmC, const __grid_constant__ MxParams p)
 {
-    constexpr int GROUPS = mx_stage_groups(FORMAT);
-    constexpr int STEPS = MX_STAGE_CHUNKS / 2;
+    constexpr int CHUNKS = mx_pair_chunks(FORMAT);
+    constexpr int GROUPS = mx_pair_groups(FORMAT);
+    constexpr int STEP_CHUNKS = mx_step_chunks(FORMAT);
+    constexpr int STEPS = CHUNKS / STEP_CHUNKS;
+    // scales are copied for so many groups and steps at a time
+    constexpr int BATCH_GROUPS = FORMAT == NVFP4 ? 3 : GROUPS;
+    constexpr int BATCH_STEPS = FORMAT == NVFP4 ? 3 : STEPS;
     constexpr int SCALES = mx_step_scales<FORMAT>;
-    constexpr uint32_t CTA_TX = 2 * MX_STAGE_CHUNKS * MX_CHUNK_BYTES + 3 * GROUPS * MX_GROUP_BYTES;
-    static_assert(SCALE_COL + GROUPS * 12 <= TMEM_COLS, "scales fit");
+    constexpr uint32_t CTA_TX = 2 * CHUNKS * MX_CHUNK_BYTES + 3 * GROUPS * MX_GROUP_BYTES;
+    static_assert(SCALE_COL + BATCH_GROUPS * 12 <= TMEM_COLS, "scales fit");
     extern __shared__ __align__(1024) uint8_t mx_smem[];
     const uint32_t raw = smem_u32(mx_smem);
     const uint32_t base = align1024(raw);
@@ -97,7 +102,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
                     const uint32_t at = base + static_cast<uint32_t>(stage) * L.stage;
                     if (leader) mbar_arrive_expect_tx(bar(BAR_FULL + stage), 2 * CTA_TX);
                     const uint32_t full = map_shared_rank(bar(BAR_FULL + stage), 0);
-                    const int c = s * MX_STAGE_CHUNKS, g = s * GROUPS;
+                    const int c = s * CHUNKS, g = s * GROUPS;
                     tma_load_2d_pair(at, &tmAc, full, 0, a_block * p.chunks + c);
                     tma_load_2d_pair(at + L.b_codes, &tmBc, full, 0, b_block * p.chunks + c);
                     tma_load_2d_pair(at + L.a_scales, &tmAs, full, 0, a_block * p.groups + g);
@@ -139,7 +144,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
         if (leader) {
             const uint32_t elected = lane == 0 ? 1u : 0u;
             const uint32_t a_sc = tmem_base + SCALE_COL;
-            const uint32_t b_sc = a_sc + GROUPS * 4;
+            const uint32_t b_sc = a_sc + BATCH_GROUPS * 4;
             int stage = 0;
             uint32_t phase = 0;
             int j = 0;
@@ -154,26 +159,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
                     if (!__all_sync(0xffffffffu, ok)) break;
                     tc_fence_after_sync();
                     const uint32_t at = base + static_cast<uint32_t>(stage) * L.stage;
-#pragma unroll
-                    for (int g = 0; g < GROUPS; ++g) {
-                        const uint32_t off = g * MX_GROUP_BYTES;
-                        copy_scales<true>(elected, a_sc + g * 4, at + L.a_scales + off);
-                        copy_scales<true>(elected, b_sc + g * 8, at + L.b_scales + off);
-                        copy_scales<true>(elected, b_sc + g * 8 + 4,
-                                          at + L.b_scales + GROUPS * MX_GROUP_BYTES + off);
-                    }
                     const uint64_t a_desc = core_desc(at, MX_CHUNK_BYTES);
                     const uint64_t b_desc = core_desc(at + L.b_codes, MX_CHUNK_BYTES);
-                    const int left = p.steps - s * STEPS;
+                    constexpr uint64_t CHUNK = MX_CHUNK_BYTES >> 4;
+                    const int left = p.steps - s * STEPS;  // steps from this stage on
 #pragma unroll
-                    for (int i = 0; i < STEPS; ++i) {
-                        if (i >= left) break;  // uniform
-                        mx_mma<FORMAT, true>(elected, d_tmem,
-                                             a_desc + i * (2 * MX_CHUNK_BYTES >> 4),
-                                             b_desc + i * (2 * MX_CHUNK_BYTES >> 4),
-                                             mx_idesc<FORMAT>(TILE, TILE, i * SCALES % 4),
-                                             a_sc + i * SCALES / 4 * 4, b_sc + i * SCALES / 4 * 8,
-                                             s == 0 && i == 0 ? 0u : 1u);
+                    for (int h = 0; h < STEPS / BATCH_STEPS; ++h) {
+                        const int rest = left - h * BATCH_STEPS;
+                        if (rest <= 0) break;  // uniform
+#pragma unroll
+                        for (int g = 0; g < BATCH_GROUPS; ++g) {
+                            const uint32_t off = (h * BATCH_GROUPS + g) * MX_GROUP_BYTES;
+                            copy_scales<true>(elected, a_sc + g * 4, at + L.a_scales + off);
+                            copy_scales<true>(elected, b_sc + g * 8, at + L.b_scales + off);
+                            copy_scales<true>(elected, b_sc + g * 8 + 4,
+                                              at + L.b_scales + GROUPS * MX_GROUP_BYTES + off);
+                        }
+                        const uint32_t first_mma = s == 0 && h == 0 ? 0u : 1u;
+                        if (FORMAT == NVFP4 && rest >= 3) {
+                            // 192 values as two MMAs of 96
+                            constexpr uint32_t idesc = mx_idesc<FORMAT>(TILE, TILE, 0) | MX_IDESC_K96;
+                            mx_mma_k96_pair(elected, d_tmem, a_desc + h * 6 * CHUNK,
+                                            b_desc + h * 6 * CHUNK, idesc, a_sc, b_sc, first_mma);
+                            mx_mma_k96_pair(elected, d_tmem, a_desc + (h * 6 + 3) * CHUNK,
+                                            b_desc + (h * 6 + 3) * CHUNK,
+                                            idesc | mx_idesc<FORMAT>(0, 0, 2), a_sc + 4, b_sc + 8, 1u);
+                            continue;
+                        }
+#pragma unroll
+                        for (int i = 0; i < BATCH_STEPS; ++i) {
+                            if (i >= rest) break;  // uniform
+                            mx_mma<FORMAT, true>(elected, d_tmem,
+                                                 a_desc + (h * BATCH_STEPS + i) * STEP_CHUNKS * CHUNK,
+                                                 b_desc + (h * BATCH_STEPS + i) * STEP_CHUNKS * CHUNK,
+                                                 mx_idesc<FORMAT>(TILE, TILE, i * SCALES % 4),
+                                                 a_sc + i * SCALES / 4 * 4,
+                                                 b_sc + i * SCALES / 4 * 8, i == 0 ? first_mma : 1u);
+                        }
                     }
                     mx_commit_pair(elected, bar(BAR_EMPTY + stage));
                     __syncwarp();

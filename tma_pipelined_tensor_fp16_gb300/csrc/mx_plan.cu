@@ -16,6 +16,7 @@ struct gemm_mx_plan {
     int device;
     bool pair, swapped;
     int cols, split;
+    int stage_chunks, stage_groups;
     int grid_x, grid_y, pipe_depth;
     unsigned smem_bytes;
     MxParams p;
@@ -140,11 +141,13 @@ gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K, int format
         p.N = static_cast<int>(N);
         p.chunks = static_cast<int>(mx_chunks(K, format));
         p.groups = static_cast<int>(mx_groups(K, format));
-        p.steps = p.chunks / 2;
-        p.stages = static_cast<int>(ceil_div(p.chunks, MX_STAGE_CHUNKS));
+        p.steps = p.chunks / mx_step_chunks(format);
         p.group_m = GROUP_M;
         const int64_t pair_tiles = ceil_div(M, 256) * ceil_div(N, 256);
         q.pair = kernel == GEMM_MX_PAIR || (kernel == GEMM_MX_AUTO && 2 * pair_tiles >= sms);
+        q.stage_chunks = q.pair ? mx_pair_chunks(format) : mx_stage_chunks(format);
+        q.stage_groups = q.pair ? mx_pair_groups(format) : mx_stage_groups(format);
+        p.stages = static_cast<int>(ceil_div(p.chunks, q.stage_chunks));
         if (q.pair && split > 1)
             return fail(GEMM_ERR_INVALID_ARG, "only GEMM_MX_SINGLE takes a split");
         if (q.pair) {
@@ -241,19 +244,19 @@ int gemm_mx_run(gemm_mx_plan* plan, const void* codes_a, const void* scales_a, c
         CUtensorMap tmUc, tmUs, tmVc, tmVs, tmC;
         int r = encode_storage(&tmUc, swapped ? codes_b : codes_a, MX_CHUNK_BYTES,
                                (swapped ? b_blocks : a_blocks) * q.chunks, MX_CHUNK_BYTES,
-                               MX_STAGE_CHUNKS, "codes");
+                               plan->stage_chunks, "codes");
         if (r == GEMM_OK)
             r = encode_storage(&tmUs, swapped ? scales_b : scales_a, MX_GROUP_BYTES,
                                (swapped ? b_blocks : a_blocks) * q.groups, MX_GROUP_BYTES,
-                               mx_stage_groups(f), "scales");
+                               plan->stage_groups, "scales");
         if (r == GEMM_OK)
             r = encode_storage(&tmVc, swapped ? codes_a : codes_b, MX_CHUNK_BYTES,
                                (swapped ? a_blocks : b_blocks) * q.chunks, v_bytes,
-                               MX_STAGE_CHUNKS, "codes");
+                               plan->stage_chunks, "codes");
         if (r == GEMM_OK)
             r = encode_storage(&tmVs, swapped ? scales_a : scales_b, MX_GROUP_BYTES,
                                (swapped ? a_blocks : b_blocks) * q.groups, MX_GROUP_BYTES,
-                               mx_stage_groups(f), "scales");
+                               plan->stage_groups, "scales");
         if (r == GEMM_OK && plan->pair)
             r = encode_output(&tmC, C, plan->M, plan->N, plan->dtype == GEMM_OUT_F16 ? 2 : 4);
         if (r != GEMM_OK) return r;

@@ -32,21 +32,23 @@ __device__ __forceinline__ uint64_t core_desc(uint32_t smem_addr, uint32_t lead)
 // Instruction descriptor of the block-scaled kinds:
 //   [4,6) scale id of B   [7,10) type of A   [10,13) type of B   [17,23) N >> 3
 //   [23] scale type (0 = ue4m3, 1 = ue8m0)   [24,29) M >> 4      [29,31) scale id of A
+//   [31] K of the 4-bit kinds (0 = 64, 1 = 96: sm_103a)
 // Types: kind::mxf8f6f4 e4m3 = 0; kind::mxf4 and mxf4nvf4 e2m1 = 1.
+constexpr uint32_t MX_IDESC_K96 = 1u << 31;
+
 template <int FORMAT>
 __device__ __forceinline__ constexpr uint32_t mx_idesc(int M, int N, int scale_id)
 {
     const uint32_t type = FORMAT == MXFP8 ? 0u : 1u;
-    return static_cast<uint32_t>(scale_id) << 4 | type << 7 | type << 10 |
+    return (FORMAT == MXFP4 ? MX_IDESC_K96 : 0u) | static_cast<uint32_t>(scale_id) << 4 | type << 7 | type << 10 |
            static_cast<uint32_t>(N >> 3) << 17 | (FORMAT == NVFP4 ? 0u : 1u) << 23 |
            static_cast<uint32_t>(M >> 4) << 24 | static_cast<uint32_t>(scale_id) << 29;
 }
 
-// The four scales of a group, per MMA step: mxfp8 one (32 values), mxfp4 two (64),
-// nvfp4 all four.
+// Bytes of the groups of scales per smallest MMA: mxfp8 one (32 values), mxfp4 a whole group
+// of three scales (96), nvfp4 a whole group of four (64).
 template <int FORMAT>
-constexpr int mx_step_scales = mx_step(FORMAT) / mx_block(FORMAT);
-
+constexpr int mx_step_scales = FORMAT == MXFP8 ? 1 : 4;
 // D (+)= A * B^T with scales from tensor memory, issued by the lane with `elected` set.
 #define TG_MX_MMA(GROUP, KIND)                                                                  \
     asm volatile(                                                                               \
@@ -72,15 +74,25 @@ __device__ __forceinline__ void mx_mma(uint32_t elected, uint32_t d_tmem, uint64
             TG_MX_MMA("1", "mxf8f6f4.block_scale.scale_vec::1X");
     } else if constexpr (FORMAT == MXFP4) {
         if constexpr (PAIR)
-            TG_MX_MMA("2", "mxf4.block_scale.scale_vec::2X");
+            TG_MX_MMA("2", "mxf4.block_scale.block32");
         else
-            TG_MX_MMA("1", "mxf4.block_scale.scale_vec::2X");
+            TG_MX_MMA("1", "mxf4.block_scale.block32");
     } else {
         if constexpr (PAIR)
             TG_MX_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
         else
             TG_MX_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
     }
+}
+
+// The same over 96 values (three chunks) of nvfp4 on a pair; the instruction descriptor has
+// MX_IDESC_K96.  Six scales: four of a group and two of the next, or (scale id 2) two and
+// four.
+__device__ __forceinline__ void mx_mma_k96_pair(uint32_t elected, uint32_t d_tmem, uint64_t a_desc,
+                                                uint64_t b_desc, uint32_t idesc, uint32_t a_scales,
+                                                uint32_t b_scales, uint32_t accumulate)
+{
+    TG_MX_MMA("2", "mxf4nvf4.block_scale.block16");
 }
 #undef TG_MX_MMA
 

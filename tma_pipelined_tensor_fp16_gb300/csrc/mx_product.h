@@ -9,15 +9,22 @@
 
 namespace tg {
 
-// Chunks (16 bytes of a row) per pipeline stage.
-constexpr int MX_STAGE_CHUNKS = 8;
-// Groups of four scales per stage, and values of the contraction.
-TG_HD constexpr int mx_stage_k(int format) { return MX_STAGE_CHUNKS * mx_chunk(format); }
-TG_HD constexpr int mx_stage_groups(int format) { return mx_stage_k(format) / mx_group(format); }
+// Chunks (16 bytes of a row) and groups of scales per pipeline stage of single CTAs, ...
+TG_HD constexpr int mx_stage_chunks(int format) { return format == MXFP4 ? 6 : 8; }
+TG_HD constexpr int mx_stage_groups(int format)
+{
+    return mx_stage_chunks(format) * mx_chunk(format) / mx_group(format);
+}
+// ... and of pairs, whose MMAs take 96 values of either 4-bit format: four of them.
+TG_HD constexpr int mx_pair_chunks(int format) { return format == MXFP8 ? 8 : 12; }
+TG_HD constexpr int mx_pair_groups(int format)
+{
+    return mx_pair_chunks(format) * mx_chunk(format) / mx_group(format);
+}
 
 struct MxParams {
     int M, N;
-    int steps;           // MMA steps (two chunks) of the whole contraction
+    int steps;           // smallest MMAs of the whole contraction
     int stages;          // pipeline stages of the whole contraction
     int chunks, groups;  // of a row
     int tiles_m, tiles_n, group_m;
@@ -64,8 +71,9 @@ TG_HD MxSingleLayout mx_single_layout(int format, int cols, int depth, bool swap
 {
     MxSingleLayout L;
     const uint32_t groups = static_cast<uint32_t>(mx_stage_groups(format));
-    L.v_codes = MX_STAGE_CHUNKS * MX_CHUNK_BYTES;
-    L.u_scales = L.v_codes + MX_STAGE_CHUNKS * static_cast<uint32_t>(cols) * 16u;
+    const uint32_t chunks = static_cast<uint32_t>(mx_stage_chunks(format));
+    L.v_codes = chunks * MX_CHUNK_BYTES;
+    L.u_scales = L.v_codes + chunks * static_cast<uint32_t>(cols) * 16u;
     L.v_scales = L.u_scales + groups * MX_GROUP_BYTES;
     L.stage = L.v_scales + groups * MX_GROUP_BYTES;
     L.stage = (L.stage + 1023u) / 1024u * 1024u;
@@ -87,9 +95,9 @@ struct MxPairLayout {
 TG_HD MxPairLayout mx_pair_layout(int format, int depth)
 {
     MxPairLayout L;
-    const uint32_t groups = static_cast<uint32_t>(mx_stage_groups(format));
-    L.b_codes = MX_STAGE_CHUNKS * MX_CHUNK_BYTES;
-    L.a_scales = 2 * MX_STAGE_CHUNKS * MX_CHUNK_BYTES;
+    const uint32_t groups = static_cast<uint32_t>(mx_pair_groups(format));
+    L.b_codes = static_cast<uint32_t>(mx_pair_chunks(format)) * MX_CHUNK_BYTES;
+    L.a_scales = 2 * L.b_codes;
     L.b_scales = L.a_scales + groups * MX_GROUP_BYTES;
     L.stage = (L.b_scales + 2 * groups * MX_GROUP_BYTES + 1023u) / 1024u * 1024u;
     L.staging = L.stage * static_cast<uint32_t>(depth);

@@ -102,10 +102,12 @@ __device__ __forceinline__ float find_tensor_scale(const QuantizeParams& p, uint
 //
 // A lane holds eight consecutive values; four lanes a block of 32, eight rows a warp.
 // So a warp's load touches 64 contiguous bytes of each of eight rows, and a store 128
-// contiguous bytes of a chunk's column.  A warp takes 8 rows x 128 values: a group of
-// four scales (two of nvfp4) is one 32-bit store.
+// contiguous bytes of a chunk's column.  A warp takes 8 rows x 128 values (96 of mxfp4): a
+// group of scales (two of nvfp4) is one 32-bit store.
 constexpr int ROW_WARPS = 8;
-constexpr int ROW_K = 128;  // values of a row per warp
+// Blocks of 32 values of a row per warp: a group of scales (two of nvfp4).
+TG_HD constexpr int row_spans(int format) { return format == MXFP4 ? 3 : 4; }
+TG_HD constexpr int row_k(int format) { return 32 * row_spans(format); }
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8])
 {
@@ -122,6 +124,7 @@ template <int FORMAT>
 __global__ void __launch_bounds__(ROW_WARPS * 32)
     k_mx_quantize(const __grid_constant__ QuantizeParams p, int64_t spans, int64_t tiles)
 {
+    constexpr int SPANS = row_spans(FORMAT), ROW_K = row_k(FORMAT);
     __shared__ uint32_t shared[ROW_WARPS];
     griddep_wait();
     griddep_launch_dependents();
@@ -135,18 +138,18 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
     const int64_t k0 = tile % spans * ROW_K;
     const bool valid = row < p.rows;
     const __half* x_row = p.X + (valid ? row : 0) * p.K;
-    uint4 v[4];
+    uint4 v[SPANS];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < SPANS; ++j) {
         const int64_t k = k0 + j * 32 + part * 8;
         v[j] = make_uint4(0, 0, 0, 0);
         if (valid && k < p.K) v[j] = *reinterpret_cast<const uint4*>(x_row + k);
     }
     uint8_t* codes = p.codes + mx_code_offset(row, k0 / mx_chunk(FORMAT), p.chunks);
-    uint32_t bytes[4];
+    uint32_t bytes[SPANS];
     constexpr int PER_CHUNK = mx_chunk(FORMAT) / 8;  // lanes of a chunk
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < SPANS; ++j) {
         float x[8];
         unpack8(v[j], x);
         const BlockScale b = block_scale<FORMAT>(block_most<FORMAT>(most_of(x)), t, sixth);
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
     if constexpr (FORMAT == NVFP4) {
         // 128 values are eight blocks: the second of a pair is two lanes on
 #pragma unroll
-        for (int j = 0; j < 4; ++j) bytes[j] |= __shfl_down_sync(0xffffffffu, bytes[j], 2) << 8;
+        for (int j = 0; j < SPANS; ++j) bytes[j] |= __shfl_down_sync(0xffffffffu, bytes[j], 2) << 8;
         if (valid && part == 0) {
             const int64_t g = k0 / mx_group(FORMAT);
             reinterpret_cast<uint32_t*>(scales)[0] = bytes[0] | bytes[1] << 16;
@@ -175,26 +178,28 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
     } else {
         if (valid && part == 0)
             *reinterpret_cast<uint32_t*>(scales) =
-                bytes[0] | bytes[1] << 8 | bytes[2] << 16 | bytes[3] << 24;
+                bytes[0] | bytes[1] << 8 | bytes[2] << 16 |
+                (SPANS > 3 ? bytes[SPANS - 1] << 24 : 0u);
     }
 }
 
 // ------------------------------------------------------------ along columns
 //
-// X is K x rows; a CTA takes 128 of K x 64 columns through shared memory, and a thread
+// X is K x rows; a CTA takes 128 of K (96 for mxfp4) x 64 columns through shared memory, and a thread
 // two columns x 32 of K: a block (two of nvfp4) of each, 16 or 32 bytes of codes a
 // column.  The columns are rows of the result, so a warp stores 1 KB without gaps.
-constexpr int COL_THREADS = 128;
 constexpr int COL_COLS = 64;
-constexpr int COL_K = 128;
+TG_HD constexpr int col_threads(int format) { return 32 * row_spans(format); }
 
 template <int FORMAT>
-__global__ void __launch_bounds__(COL_THREADS)
+__global__ void __launch_bounds__(col_threads(FORMAT))
     k_mx_quantize_columns(const __grid_constant__ QuantizeParams p, int64_t col_tiles)
 {
+    constexpr int COL_K = row_k(FORMAT), COL_THREADS = col_threads(FORMAT);
     __shared__ uint32_t shared[COL_THREADS / 32];
     __shared__ __align__(16) uint32_t tile[COL_K][COL_COLS / 2];
-    __shared__ uint8_t scale_bytes[COL_COLS][8];
+    __shared__ __align__(4) uint8_t scale_bytes[COL_COLS][8];
+    if (FORMAT == MXFP4 && threadIdx.x < COL_COLS) scale_bytes[threadIdx.x][3] = 0;
     griddep_wait();
     griddep_launch_dependents();
     const float t = find_tensor_scale<FORMAT>(p, shared);
@@ -306,7 +311,7 @@ __device__ __forceinline__ void decode8(uint2 q, __half2 (&v)[4])
     for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<__half2*>(&h[i]);
 }
 
-// Lanes as in k_mx_quantize: a warp takes 8 rows x 128 values.  With ODD a row's length is
+// Lanes as in k_mx_quantize: a warp takes 8 rows x 128 (96) values.  With ODD a row's length is
 // no multiple of 8, so that rows start anywhere: the values go through shared memory and
 // leave as aligned words, 64 bytes and more at a time.
 template <int FORMAT, bool F16OUT, bool ODD>
@@ -318,6 +323,7 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
     const int64_t tile = static_cast<int64_t>(blockIdx.x) * ROW_WARPS + threadIdx.x / 32;
     if (tile >= tiles) return;
     const int lane = static_cast<int>(lane_id());
+    constexpr int SPANS = row_spans(FORMAT), ROW_K = row_k(FORMAT);
     using T = typename std::conditional<F16OUT, __half, float>::type;
     __shared__ T staged[ODD ? ROW_WARPS : 1][8][ROW_K + 2];
     T(*rows)[ROW_K + 2] = staged[ODD ? threadIdx.x / 32 : 0];
@@ -337,9 +343,9 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
         words[g] = valid && k0 / mx_group(FORMAT) + g < p.groups
                        ? *reinterpret_cast<const uint32_t*>(scales + g * MX_GROUP_BYTES)
                        : 0u;
-    uint2 q[4];
+    uint2 q[SPANS];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < SPANS; ++j) {
         const int64_t k = k0 + j * 32 + part * 8;
         const int chunk = (j * 4 + part) / PER_CHUNK;
         q[j] = make_uint2(0, 0);
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
         }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < SPANS; ++j) {
         const int64_t k = k0 + j * 32 + part * 8;
         if (k >= p.K) break;
         float s;
@@ -497,12 +503,12 @@ int gemm_mx_quantize(int64_t rows, int64_t K, int format, int transpose, const v
         if (rows == 0 && format != NVFP4) return ok();
         if (transpose) {
             const int64_t cols = std::max<int64_t>(1, (rows + COL_COLS - 1) / COL_COLS);
-            const int64_t grid = cols * ((K + COL_K - 1) / COL_K);
+            const int64_t grid = cols * ((K + row_k(format) - 1) / row_k(format));
             if (grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
             e = launch_format(format, k_mx_quantize_columns<MXFP8>, k_mx_quantize_columns<MXFP4>,
-                              k_mx_quantize_columns<NVFP4>, grid, COL_THREADS, stream, p, cols);
+                              k_mx_quantize_columns<NVFP4>, grid, col_threads(format), stream, p, cols);
         } else {
-            const int64_t spans = (K + ROW_K - 1) / ROW_K;
+            const int64_t spans = (K + row_k(format) - 1) / row_k(format);
             const int64_t tiles = (rows + 7) / 8 * spans;
             const int64_t grid = std::max<int64_t>(1, (tiles + ROW_WARPS - 1) / ROW_WARPS);
             if (grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
@@ -543,7 +549,7 @@ int gemm_mx_values(int64_t rows, int64_t K, int format, const void* codes, const
         p.scales = static_cast<const uint8_t*>(scales);
         p.tensor_scale = tensor_scale;
         p.values = values;
-        const int64_t spans = (K + ROW_K - 1) / ROW_K;
+        const int64_t spans = (K + row_k(format) - 1) / row_k(format);
         const int64_t tiles = (rows + 7) / 8 * spans;
         const int64_t grid = (tiles + ROW_WARPS - 1) / ROW_WARPS;
         if (grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");

@@ -62,14 +62,16 @@ __global__ void __launch_bounds__(MX_THREADS)
                 const __grid_constant__ CUtensorMap tmVc, const __grid_constant__ CUtensorMap tmVs,
                 const __grid_constant__ MxParams p, int f16out)
 {
+    constexpr int CHUNKS = mx_stage_chunks(FORMAT);
     constexpr int GROUPS = mx_stage_groups(FORMAT);
-    constexpr int STEPS = MX_STAGE_CHUNKS / 2;
+    constexpr int STEP_CHUNKS = mx_step_chunks(FORMAT);
+    constexpr int STEPS = CHUNKS / STEP_CHUNKS;
     constexpr int SCALES = mx_step_scales<FORMAT>;
     constexpr uint32_t ACC_COLS = COLS < 32 ? 32 : COLS;
     constexpr uint32_t SET_COLS = GROUPS * 8;  // scales of one stage; two sets alternate
     constexpr uint32_t TMEM_COLS = tmem_columns(ACC_COLS + 2 * SET_COLS);
     constexpr uint32_t V_LEAD = COLS * 16;
-    constexpr uint32_t TX = MX_STAGE_CHUNKS * (MX_CHUNK_BYTES + V_LEAD) + 2 * GROUPS * MX_GROUP_BYTES;
+    constexpr uint32_t TX = CHUNKS * (MX_CHUNK_BYTES + V_LEAD) + 2 * GROUPS * MX_GROUP_BYTES;
     extern __shared__ __align__(1024) uint8_t mx_smem[];
     const uint32_t raw = smem_u32(mx_smem);
     const uint32_t base = align1024(raw);
@@ -128,10 +130,10 @@ __global__ void __launch_bounds__(MX_THREADS)
                 const uint32_t at = base + static_cast<uint32_t>(stage) * L.stage;
                 const uint32_t full = bar(BAR_FULL + stage);
                 mbar_arrive_expect_tx(full, TX);
-                tma_load_2d(at, &tmUc, full, 0, u_row + s * MX_STAGE_CHUNKS);
+                tma_load_2d(at, &tmUc, full, 0, u_row + s * CHUNKS);
                 tma_load_2d(at + L.u_scales, &tmUs, full, 0, u_group + s * GROUPS);
                 tma_load_2d(at + L.v_codes, &tmVc, full, v_x,
-                            v_block * p.chunks + s * MX_STAGE_CHUNKS);
+                            v_block * p.chunks + s * CHUNKS);
                 tma_load_2d(at + L.v_scales, &tmVs, full, 0, v_block * p.groups + s * GROUPS);
             }
             ++armed;
@@ -177,8 +179,8 @@ __global__ void __launch_bounds__(MX_THREADS)
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
                 if (i >= left) break;  // uniform
-                mx_mma<FORMAT, false>(elected, tmem_base, u_desc + i * (2 * MX_CHUNK_BYTES >> 4),
-                                      v_desc + i * (2 * V_LEAD >> 4),
+                mx_mma<FORMAT, false>(elected, tmem_base, u_desc + i * (STEP_CHUNKS * MX_CHUNK_BYTES >> 4),
+                                      v_desc + i * (STEP_CHUNKS * V_LEAD >> 4),
                                       mx_idesc<FORMAT>(128, COLS, i * SCALES % 4),
                                       u_sc + i * SCALES / 4 * 4, v_sc + i * SCALES / 4 * 4,
                                       s == s0 && i == 0 ? 0u : 1u);

@@ -22,6 +22,8 @@ MX_FORMATS = {"mxfp8": 0, "mxfp4": 1, "nvfp4": 2}
 MX_KERNELS = {"auto": 0, "pair": 1, "single": 2}
 _BLOCK = {"mxfp8": 32, "mxfp4": 32, "nvfp4": 16}
 _CHUNK = {"mxfp8": 16, "mxfp4": 32, "nvfp4": 32}
+_STEP = {"mxfp8": 2, "mxfp4": 3, "nvfp4": 2}    # chunks that rows are filled up to
+_GROUP = {"mxfp8": 4, "mxfp4": 3, "nvfp4": 4}   # blocks of a group of scales
 _WORKSPACE = 4096  # GEMM_MX_WORKSPACE_BYTES
 
 
@@ -36,8 +38,9 @@ def _shapes(rows, K, format):
     """Shapes of the storage: codes (row blocks, chunks, 128, 16) and scales (row blocks,
     groups, 32, 4, 4)."""
     blocks = -(-rows // 128)
-    chunks = 2 * -(-K // (2 * _CHUNK[format]))
-    groups = -(-K // (4 * _BLOCK[format]))
+    step = _STEP[format]
+    chunks = step * -(-K // (step * _CHUNK[format]))
+    groups = -(-K // (_GROUP[format] * _BLOCK[format]))
     return (blocks, chunks, 128, 16), (blocks, groups, 32, 4, 4)
 
 
@@ -98,8 +101,9 @@ class MXTensor:
         c[:rows, :width] = codes
         if format != "mxfp8" and K % 2:
             c[:, width - 1] &= 15
-        s = scales.new_zeros((blocks * 128, groups * 4))
+        s = scales.new_zeros((blocks * 128, groups * _GROUP[format]))
         s[:rows, :per_row] = scales
+        s = torch.nn.functional.pad(s.reshape(blocks * 128, groups, -1), (0, 4 - _GROUP[format]))
         c = c.reshape(blocks, 128, chunks, 16).permute(0, 2, 1, 3).contiguous()
         s = s.reshape(blocks, 4, 32, groups, 4).permute(0, 3, 2, 1, 4).contiguous()
         return cls(rows, K, format, c, s, tensor_scale)
@@ -107,10 +111,10 @@ class MXTensor:
     def to_codes(self):
         """(codes, scales) in row-major order, as ``from_codes`` takes them."""
         blocks, chunks, _, _ = self.codes.shape
-        groups = self.scales.shape[1]
         width = self.K if self.format == "mxfp8" else -(-self.K // 2)
         c = self.codes.permute(0, 2, 1, 3).reshape(blocks * 128, chunks * 16)
-        s = self.scales.permute(0, 3, 2, 1, 4).reshape(blocks * 128, groups * 4)
+        s = self.scales.permute(0, 3, 2, 1, 4)[..., :_GROUP[self.format]]
+        s = s.reshape(blocks * 128, -1)
         return (c[:self.rows, :width].contiguous(),
                 s[:self.rows, :-(-self.K // _BLOCK[self.format])].contiguous())
 
