@@ -47,7 +47,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
     const uint32_t staging = base + L.staging;
     const uint32_t bars = base + L.bars;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gen + L.bars + TMEM_SLOT_OFFSET);
-    const int warp = static_cast<int>(threadIdx.x) >> 5;
+    const int warp = static_cast<int>(warp_uniform(threadIdx.x >> 5));
     const uint32_t lane = lane_id();
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
@@ -82,7 +82,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
     tc_fence_after_sync();
     griddep_wait();
     griddep_launch_dependents();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = warp_uniform(*tmem_slot);
 
     if (warp == 0) {
         // ---------------------------------------------------- producer

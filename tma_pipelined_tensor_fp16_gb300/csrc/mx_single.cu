@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(MX_THREADS)
     const MxSingleLayout L = mx_single_layout(FORMAT, COLS, D, SWAPPED);
     const uint32_t bars = base + L.bars;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gen + L.bars + TMEM_SLOT_OFFSET);
-    const int warp = static_cast<int>(threadIdx.x) >> 5;
+    const int warp = static_cast<int>(warp_uniform(threadIdx.x >> 5));
     const uint32_t lane = lane_id();
     const uint32_t rank = p.split > 1 ? cluster_ctarank() : 0u;
     const int u_tile = static_cast<int>(blockIdx.x) / p.split;
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(MX_THREADS)
     tc_fence_after_sync();
     griddep_wait();
     griddep_launch_dependents();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = warp_uniform(*tmem_slot);
 
     if (warp == 0) {
         // ---------------------------------------------------- producer
