@@ -20,6 +20,33 @@ constexpr uint32_t ACC_SHIFT = 192;   // second accumulator
 constexpr uint32_t SCALE_COL = 448;
 constexpr uint32_t TMEM_COLS = 512;
 
+// Both blocks of B's scales in one box.
+__device__ __forceinline__ void load_3d_pair(uint32_t dst, const CUtensorMap* map,
+                                             uint32_t cluster_bar, int32_t x, int32_t y, int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
+        : "memory");
+}
+
+// Whether the phase has completed, without waiting for it.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t"
+        ".reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 }  // namespace
 
 template <int FORMAT, bool F16OUT>
@@ -32,12 +59,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
     constexpr int GROUPS = mx_pair_groups(FORMAT);
     constexpr int STEP_CHUNKS = mx_step_chunks(FORMAT);
     constexpr int STEPS = CHUNKS / STEP_CHUNKS;
-    // scales are copied for so many groups and steps at a time
-    constexpr int BATCH_GROUPS = FORMAT == NVFP4 ? 3 : GROUPS;
-    constexpr int BATCH_STEPS = FORMAT == NVFP4 ? 3 : STEPS;
     constexpr int SCALES = mx_step_scales<FORMAT>;
     constexpr uint32_t CTA_TX = 2 * CHUNKS * MX_CHUNK_BYTES + 3 * GROUPS * MX_GROUP_BYTES;
-    static_assert(SCALE_COL + BATCH_GROUPS * 12 <= TMEM_COLS, "scales fit");
+    static_assert(SCALE_COL + GROUPS * 12 <= TMEM_COLS, "scales fit");
     extern __shared__ __align__(1024) uint8_t mx_smem[];
     const uint32_t raw = smem_u32(mx_smem);
     const uint32_t base = align1024(raw);
@@ -106,9 +130,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
                     tma_load_2d_pair(at, &tmAc, full, 0, a_block * p.chunks + c);
                     tma_load_2d_pair(at + L.b_codes, &tmBc, full, 0, b_block * p.chunks + c);
                     tma_load_2d_pair(at + L.a_scales, &tmAs, full, 0, a_block * p.groups + g);
-                    tma_load_2d_pair(at + L.b_scales, &tmBs, full, 0, nt * 2 * p.groups + g);
-                    tma_load_2d_pair(at + L.b_scales + GROUPS * MX_GROUP_BYTES, &tmBs, full, 0,
-                                     (nt * 2 + 1) * p.groups + g);
+                    load_3d_pair(at + L.b_scales, &tmBs, full, 0, g, nt * 2);
                 }
                 ++armed;
                 __syncwarp();
@@ -142,69 +164,87 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
     } else if (warp == 1) {
         // ----------------------------------------- MMA issuer (leader)
         if (leader) {
+            // (Every branch is on a vote: with one that the lanes might take apart, operands
+            // count as different per lane and each MMA of nvfp4 takes 203 ns.)
             const uint32_t elected = lane == 0 ? 1u : 0u;
             const uint32_t a_sc = tmem_base + SCALE_COL;
-            const uint32_t b_sc = a_sc + BATCH_GROUPS * 4;
+            const uint32_t b_sc = a_sc + GROUPS * 4;
             int stage = 0;
             uint32_t phase = 0;
             int j = 0;
-            for (int t = first; t < tiles && !wd.aborted; t += clusters, ++j) {
-                if (j > 0)
-                    wd.wait(bar(BAR_TMEM_EMPTY), static_cast<uint32_t>(j - 1) & 1u,
-                            WAIT_TMEM_EMPTY, t, -1);
-                tc_fence_after_sync();
+            bool ready = false;  // the next stage has been seen to be full
+            bool running = true;
+            for (int t = first; t < tiles && running; t += clusters, ++j) {
+                if (j > 0) {
+                    const bool drained = wd.wait(bar(BAR_TMEM_EMPTY), static_cast<uint32_t>(j - 1) & 1u,
+                                                 WAIT_TMEM_EMPTY, t, -1);
+                    running = __all_sync(0xffffffffu, drained);
+                }
                 const uint32_t d_tmem = tmem_base + (j & 1 ? ACC_SHIFT : 0u);
-                for (int s = 0; s < p.stages; ++s) {
-                    const bool ok = wd.wait(bar(BAR_FULL + stage), phase, WAIT_FULL, t, s);
-                    if (!__all_sync(0xffffffffu, ok)) break;
+                for (int s = 0; s < p.stages && running; ++s) {
+                    if (!ready) {
+                        const bool full = wd.wait(bar(BAR_FULL + stage), phase, WAIT_FULL, t, s);
+                        running = __all_sync(0xffffffffu, full);
+                        if (!running) break;
+                    }
                     tc_fence_after_sync();
                     const uint32_t at = base + static_cast<uint32_t>(stage) * L.stage;
-                    const uint64_t a_desc = core_desc(at, MX_CHUNK_BYTES);
-                    const uint64_t b_desc = core_desc(at + L.b_codes, MX_CHUNK_BYTES);
-                    constexpr uint64_t CHUNK = MX_CHUNK_BYTES >> 4;
-                    const int left = p.steps - s * STEPS;  // steps from this stage on
-#pragma unroll
-                    for (int h = 0; h < STEPS / BATCH_STEPS; ++h) {
-                        const int rest = left - h * BATCH_STEPS;
-                        if (rest <= 0) break;  // uniform
-#pragma unroll
-                        for (int g = 0; g < BATCH_GROUPS; ++g) {
-                            const uint32_t off = (h * BATCH_GROUPS + g) * MX_GROUP_BYTES;
-                            copy_scales<true>(elected, a_sc + g * 4, at + L.a_scales + off);
-                            copy_scales<true>(elected, b_sc + g * 8, at + L.b_scales + off);
-                            copy_scales<true>(elected, b_sc + g * 8 + 4,
-                                              at + L.b_scales + GROUPS * MX_GROUP_BYTES + off);
-                        }
-                        const uint32_t first_mma = s == 0 && h == 0 ? 0u : 1u;
-                        if (FORMAT == NVFP4 && rest >= 3) {
-                            // 192 values as two MMAs of 96
-                            constexpr uint32_t idesc = mx_idesc<FORMAT>(TILE, TILE, 0) | MX_IDESC_K96;
-                            mx_mma_k96_pair(elected, d_tmem, a_desc + h * 6 * CHUNK,
-                                            b_desc + h * 6 * CHUNK, idesc, a_sc, b_sc, first_mma);
-                            mx_mma_k96_pair(elected, d_tmem, a_desc + (h * 6 + 3) * CHUNK,
-                                            b_desc + (h * 6 + 3) * CHUNK,
-                                            idesc | mx_idesc<FORMAT>(0, 0, 2), a_sc + 4, b_sc + 8, 1u);
-                            continue;
-                        }
-#pragma unroll
-                        for (int i = 0; i < BATCH_STEPS; ++i) {
-                            if (i >= rest) break;  // uniform
-                            mx_mma<FORMAT, true>(elected, d_tmem,
-                                                 a_desc + (h * BATCH_STEPS + i) * STEP_CHUNKS * CHUNK,
-                                                 b_desc + (h * BATCH_STEPS + i) * STEP_CHUNKS * CHUNK,
-                                                 mx_idesc<FORMAT>(TILE, TILE, i * SCALES % 4),
-                                                 a_sc + i * SCALES / 4 * 4,
-                                                 b_sc + i * SCALES / 4 * 8, i == 0 ? first_mma : 1u);
-                        }
-                    }
-                    mx_commit_pair(elected, bar(BAR_EMPTY + stage));
-                    __syncwarp();
+                    const uint32_t empty = bar(BAR_EMPTY + stage);
                     if (++stage == D) {
                         stage = 0;
                         phase ^= 1u;
                     }
+                    const uint64_t a_desc = core_desc(at, MX_CHUNK_BYTES);
+                    const uint64_t b_desc = core_desc(at + L.b_codes, MX_CHUNK_BYTES);
+                    constexpr uint64_t CHUNK = MX_CHUNK_BYTES >> 4;
+                    const int rest = p.steps - s * STEPS;  // steps from this stage on
+                    const uint32_t more = s == 0 ? 0u : 1u;
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g) {
+                        const uint32_t off = g * MX_GROUP_BYTES;
+                        copy_scales<true>(elected, a_sc + g * 4, at + L.a_scales + off);
+                        copy_scales<true>(elected, b_sc + g * 8, at + L.b_scales + off);
+                        copy_scales<true>(elected, b_sc + g * 8 + 4,
+                                          at + L.b_scales + GROUPS * MX_GROUP_BYTES + off);
+                    }
+                    if (rest >= STEPS) {
+                        if constexpr (FORMAT == NVFP4) {
+                            // 192 values as two MMAs of 96
+                            constexpr uint32_t idesc = mx_idesc<FORMAT>(TILE, TILE, 0) | MX_IDESC_K96;
+                            mx_mma_k96_pair(elected, d_tmem, a_desc, b_desc, idesc, a_sc, b_sc, more);
+                            ready = __all_sync(0xffffffffu, mbar_test(bar(BAR_FULL + stage), phase));
+                            mx_mma_k96_pair(elected, d_tmem, a_desc + 3 * CHUNK, b_desc + 3 * CHUNK,
+                                            idesc | mx_idesc<FORMAT>(0, 0, 2), a_sc + 4, b_sc + 8, 1u);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < STEPS; ++i) {
+                                // looked at before the stage's last MMA: those that are
+                                // queued cover the look
+                                if (i == STEPS - 1) ready = __all_sync(0xffffffffu, mbar_test(bar(BAR_FULL + stage), phase));
+                                mx_mma<FORMAT, true>(
+                                    elected, d_tmem, a_desc + i * STEP_CHUNKS * CHUNK,
+                                    b_desc + i * STEP_CHUNKS * CHUNK,
+                                    mx_idesc<FORMAT>(TILE, TILE, i * SCALES % 4),
+                                    a_sc + i * SCALES / 4 * 4, b_sc + i * SCALES / 4 * 8,
+                                    i == 0 ? more : 1u);
+                            }
+                        }
+                    } else {
+                        ready = false;
+#pragma unroll
+                        for (int i = 0; i < STEPS - 1; ++i) {
+                            if (i >= rest) break;  // uniform
+                            mx_mma<FORMAT, true>(
+                                elected, d_tmem, a_desc + i * STEP_CHUNKS * CHUNK,
+                                b_desc + i * STEP_CHUNKS * CHUNK,
+                                mx_idesc<FORMAT>(TILE, TILE, i * SCALES % 4),
+                                a_sc + i * SCALES / 4 * 4, b_sc + i * SCALES / 4 * 8,
+                                i == 0 ? more : 1u);
+                        }
+                    }
+                    mx_commit_pair(elected, empty);
                 }
-                if (__all_sync(0xffffffffu, !wd.aborted)) mx_commit_pair(elected, bar(BAR_TMEM_FULL));
+                if (running) mx_commit_pair(elected, bar(BAR_TMEM_FULL));
             }
             if (lane == 0) {
                 mma_commit_pair_multicast(bar(BAR_DRAIN), static_cast<uint16_t>(1u));

@@ -35,18 +35,20 @@ constexpr int GROUP_M = 8;
 
 // Tensor map over operand storage as rows of `row_bytes` (a chunk or a group of scales of
 // 128 rows), boxes of `box_bytes` x `box_rows`; 64-bit elements, no swizzle, zero fill.
+// With `blocks` a third dimension of so many blocks of `rows` rows, and boxes of two.
 int encode_storage(CUtensorMap* map, const void* base, int64_t row_bytes, int64_t rows,
-                   int box_bytes, int box_rows, const char* what)
+                   int box_bytes, int box_rows, const char* what, int64_t blocks = 0)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode_fn();
     if (!enc) return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes / 8),
-                                static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes / 8),
-                               static_cast<cuuint32_t>(box_rows)};
-    const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<void*>(base), dims,
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(row_bytes / 8),
+                                static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(blocks)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes),
+                                   static_cast<cuuint64_t>(row_bytes * rows)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / 8),
+                               static_cast<cuuint32_t>(box_rows), 2};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, blocks ? 3 : 2, const_cast<void*>(base), dims,
                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -254,9 +256,11 @@ int gemm_mx_run(gemm_mx_plan* plan, const void* codes_a, const void* scales_a, c
                                (swapped ? a_blocks : b_blocks) * q.chunks, v_bytes,
                                plan->stage_chunks, "codes");
         if (r == GEMM_OK)
-            r = encode_storage(&tmVs, swapped ? scales_a : scales_b, MX_GROUP_BYTES,
-                               (swapped ? a_blocks : b_blocks) * q.groups, MX_GROUP_BYTES,
-                               plan->stage_groups, "scales");
+            r = plan->pair ? encode_storage(&tmVs, scales_b, MX_GROUP_BYTES, q.groups,
+                                            MX_GROUP_BYTES, plan->stage_groups, "scales", b_blocks)
+                           : encode_storage(&tmVs, swapped ? scales_a : scales_b, MX_GROUP_BYTES,
+                                            (swapped ? a_blocks : b_blocks) * q.groups,
+                                            MX_GROUP_BYTES, plan->stage_groups, "scales");
         if (r == GEMM_OK && plan->pair)
             r = encode_output(&tmC, C, plan->M, plan->N, plan->dtype == GEMM_OUT_F16 ? 2 : 4);
         if (r != GEMM_OK) return r;
