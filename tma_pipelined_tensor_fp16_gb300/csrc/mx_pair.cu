@@ -20,6 +20,65 @@ constexpr uint32_t ACC_SHIFT = 192;   // second accumulator
 constexpr uint32_t SCALE_COL = 448;
 constexpr uint32_t TMEM_COLS = 512;
 
+// 64 columns, one wait for both halves.
+__device__ __forceinline__ void tmem_load_64cols(uint32_t taddr, uint32_t (&r)[64])
+{
+#define TG_LD32(base, col)                                                                       \
+    asm volatile(                                                                                \
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "                                                \
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "                \
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];" \
+        : "=r"(r[base + 0]), "=r"(r[base + 1]), "=r"(r[base + 2]), "=r"(r[base + 3]),            \
+          "=r"(r[base + 4]), "=r"(r[base + 5]), "=r"(r[base + 6]), "=r"(r[base + 7]),            \
+          "=r"(r[base + 8]), "=r"(r[base + 9]), "=r"(r[base + 10]), "=r"(r[base + 11]),          \
+          "=r"(r[base + 12]), "=r"(r[base + 13]), "=r"(r[base + 14]), "=r"(r[base + 15]),        \
+          "=r"(r[base + 16]), "=r"(r[base + 17]), "=r"(r[base + 18]), "=r"(r[base + 19]),        \
+          "=r"(r[base + 20]), "=r"(r[base + 21]), "=r"(r[base + 22]), "=r"(r[base + 23]),        \
+          "=r"(r[base + 24]), "=r"(r[base + 25]), "=r"(r[base + 26]), "=r"(r[base + 27]),        \
+          "=r"(r[base + 28]), "=r"(r[base + 29]), "=r"(r[base + 30]), "=r"(r[base + 31])         \
+        : "r"(taddr + (col))                                                                     \
+        : "memory")
+    TG_LD32(0, 0);
+    TG_LD32(32, 32);
+#undef TG_LD32
+    // the registers are used as results of the wait, so that nothing reads them before it
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i])::"memory");
+}
+
+// As stage_and_store (device_common.cuh) with one buffer a warp: it is written once the
+// store before has read it.
+template <bool F16OUT>
+__device__ __forceinline__ void stage_one(const uint32_t* v, uint32_t row, uint32_t staging,
+                                          const CUtensorMap* tmap_c, int col0, int m0, int M)
+{
+    const uint32_t quarter = row >> 5;
+    const uint32_t r = row & 31u;
+    const uint32_t buf = staging + quarter * WARP_STAGING_BYTES;
+    if (r == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+    const uint32_t row_base = buf + r * 128u;
+#pragma unroll
+    for (uint32_t c = 0; c < 8; ++c) {
+        const uint32_t dst = row_base + ((c ^ (r & 7u)) << 4);
+        if constexpr (F16OUT)
+            st_shared_v4(dst, pack_half2(v[8 * c + 0], v[8 * c + 1]),
+                         pack_half2(v[8 * c + 2], v[8 * c + 3]),
+                         pack_half2(v[8 * c + 4], v[8 * c + 5]),
+                         pack_half2(v[8 * c + 6], v[8 * c + 7]));
+        else
+            st_shared_v4(dst, v[4 * c + 0], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    const int wm0 = m0 + static_cast<int>(quarter * 32u);
+    if (r == 0 && wm0 < M) {
+        tma_store_2d(tmap_c, buf, col0, wm0);
+        bulk_commit_group();
+    }
+}
+
 // Both blocks of B's scales in one box.
 __device__ __forceinline__ void load_3d_pair(uint32_t dst, const CUtensorMap* map,
                                              uint32_t cluster_bar, int32_t x, int32_t y, int32_t z)
@@ -255,14 +314,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
     } else {
         // -------------------------------------------------------- epilogue
         if (p.debug_stall == 2) wd.wait(bar(BAR_STALL), 0, WAIT_STALL, -1, -1);
-        constexpr int SUB = F16OUT ? 64 : 32;  // columns of 128 bytes
-        constexpr int SUBS = TILE / SUB;
-        constexpr int SHARED_SUBS = (TILE - static_cast<int>(ACC_SHIFT)) / SUB;
+        constexpr int READ = 64;               // columns read at a time,
+        constexpr int SUB = F16OUT ? 64 : 32;  // and stored: 128 bytes
+        static_assert(TILE - static_cast<int>(ACC_SHIFT) == READ, "the shared columns");
         const uint32_t q = static_cast<uint32_t>(warp & 3);
         const uint32_t row = q * 32u + lane;
         const uint32_t to_leader = map_shared_rank(bar(BAR_TMEM_EMPTY), 0);
         const float alpha = mx_alpha(p);
-        uint32_t sub_count = 0;
         int j = 0;
         for (int t = first; t < tiles; t += clusters, ++j) {
             int mt, nt;
@@ -274,28 +332,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
             const uint32_t taddr = tmem_base + (j & 1 ? ACC_SHIFT : 0u) + (q * 32u << 16);
             const int m0 = mt * TILE + static_cast<int>(rank) * MX_ROWS;
             // the columns that the next tile's accumulator shares come first
-            const int start = j & 1 ? 0 : SUBS - SHARED_SUBS;
+            const int start = j & 1 ? 0 : TILE - READ;
 #pragma unroll 1
-            for (int i = 0; i < SUBS; ++i) {
-                const int sub = (start + i) % SUBS;
-                const int col0 = nt * TILE + sub * SUB;
-                uint32_t v[SUB];
-                if (col0 < p.N) {
-#pragma unroll
-                    for (int h = 0; h < SUB; h += 32)
-                        tmem_load_32cols(taddr + sub * SUB + h,
-                                         *reinterpret_cast<uint32_t(*)[32]>(&v[h]));
-                }
-                if (i == SHARED_SUBS - 1) {
+            for (int i = 0; i < TILE; i += READ) {
+                const int col = (start + i) % TILE;
+                uint32_t v[READ];
+                tmem_load_64cols(taddr + col, v);
+                if (i == 0) {
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(to_leader);
                 }
-                if (col0 < p.N) {
 #pragma unroll
-                    for (int c = 0; c < SUB; ++c)
-                        v[c] = __float_as_uint(__uint_as_float(v[c]) * alpha);
-                    stage_and_store<F16OUT>(v, row, staging, &tmC, col0, m0, p.M, sub_count, true);
+                for (int c = 0; c < READ; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * alpha);
+#pragma unroll
+                for (int c = 0; c < READ; c += SUB) {
+                    const int col0 = nt * TILE + col + c;
+                    if (col0 < p.N)  // uniform
+                        stage_one<F16OUT>(v + c, row, staging, &tmC, col0, m0, p.M);
                 }
             }
         }
