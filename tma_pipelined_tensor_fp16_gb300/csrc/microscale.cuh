@@ -65,7 +65,8 @@ __device__ __forceinline__ BlockScale block_scale(float most, float t, float six
         if (!finite) byte = 0x7fu;
         b.byte = byte;
         b.divisor = float_of_e4m3(byte) * t;
-        b.factor = 1.0f / b.divisor;
+        // an approximation is enough: scaled() corrects with the exact remainder
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b.factor) : "f"(b.divisor));
     } else {
         // most = m * 2^k with 1 <= m < 2; the largest value is M * 2^K with the same
         // bounds: s = 2^(k - K), doubled where m > M
@@ -165,15 +166,15 @@ __device__ __forceinline__ float most_of(const float (&x)[8])
 // of the warp take part; those at or past the row's padded end store nothing.
 template <int FORMAT>
 __device__ __forceinline__ void quantize_store(const float (&x)[8], float t, float sixth,
-                                               int64_t vec, uint8_t* codes_row,
-                                               uint8_t* scales_row, int64_t chunks,
-                                               int64_t groups, bool row_valid)
+                                               int vec, uint8_t* codes_row,
+                                               uint8_t* scales_row, int chunks, int groups,
+                                               bool row_valid)
 {
     const BlockScale b = block_scale<FORMAT>(block_most<FORMAT>(most_of(x)), t, sixth);
     const uint2 q = encode8<FORMAT>(x, b);
     constexpr int PER_CHUNK = mx_chunk(FORMAT) / 8;
-    const int64_t chunk = vec / PER_CHUNK;
-    const int part = static_cast<int>(vec % PER_CHUNK);
+    const int chunk = vec / PER_CHUNK;
+    const int part = vec % PER_CHUNK;
     if (row_valid && chunk < chunks) {
         uint8_t* to = codes_row + chunk * MX_CHUNK_BYTES;
         if constexpr (FORMAT == MXFP8)
@@ -187,16 +188,26 @@ __device__ __forceinline__ void quantize_store(const float (&x)[8], float t, flo
         uint32_t word = b.byte;
         word |= __shfl_down_sync(0xffffffffu, word, LANES) << 8;
         word |= __shfl_down_sync(0xffffffffu, word, 2 * LANES) << 16;
-        const int64_t group = vec / (4 * LANES);
+        const int group = vec / (4 * LANES);
         if (row_valid && vec % (4 * LANES) == 0 && group < groups)
             *reinterpret_cast<uint32_t*>(scales_row + group * MX_GROUP_BYTES) = word;
     } else {
-        const int64_t block = vec / LANES;
-        const int64_t group = block / mx_group_blocks(FORMAT);
+        const int block = vec / LANES;
+        const int group = block / mx_group_blocks(FORMAT);
         if (row_valid && vec % LANES == 0 && group < groups)
             scales_row[group * MX_GROUP_BYTES + block % mx_group_blocks(FORMAT)] =
                 static_cast<uint8_t>(b.byte);
     }
+}
+
+// Magnitudes of eight fp16 values in four words: the largest, NaN above the infinity.
+__device__ __forceinline__ float most_of_halves(const uint4& v)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    __half2 m = __habs2(*reinterpret_cast<const __half2*>(&w[0]));
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __half2*>(&w[i])));
+    return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
 }
 
 // Largest finite magnitude `bits` of a tensor -> the least power of two t with most <=

@@ -120,9 +120,37 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8])
     }
 }
 
+// How a CTA's warps lie: 1 << k_log along a row, the others in the next rows.
+struct RowTiling {
+    uint32_t cta_spans;  // CTAs along a row
+    int k_log;
+    int64_t grid;
+};
+
+RowTiling row_tiling(int64_t rows, int64_t K, int format)
+{
+    const int64_t spans = (K + row_k(format) - 1) / row_k(format);
+    RowTiling t;
+    t.k_log = spans >= 8 ? 3 : spans >= 4 ? 2 : spans >= 2 ? 1 : 0;
+    t.cta_spans = static_cast<uint32_t>((spans + (1 << t.k_log) - 1) >> t.k_log);
+    const int64_t cta_rows = 8 * (ROW_WARPS >> t.k_log);
+    t.grid = std::max<int64_t>(1, (rows + cta_rows - 1) / cta_rows) * t.cta_spans;
+    return t;
+}
+
+// First row and first value of this warp's tile.
+__device__ __forceinline__ void row_tile(uint32_t cta_spans, int k_log, int width, int64_t& row0,
+                                         int64_t& k0)
+{
+    const uint32_t warp = threadIdx.x / 32;
+    const uint32_t y = blockIdx.x / cta_spans, x = blockIdx.x - y * cta_spans;
+    row0 = (static_cast<int64_t>(y) * (ROW_WARPS >> k_log) + (warp >> k_log)) * 8;
+    k0 = (static_cast<int64_t>(x) * (1 << k_log) + (warp & ((1u << k_log) - 1u))) * width;
+}
+
 template <int FORMAT>
 __global__ void __launch_bounds__(ROW_WARPS * 32)
-    k_mx_quantize(const __grid_constant__ QuantizeParams p, int64_t spans, int64_t tiles)
+    k_mx_quantize(const __grid_constant__ QuantizeParams p, uint32_t cta_spans, int k_log)
 {
     constexpr int SPANS = row_spans(FORMAT), ROW_K = row_k(FORMAT);
     __shared__ uint32_t shared[ROW_WARPS];
@@ -132,10 +160,10 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
     const float sixth = 1.0f / (6.0f * t);
     const int lane = static_cast<int>(lane_id());
     const int r = lane / 4, part = lane % 4;
-    const int64_t tile = static_cast<int64_t>(blockIdx.x) * ROW_WARPS + threadIdx.x / 32;
-    if (tile >= tiles) return;
-    const int64_t row = tile / spans * 8 + r;
-    const int64_t k0 = tile % spans * ROW_K;
+    int64_t row0, k0;
+    row_tile(cta_spans, k_log, ROW_K, row0, k0);
+    if (row0 >= p.rows || k0 >= p.K) return;
+    const int64_t row = row0 + r;
     const bool valid = row < p.rows;
     const __half* x_row = p.X + (valid ? row : 0) * p.K;
     uint4 v[SPANS];
@@ -152,7 +180,8 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
     for (int j = 0; j < SPANS; ++j) {
         float x[8];
         unpack8(v[j], x);
-        const BlockScale b = block_scale<FORMAT>(block_most<FORMAT>(most_of(x)), t, sixth);
+        const BlockScale b =
+            block_scale<FORMAT>(block_most<FORMAT>(most_of_halves(v[j])), t, sixth);
         const uint2 q = encode8<FORMAT>(x, b);
         const int chunk = (j * 4 + part) / PER_CHUNK;
         if (valid && k0 / mx_chunk(FORMAT) + chunk < p.chunks) {
@@ -193,7 +222,7 @@ TG_HD constexpr int col_threads(int format) { return 32 * row_spans(format); }
 
 template <int FORMAT>
 __global__ void __launch_bounds__(col_threads(FORMAT))
-    k_mx_quantize_columns(const __grid_constant__ QuantizeParams p, int64_t col_tiles)
+    k_mx_quantize_columns(const __grid_constant__ QuantizeParams p, uint32_t col_tiles)
 {
     constexpr int COL_K = row_k(FORMAT), COL_THREADS = col_threads(FORMAT);
     __shared__ uint32_t shared[COL_THREADS / 32];
@@ -205,8 +234,9 @@ __global__ void __launch_bounds__(col_threads(FORMAT))
     const float t = find_tensor_scale<FORMAT>(p, shared);
     const float sixth = 1.0f / (6.0f * t);
     const int tid = static_cast<int>(threadIdx.x);
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x) % col_tiles * COL_COLS;
-    const int64_t k0 = static_cast<int64_t>(blockIdx.x) / col_tiles * COL_K;
+    const uint32_t k_tile = blockIdx.x / col_tiles;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x - k_tile * col_tiles) * COL_COLS;
+    const int64_t k0 = static_cast<int64_t>(k_tile) * COL_K;
 #pragma unroll
     for (int i = 0; i < COL_K * COL_COLS / 8 / COL_THREADS; ++i) {
         const int line = i * (COL_THREADS / 8) + tid / 8;
@@ -316,22 +346,22 @@ __device__ __forceinline__ void decode8(uint2 q, __half2 (&v)[4])
 // leave as aligned words, 64 bytes and more at a time.
 template <int FORMAT, bool F16OUT, bool ODD>
 __global__ void __launch_bounds__(ROW_WARPS * 32)
-    k_mx_values(const __grid_constant__ ValuesParams p, int64_t spans, int64_t tiles)
+    k_mx_values(const __grid_constant__ ValuesParams p, uint32_t cta_spans, int k_log)
 {
+    int64_t row0, k0;
+    row_tile(cta_spans, k_log, row_k(FORMAT), row0, k0);
+    if (row0 >= p.rows || k0 >= p.K) return;
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t tile = static_cast<int64_t>(blockIdx.x) * ROW_WARPS + threadIdx.x / 32;
-    if (tile >= tiles) return;
     const int lane = static_cast<int>(lane_id());
     constexpr int SPANS = row_spans(FORMAT), ROW_K = row_k(FORMAT);
     using T = typename std::conditional<F16OUT, __half, float>::type;
     __shared__ T staged[ODD ? ROW_WARPS : 1][8][ROW_K + 2];
     T(*rows)[ROW_K + 2] = staged[ODD ? threadIdx.x / 32 : 0];
-    const int64_t row = tile / spans * 8 + lane / 4;
+    const int64_t row = row0 + lane / 4;
     if (!ODD && row >= p.rows) return;
     const bool valid = row < p.rows;
     const int part = lane % 4;
-    const int64_t k0 = tile % spans * ROW_K;
     const float t = p.tensor_scale ? *p.tensor_scale : 1.0f;
     constexpr int PER_CHUNK = mx_chunk(FORMAT) / 8;
     const uint8_t* codes = p.codes + mx_code_offset(row, k0 / mx_chunk(FORMAT), p.chunks);
@@ -399,8 +429,8 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
     if constexpr (ODD) {
         __syncwarp();
         const int n = static_cast<int>(min(p.K - k0, static_cast<int64_t>(ROW_K)));
-        for (int r = 0; r < 8 && tile / spans * 8 + r < p.rows; ++r) {
-            const int64_t at = (tile / spans * 8 + r) * p.K + k0;
+        for (int r = 0; r < 8 && row0 + r < p.rows; ++r) {
+            const int64_t at = (row0 + r) * p.K + k0;
             T* to = static_cast<T*>(p.values) + at;
             if constexpr (F16OUT) {
                 const int shift = static_cast<int>(at & 1);
@@ -506,14 +536,14 @@ int gemm_mx_quantize(int64_t rows, int64_t K, int format, int transpose, const v
             const int64_t grid = cols * ((K + row_k(format) - 1) / row_k(format));
             if (grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
             e = launch_format(format, k_mx_quantize_columns<MXFP8>, k_mx_quantize_columns<MXFP4>,
-                              k_mx_quantize_columns<NVFP4>, grid, col_threads(format), stream, p, cols);
+                              k_mx_quantize_columns<NVFP4>, grid, col_threads(format), stream, p,
+                              static_cast<uint32_t>(cols));
         } else {
-            const int64_t spans = (K + row_k(format) - 1) / row_k(format);
-            const int64_t tiles = (rows + 7) / 8 * spans;
-            const int64_t grid = std::max<int64_t>(1, (tiles + ROW_WARPS - 1) / ROW_WARPS);
-            if (grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
+            const RowTiling t = row_tiling(rows, K, format);
+            if (t.grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
             e = launch_format(format, k_mx_quantize<MXFP8>, k_mx_quantize<MXFP4>,
-                              k_mx_quantize<NVFP4>, grid, ROW_WARPS * 32, stream, p, spans, tiles);
+                              k_mx_quantize<NVFP4>, t.grid, ROW_WARPS * 32, stream, p, t.cta_spans,
+                              t.k_log);
         }
         return e == cudaSuccess ? ok() : cuda_fail("quantisation launch", e);
     });
@@ -549,16 +579,14 @@ int gemm_mx_values(int64_t rows, int64_t K, int format, const void* codes, const
         p.scales = static_cast<const uint8_t*>(scales);
         p.tensor_scale = tensor_scale;
         p.values = values;
-        const int64_t spans = (K + row_k(format) - 1) / row_k(format);
-        const int64_t tiles = (rows + 7) / 8 * spans;
-        const int64_t grid = (tiles + ROW_WARPS - 1) / ROW_WARPS;
-        if (grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
+        const RowTiling t = row_tiling(rows, K, format);
+        if (t.grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
         cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
         auto launch = [&](auto f16, auto odd) {
             constexpr bool F = decltype(f16)::value, O = decltype(odd)::value;
             return launch_format(format, k_mx_values<MXFP8, F, O>, k_mx_values<MXFP4, F, O>,
-                                 k_mx_values<NVFP4, F, O>, grid, ROW_WARPS * 32, stream, p, spans,
-                                 tiles);
+                                 k_mx_values<NVFP4, F, O>, t.grid, ROW_WARPS * 32, stream, p,
+                                 t.cta_spans, t.k_log);
         };
         const std::true_type yes;
         const std::false_type no;

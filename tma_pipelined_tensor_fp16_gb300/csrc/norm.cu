@@ -128,8 +128,8 @@ __global__ void __launch_bounds__(THREADS) k_rms_norm(const __grid_constant__ No
         if constexpr (FORMAT >= 0)
             quantize_store<FORMAT>(z, 1.0f, 1.0f / 6.0f, vec,
                                    p.codes + mx_code_offset(row, 0, p.chunks),
-                                   p.scales + mx_scale_offset(row, 0, p.groups), p.chunks,
-                                   p.groups, valid);
+                                   p.scales + mx_scale_offset(row, 0, p.groups),
+                                   static_cast<int>(p.chunks), static_cast<int>(p.groups), valid);
     }
 }
 

@@ -9,6 +9,7 @@ in a layer and in its training step.
 Conventions are those of ``experts``.
 """
 import ctypes
+import functools
 import math
 
 from .binding import GemmError, last_error, lib
@@ -59,6 +60,15 @@ def rms_norm(X, weight, residual=None, eps=1e-6, half=True, format=None, out=Non
     return Z, X if residual is None else H, Q
 
 
+@functools.lru_cache(maxsize=256)
+def _grad_workspace(tokens, width):
+    """Bytes that rms_norm_grad needs."""
+    size = lib().gemm_rms_norm_grad_workspace(tokens, width)
+    if size < 0:
+        raise GemmError(lib().gemm_last_status(), last_error())
+    return size
+
+
 def rms_norm_grad(dZ, H, weight, dH=None, eps=1e-6, out=None, dweight=None, stream=None):
     """(dX, dweight) of ``rms_norm`` for dZ (tokens x width fp16), its H and, with a
     residual, dH: the gradient that reaches H by its other uses.  dX (fp16; `out` may be
@@ -73,10 +83,7 @@ def rms_norm_grad(dZ, H, weight, dH=None, eps=1e-6, out=None, dweight=None, stre
         _tensor("dH", dH, dZ.shape, torch.float16, dev)
     dX = _output("out", out, dZ.shape, torch.float16, dev, stream)
     dw = _output("dweight", dweight, (width,), torch.float32, dev, stream)
-    size = lib().gemm_rms_norm_grad_workspace(tokens, width)
-    if size < 0:
-        raise GemmError(lib().gemm_last_status(), last_error())
-    work = _empty((size,), torch.uint8, dev, stream)
+    work = _empty((_grad_workspace(tokens, width),), torch.uint8, dev, stream)
     _call(lib().gemm_rms_norm_grad, dev, stream, tokens, width, _ptr(dZ), _ptr(H), _ptr(weight),
           _ptr(dH), eps, _ptr(dX), _ptr(dw), _ptr(work))
     if stream is not None:
