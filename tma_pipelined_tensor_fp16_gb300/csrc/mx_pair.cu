@@ -339,9 +339,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
                 uint32_t v[READ];
                 tmem_load_64cols(taddr + col, v);
                 if (i == 0) {
+                    // relaxed: the loads are complete, and nothing else is handed over
                     tc_fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(to_leader);
+                    if (lane == 0) mbar_arrive_cluster_relaxed(to_leader);
                 }
 #pragma unroll
                 for (int c = 0; c < READ; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * alpha);
