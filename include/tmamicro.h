@@ -85,16 +85,10 @@ typedef struct gemm_mx_plan gemm_mx_plan; /* opaque; owned by the library */
 TMAGEMM_API gemm_mx_plan* gemm_mx_create_plan(int64_t M, int64_t N, int64_t K, int format,
                                               int dtype_out);
 
-/* Same with an explicit kernel: tiles of 256 x 256 on CTA pairs, two such pairs that share
- * their columns (rows of B) in a cluster (QUAD), or 128 rows of one operand
+/* Same with an explicit kernel: tiles of 256 x 256 on CTA pairs, or 128 rows of one operand
  * and up to 128 of the other on single CTAs, with `split` (1, 2, 4 or 8; 0: automatic) CTAs
  * of a cluster sharing a tile's length. */
-typedef enum {
-    GEMM_MX_AUTO = 0,
-    GEMM_MX_PAIR = 1,
-    GEMM_MX_SINGLE = 2,
-    GEMM_MX_QUAD = 3
-} gemm_mx_kernel;
+typedef enum { GEMM_MX_AUTO = 0, GEMM_MX_PAIR = 1, GEMM_MX_SINGLE = 2 } gemm_mx_kernel;
 
 TMAGEMM_API gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K, int format,
                                                  int dtype_out, int kernel, int split);

@@ -90,44 +90,6 @@ __device__ __forceinline__ void load_3d_pair(uint32_t dst, const CUtensorMap* ma
         : "memory");
 }
 
-// The same boxes to every CTA of `mask`; the bytes count at the barrier of the leader of
-// each one's pair.
-__device__ __forceinline__ void load_2d_multicast(uint32_t dst, const CUtensorMap* map,
-                                                  uint32_t cluster_bar, int32_t x, int32_t y,
-                                                  uint16_t mask)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(cluster_bar), "h"(mask)
-        : "memory");
-}
-
-__device__ __forceinline__ void load_3d_multicast(uint32_t dst, const CUtensorMap* map,
-                                                  uint32_t cluster_bar, int32_t x, int32_t y,
-                                                  int32_t z, uint16_t mask)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".multicast::cluster [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar), "h"(mask)
-        : "memory");
-}
-
-// An arrival in every CTA of `mask` once the lane's MMAs so far are complete.
-__device__ __forceinline__ void commit_multicast(uint32_t elected, uint32_t bar, uint32_t mask)
-{
-    asm volatile(
-        "{\n\t"
-        ".reg .pred p;\n\t"
-        "setp.ne.b32 p, %1, 0;\n\t"
-        "@p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
-        ".b64 [%0], %2;\n\t"
-        "}\n" ::"r"(bar),
-        "r"(elected), "h"(static_cast<uint16_t>(mask))
-        : "memory");
-}
-
 // Whether the phase has completed, without waiting for it.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
 {
@@ -146,8 +108,8 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
 
 }  // namespace
 
-template <int FORMAT, bool F16OUT, int PAIRS>
-__global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(MX_THREADS, 1)
+template <int FORMAT, bool F16OUT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
     k_mx_pair(const __grid_constant__ CUtensorMap tmAc, const __grid_constant__ CUtensorMap tmAs,
               const __grid_constant__ CUtensorMap tmBc, const __grid_constant__ CUtensorMap tmBs,
               const __grid_constant__ CUtensorMap tmC, const __grid_constant__ MxParams p)
@@ -170,14 +132,11 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(MX_THREADS, 
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gen + L.bars + TMEM_SLOT_OFFSET);
     const int warp = static_cast<int>(warp_uniform(threadIdx.x >> 5));
     const uint32_t lane = lane_id();
-    const uint32_t cta = cluster_ctarank();
-    const uint32_t pair = PAIRS == 1 ? 0u : cta >> 1;
-    const uint32_t rank = cta & 1u;            // in the pair
-    const uint32_t leader_cta = cta - rank;
+    const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
-    const int clusters = static_cast<int>(gridDim.x) / (2 * PAIRS);
-    const int first = static_cast<int>(blockIdx.x) / (2 * PAIRS);
-    const int tiles = p.tiles_m * p.tiles_n;   // of PAIRS * 256 rows x 256 columns
+    const int clusters = static_cast<int>(gridDim.x) / 2;
+    const int first = static_cast<int>(blockIdx.x) / 2;
+    const int tiles = p.tiles_m * p.tiles_n;
     Watchdog wd = mx_watchdog(p);
     auto bar = [&](int slot) { return bars + static_cast<uint32_t>(slot) * 8u; };
 
@@ -188,8 +147,8 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(MX_THREADS, 
         prefetch_tensormap(&tmBs);
         prefetch_tensormap(&tmC);
         for (int s = 0; s < D; ++s) {
-            mbar_init(bar(BAR_FULL + s), 1);       // leader: its producer
-            mbar_init(bar(BAR_EMPTY + s), PAIRS);  // the leaders' multicast commits
+            mbar_init(bar(BAR_FULL + s), 1);   // leader: its producer
+            mbar_init(bar(BAR_EMPTY + s), 1);  // the leader's multicast commit
         }
         mbar_init(bar(BAR_TMEM_FULL), 1);      // the leader's multicast commit
         mbar_init(bar(BAR_TMEM_EMPTY), 8);     // leader: 4 epilogue warps x 2 CTAs
@@ -214,40 +173,23 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(MX_THREADS, 
         int stage = 0;
         uint32_t phase = 0;
         int armed = 0;
-        bool running = true;
-        const uint32_t full0 = map_shared_rank(bar(BAR_FULL), leader_cta);
-        for (int t = first; t < tiles && running; t += clusters) {
+        for (int t = first; t < tiles && !wd.aborted; t += clusters) {
             int mt, nt;
             raster_tile(t, p.tiles_m, p.tiles_n, p.group_m, mt, nt);
-            const int a_block = (mt * PAIRS + static_cast<int>(pair)) * 2 + static_cast<int>(rank);
+            const int a_block = mt * 2 + static_cast<int>(rank);
             const int b_block = nt * 2 + static_cast<int>(rank);
             for (int s = 0; s < p.stages; ++s) {
                 const bool ok = wd.wait(bar(BAR_EMPTY + stage), phase ^ 1u, WAIT_EMPTY, t, s);
-                running = __all_sync(0xffffffffu, ok);
-                if (!running) break;
+                if (!ok) break;
                 if (lane == 0) {
                     const uint32_t at = base + static_cast<uint32_t>(stage) * L.stage;
                     if (leader) mbar_arrive_expect_tx(bar(BAR_FULL + stage), 2 * CTA_TX);
-                    const uint32_t full = full0 + static_cast<uint32_t>(stage) * 8u;
+                    const uint32_t full = map_shared_rank(bar(BAR_FULL + stage), 0);
                     const int c = s * CHUNKS, g = s * GROUPS;
                     tma_load_2d_pair(at, &tmAc, full, 0, a_block * p.chunks + c);
+                    tma_load_2d_pair(at + L.b_codes, &tmBc, full, 0, b_block * p.chunks + c);
                     tma_load_2d_pair(at + L.a_scales, &tmAs, full, 0, a_block * p.groups + g);
-                    if constexpr (PAIRS == 1) {
-                        tma_load_2d_pair(at + L.b_codes, &tmBc, full, 0, b_block * p.chunks + c);
-                        load_3d_pair(at + L.b_scales, &tmBs, full, 0, g, nt * 2);
-                    } else {
-                        // half of this rank's block of B for both CTAs of the rank, and, in
-                        // turn, a block of scales for all
-                        constexpr int HALF = CHUNKS / 2;
-                        const int h = static_cast<int>(pair) * HALF;
-                        load_2d_multicast(at + L.b_codes + h * MX_CHUNK_BYTES, &tmBc, full, 0,
-                                          b_block * p.chunks + c + h,
-                                          static_cast<uint16_t>(5u << rank));
-                        if ((static_cast<uint32_t>(s) & 1u) == pair)
-                            load_3d_multicast(at + L.b_scales + rank * GROUPS * MX_GROUP_BYTES,
-                                              &tmBs, full, 0, g, b_block,
-                                              static_cast<uint16_t>(15u));
-                    }
+                    load_3d_pair(at + L.b_scales, &tmBs, full, 0, g, nt * 2);
                 }
                 ++armed;
                 __syncwarp();
@@ -258,9 +200,8 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(MX_THREADS, 
             }
         }
         // The copies in flight land before the CTAs can exit: the leader drains the phases it
-        // armed, which take in the copies of all CTAs to its pair; a CTA whose run is
-        // abandoned allows a grace period too, as a leader may not have armed a phase for
-        // its copies.
+        // armed, which take in the peer's copies; a peer that gave up allows a grace
+        // period too, as its leader may not have armed a phase for them.
         if (lane == 0) {
             if (leader) {
                 for (int i = 0; i < D && i < armed; ++i) {
@@ -272,8 +213,7 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(MX_THREADS, 
                     }
                     wd.drain(bar(BAR_FULL + stage), phase);
                 }
-            }
-            if (!running) {
+            } else if (wd.aborted) {
                 const uint64_t t0 = globaltimer_ns();
                 while (globaltimer_ns() - t0 < 200000ull) {
                 }
@@ -361,12 +301,12 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(MX_THREADS, 
                                 i == 0 ? more : 1u);
                         }
                     }
-                    commit_multicast(elected, empty, PAIRS == 1 ? 3u : 15u);
+                    mx_commit_pair(elected, empty);
                 }
-                if (running) commit_multicast(elected, bar(BAR_TMEM_FULL), 3u << leader_cta);
+                if (running) mx_commit_pair(elected, bar(BAR_TMEM_FULL));
             }
             if (lane == 0) {
-                mma_commit_pair_multicast(bar(BAR_DRAIN), static_cast<uint16_t>(1u << leader_cta));
+                mma_commit_pair_multicast(bar(BAR_DRAIN), static_cast<uint16_t>(1u));
                 wd.drain(bar(BAR_DRAIN), 0);
             }
             __syncwarp();
@@ -379,7 +319,7 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(MX_THREADS, 
         static_assert(TILE - static_cast<int>(ACC_SHIFT) == READ, "the shared columns");
         const uint32_t q = static_cast<uint32_t>(warp & 3);
         const uint32_t row = q * 32u + lane;
-        const uint32_t to_leader = map_shared_rank(bar(BAR_TMEM_EMPTY), leader_cta);
+        const uint32_t to_leader = map_shared_rank(bar(BAR_TMEM_EMPTY), 0);
         const float alpha = mx_alpha(p);
         int j = 0;
         for (int t = first; t < tiles; t += clusters, ++j) {
@@ -390,7 +330,7 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(MX_THREADS, 
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after_sync();
             const uint32_t taddr = tmem_base + (j & 1 ? ACC_SHIFT : 0u) + (q * 32u << 16);
-            const int m0 = (mt * PAIRS + static_cast<int>(pair)) * TILE + static_cast<int>(rank) * MX_ROWS;
+            const int m0 = mt * TILE + static_cast<int>(rank) * MX_ROWS;
             // the columns that the next tile's accumulator shares come first
             const int start = j & 1 ? 0 : TILE - READ;
 #pragma unroll 1
@@ -418,7 +358,7 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(MX_THREADS, 
         __syncwarp();
     }
 
-    // nothing of any CTA is touched remotely after this point
+    // nothing of either CTA is touched remotely after this point
     tc_fence_before_sync();
     cluster_sync_all();
     if (warp == 1) {
@@ -427,53 +367,15 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(MX_THREADS, 
     }
 }
 
-template <int FORMAT, int PAIRS>
-static cudaError_t launch_pairs(const MxSpec& s, cudaStream_t stream)
+template <int FORMAT>
+static cudaError_t launch_format(const MxSpec& s, cudaStream_t stream)
 {
-    auto kernel = s.f16out ? k_mx_pair<FORMAT, true, PAIRS> : k_mx_pair<FORMAT, false, PAIRS>;
+    auto kernel = s.f16out ? k_mx_pair<FORMAT, true> : k_mx_pair<FORMAT, false>;
     cudaError_t e = ensure_smem_limit(kernel, s.smem_bytes);
     if (e != cudaSuccess) return e;
     return launch_dependent(kernel, dim3(static_cast<unsigned>(s.grid_x)), dim3(MX_THREADS),
                             s.smem_bytes, 1, stream, *s.codes_u, *s.scales_u, *s.codes_v,
                             *s.scales_v, *s.out, s.p);
-}
-
-template <int FORMAT>
-static cudaError_t launch_format(const MxSpec& s, cudaStream_t stream)
-{
-    return s.pairs == 2 ? launch_pairs<FORMAT, 2>(s, stream) : launch_pairs<FORMAT, 1>(s, stream);
-}
-
-cudaError_t mx_pair_clusters(int format, int pairs, unsigned smem_bytes, int* clusters)
-{
-    const void* kernel = nullptr;
-    cudaError_t e = cudaSuccess;
-    auto prepare = [&](auto k) {
-        kernel = reinterpret_cast<const void*>(k);
-        e = ensure_smem_limit(k, smem_bytes);
-    };
-    if (pairs == 2) {
-        if (format == MXFP8) prepare(k_mx_pair<MXFP8, true, 2>);
-        else if (format == MXFP4) prepare(k_mx_pair<MXFP4, true, 2>);
-        else prepare(k_mx_pair<NVFP4, true, 2>);
-    } else {
-        if (format == MXFP8) prepare(k_mx_pair<MXFP8, true, 1>);
-        else if (format == MXFP4) prepare(k_mx_pair<MXFP4, true, 1>);
-        else prepare(k_mx_pair<NVFP4, true, 1>);
-    }
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-    cfg.blockDim = dim3(MX_THREADS);
-    cfg.dynamicSmemBytes = smem_bytes;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(2 * pairs);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaOccupancyMaxActiveClusters(clusters, kernel, &cfg);
 }
 
 cudaError_t launch_mx_pair(const MxSpec& s, cudaStream_t stream)

@@ -15,7 +15,7 @@ struct gemm_mx_plan {
     int format, dtype;
     int device;
     bool pair, swapped;
-    int cols, split, pairs;
+    int cols, split;
     int stage_chunks, stage_groups;
     int grid_x, grid_y, pipe_depth;
     unsigned smem_bytes;
@@ -35,10 +35,9 @@ constexpr int GROUP_M = 8;
 
 // Tensor map over operand storage as rows of `row_bytes` (a chunk or a group of scales of
 // 128 rows), boxes of `box_bytes` x `box_rows`; 64-bit elements, no swizzle, zero fill.
-// With `blocks` a third dimension of so many blocks of `rows` rows, and boxes of `box_blocks`.
+// With `blocks` a third dimension of so many blocks of `rows` rows, and boxes of two.
 int encode_storage(CUtensorMap* map, const void* base, int64_t row_bytes, int64_t rows,
-                   int box_bytes, int box_rows, const char* what, int64_t blocks = 0,
-                   int box_blocks = 2)
+                   int box_bytes, int box_rows, const char* what, int64_t blocks = 0)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode_fn();
     if (!enc) return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
@@ -47,8 +46,7 @@ int encode_storage(CUtensorMap* map, const void* base, int64_t row_bytes, int64_
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes),
                                    static_cast<cuuint64_t>(row_bytes * rows)};
     const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / 8),
-                               static_cast<cuuint32_t>(box_rows),
-                               static_cast<cuuint32_t>(box_blocks)};
+                               static_cast<cuuint32_t>(box_rows), 2};
     const cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, blocks ? 3 : 2, const_cast<void*>(base), dims,
                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -100,7 +98,7 @@ int check_product(int64_t M, int64_t N, int64_t K, int format, int dtype, int ke
         return fail(GEMM_ERR_INVALID_ARG, "M, N and K must be in [1, 2^31-65536]");
     if (dtype != GEMM_OUT_F32 && dtype != GEMM_OUT_F16)
         return fail(GEMM_ERR_INVALID_ARG, "dtype_out must be GEMM_OUT_F32 (0) or GEMM_OUT_F16 (1)");
-    if (kernel < GEMM_MX_AUTO || kernel > GEMM_MX_QUAD)
+    if (kernel < GEMM_MX_AUTO || kernel > GEMM_MX_SINGLE)
         return fail(GEMM_ERR_INVALID_ARG, "unknown gemm_mx_kernel");
     if (split != 0 && split != 1 && split != 2 && split != 4 && split != 8)
         return fail(GEMM_ERR_INVALID_ARG, "split must be 0, 1, 2, 4 or 8");
@@ -148,7 +146,7 @@ gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K, int format
         p.steps = p.chunks / mx_step_chunks(format);
         p.group_m = GROUP_M;
         const int64_t pair_tiles = ceil_div(M, 256) * ceil_div(N, 256);
-        q.pair = kernel == GEMM_MX_PAIR || kernel == GEMM_MX_QUAD || (kernel == GEMM_MX_AUTO && 2 * pair_tiles >= sms);
+        q.pair = kernel == GEMM_MX_PAIR || (kernel == GEMM_MX_AUTO && 2 * pair_tiles >= sms);
         q.stage_chunks = q.pair ? mx_pair_chunks(format) : mx_stage_chunks(format);
         q.stage_groups = q.pair ? mx_pair_groups(format) : mx_stage_groups(format);
         p.stages = static_cast<int>(ceil_div(p.chunks, q.stage_chunks));
@@ -157,27 +155,15 @@ gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K, int format
         if (q.pair) {
             if (pair_tiles > MAX_COORDINATE)
                 return fail(GEMM_ERR_UNSUPPORTED, "too many output tiles");
+            p.tiles_m = static_cast<int>(ceil_div(M, 256));
+            p.tiles_n = static_cast<int>(ceil_div(N, 256));
+            q.grid_x = static_cast<int>(2 * std::min<int64_t>(std::max(1, sms / 2), pair_tiles));
+            q.grid_y = 1;
             q.split = 1;
             q.cols = 256;
             for (q.pipe_depth = MAX_STAGES; q.pipe_depth > 1; --q.pipe_depth)
                 if (mx_pair_layout(format, q.pipe_depth).total <= static_cast<uint32_t>(smem_optin))
                     break;
-            const unsigned bytes = mx_pair_layout(format, q.pipe_depth).total;
-            q.pairs = kernel == GEMM_MX_QUAD || (kernel == GEMM_MX_AUTO && pair_tiles >= 4 * sms / 2)
-                          ? 2 : 1;
-            int clusters = 0;
-            cudaError_t e = mx_pair_clusters(format, q.pairs, bytes, &clusters);
-            if (e == cudaSuccess && clusters < 1 && q.pairs == 2) {
-                q.pairs = 1;
-                e = mx_pair_clusters(format, q.pairs, bytes, &clusters);
-            }
-            if (e != cudaSuccess) return cuda_fail("cudaOccupancyMaxActiveClusters", e);
-            if (clusters < 1) return fail(GEMM_ERR_UNSUPPORTED, "no pair of CTAs fits the device");
-            p.tiles_m = static_cast<int>(ceil_div(M, 256 * q.pairs));
-            p.tiles_n = static_cast<int>(ceil_div(N, 256));
-            const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-            q.grid_x = static_cast<int>(2 * q.pairs * std::min<int64_t>(clusters, tiles));
-            q.grid_y = 1;
             q.smem_bytes = mx_pair_layout(format, q.pipe_depth).total;
         } else {
             q.swapped = M <= 64;
@@ -213,7 +199,7 @@ gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K, int format
                       "pipe_depth=%d smem=%u grid=%dx%d out=%s",
                       format_name(format), static_cast<long long>(M), static_cast<long long>(N),
                       static_cast<long long>(K),
-                      q.pair ? (q.pairs == 2 ? "quad" : "pair") : q.swapped ? "rows" : "single", q.pair ? 256 * q.pairs : 128, q.cols,
+                      q.pair ? "pair" : q.swapped ? "rows" : "single", q.pair ? 256 : 128, q.cols,
                       q.split, q.pipe_depth, q.smem_bytes, q.grid_x, q.grid_y,
                       dtype_out == GEMM_OUT_F16 ? "f16" : "f32");
         cudaError_t e = cudaMalloc(&q.d_status, sizeof(DevStatus));
@@ -265,15 +251,13 @@ int gemm_mx_run(gemm_mx_plan* plan, const void* codes_a, const void* scales_a, c
             r = encode_storage(&tmUs, swapped ? scales_b : scales_a, MX_GROUP_BYTES,
                                (swapped ? b_blocks : a_blocks) * q.groups, MX_GROUP_BYTES,
                                plan->stage_groups, "scales");
-        const bool quad = plan->pair && plan->pairs == 2;  // each pair copies half of B's box
         if (r == GEMM_OK)
             r = encode_storage(&tmVc, swapped ? codes_a : codes_b, MX_CHUNK_BYTES,
                                (swapped ? a_blocks : b_blocks) * q.chunks, v_bytes,
-                               quad ? plan->stage_chunks / 2 : plan->stage_chunks, "codes");
+                               plan->stage_chunks, "codes");
         if (r == GEMM_OK)
             r = plan->pair ? encode_storage(&tmVs, scales_b, MX_GROUP_BYTES, q.groups,
-                                            MX_GROUP_BYTES, plan->stage_groups, "scales", b_blocks,
-                                            quad ? 1 : 2)
+                                            MX_GROUP_BYTES, plan->stage_groups, "scales", b_blocks)
                            : encode_storage(&tmVs, swapped ? scales_a : scales_b, MX_GROUP_BYTES,
                                             (swapped ? a_blocks : b_blocks) * q.groups,
                                             MX_GROUP_BYTES, plan->stage_groups, "scales");
@@ -284,7 +268,6 @@ int gemm_mx_run(gemm_mx_plan* plan, const void* codes_a, const void* scales_a, c
         s.format = f;
         s.f16out = plan->dtype == GEMM_OUT_F16;
         s.pair = plan->pair;
-        s.pairs = plan->pairs;
         s.cols = plan->cols;
         s.swapped = swapped;
         s.grid_x = plan->grid_x;

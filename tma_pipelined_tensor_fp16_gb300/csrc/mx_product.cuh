@@ -161,4 +161,17 @@ __device__ __forceinline__ void mx_commit(uint32_t elected, uint32_t bar)
         : "memory");
 }
 
+__device__ __forceinline__ void mx_commit_pair(uint32_t elected, uint32_t bar)
+{
+    asm volatile(
+        "{\n\t"
+        ".reg .pred p;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "@p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+        ".b64 [%0], %2;\n\t"
+        "}\n" ::"r"(bar),
+        "r"(elected), "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
 }  // namespace tg

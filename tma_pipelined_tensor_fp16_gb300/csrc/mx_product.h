@@ -44,7 +44,6 @@ struct MxSpec {
     int format;
     bool f16out;
     bool pair;
-    int pairs;     // pairs of a cluster: 1, or 2 that share their columns of the output
     int cols;      // single CTAs: rows of the second operand in a tile, 16 .. 128
     bool swapped;  // single CTAs: B is the operand with 128 rows a tile
     int grid_x, grid_y;
@@ -111,7 +110,5 @@ TG_HD MxPairLayout mx_pair_layout(int format, int depth)
 
 cudaError_t launch_mx_single(const MxSpec& s, cudaStream_t stream);
 cudaError_t launch_mx_pair(const MxSpec& s, cudaStream_t stream);
-// How many clusters of the pair kernel fit on the device at a time.
-cudaError_t mx_pair_clusters(int format, int pairs, unsigned smem_bytes, int* clusters);
 
 }  // namespace tg

@@ -19,7 +19,7 @@ from .experts import (_call, _empty, _Handle, _out_dtype, _output, _ptr, _tensor
                       _used_on)
 
 MX_FORMATS = {"mxfp8": 0, "mxfp4": 1, "nvfp4": 2}
-MX_KERNELS = {"auto": 0, "pair": 1, "single": 2, "quad": 3}
+MX_KERNELS = {"auto": 0, "pair": 1, "single": 2}
 _BLOCK = {"mxfp8": 32, "mxfp4": 32, "nvfp4": 16}
 _CHUNK = {"mxfp8": 16, "mxfp4": 32, "nvfp4": 32}
 _STEP = {"mxfp8": 2, "mxfp4": 3, "nvfp4": 2}    # chunks that rows are filled up to
@@ -177,7 +177,7 @@ def mx_quantize(X, format="mxfp8", transpose=False, tensor_scale=None, out=None,
 class MXPlan(_Handle):
     """C = A . B^T (M x N) of two MXTensors of one format, A of M x K and B of N x K.
 
-    `kernel` ("auto", "pair", "quad", "single") and `split` (CTAs that share a tile's length, for
+    `kernel` ("auto", "pair", "single") and `split` (CTAs that share a tile's length, for
     "single") choose the kernel as in include/tmamicro.h.  Runs of a plan may overlap."""
     _destroy, _describe = "gemm_mx_destroy", "gemm_mx_describe"
     _status, _wait = "gemm_mx_get_device_status", "gemm_mx_set_wait"
