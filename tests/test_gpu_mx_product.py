@@ -66,7 +66,7 @@ PAIR = [(1, 8, 8), (128, 128, 64), (256, 256, 256), (257, 264, 520), (100, 1000,
 
 
 @pytest.mark.parametrize("format", FORMATS)
-@pytest.mark.parametrize("M,N,K", PAIR)
+@pytest.mark.parametrize("M,N,K", PAIR + [(600, 1100, 4096), (2000, 2048, 520)])
 def test_pair_exact(M, N, K, format):
     for out in ("f32", "f16"):
         if N % 8 and out == "f16":

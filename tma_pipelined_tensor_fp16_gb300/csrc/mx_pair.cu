@@ -173,18 +173,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
         int stage = 0;
         uint32_t phase = 0;
         int armed = 0;
-        for (int t = first; t < tiles && !wd.aborted; t += clusters) {
+        bool running = true;
+        const uint32_t full0 = map_shared_rank(bar(BAR_FULL), 0);
+        for (int t = first; t < tiles && running; t += clusters) {
             int mt, nt;
             raster_tile(t, p.tiles_m, p.tiles_n, p.group_m, mt, nt);
             const int a_block = mt * 2 + static_cast<int>(rank);
             const int b_block = nt * 2 + static_cast<int>(rank);
             for (int s = 0; s < p.stages; ++s) {
                 const bool ok = wd.wait(bar(BAR_EMPTY + stage), phase ^ 1u, WAIT_EMPTY, t, s);
-                if (!ok) break;
+                running = __all_sync(0xffffffffu, ok);
+                if (!running) break;
                 if (lane == 0) {
                     const uint32_t at = base + static_cast<uint32_t>(stage) * L.stage;
                     if (leader) mbar_arrive_expect_tx(bar(BAR_FULL + stage), 2 * CTA_TX);
-                    const uint32_t full = map_shared_rank(bar(BAR_FULL + stage), 0);
+                    const uint32_t full = full0 + static_cast<uint32_t>(stage) * 8u;
                     const int c = s * CHUNKS, g = s * GROUPS;
                     tma_load_2d_pair(at, &tmAc, full, 0, a_block * p.chunks + c);
                     tma_load_2d_pair(at + L.b_codes, &tmBc, full, 0, b_block * p.chunks + c);
@@ -213,7 +216,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
                     }
                     wd.drain(bar(BAR_FULL + stage), phase);
                 }
-            } else if (wd.aborted) {
+            } else if (!running) {
                 const uint64_t t0 = globaltimer_ns();
                 while (globaltimer_ns() - t0 < 200000ull) {
                 }

@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(MX_THREADS)
         int armed = 0;
         for (int s = s0; s < s1; ++s) {
             const bool ok = wd.wait(bar(BAR_EMPTY + stage), phase ^ 1u, WAIT_EMPTY, u_tile, s);
-            if (!ok) break;
+            if (!__all_sync(0xffffffffu, ok)) break;
             if (lane == 0) {
                 const uint32_t at = base + static_cast<uint32_t>(stage) * L.stage;
                 const uint32_t full = bar(BAR_FULL + stage);
