@@ -146,7 +146,13 @@ gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K, int format
         p.steps = p.chunks / mx_step_chunks(format);
         p.group_m = GROUP_M;
         const int64_t pair_tiles = ceil_div(M, 256) * ceil_div(N, 256);
-        q.pair = kernel == GEMM_MX_PAIR || (kernel == GEMM_MX_AUTO && 2 * pair_tiles >= sms);
+        // Pairs from a quarter of a GPU of their tiles on, single CTAs below and for up to 64
+        // rows.  Measured, pairs and single CTAs: 512 x 8192 x 8192 nvfp4 (64 tiles of pairs)
+        // 14.1, 19.3 us; 2048 x 2048 x 2048 nvfp4 (64) 7.0, 8.6; 1024 x 4096 x 4096 mxfp8 (64)
+        // 14.8, 17.7; 512 x 4096 x 4096 mxfp8 (32) 13.4, 11.1; 256 x 4096 x 4096 nvfp4 (16)
+        // 7.8, 7.6; 64 x 16384 x 16384 mxfp8 46.9, 45.1; 1 x 16384 x 16384 nvfp4 25.9, 25.8.
+        q.pair = kernel == GEMM_MX_PAIR ||
+                 (kernel == GEMM_MX_AUTO && M > 64 && 4 * pair_tiles >= sms);
         q.stage_chunks = q.pair ? mx_pair_chunks(format) : mx_stage_chunks(format);
         q.stage_groups = q.pair ? mx_pair_groups(format) : mx_stage_groups(format);
         p.stages = static_cast<int>(ceil_div(p.chunks, q.stage_chunks));
@@ -171,10 +177,14 @@ gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K, int format
             const int64_t tu = ceil_div(q.swapped ? N : M, MX_ROWS);
             const int64_t tv = q.swapped ? 1 : ceil_div(N, q.cols);
             if (split == 0) {
-                // CTAs for two per SM, each with a few stages at least
+                // CTAs for two per SM with few rows, where the bytes in flight count, else for
+                // one; each with a few stages at least.  Measured with split = 1, 2, 4, 8: 64 x
+                // 16384 x 16384 mxfp8 50.0, 45.1, 49.4, 59.5 us; 16 x 8192 x 8192 nvfp4 11.5,
+                // 9.6, 9.8, 14.0; 4 x 4096 x 4096 nvfp4 6.3, 5.2, 4.5, 5.2; 4 x 4096 x 14336
+                // mxfp4 15.5, 10.3, 7.5, 7.3; 256 x 4096 x 4096 nvfp4 7.9, 7.6, 9.6, 17.9.
+                const int64_t room = q.swapped ? 2 * sms : sms;
                 split = 1;
-                while (split < 8 && tu * tv * split * 2 <= 2 * sms && p.stages >= 4 * split)
-                    split *= 2;
+                while (split < 8 && tu * tv * split * 2 <= room && p.stages >= 8 * split) split *= 2;
             }
             while (split > p.stages) split /= 2;
             q.split = split;

@@ -408,9 +408,14 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
             x[2 * i + 1] = f.y * s;
         }
         if constexpr (ODD) {
+            T* to = &rows[lane / 4][j * 32 + part * 8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                rows[lane / 4][j * 32 + part * 8 + i] = static_cast<T>(x[i]);
+            for (int i = 0; i < 8; i += 2) {
+                if constexpr (F16OUT)
+                    *reinterpret_cast<__half2*>(to + i) = __floats2half2_rn(x[i], x[i + 1]);
+                else
+                    *reinterpret_cast<float2*>(to + i) = make_float2(x[i], x[i + 1]);
+            }
         } else if constexpr (F16OUT) {
             uint32_t w[4];
 #pragma unroll
@@ -429,19 +434,26 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
     if constexpr (ODD) {
         __syncwarp();
         const int n = static_cast<int>(min(p.K - k0, static_cast<int64_t>(ROW_K)));
-        for (int r = 0; r < 8 && row0 + r < p.rows; ++r) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            if (row0 + r >= p.rows) break;
             const int64_t at = (row0 + r) * p.K + k0;
             T* to = static_cast<T*>(p.values) + at;
             if constexpr (F16OUT) {
+                // word w holds elements 2 w - shift and the next
                 const int shift = static_cast<int>(at & 1);
-                for (int e = 2 * lane - shift; e < n; e += 64) {
+#pragma unroll
+                for (int w = lane; w < ROW_K / 2; w += 32) {
+                    const int e = 2 * w - shift;
                     if (e >= 0 && e + 1 < n) {
-                        *reinterpret_cast<__half2*>(to + e) = __halves2half2(rows[r][e], rows[r][e + 1]);
-                    } else {
-                        const int one = e < 0 ? 0 : e;  // n > 0
+                        *reinterpret_cast<__half2*>(to + e) =
+                            __halves2half2(rows[r][e], rows[r][e + 1]);
+                    } else if (e < n) {
+                        const int one = max(e, 0);  // n > 0
                         to[one] = rows[r][one];
                     }
                 }
+                if (shift && lane == 0 && n == ROW_K) to[ROW_K - 1] = rows[r][ROW_K - 1];
             } else {
                 for (int e = lane; e < n; e += 32) to[e] = rows[r][e];
             }

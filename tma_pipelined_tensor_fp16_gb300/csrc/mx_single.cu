@@ -54,6 +54,102 @@ __device__ __forceinline__ constexpr uint32_t tmem_columns(int need)
     return need <= 32 ? 32u : need <= 64 ? 64u : need <= 128 ? 128u : need <= 256 ? 256u : 512u;
 }
 
+struct MxTile {
+    const MxParams* p;
+    uint32_t sums;  // shared address of this CTA's sums
+    uint32_t rank;
+    int u_tile, v0, tid, f16out;
+};
+
+// Add up the cluster's sums in rank order, this CTA's share of the tile, and store them.
+// Sixteen (eight wide) loads are on their way at a time: one by one, the latency of
+// distributed shared memory took 10 us of 64 rows with 16384 columns.
+template <int COLS, bool SWAPPED, int SPLIT>
+__device__ __forceinline__ void add_up(const MxTile& t)
+{
+    const MxParams& p = *t.p;
+    const float alpha = mx_alpha(p);
+    const int rank = static_cast<int>(t.rank);
+    uint32_t from[SPLIT];
+#pragma unroll
+    for (int k = 0; k < SPLIT; ++k) from[k] = SPLIT > 1 ? map_shared_rank(t.sums, k) : t.sums;
+    if constexpr (SWAPPED) {
+        // C[v0 + c][u0 + r]; columns c = rank, rank + split, ...
+        constexpr int G = 16 / SPLIT;
+        const int64_t n = static_cast<int64_t>(t.u_tile) * MX_ROWS + t.tid;
+        const int cols = min(COLS, p.M - t.v0);
+        for (int c0 = rank; c0 < cols; c0 += G * SPLIT) {
+            float x[G][SPLIT];
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+#pragma unroll
+                for (int k = 0; k < SPLIT; ++k) {
+                    const int c = c0 + i * SPLIT;
+                    x[i][k] = c < cols ? ld_cluster_f32(from[k] + static_cast<uint32_t>(
+                                                                      c * 128 + t.tid) * 4u)
+                                       : 0.0f;
+                }
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                const int c = c0 + i * SPLIT;
+                if (c >= cols || n >= p.N) continue;
+                float sum = x[i][0];
+#pragma unroll
+                for (int k = 1; k < SPLIT; ++k) sum += x[i][k];
+                const int64_t to = static_cast<int64_t>(t.v0 + c) * p.N + n;
+                if (t.f16out)
+                    static_cast<__half*>(p.C)[to] = __float2half_rn(sum * alpha);
+                else
+                    static_cast<float*>(p.C)[to] = sum * alpha;
+            }
+        }
+    } else {
+        // C[u0 + r][v0 + c], four columns a lane; rows by rank, then by warp
+        constexpr int G = 8 / SPLIT;
+        const int lane = t.tid % 32;
+        const int n = t.v0 + lane * 4;
+        const int64_t u0 = static_cast<int64_t>(t.u_tile) * MX_ROWS;
+        const int rows = static_cast<int>(min(static_cast<int64_t>(MX_ROWS), p.M - u0));
+        constexpr int STEP = 4 * SPLIT;
+        for (int r0 = rank + t.tid / 32 * SPLIT; r0 < rows; r0 += G * STEP) {
+            float4 x[G][SPLIT];
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+#pragma unroll
+                for (int k = 0; k < SPLIT; ++k) {
+                    const int r = r0 + i * STEP;
+                    x[i][k] = r < rows ? ld_cluster_f32x4(from[k] + static_cast<uint32_t>(
+                                             r * (COLS + 4) + lane * 4) * 4u)
+                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                const int r = r0 + i * STEP;
+                if (r >= rows || n >= p.N) continue;
+                float4 sum = x[i][0];
+#pragma unroll
+                for (int k = 1; k < SPLIT; ++k) {
+                    sum.x += x[i][k].x;
+                    sum.y += x[i][k].y;
+                    sum.z += x[i][k].z;
+                    sum.w += x[i][k].w;
+                }
+                const int64_t to = (u0 + r) * p.N + n;
+                if (t.f16out) {
+                    const __half2 a = __floats2half2_rn(sum.x * alpha, sum.y * alpha);
+                    const __half2 b = __floats2half2_rn(sum.z * alpha, sum.w * alpha);
+                    *reinterpret_cast<uint2*>(static_cast<__half*>(p.C) + to) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                   *reinterpret_cast<const uint32_t*>(&b));
+                } else {
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.C) + to) = make_float4(
+                        sum.x * alpha, sum.y * alpha, sum.z * alpha, sum.w * alpha);
+                }
+            }
+        }
+    }
+}
+
 }  // namespace
 
 template <int FORMAT, int COLS, bool SWAPPED>
@@ -241,62 +337,13 @@ __global__ void __launch_bounds__(MX_THREADS)
         __syncthreads();
 
     if (warp >= 2 && !wd.aborted && !wd.peer_aborted()) {
-        const float alpha = mx_alpha(p);
         const int tid = static_cast<int>(threadIdx.x) - 64;
-        if constexpr (SWAPPED) {
-            // C[v0 + c][u0 + r]; this CTA's columns c = rank, rank + split, ...
-            const int64_t n = static_cast<int64_t>(u_tile) * MX_ROWS + tid;
-            for (int c = static_cast<int>(rank); c < COLS && v0 + c < p.M; c += p.split) {
-                const uint32_t at = base + static_cast<uint32_t>(c * 128 + tid) * 4u;
-                float s = 0.0f;
-                if (p.split > 1) {
-                    for (int k = 0; k < p.split; ++k) s += ld_cluster_f32(map_shared_rank(at, k));
-                } else {
-                    s = *reinterpret_cast<const float*>(gen + (at - base));
-                }
-                s *= alpha;
-                if (n < p.N) {
-                    const int64_t to = static_cast<int64_t>(v0 + c) * p.N + n;
-                    if (f16out)
-                        static_cast<__half*>(p.C)[to] = __float2half_rn(s);
-                    else
-                        static_cast<float*>(p.C)[to] = s;
-                }
-            }
-        } else {
-            // C[u0 + r][v0 + c], four columns a lane; this CTA's rows by rank
-            const int n = v0 + static_cast<int>(lane) * 4;
-            for (int r = static_cast<int>(rank) + (warp - 2) * p.split; r < 128; r += 4 * p.split) {
-                const int64_t m = static_cast<int64_t>(u_tile) * MX_ROWS + r;
-                if (m >= p.M) break;
-                const uint32_t at =
-                    base + static_cast<uint32_t>(r * (COLS + 4) + static_cast<int>(lane) * 4) * 4u;
-                float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (p.split > 1) {
-                    for (int k = 0; k < p.split; ++k) {
-                        const float4 x = ld_cluster_f32x4(map_shared_rank(at, k));
-                        s.x += x.x;
-                        s.y += x.y;
-                        s.z += x.z;
-                        s.w += x.w;
-                    }
-                } else {
-                    s = *reinterpret_cast<const float4*>(gen + (at - base));
-                }
-                if (n < p.N) {
-                    const int64_t to = m * p.N + n;
-                    if (f16out) {
-                        const __half2 a = __floats2half2_rn(s.x * alpha, s.y * alpha);
-                        const __half2 b = __floats2half2_rn(s.z * alpha, s.w * alpha);
-                        *reinterpret_cast<uint2*>(static_cast<__half*>(p.C) + to) =
-                            make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                       *reinterpret_cast<const uint32_t*>(&b));
-                    } else {
-                        *reinterpret_cast<float4*>(static_cast<float*>(p.C) + to) =
-                            make_float4(s.x * alpha, s.y * alpha, s.z * alpha, s.w * alpha);
-                    }
-                }
-            }
+        const MxTile tile = {&p, base, rank, u_tile, v0, tid, f16out};
+        switch (p.split) {
+        case 1: add_up<COLS, SWAPPED, 1>(tile); break;
+        case 2: add_up<COLS, SWAPPED, 2>(tile); break;
+        case 4: add_up<COLS, SWAPPED, 4>(tile); break;
+        default: add_up<COLS, SWAPPED, 8>(tile); break;
         }
     }
     __syncwarp();

@@ -53,8 +53,7 @@ def rms_norm(X, weight, residual=None, eps=1e-6, half=True, format=None, out=Non
         else None
     Q = MXTensor._new(tokens, width, format, dev, stream) if format is not None else None
     _call(lib().gemm_rms_norm, dev, stream, tokens, width, _ptr(X), _ptr(residual), _ptr(weight),
-          eps, _ptr(H), _ptr(Z), code, _ptr(Q.codes) if Q is not None else None,
-          _ptr(Q.scales) if Q is not None else None)
+          eps, _ptr(H), _ptr(Z), code, *(Q._addresses() if Q is not None else (None, None)))
     if stream is not None:
         _used_on(stream, X, weight, residual, Z, H, *(Q._parts() if Q is not None else ()))
     return Z, X if residual is None else H, Q

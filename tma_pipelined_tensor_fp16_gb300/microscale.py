@@ -14,7 +14,10 @@ Argument checks and marshalling only, with the conventions of ``experts``: every
 runs in the library's CUDA kernels, asynchronously on the current stream of the tensors'
 device (or on ``stream``).
 """
-from .binding import _check, lib
+import functools
+import math
+
+from .binding import lib
 from .experts import (_call, _empty, _Handle, _out_dtype, _output, _ptr, _tensor, _torch,
                       _used_on)
 
@@ -44,6 +47,12 @@ def _shapes(rows, K, format):
     return (blocks, chunks, 128, 16), (blocks, groups, 32, 4, 4)
 
 
+@functools.lru_cache(maxsize=512)
+def _bytes(rows, K, format):
+    """Bytes of the codes and of the scales."""
+    return tuple(math.prod(shape) for shape in _shapes(rows, K, format))
+
+
 class MXTensor:
     """A quantised matrix of ``rows`` x ``K``: ``codes`` and ``scales`` (uint8, in the
     storage order that include/tmamicro.h describes) and for nvfp4 ``tensor_scale`` (one
@@ -62,26 +71,45 @@ class MXTensor:
                 raise ValueError("only nvfp4 has a tensor_scale")
             _tensor("tensor_scale", tensor_scale, (1,), torch.float32, codes.device)
         self.rows, self.K, self.format = rows, K, format
-        self.codes, self.scales, self.tensor_scale = codes, scales, tensor_scale
+        self.device = codes.device
+        self._memory = codes, scales
+        self.tensor_scale = tensor_scale
 
     @classmethod
     def _new(cls, rows, K, format, device, stream, tensor_scale=None):
-        """Storage to be written by the library (no checks of its own tensors)."""
-        torch = _torch()
-        shape_c, shape_s = _shapes(rows, K, format)
+        """Storage to be written by the library: one allocation, the scales behind the codes
+        (both are whole numbers of 512 bytes)."""
         t = cls.__new__(cls)
-        t.rows, t.K, t.format = rows, K, format
-        t.codes = _empty(shape_c, torch.uint8, device, stream)
-        t.scales = _empty(shape_s, torch.uint8, device, stream)
+        t.rows, t.K, t.format, t.device = rows, K, format, device
+        codes, scales = _bytes(rows, K, format)
+        t._memory = _empty((codes + scales,), _torch().uint8, device, stream),
         t.tensor_scale = tensor_scale
         return t
 
+    def _views(self):
+        if len(self._memory) == 1:
+            codes, scales = _shapes(self.rows, self.K, self.format)
+            n = _bytes(self.rows, self.K, self.format)[0]
+            self._memory = self._memory[0][:n].view(codes), self._memory[0][n:].view(scales)
+        return self._memory
+
     @property
-    def device(self):
-        return self.codes.device
+    def codes(self):
+        return self._views()[0]
+
+    @property
+    def scales(self):
+        return self._views()[1]
+
+    def _addresses(self):
+        """Of the codes and the scales."""
+        at = self._memory[0].data_ptr()
+        if len(self._memory) == 1:
+            return at, at + _bytes(self.rows, self.K, self.format)[0] if at else None
+        return at, self._memory[1].data_ptr()
 
     def _parts(self):
-        return self.codes, self.scales, self.tensor_scale
+        return self._memory + (self.tensor_scale,)
 
     @classmethod
     def from_codes(cls, codes, scales, K, format, tensor_scale=None):
@@ -122,11 +150,11 @@ class MXTensor:
         """The values that the codes stand for (rows x K), rounded once to `out`'s type
         (fp16 when not given; fp32 holds them exactly)."""
         torch = _torch()
-        dev = self.codes.device
+        dev = self.device
         dtype = torch.float32 if out is not None and out.dtype == torch.float32 else torch.float16
         V = _output("out", out, (self.rows, self.K), dtype, dev, stream)
         _call(lib().gemm_mx_values, dev, stream, self.rows, self.K, MX_FORMATS[self.format],
-              _ptr(self.codes), _ptr(self.scales), _ptr(self.tensor_scale),
+              *self._addresses(), _ptr(self.tensor_scale),
               0 if dtype == torch.float32 else 1, _ptr(V))
         if stream is not None:
             _used_on(stream, *self._parts(), V)
@@ -168,7 +196,7 @@ def mx_quantize(X, format="mxfp8", transpose=False, tensor_scale=None, out=None,
         if Q.tensor_scale is None:
             Q.tensor_scale = _empty((1,), torch.float32, dev, stream)
     _call(lib().gemm_mx_quantize, dev, stream, rows, K, code, 1 if transpose else 0, _ptr(X),
-          _ptr(Q.codes), _ptr(Q.scales), _ptr(Q.tensor_scale), _ptr(work))
+          *Q._addresses(), _ptr(Q.tensor_scale), _ptr(work))
     if stream is not None:
         _used_on(stream, X, *Q._parts(), work)
     return Q
@@ -197,12 +225,12 @@ class MXPlan(_Handle):
             if t.rows != rows or t.K != self.K or t.format != self.format:
                 raise ValueError("%s must be a %s MXTensor of %d x %d, not %s of %d x %d"
                                  % (name, self.format, rows, self.K, t.format, t.rows, t.K))
-        dev = A.codes.device
-        if B.codes.device != dev:
-            raise ValueError("B is on %s, the other tensors on %s" % (B.codes.device, dev))
+        dev = A.device
+        if B.device != dev:
+            raise ValueError("B is on %s, the other tensors on %s" % (B.device, dev))
         C = _output("out", out, (self.M, self.N), self.dtype, dev, stream)
-        _call(lib().gemm_mx_run, dev, stream, self._h, _ptr(A.codes), _ptr(A.scales),
-              _ptr(A.tensor_scale), _ptr(B.codes), _ptr(B.scales), _ptr(B.tensor_scale), _ptr(C))
+        _call(lib().gemm_mx_run, dev, stream, self._h, *A._addresses(), _ptr(A.tensor_scale),
+              *B._addresses(), _ptr(B.tensor_scale), _ptr(C))
         if stream is not None:
             _used_on(stream, *A._parts(), *B._parts(), C)
         return C
