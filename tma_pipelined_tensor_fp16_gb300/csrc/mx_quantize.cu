@@ -434,29 +434,47 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
     if constexpr (ODD) {
         __syncwarp();
         const int n = static_cast<int>(min(p.K - k0, static_cast<int64_t>(ROW_K)));
+        const int count = static_cast<int>(min(p.rows - row0, static_cast<int64_t>(8)));
+        T* to = static_cast<T*>(p.values) + row0 * p.K + k0;
+        if constexpr (F16OUT) {
+            if (n == ROW_K) {
+                // Word w of a row that starts on an odd element is the second half of word w -
+                // 1 and the first of word w in shared memory; its ends are single elements.
+                const uint32_t odd_row0 = (reinterpret_cast<uintptr_t>(to) >> 1) & 1u;
+                const uint32_t odd_step = static_cast<uint32_t>(p.K) & 1u;
+                constexpr int WORDS = ROW_K / 2;  // 64, 48 of mxfp4
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            if (row0 + r >= p.rows) break;
-            const int64_t at = (row0 + r) * p.K + k0;
-            T* to = static_cast<T*>(p.values) + at;
-            if constexpr (F16OUT) {
-                // word w holds elements 2 w - shift and the next
-                const int shift = static_cast<int>(at & 1);
-#pragma unroll
-                for (int w = lane; w < ROW_K / 2; w += 32) {
-                    const int e = 2 * w - shift;
-                    if (e >= 0 && e + 1 < n) {
-                        *reinterpret_cast<__half2*>(to + e) =
-                            __halves2half2(rows[r][e], rows[r][e + 1]);
-                    } else if (e < n) {
-                        const int one = max(e, 0);  // n > 0
-                        to[one] = rows[r][one];
+                for (int r = 0; r < 8; ++r) {
+                    if (r >= count) break;  // uniform
+                    const uint32_t* from = reinterpret_cast<const uint32_t*>(rows[r]);
+                    const bool second = lane + 32 < WORDS;
+                    const uint32_t v0 = from[lane];
+                    const uint32_t v1 = second ? from[lane + 32] : 0u;
+                    if (((odd_row0 + static_cast<uint32_t>(r) * odd_step) & 1u) == 0) {
+                        uint32_t* words = reinterpret_cast<uint32_t*>(to);
+                        words[lane] = v0;
+                        if (second) words[lane + 32] = v1;
+                    } else {
+                        uint32_t* words = reinterpret_cast<uint32_t*>(to - 1);
+                        const uint32_t p0 = __shfl_up_sync(0xffffffffu, v0, 1);
+                        uint32_t p1 = __shfl_up_sync(0xffffffffu, v1, 1);
+                        const uint32_t last = __shfl_sync(0xffffffffu, v0, 31);
+                        if (lane == 0) p1 = last;
+                        if (lane > 0)
+                            words[lane] = __byte_perm(p0, v0, 0x5432);
+                        else
+                            to[0] = rows[r][0];
+                        if (second) words[lane + 32] = __byte_perm(p1, v1, 0x5432);
+                        if (lane == 31) to[ROW_K - 1] = rows[r][ROW_K - 1];
                     }
+                    to += p.K;
                 }
-                if (shift && lane == 0 && n == ROW_K) to[ROW_K - 1] = rows[r][ROW_K - 1];
-            } else {
-                for (int e = lane; e < n; e += 32) to[e] = rows[r][e];
+                return;
             }
+        }
+        for (int r = 0; r < count; ++r) {
+            for (int e = lane; e < n; e += 32) to[e] = rows[r][e];
+            to += p.K;
         }
     }
 }
