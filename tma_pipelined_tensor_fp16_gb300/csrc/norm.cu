@@ -181,11 +181,19 @@ __device__ __forceinline__ float2 warp_sum2(float2 s)
     return s;
 }
 
+// CTAs on an SM, which the registers are held to.  Several of them cover each other's
+// reductions better than one that reads a row ahead (16384 x 4096 with dH: four CTAs 87 us,
+// three with a row ahead 96; 8192 x 8192: two 92, one 125).
+constexpr int grad_resident(int warps, int vec)
+{
+    return warps == 1 ? (vec == 1 ? 5 : 4) : warps == 4 ? 10 : warps == 8 ? 6 - vec : warps == 16 ? 2 : 1;
+}
+
 // Rows as in k_rms_norm, each group of WARPS warps taking every stride-th row; a lane's
 // columns stay the same, so their sums over its rows stay in registers and are written
 // once as the group's part of dweight.
 template <int WARPS, int VEC, int THREADS>
-__global__ void __launch_bounds__(THREADS) k_rms_norm_grad(const __grid_constant__ NormGradParams p)
+__global__ void __launch_bounds__(THREADS, grad_resident(WARPS, VEC)) k_rms_norm_grad(const __grid_constant__ NormGradParams p)
 {
     constexpr int ROWS = THREADS / 32 / WARPS;
     constexpr int LANES = WARPS * 32;
@@ -201,24 +209,18 @@ __global__ void __launch_bounds__(THREADS) k_rms_norm_grad(const __grid_constant
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
     int turn = 0;
-    uint4 hv[VEC], dv[VEC], rv[VEC];
-    auto load = [&](int64_t row) {
+    for (int64_t row = group; row < p.tokens; row += groups) {
+        uint4 hv[VEC], dv[VEC], rv[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
             const int k = (i * LANES + lane) * 8;
             hv[i] = dv[i] = rv[i] = make_uint4(0, 0, 0, 0);
-            if (k < p.width && row < p.tokens) {
+            if (k < p.width) {
                 hv[i] = *reinterpret_cast<const uint4*>(p.H + row * p.width + k);
                 dv[i] = *reinterpret_cast<const uint4*>(p.dZ + row * p.width + k);
                 if (p.dH) rv[i] = *reinterpret_cast<const uint4*>(p.dH + row * p.width + k);
             }
         }
-    };
-    // a row ahead, where the registers allow it
-    constexpr bool AHEAD = THREADS < 1024;
-    if (AHEAD) load(group);
-    for (int64_t row = group; row < p.tokens; row += groups) {
-        if (!AHEAD) load(row);
         float2 s = make_float2(0.0f, 0.0f);  // sum of h^2, of u h
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
@@ -247,14 +249,6 @@ __global__ void __launch_bounds__(THREADS) k_rms_norm_grad(const __grid_constant
                 s.y += slots[i].y;
             }
         }
-        uint4 h0[VEC], d0[VEC], r0[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            h0[i] = hv[i];
-            d0[i] = dv[i];
-            r0[i] = rv[i];
-        }
-        if (AHEAD) load(row + groups);  // on their way while this row is written
         const float rstd = 1.0f / sqrtf(fmaf(s.x, p.inv_width, p.eps));
         const float along = s.y * p.inv_width * rstd * rstd;  // mean(u n) * rstd
 #pragma unroll
@@ -262,8 +256,8 @@ __global__ void __launch_bounds__(THREADS) k_rms_norm_grad(const __grid_constant
             const int k = (i * LANES + lane) * 8;
             if (k >= p.width) continue;
             float h[8], d[8], w[8], x[8];
-            widen8(h0[i], h);
-            widen8(d0[i], d);
+            widen8(hv[i], h);
+            widen8(dv[i], d);
             widen8(__ldg(reinterpret_cast<const uint4*>(p.weight + k)), w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -272,7 +266,7 @@ __global__ void __launch_bounds__(THREADS) k_rms_norm_grad(const __grid_constant
             }
             if (p.dH) {
                 float r[8];
-                widen8(r0[i], r);
+                widen8(rv[i], r);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] += r[j];
             }
@@ -327,13 +321,15 @@ GradShape grad_shape(int64_t tokens, int64_t width)
     const int64_t vecs = (width + 7) / 8;
     GradShape s;
     int resident;
-    if (vecs <= 32) s = {0, 8, 0}, resident = 4;  // by registers
-    else if (vecs <= 64) s = {1, 8, 0}, resident = 2;
-    else if (vecs <= 256) s = {2, 1, 0}, resident = 4;
-    else if (vecs <= 512) s = {3, 1, 0}, resident = 3;
-    else if (vecs <= 1024) s = {4, 1, 0}, resident = 1;
-    else if (vecs <= 2048) s = {5, 1, 0}, resident = 1;
-    else s = {6, 1, 0}, resident = 1;
+    if (vecs <= 32) s = {0, 8, 0}, resident = grad_resident(1, 1);
+    else if (vecs <= 64) s = {1, 8, 0}, resident = grad_resident(1, 2);
+    else if (vecs <= 128) s = {2, 1, 0}, resident = grad_resident(4, 1);
+    else if (vecs <= 256) s = {3, 1, 0}, resident = grad_resident(8, 1);
+    else if (vecs <= 512) s = {4, 1, 0}, resident = grad_resident(8, 2);
+    else if (vecs <= 768) s = {5, 1, 0}, resident = grad_resident(8, 3);
+    else if (vecs <= 1024) s = {6, 1, 0}, resident = grad_resident(16, 2);
+    else if (vecs <= 2048) s = {7, 1, 0}, resident = grad_resident(32, 2);
+    else s = {8, 1, 0}, resident = grad_resident(32, 4);
     const int64_t want = (tokens + s.rows - 1) / s.rows;
     s.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, resident * GRAD_SMS)));
     return s;
@@ -348,10 +344,12 @@ cudaError_t launch_norm_grad(const NormGradParams& p, const GradShape& s, cudaSt
     switch (s.config) {
     case 0: return go(k_rms_norm_grad<1, 1, 256>, 256);
     case 1: return go(k_rms_norm_grad<1, 2, 256>, 256);
-    case 2: return go(k_rms_norm_grad<8, 1, 256>, 256);
-    case 3: return go(k_rms_norm_grad<8, 2, 256>, 256);
-    case 4: return go(k_rms_norm_grad<16, 2, 512>, 512);
-    case 5: return go(k_rms_norm_grad<32, 2, 1024>, 1024);
+    case 2: return go(k_rms_norm_grad<4, 1, 128>, 128);
+    case 3: return go(k_rms_norm_grad<8, 1, 256>, 256);
+    case 4: return go(k_rms_norm_grad<8, 2, 256>, 256);
+    case 5: return go(k_rms_norm_grad<8, 3, 256>, 256);
+    case 6: return go(k_rms_norm_grad<16, 2, 512>, 512);
+    case 7: return go(k_rms_norm_grad<32, 2, 1024>, 1024);
     default: return go(k_rms_norm_grad<32, 4, 1024>, 1024);
     }
 }
