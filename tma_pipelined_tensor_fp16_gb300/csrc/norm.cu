@@ -49,50 +49,52 @@ __device__ __forceinline__ uint4 narrow8(const float (&x)[8])
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Sum over the LANES (16 or 32) lanes of a warp that share a row; rows of one warp may have
+// left the loop they are in.
+template <int LANES = 32>
 __device__ __forceinline__ float warp_sum(float s)
 {
+    const uint32_t mask = LANES == 32 ? 0xffffffffu : 0xffffu << (lane_id() & 16u);
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int o = LANES / 2; o > 0; o /= 2) s += __shfl_xor_sync(mask, s, o);
     return s;
 }
 
-// Sum over the `WARPS` warps of a row; `shared` holds one slot per warp and is free again
-// after the next call's barrier (two alternate).
-template <int WARPS>
+// Sum over the LANES lanes of a row: part of a warp, a warp, or the whole CTA.
+template <int LANES>
 __device__ __forceinline__ float row_sum(float s, float* shared)
 {
+    if constexpr (LANES <= 32) return warp_sum<LANES>(s);
     s = warp_sum(s);
-    if constexpr (WARPS > 1) {
-        if (lane_id() == 0) shared[threadIdx.x / 32] = s;
-        __syncthreads();
-        s = 0.0f;
+    if (lane_id() == 0) shared[threadIdx.x / 32] = s;
+    __syncthreads();
+    s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < WARPS; ++i) s += shared[i];
-    }
+    for (int i = 0; i < LANES / 32; ++i) s += shared[i];
     return s;
 }
 
-// A row by WARPS warps (1, or all of the CTA), VEC vectors of eight values per lane,
+// A row by LANES lanes (half a warp, a warp, or all of the CTA), VEC vectors of eight values
+// per lane,
 // held in registers between the sum of squares and the outputs.
-template <int FORMAT, int WARPS, int VEC, int THREADS>
+template <int FORMAT, int LANES, int VEC, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_rms_norm(const __grid_constant__ NormParams p)
 {
-    constexpr int ROWS = THREADS / 32 / WARPS;  // per CTA
-    constexpr int LANES = WARPS * 32;
+    constexpr int ROWS = THREADS / LANES;  // per CTA
     __shared__ float shared[THREADS / 32];
     const int lane = static_cast<int>(threadIdx.x) % LANES;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / LANES;
     const bool valid = row < p.tokens;
     griddep_wait();
     griddep_launch_dependents();
-    if (WARPS == 1 && !valid) return;
+    if (!__any_sync(0xffffffffu, valid)) return;  // a warp stays together for its shuffles
     float h[VEC][8];
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
         const int k = (i * LANES + lane) * 8;
         uint4 x = make_uint4(0, 0, 0, 0), r = make_uint4(0, 0, 0, 0);
-        if (k < p.width) {
+        if (valid && k < p.width) {
             x = *reinterpret_cast<const uint4*>(p.X + row * p.width + k);
             if (p.residual) r = *reinterpret_cast<const uint4*>(p.residual + row * p.width + k);
         }
@@ -108,7 +110,7 @@ __global__ void __launch_bounds__(THREADS) k_rms_norm(const __grid_constant__ No
     for (int i = 0; i < VEC; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum = fmaf(h[i][j], h[i][j], sum);
-    sum = row_sum<WARPS>(sum, shared);
+    sum = row_sum<LANES>(sum, shared);
     const float rstd = 1.0f / sqrtf(fmaf(sum, p.inv_width, p.eps));
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(THREADS) k_rms_norm(const __grid_constant__ No
         float z[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[j] = 0.0f;
-        if (k < p.width) {
+        if (valid && k < p.width) {
             if (p.total) *reinterpret_cast<uint4*>(p.total + row * p.width + k) = narrow8(h[i]);
             float w[8];
             widen8(__ldg(reinterpret_cast<const uint4*>(p.weight + k)), w);
@@ -146,15 +148,16 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t stream)
         return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)),
                                 dim3(static_cast<unsigned>(threads)), 0, 1, stream, p);
     };
-    // up to 1024 values a warp holds a row
-    if (vecs <= 32) return go(k_rms_norm<FORMAT, 1, 1, 256>, 8, 256);
-    if (vecs <= 64) return go(k_rms_norm<FORMAT, 1, 2, 256>, 8, 256);
-    if (vecs <= 128) return go(k_rms_norm<FORMAT, 1, 4, 256>, 8, 256);
-    if (vecs <= 256) return go(k_rms_norm<FORMAT, 8, 1, 256>, 1, 256);
-    if (vecs <= 512) return go(k_rms_norm<FORMAT, 8, 2, 256>, 1, 256);
-    if (vecs <= 1024) return go(k_rms_norm<FORMAT, 8, 4, 256>, 1, 256);
-    if (vecs <= 2048) return go(k_rms_norm<FORMAT, 16, 4, 512>, 1, 512);
-    return go(k_rms_norm<FORMAT, 32, 4, 1024>, 1, 1024);
+    // up to 128 values half a warp holds a row, up to 1024 a warp
+    if (vecs <= 16) return go(k_rms_norm<FORMAT, 16, 1, 256>, 16, 256);
+    if (vecs <= 32) return go(k_rms_norm<FORMAT, 32, 1, 256>, 8, 256);
+    if (vecs <= 64) return go(k_rms_norm<FORMAT, 32, 2, 256>, 8, 256);
+    if (vecs <= 128) return go(k_rms_norm<FORMAT, 32, 4, 256>, 8, 256);
+    if (vecs <= 256) return go(k_rms_norm<FORMAT, 256, 1, 256>, 1, 256);
+    if (vecs <= 512) return go(k_rms_norm<FORMAT, 256, 2, 256>, 1, 256);
+    if (vecs <= 1024) return go(k_rms_norm<FORMAT, 256, 4, 256>, 1, 256);
+    if (vecs <= 2048) return go(k_rms_norm<FORMAT, 512, 4, 512>, 1, 512);
+    return go(k_rms_norm<FORMAT, 1024, 4, 1024>, 1, 1024);
 }
 
 // ------------------------------------------------------------------ gradient
@@ -171,32 +174,26 @@ struct NormGradParams {
     float* parts;  // [part][width]
 };
 
-__device__ __forceinline__ float2 warp_sum2(float2 s)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) {
-        s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
-        s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
-    }
-    return s;
-}
 
 // CTAs on an SM, which the registers are held to.  Several of them cover each other's
 // reductions better than one that reads a row ahead (16384 x 4096 with dH: four CTAs 87 us,
 // three with a row ahead 96; 8192 x 8192: two 92, one 125).
-constexpr int grad_resident(int warps, int vec)
+constexpr int grad_resident(int lanes, int vec)
 {
-    return warps == 1 ? (vec == 1 ? 5 : 4) : warps == 4 ? 10 : warps == 8 ? 6 - vec : warps == 16 ? 2 : 1;
+    return lanes <= 32   ? (vec == 1 ? 5 : 4)
+           : lanes == 128 ? 10
+           : lanes == 256 ? 6 - vec
+           : lanes == 512 ? 2
+                          : 1;
 }
 
-// Rows as in k_rms_norm, each group of WARPS warps taking every stride-th row; a lane's
+// Rows as in k_rms_norm, each group of LANES lanes taking every stride-th row; a lane's
 // columns stay the same, so their sums over its rows stay in registers and are written
 // once as the group's part of dweight.
-template <int WARPS, int VEC, int THREADS>
-__global__ void __launch_bounds__(THREADS, grad_resident(WARPS, VEC)) k_rms_norm_grad(const __grid_constant__ NormGradParams p)
+template <int LANES, int VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS, grad_resident(LANES, VEC)) k_rms_norm_grad(const __grid_constant__ NormGradParams p)
 {
-    constexpr int ROWS = THREADS / 32 / WARPS;
-    constexpr int LANES = WARPS * 32;
+    constexpr int ROWS = THREADS / LANES;
     __shared__ float2 shared[2][THREADS / 32];
     const int lane = static_cast<int>(threadIdx.x) % LANES;
     const int64_t group = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / LANES;
@@ -236,15 +233,16 @@ __global__ void __launch_bounds__(THREADS, grad_resident(WARPS, VEC)) k_rms_norm
                 s.y = fmaf(d[j] * w[j], h[j], s.y);
             }
         }
-        s = warp_sum2(s);
-        if constexpr (WARPS > 1) {
+        s.x = warp_sum<LANES < 32 ? LANES : 32>(s.x);
+        s.y = warp_sum<LANES < 32 ? LANES : 32>(s.y);
+        if constexpr (LANES > 32) {
             float2* slots = shared[turn & 1];
             ++turn;
             if (lane_id() == 0) slots[threadIdx.x / 32] = s;
             __syncthreads();
             s = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < WARPS; ++i) {
+            for (int i = 0; i < LANES / 32; ++i) {
                 s.x += slots[i].x;
                 s.y += slots[i].y;
             }
@@ -321,15 +319,16 @@ GradShape grad_shape(int64_t tokens, int64_t width)
     const int64_t vecs = (width + 7) / 8;
     GradShape s;
     int resident;
-    if (vecs <= 32) s = {0, 8, 0}, resident = grad_resident(1, 1);
-    else if (vecs <= 64) s = {1, 8, 0}, resident = grad_resident(1, 2);
-    else if (vecs <= 128) s = {2, 1, 0}, resident = grad_resident(4, 1);
-    else if (vecs <= 256) s = {3, 1, 0}, resident = grad_resident(8, 1);
-    else if (vecs <= 512) s = {4, 1, 0}, resident = grad_resident(8, 2);
-    else if (vecs <= 768) s = {5, 1, 0}, resident = grad_resident(8, 3);
-    else if (vecs <= 1024) s = {6, 1, 0}, resident = grad_resident(16, 2);
-    else if (vecs <= 2048) s = {7, 1, 0}, resident = grad_resident(32, 2);
-    else s = {8, 1, 0}, resident = grad_resident(32, 4);
+    if (vecs <= 16) s = {0, 16, 0}, resident = grad_resident(16, 1);
+    else if (vecs <= 32) s = {1, 8, 0}, resident = grad_resident(32, 1);
+    else if (vecs <= 64) s = {2, 8, 0}, resident = grad_resident(32, 2);
+    else if (vecs <= 128) s = {3, 1, 0}, resident = grad_resident(128, 1);
+    else if (vecs <= 256) s = {4, 1, 0}, resident = grad_resident(256, 1);
+    else if (vecs <= 512) s = {5, 1, 0}, resident = grad_resident(256, 2);
+    else if (vecs <= 768) s = {6, 1, 0}, resident = grad_resident(256, 3);
+    else if (vecs <= 1024) s = {7, 1, 0}, resident = grad_resident(512, 2);
+    else if (vecs <= 2048) s = {8, 1, 0}, resident = grad_resident(1024, 2);
+    else s = {9, 1, 0}, resident = grad_resident(1024, 4);
     const int64_t want = (tokens + s.rows - 1) / s.rows;
     s.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, resident * GRAD_SMS)));
     return s;
@@ -342,15 +341,16 @@ cudaError_t launch_norm_grad(const NormGradParams& p, const GradShape& s, cudaSt
                                 dim3(static_cast<unsigned>(threads)), 0, 1, stream, p);
     };
     switch (s.config) {
-    case 0: return go(k_rms_norm_grad<1, 1, 256>, 256);
-    case 1: return go(k_rms_norm_grad<1, 2, 256>, 256);
-    case 2: return go(k_rms_norm_grad<4, 1, 128>, 128);
-    case 3: return go(k_rms_norm_grad<8, 1, 256>, 256);
-    case 4: return go(k_rms_norm_grad<8, 2, 256>, 256);
-    case 5: return go(k_rms_norm_grad<8, 3, 256>, 256);
-    case 6: return go(k_rms_norm_grad<16, 2, 512>, 512);
-    case 7: return go(k_rms_norm_grad<32, 2, 1024>, 1024);
-    default: return go(k_rms_norm_grad<32, 4, 1024>, 1024);
+    case 0: return go(k_rms_norm_grad<16, 1, 256>, 256);
+    case 1: return go(k_rms_norm_grad<32, 1, 256>, 256);
+    case 2: return go(k_rms_norm_grad<32, 2, 256>, 256);
+    case 3: return go(k_rms_norm_grad<128, 1, 128>, 128);
+    case 4: return go(k_rms_norm_grad<256, 1, 256>, 256);
+    case 5: return go(k_rms_norm_grad<256, 2, 256>, 256);
+    case 6: return go(k_rms_norm_grad<256, 3, 256>, 256);
+    case 7: return go(k_rms_norm_grad<512, 2, 512>, 512);
+    case 8: return go(k_rms_norm_grad<1024, 2, 1024>, 1024);
+    default: return go(k_rms_norm_grad<1024, 4, 1024>, 1024);
     }
 }
 
