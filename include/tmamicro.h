@@ -93,7 +93,8 @@ typedef enum { GEMM_MX_AUTO = 0, GEMM_MX_PAIR = 1, GEMM_MX_SINGLE = 2 } gemm_mx_
 TMAGEMM_API gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K, int format,
                                                  int dtype_out, int kernel, int split);
 
-/* Enqueue the product.  scale_a, scale_b: the tensor scales of GEMM_NVFP4 (one fp32 each,
+/* Enqueue the product.  No scale may have its sign bit set (gemm_mx_quantize sets none).
+ * scale_a, scale_b: the tensor scales of GEMM_NVFP4 (one fp32 each,
  * any value), or NULL for 1. */
 TMAGEMM_API int gemm_mx_run(gemm_mx_plan* plan, const void* codes_a, const void* scales_a,
                             const float* scale_a, const void* codes_b, const void* scales_b,

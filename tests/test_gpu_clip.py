@@ -59,7 +59,7 @@ def _check(grads, max_norm, out=None):
 
 
 @pytest.mark.parametrize("place", ["out", "in place"])
-@pytest.mark.parametrize("sizes", [[1], [7], [16384], [16385], [0, 5, 0], [3, 1, 100, 20000, 4096],
+@pytest.mark.parametrize("sizes", [[1], [7], [16384], [16385], [0, 5, 0], [0, 0], [3, 1, 100, 20000, 4096],
                                    list(range(1, 400)), [3000001], [1 << 20] * 5])
 def test_sizes_and_types(sizes, place):
     import torch
@@ -161,3 +161,17 @@ def test_refusals():
     b.data = torch.ones(100, device="cuda")
     with pytest.raises(ValueError, match="moved"):
         clip(1.0)
+
+
+def test_offsets_past_32_bits():
+    """A tensor of 2^32 + 5 fp16 values, 8.6 GB: only its ends are not zero."""
+    import torch
+
+    import tma_pipelined_tensor_fp16_gb300 as tg
+    x = torch.zeros(2 ** 32 + 5, dtype=torch.float16, device="cuda")
+    x[0], x[-1], x[2 ** 31] = 3.0, 4.0, 12.0
+    assert float(tg.clip_grad_norm([x], 1.3)) == 13.0
+    for i, v in ((0, 0.3), (-1, 0.4), (2 ** 31, 1.2)):
+        assert abs(float(x[i]) - v) < 1e-3
+    x[0] = x[-1] = x[2 ** 31] = 0.0
+    assert int(torch.count_nonzero(x)) == 0

@@ -108,6 +108,17 @@ def test_decode():
     assert none[0].shape == none[1].shape == (0, 256)
 
 
+def test_no_tokens():
+    import torch
+    block, X, R, ids, w = _block("nvfp4")
+    Y, H, saved = block.forward(X[:0], R[:0], ids[:0], w[:0])
+    for g in block.grads:
+        g.fill_(7.0)
+    dX, dw = block.backward(Y, None, saved)
+    assert Y.shape == H.shape == dX.shape == (0, 136) and dw.shape == (0, 2)
+    assert all((g == 0).all() for g in block.grads) and float(block.clip(1.0)) == 0.0
+
+
 def test_a_step_in_a_graph():
     """Forward, backward and clipping captured and replayed, against the calls."""
     import torch

@@ -183,3 +183,27 @@ def test_storage_order_and_row_major_codes():
         assert (Q.codes.cpu().numpy() == c).all() and (Q.scales.cpu().numpy() == s).all()
         back = Q.to_codes()
         assert (back[0].cpu().numpy() == packed).all() and (back[1].cpu().numpy() == scales).all()
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_offsets_past_32_bits(transpose):
+    """2.2e9 values: the last rows and columns are those of the small matrix that they hold."""
+    import torch
+
+    import tma_pipelined_tensor_fp16_gb300 as tg
+    rows, K = (65600, 33536)
+    assert rows * K > 2 ** 31
+    X = torch.zeros((rows, K), dtype=torch.float16, device="cuda")
+    x = _inputs(np.random.default_rng(1), 64, 128)
+    X[-64:, -128:] = device(x)
+    want = x.T.copy() if transpose else x
+    for format in ("mxfp8", "nvfp4"):
+        Q = tg.mx_quantize(X, format, transpose=transpose)
+        codes, scales, t = mx_util.quantize(want.astype(np.float64), format)
+        ref = mx_util.values(codes, scales, format, t)
+        V = Q.values(torch.empty((Q.rows, Q.K), dtype=torch.float32, device="cuda"))
+        end = V[-want.shape[0]:, -want.shape[1]:]
+        assert np.array_equal(end.double().cpu().numpy(), ref)
+        assert int((V[:-want.shape[0]] != 0).sum()) == 0
+        assert int((V[:, :-want.shape[1]] != 0).sum()) == 0
+        del V, Q

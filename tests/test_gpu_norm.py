@@ -214,3 +214,24 @@ def test_gradient_of_no_tokens():
     assert dX.shape == (0, 64) and (dw == 0).all()
     Z, H, Q = tg.rms_norm(e, w, residual=e, format="mxfp4")
     assert Z.shape == H.shape == (0, 64) and Q.rows == 0
+
+
+def test_offsets_past_32_bits():
+    import torch
+
+    import tma_pipelined_tensor_fp16_gb300 as tg
+    tokens, width = 540000, 4096
+    assert tokens * width > 2 ** 31
+    x, r, w = _inputs(np.random.default_rng(11), 3, width)
+    X = torch.zeros((tokens, width), dtype=torch.float16, device="cuda")
+    X[-3:] = device(x)
+    W = device(w)
+    Z, _, Q = tg.rms_norm(X, W, eps=1.0, format="mxfp4")
+    small = tg.rms_norm(device(x), W, eps=1.0, format="mxfp4")
+    assert torch.equal(Z[-3:], small[0]) and int(torch.count_nonzero(Z[:-3])) == 0
+    V = Q.values(Z)
+    assert torch.equal(V[-3:], small[2].values()) and int(torch.count_nonzero(V[:-3])) == 0
+    dX, dw = tg.rms_norm_grad(X, X, W, eps=1.0, out=Z)
+    dx, dws = tg.rms_norm_grad(device(x), device(x), W, eps=1.0)
+    assert torch.equal(dX[-3:], dx) and int(torch.count_nonzero(dX[:-3])) == 0
+    assert torch.allclose(dw, dws, rtol=1e-6, atol=1e-6)

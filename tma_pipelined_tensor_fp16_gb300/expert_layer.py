@@ -136,6 +136,8 @@ class SharedExpert:
     def forward(self, Q):
         """Y (tokens x width) of quantised rows, and what ``backward`` needs."""
         T, I, W = Q.rows, self.inner, self.width
+        if T == 0:  # a plan has a row at least
+            return self.S1.new_empty((0, W)), self.S1.new_empty((0, I))
         A = self._plan(T, I, W)(Q, self._weights[0]).relu_()
         return self._plan(T, W, I)(mx_quantize(A, self.format), self._weights[1]), A
 
@@ -143,6 +145,9 @@ class SharedExpert:
         """(dX, dS1, dS2) for the rows X that forward had quantised; the weights' in fp32,
         in `out` = (dS1, dS2) where it is given."""
         T, I, W, f = A.shape[0], self.inner, self.width, self.format
+        if T == 0:
+            dS1, dS2 = out or (self.S1.float(), self.S2.float())
+            return dY.new_empty((0, W)), dS1.zero_(), dS2.zero_()
         to1, to2 = ((), ()) if out is None else (out[:1], out[1:])
         dS2 = self._plan(W, I, T, "f32")(mx_quantize(dY, f, transpose=True),
                                          mx_quantize(A, f, transpose=True), *to2)
@@ -202,9 +207,7 @@ class ExpertBlock:
         Z, H, Q = rms_norm(X, self.norm_weight, residual=residual, eps=self.eps,
                            format=self.shared.format)
         Y = self.layer.decode(Z, ids, weights)
-        if Q.rows:  # a plan has a row at least
-            Y = Y.add_(self.shared.forward(Q)[0])
-        return Y, H
+        return Y.add_(self.shared.forward(Q)[0]), H
 
 
 def random_block(experts, width, inner, topk, shared, format="mxfp8", seed=0):

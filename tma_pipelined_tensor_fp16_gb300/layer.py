@@ -161,8 +161,9 @@ class GradClip:
 
 
 def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, stream=None):
-    """One pass of a GradClip; it is kept by no one, so this waits for the GPU.  A training
-    loop whose gradients stay where they are keeps a GradClip."""
+    """One pass of a GradClip; it is kept by no one, so this waits for the GPU (and cannot be
+    captured into a graph).  A training loop whose gradients stay where they are keeps a
+    GradClip."""
     clip = GradClip(grads, out)
     norm = clip(max_norm, eps, stream)
     _torch().cuda.synchronize(clip.device)
