@@ -47,17 +47,20 @@ __device__ __forceinline__ void tmem_load_64cols(uint32_t taddr, uint32_t (&r)[6
     for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i])::"memory");
 }
 
-// As stage_and_store (device_common.cuh) with one buffer a warp: it is written once the
-// store before has read it.
+// As stage_and_store (device_common.cuh) from a buffer that the caller chooses; with `reused`
+// it is written once the store before has read it.
 template <bool F16OUT>
 __device__ __forceinline__ void stage_one(const uint32_t* v, uint32_t row, uint32_t staging,
-                                          const CUtensorMap* tmap_c, int col0, int m0, int M)
+                                          const CUtensorMap* tmap_c, int col0, int m0, int M,
+                                          bool reused)
 {
     const uint32_t quarter = row >> 5;
     const uint32_t r = row & 31u;
     const uint32_t buf = staging + quarter * WARP_STAGING_BYTES;
-    if (r == 0) bulk_wait_group_read<0>();
-    __syncwarp();
+    if (reused) {
+        if (r == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+    }
     const uint32_t row_base = buf + r * 128u;
 #pragma unroll
     for (uint32_t c = 0; c < 8; ++c) {
@@ -320,6 +323,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
         constexpr int READ = 64;               // columns read at a time,
         constexpr int SUB = F16OUT ? 64 : 32;  // and stored: 128 bytes
         static_assert(TILE - static_cast<int>(ACC_SHIFT) == READ, "the shared columns");
+        static_assert(TILE / SUB * STAGING_BYTES <= MX_PAIR_MIN_STAGES * 2 * CHUNKS * MX_CHUNK_BYTES,
+                      "the last tile's buffers");
         const uint32_t q = static_cast<uint32_t>(warp & 3);
         const uint32_t row = q * 32u + lane;
         const uint32_t to_leader = map_shared_rank(bar(BAR_TMEM_EMPTY), 0);
@@ -334,6 +339,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
             tc_fence_after_sync();
             const uint32_t taddr = tmem_base + (j & 1 ? ACC_SHIFT : 0u) + (q * 32u << 16);
             const int m0 = mt * TILE + static_cast<int>(rank) * MX_ROWS;
+            // A cluster's last tile has the stages' memory to itself, a buffer for each store
+            // (its MMAs are complete, and no copy follows): no store waits for another.
+            const bool last = t + clusters >= tiles;
             // the columns that the next tile's accumulator shares come first
             const int start = j & 1 ? 0 : TILE - READ;
 #pragma unroll 1
@@ -353,7 +361,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
                 for (int c = 0; c < READ; c += SUB) {
                     const int col0 = nt * TILE + col + c;
                     if (col0 < p.N)  // uniform
-                        stage_one<F16OUT>(v + c, row, staging, &tmC, col0, m0, p.M);
+                        stage_one<F16OUT>(
+                            v + c, row,
+                            last ? base + static_cast<uint32_t>((i + c) / SUB) * STAGING_BYTES : staging,
+                            &tmC, col0, m0, p.M, !last);
                 }
             }
         }

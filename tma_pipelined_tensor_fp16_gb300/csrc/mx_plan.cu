@@ -167,7 +167,7 @@ gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K, int format
             q.grid_y = 1;
             q.split = 1;
             q.cols = 256;
-            for (q.pipe_depth = MAX_STAGES; q.pipe_depth > 1; --q.pipe_depth)
+            for (q.pipe_depth = MAX_STAGES; q.pipe_depth > MX_PAIR_MIN_STAGES; --q.pipe_depth)
                 if (mx_pair_layout(format, q.pipe_depth).total <= static_cast<uint32_t>(smem_optin))
                     break;
             q.smem_bytes = mx_pair_layout(format, q.pipe_depth).total;

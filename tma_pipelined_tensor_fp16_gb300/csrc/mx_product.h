@@ -94,6 +94,8 @@ struct MxPairLayout {
     uint32_t staging, bars, total;
 };
 
+constexpr int MX_PAIR_MIN_STAGES = 6;  // they hold a whole tile of the output at the end
+
 TG_HD MxPairLayout mx_pair_layout(int format, int depth)
 {
     MxPairLayout L;
