@@ -120,6 +120,24 @@ def test_given_tensor_scale(t):
     assert float(scale) == t
 
 
+def test_a_given_scale_stays_the_callers():
+    """Quantising again into the same tensor finds a scale of its own."""
+    import torch
+
+    import tma_pipelined_tensor_fp16_gb300 as tg
+    rng = np.random.default_rng(5)
+    x = (rng.standard_normal((20, 64)) * 300).astype(np.float16)
+    scale = torch.tensor([0.25], device="cuda")
+    Q = tg.mx_quantize(device(x), "nvfp4", tensor_scale=scale)
+    assert Q.tensor_scale is scale
+    _check(tg.mx_quantize(device(x), "nvfp4", out=Q), x)
+    assert float(scale) == 0.25 and Q.tensor_scale is not scale
+    packed, scales, _, _ = mx_util.random_operand(rng, 20, 64, "nvfp4", True)
+    R = tg.MXTensor.from_codes(device(packed), device(scales), 64, "nvfp4", scale)
+    _check(tg.mx_quantize(device(x), "nvfp4", out=R), x)
+    assert float(scale) == 0.25
+
+
 def test_zeros_and_no_rows():
     import torch
 

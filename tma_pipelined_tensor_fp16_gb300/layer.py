@@ -20,10 +20,12 @@ _CLIP_WORKSPACE = 16384  # GEMM_CLIP_WORKSPACE_BYTES
 
 
 def _matrix(name, t):
-    torch = _torch()
-    if t.dim() != 2:
+    """The shape of a contiguous fp16 CUDA matrix; raises unless `t` is one."""
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError("%s must be a matrix (tokens x width)" % name)
-    return _tensor(name, t, t.shape, torch.float16)
+    _tensor(name, t, shape, _torch().float16)
+    return shape
 
 
 def rms_norm(X, weight, residual=None, eps=1e-6, half=True, format=None, out=None, total=None,
@@ -35,28 +37,39 @@ def rms_norm(X, weight, residual=None, eps=1e-6, half=True, format=None, out=Non
     which may be X or residual itself, or a new tensor; X itself without a residual) and Q is
     z as an MXTensor of `format` (None without; nvfp4 with the tensor scale 1)."""
     torch = _torch()
-    _matrix("X", X)
+    f16 = torch.float16
+    shape = _matrix("X", X)
     dev = X.device
-    tokens, width = X.shape
-    _tensor("weight", weight, (width,), torch.float16, dev)
+    tokens, width = shape
+    _tensor("weight", weight, (width,), f16, dev)
     if residual is not None:
-        _tensor("residual", residual, X.shape, torch.float16, dev)
+        _tensor("residual", residual, shape, f16, dev)
+        H = _output("total", total, shape, f16, dev, stream)
+        at_H = H.data_ptr()
     elif total is not None:
         raise ValueError("total is for a residual: without one it would be X")
-    if out is not None and not half:
+    else:
+        H, at_H = X, None
+    if half:
+        Z = _output("out", out, shape, f16, dev, stream)
+        at_Z = Z.data_ptr()
+    elif out is not None:
         raise ValueError("out is not written with half=False")
-    if not half and format is None:
+    elif format is None:
         raise ValueError("half=False leaves no output without a format")
-    code = _format(format) if format is not None else 0
-    Z = _output("out", out, X.shape, torch.float16, dev, stream) if half else None
-    H = _output("total", total, X.shape, torch.float16, dev, stream) if residual is not None \
-        else None
-    Q = MXTensor._new(tokens, width, format, dev, stream) if format is not None else None
-    _call(lib().gemm_rms_norm, dev, stream, tokens, width, _ptr(X), _ptr(residual), _ptr(weight),
-          eps, _ptr(H), _ptr(Z), code, *(Q._addresses() if Q is not None else (None, None)))
+    else:
+        Z = at_Z = None
+    if format is None:
+        Q, code, codes, scales = None, 0, None, None
+    else:
+        code = _format(format)
+        Q = MXTensor._new(tokens, width, format, dev, stream)
+        codes, scales, _ = Q._addresses()
+    _call(lib().gemm_rms_norm, dev, stream, tokens, width, X.data_ptr(), _ptr(residual),
+          weight.data_ptr(), eps, at_H, at_Z, code, codes, scales)
     if stream is not None:
         _used_on(stream, X, weight, residual, Z, H, *(Q._parts() if Q is not None else ()))
-    return Z, X if residual is None else H, Q
+    return Z, H, Q
 
 
 @functools.lru_cache(maxsize=256)
@@ -73,18 +86,20 @@ def rms_norm_grad(dZ, H, weight, dH=None, eps=1e-6, out=None, dweight=None, stre
     residual, dH: the gradient that reaches H by its other uses.  dX (fp16; `out` may be
     dZ or dH itself) is the gradient of X and of the residual, dweight is fp32."""
     torch = _torch()
-    _matrix("dZ", dZ)
+    f16 = torch.float16
+    shape = _matrix("dZ", dZ)
     dev = dZ.device
-    tokens, width = dZ.shape
-    _tensor("H", H, dZ.shape, torch.float16, dev)
-    _tensor("weight", weight, (width,), torch.float16, dev)
+    tokens, width = shape
+    _tensor("H", H, shape, f16, dev)
+    _tensor("weight", weight, (width,), f16, dev)
     if dH is not None:
-        _tensor("dH", dH, dZ.shape, torch.float16, dev)
-    dX = _output("out", out, dZ.shape, torch.float16, dev, stream)
+        _tensor("dH", dH, shape, f16, dev)
+    size = _grad_workspace(tokens, width)
+    dX = _output("out", out, shape, f16, dev, stream)
     dw = _output("dweight", dweight, (width,), torch.float32, dev, stream)
-    work = _empty((_grad_workspace(tokens, width),), torch.uint8, dev, stream)
-    _call(lib().gemm_rms_norm_grad, dev, stream, tokens, width, _ptr(dZ), _ptr(H), _ptr(weight),
-          _ptr(dH), eps, _ptr(dX), _ptr(dw), _ptr(work))
+    work = _empty((size,), torch.uint8, dev, stream)
+    _call(lib().gemm_rms_norm_grad, dev, stream, tokens, width, dZ.data_ptr(), H.data_ptr(),
+          weight.data_ptr(), _ptr(dH), eps, dX.data_ptr(), dw.data_ptr(), work.data_ptr())
     if stream is not None:
         _used_on(stream, dZ, H, weight, dH, dX, dw, work)
     return dX, dw

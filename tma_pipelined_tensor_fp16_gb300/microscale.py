@@ -37,6 +37,12 @@ def _format(name):
         raise ValueError("format must be one of %s" % sorted(MX_FORMATS)) from None
 
 
+def _check_scale(t, format, device):
+    if format != "nvfp4":
+        raise ValueError("only nvfp4 has a tensor_scale")
+    _tensor("tensor_scale", t, (1,), _torch().float32, device)
+
+
 def _shapes(rows, K, format):
     """Shapes of the storage: codes (row blocks, chunks, 128, 16) and scales (row blocks,
     groups, 32, 4, 4)."""
@@ -49,8 +55,12 @@ def _shapes(rows, K, format):
 
 @functools.lru_cache(maxsize=512)
 def _bytes(rows, K, format):
-    """Bytes of the codes and of the scales."""
-    return tuple(math.prod(shape) for shape in _shapes(rows, K, format))
+    """Offsets in an MXTensor's own memory: of the scales, behind the codes; of the tensor
+    scale (16 bytes, nvfp4) and the space in which it is found; and the end.  All but the last
+    are multiples of 512."""
+    codes, scales = (math.prod(shape) for shape in _shapes(rows, K, format))
+    end = codes + scales
+    return codes, end, end + (16 + _WORKSPACE if format == "nvfp4" else 0)
 
 
 class MXTensor:
@@ -67,49 +77,59 @@ class MXTensor:
         _tensor("codes", codes, shape_c, torch.uint8)
         _tensor("scales", scales, shape_s, torch.uint8, codes.device)
         if tensor_scale is not None:
-            if format != "nvfp4":
-                raise ValueError("only nvfp4 has a tensor_scale")
-            _tensor("tensor_scale", tensor_scale, (1,), torch.float32, codes.device)
+            _check_scale(tensor_scale, format, codes.device)
         self.rows, self.K, self.format = rows, K, format
         self.device = codes.device
-        self._memory = codes, scales
-        self.tensor_scale = tensor_scale
+        self._buffer, self._views = None, (codes, scales)
+        self._given, self._found = tensor_scale, False
 
     @classmethod
-    def _new(cls, rows, K, format, device, stream, tensor_scale=None):
-        """Storage to be written by the library: one allocation, the scales behind the codes
-        (both are whole numbers of 512 bytes)."""
+    def _new(cls, rows, K, format, device, stream):
+        """In one allocation, to be written by the library."""
         t = cls.__new__(cls)
         t.rows, t.K, t.format, t.device = rows, K, format, device
-        codes, scales = _bytes(rows, K, format)
-        t._memory = _empty((codes + scales,), _torch().uint8, device, stream),
-        t.tensor_scale = tensor_scale
+        t._buffer, t._views = _empty((_bytes(rows, K, format)[2],), _torch().uint8, device,
+                                     stream), None
+        t._given, t._found = None, False
         return t
 
-    def _views(self):
-        if len(self._memory) == 1:
+    def _both(self):
+        if self._views is None:
             codes, scales = _shapes(self.rows, self.K, self.format)
-            n = _bytes(self.rows, self.K, self.format)[0]
-            self._memory = self._memory[0][:n].view(codes), self._memory[0][n:].view(scales)
-        return self._memory
+            n, end, _ = _bytes(self.rows, self.K, self.format)
+            self._views = self._buffer[:n].view(codes), self._buffer[n:end].view(scales)
+        return self._views
 
     @property
     def codes(self):
-        return self._views()[0]
+        return self._both()[0]
 
     @property
     def scales(self):
-        return self._views()[1]
+        return self._both()[1]
+
+    @property
+    def tensor_scale(self):
+        if not self._found:
+            return self._given
+        at = _bytes(self.rows, self.K, self.format)[1]
+        return self._buffer[at:at + 4].view(_torch().float32)
 
     def _addresses(self):
-        """Of the codes and the scales."""
-        at = self._memory[0].data_ptr()
-        if len(self._memory) == 1:
-            return at, at + _bytes(self.rows, self.K, self.format)[0] if at else None
-        return at, self._memory[1].data_ptr()
+        """Of the codes, the scales and the tensor scale."""
+        given = None if self._given is None else self._given.data_ptr()
+        if self._buffer is None:
+            codes, scales = self._views
+            return codes.data_ptr(), scales.data_ptr(), given
+        at = self._buffer.data_ptr()
+        if not at:  # no rows, no memory
+            return None, None, given
+        n, end, _ = _bytes(self.rows, self.K, self.format)
+        return at, at + n, at + end if self._found else given
 
     def _parts(self):
-        return self._memory + (self.tensor_scale,)
+        """The tensors that hold it."""
+        return (self._views if self._buffer is None else (self._buffer,)) + (self._given,)
 
     @classmethod
     def from_codes(cls, codes, scales, K, format, tensor_scale=None):
@@ -151,11 +171,10 @@ class MXTensor:
         (fp16 when not given; fp32 holds them exactly)."""
         torch = _torch()
         dev = self.device
-        dtype = torch.float32 if out is not None and out.dtype == torch.float32 else torch.float16
+        dtype = torch.float32 if out is not None and out.dtype is torch.float32 else torch.float16
         V = _output("out", out, (self.rows, self.K), dtype, dev, stream)
         _call(lib().gemm_mx_values, dev, stream, self.rows, self.K, MX_FORMATS[self.format],
-              *self._addresses(), _ptr(self.tensor_scale),
-              0 if dtype == torch.float32 else 1, _ptr(V))
+              *self._addresses(), 0 if dtype is torch.float32 else 1, _ptr(V))
         if stream is not None:
             _used_on(stream, *self._parts(), V)
         return V
@@ -165,40 +184,45 @@ def mx_quantize(X, format="mxfp8", transpose=False, tensor_scale=None, out=None,
     """Round X (fp16, contiguous; its rows hold a multiple of 8 values) to `format`:
     an MXTensor of X's shape, or of X^T's with `transpose` (blocks run along X's columns).
 
-    nvfp4: without `tensor_scale` (one fp32, a power of two) it is found from X first.
-    `out`, an MXTensor of the result's shape and format, is written and returned; its
-    tensor_scale is written where none is given."""
+    nvfp4: without `tensor_scale` (one fp32, a power of two) it is found from X first and
+    belongs to the result.  `out`, an MXTensor of the result's shape and format, is written
+    in place and returned."""
     torch = _torch()
     code = _format(format)
-    if X.dim() != 2:
+    shape = X.shape
+    if len(shape) != 2:
         raise ValueError("X must be a matrix")
-    _tensor("X", X, X.shape, torch.float16)
+    _tensor("X", X, shape, torch.float16)
     dev = X.device
-    rows, K = (X.shape[1], X.shape[0]) if transpose else (X.shape[0], X.shape[1])
+    rows, K = shape
+    if transpose:
+        rows, K = K, rows
     if K < 1:
         raise ValueError("a row must hold a value at least")
     if tensor_scale is not None:
-        if format != "nvfp4":
-            raise ValueError("only nvfp4 has a tensor_scale")
-        _tensor("tensor_scale", tensor_scale, (1,), torch.float32, dev)
+        _check_scale(tensor_scale, format, dev)
     if out is None:
-        Q = MXTensor._new(rows, K, format, dev, stream, tensor_scale)
+        Q = MXTensor._new(rows, K, format, dev, stream)
     else:
         Q = out
         if (Q.rows, Q.K, Q.format) != (rows, K, format) or Q.device != dev:
             raise ValueError("out must be a %s MXTensor of %d x %d on %s"
                              % (format, rows, K, dev))
-        if tensor_scale is not None:
-            Q.tensor_scale = tensor_scale
-    work = None
-    if format == "nvfp4" and tensor_scale is None:
-        work = _empty((_WORKSPACE,), torch.uint8, dev, stream)
-        if Q.tensor_scale is None:
-            Q.tensor_scale = _empty((1,), torch.float32, dev, stream)
-    _call(lib().gemm_mx_quantize, dev, stream, rows, K, code, 1 if transpose else 0, _ptr(X),
-          *Q._addresses(), _ptr(Q.tensor_scale), _ptr(work))
+    work = extra = None
+    if tensor_scale is not None:
+        Q._given, Q._found = tensor_scale, False
+    elif code == 2:  # nvfp4
+        if Q._buffer is None:  # made by the caller: it has no room for it
+            Q._given = _empty((1,), torch.float32, dev, stream)
+            extra = _empty((_WORKSPACE,), torch.uint8, dev, stream)
+            work = extra.data_ptr()
+        else:
+            Q._given, Q._found = None, True
+            work = Q._buffer.data_ptr() + _bytes(rows, K, format)[1] + 16
+    _call(lib().gemm_mx_quantize, dev, stream, rows, K, code, 1 if transpose else 0,
+          X.data_ptr(), *Q._addresses(), work)
     if stream is not None:
-        _used_on(stream, X, *Q._parts(), work)
+        _used_on(stream, X, *Q._parts(), extra)
     return Q
 
 
@@ -229,8 +253,8 @@ class MXPlan(_Handle):
         if B.device != dev:
             raise ValueError("B is on %s, the other tensors on %s" % (B.device, dev))
         C = _output("out", out, (self.M, self.N), self.dtype, dev, stream)
-        _call(lib().gemm_mx_run, dev, stream, self._h, *A._addresses(), _ptr(A.tensor_scale),
-              *B._addresses(), _ptr(B.tensor_scale), _ptr(C))
+        _call(lib().gemm_mx_run, dev, stream, self._h, *A._addresses(), *B._addresses(),
+              C.data_ptr())
         if stream is not None:
             _used_on(stream, *A._parts(), *B._parts(), C)
         return C
