@@ -141,6 +141,47 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], const BlockScale& 
     return r;
 }
 
+// Eight halves (in four words) to mxfp8, scaled as pairs of halves: one multiplication for two
+// values and no widening (16384 x 4096: 35.3 us, 37.3 through fp32; the 4-bit conversion from
+// halves is the slower one, 34.8 and 32.6).  That is exact where it decides a rounding: a
+// product by a power of two is inexact only below 2^-14, the smallest normal half, and such
+// values round to zero (the least border is 2^-10).  The factor 2^-e, e from -32 to 8 for fp16
+// values, is applied in two steps that a half holds; beyond 2^30 (no value of the block
+// above 2^-22) the words go through fp32.
+__device__ __forceinline__ uint2 encode8_mxfp8(const uint4& v, const BlockScale& b)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const int e = 127 - static_cast<int>(b.byte);
+    if (e > 30) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+        return encode8<MXFP8>(x, b);
+    }
+    const int e1 = min(e, 15);
+    // a block that is not finite has the byte 255: factors of zero
+    const bool finite = b.byte != 255u;
+    const uint32_t f1 = finite ? static_cast<uint32_t>(e1 + 15) << 10 : 0u;
+    const uint32_t f2 = static_cast<uint32_t>(finite ? e - e1 + 15 : 0) << 10;
+    const uint32_t p1 = f1 | f1 << 16, p2 = f2 | f2 << 16;
+    uint16_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 y = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&w[i]),
+                                          *reinterpret_cast<const __half2*>(&p1)),
+                                  *reinterpret_cast<const __half2*>(&p2));
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
+            : "=h"(q[i])
+            : "r"(*reinterpret_cast<const uint32_t*>(&y)));
+    }
+    return make_uint2(static_cast<uint32_t>(q[0]) | static_cast<uint32_t>(q[1]) << 16,
+                      static_cast<uint32_t>(q[2]) | static_cast<uint32_t>(q[3]) << 16);
+}
+
 // Lanes that share a block when a lane holds eight consecutive values, and the largest
 // magnitude over them.  A NaN counts as larger than everything (comparison of bits).
 template <int FORMAT>

@@ -3,6 +3,12 @@
 // its rows of A and of all of B's; clusters take tiles t, t + clusters, ... of the grouped
 // raster.
 //
+// Measured: 8192 x 8192 x 8192 nvfp4 134 us, 8200 TFLOP/s, mxfp4 125, mxfp8 291 (held for half a
+// second, under the power cap: 150, 139, 331); 4000 x 3000 x 5000 mxfp4 with fp32 output 22 to
+// 26; 2048 x 2048 x 2048 nvfp4 6.4.  An MMA of 96 values takes 128 cycles; with all SMs busy 159,
+// as a stage's copies take about 2200 cycles to arrive and seven stages are all that fits (the
+// issuer waits for 23 % of the time).  A tile's change costs 1000 cycles.
+//
 // Tensor memory: two accumulators of 256 columns would leave no room for scales.  They
 // lie at columns 0 and 192 and share 64; scales take columns 448 on.  The epilogue reads
 // the shared columns first and gives them up, so the next tile's MMAs wait for a quarter

@@ -1,6 +1,10 @@
 // mx_single.cu -- block-scaled products on single CTAs: few rows (decoding), and
 // products too small to fill the GPU with tiles of CTA pairs.
 //
+// Measured: one row of 16384 x 16384 nvfp4 25.8 us, 5.9 TB/s; 64 rows mxfp8 45 us, 6.2 TB/s (in
+// both 2.5 to 4 us are the launch, the first loads and the cluster's sums); 4 rows of 4096 x
+// 4096 nvfp4 4.5 us.
+//
 // One tile per CTA, or per cluster whose CTAs share its length: 128 rows of one operand
 // (U, the MMA's M side) and COLS of the other (V, the N side).  With few rows of A, U is
 // the weights B and a tile is stored transposed (`SWAPPED`); bound by reading the weights
