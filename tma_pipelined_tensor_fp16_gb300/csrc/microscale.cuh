@@ -142,8 +142,8 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], const BlockScale& 
 }
 
 // Eight halves (in four words) to mxfp8, scaled as pairs of halves: one multiplication for two
-// values and no widening (16384 x 4096: 35.3 us, 37.3 through fp32; the 4-bit conversion from
-// halves is the slower one, 34.8 and 32.6).  That is exact where it decides a rounding: a
+// values and no widening (5 % of a quantisation; the 4-bit conversion from halves is slower
+// than from fp32).  That is exact where it decides a rounding: a
 // product by a power of two is inexact only below 2^-14, the smallest normal half, and such
 // values round to zero (the least border is 2^-10).  The factor 2^-e, e from -32 to 8 for fp16
 // values, is applied in two steps that a half holds; beyond 2^30 (no value of the block

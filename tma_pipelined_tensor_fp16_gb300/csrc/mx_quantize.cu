@@ -1,8 +1,8 @@
 // mx_quantize.cu -- fp16 matrices to the block-scaled formats of include/tmamicro.h and
 // back.  On paper all are bound by memory: every value is read once (twice where the tensor
-// scale has to be found first) and its codes and scales are written once.  In fact the
-// roundings are bound by issue slots (60 to 77 % busy): 16384 x 4096 to mxfp8 35 us, 5.8 TB/s,
-// mxfp4 33, nvfp4 39; along columns 33, 30, 35; decoding 31, 27, 27 us, 6.3 to 6.6 TB/s.
+// scale has to be found first) and its codes and scales are written once.  Measured: 16384 x
+// 4096 to mxfp8 31 us, 6.5 TB/s, mxfp4 28, nvfp4 33 (bound by issue slots, 5.2 TB/s); along
+// columns 33, 30, 35; decoding 31, 27, 27 us, 6.3 to 6.6 TB/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -102,12 +102,10 @@ __device__ __forceinline__ float find_tensor_scale(const QuantizeParams& p, uint
 
 // --------------------------------------------------------------- along rows
 //
-// A lane holds eight consecutive values; four lanes a block of 32, eight rows a warp.
-// So a warp's load touches 64 contiguous bytes of each of eight rows, and a store 128
-// contiguous bytes of a chunk's column.  A warp takes 8 rows x 128 values (96 of mxfp4): a
-// group of scales (two of nvfp4) is one 32-bit store.
-constexpr int ROW_WARPS = 8;
-// Blocks of 32 values of a row per warp: a group of scales (two of nvfp4).
+// A CTA takes 32 rows x 128 values (96 of mxfp4) through shared memory, and a thread 32 values
+// of a row: a block (two of nvfp4), 16 or 32 bytes of codes.  So a scale is found once and
+// without exchange between lanes (with four lanes a block, each finding it: 35, 33, 39 us), and
+// a warp, whose lanes are consecutive rows, stores 512 contiguous bytes of a chunk's column.
 TG_HD constexpr int row_spans(int format) { return format == MXFP4 ? 3 : 4; }
 TG_HD constexpr int row_k(int format) { return 32 * row_spans(format); }
 
@@ -122,100 +120,79 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8])
     }
 }
 
-// How a CTA's warps lie: 1 << k_log along a row, the others in the next rows.
-struct RowTiling {
-    uint32_t cta_spans;  // CTAs along a row
-    int k_log;
-    int64_t grid;
-};
-
-RowTiling row_tiling(int64_t rows, int64_t K, int format)
-{
-    const int64_t spans = (K + row_k(format) - 1) / row_k(format);
-    RowTiling t;
-    t.k_log = spans >= 8 ? 3 : spans >= 4 ? 2 : spans >= 2 ? 1 : 0;
-    t.cta_spans = static_cast<uint32_t>((spans + (1 << t.k_log) - 1) >> t.k_log);
-    const int64_t cta_rows = 8 * (ROW_WARPS >> t.k_log);
-    t.grid = std::max<int64_t>(1, (rows + cta_rows - 1) / cta_rows) * t.cta_spans;
-    return t;
-}
-
-// First row and first value of this warp's tile.
-__device__ __forceinline__ void row_tile(uint32_t cta_spans, int k_log, int width, int64_t& row0,
-                                         int64_t& k0)
-{
-    const uint32_t warp = threadIdx.x / 32;
-    const uint32_t y = blockIdx.x / cta_spans, x = blockIdx.x - y * cta_spans;
-    row0 = (static_cast<int64_t>(y) * (ROW_WARPS >> k_log) + (warp >> k_log)) * 8;
-    k0 = (static_cast<int64_t>(x) * (1 << k_log) + (warp & ((1u << k_log) - 1u))) * width;
-}
-
 template <int FORMAT>
-__global__ void __launch_bounds__(ROW_WARPS * 32)
-    k_mx_quantize(const __grid_constant__ QuantizeParams p, uint32_t cta_spans, int k_log)
+__global__ void __launch_bounds__(row_k(FORMAT))
+    k_mx_quantize(const __grid_constant__ QuantizeParams p, uint32_t spans)
 {
-    constexpr int SPANS = row_spans(FORMAT), ROW_K = row_k(FORMAT);
-    __shared__ uint32_t shared[ROW_WARPS];
+    constexpr int ROW_K = row_k(FORMAT), THREADS = ROW_K;
+    constexpr int VECS = ROW_K / 8;               // of eight values in a row of the tile
+    __shared__ uint32_t shared[THREADS / 32];
+    __shared__ __align__(16) uint4 tile[32][VECS + 1];
+    __shared__ __align__(4) uint8_t scale_bytes[32][8];
+    const int tid = static_cast<int>(threadIdx.x);
+    if (FORMAT == MXFP4 && tid < 32) scale_bytes[tid][3] = 0;
     griddep_wait();
     griddep_launch_dependents();
     const float t = find_tensor_scale<FORMAT>(p, shared);
     const float sixth = 1.0f / (6.0f * t);
-    const int lane = static_cast<int>(lane_id());
-    const int r = lane / 4, part = lane % 4;
-    int64_t row0, k0;
-    row_tile(cta_spans, k_log, ROW_K, row0, k0);
-    if (row0 >= p.rows || k0 >= p.K) return;
-    const int64_t row = row0 + r;
-    const bool valid = row < p.rows;
-    const __half* x_row = p.X + (valid ? row : 0) * p.K;
-    uint4 v[SPANS];
+    const uint32_t y = blockIdx.x / spans;
+    const int64_t row0 = static_cast<int64_t>(y) * 32;
+    const int64_t k0 = static_cast<int64_t>(blockIdx.x - y * spans) * ROW_K;
 #pragma unroll
-    for (int j = 0; j < SPANS; ++j) {
-        const int64_t k = k0 + j * 32 + part * 8;
-        v[j] = make_uint4(0, 0, 0, 0);
-        if (valid && k < p.K) v[j] = *reinterpret_cast<const uint4*>(x_row + k);
+    for (int i = 0; i < 32 * VECS / THREADS; ++i) {
+        const int at = i * THREADS + tid, line = at / VECS, vec = at % VECS;
+        const int64_t row = row0 + line, k = k0 + vec * 8;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < p.rows && k < p.K) v = *reinterpret_cast<const uint4*>(p.X + row * p.K + k);
+        tile[line][vec] = v;
     }
-    uint8_t* codes = p.codes + mx_code_offset(row, k0 / mx_chunk(FORMAT), p.chunks);
-    uint32_t bytes[SPANS];
-    constexpr int PER_CHUNK = mx_chunk(FORMAT) / 8;  // lanes of a chunk
+    __syncthreads();
+    const int line = tid % 32, part = tid / 32;  // 32 values of a row
+    const int64_t row = row0 + line;
+    uint4 v[4];
 #pragma unroll
-    for (int j = 0; j < SPANS; ++j) {
-        const BlockScale b =
-            block_scale<FORMAT>(block_most<FORMAT>(most_of_halves(v[j])), t, sixth);
-        uint2 q;
-        if constexpr (FORMAT == MXFP8) {
-            q = encode8_mxfp8(v[j], b);
-        } else {
-            float x[8];
-            unpack8(v[j], x);
-            q = encode8<FORMAT>(x, b);
+    for (int j = 0; j < 4; ++j) v[j] = tile[line][part * 4 + j];
+    constexpr int PER_BLOCK = mx_block(FORMAT) / 8;
+    uint32_t out[8];
+#pragma unroll
+    for (int j = 0; j < 4; j += PER_BLOCK) {
+        uint32_t most = 0;  // magnitudes compare as their bits, NaN above the infinity
+#pragma unroll
+        for (int i = 0; i < PER_BLOCK; ++i)
+            most = max(most, __float_as_uint(most_of_halves(v[j + i])));
+        const BlockScale b = block_scale<FORMAT>(__uint_as_float(most), t, sixth);
+#pragma unroll
+        for (int i = 0; i < PER_BLOCK; ++i) {
+            if constexpr (FORMAT == MXFP8) {
+                const uint2 q = encode8_mxfp8(v[j + i], b);
+                out[2 * (j + i)] = q.x;
+                out[2 * (j + i) + 1] = q.y;
+            } else {
+                float x[8];
+                unpack8(v[j + i], x);
+                out[j + i] = encode8<FORMAT>(x, b).x;
+            }
         }
-        const int chunk = (j * 4 + part) / PER_CHUNK;
-        if (valid && k0 / mx_chunk(FORMAT) + chunk < p.chunks) {
-            uint8_t* to = codes + chunk * MX_CHUNK_BYTES;
-            if constexpr (FORMAT == MXFP8)
-                reinterpret_cast<uint2*>(to)[part % PER_CHUNK] = q;
-            else
-                reinterpret_cast<uint32_t*>(to)[part % PER_CHUNK] = q.x;
-        }
-        bytes[j] = b.byte;
+        scale_bytes[line][(part * 4 + j) / PER_BLOCK] = static_cast<uint8_t>(b.byte);
     }
-    uint8_t* scales = p.scales + mx_scale_offset(row, k0 / mx_group(FORMAT), p.groups);
-    if constexpr (FORMAT == NVFP4) {
-        // 128 values are eight blocks: the second of a pair is two lanes on
+    if (row < p.rows) {
+        constexpr int CHUNKS = 32 / mx_chunk(FORMAT);
+        const int64_t chunk = (k0 + part * 32) / mx_chunk(FORMAT);
+        uint8_t* to = p.codes + mx_code_offset(row, chunk, p.chunks);
 #pragma unroll
-        for (int j = 0; j < SPANS; ++j) bytes[j] |= __shfl_down_sync(0xffffffffu, bytes[j], 2) << 8;
-        if (valid && part == 0) {
-            const int64_t g = k0 / mx_group(FORMAT);
-            reinterpret_cast<uint32_t*>(scales)[0] = bytes[0] | bytes[1] << 16;
-            if (g + 1 < p.groups)
-                *reinterpret_cast<uint32_t*>(scales + MX_GROUP_BYTES) = bytes[2] | bytes[3] << 16;
-        }
-    } else {
-        if (valid && part == 0)
-            *reinterpret_cast<uint32_t*>(scales) =
-                bytes[0] | bytes[1] << 8 | bytes[2] << 16 |
-                (SPANS > 3 ? bytes[SPANS - 1] << 24 : 0u);
+        for (int c = 0; c < CHUNKS; ++c)
+            if (chunk + c < p.chunks)
+                *reinterpret_cast<uint4*>(to + c * MX_CHUNK_BYTES) =
+                    make_uint4(out[4 * c], out[4 * c + 1], out[4 * c + 2], out[4 * c + 3]);
+    }
+    __syncthreads();
+    constexpr int GROUPS = ROW_K / mx_group(FORMAT);
+    if (tid < 32 * GROUPS) {
+        const int64_t to_row = row0 + tid % 32;
+        const int64_t group = k0 / mx_group(FORMAT) + tid / 32;
+        if (to_row < p.rows && group < p.groups)
+            *reinterpret_cast<uint32_t*>(p.scales + mx_scale_offset(to_row, group, p.groups)) =
+                *reinterpret_cast<const uint32_t*>(&scale_bytes[tid % 32][tid / 32 * 4]);
     }
 }
 
@@ -311,6 +288,36 @@ __global__ void __launch_bounds__(col_threads(FORMAT))
 
 // -------------------------------------------------------------------- values
 
+constexpr int ROW_WARPS = 8;
+
+// How a CTA's warps lie: 1 << k_log along a row, the others in the next rows.
+struct RowTiling {
+    uint32_t cta_spans;  // CTAs along a row
+    int k_log;
+    int64_t grid;
+};
+
+RowTiling row_tiling(int64_t rows, int64_t K, int format)
+{
+    const int64_t spans = (K + row_k(format) - 1) / row_k(format);
+    RowTiling t;
+    t.k_log = spans >= 8 ? 3 : spans >= 4 ? 2 : spans >= 2 ? 1 : 0;
+    t.cta_spans = static_cast<uint32_t>((spans + (1 << t.k_log) - 1) >> t.k_log);
+    const int64_t cta_rows = 8 * (ROW_WARPS >> t.k_log);
+    t.grid = std::max<int64_t>(1, (rows + cta_rows - 1) / cta_rows) * t.cta_spans;
+    return t;
+}
+
+// First row and first value of this warp's tile.
+__device__ __forceinline__ void row_tile(uint32_t cta_spans, int k_log, int width, int64_t& row0,
+                                         int64_t& k0)
+{
+    const uint32_t warp = threadIdx.x / 32;
+    const uint32_t y = blockIdx.x / cta_spans, x = blockIdx.x - y * cta_spans;
+    row0 = (static_cast<int64_t>(y) * (ROW_WARPS >> k_log) + (warp >> k_log)) * 8;
+    k0 = (static_cast<int64_t>(x) * (1 << k_log) + (warp & ((1u << k_log) - 1u))) * width;
+}
+
 struct ValuesParams {
     int64_t rows, K, chunks, groups;
     const uint8_t* codes;
@@ -348,7 +355,8 @@ __device__ __forceinline__ void decode8(uint2 q, __half2 (&v)[4])
     for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<__half2*>(&h[i]);
 }
 
-// Lanes as in k_mx_quantize: a warp takes 8 rows x 128 (96) values.  With ODD a row's length is
+// A lane decodes eight consecutive values; four lanes 32, eight rows a warp: a warp takes 8
+// rows x 128 (96) values.  With ODD a row's length is
 // no multiple of 8, so that rows start anywhere: the values go through shared memory and
 // leave as aligned words, 64 bytes and more at a time.
 template <int FORMAT, bool F16OUT, bool ODD>
@@ -576,11 +584,12 @@ int gemm_mx_quantize(int64_t rows, int64_t K, int format, int transpose, const v
                               k_mx_quantize_columns<NVFP4>, grid, col_threads(format), stream, p,
                               static_cast<uint32_t>(cols));
         } else {
-            const RowTiling t = row_tiling(rows, K, format);
-            if (t.grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
+            const int64_t spans = (K + row_k(format) - 1) / row_k(format);
+            const int64_t grid = std::max<int64_t>(1, (rows + 31) / 32) * spans;
+            if (grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
             e = launch_format(format, k_mx_quantize<MXFP8>, k_mx_quantize<MXFP4>,
-                              k_mx_quantize<NVFP4>, t.grid, ROW_WARPS * 32, stream, p, t.cta_spans,
-                              t.k_log);
+                              k_mx_quantize<NVFP4>, grid, row_k(format), stream, p,
+                              static_cast<uint32_t>(spans));
         }
         return e == cudaSuccess ? ok() : cuda_fail("quantisation launch", e);
     });
