@@ -134,6 +134,7 @@ class GradClip:
         self.grads, self.out, self.device = grads, out, dev
         self._tensors = grads if out is grads else grads + out
         self._addresses = [t.data_ptr() for t in self._tensors]
+        self._places = list(range(len(self._tensors)))
         n = len(grads)
         addresses = ctypes.c_void_p * n
         with torch.cuda.device(dev):
@@ -144,9 +145,17 @@ class GradClip:
         if not self._h:
             raise GemmError(lib().gemm_last_status(), last_error())
 
+    def _in_place(self, torch):
+        """Whether every tensor is where it was (in one call where torch has one for its own
+        graphs: 21 us for 640 tensors, one by one 37)."""
+        same = getattr(torch._C, "_tensors_data_ptrs_at_indices_equal", None)
+        if same is not None:
+            return same(self._tensors, self._addresses, self._places)
+        return [t.data_ptr() for t in self._tensors] == self._addresses
+
     def _run(self, fn, stream, *args):
         torch = _torch()
-        if list(map(torch._C.TensorBase.data_ptr, self._tensors)) != self._addresses:
+        if not self._in_place(torch):
             raise ValueError("a tensor's memory has moved: make a new GradClip")
         norm = _empty((1,), torch.float32, self.device, stream)
         work = _empty((_CLIP_WORKSPACE,), torch.uint8, self.device, stream)
