@@ -104,14 +104,17 @@ __device__ __forceinline__ double warp_sum(double s)
     return s;
 }
 
-// The CTA's sum, in its first warp.
-__device__ __forceinline__ double block_sum(double s, double* shared)
+// The CTA's sum, in its first warp: which adds all up, as an fp64 addition keeps the SM's
+// fp64 unit busy for 16 cycles whether a warp's lanes need it or not.
+__device__ __forceinline__ double block_sum(double s, double (&shared)[CLIP_THREADS])
 {
-    s = warp_sum(s);
-    if (lane_id() == 0) shared[threadIdx.x / 32] = s;
+    shared[threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.x >= 32) return 0.0;
-    return warp_sum(threadIdx.x < CLIP_THREADS / 32 ? shared[threadIdx.x] : 0.0);
+    s = 0.0;
+#pragma unroll
+    for (int i = 0; i < CLIP_THREADS / 32; ++i) s += shared[i * 32 + threadIdx.x];
+    return warp_sum(s);
 }
 
 // Vectors of a whole chunk per thread.
@@ -121,7 +124,7 @@ constexpr int CHUNK_F16 = static_cast<int>(CHUNK / 8 / CLIP_THREADS);
 __global__ void __launch_bounds__(CLIP_THREADS) k_grad_squares(const Chunk* table, int64_t chunks,
                                                                double* parts)
 {
-    __shared__ double shared[CLIP_THREADS / 32];
+    __shared__ double shared[CLIP_THREADS];
     griddep_wait();
     griddep_launch_dependents();
     const int tid = static_cast<int>(threadIdx.x);
@@ -205,6 +208,23 @@ __global__ void __launch_bounds__(CLIP_THREADS) k_grad_squares(const Chunk* tabl
     if (tid == 0) parts[blockIdx.x] = sum;
 }
 
+// Square root and reciprocal from fp32 ones and a Newton step in fp64 (2^-44 off at most),
+// where fp32 holds them: the library's take several times the fp64 instructions.
+__device__ __forceinline__ double square_root(double x)
+{
+    if (!(x >= 0x1p-100 && x <= 0x1p100)) return sqrt(x);
+    const double y = static_cast<double>(rsqrtf(static_cast<float>(x)));
+    const double root = x * y;  // root + (x - root^2) y / 2
+    return fma(fma(-root, root, x), 0.5 * y, root);
+}
+
+__device__ __forceinline__ double reciprocal(double x)
+{
+    if (!(x >= 0x1p-100 && x <= 0x1p100)) return 1.0 / x;
+    const double y = static_cast<double>(1.0f / static_cast<float>(x));
+    return fma(fma(-x, y, 1.0), y, y);
+}
+
 __device__ __forceinline__ uint4 scaled8(const uint4& v, float first, float f)
 {
     float x[8];
@@ -235,16 +255,18 @@ __global__ void __launch_bounds__(CLIP_THREADS)
         // one warp adds the parts up, as fp64 instructions are slow
         double sum = 0.0;
         for (int i = tid; i < part_count; i += 32) sum += parts[i];
-        const double length = sqrt(warp_sum(sum));
+        sum = warp_sum(sum);
         if (tid == 0) {
+            const double length = square_root(sum);
             if (blockIdx.x == 0) *norm = static_cast<float>(length);
-            const double ratio = static_cast<double>(max_norm) / (length + static_cast<double>(eps));
+            const double ratio =
+                static_cast<double>(max_norm) * reciprocal(length + static_cast<double>(eps));
             // NaN stays NaN; no length, nothing to scale (and perhaps no quotient)
             const double factor = ratio >= 1.0 || length == 0.0 ? 1.0 : ratio;
             // in two steps, the first a power of two: fp32 does not hold the smallest
             // factors whole
             factors[0] = factor < 0x1p-100 ? 0x1p-64f : 1.0f;
-            factors[1] = static_cast<float>(factor / static_cast<double>(factors[0]));
+            factors[1] = static_cast<float>(factor < 0x1p-100 ? factor * 0x1p64 : factor);
         }
     }
     if (!scale) return;
