@@ -170,7 +170,8 @@ def test_the_formula_against_differences():
 
 
 @pytest.mark.parametrize("tokens,width", SHAPES + [(700, 1024), (2000, 4096), (1, 4096),
-                                                   (5000, 264), (3000, 512)])
+                                                   (5000, 264), (3000, 512), (900, 8200),
+                                                   (700, 12296), (650, 16384), (400, 32768)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_gradient(tokens, width, residual):
     """dX: n (u h) is a sum of `width` terms, S = sum |u h|, entering dX through |h| rstd^3 /

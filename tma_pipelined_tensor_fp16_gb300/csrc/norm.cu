@@ -1,8 +1,8 @@
 // norm.cu -- root-mean-square norm with the residual's addition and quantised rows, and
 // its gradient.  Bound by memory: every value is read once and written once per output.
 // Measured on 67 M values, residual, fp16 and mxfp8 rows: 92 to 97 us for widths from 128 to
-// 16384, 6.2 to 6.6 TB/s; gradient with the residual's: 87 to 102 us (widths to 8192), 5.3 to
-// 6.1 TB/s.  16 rows of 4096: 2.3 us.
+// 16384, 6.2 to 6.6 TB/s; gradient with the residual's: 87 to 97 us for widths from 128 to 8192,
+// 5.5 to 6.2 TB/s, 100 to 106 to 16384, 129 at 32768.  16 rows of 4096: 2.3 us.
 #include <algorithm>
 #include <cmath>
 
@@ -190,12 +190,28 @@ constexpr int grad_resident(int lanes, int vec)
                           : 1;
 }
 
+// 16 bytes to a thread's own place in shared memory, without a register on the way.
+__device__ __forceinline__ void copy_ahead(uint4* to, const __half* from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+                 "l"(from)
+                 : "memory");
+}
+
 // Rows as in k_rms_norm, each group of LANES lanes taking every stride-th row; a lane's
 // columns stay the same, so their sums over its rows stay in registers and are written
 // once as the group's part of dweight.
-template <int LANES, int VEC, int THREADS>
-__global__ void __launch_bounds__(THREADS, grad_resident(LANES, VEC)) k_rms_norm_grad(const __grid_constant__ NormGradParams p)
+// STAGED: a row waits in shared memory instead of registers, every thread's vectors at places
+// of its own, which the next row's take as soon as the last reading is over.  For rows whose
+// registers would leave room for one CTA on an SM only (67 M values, 9472 wide: 104 us, in
+// registers 146; 16384 wide 105, 111; 32768 wide 129, 170, with spills).  Shorter rows are faster
+// in registers (4096 wide 87, staged 92; 8192 wide 92, 99).
+template <int LANES, int VEC, int THREADS, bool STAGED = false>
+__global__ void __launch_bounds__(THREADS, grad_resident(LANES, VEC))
+    k_rms_norm_grad(const __grid_constant__ NormGradParams p)
 {
+    extern __shared__ uint4 staged[];  // STAGED: [VEC][h, dz, dh][THREADS]
     constexpr int ROWS = THREADS / LANES;
     __shared__ float2 shared[2][THREADS / 32];
     const int lane = static_cast<int>(threadIdx.x) % LANES;
@@ -208,17 +224,33 @@ __global__ void __launch_bounds__(THREADS, grad_resident(LANES, VEC)) k_rms_norm
     for (int i = 0; i < VEC; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+    const auto stage = [&](int i) { return staged + i * 3 * THREADS + threadIdx.x; };
+    const auto fetch = [&](int64_t row, int i) {
+        const int k = (i * LANES + lane) * 8;
+        if (row >= p.tokens || k >= p.width) return;
+        copy_ahead(stage(i), p.H + row * p.width + k);
+        copy_ahead(stage(i) + THREADS, p.dZ + row * p.width + k);
+        if (p.dH) copy_ahead(stage(i) + 2 * THREADS, p.dH + row * p.width + k);
+    };
+    if constexpr (STAGED)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) fetch(group, i);
     int turn = 0;
     for (int64_t row = group; row < p.tokens; row += groups) {
-        uint4 hv[VEC], dv[VEC], rv[VEC];
+        constexpr int HELD = STAGED ? 1 : VEC;
+        uint4 hv[HELD], dv[HELD], rv[HELD];
+        if constexpr (STAGED) {
+            asm volatile("cp.async.wait_all;" ::: "memory");  // a thread reads its own copies
+        } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int k = (i * LANES + lane) * 8;
-            hv[i] = dv[i] = rv[i] = make_uint4(0, 0, 0, 0);
-            if (k < p.width) {
-                hv[i] = *reinterpret_cast<const uint4*>(p.H + row * p.width + k);
-                dv[i] = *reinterpret_cast<const uint4*>(p.dZ + row * p.width + k);
-                if (p.dH) rv[i] = *reinterpret_cast<const uint4*>(p.dH + row * p.width + k);
+            for (int i = 0; i < VEC; ++i) {
+                const int k = (i * LANES + lane) * 8;
+                hv[i] = dv[i] = rv[i] = make_uint4(0, 0, 0, 0);
+                if (k < p.width) {
+                    hv[i] = *reinterpret_cast<const uint4*>(p.H + row * p.width + k);
+                    dv[i] = *reinterpret_cast<const uint4*>(p.dZ + row * p.width + k);
+                    if (p.dH) rv[i] = *reinterpret_cast<const uint4*>(p.dH + row * p.width + k);
+                }
             }
         }
         float2 s = make_float2(0.0f, 0.0f);  // sum of h^2, of u h
@@ -227,8 +259,8 @@ __global__ void __launch_bounds__(THREADS, grad_resident(LANES, VEC)) k_rms_norm
             const int k = (i * LANES + lane) * 8;
             if (k >= p.width) continue;
             float h[8], d[8], w[8];
-            widen8(hv[i], h);
-            widen8(dv[i], d);
+            widen8(STAGED ? stage(i)[0] : hv[i % HELD], h);
+            widen8(STAGED ? stage(i)[THREADS] : dv[i % HELD], d);
             widen8(__ldg(reinterpret_cast<const uint4*>(p.weight + k)), w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -257,8 +289,8 @@ __global__ void __launch_bounds__(THREADS, grad_resident(LANES, VEC)) k_rms_norm
             const int k = (i * LANES + lane) * 8;
             if (k >= p.width) continue;
             float h[8], d[8], w[8], x[8];
-            widen8(hv[i], h);
-            widen8(dv[i], d);
+            widen8(STAGED ? stage(i)[0] : hv[i % HELD], h);
+            widen8(STAGED ? stage(i)[THREADS] : dv[i % HELD], d);
             widen8(__ldg(reinterpret_cast<const uint4*>(p.weight + k)), w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -267,10 +299,11 @@ __global__ void __launch_bounds__(THREADS, grad_resident(LANES, VEC)) k_rms_norm
             }
             if (p.dH) {
                 float r[8];
-                widen8(rv[i], r);
+                widen8(STAGED ? stage(i)[2 * THREADS] : rv[i % HELD], r);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] += r[j];
             }
+            if constexpr (STAGED) fetch(row + groups, i);
             *reinterpret_cast<uint4*>(p.dX + row * p.width + k) = narrow8(x);
         }
     }
@@ -351,8 +384,9 @@ GradShape grad_shape(int64_t tokens, int64_t width)
     else if (vecs <= 512) s = {5, 1, 0}, resident = grad_resident(256, 2);
     else if (vecs <= 768) s = {6, 1, 0}, resident = grad_resident(256, 3);
     else if (vecs <= 1024) s = {7, 1, 0}, resident = grad_resident(512, 2);
-    else if (vecs <= 2048) s = {8, 1, 0}, resident = grad_resident(1024, 2);
-    else s = {9, 1, 0}, resident = grad_resident(1024, 4);
+    else if (vecs <= 1536) s = {8, 1, 0}, resident = grad_resident(512, 3);
+    else if (vecs <= 2048) s = {9, 1, 0}, resident = grad_resident(512, 4);
+    else s = {10, 1, 0}, resident = grad_resident(1024, 4);
     const int64_t want = (tokens + s.rows - 1) / s.rows;
     s.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, resident * GRAD_SMS)));
     return s;
@@ -360,9 +394,11 @@ GradShape grad_shape(int64_t tokens, int64_t width)
 
 cudaError_t launch_norm_grad(const NormGradParams& p, const GradShape& s, cudaStream_t stream)
 {
-    auto go = [&](auto kernel, int threads) {
+    auto go = [&](auto kernel, int threads, unsigned smem = 0) {
+        const cudaError_t e = smem ? ensure_smem_limit(kernel, smem) : cudaSuccess;
+        if (e != cudaSuccess) return e;
         return launch_dependent(kernel, dim3(static_cast<unsigned>(s.ctas)),
-                                dim3(static_cast<unsigned>(threads)), 0, 1, stream, p);
+                                dim3(static_cast<unsigned>(threads)), smem, 1, stream, p);
     };
     switch (s.config) {
     case 0: return go(k_rms_norm_grad<16, 1, 256>, 256);
@@ -373,8 +409,9 @@ cudaError_t launch_norm_grad(const NormGradParams& p, const GradShape& s, cudaSt
     case 5: return go(k_rms_norm_grad<256, 2, 256>, 256);
     case 6: return go(k_rms_norm_grad<256, 3, 256>, 256);
     case 7: return go(k_rms_norm_grad<512, 2, 512>, 512);
-    case 8: return go(k_rms_norm_grad<1024, 2, 1024>, 1024);
-    default: return go(k_rms_norm_grad<1024, 4, 1024>, 1024);
+    case 8: return go(k_rms_norm_grad<512, 3, 512, true>, 512, 3 * 3 * 512 * 16);
+    case 9: return go(k_rms_norm_grad<512, 4, 512, true>, 512, 4 * 3 * 512 * 16);
+    default: return go(k_rms_norm_grad<1024, 4, 1024, true>, 1024, 4 * 3 * 1024 * 16);
     }
 }
 
