@@ -96,6 +96,34 @@ def test_norm(tokens, width, residual):
                     torch.equal(a, b) for a, b in zip(alone[2].to_codes(), Q.to_codes()))
 
 
+@pytest.mark.parametrize("width", [
+    64, 200, 384, 504, 640, 760, 1000, 1184, 1512, 1968, 2552, 2960, 4088, 4960, 6136, 8000,
+    10000, 12240, 16384, 20000])
+def test_many_tokens(width):
+    """Enough rows for the shapes that long batches take: the rows repeat 37 different ones,
+    whose results are compared with 64 bits and must be the same wherever they stand."""
+    import torch
+
+    import tma_pipelined_tensor_fp16_gb300 as tg
+    tokens, distinct = 152 * 2048 * 8 // width + 131, 37
+    x, r, w = _inputs(np.random.default_rng(width), distinct, width)
+    h = x.astype(np.float64) + r
+    z = _norm(h, w)
+    index = torch.arange(tokens, device="cuda") % distinct
+    X, R, W = device(x)[index], device(r)[index], device(w)
+    for format in FORMATS:
+        Z, H, Q = tg.rms_norm(X, W, residual=R, eps=EPS, format=format)
+        assert torch.equal(Z, Z[:distinct][index]) and torch.equal(H, H[:distinct][index])
+        assert np.array_equal(H[:distinct].cpu().numpy(), h.astype(np.float16))
+        tol = _z_error(width) * np.abs(z) + 2.0 ** -11 * np.abs(z) + 2.0 ** -25
+        assert_within(Z[:distinct].cpu().numpy(), z, tol, "Z")
+        if format is not None:
+            parts = Q.to_codes()
+            assert all(torch.equal(t, t[:distinct][index]) for t in parts)
+            _check_codes(tg.MXTensor.from_codes(*(t[:distinct].contiguous() for t in parts),
+                                                width, format), z, width)
+
+
 def test_zero_rows_tiny_rows_and_infinities():
     import torch
 

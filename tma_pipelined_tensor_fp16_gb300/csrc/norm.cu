@@ -1,10 +1,11 @@
 // norm.cu -- root-mean-square norm with the residual's addition and quantised rows, and
 // its gradient.  Bound by memory: every value is read once and written once per output.
-// Measured on 67 M values, residual, fp16 and mxfp8 rows: 92 to 97 us for widths from 128 to
-// 16384, 6.2 to 6.6 TB/s; gradient with the residual's: 87 to 97 us for widths from 128 to 8192,
+// Measured on 67 M values, residual, fp16 and mxfp8 rows: 88 to 101 us for widths from 128 to
+// 16384, 6.0 to 6.8 TB/s; nvfp4 rows alone 46 to 71; gradient with the residual's: 87 to 97 us for widths from 128 to 8192,
 // 5.5 to 6.2 TB/s, 100 to 106 to 16384, 129 at 32768.  16 rows of 4096: 2.3 us.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/tmalayer.h"
 #include "device_common.cuh"
@@ -78,8 +79,7 @@ __device__ __forceinline__ float row_sum(float s, float* shared)
 }
 
 // A row by LANES lanes (half a warp, a warp, or all of the CTA), VEC vectors of eight values
-// per lane,
-// held in registers between the sum of squares and the outputs.
+// per lane, held in registers between the sum of squares and the outputs.
 template <int FORMAT, int LANES, int VEC, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_rms_norm(const __grid_constant__ NormParams p)
 {
@@ -146,21 +146,52 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t stream)
     if constexpr (FORMAT >= 0)
         padded = std::max<int64_t>(p.chunks * mx_chunk(FORMAT), p.groups * mx_group(FORMAT));
     const int64_t vecs = (padded + 7) / 8;
-    auto go = [&](auto kernel, int rows_per_cta, int threads) {
-        const int64_t grid = (p.tokens + rows_per_cta - 1) / rows_per_cta;
-        return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)),
-                                dim3(static_cast<unsigned>(threads)), 0, 1, stream, p);
+    auto go = [&](auto lanes, auto vec) {
+        constexpr int LANES = decltype(lanes)::value;
+        constexpr int THREADS = LANES <= 32 ? 256 : LANES;
+        constexpr int ROWS = THREADS / LANES;
+        const int64_t grid = (p.tokens + ROWS - 1) / ROWS;
+        return launch_dependent(k_rms_norm<FORMAT, LANES, decltype(vec)::value, THREADS>,
+                                dim3(static_cast<unsigned>(grid)), dim3(THREADS), 0, 1, stream, p);
     };
-    // up to 128 values half a warp holds a row, up to 1024 a warp
-    if (vecs <= 16) return go(k_rms_norm<FORMAT, 16, 1, 256>, 16, 256);
-    if (vecs <= 32) return go(k_rms_norm<FORMAT, 32, 1, 256>, 8, 256);
-    if (vecs <= 64) return go(k_rms_norm<FORMAT, 32, 2, 256>, 8, 256);
-    if (vecs <= 128) return go(k_rms_norm<FORMAT, 32, 4, 256>, 8, 256);
-    if (vecs <= 256) return go(k_rms_norm<FORMAT, 256, 1, 256>, 1, 256);
-    if (vecs <= 512) return go(k_rms_norm<FORMAT, 256, 2, 256>, 1, 256);
-    if (vecs <= 1024) return go(k_rms_norm<FORMAT, 256, 4, 256>, 1, 256);
-    if (vecs <= 2048) return go(k_rms_norm<FORMAT, 512, 4, 512>, 1, 512);
-    return go(k_rms_norm<FORMAT, 1024, 4, 1024>, 1, 1024);
+#define TG_NORM(lanes, vec) \
+    go(std::integral_constant<int, lanes>{}, std::integral_constant<int, vec>{})
+    // As long as the GPU (152 SMs) can hold a thread for every vector, a row is done soonest by
+    // as many lanes (16 x 4096, fp16 and mxfp8: 512 lanes 2.6 us, 128 lanes 3.3; 16 x 1024: 128
+    // lanes 2.05, 32 lanes 3.5).
+    if (vecs <= 16) return TG_NORM(16, 1);
+    if (p.tokens * vecs <= 152 * 2048) {
+        if (vecs <= 32) return TG_NORM(32, 1);
+        if (vecs <= 64) return TG_NORM(32, 2);
+        if (vecs <= 128) return TG_NORM(128, 1);
+        if (vecs <= 256) return TG_NORM(256, 1);
+        if (vecs <= 512) return TG_NORM(512, 1);
+        if (vecs <= 1024) return TG_NORM(1024, 1);
+    }
+    // Beyond, few lanes with four to six vectors each: fewer reductions, and hardly a lane
+    // without values, whose codes would cost as much as another's (67 M values to nvfp4 alone, 1528
+    // wide: 32 lanes of six 50 us, 256 of one 87; 5120 wide: 128 of five 46, 256 of four 68).
+    if (vecs <= 32) return TG_NORM(16, 2);
+    if (vecs <= 48) return TG_NORM(16, 3);
+    if (vecs <= 64) return TG_NORM(16, 4);
+    if (vecs <= 80) return TG_NORM(16, 5);
+    if (vecs <= 96) return TG_NORM(32, 3);
+    if (vecs <= 128) return TG_NORM(32, 4);
+    if (vecs <= 160) return TG_NORM(32, 5);
+    if (vecs <= 192) return TG_NORM(32, 6);
+    if (vecs <= 256) return TG_NORM(64, 4);
+    if (vecs <= 320) return TG_NORM(64, 5);
+    if (vecs <= 384) return TG_NORM(64, 6);
+    if (vecs <= 512) return TG_NORM(128, 4);
+    if (vecs <= 640) return TG_NORM(128, 5);
+    if (vecs <= 768) return TG_NORM(128, 6);
+    if (vecs <= 1024) return TG_NORM(256, 4);
+    if (vecs <= 1280) return TG_NORM(256, 5);
+    if (vecs <= 1536) return TG_NORM(256, 6);
+    if (vecs <= 2048) return TG_NORM(512, 4);
+    if (vecs <= 2560) return TG_NORM(512, 5);
+    return TG_NORM(1024, 4);
+#undef TG_NORM
 }
 
 // ------------------------------------------------------------------ gradient
