@@ -25,7 +25,8 @@ extern "C" {
  *           for GEMM_NVFP4 with the tensor scale 1, which suits values of this size:
  *           blocks of magnitudes from 0.1 to 2688 keep all bits of their scale
  * X, residual, weight (width values) are fp16.  width is a multiple of 8, 8 <= width <=
- * 32768; tokens >= 0; eps >= 0.  A row of zeros gives zeros (with eps = 0: NaN). */
+ * 32768; tokens >= 0; eps >= 0.  A row of zeros gives zeros (with eps = 0: NaN).  A row's
+ * results do not depend on the other rows, nor on how many there are. */
 TMAGEMM_API int gemm_rms_norm(int64_t tokens, int64_t width, const void* X, const void* residual,
                               const void* weight, float eps, void* total, void* Z, int format,
                               void* codes, void* scales, void* cuda_stream);
@@ -36,7 +37,8 @@ TMAGEMM_API int gemm_rms_norm(int64_t tokens, int64_t width, const void* X, cons
  *                                          u = dZ weight
  * (fp16; the gradient of X and of residual alike; may be dZ or dH itself) and
  *   dweight = sum over the tokens of dZ n      (fp32).
- * The quantised rows count as z.  The workspace is this call's alone until it has run. */
+ * The quantised rows count as z.  A row of dX does not depend on the other rows.  The
+ * workspace is this call's alone until it has run. */
 TMAGEMM_API int64_t gemm_rms_norm_grad_workspace(int64_t tokens, int64_t width); /* bytes */
 TMAGEMM_API int gemm_rms_norm_grad(int64_t tokens, int64_t width, const void* dZ, const void* H,
                                    const void* weight, const void* dH, float eps, void* dX,

@@ -117,11 +117,25 @@ def test_many_tokens(width):
         assert np.array_equal(H[:distinct].cpu().numpy(), h.astype(np.float16))
         tol = _z_error(width) * np.abs(z) + 2.0 ** -11 * np.abs(z) + 2.0 ** -25
         assert_within(Z[:distinct].cpu().numpy(), z, tol, "Z")
+        few = tg.rms_norm(X[:distinct], W, residual=R[:distinct], eps=EPS, format=format)
+        assert torch.equal(few[0], Z[:distinct])
         if format is not None:
             parts = Q.to_codes()
             assert all(torch.equal(t, t[:distinct][index]) for t in parts)
+            assert all(torch.equal(t[:distinct], f) for t, f in zip(parts, few[2].to_codes()))
             _check_codes(tg.MXTensor.from_codes(*(t[:distinct].contiguous() for t in parts),
                                                 width, format), z, width)
+
+
+@pytest.mark.parametrize("width", [72, 384, 640, 1024, 1528, 2048, 3000, 5120, 9472, 16384])
+def test_a_rows_gradient_does_not_depend_on_the_others(width):
+    import torch
+
+    import tma_pipelined_tensor_fp16_gb300 as tg
+    h, dz, w = (device(a) for a in _inputs(np.random.default_rng(width), 3000, width))
+    dX, _ = tg.rms_norm_grad(dz, h, w, dH=h)
+    for few in (1, 5, 300):
+        assert torch.equal(tg.rms_norm_grad(dz[:few], h[:few], w, dH=h[:few])[0], dX[:few])
 
 
 def test_zero_rows_tiny_rows_and_infinities():

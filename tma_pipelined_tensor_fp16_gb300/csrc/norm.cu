@@ -1,11 +1,13 @@
 // norm.cu -- root-mean-square norm with the residual's addition and quantised rows, and
 // its gradient.  Bound by memory: every value is read once and written once per output.
 // Measured on 67 M values, residual, fp16 and mxfp8 rows: 88 to 101 us for widths from 128 to
-// 16384, 6.0 to 6.8 TB/s; nvfp4 rows alone 46 to 71; gradient with the residual's: 87 to 97 us for widths from 128 to 8192,
-// 5.5 to 6.2 TB/s, 100 to 106 to 16384, 129 at 32768.  16 rows of 4096: 2.3 us.
+// 16384, 6.0 to 6.8 TB/s; nvfp4 rows alone 47 to 71; gradient with the residual's: 85 to 92 us
+// for widths from 128 to 8192, 5.8 to 6.3 TB/s, 100 to 106 to 16384, 129 at 32768.
+// 16 rows of 4096: 2.5 us.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
+#include <utility>
 
 #include "../../include/tmalayer.h"
 #include "device_common.cuh"
@@ -64,18 +66,39 @@ __device__ __forceinline__ float warp_sum(float s)
     return s;
 }
 
-// Sum over the LANES lanes of a row: part of a warp, a warp, or the whole CTA.
-template <int LANES>
-__device__ __forceinline__ float row_sum(float s, float* shared)
+// The sum of a row's vectors, whose sums are `v` (vector i * LANES + lane), in an order that does
+// not depend on LANES and VEC, so that a row's result does not depend on how many others there
+// are: every 1024th vector in turn, and those 1024 sums in a tree from the highest bit of their
+// number down.
+template <int LANES, int VEC>
+__device__ __forceinline__ float row_sum(const float (&v)[VEC], float* shared)
 {
-    if constexpr (LANES <= 32) return warp_sum<LANES>(s);
-    s = warp_sum(s);
-    if (lane_id() == 0) shared[threadIdx.x / 32] = s;
-    __syncthreads();
-    s = 0.0f;
+    constexpr int MINE = 1024 / LANES;  // of the 1024 sums, this lane's
+    constexpr int LIVE = VEC < MINE ? VEC : MINE;
+    float s[LIVE];
 #pragma unroll
-    for (int i = 0; i < LANES / 32; ++i) s += shared[i];
-    return s;
+    for (int i = 0; i < LIVE; ++i) s[i] = v[i];
+#pragma unroll
+    for (int i = LIVE; i < VEC; ++i) s[i % MINE] += v[i];
+#pragma unroll
+    for (int n = MINE / 2; n > 0; n /= 2)
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            if (i + n < LIVE) s[i] += s[i + n];
+    if constexpr (LANES <= 32) {
+        return warp_sum<LANES>(s[0]);
+    } else {
+        shared[threadIdx.x] = s[0];
+        __syncthreads();
+        float t[LANES / 32];
+#pragma unroll
+        for (int i = 0; i < LANES / 32; ++i) t[i] = shared[i * 32 + lane_id()];
+#pragma unroll
+        for (int n = LANES / 64; n > 0; n /= 2)
+#pragma unroll
+            for (int i = 0; i < n; ++i) t[i] += t[i + n];
+        return warp_sum(t[0]);
+    }
 }
 
 // A row by LANES lanes (half a warp, a warp, or all of the CTA), VEC vectors of eight values
@@ -84,36 +107,42 @@ template <int FORMAT, int LANES, int VEC, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_rms_norm(const __grid_constant__ NormParams p)
 {
     constexpr int ROWS = THREADS / LANES;  // per CTA
-    __shared__ float shared[THREADS / 32];
+    __shared__ float shared[LANES];
     const int lane = static_cast<int>(threadIdx.x) % LANES;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / LANES;
     const bool valid = row < p.tokens;
     griddep_wait();
     griddep_launch_dependents();
     if (!__any_sync(0xffffffffu, valid)) return;  // a warp stays together for its shuffles
-    float h[VEC][8];
-    float sum = 0.0f;
+    uint4 x[VEC], r[VEC];  // all on their way before the first is used
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
         const int k = (i * LANES + lane) * 8;
-        uint4 x = make_uint4(0, 0, 0, 0), r = make_uint4(0, 0, 0, 0);
+        x[i] = r[i] = make_uint4(0, 0, 0, 0);
         if (valid && k < p.width) {
-            x = *reinterpret_cast<const uint4*>(p.X + row * p.width + k);
-            if (p.residual) r = *reinterpret_cast<const uint4*>(p.residual + row * p.width + k);
+            x[i] = *reinterpret_cast<const uint4*>(p.X + row * p.width + k);
+            if (p.residual) r[i] = *reinterpret_cast<const uint4*>(p.residual + row * p.width + k);
         }
-        widen8(x, h[i]);
+    }
+    float h[VEC][8];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        widen8(x[i], h[i]);
         if (p.residual) {
             float f[8];
-            widen8(r, f);
+            widen8(r[i], f);
 #pragma unroll
             for (int j = 0; j < 8; ++j) h[i][j] += f[j];
         }
     }
+    float squares[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i)
+    for (int i = 0; i < VEC; ++i) {
+        squares[i] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fmaf(h[i][j], h[i][j], sum);
-    sum = row_sum<LANES>(sum, shared);
+        for (int j = 0; j < 8; ++j) squares[i] = fmaf(h[i][j], h[i][j], squares[i]);
+    }
+    const float sum = row_sum<LANES, VEC>(squares, shared);
     const float rstd = 1.0f / sqrtf(fmaf(sum, p.inv_width, p.eps));
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
@@ -157,8 +186,8 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t stream)
 #define TG_NORM(lanes, vec) \
     go(std::integral_constant<int, lanes>{}, std::integral_constant<int, vec>{})
     // As long as the GPU (152 SMs) can hold a thread for every vector, a row is done soonest by
-    // as many lanes (16 x 4096, fp16 and mxfp8: 512 lanes 2.6 us, 128 lanes 3.3; 16 x 1024: 128
-    // lanes 2.05, 32 lanes 3.5).
+    // about as many lanes (16 x 4096, fp16 and mxfp8: 512 lanes 2.6 us, 128 lanes 3.3; 16 x 1024:
+    // 128 lanes 2.05, 32 lanes 3.5).
     if (vecs <= 16) return TG_NORM(16, 1);
     if (p.tokens * vecs <= 152 * 2048) {
         if (vecs <= 32) return TG_NORM(32, 1);
@@ -166,11 +195,11 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t stream)
         if (vecs <= 128) return TG_NORM(128, 1);
         if (vecs <= 256) return TG_NORM(256, 1);
         if (vecs <= 512) return TG_NORM(512, 1);
-        if (vecs <= 1024) return TG_NORM(1024, 1);
+        if (vecs <= 1024) return TG_NORM(512, 2);
     }
     // Beyond, few lanes with four to six vectors each: fewer reductions, and hardly a lane
     // without values, whose codes would cost as much as another's (67 M values to nvfp4 alone, 1528
-    // wide: 32 lanes of six 50 us, 256 of one 87; 5120 wide: 128 of five 46, 256 of four 68).
+    // wide: 32 lanes of six 51 us, 256 of one 87; 5120 wide: 128 of five 47, 256 of four 68).
     if (vecs <= 32) return TG_NORM(16, 2);
     if (vecs <= 48) return TG_NORM(16, 3);
     if (vecs <= 64) return TG_NORM(16, 4);
@@ -209,17 +238,35 @@ struct NormGradParams {
 };
 
 
-// CTAs on an SM, which the registers are held to.  Several of them cover each other's
-// reductions better than one that reads a row ahead (16384 x 4096 with dH: four CTAs 87 us,
-// three with a row ahead 96; 8192 x 8192: two 92, one 125).
-constexpr int grad_resident(int lanes, int vec)
-{
-    return lanes <= 32   ? (vec == 1 ? 5 : 4)
-           : lanes == 128 ? 10
-           : lanes == 256 ? 6 - vec
-           : lanes == 512 ? 2
-                          : 1;
-}
+// How rows are held: by `lanes` lanes with `vec` vectors of eight values each; CTAs of `threads`
+// threads, `resident` of them on an SM, which the registers are held to.  Several CTAs cover each
+// other's reductions better than one that reads a row ahead (16384 x 4096 with dH: four 87 us,
+// three with a row ahead 96).
+//
+// staged: a row waits in shared memory instead of registers, every thread's vectors at places
+// of its own, which the next row's take as soon as the last reading is over.  For rows whose
+// registers would leave room for one CTA on an SM only (67 M values, 9472 wide: 104 us, in
+// registers 146; 16384 wide 105, 111; 32768 wide 129, 170, with spills).  Shorter rows are faster
+// in registers (4096 wide 87, staged 92; 8192 wide 92, 99).
+struct GradConfig {
+    int lanes, vec, threads, resident;
+    bool staged;
+};
+
+// A row takes the first that holds it, however many rows there are, so dX does not depend on
+// the other rows (a vector a lane would be faster for few: 77 x 4096 5.1 us, 5.6): two to four vectors a lane, hardly a lane without any, and
+// a few groups of lanes in a CTA, which write one part of dweight (640 wide: 32 lanes of three 90
+// us, 128 of one 119; 1528 wide: 64 of three 90, 256 of one 110; 1000 rows of 1024: 64 lanes of
+// two, four groups a CTA, 6.4 us, 128 of one and a CTA for each 8.0).
+constexpr GradConfig GRAD[] = {
+    {16, 1, 256, 6, false},  {32, 1, 256, 5, false},  {16, 3, 256, 3, false},
+    {32, 2, 256, 4, false},  {32, 3, 256, 3, false},  {64, 2, 256, 4, false},
+    {64, 3, 256, 3, false},  {128, 2, 256, 4, false}, {160, 2, 160, 6, false},
+    {128, 3, 128, 6, false}, {256, 2, 256, 4, false}, {160, 4, 160, 4, false},
+    {256, 3, 256, 3, false}, {512, 2, 512, 2, false}, {512, 3, 512, 2, true},
+    {512, 4, 512, 2, true},  {1024, 4, 1024, 1, true},
+};
+constexpr int GRAD_CONFIGS = static_cast<int>(sizeof(GRAD) / sizeof(GRAD[0]));
 
 // 16 bytes to a thread's own place in shared memory, without a register on the way.
 __device__ __forceinline__ void copy_ahead(uint4* to, const __half* from)
@@ -233,13 +280,8 @@ __device__ __forceinline__ void copy_ahead(uint4* to, const __half* from)
 // Rows as in k_rms_norm, each group of LANES lanes taking every stride-th row; a lane's
 // columns stay the same, so their sums over its rows stay in registers and are written
 // once as the group's part of dweight.
-// STAGED: a row waits in shared memory instead of registers, every thread's vectors at places
-// of its own, which the next row's take as soon as the last reading is over.  For rows whose
-// registers would leave room for one CTA on an SM only (67 M values, 9472 wide: 104 us, in
-// registers 146; 16384 wide 105, 111; 32768 wide 129, 170, with spills).  Shorter rows are faster
-// in registers (4096 wide 87, staged 92; 8192 wide 92, 99).
-template <int LANES, int VEC, int THREADS, bool STAGED = false>
-__global__ void __launch_bounds__(THREADS, grad_resident(LANES, VEC))
+template <int LANES, int VEC, int THREADS, int RESIDENT, bool STAGED>
+__global__ void __launch_bounds__(THREADS, RESIDENT)
     k_rms_norm_grad(const __grid_constant__ NormGradParams p)
 {
     extern __shared__ uint4 staged[];  // STAGED: [VEC][h, dz, dh][THREADS]
@@ -302,10 +344,14 @@ __global__ void __launch_bounds__(THREADS, grad_resident(LANES, VEC))
         s.x = warp_sum<LANES < 32 ? LANES : 32>(s.x);
         s.y = warp_sum<LANES < 32 ? LANES : 32>(s.y);
         if constexpr (LANES > 32) {
-            float2* slots = shared[turn & 1];
+            const int mine = static_cast<int>(threadIdx.x) / LANES;  // groups differ in their rows
+            float2* slots = shared[turn & 1] + mine * (LANES / 32);
             ++turn;
-            if (lane_id() == 0) slots[threadIdx.x / 32] = s;
-            __syncthreads();
+            if (lane_id() == 0) slots[lane / 32] = s;
+            if constexpr (LANES < THREADS)
+                named_bar_sync(1 + mine, LANES);
+            else
+                __syncthreads();
             s = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int i = 0; i < LANES / 32; ++i) {
@@ -392,11 +438,9 @@ __global__ void __launch_bounds__(1024) k_rms_norm_weight(const float* parts, in
     if (lane == 0 && column < width) dweight[column] = s;
 }
 
-// How many parts dweight has: rows per CTA and CTAs, by the width.
+// Which configuration, and how many CTAs: each has a part of dweight.
 struct GradShape {
-    int config;
-    int rows;  // per CTA
-    int ctas;
+    int config, ctas;
 };
 
 // Independent of the device (GB300 has 152 SMs), so that the workspace is known without one.
@@ -405,45 +449,39 @@ constexpr int GRAD_SMS = 152;
 GradShape grad_shape(int64_t tokens, int64_t width)
 {
     const int64_t vecs = (width + 7) / 8;
-    GradShape s;
-    int resident;
-    if (vecs <= 16) s = {0, 16, 0}, resident = grad_resident(16, 1);
-    else if (vecs <= 32) s = {1, 8, 0}, resident = grad_resident(32, 1);
-    else if (vecs <= 64) s = {2, 8, 0}, resident = grad_resident(32, 2);
-    else if (vecs <= 128) s = {3, 1, 0}, resident = grad_resident(128, 1);
-    else if (vecs <= 256) s = {4, 1, 0}, resident = grad_resident(256, 1);
-    else if (vecs <= 512) s = {5, 1, 0}, resident = grad_resident(256, 2);
-    else if (vecs <= 768) s = {6, 1, 0}, resident = grad_resident(256, 3);
-    else if (vecs <= 1024) s = {7, 1, 0}, resident = grad_resident(512, 2);
-    else if (vecs <= 1536) s = {8, 1, 0}, resident = grad_resident(512, 3);
-    else if (vecs <= 2048) s = {9, 1, 0}, resident = grad_resident(512, 4);
-    else s = {10, 1, 0}, resident = grad_resident(1024, 4);
-    const int64_t want = (tokens + s.rows - 1) / s.rows;
-    s.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, resident * GRAD_SMS)));
+    GradShape s = {0, 0};
+    while (GRAD[s.config].lanes * GRAD[s.config].vec < vecs) ++s.config;
+    const GradConfig& c = GRAD[s.config];
+    const int64_t rows = c.threads / c.lanes;
+    s.ctas = static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>((tokens + rows - 1) / rows, c.resident * GRAD_SMS)));
     return s;
+}
+
+template <int I>
+cudaError_t launch_grad_config(const NormGradParams& p, int ctas, cudaStream_t stream)
+{
+    constexpr GradConfig c = GRAD[I];
+    constexpr unsigned smem = c.staged ? c.vec * 3 * c.threads * 16 : 0;
+    auto kernel = k_rms_norm_grad<c.lanes, c.vec, c.threads, c.resident, c.staged>;
+    const cudaError_t e = c.staged ? ensure_smem_limit(kernel, smem) : cudaSuccess;
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), dim3(c.threads), smem, 1,
+                            stream, p);
+}
+
+template <int... I>
+cudaError_t launch_norm_grad(const NormGradParams& p, const GradShape& s, cudaStream_t stream,
+                             std::integer_sequence<int, I...>)
+{
+    cudaError_t e = cudaErrorInvalidValue;
+    ((s.config == I ? void(e = launch_grad_config<I>(p, s.ctas, stream)) : void()), ...);
+    return e;
 }
 
 cudaError_t launch_norm_grad(const NormGradParams& p, const GradShape& s, cudaStream_t stream)
 {
-    auto go = [&](auto kernel, int threads, unsigned smem = 0) {
-        const cudaError_t e = smem ? ensure_smem_limit(kernel, smem) : cudaSuccess;
-        if (e != cudaSuccess) return e;
-        return launch_dependent(kernel, dim3(static_cast<unsigned>(s.ctas)),
-                                dim3(static_cast<unsigned>(threads)), smem, 1, stream, p);
-    };
-    switch (s.config) {
-    case 0: return go(k_rms_norm_grad<16, 1, 256>, 256);
-    case 1: return go(k_rms_norm_grad<32, 1, 256>, 256);
-    case 2: return go(k_rms_norm_grad<32, 2, 256>, 256);
-    case 3: return go(k_rms_norm_grad<128, 1, 128>, 128);
-    case 4: return go(k_rms_norm_grad<256, 1, 256>, 256);
-    case 5: return go(k_rms_norm_grad<256, 2, 256>, 256);
-    case 6: return go(k_rms_norm_grad<256, 3, 256>, 256);
-    case 7: return go(k_rms_norm_grad<512, 2, 512>, 512);
-    case 8: return go(k_rms_norm_grad<512, 3, 512, true>, 512, 3 * 3 * 512 * 16);
-    case 9: return go(k_rms_norm_grad<512, 4, 512, true>, 512, 4 * 3 * 512 * 16);
-    default: return go(k_rms_norm_grad<1024, 4, 1024, true>, 1024, 4 * 3 * 1024 * 16);
-    }
+    return launch_norm_grad(p, s, stream, std::make_integer_sequence<int, GRAD_CONFIGS>{});
 }
 
 int check_norm(int64_t tokens, int64_t width, float eps)

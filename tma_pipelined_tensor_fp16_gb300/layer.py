@@ -35,7 +35,8 @@ def rms_norm(X, weight, residual=None, eps=1e-6, half=True, format=None, out=Non
 
     Z is z in fp16 (`out` or a new tensor; None with half=False), H is h in fp16 (`total`,
     which may be X or residual itself, or a new tensor; X itself without a residual) and Q is
-    z as an MXTensor of `format` (None without; nvfp4 with the tensor scale 1)."""
+    z as an MXTensor of `format` (None without; nvfp4 with the tensor scale 1).  A row's
+    results do not depend on the other rows, nor on how many there are."""
     torch = _torch()
     f16 = torch.float16
     shape = _matrix("X", X)
