@@ -225,3 +225,29 @@ def test_offsets_past_32_bits(transpose):
         assert int((V[:-want.shape[0]] != 0).sum()) == 0
         assert int((V[:, :-want.shape[1]] != 0).sum()) == 0
         del V, Q
+
+
+@pytest.mark.parametrize("format", ["mxfp8", "mxfp4", "nvfp4"])
+@pytest.mark.parametrize("width", [256, 260, 289])
+def test_values_of_every_code_and_scale(format, width):
+    """fp16 values are the exact products, rounded once: those that fp32 holds.  The rows' lengths
+    let them start anywhere."""
+    import torch
+
+    import tma_pipelined_tensor_fp16_gb300 as tg
+    rng = np.random.default_rng(width)
+    rows, per = 256, 1 if format == "mxfp8" else 2
+    block = 16 if format == "nvfp4" else 32
+    codes = torch.from_numpy(np.stack([rng.permutation(256) for _ in range(rows)] * 2, 1)
+                             .reshape(rows, 512)[:, :-(-width // per)].astype(np.uint8)).cuda()
+    scales = torch.arange(rows, device="cuda").to(torch.uint8)[:, None].repeat(1, -(-width // block))
+    scales[:, 1::2] = scales[:, 1::2] ^ 1
+    for t in [None] if format != "nvfp4" else [2.0 ** -126, 2.0 ** -16, 2.0 ** -15, 2.0 ** -9, 1.0,
+                                               2.0 ** 7, 2.0 ** 8, 2.0 ** 100, 0.75]:
+        scale = None if t is None else torch.tensor([t], dtype=torch.float32, device="cuda")
+        Q = tg.MXTensor.from_codes(codes.contiguous(), scales, width, format, scale)
+        full = Q.values(torch.empty(rows, width, device="cuda"))
+        half, want = Q.values(), full.half()
+        same = (half.view(torch.int16) == want.view(torch.int16)) | (half.isnan() & want.isnan())
+        assert bool(same.all()), (t, int((~same).sum()))
+        assert bool((full.isnan() == half.isnan()).all())

@@ -355,24 +355,72 @@ __device__ __forceinline__ void decode8(uint2 q, __half2 (&v)[4])
     for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<__half2*>(&h[i]);
 }
 
+// The scale of a block in fp16, twice, where fp16 holds it: then one multiplication of halves
+// rounds as a product in fp32 that is rounded to fp16 (both round the exact product once).
+// False: the scale needs fp32.
+template <int FORMAT>
+__device__ __forceinline__ bool scale_of_halves(uint32_t byte, float t, uint32_t& scale)
+{
+    if constexpr (FORMAT == NVFP4) {
+        // a multiple of 2^-9 up to 448 (or NaN), times a power of two from 2^-15 to 2^7
+        const uint32_t bits = __float_as_uint(t);
+        if ((bits & 0x7fffffu) || bits < (127u - 15u) << 23 || bits > (127u + 7u) << 23) return false;
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(byte * 0x101u)));
+        const __half2 s = __hmul2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(t));
+        scale = *reinterpret_cast<const uint32_t*>(&s);
+    } else {
+        const uint32_t e = byte - (127u - 15u);  // of a normal half
+        if (e - 1u > 29u) return false;
+        scale = e << 10 | e << 26;
+    }
+    return true;
+}
+
+template <int FORMAT>
+__device__ __forceinline__ float scale_of(uint32_t byte, float t)
+{
+    return FORMAT == NVFP4 ? float_of_e4m3(byte) * t : float_of_e8m0(byte);
+}
+
+__device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+
+// The codes of eight values that start `skew` (0 to 7) before q's, of which `prev` are those in
+// front.
+template <int FORMAT>
+__device__ __forceinline__ uint2 codes_before(uint2 prev, uint2 q, int skew)
+{
+    if constexpr (FORMAT == MXFP8) {
+        const int n = 8 * (skew & 3);
+        const bool far = skew >= 4;
+        const uint32_t a = far ? prev.x : prev.y, b = far ? prev.y : q.x, c = far ? q.x : q.y;
+        return make_uint2(__funnelshift_l(a, b, n), __funnelshift_l(b, c, n));
+    } else {
+        return make_uint2(__funnelshift_l(prev.x, q.x, 4 * skew), 0);
+    }
+}
+
 // A lane decodes eight consecutive values; four lanes 32, eight rows a warp: a warp takes 8
-// rows x 128 (96) values.  With ODD a row's length is
-// no multiple of 8, so that rows start anywhere: the values go through shared memory and
-// leave as aligned words, 64 bytes and more at a time.
+// rows x 128 (96) values.  With ODD a row's length is no multiple of 8, so that rows start
+// anywhere.  To fp32 the values then go through shared memory and leave as aligned words.  To
+// fp16 a lane takes the eight values of an aligned vector of 16 bytes instead, which start up to
+// seven in front of its own codes: it shifts its codes together with its neighbour's, and up to
+// seven values have the scale of the block in front (5000 x 4001 nvfp4 11.4 us; through shared
+// memory 13.8).
 template <int FORMAT, bool F16OUT, bool ODD>
 __global__ void __launch_bounds__(ROW_WARPS * 32)
     k_mx_values(const __grid_constant__ ValuesParams p, uint32_t cta_spans, int k_log)
 {
+    constexpr bool SHIFTED = ODD && F16OUT, STAGED = ODD && !F16OUT;
     int64_t row0, k0;
     row_tile(cta_spans, k_log, row_k(FORMAT), row0, k0);
-    if (row0 >= p.rows || k0 >= p.K) return;
+    if (row0 >= p.rows || k0 >= p.K + (SHIFTED ? 7 : 0)) return;
     griddep_wait();
     griddep_launch_dependents();
     const int lane = static_cast<int>(lane_id());
     constexpr int SPANS = row_spans(FORMAT), ROW_K = row_k(FORMAT);
-    using T = typename std::conditional<F16OUT, __half, float>::type;
-    __shared__ T staged[ODD ? ROW_WARPS : 1][8][ROW_K + 2];
-    T(*rows)[ROW_K + 2] = staged[ODD ? threadIdx.x / 32 : 0];
+    __shared__ float staged[STAGED ? ROW_WARPS : 1][8][ROW_K + 2];
+    float(*rows)[ROW_K + 2] = staged[STAGED ? threadIdx.x / 32 : 0];
     const int64_t row = row0 + lane / 4;
     if (!ODD && row >= p.rows) return;
     const bool valid = row < p.rows;
@@ -382,6 +430,12 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
     const uint8_t* codes = p.codes + mx_code_offset(row, k0 / mx_chunk(FORMAT), p.chunks);
     const uint8_t* scales = p.scales + mx_scale_offset(row, k0 / mx_group(FORMAT), p.groups);
     constexpr int GROUPS = ROW_K / mx_group(FORMAT);
+    const auto codes_at = [](const uint8_t* chunk, int eight) {
+        if constexpr (FORMAT == MXFP8)
+            return reinterpret_cast<const uint2*>(chunk)[eight];
+        else
+            return make_uint2(reinterpret_cast<const uint32_t*>(chunk)[eight], 0);
+    };
     uint32_t words[GROUPS];
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g)
@@ -394,99 +448,114 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
         const int64_t k = k0 + j * 32 + part * 8;
         const int chunk = (j * 4 + part) / PER_CHUNK;
         q[j] = make_uint2(0, 0);
-        if (valid && k < p.K) {
-            if constexpr (FORMAT == MXFP8)
-                q[j] = reinterpret_cast<const uint2*>(codes + chunk * MX_CHUNK_BYTES)[part % PER_CHUNK];
-            else
-                q[j].x =
-                    reinterpret_cast<const uint32_t*>(codes + chunk * MX_CHUNK_BYTES)[part % PER_CHUNK];
+        if (valid && k < p.K) q[j] = codes_at(codes + chunk * MX_CHUNK_BYTES, part % PER_CHUNK);
+    }
+    const auto byte_of = [&](int block) { return (words[block / 4] >> (8 * (block % 4))) & 0xffu; };
+    const auto block_of = [&](int j) { return FORMAT == NVFP4 ? j * 2 + part / 2 : j; };
+    if constexpr (SHIFTED) {
+        __half* to = static_cast<__half*>(p.values) + row * p.K;
+        const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(to) >> 1) & 7;
+        uint2 front = make_uint2(0, 0);  // of the eight values in front of the tile
+        uint32_t front_byte = byte_of(0);
+        if (part == 0 && valid && k0 > 0) {
+            constexpr int LAST = mx_group_blocks(FORMAT) - 1;
+            front = codes_at(codes - MX_CHUNK_BYTES, PER_CHUNK - 1);
+            front_byte = scales[LAST - MX_GROUP_BYTES];
+        }
+        // of a pair of values, which have the scale in front (the second word's)
+        uint32_t pick[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            pick[i] = 2 * i + 1 < skew ? 0x7654u : 2 * i < skew ? 0x3254u : 0x3210u;
+#pragma unroll
+        for (int j = 0; j < SPANS; ++j) {
+            // the codes of the lane in front; the row's first has them of the span in front
+            const uint2 give = part == 3 && j > 0 ? q[j > 0 ? j - 1 : 0] : q[j];
+            const int from = (lane & ~3) | ((lane + 3) & 3);
+            uint2 prev;
+            prev.x = __shfl_sync(0xffffffffu, give.x, from);
+            prev.y = FORMAT == MXFP8 ? __shfl_sync(0xffffffffu, give.y, from) : 0u;
+            if (j == 0 && part == 0) prev = front;
+            const int block = block_of(j);
+            const bool starts = (part * 8) % mx_block(FORMAT) == 0;  // a block
+            const uint32_t byte = byte_of(block);
+            const uint32_t before = !starts ? byte : block > 0 ? byte_of(max(block - 1, 0)) : front_byte;
+            __half2 v[4];
+            decode8<FORMAT>(codes_before<FORMAT>(prev, q[j], skew), v);
+            uint32_t s = 0, s0 = 0;
+            if (scale_of_halves<FORMAT>(byte, t, s) && scale_of_halves<FORMAT>(before, t, s0)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = __hmul2(v[i], half2_of(__byte_perm(s, s0, pick[i])));
+            } else {
+                const float f = scale_of<FORMAT>(byte, t), f0 = scale_of<FORMAT>(before, t);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 x = __half22float2(v[i]);
+                    v[i] = __floats2half2_rn(x.x * (2 * i < skew ? f0 : f),
+                                             x.y * (2 * i + 1 < skew ? f0 : f));
+                }
+            }
+            const int64_t at = k0 + j * 32 + part * 8 - skew;
+            if (!valid) continue;
+            if (at >= 0 && at + 8 <= p.K) {
+                *reinterpret_cast<uint4*>(to + at) = *reinterpret_cast<const uint4*>(v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (at + e >= 0 && at + e < p.K)
+                        to[at + e] = e & 1 ? __high2half(v[e / 2]) : __low2half(v[e / 2]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < SPANS; ++j) {
+            const int64_t k = k0 + j * 32 + part * 8;
+            if (k >= p.K) break;
+            const uint32_t byte = byte_of(block_of(j));
+            __half2 v[4];
+            decode8<FORMAT>(q[j], v);
+            if constexpr (F16OUT) {
+                uint32_t s = 0;
+                if (scale_of_halves<FORMAT>(byte, t, s)) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = __hmul2(v[i], half2_of(s));
+                } else {
+                    const float f = scale_of<FORMAT>(byte, t);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 x = __half22float2(v[i]);
+                        v[i] = __floats2half2_rn(x.x * f, x.y * f);
+                    }
+                }
+                *reinterpret_cast<uint4*>(static_cast<__half*>(p.values) + row * p.K + k) =
+                    *reinterpret_cast<const uint4*>(v);
+            } else {
+                const float f = scale_of<FORMAT>(byte, t);
+                float2 x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = __half22float2(v[i]);
+                    x[i].x *= f;
+                    x[i].y *= f;
+                }
+                if constexpr (STAGED) {
+                    float2* to = reinterpret_cast<float2*>(&rows[lane / 4][j * 32 + part * 8]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) to[i] = x[i];
+                } else {
+                    float4* to = reinterpret_cast<float4*>(static_cast<float*>(p.values) + row * p.K + k);
+                    to[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+                    to[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+                }
+            }
         }
     }
-#pragma unroll
-    for (int j = 0; j < SPANS; ++j) {
-        const int64_t k = k0 + j * 32 + part * 8;
-        if (k >= p.K) break;
-        float s;
-        if constexpr (FORMAT == NVFP4) {
-            const int b = j * 2 + part / 2;
-            s = float_of_e4m3((words[b / 4] >> (8 * (b % 4))) & 0xffu) * t;
-        } else {
-            s = float_of_e8m0((words[0] >> (8 * j)) & 0xffu);
-        }
-        __half2 v[4];
-        decode8<FORMAT>(q[j], v);
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(v[i]);
-            x[2 * i] = f.x * s;
-            x[2 * i + 1] = f.y * s;
-        }
-        if constexpr (ODD) {
-            T* to = &rows[lane / 4][j * 32 + part * 8];
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                if constexpr (F16OUT)
-                    *reinterpret_cast<__half2*>(to + i) = __floats2half2_rn(x[i], x[i + 1]);
-                else
-                    *reinterpret_cast<float2*>(to + i) = make_float2(x[i], x[i + 1]);
-            }
-        } else if constexpr (F16OUT) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            *reinterpret_cast<uint4*>(static_cast<__half*>(p.values) + row * p.K + k) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-            float4* to = reinterpret_cast<float4*>(static_cast<float*>(p.values) + row * p.K + k);
-            to[0] = make_float4(x[0], x[1], x[2], x[3]);
-            to[1] = make_float4(x[4], x[5], x[6], x[7]);
-        }
-    }
-    if constexpr (ODD) {
+    if constexpr (STAGED) {
         __syncwarp();
         const int n = static_cast<int>(min(p.K - k0, static_cast<int64_t>(ROW_K)));
         const int count = static_cast<int>(min(p.rows - row0, static_cast<int64_t>(8)));
-        T* to = static_cast<T*>(p.values) + row0 * p.K + k0;
-        if constexpr (F16OUT) {
-            if (n == ROW_K) {
-                // Word w of a row that starts on an odd element is the second half of word w -
-                // 1 and the first of word w in shared memory; its ends are single elements.
-                const uint32_t odd_row0 = (reinterpret_cast<uintptr_t>(to) >> 1) & 1u;
-                const uint32_t odd_step = static_cast<uint32_t>(p.K) & 1u;
-                constexpr int WORDS = ROW_K / 2;  // 64, 48 of mxfp4
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    if (r >= count) break;  // uniform
-                    const uint32_t* from = reinterpret_cast<const uint32_t*>(rows[r]);
-                    const bool second = lane + 32 < WORDS;
-                    const uint32_t v0 = from[lane];
-                    const uint32_t v1 = second ? from[lane + 32] : 0u;
-                    if (((odd_row0 + static_cast<uint32_t>(r) * odd_step) & 1u) == 0) {
-                        uint32_t* words = reinterpret_cast<uint32_t*>(to);
-                        words[lane] = v0;
-                        if (second) words[lane + 32] = v1;
-                    } else {
-                        uint32_t* words = reinterpret_cast<uint32_t*>(to - 1);
-                        const uint32_t p0 = __shfl_up_sync(0xffffffffu, v0, 1);
-                        uint32_t p1 = __shfl_up_sync(0xffffffffu, v1, 1);
-                        const uint32_t last = __shfl_sync(0xffffffffu, v0, 31);
-                        if (lane == 0) p1 = last;
-                        if (lane > 0)
-                            words[lane] = __byte_perm(p0, v0, 0x5432);
-                        else
-                            to[0] = rows[r][0];
-                        if (second) words[lane + 32] = __byte_perm(p1, v1, 0x5432);
-                        if (lane == 31) to[ROW_K - 1] = rows[r][ROW_K - 1];
-                    }
-                    to += p.K;
-                }
-                return;
-            }
-        }
+        float* to = static_cast<float*>(p.values) + row0 * p.K + k0;
         for (int r = 0; r < count; ++r) {
             for (int e = lane; e < n; e += 32) to[e] = rows[r][e];
             to += p.K;
@@ -625,7 +694,10 @@ int gemm_mx_values(int64_t rows, int64_t K, int format, const void* codes, const
         p.scales = static_cast<const uint8_t*>(scales);
         p.tensor_scale = tensor_scale;
         p.values = values;
-        const RowTiling t = row_tiling(rows, K, format);
+        const bool odd = K % 8 != 0;
+        // shifted vectors reach up to seven values behind the row's end
+        const RowTiling t =
+            row_tiling(rows, odd && dtype_out == GEMM_OUT_F16 ? K + 7 : K, format);
         if (t.grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
         cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
         auto launch = [&](auto f16, auto odd) {
@@ -636,7 +708,6 @@ int gemm_mx_values(int64_t rows, int64_t K, int format, const void* codes, const
         };
         const std::true_type yes;
         const std::false_type no;
-        const bool odd = K % 8 != 0;
         const cudaError_t e = dtype_out == GEMM_OUT_F16 ? odd ? launch(yes, yes) : launch(yes, no)
                               : odd                     ? launch(no, yes)
                                                         : launch(no, no);
