@@ -1,8 +1,10 @@
 """The global gradient norm and clipping against numpy in 64 bits.
 
-The norm is the square root of sums that are fp32 over at most eight squares (each off by
-2^-24, the additions by 2^-24 of partial sums: at most 8 * 2^-24 together) and fp64 beyond:
-off by 4 * 2^-24 of itself, plus its own rounding to fp32.  The factor adds one rounding and
+The norm is the square root of sums that are fp32 over at most 32 squares and fp64 beyond.  Of
+the 32, four (eight of fp16, whose squares are exact) are added in turn and those sums in a tree:
+seven roundings (nine) of partial sums, so at most 7 * 2^-24 (9, only if each partial sum were the
+whole one already; 8 is kept to), and half of it for the norm, plus the norm's own rounding to fp32.
+The factor adds one rounding and
 each value one of its product and one to its type.
 """
 import numpy as np
