@@ -1,7 +1,7 @@
 // mx_quantize.cu -- fp16 matrices to the block-scaled formats of include/tmamicro.h and
 // back.  On paper all are bound by memory: every value is read once (twice where the tensor
 // scale has to be found first) and its codes and scales are written once.  Measured: 16384 x
-// 4096 to mxfp8 31 us, 6.5 TB/s, mxfp4 28, nvfp4 33 (bound by issue slots, 5.2 TB/s); along
+// 4096 to mxfp8 31 us, 6.5 TB/s, mxfp4 28, nvfp4 31 (bound by issue slots, 5.6 TB/s); along
 // columns 33, 30, 35; decoding 31, 27, 27 us, 6.3 to 6.6 TB/s.
 #include <algorithm>
 #include <type_traits>
@@ -133,19 +133,32 @@ __global__ void __launch_bounds__(row_k(FORMAT))
     if (FORMAT == MXFP4 && tid < 32) scale_bytes[tid][3] = 0;
     griddep_wait();
     griddep_launch_dependents();
-    const float t = find_tensor_scale<FORMAT>(p, shared);
-    const float sixth = 1.0f / (6.0f * t);
     const uint32_t y = blockIdx.x / spans;
     const int64_t row0 = static_cast<int64_t>(y) * 32;
     const int64_t k0 = static_cast<int64_t>(blockIdx.x - y * spans) * ROW_K;
+    const auto load = [&](int i) {
+        const int at = i * THREADS + tid;
+        const int64_t row = row0 + at / VECS, k = k0 + at % VECS * 8;
+        return row < p.rows && k < p.K ? *reinterpret_cast<const uint4*>(p.X + row * p.K + k)
+                                       : make_uint4(0, 0, 0, 0);
+    };
+    constexpr int LOADS = 32 * VECS / THREADS;
+    float t = 1.0f;
+    if constexpr (FORMAT == NVFP4) {
+        // the values are on their way while the tensor scale is found (16384 x 4096, given: 31.2
+        // us, 33.1 one after the other)
+        uint4 in[LOADS];
 #pragma unroll
-    for (int i = 0; i < 32 * VECS / THREADS; ++i) {
-        const int at = i * THREADS + tid, line = at / VECS, vec = at % VECS;
-        const int64_t row = row0 + line, k = k0 + vec * 8;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < p.rows && k < p.K) v = *reinterpret_cast<const uint4*>(p.X + row * p.K + k);
-        tile[line][vec] = v;
+        for (int i = 0; i < LOADS; ++i) in[i] = load(i);
+        t = find_tensor_scale<FORMAT>(p, shared);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) tile[(i * THREADS + tid) / VECS][(i * THREADS + tid) % VECS] = in[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            tile[(i * THREADS + tid) / VECS][(i * THREADS + tid) % VECS] = load(i);
     }
+    const float sixth = 1.0f / (6.0f * t);
     __syncthreads();
     const int line = tid % 32, part = tid / 32;  // 32 values of a row
     const int64_t row = row0 + line;
