@@ -31,9 +31,12 @@ struct QuantizeParams {
 
 // ------------------------------------------------------------ tensor scale
 
-// Largest finite magnitude of each CTA's share of `vecs` vectors of eight values.
-// Magnitudes of fp16 compare as their bits; infinities and NaN do not count.
-__global__ void __launch_bounds__(512) k_mx_most(const uint4* X, int64_t vecs, uint32_t* parts)
+// Largest finite magnitude of each CTA's share of `vecs` vectors of eight values: 4096 of them
+// at a time (64 KB).  Magnitudes of fp16 compare as their bits; infinities and NaN do not count.
+// Two CTAs on an SM: there are few parts for every CTA of the quantiser to read.
+constexpr int MOST_THREADS = 1024;
+
+__global__ void __launch_bounds__(MOST_THREADS) k_mx_most(const uint4* X, int64_t vecs, uint32_t* parts)
 {
     griddep_wait();
     griddep_launch_dependents();
@@ -43,12 +46,12 @@ __global__ void __launch_bounds__(512) k_mx_most(const uint4* X, int64_t vecs, u
         if (a < 0x7c00u) most = max(most, a);
         if (b < 0x7c00u) most = max(most, b);
     };
-    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    for (; i + 3 * step < vecs; i += 4 * step) {
+    const int64_t turn = static_cast<int64_t>(gridDim.x) * 4 * MOST_THREADS;
+    int64_t i = static_cast<int64_t>(blockIdx.x) * 4 * MOST_THREADS + threadIdx.x;
+    for (; i + 3 * MOST_THREADS < vecs; i += turn) {
         uint4 v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = X[i + j * step];
+        for (int j = 0; j < 4; ++j) v[j] = X[i + j * MOST_THREADS];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             take(v[j].x);
@@ -57,20 +60,19 @@ __global__ void __launch_bounds__(512) k_mx_most(const uint4* X, int64_t vecs, u
             take(v[j].w);
         }
     }
-    for (; i < vecs; i += step) {
+    for (; i < vecs; i += MOST_THREADS) {  // of the last 4096
         const uint4 v = X[i];
         take(v.x);
         take(v.y);
         take(v.z);
         take(v.w);
     }
-    __shared__ uint32_t warps[16];
+    __shared__ uint32_t warps[MOST_THREADS / 32];
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane_id() == 0) warps[threadIdx.x / 32] = most;
     __syncthreads();
     if (threadIdx.x < 32) {
-        most = threadIdx.x < blockDim.x / 32 ? warps[threadIdx.x] : 0u;
-        most = __reduce_max_sync(0xffffffffu, most);
+        most = __reduce_max_sync(0xffffffffu, warps[threadIdx.x]);
         if (threadIdx.x == 0) {
             const float f = __half2float(__ushort_as_half(static_cast<unsigned short>(most)));
             parts[blockIdx.x] = __float_as_uint(f);
@@ -78,18 +80,29 @@ __global__ void __launch_bounds__(512) k_mx_most(const uint4* X, int64_t vecs, u
     }
 }
 
-// The tensor scale (nvfp4): from the parts, by every CTA for itself, or as given.
-template <int FORMAT>
+// The tensor scale: from the parts, by every CTA for itself, as given, or none.
+enum : int { SCALE_NONE, SCALE_GIVEN, SCALE_FOUND };
+
+template <int SCALE>
 __device__ __forceinline__ float find_tensor_scale(const QuantizeParams& p, uint32_t* shared)
 {
-    if constexpr (FORMAT != NVFP4) return 1.0f;
-    if (p.parts == nullptr) {
+    if constexpr (SCALE == SCALE_NONE) return 1.0f;
+    if constexpr (SCALE == SCALE_GIVEN) {
         const uint32_t e = (__float_as_uint(*p.tensor_scale) >> 23) & 0xffu;
         return power_of_two(static_cast<int>(min(max(e, 1u), 254u)) - 127);
     }
     uint32_t most = 0;
-    for (int i = static_cast<int>(threadIdx.x); i < p.part_count; i += static_cast<int>(blockDim.x))
-        most = max(most, p.parts[i]);
+    for (int i = static_cast<int>(threadIdx.x); i < p.part_count;
+         i += 4 * static_cast<int>(blockDim.x)) {
+        uint32_t v[4];  // on their way together
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int at = i + j * static_cast<int>(blockDim.x);
+            v[j] = at < p.part_count ? p.parts[at] : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) most = max(most, v[j]);
+    }
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane_id() == 0) shared[threadIdx.x / 32] = most;
     __syncthreads();
@@ -120,7 +133,15 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8])
     }
 }
 
-template <int FORMAT>
+// Where the scale was found first, the tiles go from the last to the first: the L2 still holds what
+// the search has read last (16384 x 4096 with the search 55 us, in the other order 61).
+template <int SCALE>
+__device__ __forceinline__ uint32_t tile_number()
+{
+    return SCALE == SCALE_FOUND ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+}
+
+template <int FORMAT, int SCALE>
 __global__ void __launch_bounds__(row_k(FORMAT))
     k_mx_quantize(const __grid_constant__ QuantizeParams p, uint32_t spans)
 {
@@ -133,9 +154,9 @@ __global__ void __launch_bounds__(row_k(FORMAT))
     if (FORMAT == MXFP4 && tid < 32) scale_bytes[tid][3] = 0;
     griddep_wait();
     griddep_launch_dependents();
-    const uint32_t y = blockIdx.x / spans;
+    const uint32_t number = tile_number<SCALE>(), y = number / spans;
     const int64_t row0 = static_cast<int64_t>(y) * 32;
-    const int64_t k0 = static_cast<int64_t>(blockIdx.x - y * spans) * ROW_K;
+    const int64_t k0 = static_cast<int64_t>(number - y * spans) * ROW_K;
     const auto load = [&](int i) {
         const int at = i * THREADS + tid;
         const int64_t row = row0 + at / VECS, k = k0 + at % VECS * 8;
@@ -150,7 +171,7 @@ __global__ void __launch_bounds__(row_k(FORMAT))
         uint4 in[LOADS];
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) in[i] = load(i);
-        t = find_tensor_scale<FORMAT>(p, shared);
+        t = find_tensor_scale<SCALE>(p, shared);
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) tile[(i * THREADS + tid) / VECS][(i * THREADS + tid) % VECS] = in[i];
     } else {
@@ -217,7 +238,7 @@ __global__ void __launch_bounds__(row_k(FORMAT))
 constexpr int COL_COLS = 64;
 TG_HD constexpr int col_threads(int format) { return 32 * row_spans(format); }
 
-template <int FORMAT>
+template <int FORMAT, int SCALE>
 __global__ void __launch_bounds__(col_threads(FORMAT))
     k_mx_quantize_columns(const __grid_constant__ QuantizeParams p, uint32_t col_tiles)
 {
@@ -228,11 +249,11 @@ __global__ void __launch_bounds__(col_threads(FORMAT))
     if (FORMAT == MXFP4 && threadIdx.x < COL_COLS) scale_bytes[threadIdx.x][3] = 0;
     griddep_wait();
     griddep_launch_dependents();
-    const float t = find_tensor_scale<FORMAT>(p, shared);
+    const float t = find_tensor_scale<SCALE>(p, shared);
     const float sixth = 1.0f / (6.0f * t);
     const int tid = static_cast<int>(threadIdx.x);
-    const uint32_t k_tile = blockIdx.x / col_tiles;
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x - k_tile * col_tiles) * COL_COLS;
+    const uint32_t number = tile_number<SCALE>(), k_tile = number / col_tiles;
+    const int64_t c0 = static_cast<int64_t>(number - k_tile * col_tiles) * COL_COLS;
     const int64_t k0 = static_cast<int64_t>(k_tile) * COL_K;
 #pragma unroll
     for (int i = 0; i < COL_K * COL_COLS / 8 / COL_THREADS; ++i) {
@@ -649,11 +670,12 @@ int gemm_mx_quantize(int64_t rows, int64_t K, int format, int transpose, const v
         p.tensor_scale = tensor_scale;
         if (format == NVFP4 && workspace) {
             const int64_t vecs = rows * K / 8;
-            const int64_t want = std::max<int64_t>(1, (vecs + 4 * 512 - 1) / (4 * 512));
-            p.part_count = static_cast<int>(std::min<int64_t>(want, std::min(4 * sms, AMAX_PARTS)));
+            const int64_t want =
+                std::max<int64_t>(1, (vecs + 4 * MOST_THREADS - 1) / (4 * MOST_THREADS));
+            p.part_count = static_cast<int>(std::min<int64_t>(want, std::min(2 * sms, AMAX_PARTS)));
             p.parts = static_cast<const uint32_t*>(workspace);
-            e = launch_dependent(k_mx_most, dim3(static_cast<unsigned>(p.part_count)), dim3(512), 0,
-                                 1, stream, static_cast<const uint4*>(X), vecs,
+            e = launch_dependent(k_mx_most, dim3(static_cast<unsigned>(p.part_count)),
+                                 dim3(MOST_THREADS), 0, 1, stream, static_cast<const uint4*>(X), vecs,
                                  static_cast<uint32_t*>(workspace));
             if (e != cudaSuccess) return cuda_fail("tensor scale launch", e);
         }
@@ -662,16 +684,20 @@ int gemm_mx_quantize(int64_t rows, int64_t K, int format, int transpose, const v
             const int64_t cols = std::max<int64_t>(1, (rows + COL_COLS - 1) / COL_COLS);
             const int64_t grid = cols * ((K + row_k(format) - 1) / row_k(format));
             if (grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
-            e = launch_format(format, k_mx_quantize_columns<MXFP8>, k_mx_quantize_columns<MXFP4>,
-                              k_mx_quantize_columns<NVFP4>, grid, col_threads(format), stream, p,
-                              static_cast<uint32_t>(cols));
+            e = launch_format(format, k_mx_quantize_columns<MXFP8, SCALE_NONE>,
+                              k_mx_quantize_columns<MXFP4, SCALE_NONE>,
+                              p.parts ? k_mx_quantize_columns<NVFP4, SCALE_FOUND>
+                                      : k_mx_quantize_columns<NVFP4, SCALE_GIVEN>,
+                              grid, col_threads(format), stream, p, static_cast<uint32_t>(cols));
         } else {
             const int64_t spans = (K + row_k(format) - 1) / row_k(format);
             const int64_t grid = std::max<int64_t>(1, (rows + 31) / 32) * spans;
             if (grid > MAX_COORDINATE) return fail(GEMM_ERR_UNSUPPORTED, "rows * K is too large");
-            e = launch_format(format, k_mx_quantize<MXFP8>, k_mx_quantize<MXFP4>,
-                              k_mx_quantize<NVFP4>, grid, row_k(format), stream, p,
-                              static_cast<uint32_t>(spans));
+            e = launch_format(format, k_mx_quantize<MXFP8, SCALE_NONE>,
+                              k_mx_quantize<MXFP4, SCALE_NONE>,
+                              p.parts ? k_mx_quantize<NVFP4, SCALE_FOUND>
+                                      : k_mx_quantize<NVFP4, SCALE_GIVEN>,
+                              grid, row_k(format), stream, p, static_cast<uint32_t>(spans));
         }
         return e == cudaSuccess ? ok() : cuda_fail("quantisation launch", e);
     });
