@@ -76,6 +76,15 @@ def test_pair_exact(M, N, K, format):
 
 
 @pytest.mark.parametrize("format", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(4900, 2568, 264), (5004, 2312, 1536), (4640, 2824, 1544)])
+def test_pair_many_tiles(M, N, K, format):
+    """Several tiles a cluster, some of whose warps have no rows to store, between full ones."""
+    for out in ("f32", "f16"):
+        got, ref, _, what = _run(M, N, K, format, out, True, kernel="pair")
+        assert_same(got, ref, out, what)
+
+
+@pytest.mark.parametrize("format", FORMATS)
 @pytest.mark.parametrize("M,N,K,options", [
     (7, 264, 4096, {}), (64, 512, 2048, {}), (300, 520, 1000, {}),
     (600, 776, 1500 // 4 * 4, {"kernel": "pair"}), (1, 1024, 16384, {})])

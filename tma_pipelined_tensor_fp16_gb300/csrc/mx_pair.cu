@@ -54,8 +54,9 @@ __device__ __forceinline__ void tmem_load_64cols(uint32_t taddr, uint32_t (&r)[6
 }
 
 // As stage_and_store (device_common.cuh) from a buffer that the caller chooses; with `reused`
-// it is written once the store before has read it.
-template <bool F16OUT>
+// it is written once the store from it has read it, STAGING calls before.  With two buffers every
+// call is a group of stores, even one without any, as the wait counts them.
+template <bool F16OUT, int STAGING>
 __device__ __forceinline__ void stage_one(const uint32_t* v, uint32_t row, uint32_t staging,
                                           const CUtensorMap* tmap_c, int col0, int m0, int M,
                                           bool reused)
@@ -64,7 +65,7 @@ __device__ __forceinline__ void stage_one(const uint32_t* v, uint32_t row, uint3
     const uint32_t r = row & 31u;
     const uint32_t buf = staging + quarter * WARP_STAGING_BYTES;
     if (reused) {
-        if (r == 0) bulk_wait_group_read<0>();
+        if (r == 0) bulk_wait_group_read<STAGING - 1>();
         __syncwarp();
     }
     const uint32_t row_base = buf + r * 128u;
@@ -82,8 +83,8 @@ __device__ __forceinline__ void stage_one(const uint32_t* v, uint32_t row, uint3
     fence_proxy_async_smem();
     __syncwarp();
     const int wm0 = m0 + static_cast<int>(quarter * 32u);
-    if (r == 0 && wm0 < M) {
-        tma_store_2d(tmap_c, buf, col0, wm0);
+    if (r == 0 && (STAGING > 1 || wm0 < M)) {
+        if (wm0 < M) tma_store_2d(tmap_c, buf, col0, wm0);
         bulk_commit_group();
     }
 }
@@ -117,7 +118,8 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
 
 }  // namespace
 
-template <int FORMAT, bool F16OUT>
+// STAGING: output buffers of an epilogue warp.
+template <int FORMAT, bool F16OUT, int STAGING>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
     k_mx_pair(const __grid_constant__ CUtensorMap tmAc, const __grid_constant__ CUtensorMap tmAs,
               const __grid_constant__ CUtensorMap tmBc, const __grid_constant__ CUtensorMap tmBs,
@@ -135,7 +137,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
     const uint32_t base = align1024(raw);
     uint8_t* gen = mx_smem + (base - raw);
     const int D = p.pipe_depth;
-    const MxPairLayout L = mx_pair_layout(FORMAT, D);
+    const MxPairLayout L = mx_pair_layout(FORMAT, D, STAGING);
     const uint32_t staging = base + L.staging;
     const uint32_t bars = base + L.bars;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gen + L.bars + TMEM_SLOT_OFFSET);
@@ -336,6 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
         const uint32_t to_leader = map_shared_rank(bar(BAR_TMEM_EMPTY), 0);
         const float alpha = mx_alpha(p);
         int j = 0;
+        uint32_t turn = 0;  // which staging buffer's
         for (int t = first; t < tiles; t += clusters, ++j) {
             int mt, nt;
             raster_tile(t, p.tiles_m, p.tiles_n, p.group_m, mt, nt);
@@ -366,11 +369,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < READ; c += SUB) {
                     const int col0 = nt * TILE + col + c;
-                    if (col0 < p.N)  // uniform
-                        stage_one<F16OUT>(
-                            v + c, row,
-                            last ? base + static_cast<uint32_t>((i + c) / SUB) * STAGING_BYTES : staging,
-                            &tmC, col0, m0, p.M, !last);
+                    if (col0 >= p.N) continue;  // uniform
+                    stage_one<F16OUT, STAGING>(
+                        v + c, row,
+                        last ? base + static_cast<uint32_t>((i + c) / SUB) * STAGING_BYTES
+                             : staging + turn * STAGING_BYTES,
+                        &tmC, col0, m0, p.M, !last);
+                    if constexpr (STAGING > 1) turn ^= 1u;
                 }
             }
         }
@@ -387,10 +392,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
     }
 }
 
-template <int FORMAT>
+template <int FORMAT, int STAGING>
 static cudaError_t launch_format(const MxSpec& s, cudaStream_t stream)
 {
-    auto kernel = s.f16out ? k_mx_pair<FORMAT, true> : k_mx_pair<FORMAT, false>;
+    auto kernel = s.f16out ? k_mx_pair<FORMAT, true, STAGING> : k_mx_pair<FORMAT, false, STAGING>;
     cudaError_t e = ensure_smem_limit(kernel, s.smem_bytes);
     if (e != cudaSuccess) return e;
     return launch_dependent(kernel, dim3(static_cast<unsigned>(s.grid_x)), dim3(MX_THREADS),
@@ -401,9 +406,11 @@ static cudaError_t launch_format(const MxSpec& s, cudaStream_t stream)
 cudaError_t launch_mx_pair(const MxSpec& s, cudaStream_t stream)
 {
     switch (s.format) {
-    case MXFP8: return launch_format<MXFP8>(s, stream);
-    case MXFP4: return launch_format<MXFP4>(s, stream);
-    default: return launch_format<NVFP4>(s, stream);
+    case MXFP8: return launch_format<MXFP8, 1>(s, stream);
+    case MXFP4:
+        return s.staging == 2 ? launch_format<MXFP4, 2>(s, stream) : launch_format<MXFP4, 1>(s, stream);
+    default:
+        return s.staging == 2 ? launch_format<NVFP4, 2>(s, stream) : launch_format<NVFP4, 1>(s, stream);
     }
 }
 

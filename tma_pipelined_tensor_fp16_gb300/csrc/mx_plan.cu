@@ -17,7 +17,7 @@ struct gemm_mx_plan {
     bool pair, swapped;
     int cols, split;
     int stage_chunks, stage_groups;
-    int grid_x, grid_y, pipe_depth;
+    int grid_x, grid_y, pipe_depth, staging;
     unsigned smem_bytes;
     MxParams p;
     DevStatus* d_status;
@@ -167,10 +167,15 @@ gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K, int format
             q.grid_y = 1;
             q.split = 1;
             q.cols = 256;
+            const auto bytes = [&](int depth) { return mx_pair_layout(format, depth, q.staging).total; };
+            // Short contractions are bound by their tiles' stores: two staging buffers a warp,
+            // and a stage less.  8192 x 8192 nvfp4 to fp16, two and one: K = 384 24.7, 31.4 us;
+            // 768 28.8, 33.1; 1536 40.2, 41.0; 2048 50.0, 46.4.  (mxfp8 has no room for them.)
+            q.staging = 2;
+            if (format == MXFP8 || p.stages > 8) q.staging = 1;
             for (q.pipe_depth = MAX_STAGES; q.pipe_depth > MX_PAIR_MIN_STAGES; --q.pipe_depth)
-                if (mx_pair_layout(format, q.pipe_depth).total <= static_cast<uint32_t>(smem_optin))
-                    break;
-            q.smem_bytes = mx_pair_layout(format, q.pipe_depth).total;
+                if (bytes(q.pipe_depth) <= static_cast<uint32_t>(smem_optin)) break;
+            q.smem_bytes = bytes(q.pipe_depth);
         } else {
             q.swapped = M <= 64;
             q.cols = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
@@ -282,6 +287,7 @@ int gemm_mx_run(gemm_mx_plan* plan, const void* codes_a, const void* scales_a, c
         s.swapped = swapped;
         s.grid_x = plan->grid_x;
         s.grid_y = plan->grid_y;
+        s.staging = plan->staging;
         s.smem_bytes = plan->smem_bytes;
         s.codes_u = &tmUc;
         s.scales_u = &tmUs;

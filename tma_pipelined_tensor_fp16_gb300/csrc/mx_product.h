@@ -47,6 +47,7 @@ struct MxSpec {
     int cols;      // single CTAs: rows of the second operand in a tile, 16 .. 128
     bool swapped;  // single CTAs: B is the operand with 128 rows a tile
     int grid_x, grid_y;
+    int staging;   // pair: output buffers of an epilogue warp, 1 or 2 (4-bit formats)
     unsigned smem_bytes;
     const CUtensorMap* codes_u;   // pair: A; single: the operand with 128 rows a tile
     const CUtensorMap* scales_u;
@@ -87,8 +88,8 @@ TG_HD MxSingleLayout mx_single_layout(int format, int cols, int depth, bool swap
 }
 
 // Shared memory of a CTA of a pair: stages of 128 rows of each operand and the scales of
-// 128 rows of A and 256 of B, the output staging (one buffer of 4 KB for each epilogue warp:
-// a second one would take a stage's place, 8192^3 nvfp4 149 us instead of 141), the barriers.
+// 128 rows of A and 256 of B, the output staging (one buffer of 4 KB for each epilogue warp, or
+// two: the second takes a stage's place, 8192^3 nvfp4 142 us instead of 134), the barriers.
 struct MxPairLayout {
     uint32_t stage, b_codes, a_scales, b_scales;
     uint32_t staging, bars, total;
@@ -96,7 +97,7 @@ struct MxPairLayout {
 
 constexpr int MX_PAIR_MIN_STAGES = 6;  // they hold a whole tile of the output at the end
 
-TG_HD MxPairLayout mx_pair_layout(int format, int depth)
+TG_HD MxPairLayout mx_pair_layout(int format, int depth, int staging)
 {
     MxPairLayout L;
     const uint32_t groups = static_cast<uint32_t>(mx_pair_groups(format));
@@ -105,7 +106,7 @@ TG_HD MxPairLayout mx_pair_layout(int format, int depth)
     L.b_scales = L.a_scales + groups * MX_GROUP_BYTES;
     L.stage = (L.b_scales + 2 * groups * MX_GROUP_BYTES + 1023u) / 1024u * 1024u;
     L.staging = L.stage * static_cast<uint32_t>(depth);
-    L.bars = L.staging + STAGING_BYTES;
+    L.bars = L.staging + static_cast<uint32_t>(staging) * STAGING_BYTES;
     L.total = L.bars + BAR_AREA_BYTES + 1024;
     return L;
 }
