@@ -1,7 +1,7 @@
 // mx_quantize.cu -- fp16 matrices to the block-scaled formats of include/tmamicro.h and
 // back.  On paper all are bound by memory: every value is read once (twice where the tensor
 // scale has to be found first) and its codes and scales are written once.  Measured: 16384 x
-// 4096 to mxfp8 31 us, 6.5 TB/s, mxfp4 28, nvfp4 31 (bound by issue slots, 5.6 TB/s); along
+// 4096 to mxfp8 31 us, 6.5 TB/s, mxfp4 28, nvfp4 33 (bound by issue slots, 5.2 TB/s); along
 // columns 33, 30, 35; decoding 31, 27, 27 us, 6.3 to 6.6 TB/s.
 #include <algorithm>
 #include <type_traits>
@@ -36,7 +36,8 @@ struct QuantizeParams {
 // Two CTAs on an SM: there are few parts for every CTA of the quantiser to read.
 constexpr int MOST_THREADS = 1024;
 
-__global__ void __launch_bounds__(MOST_THREADS) k_mx_most(const uint4* X, int64_t vecs, uint32_t* parts)
+__global__ void __launch_bounds__(MOST_THREADS)
+    k_mx_most(const uint4* X, int64_t vecs, uint32_t* parts)
 {
     griddep_wait();
     griddep_launch_dependents();
@@ -133,8 +134,8 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8])
     }
 }
 
-// Where the scale was found first, the tiles go from the last to the first: the L2 still holds what
-// the search has read last (16384 x 4096 with the search 55 us, in the other order 61).
+// Where the scale was found first, the tiles go from the last to the first: the L2 still holds
+// what the search has read last (16384 x 4096 with the search 55 us, in the other order 61).
 template <int SCALE>
 __device__ __forceinline__ uint32_t tile_number()
 {
@@ -163,21 +164,24 @@ __global__ void __launch_bounds__(row_k(FORMAT))
         return row < p.rows && k < p.K ? *reinterpret_cast<const uint4*>(p.X + row * p.K + k)
                                        : make_uint4(0, 0, 0, 0);
     };
+    const auto place = [&](int i) -> uint4& {
+        const int at = i * THREADS + tid;
+        return tile[at / VECS][at % VECS];
+    };
     constexpr int LOADS = 32 * VECS / THREADS;
     float t = 1.0f;
     if constexpr (FORMAT == NVFP4) {
-        // the values are on their way while the tensor scale is found (16384 x 4096, given: 31.2
-        // us, 33.1 one after the other)
+        // the values are on their way while the tensor scale is found (1024 x 4096 with the search:
+        // 0.9 us of 8)
         uint4 in[LOADS];
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) in[i] = load(i);
         t = find_tensor_scale<SCALE>(p, shared);
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) tile[(i * THREADS + tid) / VECS][(i * THREADS + tid) % VECS] = in[i];
+        for (int i = 0; i < LOADS; ++i) place(i) = in[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i)
-            tile[(i * THREADS + tid) / VECS][(i * THREADS + tid) % VECS] = load(i);
+        for (int i = 0; i < LOADS; ++i) place(i) = load(i);
     }
     const float sixth = 1.0f / (6.0f * t);
     __syncthreads();
@@ -232,9 +236,9 @@ __global__ void __launch_bounds__(row_k(FORMAT))
 
 // ------------------------------------------------------------ along columns
 //
-// X is K x rows; a CTA takes 128 of K (96 for mxfp4) x 64 columns through shared memory, and a thread
-// two columns x 32 of K: a block (two of nvfp4) of each, 16 or 32 bytes of codes a
-// column.  The columns are rows of the result, so a warp stores 1 KB without gaps.
+// X is K x rows; a CTA takes 128 of K (96 for mxfp4) x 64 columns through shared memory, and a
+// thread two columns x 32 of K: a block (two of nvfp4) of each, 16 or 32 bytes of codes a column.
+// The columns are rows of the result, so a warp stores 1 KB without gaps.
 constexpr int COL_COLS = 64;
 TG_HD constexpr int col_threads(int format) { return 32 * row_spans(format); }
 
@@ -398,7 +402,8 @@ __device__ __forceinline__ bool scale_of_halves(uint32_t byte, float t, uint32_t
     if constexpr (FORMAT == NVFP4) {
         // a multiple of 2^-9 up to 448 (or NaN), times a power of two from 2^-15 to 2^7
         const uint32_t bits = __float_as_uint(t);
-        if ((bits & 0x7fffffu) || bits < (127u - 15u) << 23 || bits > (127u + 7u) << 23) return false;
+        if ((bits & 0x7fffffu) || bits < (127u - 15u) << 23 || bits > (127u + 7u) << 23)
+            return false;
         uint32_t h;
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(byte * 0x101u)));
         const __half2 s = __hmul2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(t));
@@ -417,7 +422,10 @@ __device__ __forceinline__ float scale_of(uint32_t byte, float t)
     return FORMAT == NVFP4 ? float_of_e4m3(byte) * t : float_of_e8m0(byte);
 }
 
-__device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+__device__ __forceinline__ __half2 half2_of(uint32_t w)
+{
+    return *reinterpret_cast<const __half2*>(&w);
+}
 
 // The codes of eight values that start `skew` (0 to 7) before q's, of which `prev` are those in
 // front.
@@ -513,7 +521,9 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
             const int block = block_of(j);
             const bool starts = (part * 8) % mx_block(FORMAT) == 0;  // a block
             const uint32_t byte = byte_of(block);
-            const uint32_t before = !starts ? byte : block > 0 ? byte_of(max(block - 1, 0)) : front_byte;
+            const uint32_t before = !starts     ? byte
+                                    : block > 0 ? byte_of(max(block - 1, 0))
+                                                : front_byte;
             __half2 v[4];
             decode8<FORMAT>(codes_before<FORMAT>(prev, q[j], skew), v);
             uint32_t s = 0, s0 = 0;
@@ -578,7 +588,8 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) to[i] = x[i];
                 } else {
-                    float4* to = reinterpret_cast<float4*>(static_cast<float*>(p.values) + row * p.K + k);
+                    float* at = static_cast<float*>(p.values) + row * p.K + k;
+                    float4* to = reinterpret_cast<float4*>(at);
                     to[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
                     to[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
                 }

@@ -237,7 +237,6 @@ struct NormGradParams {
     float* parts;  // [part][width]
 };
 
-
 // How rows are held: by `lanes` lanes with `vec` vectors of eight values each; CTAs of `threads`
 // threads, `resident` of them on an SM, which the registers are held to.  Several CTAs cover each
 // other's reductions better than one that reads a row ahead (16384 x 4096 with dH: four 87 us,
@@ -254,10 +253,11 @@ struct GradConfig {
 };
 
 // A row takes the first that holds it, however many rows there are, so dX does not depend on
-// the other rows (a vector a lane would be faster for few: 77 x 4096 5.1 us, 5.6): two to four vectors a lane, hardly a lane without any, and
-// a few groups of lanes in a CTA, which write one part of dweight (640 wide: 32 lanes of three 90
-// us, 128 of one 119; 1528 wide: 64 of three 90, 256 of one 110; 1000 rows of 1024: 64 lanes of
-// two, four groups a CTA, 6.4 us, 128 of one and a CTA for each 8.0).
+// the other rows (a vector a lane would be faster for few: 77 x 4096 5.1 us, 5.6): two to four
+// vectors a lane, hardly a lane without any, and a few groups of lanes in a CTA, which write one
+// part of dweight (640 wide: 32 lanes of three 90 us, 128 of one 119; 1528 wide: 64 of three 90,
+// 256 of one 110; 1000 rows of 1024: 64 lanes of two, four groups a CTA, 6.4 us, 128 of one and
+// a CTA for each 8.0).
 constexpr GradConfig GRAD[] = {
     {16, 1, 256, 6, false},  {32, 1, 256, 5, false},  {16, 3, 256, 3, false},
     {32, 2, 256, 4, false},  {32, 3, 256, 3, false},  {64, 2, 256, 4, false},
