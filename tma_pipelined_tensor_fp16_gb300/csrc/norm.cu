@@ -101,6 +101,16 @@ __device__ __forceinline__ float row_sum(const float (&v)[VEC], float* shared)
     }
 }
 
+constexpr int64_t MAX_WIDTH = 32768;
+
+// Rows of mxfp4 are filled up to whole steps of 96 values, those of the largest widths by up to
+// 64 past MAX_WIDTH: past the vectors of the lanes that hold such a row.  The row's first warp
+// writes them in a turn of its own.
+template <int FORMAT, int LANES, int VEC>
+constexpr bool fills_up_past =
+    FORMAT == MXFP4 && static_cast<int64_t>(LANES) * VEC * 8 == MAX_WIDTH;
+static_assert((MAX_WIDTH + 95) / 96 * 96 <= MAX_WIDTH + 32 * 8, "one turn of a warp");
+
 // A row by LANES lanes (half a warp, a warp, or all of the CTA), VEC vectors of eight values
 // per lane, held in registers between the sum of squares and the outputs.
 template <int FORMAT, int LANES, int VEC, int THREADS>
@@ -165,6 +175,15 @@ __global__ void __launch_bounds__(THREADS) k_rms_norm(const __grid_constant__ No
                                    p.scales + mx_scale_offset(row, 0, p.groups),
                                    static_cast<int>(p.chunks), static_cast<int>(p.groups), valid);
     }
+    if constexpr (fills_up_past<FORMAT, LANES, VEC>) {
+        if (lane < 32) {
+            const float zeros[8] = {};
+            quantize_store<FORMAT>(zeros, 1.0f, 1.0f / 6.0f, VEC * LANES + lane,
+                                   p.codes + mx_code_offset(row, 0, p.chunks),
+                                   p.scales + mx_scale_offset(row, 0, p.groups),
+                                   static_cast<int>(p.chunks), static_cast<int>(p.groups), valid);
+        }
+    }
 }
 
 template <int FORMAT>
@@ -176,11 +195,13 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t stream)
         padded = std::max<int64_t>(p.chunks * mx_chunk(FORMAT), p.groups * mx_group(FORMAT));
     const int64_t vecs = (padded + 7) / 8;
     auto go = [&](auto lanes, auto vec) {
-        constexpr int LANES = decltype(lanes)::value;
+        constexpr int LANES = decltype(lanes)::value, VEC = decltype(vec)::value;
         constexpr int THREADS = LANES <= 32 ? 256 : LANES;
+        constexpr int HELD = LANES * VEC + (fills_up_past<FORMAT, LANES, VEC> ? 32 : 0);
+        if (vecs > HELD) return cudaErrorInvalidValue;
         constexpr int ROWS = THREADS / LANES;
         const int64_t grid = (p.tokens + ROWS - 1) / ROWS;
-        return launch_dependent(k_rms_norm<FORMAT, LANES, decltype(vec)::value, THREADS>,
+        return launch_dependent(k_rms_norm<FORMAT, LANES, VEC, THREADS>,
                                 dim3(static_cast<unsigned>(grid)), dim3(THREADS), 0, 1, stream, p);
     };
 #define TG_NORM(lanes, vec) \
@@ -488,7 +509,7 @@ int check_norm(int64_t tokens, int64_t width, float eps)
 {
     if (tokens < 0 || tokens > MAX_COORDINATE)
         return fail(GEMM_ERR_INVALID_ARG, "tokens must be in [0, 2^31-65536]");
-    if (width < 8 || width > 32768 || width % 8 != 0)
+    if (width < 8 || width > MAX_WIDTH || width % 8 != 0)
         return fail(GEMM_ERR_UNSUPPORTED, "width must be a multiple of 8 from 8 to 32768");
     if (!(eps >= 0.0f)) return fail(GEMM_ERR_INVALID_ARG, "eps must be >= 0");
     return GEMM_OK;
