@@ -50,6 +50,31 @@ int require_device(int* dev, int* sms, int* smem_optin)
     return GEMM_OK;
 }
 
+namespace {
+std::mutex g_fill_mutex;
+cudaStream_t g_fill_streams[MAX_DEVICES] = {};
+}  // namespace
+
+cudaError_t fill_new_memory(void* to, const void* from, size_t bytes)
+{
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= MAX_DEVICES) return cudaErrorInvalidDevice;
+    cudaStream_t stream = nullptr;
+    {
+        std::lock_guard<std::mutex> lock(g_fill_mutex);
+        if (!g_fill_streams[dev])
+            e = cudaStreamCreateWithFlags(&g_fill_streams[dev], cudaStreamNonBlocking);
+        if (e != cudaSuccess) return e;
+        stream = g_fill_streams[dev];
+    }
+    e = from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyHostToDevice, stream)
+             : cudaMemsetAsync(to, 0, bytes, stream);
+    const cudaError_t done = cudaStreamSynchronize(stream);
+    return e != cudaSuccess ? e : done;
+}
+
 int read_device_status(DevStatus* record)
 {
     DevStatus st;
