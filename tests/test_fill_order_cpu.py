@@ -16,7 +16,7 @@ def _source(name):
 def test_a_fill_is_waited_for():
     """On a stream that waits for no other one, on which nothing else runs."""
     body = _source("runtime.cu")
-    body = body[body.index("cudaError_t fill_new_memory("):]
+    body = body[body.index("cudaError_t fill_memory("):]
     body = body[:body.index("\n}")]
     order = [body.index(s) for s in ("cudaStreamNonBlocking", "cudaMemcpyAsync(", "cudaMemsetAsync(",
                                      "cudaStreamSynchronize(stream)", "return e != cudaSuccess")]
@@ -24,8 +24,16 @@ def test_a_fill_is_waited_for():
     assert len(re.findall(r"\breturn\b", body[order[1]:order[3]])) == 0
 
 
-@pytest.mark.parametrize("file", ["clip.cu"])
+@pytest.mark.parametrize("file", ["api.cu", "clip.cu", "grouped.cu", "mx_plan.cu", "w4.cu"])
 def test_creators_fill_through_it(file):
     text = _source(file)
-    assert not re.search(r"\bcudaMem(cpy|set)\(", text)
-    assert "fill_new_memory(" in text
+    plain = re.findall(r"\bcudaMem(?:cpy|set)\([^;]*;", text)
+    assert all("cudaMemcpyDeviceToHost" in call for call in plain)
+    assert "fill_memory(" in text
+
+
+def test_a_records_clearing_is_waited_for():
+    """The next run may have ended with a status of its own before a late clearing."""
+    body = _source("runtime.cu")
+    body = body[body.index("int read_device_status("):]
+    assert "cudaMemcpyHostToDevice" not in body and "fill_memory(record" in body

@@ -609,11 +609,12 @@ gemm_plan* gemm_create_plan_ex(int64_t M, int64_t N, int64_t K, int dtype_out,
     // as the static schedule of a full grid (SM count / 2 clusters) would.
     p->snake_span = snake_span_of(p->cfg, sms);
     e = cudaMalloc(&p->d_status, sizeof(DevStatus));
-    if (e == cudaSuccess) e = cudaMemset(p->d_status, 0, sizeof(DevStatus));
+    if (e == cudaSuccess) e = fill_memory(p->d_status, nullptr, sizeof(DevStatus));
     if (e == cudaSuccess && p->cfg.workspace_bytes > 0) {
         e = cudaMalloc(&p->d_workspace, static_cast<size_t>(p->cfg.workspace_bytes));
         if (e == cudaSuccess)
-            e = cudaMemset(p->d_workspace, 0, static_cast<size_t>(p->cfg.workspace_bytes));
+            e = fill_memory(p->d_workspace, nullptr,
+                                static_cast<size_t>(p->cfg.workspace_bytes));
     }
     if (e != cudaSuccess) {
         cuda_fail("allocating the device status record / stream-K workspace", e);

@@ -428,7 +428,7 @@ gemm_clip_plan* gemm_clip_create_plan(int64_t count, const void* const* grads, v
             const size_t bytes = table.size() * sizeof(Chunk);
             cudaError_t e = cudaMalloc(&plan->d_chunks, bytes);
             if (e == cudaSuccess)
-                e = fill_new_memory(plan->d_chunks, table.data(), bytes);
+                e = fill_memory(plan->d_chunks, table.data(), bytes);
             if (e != cudaSuccess) {
                 if (plan->d_chunks) cudaFree(plan->d_chunks);
                 return cuda_fail("allocating the table of gradients", e);

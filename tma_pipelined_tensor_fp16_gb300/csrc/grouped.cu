@@ -171,7 +171,7 @@ int make_counters(int dev)
     std::unique_ptr<CounterPool> pool(new CounterPool);
     constexpr size_t BYTES = CounterSlots::COUNT * sizeof(unsigned long long);
     cudaError_t e = cudaMalloc(&pool->d_counters, BYTES);
-    if (e == cudaSuccess) e = cudaMemset(pool->d_counters, 0, BYTES);
+    if (e == cudaSuccess) e = fill_memory(pool->d_counters, nullptr, BYTES);
     if (e != cudaSuccess) {
         if (pool->d_counters) cudaFree(pool->d_counters);
         return cuda_fail("allocating the tile counters", e);
@@ -319,7 +319,7 @@ gemm_grouped_plan* gemm_grouped_create_plan_ex(int64_t rows, int64_t N, int64_t 
         r = make_counters(dev);
         if (r != GEMM_OK) return r;
         cudaError_t e = cudaMalloc(&p.d_status, sizeof(DevStatus));
-        if (e == cudaSuccess) e = cudaMemset(p.d_status, 0, sizeof(DevStatus));
+        if (e == cudaSuccess) e = fill_memory(p.d_status, nullptr, sizeof(DevStatus));
         if (e != cudaSuccess) {
             if (p.d_status) cudaFree(p.d_status);
             return cuda_fail("allocating the device status record", e);

@@ -218,7 +218,7 @@ gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K, int format
                       q.split, q.pipe_depth, q.smem_bytes, q.grid_x, q.grid_y,
                       dtype_out == GEMM_OUT_F16 ? "f16" : "f32");
         cudaError_t e = cudaMalloc(&q.d_status, sizeof(DevStatus));
-        if (e == cudaSuccess) e = cudaMemset(q.d_status, 0, sizeof(DevStatus));
+        if (e == cudaSuccess) e = fill_memory(q.d_status, nullptr, sizeof(DevStatus));
         if (e != cudaSuccess) {
             if (q.d_status) cudaFree(q.d_status);
             return cuda_fail("allocating the device status record", e);

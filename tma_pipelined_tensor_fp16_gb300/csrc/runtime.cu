@@ -55,7 +55,7 @@ std::mutex g_fill_mutex;
 cudaStream_t g_fill_streams[MAX_DEVICES] = {};
 }  // namespace
 
-cudaError_t fill_new_memory(void* to, const void* from, size_t bytes)
+cudaError_t fill_memory(void* to, const void* from, size_t bytes)
 {
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
@@ -83,7 +83,7 @@ int read_device_status(DevStatus* record)
     DevStatus left = st;
     const int code = take_status(&left);
     if (code == DEV_OK) return ok();
-    e = cudaMemcpy(record, &left, sizeof(left), cudaMemcpyHostToDevice);
+    e = fill_memory(record, &left, sizeof(left));
     if (e != cudaSuccess) return cuda_fail("clearing the device status record", e);
     char buf[200];
     std::snprintf(buf, sizeof(buf),

@@ -30,12 +30,12 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn();
 // are read once per device.
 int require_device(int* dev, int* sms, int* smem_optin);
 
-// Fill memory that cudaMalloc has just returned, from `from` or (NULL) with zeros, before
-// returning.  A plain cudaMemcpy from pageable memory may return when the bytes have been
-// staged, a cudaMemset at once, and the streams of a caller need not wait for the legacy one
-// that they run on.  So both run on a stream of the library's own, which is waited for: it
-// waits for no work of the caller's either.
-cudaError_t fill_new_memory(void* to, const void* from, size_t bytes);
+// Fill device memory that no run uses (new, or a record after synchronising), from `from`
+// or (NULL) with zeros, before returning.  A plain cudaMemcpy from pageable memory may return
+// when the bytes have been staged, a cudaMemset at once, and the streams of a caller need not
+// wait for the legacy one that they run on.  So both run on a stream of the library's own,
+// which is waited for: it waits for no work of the caller's either.
+cudaError_t fill_memory(void* to, const void* from, size_t bytes);
 
 // Read a plan's device status record after its stream has been synchronised, and
 // clear it: GEMM_OK, GEMM_ERR_TIMEOUT or GEMM_ERR_CUDA.

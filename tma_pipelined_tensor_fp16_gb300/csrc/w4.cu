@@ -1231,7 +1231,7 @@ gemm_w4_plan* gemm_w4_create_plan_ex(int64_t M, int64_t N, int64_t K, int group,
         const char* what = "allocating the device status record";
         if (!p.expand || !p.rounded) {
             e = cudaMalloc(&p.d_status, sizeof(DevStatus));
-            if (e == cudaSuccess) e = cudaMemset(p.d_status, 0, sizeof(DevStatus));
+            if (e == cudaSuccess) e = fill_memory(p.d_status, nullptr, sizeof(DevStatus));
         }
         if (e == cudaSuccess && p.expand) {
             what = "allocating the expanded weights";
