@@ -68,7 +68,9 @@ TMAGEMM_API int gemm_mx_quantize(int64_t rows, int64_t K, int format, int transp
                                  void* codes, void* scales, float* tensor_scale, void* workspace,
                                  void* cuda_stream);
 
-/* values[r][k] = q * s * t, rows x K of dtype_out (a gemm_dtype), contiguous.  fp32 holds every value exactly (but products under 2^-149); fp16 rounds once. */
+/* values[r][k] = q * s * t, rows x K of dtype_out (a gemm_dtype), contiguous, rounded once to
+ * fp32, which holds every value where t is a power of two (but products under 2^-149), and
+ * from there to fp16. */
 TMAGEMM_API int gemm_mx_values(int64_t rows, int64_t K, int format, const void* codes,
                                const void* scales, const float* tensor_scale, int dtype_out,
                                void* values, void* cuda_stream);

@@ -417,9 +417,17 @@ __device__ __forceinline__ bool scale_of_halves(uint32_t byte, float t, uint32_t
 }
 
 template <int FORMAT>
-__device__ __forceinline__ float scale_of(uint32_t byte, float t)
+__device__ __forceinline__ float scale_of(uint32_t byte)
 {
-    return FORMAT == NVFP4 ? float_of_e4m3(byte) * t : float_of_e8m0(byte);
+    return FORMAT == NVFP4 ? float_of_e4m3(byte) : float_of_e8m0(byte);
+}
+
+// A value from its code and its block's scale, and the tensor's: q s is exact for nvfp4 (six
+// bits) and rounded once by t, whose product with s alone may leave fp32 where q s t does not.
+template <int FORMAT>
+__device__ __forceinline__ float value_of(float q, float s, float t)
+{
+    return FORMAT == NVFP4 ? q * s * t : q * s;
 }
 
 __device__ __forceinline__ __half2 half2_of(uint32_t w)
@@ -532,12 +540,13 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
                 for (int i = 0; i < 4; ++i)
                     v[i] = __hmul2(v[i], half2_of(__byte_perm(s, s0, pick[i])));
             } else {
-                const float f = scale_of<FORMAT>(byte, t), f0 = scale_of<FORMAT>(before, t);
+                const float f = scale_of<FORMAT>(byte), f0 = scale_of<FORMAT>(before);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 x = __half22float2(v[i]);
-                    v[i] = __floats2half2_rn(x.x * (2 * i < skew ? f0 : f),
-                                             x.y * (2 * i + 1 < skew ? f0 : f));
+                    v[i] = __floats2half2_rn(
+                        value_of<FORMAT>(x.x, 2 * i < skew ? f0 : f, t),
+                        value_of<FORMAT>(x.y, 2 * i + 1 < skew ? f0 : f, t));
                 }
             }
             const int64_t at = k0 + j * 32 + part * 8 - skew;
@@ -565,23 +574,24 @@ __global__ void __launch_bounds__(ROW_WARPS * 32)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) v[i] = __hmul2(v[i], half2_of(s));
                 } else {
-                    const float f = scale_of<FORMAT>(byte, t);
+                    const float f = scale_of<FORMAT>(byte);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 x = __half22float2(v[i]);
-                        v[i] = __floats2half2_rn(x.x * f, x.y * f);
+                        v[i] = __floats2half2_rn(value_of<FORMAT>(x.x, f, t),
+                                                 value_of<FORMAT>(x.y, f, t));
                     }
                 }
                 *reinterpret_cast<uint4*>(static_cast<__half*>(p.values) + row * p.K + k) =
                     *reinterpret_cast<const uint4*>(v);
             } else {
-                const float f = scale_of<FORMAT>(byte, t);
+                const float f = scale_of<FORMAT>(byte);
                 float2 x[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     x[i] = __half22float2(v[i]);
-                    x[i].x *= f;
-                    x[i].y *= f;
+                    x[i].x = value_of<FORMAT>(x[i].x, f, t);
+                    x[i].y = value_of<FORMAT>(x[i].y, f, t);
                 }
                 if constexpr (STAGED) {
                     float2* to = reinterpret_cast<float2*>(&rows[lane / 4][j * 32 + part * 8]);
