@@ -15,17 +15,19 @@
  *
  *   GEMM_MXFP8   q e4m3 (largest 448), s a power of two (e8m0) for every 32 values
  *   GEMM_MXFP4   q e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6), s a power of two for every 32
- *   GEMM_NVFP4   q e2m1, s e4m3 for every 16, and one fp32 power of two, the tensor
- *                scale t, for the whole matrix: a value is q * s * t
+ *   GEMM_NVFP4   q e2m1, s e4m3 for every 16, and one fp32, the tensor scale t, for the
+ *                whole matrix: a value is q * s * t
  *
  * Quantisation of a block whose largest magnitude is a:
  *   MXFP8, MXFP4   s is the least power of two (of those from 2^-127) with a <= largest *
  *                  s, so that no value is cut off; q = round(x / s)
  *   NVFP4          t is the least power of two with max|X| <= 6 * 448 * t (1 for a matrix
- *                  of zeros), s = max(round_e4m3(a / (6 t)), 2^-9), q = round(x / (s t)),
- *                  at most 6 in magnitude
- * Every rounding is to the nearest, ties to even.  A block that holds an infinity or a NaN
- * gets the scale NaN: all its values are NaN.  Such values do not enter t.
+ *                  of zeros) unless it is given, s = max(round_e4m3(a / (6 t)), 2^-9), at most
+ *                  448, q = round(x / (s t)), at most 6 in magnitude
+ * Every rounding is to the nearest, ties to even; with a given t that is no power of two,
+ * of quotients that fp32 arithmetic leaves off by up to 2^-22 of themselves.  A block that
+ * holds an infinity or a NaN gets the scale NaN: all its values are NaN.  Such values do not
+ * enter t.
  *
  * Storage.  A matrix of `rows` x `K` is kept in the order in which the tensor cores read
  * it, in blocks of 128 rows:
@@ -62,8 +64,8 @@ TMAGEMM_API int gemm_mx_sizes(int64_t rows, int64_t K, int format, int64_t* code
  * transpose: blocks run along the columns of X.
  * tensor_scale (GEMM_NVFP4 only, else NULL): one fp32 in device memory.  With a workspace
  * (GEMM_MX_WORKSPACE_BYTES, for this call alone until it has run) it is found from X and
- * written; with workspace = NULL the power of two that it holds is used: values beyond
- * 2688 times it are cut off. */
+ * written; with workspace = NULL the number that it holds is used as it is: values beyond
+ * 2688 times it are cut off.  With a negative number or a NaN all values are NaN. */
 TMAGEMM_API int gemm_mx_quantize(int64_t rows, int64_t K, int format, int transpose, const void* X,
                                  void* codes, void* scales, float* tensor_scale, void* workspace,
                                  void* cuda_stream);
@@ -96,8 +98,8 @@ TMAGEMM_API gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K
                                                  int dtype_out, int kernel, int split);
 
 /* Enqueue the product.  No scale may have its sign bit set (gemm_mx_quantize sets none).
- * scale_a, scale_b: the tensor scales of GEMM_NVFP4 (one fp32 each,
- * any value), or NULL for 1. */
+ * scale_a, scale_b: the tensor scales of GEMM_NVFP4 (one fp32 each, whose product is a
+ * finite fp32), or NULL for 1. */
 TMAGEMM_API int gemm_mx_run(gemm_mx_plan* plan, const void* codes_a, const void* scales_a,
                             const float* scale_a, const void* codes_b, const void* scales_b,
                             const float* scale_b, void* C, void* cuda_stream);

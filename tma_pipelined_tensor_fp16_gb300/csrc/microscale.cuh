@@ -58,7 +58,9 @@ __device__ __forceinline__ BlockScale block_scale(float most, float t, float six
         // a / (6 t) with the product instead of the quotient: a has 11 bits (24 in the
         // norm) and a border of e4m3 has 5, so for fp16 values the rounding error of
         // the product decides only where a / 6 lies on a border, which needs a = 6 m
-        // with m of 5 bits: there the quotient is exact and the product is refined to it
+        // with m of 5 bits: there the quotient is exact and the product is refined to it.
+        // (With a given t that is no power of two, 6 t and s t are rounded to fp32 first: a
+        // quotient within 2^-22 of a border may go either way.)
         float y = most * sixth;
         y = fmaf(fmaf(-y, 6.0f * t, most), sixth, y);
         uint32_t byte = max(e4m3_of(y), 1u);

@@ -89,8 +89,11 @@ __device__ __forceinline__ float find_tensor_scale(const QuantizeParams& p, uint
 {
     if constexpr (SCALE == SCALE_NONE) return 1.0f;
     if constexpr (SCALE == SCALE_GIVEN) {
-        const uint32_t e = (__float_as_uint(*p.tensor_scale) >> 23) & 0xffu;
-        return power_of_two(static_cast<int>(min(max(e, 1u), 254u)) - 127);
+        // Beyond 2^100 every fp16 value rounds to zero, and below 2^-100 every one but zero is cut
+        // off, as at these borders: no quotient need leave fp32.  A negative number or a NaN
+        // scales nothing: every block gets the scale NaN.
+        const float t = *p.tensor_scale;
+        return t >= 0.0f ? fminf(fmaxf(t, 0x1p-100f), 0x1p100f) : __uint_as_float(0x7fc00000u);
     }
     uint32_t most = 0;
     for (int i = static_cast<int>(threadIdx.x); i < p.part_count;

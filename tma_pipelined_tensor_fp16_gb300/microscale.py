@@ -8,7 +8,7 @@
 
 Formats: ``mxfp8`` (e4m3, a power of two for every 32 values of a row), ``mxfp4``
 (e2m1, a power of two for every 32) and ``nvfp4`` (e2m1, an e4m3 scale for every 16 and
-a power of two for the whole tensor).
+one fp32 for the whole tensor, a power of two where it is found).
 
 Argument checks and marshalling only, with the conventions of ``experts``: every operator
 runs in the library's CUDA kernels, asynchronously on the current stream of the tensors'
@@ -135,8 +135,8 @@ class MXTensor:
     def from_codes(cls, codes, scales, K, format, tensor_scale=None):
         """From row-major codes (rows x K uint8 for mxfp8, rows x ceil(K / 2) for the
         others, the first of two in the low half) and row-major scales (rows x
-        ceil(K / block) bytes of e8m0, e4m3 for nvfp4), as other programs keep them.  A
-        set-up step."""
+        ceil(K / block) bytes of e8m0, e4m3 without a sign for nvfp4), as other programs
+        keep them.  A set-up step."""
         torch = _torch()
         _format(format)
         rows = codes.shape[0]
@@ -167,8 +167,8 @@ class MXTensor:
                 s[:self.rows, :-(-self.K // _BLOCK[self.format])].contiguous())
 
     def values(self, out=None, stream=None):
-        """The values that the codes stand for (rows x K), rounded once to `out`'s type
-        (fp16 when not given; fp32 holds them exactly)."""
+        """The values that the codes stand for (rows x K) in `out`'s type (fp16 when not
+        given; fp32 holds them exactly where the tensor scale is a power of two)."""
         torch = _torch()
         dev = self.device
         dtype = torch.float32 if out is not None and out.dtype is torch.float32 else torch.float16
@@ -184,8 +184,8 @@ def mx_quantize(X, format="mxfp8", transpose=False, tensor_scale=None, out=None,
     """Round X (fp16, contiguous; its rows hold a multiple of 8 values) to `format`:
     an MXTensor of X's shape, or of X^T's with `transpose` (blocks run along X's columns).
 
-    nvfp4: without `tensor_scale` (one fp32, a power of two) it is found from X first and
-    belongs to the result.  `out`, an MXTensor of the result's shape and format, is written
+    nvfp4: without `tensor_scale` (one fp32, 0 or larger; values beyond 2688 times it are cut
+    off) it is found from X first and belongs to the result.  `out`, an MXTensor of the result's shape and format, is written
     in place and returned."""
     torch = _torch()
     code = _format(format)
