@@ -209,6 +209,7 @@ def mx_quantize(X, format="mxfp8", transpose=False, tensor_scale=None, out=None,
             raise ValueError("out must be a %s MXTensor of %d x %d on %s"
                              % (format, rows, K, dev))
     work = extra = None
+    before = Q._given, Q._found
     if tensor_scale is not None:
         Q._given, Q._found = tensor_scale, False
     elif code == 2:  # nvfp4
@@ -219,8 +220,12 @@ def mx_quantize(X, format="mxfp8", transpose=False, tensor_scale=None, out=None,
         else:
             Q._given, Q._found = None, True
             work = Q._buffer.data_ptr() + _bytes(rows, K, format)[1] + 16
-    _call(lib().gemm_mx_quantize, dev, stream, rows, K, code, 1 if transpose else 0,
-          X.data_ptr(), *Q._addresses(), work)
+    try:
+        _call(lib().gemm_mx_quantize, dev, stream, rows, K, code, 1 if transpose else 0,
+              X.data_ptr(), *Q._addresses(), work)
+    except BaseException:  # its codes are the old ones: so is its scale
+        Q._given, Q._found = before
+        raise
     if stream is not None:
         _used_on(stream, X, *Q._parts(), extra)
     return Q
