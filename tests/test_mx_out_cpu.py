@@ -40,3 +40,20 @@ def test_a_call_that_fails_leaves_the_scale(fake, monkeypatch, own, was_given, g
         with pytest.raises(GemmError):
             m.mx_quantize(X, "nvfp4", out=Q, tensor_scale=Tensor((1,), f32) if given else None)
     assert Q._addresses() == before
+
+
+@pytest.mark.parametrize("own", [False, True])
+def test_a_found_scale_keeps_its_place(fake, own):
+    """A captured product reads the scale where it was: quantising again writes it there, also
+    after a call with a scale of the caller's."""
+    from tma_pipelined_tensor_fp16_gb300 import microscale as m
+    torch, library = fake
+    X = Tensor((20, 64), torch.float16)
+    Q = _tensor(torch, own)
+    first = m.mx_quantize(X, "nvfp4", out=Q)._addresses()
+    assert m.mx_quantize(X, "nvfp4", out=Q)._addresses() == first
+    given = Tensor((1,), torch.float32)
+    assert m.mx_quantize(X, "nvfp4", out=Q, tensor_scale=given)._addresses()[2] == given.address
+    assert m.mx_quantize(X, "nvfp4", out=Q)._addresses() == first
+    name, args = library.calls[-1]
+    assert name == "gemm_mx_quantize" and args[7] == first[2]

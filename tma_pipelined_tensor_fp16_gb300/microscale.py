@@ -82,6 +82,7 @@ class MXTensor:
         self.device = codes.device
         self._buffer, self._views = None, (codes, scales)
         self._given, self._found = tensor_scale, False
+        self._own_scale = None
 
     @classmethod
     def _new(cls, rows, K, format, device, stream):
@@ -90,7 +91,7 @@ class MXTensor:
         t.rows, t.K, t.format, t.device = rows, K, format, device
         t._buffer, t._views = _empty((_bytes(rows, K, format)[2],), _torch().uint8, device,
                                      stream), None
-        t._given, t._found = None, False
+        t._given, t._found, t._own_scale = None, False, None
         return t
 
     def _both(self):
@@ -214,7 +215,10 @@ def mx_quantize(X, format="mxfp8", transpose=False, tensor_scale=None, out=None,
         Q._given, Q._found = tensor_scale, False
     elif code == 2:  # nvfp4
         if Q._buffer is None:  # made by the caller: it has no room for it
-            Q._given = _empty((1,), torch.float32, dev, stream)
+            # one for all calls: a captured product finds it in place
+            if Q._own_scale is None:
+                Q._own_scale = _empty((1,), torch.float32, dev, stream)
+            Q._given = Q._own_scale
             extra = _empty((_WORKSPACE,), torch.uint8, dev, stream)
             work = extra.data_ptr()
         else:
