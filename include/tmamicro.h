@@ -97,6 +97,14 @@ typedef enum { GEMM_MX_AUTO = 0, GEMM_MX_PAIR = 1, GEMM_MX_SINGLE = 2 } gemm_mx_
 TMAGEMM_API gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K, int format,
                                                  int dtype_out, int kernel, int split);
 
+/* A plan of other sizes in `plan`'s format, for products whose sizes change from call to call:
+ * it has no device memory of its own and is made without a call that waits, also while a
+ * stream is being captured.  Both use one status record, which reports a timeout in a run of
+ * either and stays until the last of its plans is destroyed. */
+TMAGEMM_API gemm_mx_plan* gemm_mx_create_plan_beside(const gemm_mx_plan* plan, int64_t M,
+                                                     int64_t N, int64_t K, int dtype_out,
+                                                     int kernel, int split);
+
 /* Enqueue the product.  No scale may have its sign bit set (gemm_mx_quantize sets none).
  * scale_a, scale_b: the tensor scales of GEMM_NVFP4 (one fp32 each, whose product is a
  * finite fp32), or NULL for 1. */

@@ -116,6 +116,8 @@ _SIGS = {
                        + [ctypes.c_void_p] * 3 + [ctypes.c_int] + [ctypes.c_void_p] * 2),
     "gemm_mx_create_plan": (ctypes.c_void_p, [ctypes.c_int64] * 3 + [ctypes.c_int] * 2),
     "gemm_mx_create_plan_ex": (ctypes.c_void_p, [ctypes.c_int64] * 3 + [ctypes.c_int] * 4),
+    "gemm_mx_create_plan_beside": (ctypes.c_void_p, [ctypes.c_void_p] + [ctypes.c_int64] * 3
+                                   + [ctypes.c_int] * 3),
     "gemm_mx_run": (ctypes.c_int, [ctypes.c_void_p] * 9),
     "gemm_mx_set_wait": (ctypes.c_int, [ctypes.c_void_p] + [ctypes.c_int] * 2),
     "gemm_mx_get_device_status": (ctypes.c_int, [ctypes.c_void_p]),

@@ -1,6 +1,7 @@
 // mx_plan.cu -- host side of the block-scaled products: argument checks, the choice of the
 // kernel, the tensor maps and the launch.
 #include <algorithm>
+#include <atomic>
 #include <cstdio>
 #include <new>
 
@@ -9,6 +10,14 @@
 #include "runtime.h"
 
 using namespace tg;
+
+// The status record of one plan or of several, and the number of their last run.
+struct MxRecord {
+    DevStatus* d_status;
+    int device;
+    unsigned epoch;
+    std::atomic<int> plans;
+};
 
 struct gemm_mx_plan {
     int64_t M, N, K;
@@ -20,8 +29,7 @@ struct gemm_mx_plan {
     int grid_x, grid_y, pipe_depth, staging;
     unsigned smem_bytes;
     MxParams p;
-    DevStatus* d_status;
-    unsigned epoch;
+    MxRecord* record;
     unsigned long long budget_ns;
     int debug_stall;
     char desc[256];
@@ -111,17 +119,33 @@ int check_product(int64_t M, int64_t N, int64_t K, int format, int dtype, int ke
     return GEMM_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-gemm_mx_plan* gemm_mx_create_plan(int64_t M, int64_t N, int64_t K, int format, int dtype_out)
+int make_record(int dev, MxRecord** made)
 {
-    return gemm_mx_create_plan_ex(M, N, K, format, dtype_out, GEMM_MX_AUTO, 0);
+    MxRecord* r = new (std::nothrow) MxRecord{};
+    if (!r) return fail(GEMM_ERR_CUDA, "out of host memory");
+    r->device = dev;
+    r->plans = 1;
+    cudaError_t e = cudaMalloc(&r->d_status, sizeof(DevStatus));
+    if (e == cudaSuccess) e = fill_memory(r->d_status, nullptr, sizeof(DevStatus));
+    if (e != cudaSuccess) {
+        if (r->d_status) cudaFree(r->d_status);
+        delete r;
+        return cuda_fail("allocating the device status record", e);
+    }
+    *made = r;
+    return GEMM_OK;
 }
 
-gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K, int format, int dtype_out,
-                                     int kernel, int split)
+void release(MxRecord* r)
+{
+    if (r->plans.fetch_sub(1) > 1) return;
+    cudaFree(r->d_status);
+    delete r;
+}
+
+// A plan with the record of `first`, or with one of its own where that is NULL.
+gemm_mx_plan* make_plan(int64_t M, int64_t N, int64_t K, int format, int dtype_out, int kernel,
+                        int split, const gemm_mx_plan* first)
 {
     gemm_mx_plan* plan = nullptr;
     guarded([&] {
@@ -130,6 +154,8 @@ gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K, int format
         int dev, sms, smem_optin;
         r = require_device(&dev, &sms, &smem_optin);
         if (r != GEMM_OK) return r;
+        if (first && first->device != dev)
+            return fail(GEMM_ERR_INVALID_ARG, "plan was created on another device");
         gemm_mx_plan q = {};
         q.M = M;
         q.N = N;
@@ -217,20 +243,46 @@ gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K, int format
                       q.pair ? "pair" : q.swapped ? "rows" : "single", q.pair ? 256 : 128, q.cols,
                       q.split, q.pipe_depth, q.smem_bytes, q.grid_x, q.grid_y,
                       dtype_out == GEMM_OUT_F16 ? "f16" : "f32");
-        cudaError_t e = cudaMalloc(&q.d_status, sizeof(DevStatus));
-        if (e == cudaSuccess) e = fill_memory(q.d_status, nullptr, sizeof(DevStatus));
-        if (e != cudaSuccess) {
-            if (q.d_status) cudaFree(q.d_status);
-            return cuda_fail("allocating the device status record", e);
+        if (first) {
+            q.record = first->record;
+            q.record->plans.fetch_add(1);
+        } else {
+            r = make_record(dev, &q.record);
+            if (r != GEMM_OK) return r;
         }
         plan = new (std::nothrow) gemm_mx_plan(q);
         if (!plan) {
-            cudaFree(q.d_status);
+            release(q.record);
             return fail(GEMM_ERR_CUDA, "out of host memory");
         }
         return ok();
     });
     return plan;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_mx_plan* gemm_mx_create_plan(int64_t M, int64_t N, int64_t K, int format, int dtype_out)
+{
+    return make_plan(M, N, K, format, dtype_out, GEMM_MX_AUTO, 0, nullptr);
+}
+
+gemm_mx_plan* gemm_mx_create_plan_ex(int64_t M, int64_t N, int64_t K, int format, int dtype_out,
+                                     int kernel, int split)
+{
+    return make_plan(M, N, K, format, dtype_out, kernel, split, nullptr);
+}
+
+gemm_mx_plan* gemm_mx_create_plan_beside(const gemm_mx_plan* plan, int64_t M, int64_t N, int64_t K,
+                                         int dtype_out, int kernel, int split)
+{
+    if (!plan) {
+        guarded([&] { return fail(GEMM_ERR_INVALID_ARG, "plan is NULL"); });
+        return nullptr;
+    }
+    return make_plan(M, N, K, plan->format, dtype_out, kernel, split, plan);
 }
 
 int gemm_mx_run(gemm_mx_plan* plan, const void* codes_a, const void* scales_a, const float* scale_a,
@@ -298,8 +350,8 @@ int gemm_mx_run(gemm_mx_plan* plan, const void* codes_a, const void* scales_a, c
         s.p.scale_a = scale_a;
         s.p.scale_b = scale_b;
         s.p.C = C;
-        s.p.status = plan->d_status;
-        s.p.epoch = next_epoch(&plan->epoch);
+        s.p.status = plan->record->d_status;
+        s.p.epoch = next_epoch(&plan->record->epoch);
         s.p.budget_ns = plan->budget_ns;
         s.p.debug_stall = plan->debug_stall;
         cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
@@ -324,14 +376,14 @@ int gemm_mx_get_device_status(gemm_mx_plan* plan)
 {
     return guarded([&] {
         if (!plan) return fail(GEMM_ERR_INVALID_ARG, "plan is NULL");
-        return read_device_status(plan->d_status);
+        return read_device_status(plan->record->d_status);
     });
 }
 
 void gemm_mx_destroy(gemm_mx_plan* plan)
 {
     if (!plan) return;
-    if (plan->d_status) cudaFree(plan->d_status);
+    release(plan->record);
     delete plan;
 }
 

@@ -16,6 +16,7 @@ of a training step and of a decoding step, and how far the decoding step with
 training and decoding steps (--shared 0: without the block).
 """
 import argparse
+import functools
 
 from .binding import GemmError
 from .experts import ExpertRoute, GroupedPlan, W4Plan, w4_pack
@@ -106,27 +107,36 @@ class ExpertLayer:
             Ys, weights=weights, ids=ids)
 
 
+def _plan_beside(first, M, N, K, out="f16"):
+    return MXPlan(M, N, K, format=first.format, out=out, beside=first)
+
+
 class SharedExpert:
     """Y = S2 . relu(S1 . X) for every token (S1 inner x width, S2 width x inner, fp16), its
     products on operands in a block-scaled format; gradients take the rounding as the
     identity.  ``quantize`` lays the weights out as they are now, for ``forward``: call it
-    again once they have changed (``backward`` rounds them anew)."""
+    again once they have changed (``backward`` rounds them anew).
+
+    A number of tokens that is new takes new plans on the host alone, beside one whose status
+    record they share, and only the latest are kept; a graph that captured others replays
+    without them."""
 
     def __init__(self, S1, S2, format="mxfp8"):
         self.S1, self.S2, self.format = S1, S2, format
         self.inner, self.width = S1.shape
-        self._plans = {}
+        self._first = MXPlan(1, self.inner, self.width, format=format)
+        self._plan = functools.lru_cache(maxsize=64)(functools.partial(_plan_beside, self._first))
         self._weights = (None, None)
         self.quantize()
 
-    def _plan(self, M, N, K, out="f16"):
-        key = (M, N, K, out)
-        if key not in self._plans:
-            self._plans[key] = MXPlan(M, N, K, format=self.format, out=out)
-        return self._plans[key]
-
     def plans(self):
-        return list(self._plans.values())
+        """The plan whose status record is that of all."""
+        return [self._first]
+
+    def device_status(self):
+        """GEMM_OK, or the status of a product with a wait that ran out; call after
+        synchronising."""
+        return self._first.device_status()
 
     def quantize(self):
         """The weights for ``forward``, always in the same memory."""
@@ -174,8 +184,7 @@ class ExpertBlock:
         self.clip = GradClip(self.grads)
 
     def device_status(self):
-        status = [p.device_status() for p in self.shared.plans()]
-        return next((s for s in status if s != 0), self.layer.device_status())
+        return self.shared.device_status() or self.layer.device_status()
 
     def forward(self, X, residual, ids, weights):
         """(Y, H, saved)."""

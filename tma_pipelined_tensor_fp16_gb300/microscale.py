@@ -239,17 +239,26 @@ class MXPlan(_Handle):
     """C = A . B^T (M x N) of two MXTensors of one format, A of M x K and B of N x K.
 
     `kernel` ("auto", "pair", "single") and `split` (CTAs that share a tile's length, for
-    "single") choose the kernel as in include/tmamicro.h.  Runs of a plan may overlap."""
+    "single") choose the kernel as in include/tmamicro.h.  Runs of a plan may overlap.
+    `beside`, a plan of the same format, lends its status record: the new plan takes no device
+    memory, and `device_status` of either is that of both."""
     _destroy, _describe = "gemm_mx_destroy", "gemm_mx_describe"
     _status, _wait = "gemm_mx_get_device_status", "gemm_mx_set_wait"
 
-    def __init__(self, M, N, K, format="mxfp8", out="f16", kernel="auto", split=0):
+    def __init__(self, M, N, K, format="mxfp8", out="f16", kernel="auto", split=0, beside=None):
         if kernel not in MX_KERNELS:
             raise ValueError("kernel must be one of %s" % sorted(MX_KERNELS))
         code = _format(format)
         self.M, self.N, self.K, self.format = M, N, K, format
         self.dtype, out_code = _out_dtype(out)
-        self._own(lib().gemm_mx_create_plan_ex(M, N, K, code, out_code, MX_KERNELS[kernel], split))
+        if beside is None:
+            made = lib().gemm_mx_create_plan_ex(M, N, K, code, out_code, MX_KERNELS[kernel], split)
+        elif beside.format != format:
+            raise ValueError("beside is a plan of %s, not %s" % (beside.format, format))
+        else:
+            made = lib().gemm_mx_create_plan_beside(beside.handle, M, N, K, out_code,
+                                                    MX_KERNELS[kernel], split)
+        self._own(made)
 
     def __call__(self, A, B, out=None, stream=None):
         for name, t, rows in (("A", A, self.M), ("B", B, self.N)):
