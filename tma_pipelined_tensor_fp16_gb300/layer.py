@@ -33,8 +33,9 @@ def rms_norm(X, weight, residual=None, eps=1e-6, half=True, format=None, out=Non
     """(Z, H, Q) with h = X + residual and z = h / sqrt(mean(h^2) + eps) * weight along the
     rows of X (tokens x width fp16; weight: width fp16).
 
-    Z is z in fp16 (`out` or a new tensor; None with half=False), H is h in fp16 (`total`,
-    which may be X or residual itself, or a new tensor; X itself without a residual) and Q is
+    Z is z in fp16 (`out`, which may be X or residual itself unless `total` is, or a new tensor;
+    None with half=False), H is h in fp16 (`total`, which may be X or residual itself, or a new
+    tensor; without a residual X itself, or None where `out` has taken its place) and Q is
     z as an MXTensor of `format` (None without; nvfp4 with the tensor scale 1).  A row's
     results do not depend on the other rows, nor on how many there are."""
     torch = _torch()
@@ -54,6 +55,8 @@ def rms_norm(X, weight, residual=None, eps=1e-6, half=True, format=None, out=Non
     if half:
         Z = _output("out", out, shape, f16, dev, stream)
         at_Z = Z.data_ptr()
+        if out is not None and at_Z == X.data_ptr() and residual is None and tokens > 0:
+            H = None
     elif out is not None:
         raise ValueError("out is not written with half=False")
     elif format is None:
