@@ -575,10 +575,14 @@ int gemm_rms_norm(int64_t tokens, int64_t width, const void* X, const void* resi
 
 int64_t gemm_rms_norm_grad_workspace(int64_t tokens, int64_t width)
 {
-    if (check_norm(tokens, width, 0.0f) != GEMM_OK) return -1;
-    ok();
-    const GradShape s = grad_shape(tokens, width);
-    return static_cast<int64_t>(s.ctas) * width * 4;
+    int64_t bytes = -1;
+    guarded([&] {
+        const int r = check_norm(tokens, width, 0.0f);
+        if (r != GEMM_OK) return r;
+        bytes = static_cast<int64_t>(grad_shape(tokens, width).ctas) * width * 4;
+        return ok();
+    });
+    return bytes;
 }
 
 int gemm_rms_norm_grad(int64_t tokens, int64_t width, const void* dZ, const void* H,
