@@ -86,17 +86,6 @@ __device__ __forceinline__ double square_sum(const float (&x)[N])
     return holds(s) ? static_cast<double>(s) : squares_in_64<N>(x);
 }
 
-__device__ __forceinline__ void widen(const uint4& v, float (&x)[8])
-{
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
-}
-
 __device__ __forceinline__ double warp_sum(double s)
 {
 #pragma unroll
@@ -144,7 +133,7 @@ __global__ void __launch_bounds__(CLIP_THREADS) k_grad_squares(const Chunk* tabl
 #pragma unroll
                 for (int i = 0; i < CHUNK_F16; ++i) {
                     float x[8];
-                    widen(w[i], x);
+                    widen8(w[i], x);
                     s += squares(x);
                 }
                 sum += static_cast<double>(s);
@@ -154,7 +143,7 @@ __global__ void __launch_bounds__(CLIP_THREADS) k_grad_squares(const Chunk* tabl
                 done = k.count & ~7;
                 for (int i = tid; i < done / 8; i += CLIP_THREADS) {
                     float x[8];
-                    widen(v[i], x);
+                    widen8(v[i], x);
                     sum += static_cast<double>(squares(x));
                 }
             }
@@ -228,7 +217,7 @@ __device__ __forceinline__ double reciprocal(double x)
 __device__ __forceinline__ uint4 scaled8(const uint4& v, float first, float f)
 {
     float x[8];
-    widen(v, x);
+    widen8(v, x);
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -336,7 +325,8 @@ bool outputs_apart(int64_t count, const void* const* grads, void* const* outs,
     std::vector<Span> spans;
     for (int64_t i = 0; i < count; ++i) {
         if (sizes[i] == 0) continue;
-        const uintptr_t bytes = static_cast<uintptr_t>(sizes[i]) * (dtypes[i] == GEMM_OUT_F16 ? 2 : 4);
+        const uintptr_t bytes =
+            static_cast<uintptr_t>(sizes[i]) * (dtypes[i] == GEMM_OUT_F16 ? 2 : 4);
         const uintptr_t to = reinterpret_cast<uintptr_t>(outs[i]);
         const uintptr_t from = reinterpret_cast<uintptr_t>(grads[i]);
         spans.push_back({to, to + bytes, true});

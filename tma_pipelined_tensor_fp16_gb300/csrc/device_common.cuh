@@ -476,6 +476,18 @@ __device__ __forceinline__ void epilogue_direct_store(uint32_t tmem_acc, int q, 
     }
 }
 
+// Eight halves in four words, the first in the lowest bits, as fp32.
+__device__ __forceinline__ void widen8(const uint4& v, float (&x)[8])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
 // Round x up to a multiple of 1024 (shared-memory tile alignment that the
 // 128-byte swizzle pattern and the MMA descriptors assume).
 __device__ __forceinline__ uint32_t align1024(uint32_t x) { return (x + 1023u) & ~1023u; }

@@ -249,7 +249,8 @@ __device__ __forceinline__ float most_of_halves(const uint4& v)
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     __half2 m = __habs2(*reinterpret_cast<const __half2*>(&w[0]));
 #pragma unroll
-    for (int i = 1; i < 4; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __half2*>(&w[i])));
+    for (int i = 1; i < 4; ++i)
+        m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __half2*>(&w[i])));
     return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
 }
 
@@ -258,7 +259,8 @@ __device__ __forceinline__ float most_of_halves(const uint4& v)
 __device__ __forceinline__ float tensor_scale_of(uint32_t bits)
 {
     if (bits == 0) return 1.0f;
-    const int e = static_cast<int>(bits >> 23) - 127 - 11 + ((bits & 0x7fffffu) > 0x280000u ? 1 : 0);
+    const int up = (bits & 0x7fffffu) > 0x280000u ? 1 : 0;
+    const int e = static_cast<int>(bits >> 23) - 127 - 11 + up;
     return power_of_two(max(e, -126));
 }
 

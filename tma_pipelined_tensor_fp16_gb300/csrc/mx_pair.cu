@@ -249,8 +249,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
             bool running = true;
             for (int t = first; t < tiles && running; t += clusters, ++j) {
                 if (j > 0) {
-                    const bool drained = wd.wait(bar(BAR_TMEM_EMPTY), static_cast<uint32_t>(j - 1) & 1u,
-                                                 WAIT_TMEM_EMPTY, t, -1);
+                    const bool drained =
+                        wd.wait(bar(BAR_TMEM_EMPTY), static_cast<uint32_t>(j - 1) & 1u,
+                                WAIT_TMEM_EMPTY, t, -1);
                     running = __all_sync(0xffffffffu, drained);
                 }
                 const uint32_t d_tmem = tmem_base + (j & 1 ? ACC_SHIFT : 0u);
@@ -283,17 +284,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
                     if (rest >= STEPS) {
                         if constexpr (FORMAT == NVFP4) {
                             // 192 values as two MMAs of 96
-                            constexpr uint32_t idesc = mx_idesc<FORMAT>(TILE, TILE, 0) | MX_IDESC_K96;
-                            mx_mma_k96_pair(elected, d_tmem, a_desc, b_desc, idesc, a_sc, b_sc, more);
-                            ready = __all_sync(0xffffffffu, mbar_test(bar(BAR_FULL + stage), phase));
+                            constexpr uint32_t idesc =
+                                mx_idesc<FORMAT>(TILE, TILE, 0) | MX_IDESC_K96;
+                            mx_mma_k96_pair(elected, d_tmem, a_desc, b_desc, idesc, a_sc, b_sc,
+                                            more);
+                            ready = __all_sync(0xffffffffu,
+                                               mbar_test(bar(BAR_FULL + stage), phase));
                             mx_mma_k96_pair(elected, d_tmem, a_desc + 3 * CHUNK, b_desc + 3 * CHUNK,
-                                            idesc | mx_idesc<FORMAT>(0, 0, 2), a_sc + 4, b_sc + 8, 1u);
+                                            idesc | mx_idesc<FORMAT>(0, 0, 2), a_sc + 4, b_sc + 8,
+                                            1u);
                         } else {
 #pragma unroll
                             for (int i = 0; i < STEPS; ++i) {
                                 // looked at before the stage's last MMA: those that are
                                 // queued cover the look
-                                if (i == STEPS - 1) ready = __all_sync(0xffffffffu, mbar_test(bar(BAR_FULL + stage), phase));
+                                if (i == STEPS - 1)
+                                    ready = __all_sync(0xffffffffu,
+                                                       mbar_test(bar(BAR_FULL + stage), phase));
                                 mx_mma<FORMAT, true>(
                                     elected, d_tmem, a_desc + i * STEP_CHUNKS * CHUNK,
                                     b_desc + i * STEP_CHUNKS * CHUNK,
@@ -331,7 +338,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
         constexpr int READ = 64;               // columns read at a time,
         constexpr int SUB = F16OUT ? 64 : 32;  // and stored: 128 bytes
         static_assert(TILE - static_cast<int>(ACC_SHIFT) == READ, "the shared columns");
-        static_assert(TILE / SUB * STAGING_BYTES <= MX_PAIR_MIN_STAGES * 2 * CHUNKS * MX_CHUNK_BYTES,
+        static_assert(TILE / SUB * STAGING_BYTES <=
+                          MX_PAIR_MIN_STAGES * 2 * CHUNKS * MX_CHUNK_BYTES,
                       "the last tile's buffers");
         const uint32_t q = static_cast<uint32_t>(warp & 3);
         const uint32_t row = q * 32u + lane;
@@ -365,7 +373,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
                     if (lane == 0) mbar_arrive_cluster_relaxed(to_leader);
                 }
 #pragma unroll
-                for (int c = 0; c < READ; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * alpha);
+                for (int c = 0; c < READ; ++c)
+                    v[c] = __float_as_uint(__uint_as_float(v[c]) * alpha);
 #pragma unroll
                 for (int c = 0; c < READ; c += SUB) {
                     const int col0 = nt * TILE + col + c;
@@ -408,9 +417,11 @@ cudaError_t launch_mx_pair(const MxSpec& s, cudaStream_t stream)
     switch (s.format) {
     case MXFP8: return launch_format<MXFP8, 1>(s, stream);
     case MXFP4:
-        return s.staging == 2 ? launch_format<MXFP4, 2>(s, stream) : launch_format<MXFP4, 1>(s, stream);
+        return s.staging == 2 ? launch_format<MXFP4, 2>(s, stream)
+                              : launch_format<MXFP4, 1>(s, stream);
     default:
-        return s.staging == 2 ? launch_format<NVFP4, 2>(s, stream) : launch_format<NVFP4, 1>(s, stream);
+        return s.staging == 2 ? launch_format<NVFP4, 2>(s, stream)
+                              : launch_format<NVFP4, 1>(s, stream);
     }
 }
 

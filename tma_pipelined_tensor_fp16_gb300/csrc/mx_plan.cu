@@ -56,10 +56,10 @@ int encode_storage(CUtensorMap* map, const void* base, int64_t row_bytes, int64_
     const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / 8),
                                static_cast<cuuint32_t>(box_rows), 2};
     const cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, blocks ? 3 : 2, const_cast<void*>(base), dims,
-                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, blocks ? 3 : 2,
+                           const_cast<void*>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         char buf[160];
         std::snprintf(buf, sizeof(buf), "cuTensorMapEncodeTiled(%s) failed with CUresult %d", what,
@@ -193,7 +193,9 @@ gemm_mx_plan* make_plan(int64_t M, int64_t N, int64_t K, int format, int dtype_o
             q.grid_y = 1;
             q.split = 1;
             q.cols = 256;
-            const auto bytes = [&](int depth) { return mx_pair_layout(format, depth, q.staging).total; };
+            const auto bytes = [&](int depth) {
+                return mx_pair_layout(format, depth, q.staging).total;
+            };
             // Short contractions are bound by their tiles' stores: two staging buffers a warp,
             // and a stage less.  8192 x 8192 nvfp4 to fp16, two and one: K = 384 24.7, 31.4 us;
             // 768 28.8, 33.1; 1536 40.2, 41.0; 2048 50.0, 46.4.  (mxfp8 has no room for them.)
@@ -215,7 +217,8 @@ gemm_mx_plan* make_plan(int64_t M, int64_t N, int64_t K, int format, int dtype_o
                 // mxfp4 15.5, 10.3, 7.5, 7.3; 256 x 4096 x 4096 nvfp4 7.9, 7.6, 9.6, 17.9.
                 const int64_t room = q.swapped ? 2 * sms : sms;
                 split = 1;
-                while (split < 8 && tu * tv * split * 2 <= room && p.stages >= 8 * split) split *= 2;
+                while (split < 8 && tu * tv * split * 2 <= room && p.stages >= 8 * split)
+                    split *= 2;
             }
             while (split > p.stages) split /= 2;
             q.split = split;

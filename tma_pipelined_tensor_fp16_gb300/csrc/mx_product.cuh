@@ -50,8 +50,8 @@ template <int FORMAT>
 __device__ __forceinline__ constexpr uint32_t mx_idesc(int M, int N, int scale_id)
 {
     const uint32_t type = FORMAT == MXFP8 ? 0u : 1u;
-    return (FORMAT == MXFP4 ? MX_IDESC_K96 : 0u) | static_cast<uint32_t>(scale_id) << 4 | type << 7 | type << 10 |
-           static_cast<uint32_t>(N >> 3) << 17 | (FORMAT == NVFP4 ? 0u : 1u) << 23 |
+    return (FORMAT == MXFP4 ? MX_IDESC_K96 : 0u) | static_cast<uint32_t>(scale_id) << 4 |
+           type << 7 | type << 10 | static_cast<uint32_t>(N >> 3) << 17 | (FORMAT == NVFP4 ? 0u : 1u) << 23 |
            static_cast<uint32_t>(M >> 4) << 24 | static_cast<uint32_t>(scale_id) << 29;
 }
 

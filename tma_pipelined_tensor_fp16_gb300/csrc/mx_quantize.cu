@@ -126,17 +126,6 @@ __device__ __forceinline__ float find_tensor_scale(const QuantizeParams& p, uint
 TG_HD constexpr int row_spans(int format) { return format == MXFP4 ? 3 : 4; }
 TG_HD constexpr int row_k(int format) { return 32 * row_spans(format); }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8])
-{
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
-}
-
 // Where the scale was found first, the tiles go from the last to the first: the L2 still holds
 // what the search has read last (16384 x 4096 with the search 55 us, in the other order 61).
 template <int SCALE>
@@ -210,7 +199,7 @@ __global__ void __launch_bounds__(row_k(FORMAT))
                 out[2 * (j + i) + 1] = q.y;
             } else {
                 float x[8];
-                unpack8(v[j + i], x);
+                widen8(v[j + i], x);
                 out[j + i] = encode8<FORMAT>(x, b).x;
             }
         }
@@ -676,7 +665,8 @@ int gemm_mx_quantize(int64_t rows, int64_t K, int format, int transpose, const v
             return fail(GEMM_ERR_INVALID_ARG, "X, codes and scales must be non-NULL");
         if (!aligned16(X) || !aligned16(codes) || !aligned16(scales))
             return fail(GEMM_ERR_UNSUPPORTED, "X, codes and scales must be 16-byte aligned");
-        if ((reinterpret_cast<uintptr_t>(tensor_scale) | reinterpret_cast<uintptr_t>(workspace)) & 3u)
+        if ((reinterpret_cast<uintptr_t>(tensor_scale) |
+             reinterpret_cast<uintptr_t>(workspace)) & 3u)
             return fail(GEMM_ERR_UNSUPPORTED, "tensor_scale and workspace must be 4-byte aligned");
         int dev, sms;
         r = require_device(&dev, &sms, nullptr);
@@ -699,8 +689,8 @@ int gemm_mx_quantize(int64_t rows, int64_t K, int format, int transpose, const v
             p.part_count = static_cast<int>(std::min<int64_t>(want, std::min(2 * sms, AMAX_PARTS)));
             p.parts = static_cast<const uint32_t*>(workspace);
             e = launch_dependent(k_mx_most, dim3(static_cast<unsigned>(p.part_count)),
-                                 dim3(MOST_THREADS), 0, 1, stream, static_cast<const uint4*>(X), vecs,
-                                 static_cast<uint32_t*>(workspace));
+                                 dim3(MOST_THREADS), 0, 1, stream, static_cast<const uint4*>(X),
+                                 vecs, static_cast<uint32_t*>(workspace));
             if (e != cudaSuccess) return cuda_fail("tensor scale launch", e);
         }
         if (rows == 0 && format != NVFP4) return ok();

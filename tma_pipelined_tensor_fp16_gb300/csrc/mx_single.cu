@@ -279,7 +279,8 @@ __global__ void __launch_bounds__(MX_THREADS)
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
                 if (i >= left) break;  // uniform
-                mx_mma<FORMAT, false>(elected, tmem_base, u_desc + i * (STEP_CHUNKS * MX_CHUNK_BYTES >> 4),
+                mx_mma<FORMAT, false>(elected, tmem_base,
+                                      u_desc + i * (STEP_CHUNKS * MX_CHUNK_BYTES >> 4),
                                       v_desc + i * (STEP_CHUNKS * V_LEAD >> 4),
                                       mx_idesc<FORMAT>(128, COLS, i * SCALES % 4),
                                       u_sc + i * SCALES / 4 * 4, v_sc + i * SCALES / 4 * 4,

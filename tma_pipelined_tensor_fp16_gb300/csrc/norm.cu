@@ -33,17 +33,6 @@ struct NormParams {
     int64_t chunks, groups;
 };
 
-__device__ __forceinline__ void widen8(const uint4& v, float (&x)[8])
-{
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
-}
-
 __device__ __forceinline__ uint4 narrow8(const float (&x)[8])
 {
     uint32_t w[4];

@@ -316,8 +316,8 @@ def _run_block(a, X, ids, weights, x, i, w):
     status = block.device_status()
     if status != 0:
         raise GemmError(status, "a wait inside a kernel ran out")
-    print("block's training step: norm, experts, shared expert of %d in %s, clipping to %g of %.3g: "
-          "%.3f ms, %.0f TFLOP/s" % (a.shared, a.format, a.clip, float(norms[0]), ms,
+    print("block's training step: norm, experts, shared expert of %d in %s, clipping to %g of %.3g"
+          ": %.3f ms, %.0f TFLOP/s" % (a.shared, a.format, a.clip, float(norms[0]), ms,
                                      flops / ms * 1e-9))
     block.layer.pack()
     ms = _milliseconds(lambda: block.decode(x, x, i, w), 10 * a.steps)

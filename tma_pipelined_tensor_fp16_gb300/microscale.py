@@ -186,8 +186,8 @@ def mx_quantize(X, format="mxfp8", transpose=False, tensor_scale=None, out=None,
     an MXTensor of X's shape, or of X^T's with `transpose` (blocks run along X's columns).
 
     nvfp4: without `tensor_scale` (one fp32, 0 or larger; values beyond 2688 times it are cut
-    off) it is found from X first and belongs to the result.  `out`, an MXTensor of the result's shape and format, is written
-    in place and returned."""
+    off) it is found from X first and belongs to the result.  `out`, an MXTensor of the result's
+    shape and format, is written in place and returned."""
     torch = _torch()
     code = _format(format)
     shape = X.shape
