@@ -3,11 +3,13 @@
 // its rows of A and of all of B's; clusters take tiles t, t + clusters, ... of the grouped
 // raster.
 //
-// Measured: 8192 x 8192 x 8192 nvfp4 134 us, 8200 TFLOP/s, mxfp4 125, mxfp8 291 (held for half a
-// second, under the power cap: 150, 139, 331); 4000 x 3000 x 5000 mxfp4 with fp32 output 22 to
-// 26; 2048 x 2048 x 2048 nvfp4 6.4.  An MMA of 96 values takes 128 cycles; with all SMs busy 159,
-// as a stage's copies take about 2200 cycles to arrive and seven stages are all that fits (the
-// issuer waits for 23 % of the time).  A tile's change costs 1000 cycles.
+// Measured: 8192 x 8192 x 8192 nvfp4 135 us, 8150 TFLOP/s, mxfp4 127, mxfp8 291 in a burst, at
+// 1800, 1890 and 1690 MHz; held, under the power cap, 154, 142, 336 at 1500, 1575, 1425; 4000 x
+// 3000 x 5000 mxfp4 with fp32 output 22 to 26; 2048 x 2048 x 2048 nvfp4 6.4.  Of 224,000 cycles
+// of a pair's MMA warp (nvfp4, burst; held 215,500) 148,300 are its 13.5 tiles' MMAs at 128
+// cycles each 96 values, 50,100 (41,400) waits for a stage, as its copies take about 2200 cycles
+// to arrive and seven stages are all that fits, 6,500 waits for an accumulator (520 a tile's
+// change), 2,200 the first stage, and the rest MMAs that take 143 cycles beside the copies.
 //
 // Tensor memory: two accumulators of 256 columns would leave no room for scales.  They
 // lie at columns 0 and 192 and share 64; scales take columns 448 on.  The epilogue reads
@@ -367,7 +369,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_THREADS, 1)
                 uint32_t v[READ];
                 tmem_load_64cols(taddr + col, v);
                 if (i == 0) {
-                    // relaxed: the loads are complete, and nothing else is handed over
+                    // Relaxed: what is handed over is that the 32 lanes have read.  The loads are
+                    // the warp's (.sync.aligned), its wait::ld has completed them in every
+                    // lane's registers, and instructions issue in order, so lane 0 arrives
+                    // behind them; the next tile's MMAs, which write what was read, come behind
+                    // the issuer's wait and its fence.  Nothing written is handed over, which a
+                    // release would be for (with one the next tile waited another 1200 cycles).
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster_relaxed(to_leader);
