@@ -10,7 +10,8 @@ class Plan:
     """A product in plain torch; `all` holds the plans that live."""
     all = weakref.WeakSet()
 
-    def __init__(self, M, N, K, format="mxfp8", out="f16", beside=None):
+    def __init__(self, M, N, K, format="mxfp8", out="f16", beside=None, device=None):
+        assert beside is not None or device is not None
         self.sizes, self.format, self.beside = (M, N, K), format, beside
         Plan.all.add(self)
 

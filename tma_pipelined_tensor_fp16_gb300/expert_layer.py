@@ -124,7 +124,7 @@ class SharedExpert:
     def __init__(self, S1, S2, format="mxfp8"):
         self.S1, self.S2, self.format = S1, S2, format
         self.inner, self.width = S1.shape
-        self._first = MXPlan(1, self.inner, self.width, format=format)
+        self._first = MXPlan(1, self.inner, self.width, format=format, device=S1.device)
         self._plan = functools.lru_cache(maxsize=64)(functools.partial(_plan_beside, self._first))
         self._weights = (None, None)
         self.quantize()

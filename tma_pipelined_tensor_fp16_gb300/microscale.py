@@ -14,6 +14,7 @@ Argument checks and marshalling only, with the conventions of ``experts``: every
 runs in the library's CUDA kernels, asynchronously on the current stream of the tensors'
 device (or on ``stream``).
 """
+import contextlib
 import functools
 import math
 
@@ -187,7 +188,8 @@ def mx_quantize(X, format="mxfp8", transpose=False, tensor_scale=None, out=None,
 
     nvfp4: without `tensor_scale` (one fp32, 0 or larger; values beyond 2688 times it are cut
     off) it is found from X first and belongs to the result.  `out`, an MXTensor of the result's
-    shape and format, is written in place and returned."""
+    shape and format, is written in place and returned.  A `tensor_scale` becomes part of the
+    result as it is, not as a copy."""
     torch = _torch()
     code = _format(format)
     shape = X.shape
@@ -241,23 +243,29 @@ class MXPlan(_Handle):
     `kernel` ("auto", "pair", "single") and `split` (CTAs that share a tile's length, for
     "single") choose the kernel as in include/tmamicro.h.  Runs of a plan may overlap.
     `beside`, a plan of the same format, lends its status record: the new plan takes no device
-    memory, and `device_status` of either is that of both."""
+    memory, and `device_status` of either is that of both.  A plan belongs to a device: that of
+    `beside`, or `device`, or the current one."""
     _destroy, _describe = "gemm_mx_destroy", "gemm_mx_describe"
     _status, _wait = "gemm_mx_get_device_status", "gemm_mx_set_wait"
 
-    def __init__(self, M, N, K, format="mxfp8", out="f16", kernel="auto", split=0, beside=None):
+    def __init__(self, M, N, K, format="mxfp8", out="f16", kernel="auto", split=0, beside=None,
+                 device=None):
         if kernel not in MX_KERNELS:
             raise ValueError("kernel must be one of %s" % sorted(MX_KERNELS))
         code = _format(format)
         self.M, self.N, self.K, self.format = M, N, K, format
         self.dtype, out_code = _out_dtype(out)
-        if beside is None:
-            made = lib().gemm_mx_create_plan_ex(M, N, K, code, out_code, MX_KERNELS[kernel], split)
-        elif beside.format != format:
+        if beside is not None and beside.format != format:
             raise ValueError("beside is a plan of %s, not %s" % (beside.format, format))
-        else:
-            made = lib().gemm_mx_create_plan_beside(beside.handle, M, N, K, out_code,
-                                                    MX_KERNELS[kernel], split)
+        self.device = device if beside is None else beside.device
+        with contextlib.nullcontext() if self.device is None else \
+                _torch().cuda.device(self.device):
+            if beside is None:
+                made = lib().gemm_mx_create_plan_ex(M, N, K, code, out_code, MX_KERNELS[kernel],
+                                                    split)
+            else:
+                made = lib().gemm_mx_create_plan_beside(beside.handle, M, N, K, out_code,
+                                                        MX_KERNELS[kernel], split)
         self._own(made)
 
     def __call__(self, A, B, out=None, stream=None):
