@@ -52,7 +52,8 @@ typedef struct gemm_clip_plan gemm_clip_plan; /* opaque; owned by the library */
  * outs[i] where the clipped values go: grads[i] itself, or memory that overlaps none of
  * the tensors.  The tensors are
  * aligned to their values' size (to 16 bytes they are faster).  The plan keeps a table of
- * the addresses in device memory (32 bytes for every 16384 values or part of a tensor). */
+ * the addresses in device memory (32 bytes for every 16384 values or part of a tensor), which
+ * a graph that captured a run reads: it must not be replayed once the plan is destroyed. */
 TMAGEMM_API gemm_clip_plan* gemm_clip_create_plan(int64_t count, const void* const* grads,
                                                   void* const* outs, const int64_t* sizes,
                                                   const int* dtypes);

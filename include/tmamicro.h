@@ -85,7 +85,8 @@ typedef struct gemm_mx_plan gemm_mx_plan; /* opaque; owned by the library */
  * format, A of M x K and B of N x K; C is M x N of dtype_out, row-major.  N * sizeof(C
  * element) is a multiple of 16; M, N, K >= 1 and at most 2^31 - 65536.  The products
  * are exact and summed in the tensor cores' fp32.  A plan owns a status record of
- * 32 bytes and no workspace: its runs may overlap. */
+ * 32 bytes and no workspace: its runs may overlap.  A graph that captured a run must not be
+ * replayed once the record is gone. */
 TMAGEMM_API gemm_mx_plan* gemm_mx_create_plan(int64_t M, int64_t N, int64_t K, int format,
                                               int dtype_out);
 

@@ -116,7 +116,8 @@ class GradClip:
     ``clip(max_norm)`` writes every gradient times min(1, max_norm / (norm + eps)) into `out`
     (tensors of the same shapes and types; in place when not given) and returns the norm
     before clipping, one fp32; ``clip.norm()`` returns it alone.  The object keeps the tensors
-    and a table of their addresses; a tensor whose memory has moved since is refused."""
+    and a table of their addresses; a tensor whose memory has moved since is refused.  A graph
+    that captured a call reads that table: the object has to live as long as the graph."""
 
     def __init__(self, grads, out=None):
         torch = _torch()

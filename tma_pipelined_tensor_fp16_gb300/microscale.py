@@ -243,8 +243,8 @@ class MXPlan(_Handle):
     `kernel` ("auto", "pair", "single") and `split` (CTAs that share a tile's length, for
     "single") choose the kernel as in include/tmamicro.h.  Runs of a plan may overlap.
     `beside`, a plan of the same format, lends its status record: the new plan takes no device
-    memory, and `device_status` of either is that of both.  A plan belongs to a device: that of
-    `beside`, or `device`, or the current one."""
+    memory, and `device_status` of either is that of both.  A graph that captured a run needs one
+    of them alive.  A plan belongs to a device: that of `beside`, or `device`, or the current one."""
     _destroy, _describe = "gemm_mx_destroy", "gemm_mx_describe"
     _status, _wait = "gemm_mx_get_device_status", "gemm_mx_set_wait"
 
